@@ -75,7 +75,9 @@ MAGICDEC_API const char *magicdec_status_string(int status);
  * (synchronises the device).  Non-zero means a kernel gave up on a bounded
  * wait (value 1) or met an inconsistent internal state (value 2), and its
  * outputs are then undefined; or that magicdec_draft_cache_update skipped a
- * row whose slot was at or past the cache capacity (value 3).  In the
+ * row whose slot was at or past the cache capacity (value 3; the calls on a
+ * paged cache likewise), or that a call on a paged cache met a block-table
+ * entry outside the pool (value 5).  In the
  * range-checking build (libmagicdec_debug.so, compiled with
  * MAGICDEC_DEBUG_CHECKS) value 4 means a kernel read a sequence length
  * outside [0, capacity] or a gather index outside [0, L_cap) other than the
@@ -391,6 +393,135 @@ MAGICDEC_API magicdec_status magicdec_spec_accept(int B, int gamma, int V, const
                                      const float *draft_logits, const int32_t *draft_tok, const float *u_acc,
                                      const float *u_res, int greedy, int32_t *n_acc, int32_t *out_tok,
                                      int32_t *n_ambiguous, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Paged KV cache, and the tree of drafted tokens over it.
+ *
+ * A cache is a pool of n_pages pages k_pages, v_pages [n_pages, page_size,
+ * H_kv, d] bf16 and a table block_table [B, max_pages] int32: slot s of
+ * sequence b is row s % page_size of page block_table[b, s / page_size].  Any
+ * page_size >= 1.  A dense cache [B, L_cap, H_kv, d] is the pool with n_pages =
+ * B, page_size = L_cap, max_pages = 1 and block_table[b, 0] = b.  The capacity of
+ * a sequence is page_size * max_pages slots (at most INT_MAX).  Only entries of
+ * the slots that a call reads or writes are looked at; one outside [0, n_pages)
+ * sets the device error word to 5, and nothing outside the pool is touched.
+ *
+ * A tree: len[b] positions of sequence b are committed.  Its node i (a drafted
+ * token; node 0 is the last emitted one, whose K and V are not in the cache yet)
+ * has slot len[b] + i.  parent[b, i] < i is the node before it; a negative entry
+ * makes it a root, which follows the committed positions directly.  An entry >= i
+ * counts as negative (and, in the range-checking build, sets error 4).  parent ==
+ * NULL is the chain, parent i - 1.  n_nodes[b], clamped to [0, n], is the number
+ * of nodes of sequence b (NULL: n for all).
+ *
+ * One step of tree speculation, per layer: magicdec_paged_append writes the
+ * nodes' keys and values, magicdec_tree_attn attends; then, once,
+ * magicdec_tree_accept walks down the tree and magicdec_tree_commit moves the
+ * accepted rows to the slots [len, len + n_acc + 1), all layers in one call; and
+ * magicdec_step_lengths gives the next len.
+ */
+typedef struct {
+    int B;
+    int H_q;
+    int H_kv;
+    int d;
+    int page_size;
+    int n_pages;
+    int max_pages;
+} magicdec_paged_shape;
+
+/*
+ * Append of n new tokens per sequence to a paged cache, with the rotary position
+ * embedding applied on the way.  Token i of sequence b has slot len[b] + i and
+ * position len[b] + i, or, with parent, len[b] + the number of nodes before node i
+ * on its path.  K goes to its slot rotated, V unchanged; q, if given, is rotated
+ * into q_out.  Rotation of channels [0, rot_dim) of every head: pair f, 0 <= f <
+ * rot_dim / 2, turns by the angle position * inv_freq[f]; it is channels (f, f +
+ * rot_dim / 2), or (2f, 2f + 1) if interleaved.  Other channels are copied.
+ *   q, k, v  bf16; token i of sequence b starts at element (b * n + i) * stride,
+ *            its heads dense ([H_q, d], [H_kv, d], [H_kv, d]); strides are multiples
+ *            of 8 elements, so the three may be views of one projection's output
+ *   q_out    [B, n, H_q, d] bf16; NULL together with q; may be q itself if that is
+ *            dense (q_stride == H_q * d)
+ *   n_new    (nullable) [B] int32: tokens i >= n_new[b], clamped to [0, n], are
+ *            neither read nor written
+ *   parent   (nullable) [B, n] int32, n <= 256
+ *   inv_freq [rot_dim / 2] fp32 (NULL if rot_dim == 0)
+ * A token whose slot is at or past the capacity is not stored (device error 3),
+ * nor one whose page is outside the pool (error 5); its query is rotated all the same.
+ * No two sequences may share a page that the call writes.
+ * Errors: NULL pointers, bad shape, n <= 0, rot_dim < 0, odd or > d, a stride below
+ * the row, alignment (pointers to 16 bytes, strides to 8 elements);
+ * MAGICDEC_ERR_UNSUPPORTED when rot_dim is not a multiple of 16, or parent is given
+ * and n > 256.
+ */
+MAGICDEC_API magicdec_status magicdec_paged_append(magicdec_paged_shape shape, int n, const uint16_t *q,
+                                                   long long q_stride, const uint16_t *k, long long k_stride,
+                                                   const uint16_t *v, long long v_stride, const int32_t *len,
+                                                   const int32_t *n_new, const int32_t *parent, const float *inv_freq,
+                                                   int rot_dim, int interleaved, const int32_t *block_table,
+                                                   uint16_t *q_out, uint16_t *k_pages, uint16_t *v_pages,
+                                                   void *stream);
+
+/* Workspace bytes magicdec_tree_attn needs for this shape and node count on the
+ * current device (0 for a shape that it refuses). */
+MAGICDEC_API size_t magicdec_tree_attn_workspace_size(magicdec_paged_shape shape, int n);
+
+/*
+ * Attention of the tree's nodes over a paged cache.  Node i of sequence b attends
+ * to positions [0, len[b]) and to the slots of its ancestors and itself; softmax
+ * scale 1/sqrt(d); query head hq reads KV head hq / (H_q/H_kv).  With n = 1 it is
+ * the attention of a single new token, with parent NULL that of a causal block.
+ *   q   [B, n, H_q, d] bf16;  out [B, n, H_q, d] bf16: rows of nodes i >=
+ *       n_nodes[b] are zero, as is a row that sees nothing
+ *   len [B] int32, clamped to [0, capacity]; slots at or past the capacity hold
+ *       nothing (no node sees them)
+ *   ws  workspace of magicdec_tree_attn_workspace_size(shape, n) bytes; no initial
+ *       contents needed
+ * Pool rows outside [0, len + n_nodes) may hold anything, NaN included.  A page
+ * outside the pool counts as keys and values of zero (device error 5).
+ * Supported: n <= 256, H_q/H_kv <= 128 (MAGICDEC_ERR_UNSUPPORTED beyond).
+ * Errors: NULL pointers, bad shape, n <= 0, alignment, workspace too small.
+ */
+MAGICDEC_API magicdec_status magicdec_tree_attn(magicdec_paged_shape shape, int n, const uint16_t *q,
+                                                const uint16_t *k_pages, const uint16_t *v_pages,
+                                                const int32_t *block_table, const int32_t *len,
+                                                const int32_t *n_nodes, const int32_t *parent, uint16_t *out, void *ws,
+                                                size_t ws_bytes, void *stream);
+
+/*
+ * Greedy acceptance down the tree.  From node u = 0: t = argmax target[b, u], ties
+ * to the smaller token; the walk goes on to the lowest node whose parent is u and
+ * whose token is t, and ends where there is none.
+ *   target [B, n, V] fp32 logits of the target at every node (-inf allowed)
+ *   tok    [B, n] int32: the nodes' tokens (tok[b, 0] is not looked at)
+ * Outputs: n_acc [B]: nodes accepted after node 0, -1 for a sequence without nodes
+ *   (so that len + n_acc + 1 is its next length in every case); path [B, n]: node 0
+ *   and the accepted nodes, then -1; out_tok [B, n]: the n_acc accepted tokens, then
+ *   the emitted one (the argmax at the last node of the path), then -1.
+ * Errors: NULL pointers, B <= 0, n <= 0, V <= 0, alignment (target);
+ * MAGICDEC_ERR_UNSUPPORTED when n > 256 or B > 65536.
+ */
+MAGICDEC_API magicdec_status magicdec_tree_accept(int B, int n, int V, const float *target_logits, const int32_t *tok,
+                                                  const int32_t *parent, const int32_t *n_nodes, int32_t *n_acc,
+                                                  int32_t *path, int32_t *out_tok, void *stream);
+
+/*
+ * Commit of an accepted path: in every layer, slot len[b] + i takes the row of slot
+ * len[b] + path[b, i], for i = 0 .. n_acc[b] (clamped to [-1, n - 1]).  path ascends
+ * with path[b, i] >= i, as magicdec_tree_accept gives it; an entry outside [0, n) is
+ * skipped, and other orders give unspecified rows of the same slots.
+ *   k_pages, v_pages [layers, n_pages, page_size, H_kv, d] bf16, one block_table for
+ *   all layers
+ * A move from or to a slot at or past the capacity is skipped (device error 3), as is
+ * one through a page outside the pool (error 5).
+ * Errors: NULL pointers, bad shape, n <= 0, layers <= 0, alignment;
+ * MAGICDEC_ERR_UNSUPPORTED when n > 256 or layers > 65535.
+ */
+MAGICDEC_API magicdec_status magicdec_tree_commit(magicdec_paged_shape shape, int n, int layers, const int32_t *len,
+                                                  const int32_t *path, const int32_t *n_acc,
+                                                  const int32_t *block_table, uint16_t *k_pages, uint16_t *v_pages,
+                                                  void *stream);
 
 #ifdef __cplusplus
 }

@@ -36,8 +36,14 @@ class KVShape(ctypes.Structure):
                 ("L_cap", ctypes.c_int)]
 
 
+class PagedShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H_q", ctypes.c_int), ("H_kv", ctypes.c_int), ("d", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("n_pages", ctypes.c_int), ("max_pages", ctypes.c_int)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_longlong
 _S = ctypes.c_size_t
 
 _SIGNATURES = {
@@ -62,6 +68,11 @@ _SIGNATURES = {
     "magicdec_topk_draft_attn": ([KVShape, _P, _P, _P, _P, _I, _P, _P, _P, _S, _P], _I),
     "magicdec_spec_accept_workspace_size": ([_I, _I, _I], _S),
     "magicdec_spec_accept": ([_I, _I, _I, _P, _P, _P, _P, _P, _I, _P, _P, _P, _P, _S, _P], _I),
+    "magicdec_paged_append": ([PagedShape, _I, _P, _L, _P, _L, _P, _L, _P, _P, _P, _P, _I, _I, _P, _P, _P, _P, _P], _I),
+    "magicdec_tree_attn_workspace_size": ([PagedShape, _I], _S),
+    "magicdec_tree_attn": ([PagedShape, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S, _P], _I),
+    "magicdec_tree_accept": ([_I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P], _I),
+    "magicdec_tree_commit": ([PagedShape, _I, _I, _P, _P, _P, _P, _P, _P, _P], _I),
 }
 
 EXPORTED = tuple(_SIGNATURES)
@@ -537,3 +548,203 @@ def magicdec_spec_accept(target: torch.Tensor, draft: Optional[torch.Tensor], dr
                                       _ptr(u_res), int(bool(greedy)), _ptr(n_acc), _ptr(out_tok), _ptr(n_amb),
                                       _ptr(ws), ws.numel() * ws.element_size(), _stream(stream, dev)))
     return n_acc, out_tok, n_amb
+
+
+# ------------------------------------------------- paged cache, tree of drafted tokens
+# These calls run on the device of their tensors, whichever is current, and what they
+# allocate belongs to the stream they launch on: with `stream`, to that one, so nothing
+# here is shared between two streams or two captured graphs.
+class _On:
+    """The tensors' device and the stream of the call as the current ones."""
+
+    def __init__(self, dev, stream):
+        cur = torch.cuda.current_stream(dev)
+        if stream is not None and not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        self.ptr = (cur if stream is None else stream).cuda_stream
+        self.guard = None
+        if stream is not None and stream.cuda_stream != cur.cuda_stream:
+            self.guard = torch.cuda.stream(stream)
+        elif dev.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.ptr
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def paged_shape(B, H_q, H_kv, d, page_size, n_pages, max_pages) -> PagedShape:
+    return PagedShape(int(B), int(H_q), int(H_kv), int(d), int(page_size), int(n_pages), int(max_pages))
+
+
+def _paged_cache(k_pages, v_pages, block_table, seq_len, B, dev):
+    """Checks of the pool and its table; (page_size, n_pages, max_pages, H_kv, d)."""
+    _need(k_pages, "k_pages", torch.bfloat16, dev)
+    _need(v_pages, "v_pages", torch.bfloat16, dev)
+    if k_pages.dim() < 4 or v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must both be [n_pages, page_size, H_kv, d]")
+    _need(block_table, "block_table", torch.int32, dev)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must be [{B}, max_pages]")
+    _need_shape(seq_len, "seq_len", torch.int32, dev, (B,))
+    n_pages, page_size, H_kv, d = k_pages.shape[-4:]
+    return page_size, n_pages, block_table.shape[1], H_kv, d
+
+
+def _tokens(t, name, dev, B, n, d):
+    """Checks of token rows [B, n, H, d] with dense heads and a stride between tokens; (H, stride)."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be a torch.bfloat16 tensor")
+    if t.device != dev or not t.is_cuda:
+        raise ValueError(f"{name} is on {t.device}, expected a CUDA tensor on {dev}")
+    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != n or t.shape[3] != d:
+        raise ValueError(f"{name} must have shape ({B}, {n}, H, {d}), got {tuple(t.shape)}")
+    H = t.shape[2]
+    sb, sn, sh, sd = t.stride()
+    # The stride between tokens; a dimension of one element has none of its own.
+    stride = sn if n > 1 else sb if B > 1 else H * d
+    if sd != 1 or (H > 1 and sh != d) or (n > 1 and B > 1 and sb != n * sn):
+        raise ValueError(f"{name} needs dense heads and one stride between the tokens of all sequences")
+    return H, stride
+
+
+def magicdec_paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                          block_table: torch.Tensor, seq_len: torch.Tensor, inv_freq: Optional[torch.Tensor] = None,
+                          q: Optional[torch.Tensor] = None, n_new: Optional[torch.Tensor] = None,
+                          parent: Optional[torch.Tensor] = None, interleaved: bool = False,
+                          q_out: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """Append k, v [B, n, H_kv, d] (token-strided views allowed) at slots seq_len + i of the paged cache
+    k_pages / v_pages [n_pages, page_size, H_kv, d], k rotated by inv_freq [rot_dim / 2] fp32 (None: not);
+    q [B, n, H_q, d] is rotated into q_out, which is returned (None without q)."""
+    dev = k.device
+    if k.dim() != 4:
+        raise ValueError("k must be [B, n, H_kv, d]")
+    B, n, H_kv, d = k.shape
+    page_size, n_pages, max_pages, H_c, d_c = _paged_cache(k_pages, v_pages, block_table, seq_len, B, dev)
+    if H_c != H_kv or d_c != d or k_pages.dim() != 4:
+        raise ValueError("k and k_pages disagree: k [B, n, H_kv, d], k_pages [n_pages, page_size, H_kv, d]")
+    _, ks = _tokens(k, "k", dev, B, n, d)
+    H_v, vs = _tokens(v, "v", dev, B, n, d)
+    if H_v != H_kv:
+        raise ValueError("k and v have different numbers of heads")
+    H_q, qs = _tokens(q, "q", dev, B, n, d) if q is not None else (H_kv, 0)
+    if q is None and q_out is not None:
+        raise ValueError("q_out without q")
+    if n_new is not None:
+        _need_shape(n_new, "n_new", torch.int32, dev, (B,))
+    if parent is not None:
+        _need_shape(parent, "parent", torch.int32, dev, (B, n))
+    if inv_freq is not None:
+        _need(inv_freq, "inv_freq", torch.float32, dev)
+        if inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be [rot_dim / 2]")
+    if q_out is not None:
+        _need_shape(q_out, "q_out", torch.bfloat16, dev, (B, n, H_q, d))
+    with _On(dev, stream) as st:
+        if q is not None and q_out is None:
+            q_out = torch.empty((B, n, H_q, d), dtype=torch.bfloat16, device=dev)
+        _check("magicdec_paged_append",
+               lib().magicdec_paged_append(PagedShape(B, H_q, H_kv, d, page_size, n_pages, max_pages), n, _ptr(q), qs,
+                                           _ptr(k), ks, _ptr(v), vs, _ptr(seq_len), _ptr(n_new), _ptr(parent),
+                                           _ptr(inv_freq), 0 if inv_freq is None else 2 * inv_freq.numel(),
+                                           int(bool(interleaved)), _ptr(block_table), _ptr(q_out), _ptr(k_pages),
+                                           _ptr(v_pages), st))
+    return q_out
+
+
+def magicdec_tree_attn_workspace_size(shape: PagedShape, n: int) -> int:
+    return int(lib().magicdec_tree_attn_workspace_size(shape, int(n)))
+
+
+def magicdec_tree_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
+                       seq_len: torch.Tensor, parent: Optional[torch.Tensor] = None,
+                       n_nodes: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                       ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """q [B, n, H_q, d] over the paged cache k_pages / v_pages [n_pages, page_size, H_kv, d] through
+    block_table [B, max_pages]: node i sees positions [0, seq_len) and the slots seq_len + a of its
+    ancestors a (parent [B, n], None: a chain) and itself -> out [B, n, H_q, d] bf16."""
+    _need(q, "q", torch.bfloat16)
+    dev = q.device
+    if q.dim() != 4:
+        raise ValueError("q must be [B, n, H_q, d]")
+    B, n, H_q, d = q.shape
+    page_size, n_pages, max_pages, H_kv, d_c = _paged_cache(k_pages, v_pages, block_table, seq_len, B, dev)
+    if d_c != d or k_pages.dim() != 4:
+        raise ValueError("q and k_pages disagree: q [B, n, H_q, d], k_pages [n_pages, page_size, H_kv, d]")
+    if parent is not None:
+        _need_shape(parent, "parent", torch.int32, dev, (B, n))
+    if n_nodes is not None:
+        _need_shape(n_nodes, "n_nodes", torch.int32, dev, (B,))
+    if out is not None:
+        _need_shape(out, "out", torch.bfloat16, dev, (B, n, H_q, d))
+    if ws is not None and (ws.device != dev or not ws.is_contiguous()):
+        raise ValueError(f"ws must be contiguous and on {dev}")
+    shape = PagedShape(B, H_q, H_kv, d, page_size, n_pages, max_pages)
+    with _On(dev, stream) as st:
+        if out is None:
+            out = torch.empty_like(q)
+        if ws is None:
+            # No contents are kept between calls, so it comes from torch's allocator each time.
+            ws = torch.empty(max(256, magicdec_tree_attn_workspace_size(shape, n)), dtype=torch.uint8, device=dev)
+        _check("magicdec_tree_attn",
+               lib().magicdec_tree_attn(shape, n, _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table),
+                                        _ptr(seq_len), _ptr(n_nodes), _ptr(parent), _ptr(out), _ptr(ws),
+                                        ws.numel() * ws.element_size(), st))
+    return out
+
+
+def magicdec_tree_accept(target: torch.Tensor, tok: torch.Tensor, parent: Optional[torch.Tensor] = None,
+                         n_nodes: Optional[torch.Tensor] = None, n_acc: Optional[torch.Tensor] = None,
+                         path: Optional[torch.Tensor] = None, out_tok: Optional[torch.Tensor] = None, stream=None):
+    """Greedy acceptance down the tree: target [B, n, V] f32, tok [B, n] int32 ->
+    (n_acc [B], path [B, n], out_tok [B, n]) int32."""
+    _need(target, "target", torch.float32)
+    dev = target.device
+    if target.dim() != 3:
+        raise ValueError("target must be [B, n, V]")
+    B, n, V = target.shape
+    _need_shape(tok, "tok", torch.int32, dev, (B, n))
+    if parent is not None:
+        _need_shape(parent, "parent", torch.int32, dev, (B, n))
+    if n_nodes is not None:
+        _need_shape(n_nodes, "n_nodes", torch.int32, dev, (B,))
+    for name, t, shape in (("n_acc", n_acc, (B,)), ("path", path, (B, n)), ("out_tok", out_tok, (B, n))):
+        if t is not None:
+            _need_shape(t, name, torch.int32, dev, shape)
+    with _On(dev, stream) as st:
+        if n_acc is None:
+            n_acc = torch.empty((B,), dtype=torch.int32, device=dev)
+        if path is None:
+            path = torch.empty((B, n), dtype=torch.int32, device=dev)
+        if out_tok is None:
+            out_tok = torch.empty((B, n), dtype=torch.int32, device=dev)
+        _check("magicdec_tree_accept",
+               lib().magicdec_tree_accept(B, n, V, _ptr(target), _ptr(tok), _ptr(parent), _ptr(n_nodes), _ptr(n_acc),
+                                          _ptr(path), _ptr(out_tok), st))
+    return n_acc, path, out_tok
+
+
+def magicdec_tree_commit(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
+                         seq_len: torch.Tensor, path: torch.Tensor, n_acc: torch.Tensor, stream=None) -> None:
+    """Move the rows of the accepted path [B, n] (magicdec_tree_accept) to slots seq_len + 0 .. n_acc, in
+    place, in k_pages / v_pages [n_pages, page_size, H_kv, d] or [layers, n_pages, page_size, H_kv, d]."""
+    _need(path, "path", torch.int32)
+    dev = path.device
+    if path.dim() != 2:
+        raise ValueError("path must be [B, n]")
+    B, n = path.shape
+    page_size, n_pages, max_pages, H_kv, d = _paged_cache(k_pages, v_pages, block_table, seq_len, B, dev)
+    if k_pages.dim() > 5:
+        raise ValueError("k_pages must be [n_pages, page_size, H_kv, d] or [layers, n_pages, page_size, H_kv, d]")
+    layers = k_pages.shape[0] if k_pages.dim() == 5 else 1
+    _need_shape(n_acc, "n_acc", torch.int32, dev, (B,))
+    with _On(dev, stream) as st:
+        _check("magicdec_tree_commit",
+               lib().magicdec_tree_commit(PagedShape(B, H_kv, H_kv, d, page_size, n_pages, max_pages), n, layers,
+                                          _ptr(seq_len), _ptr(path), _ptr(n_acc), _ptr(block_table), _ptr(k_pages),
+                                          _ptr(v_pages), st))

@@ -43,6 +43,21 @@ size_t accept_workspace_bytes(int B, int gamma, int V);
 magicdec_status launch_spec_accept(int B, int gamma, int V, const float *target, const float *draft,
                                    const int32_t *draft_tok, const float *u_acc, const float *u_res, int greedy,
                                    int32_t *n_acc, int32_t *out_tok, int32_t *n_amb, void *ws, cudaStream_t st);
+magicdec_status launch_paged_append(const magicdec_paged_shape &s, int n, const uint16_t *q, long long q_stride,
+                                    const uint16_t *k, long long k_stride, const uint16_t *v, long long v_stride,
+                                    const int32_t *len, const int32_t *n_new, const int32_t *parent,
+                                    const float *inv_freq, int rot_dim, int interleaved, const int32_t *table,
+                                    uint16_t *q_out, uint16_t *kp, uint16_t *vp, cudaStream_t st);
+size_t tree_attn_workspace_bytes(const magicdec_paged_shape &s, int n);
+magicdec_status launch_tree_attn(const magicdec_paged_shape &s, int n, const uint16_t *q, const uint16_t *kp,
+                                 const uint16_t *vp, const int32_t *table, const int32_t *len, const int32_t *n_nodes,
+                                 const int32_t *parent, uint16_t *out, void *ws, cudaStream_t st);
+magicdec_status launch_tree_accept(int B, int n, int V, const float *target, const int32_t *tok,
+                                   const int32_t *parent, const int32_t *n_nodes, int32_t *n_acc, int32_t *path,
+                                   int32_t *out_tok, cudaStream_t st);
+magicdec_status launch_tree_commit(const magicdec_paged_shape &s, int n, int layers, const int32_t *len,
+                                   const int32_t *path, const int32_t *n_acc, const int32_t *table, uint16_t *kp,
+                                   uint16_t *vp, cudaStream_t st);
 
 // The library's device error word (one per device that loads the library).
 __device__ int g_error_word;
@@ -127,6 +142,14 @@ static bool shape_ok(const magicdec_kv_shape &s) {
     return s.B > 0 && s.H_q > 0 && s.H_kv > 0 && s.H_q % s.H_kv == 0 && (s.d == 64 || s.d == 128) &&
            s.L_cap > 0 && s.B <= 4096;
 }
+
+static bool paged_ok(const magicdec_paged_shape &s) {
+    return s.B > 0 && s.B <= 4096 && s.H_q > 0 && s.H_kv > 0 && s.H_kv <= 65535 && s.H_q % s.H_kv == 0 &&
+           (s.d == 64 || s.d == 128) && s.page_size > 0 && s.n_pages > 0 && s.max_pages > 0 &&
+           (long long)s.page_size * s.max_pages <= INT_MAX;
+}
+
+constexpr int kTreeMaxNodes = 256;
 
 extern "C" {
 
@@ -356,6 +379,72 @@ magicdec_status magicdec_spec_accept(int B, int gamma, int V, const float *targe
     if (ws_bytes < magicdec_spec_accept_workspace_size(B, gamma, V)) return MAGICDEC_ERR_WORKSPACE;
     return magicdec::launch_spec_accept(B, gamma, V, target_logits, draft_logits, draft_tok, u_acc, u_res, greedy,
                                         n_acc, out_tok, n_ambiguous, ws, static_cast<cudaStream_t>(stream));
+}
+
+magicdec_status magicdec_paged_append(magicdec_paged_shape shape, int n, const uint16_t *q, long long q_stride,
+                                      const uint16_t *k, long long k_stride, const uint16_t *v, long long v_stride,
+                                      const int32_t *len, const int32_t *n_new, const int32_t *parent,
+                                      const float *inv_freq, int rot_dim, int interleaved,
+                                      const int32_t *block_table, uint16_t *q_out, uint16_t *k_pages,
+                                      uint16_t *v_pages, void *stream) {
+    if (!k || !v || !len || !block_table || !k_pages || !v_pages || (!q) != (!q_out) || (rot_dim > 0 && !inv_freq))
+        return MAGICDEC_ERR_NULL;
+    if (!paged_ok(shape) || n <= 0 || rot_dim < 0 || rot_dim > shape.d || (rot_dim & 1)) return MAGICDEC_ERR_SHAPE;
+    const long long kv_row = (long long)shape.H_kv * shape.d, q_row = (long long)shape.H_q * shape.d;
+    if (k_stride < kv_row || v_stride < kv_row || (q && q_stride < q_row)) return MAGICDEC_ERR_SHAPE;
+    if (rot_dim % 16 || (parent && n > kTreeMaxNodes)) return MAGICDEC_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_pages) ||
+        !aligned16(v_pages) || k_stride % 8 || v_stride % 8 || (q && q_stride % 8))
+        return MAGICDEC_ERR_ALIGN;
+    return magicdec::launch_paged_append(shape, n, q, q_stride, k, k_stride, v, v_stride, len, n_new, parent, inv_freq,
+                                         rot_dim, interleaved, block_table, q_out, k_pages, v_pages,
+                                         static_cast<cudaStream_t>(stream));
+}
+
+static magicdec_status tree_shape(const magicdec_paged_shape &shape, int n) {
+    if (!paged_ok(shape) || n <= 0) return MAGICDEC_ERR_SHAPE;
+    if (n > kTreeMaxNodes || shape.H_q / shape.H_kv > 128) return MAGICDEC_ERR_UNSUPPORTED;
+    return MAGICDEC_OK;
+}
+
+size_t magicdec_tree_attn_workspace_size(magicdec_paged_shape shape, int n) {
+    return tree_shape(shape, n) == MAGICDEC_OK ? magicdec::tree_attn_workspace_bytes(shape, n) : 0;
+}
+
+magicdec_status magicdec_tree_attn(magicdec_paged_shape shape, int n, const uint16_t *q, const uint16_t *k_pages,
+                                   const uint16_t *v_pages, const int32_t *block_table, const int32_t *len,
+                                   const int32_t *n_nodes, const int32_t *parent, uint16_t *out, void *ws,
+                                   size_t ws_bytes, void *stream) {
+    if (!q || !k_pages || !v_pages || !block_table || !len || !out || !ws) return MAGICDEC_ERR_NULL;
+    const magicdec_status s = tree_shape(shape, n);
+    if (s != MAGICDEC_OK) return s;
+    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) || !aligned16(ws))
+        return MAGICDEC_ERR_ALIGN;
+    if (ws_bytes < magicdec::tree_attn_workspace_bytes(shape, n)) return MAGICDEC_ERR_WORKSPACE;
+    return magicdec::launch_tree_attn(shape, n, q, k_pages, v_pages, block_table, len, n_nodes, parent, out, ws,
+                                      static_cast<cudaStream_t>(stream));
+}
+
+magicdec_status magicdec_tree_accept(int B, int n, int V, const float *target_logits, const int32_t *tok,
+                                     const int32_t *parent, const int32_t *n_nodes, int32_t *n_acc, int32_t *path,
+                                     int32_t *out_tok, void *stream) {
+    if (!target_logits || !tok || !n_acc || !path || !out_tok) return MAGICDEC_ERR_NULL;
+    if (B <= 0 || n <= 0 || V <= 0) return MAGICDEC_ERR_SHAPE;
+    if (n > kTreeMaxNodes || B > magicdec::kAcceptMaxBatch) return MAGICDEC_ERR_UNSUPPORTED;
+    if (!aligned16(target_logits)) return MAGICDEC_ERR_ALIGN;
+    return magicdec::launch_tree_accept(B, n, V, target_logits, tok, parent, n_nodes, n_acc, path, out_tok,
+                                        static_cast<cudaStream_t>(stream));
+}
+
+magicdec_status magicdec_tree_commit(magicdec_paged_shape shape, int n, int layers, const int32_t *len,
+                                     const int32_t *path, const int32_t *n_acc, const int32_t *block_table,
+                                     uint16_t *k_pages, uint16_t *v_pages, void *stream) {
+    if (!len || !path || !n_acc || !block_table || !k_pages || !v_pages) return MAGICDEC_ERR_NULL;
+    if (!paged_ok(shape) || n <= 0 || layers <= 0) return MAGICDEC_ERR_SHAPE;
+    if (n > kTreeMaxNodes || layers > 65535) return MAGICDEC_ERR_UNSUPPORTED;
+    if (!aligned16(k_pages) || !aligned16(v_pages)) return MAGICDEC_ERR_ALIGN;
+    return magicdec::launch_tree_commit(shape, n, layers, len, path, n_acc, block_table, k_pages, v_pages,
+                                        static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -20,11 +20,12 @@ namespace magicdec {
 // address): 1 = a bounded wait gave up, 2 = inconsistent internal state,
 // 3 = a draft-cache copy needed a slot at or past the cache capacity,
 // 4 = (debug build only) a length or index outside the range the kernel
-// clamps or skips it to.
+// clamps or skips it to, 5 = a block-table entry outside the page pool.
 constexpr int kErrTimeout = 1;
 constexpr int kErrState = 2;
 constexpr int kErrCapacity = 3;
 constexpr int kErrRange = 4;
+constexpr int kErrPage = 5;
 
 // Fixed-size counter regions at the start of the caller's workspaces: the
 // attention kernels keep one counter per (sequence, KV head) pair, the
