@@ -11,6 +11,7 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional, Tuple
@@ -553,55 +554,73 @@ def magicdec_spec_accept(target: torch.Tensor, draft: Optional[torch.Tensor], dr
 # ------------------------------------------------- paged cache, tree of drafted tokens
 # These calls run on the device of their tensors, whichever is current, and what they
 # allocate belongs to the stream they launch on: with `stream`, to that one, so nothing
-# here is shared between two streams or two captured graphs.
-class _On:
-    """The tensors' device and the stream of the call as the current ones."""
+# here is shared between two streams or two captured graphs.  A decode step makes hundreds
+# of them, each a few microseconds of kernel, so the checks are written to cost about as
+# little: one pass over a tensor's properties where all is well, the words where it is not.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
-    def __init__(self, dev, stream):
-        cur = torch.cuda.current_stream(dev)
-        if stream is not None and not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=dev)
-        self.ptr = (cur if stream is None else stream).cuda_stream
-        self.guard = None
-        if stream is not None and stream.cuda_stream != cur.cuda_stream:
-            self.guard = torch.cuda.stream(stream)
-        elif dev.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(dev)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.ptr
+def _at(t, name, dtype, dev, shape) -> int:
+    """The address of a dense tensor of this type, device and shape; raises for any other."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
+            and t.is_contiguous()):
+        _need_shape(t, name, dtype, dev, shape)
+    return t.data_ptr()
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+
+def _cuda_device(t, name, dtype):
+    """The device of a call's first tensor, which has to be a CUDA one."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _launch(name, dev, stream, call):
+    """call(address of the stream) with the tensors' device, and the stream, as the current ones."""
+    raw = _raw_stream(dev.index)
+    if (stream is None or getattr(stream, "cuda_stream", stream) == raw) and _current_device() == dev.index:
+        _check(name, call(raw))
+        return
+    if stream is None:
+        with torch.cuda.device(dev):
+            _check(name, call(raw))
+        return
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    with torch.cuda.stream(stream):
+        _check(name, call(stream.cuda_stream))
 
 
 def paged_shape(B, H_q, H_kv, d, page_size, n_pages, max_pages) -> PagedShape:
     return PagedShape(int(B), int(H_q), int(H_kv), int(d), int(page_size), int(n_pages), int(max_pages))
 
 
-def _paged_cache(k_pages, v_pages, block_table, seq_len, B, dev):
-    """Checks of the pool and its table; (page_size, n_pages, max_pages, H_kv, d)."""
-    _need(k_pages, "k_pages", torch.bfloat16, dev)
-    _need(v_pages, "v_pages", torch.bfloat16, dev)
-    if k_pages.dim() < 4 or v_pages.shape != k_pages.shape:
-        raise ValueError("k_pages and v_pages must both be [n_pages, page_size, H_kv, d]")
-    _need(block_table, "block_table", torch.int32, dev)
-    if block_table.dim() != 2 or block_table.shape[0] != B:
+def _paged_cache(k_pages, v_pages, block_table, B, dev, dims=4):
+    """Checks of the pool and its table; their addresses and (page_size, n_pages, max_pages, H_kv, d)."""
+    shape = getattr(k_pages, "shape", ())
+    if len(shape) not in (4, dims):
+        raise ValueError(f"k_pages must be [n_pages, page_size, H_kv, d]{' or [layers, ...]' if dims == 5 else ''}")
+    kp = _at(k_pages, "k_pages", torch.bfloat16, dev, shape)
+    vp = _at(v_pages, "v_pages", torch.bfloat16, dev, shape)
+    ts = getattr(block_table, "shape", ())
+    if len(ts) != 2 or ts[0] != B:
         raise ValueError(f"block_table must be [{B}, max_pages]")
-    _need_shape(seq_len, "seq_len", torch.int32, dev, (B,))
-    n_pages, page_size, H_kv, d = k_pages.shape[-4:]
-    return page_size, n_pages, block_table.shape[1], H_kv, d
+    table = _at(block_table, "block_table", torch.int32, dev, ts)
+    n_pages, page_size, H_kv, d = shape[-4:]
+    return kp, vp, table, page_size, n_pages, ts[1], H_kv, d
 
 
 def _tokens(t, name, dev, B, n, d):
-    """Checks of token rows [B, n, H, d] with dense heads and a stride between tokens; (H, stride)."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+    """Checks of token rows [B, n, H, d] with dense heads and one stride between tokens; (H, stride)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be a torch.bfloat16 tensor")
-    if t.device != dev or not t.is_cuda:
-        raise ValueError(f"{name} is on {t.device}, expected a CUDA tensor on {dev}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
     if t.dim() != 4 or t.shape[0] != B or t.shape[1] != n or t.shape[3] != d:
         raise ValueError(f"{name} must have shape ({B}, {n}, H, {d}), got {tuple(t.shape)}")
     H = t.shape[2]
@@ -621,12 +640,12 @@ def magicdec_paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tenso
     """Append k, v [B, n, H_kv, d] (token-strided views allowed) at slots seq_len + i of the paged cache
     k_pages / v_pages [n_pages, page_size, H_kv, d], k rotated by inv_freq [rot_dim / 2] fp32 (None: not);
     q [B, n, H_q, d] is rotated into q_out, which is returned (None without q)."""
-    dev = k.device
+    dev = _cuda_device(k, "k", torch.bfloat16)
     if k.dim() != 4:
         raise ValueError("k must be [B, n, H_kv, d]")
     B, n, H_kv, d = k.shape
-    page_size, n_pages, max_pages, H_c, d_c = _paged_cache(k_pages, v_pages, block_table, seq_len, B, dev)
-    if H_c != H_kv or d_c != d or k_pages.dim() != 4:
+    kp, vp, table, page_size, n_pages, max_pages, H_c, d_c = _paged_cache(k_pages, v_pages, block_table, B, dev)
+    if H_c != H_kv or d_c != d:
         raise ValueError("k and k_pages disagree: k [B, n, H_kv, d], k_pages [n_pages, page_size, H_kv, d]")
     _, ks = _tokens(k, "k", dev, B, n, d)
     H_v, vs = _tokens(v, "v", dev, B, n, d)
@@ -635,30 +654,35 @@ def magicdec_paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tenso
     H_q, qs = _tokens(q, "q", dev, B, n, d) if q is not None else (H_kv, 0)
     if q is None and q_out is not None:
         raise ValueError("q_out without q")
-    if n_new is not None:
-        _need_shape(n_new, "n_new", torch.int32, dev, (B,))
-    if parent is not None:
-        _need_shape(parent, "parent", torch.int32, dev, (B, n))
+    length = _at(seq_len, "seq_len", torch.int32, dev, (B,))
+    count = None if n_new is None else _at(n_new, "n_new", torch.int32, dev, (B,))
+    par = None if parent is None else _at(parent, "parent", torch.int32, dev, (B, n))
+    inv, rot = None, 0
     if inv_freq is not None:
-        _need(inv_freq, "inv_freq", torch.float32, dev)
-        if inv_freq.dim() != 1:
-            raise ValueError("inv_freq must be [rot_dim / 2]")
+        inv = _at(inv_freq, "inv_freq", torch.float32, dev, (inv_freq.numel(),))
+        rot = 2 * inv_freq.numel()
     if q_out is not None:
-        _need_shape(q_out, "q_out", torch.bfloat16, dev, (B, n, H_q, d))
-    with _On(dev, stream) as st:
+        _at(q_out, "q_out", torch.bfloat16, dev, (B, n, H_q, d))
+
+    def call(st):
+        nonlocal q_out
         if q is not None and q_out is None:
             q_out = torch.empty((B, n, H_q, d), dtype=torch.bfloat16, device=dev)
-        _check("magicdec_paged_append",
-               lib().magicdec_paged_append(PagedShape(B, H_q, H_kv, d, page_size, n_pages, max_pages), n, _ptr(q), qs,
-                                           _ptr(k), ks, _ptr(v), vs, _ptr(seq_len), _ptr(n_new), _ptr(parent),
-                                           _ptr(inv_freq), 0 if inv_freq is None else 2 * inv_freq.numel(),
-                                           int(bool(interleaved)), _ptr(block_table), _ptr(q_out), _ptr(k_pages),
-                                           _ptr(v_pages), st))
+        return (_lib or lib()).magicdec_paged_append(
+            PagedShape(B, H_q, H_kv, d, page_size, n_pages, max_pages), n, None if q is None else q.data_ptr(), qs,
+            k.data_ptr(), ks, v.data_ptr(), vs, length, count, par, inv, rot, 1 if interleaved else 0, table,
+            None if q is None else q_out.data_ptr(), kp, vp, st)
+    _launch("magicdec_paged_append", dev, stream, call)
     return q_out
 
 
 def magicdec_tree_attn_workspace_size(shape: PagedShape, n: int) -> int:
     return int(lib().magicdec_tree_attn_workspace_size(shape, int(n)))
+
+
+@functools.lru_cache(maxsize=256)
+def _tree_ws_bytes(device_index, *args) -> int:
+    return max(256, magicdec_tree_attn_workspace_size(PagedShape(*args[:-1]), args[-1]))
 
 
 def magicdec_tree_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
@@ -668,33 +692,33 @@ def magicdec_tree_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Te
     """q [B, n, H_q, d] over the paged cache k_pages / v_pages [n_pages, page_size, H_kv, d] through
     block_table [B, max_pages]: node i sees positions [0, seq_len) and the slots seq_len + a of its
     ancestors a (parent [B, n], None: a chain) and itself -> out [B, n, H_q, d] bf16."""
-    _need(q, "q", torch.bfloat16)
-    dev = q.device
+    dev = _cuda_device(q, "q", torch.bfloat16)
     if q.dim() != 4:
         raise ValueError("q must be [B, n, H_q, d]")
     B, n, H_q, d = q.shape
-    page_size, n_pages, max_pages, H_kv, d_c = _paged_cache(k_pages, v_pages, block_table, seq_len, B, dev)
-    if d_c != d or k_pages.dim() != 4:
+    qp = _at(q, "q", torch.bfloat16, dev, (B, n, H_q, d))
+    kp, vp, table, page_size, n_pages, max_pages, H_kv, d_c = _paged_cache(k_pages, v_pages, block_table, B, dev)
+    if d_c != d:
         raise ValueError("q and k_pages disagree: q [B, n, H_q, d], k_pages [n_pages, page_size, H_kv, d]")
-    if parent is not None:
-        _need_shape(parent, "parent", torch.int32, dev, (B, n))
-    if n_nodes is not None:
-        _need_shape(n_nodes, "n_nodes", torch.int32, dev, (B,))
+    length = _at(seq_len, "seq_len", torch.int32, dev, (B,))
+    par = None if parent is None else _at(parent, "parent", torch.int32, dev, (B, n))
+    count = None if n_nodes is None else _at(n_nodes, "n_nodes", torch.int32, dev, (B,))
     if out is not None:
-        _need_shape(out, "out", torch.bfloat16, dev, (B, n, H_q, d))
+        _at(out, "out", torch.bfloat16, dev, (B, n, H_q, d))
     if ws is not None and (ws.device != dev or not ws.is_contiguous()):
         raise ValueError(f"ws must be contiguous and on {dev}")
-    shape = PagedShape(B, H_q, H_kv, d, page_size, n_pages, max_pages)
-    with _On(dev, stream) as st:
+    dims = (B, H_q, H_kv, d, page_size, n_pages, max_pages)
+
+    def call(st):
+        nonlocal out, ws
         if out is None:
-            out = torch.empty_like(q)
+            out = torch.empty((B, n, H_q, d), dtype=torch.bfloat16, device=dev)
         if ws is None:
             # No contents are kept between calls, so it comes from torch's allocator each time.
-            ws = torch.empty(max(256, magicdec_tree_attn_workspace_size(shape, n)), dtype=torch.uint8, device=dev)
-        _check("magicdec_tree_attn",
-               lib().magicdec_tree_attn(shape, n, _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table),
-                                        _ptr(seq_len), _ptr(n_nodes), _ptr(parent), _ptr(out), _ptr(ws),
-                                        ws.numel() * ws.element_size(), st))
+            ws = torch.empty(_tree_ws_bytes(dev.index, *dims, n), dtype=torch.uint8, device=dev)
+        return (_lib or lib()).magicdec_tree_attn(PagedShape(*dims), n, qp, kp, vp, table, length, count, par,
+                                                  out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), st)
+    _launch("magicdec_tree_attn", dev, stream, call)
     return out
 
 
@@ -703,29 +727,29 @@ def magicdec_tree_accept(target: torch.Tensor, tok: torch.Tensor, parent: Option
                          path: Optional[torch.Tensor] = None, out_tok: Optional[torch.Tensor] = None, stream=None):
     """Greedy acceptance down the tree: target [B, n, V] f32, tok [B, n] int32 ->
     (n_acc [B], path [B, n], out_tok [B, n]) int32."""
-    _need(target, "target", torch.float32)
-    dev = target.device
+    dev = _cuda_device(target, "target", torch.float32)
     if target.dim() != 3:
         raise ValueError("target must be [B, n, V]")
     B, n, V = target.shape
-    _need_shape(tok, "tok", torch.int32, dev, (B, n))
-    if parent is not None:
-        _need_shape(parent, "parent", torch.int32, dev, (B, n))
-    if n_nodes is not None:
-        _need_shape(n_nodes, "n_nodes", torch.int32, dev, (B,))
+    logits = _at(target, "target", torch.float32, dev, (B, n, V))
+    tk = _at(tok, "tok", torch.int32, dev, (B, n))
+    par = None if parent is None else _at(parent, "parent", torch.int32, dev, (B, n))
+    count = None if n_nodes is None else _at(n_nodes, "n_nodes", torch.int32, dev, (B,))
     for name, t, shape in (("n_acc", n_acc, (B,)), ("path", path, (B, n)), ("out_tok", out_tok, (B, n))):
         if t is not None:
-            _need_shape(t, name, torch.int32, dev, shape)
-    with _On(dev, stream) as st:
+            _at(t, name, torch.int32, dev, shape)
+
+    def call(st):
+        nonlocal n_acc, path, out_tok
         if n_acc is None:
             n_acc = torch.empty((B,), dtype=torch.int32, device=dev)
         if path is None:
             path = torch.empty((B, n), dtype=torch.int32, device=dev)
         if out_tok is None:
             out_tok = torch.empty((B, n), dtype=torch.int32, device=dev)
-        _check("magicdec_tree_accept",
-               lib().magicdec_tree_accept(B, n, V, _ptr(target), _ptr(tok), _ptr(parent), _ptr(n_nodes), _ptr(n_acc),
-                                          _ptr(path), _ptr(out_tok), st))
+        return (_lib or lib()).magicdec_tree_accept(B, n, V, logits, tk, par, count, n_acc.data_ptr(),
+                                                    path.data_ptr(), out_tok.data_ptr(), st)
+    _launch("magicdec_tree_accept", dev, stream, call)
     return n_acc, path, out_tok
 
 
@@ -733,18 +757,14 @@ def magicdec_tree_commit(k_pages: torch.Tensor, v_pages: torch.Tensor, block_tab
                          seq_len: torch.Tensor, path: torch.Tensor, n_acc: torch.Tensor, stream=None) -> None:
     """Move the rows of the accepted path [B, n] (magicdec_tree_accept) to slots seq_len + 0 .. n_acc, in
     place, in k_pages / v_pages [n_pages, page_size, H_kv, d] or [layers, n_pages, page_size, H_kv, d]."""
-    _need(path, "path", torch.int32)
-    dev = path.device
+    dev = _cuda_device(path, "path", torch.int32)
     if path.dim() != 2:
         raise ValueError("path must be [B, n]")
     B, n = path.shape
-    page_size, n_pages, max_pages, H_kv, d = _paged_cache(k_pages, v_pages, block_table, seq_len, B, dev)
-    if k_pages.dim() > 5:
-        raise ValueError("k_pages must be [n_pages, page_size, H_kv, d] or [layers, n_pages, page_size, H_kv, d]")
+    way = _at(path, "path", torch.int32, dev, (B, n))
+    kp, vp, table, page_size, n_pages, max_pages, H_kv, d = _paged_cache(k_pages, v_pages, block_table, B, dev, 5)
+    length = _at(seq_len, "seq_len", torch.int32, dev, (B,))
+    acc = _at(n_acc, "n_acc", torch.int32, dev, (B,))
     layers = k_pages.shape[0] if k_pages.dim() == 5 else 1
-    _need_shape(n_acc, "n_acc", torch.int32, dev, (B,))
-    with _On(dev, stream) as st:
-        _check("magicdec_tree_commit",
-               lib().magicdec_tree_commit(PagedShape(B, H_kv, H_kv, d, page_size, n_pages, max_pages), n, layers,
-                                          _ptr(seq_len), _ptr(path), _ptr(n_acc), _ptr(block_table), _ptr(k_pages),
-                                          _ptr(v_pages), st))
+    _launch("magicdec_tree_commit", dev, stream, lambda st: (_lib or lib()).magicdec_tree_commit(
+        PagedShape(B, H_kv, H_kv, d, page_size, n_pages, max_pages), n, layers, length, way, acc, table, kp, vp, st))

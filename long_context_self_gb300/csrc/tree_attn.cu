@@ -26,14 +26,15 @@
 // does not own whole goes to the workspace as (O, max, sum) and is joined by a
 // second kernel in a fixed order.  No atomics: results do not change from run to run.
 //
-// Roles (320 threads): warp 0 issues the TMA boxes, warp 1 the MMAs, warps 2-5
-// and 6-9 are the two softmax warpgroups.  Every wait is bounded; after one that
+// Roles (384 threads): warp 0 issues the TMA boxes, warp 1 the MMAs, warps 4-7
+// and 8-11 are the two softmax warpgroups, which take over the registers that the
+// first one gives up.  Every wait is bounded; after one that
 // gave up (error 1) the roles run on without waiting, so that all of them end.
 #include "common.cuh"
 
 namespace magicdec {
 
-constexpr int kTrThreads = 320;
+constexpr int kTrThreads = 384;
 constexpr int kTrKeys = 128;                  // keys per tile
 constexpr int kTrBox = kTrKeys * 128;         // 128 rows x 64 channels (16 KB)
 constexpr int kTrMaxNodes = 256;
@@ -122,7 +123,42 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         TR_W8(r, 0), TR_W8(r, 8), TR_W8(r, 16), TR_W8(r, 24)
         : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        TR_W8(r, 0), TR_W8(r, 8)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Registers per thread from here on, for the whole warpgroup.  384 threads start with
+// 168 each; 80 + 208 + 208 is within 3 * 168.
+__device__ __forceinline__ void regs_give() { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); }
+__device__ __forceinline__ void regs_take() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
+
+// Two fp32 values in one 64-bit register: one instruction for both.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+    return d;
+}
+__device__ __forceinline__ uint64_t pair(float lo, float hi) { return pair(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ float2 apart(uint64_t d) {
+    uint32_t lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(d));
+    return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 
 // ------------------------------------------------------------------ work list
 // Key tile tj of a sequence: its first position and its rows that hold positions.
@@ -322,6 +358,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     bool ok = true;
 
     if (warp == 0) {
+        regs_give();
         // ------------------------------------------------------------- TMA producer
         const uint64_t pol = p.n > RT * p.NB ? policy_evict_normal() : policy_evict_first();
         uint32_t slot = 0, runs = 0;                 // ring slots issued, runs begun
@@ -393,6 +430,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             for (uint32_t i = slot - last; i < slot; ++i) mbar_wait(&full[i % NST], (i / NST) & 1, p.err);
         }
     } else if (warp == 1) {
+        regs_give();
         // -------------------------------------------------------------- MMA issuer
         const uint32_t idesc_s = umma_idesc_bf16(128, kTrKeys);
         const uint32_t idesc_o = umma_idesc_bf16(128, D) | (1u << 16);   // B (V) is MN-major
@@ -516,14 +554,17 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             umma_commit(mma_done);
             mbar_wait(mma_done, 0, p.err);
         }
+    } else if (warp < 4) {
+        regs_give();
     } else {
+        regs_take();
         // -------------------------------------------------------- softmax warpgroups
-        const int s = (warp - 2) >> 2;                       // stream
+        const int s = (warp - 4) >> 2;                       // stream
         const int quad = warp & 3;                           // TMEM lanes 32 * quad ..
         const int row = 32 * quad + lane;
         const uint32_t lane_addr = (uint32_t)(32 * quad) << 16;
         const uint32_t ts = tmem + lane_addr + s * 128, to = tmem + lane_addr + kTrOut + s * D;
-        const int wt = tid - 64 - s * 128;                   // thread of the warpgroup
+        const int wt = tid - 128 - s * 128;                  // thread of the warpgroup
         const int node_r = row / p.G;                        // node within the row tile
         const float sl = p.scale_log2;
         uint8_t *mypar = par + s * kTrMaxNodes;
@@ -535,6 +576,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             const int base = (r.rb * RT + (RT == 2 ? s : 0)) * p.NB;      // first node of the row tile
             const int node = node_r < p.NB && base + node_r < r.s.nodes ? base + node_r : -1;
             const bool active = RT == 1 || base < r.s.nodes;
+            const bool live = __any_sync(0xffffffffu, node >= 0);         // the warp has rows
             if (p.parent && par_b != r.b) {
                 // parent + 1 of every node in a byte (0: none); a parent that is not before its
                 // node counts as none.
@@ -552,68 +594,85 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 const Tile t = tile_at(p, r.t0 + j, r.s.total);
                 ok = tr_wait(&s_full[s], tiles_done & 1, p.err, ok, lane);
                 tc_fence_after();
-                uint32_t v[128];
-                tmem_ld128(ts, v);
-                if (t.rows < kTrKeys || t.p0 + t.rows > r.s.len) {
-                    uint32_t see[4];
+                if (live) {
+                    uint32_t v[128];
+                    tmem_ld128(ts, v);
+                    if (t.rows < kTrKeys || t.p0 + t.rows > r.s.len) {
+                        uint32_t see[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int c = min(r.s.len - t.p0, t.rows) - 32 * k;
-                        see[k] = node < 0 || c <= 0 ? 0u : c >= 32 ? 0xffffffffu : (1u << c) - 1u;
-                    }
-                    if (node >= 0 && t.p0 + t.rows > r.s.len) {
-                        for (int a = node; a >= 0; a = p.parent ? (int)mypar[a] - 1 : a - 1) {
-                            const int off = r.s.len + a - t.p0;
-                            if (off >= 0 && off < t.rows) {
+                        for (int k = 0; k < 4; ++k) {
+                            const int c = min(r.s.len - t.p0, t.rows) - 32 * k;
+                            see[k] = node < 0 || c <= 0 ? 0u : c >= 32 ? 0xffffffffu : (1u << c) - 1u;
+                        }
+                        if (node >= 0 && t.p0 + t.rows > r.s.len) {
+                            for (int a = node; a >= 0; a = p.parent ? (int)mypar[a] - 1 : a - 1) {
+                                const int off = r.s.len + a - t.p0;
+                                if (off >= 0 && off < t.rows) {
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    if ((off >> 5) == k) see[k] |= 1u << (off & 31);
+                                    for (int k = 0; k < 4; ++k)
+                                        if ((off >> 5) == k) see[k] |= 1u << (off & 31);
+                                }
                             }
                         }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (__all_sync(0xffffffffu, see[k] == 0xffffffffu)) continue;
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (!((see[k] >> c) & 1u)) v[32 * k + c] = 0xff800000u;
+                        }
                     }
+                    // Four chains, so that one maximum does not wait for the last.
+                    float t4[4];
 #pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (!((see[c >> 5] >> (c & 31)) & 1u)) v[c] = 0xff800000u;
-                }
-                float top = __uint_as_float(v[0]);
+                    for (int c = 0; c < 4; ++c) t4[c] = __uint_as_float(v[c]);
 #pragma unroll
-                for (int c = 1; c < 128; ++c) top = fmaxf(top, __uint_as_float(v[c]));
-                // The maximum is moved, and O scaled, only where it has grown by more than
-                // 2^kTrLazy: sums then stay below 2^kTrLazy * keys, far inside fp32.
-                const bool grow = top > m && (top - m) * sl > kTrLazy;
-                float f = 1.f;
-                if (grow) {
-                    f = m == -INFINITY ? 1.f : fast_exp2((m - top) * sl);   // from -inf: O and l are zero
-                    m = top;
-                }
-                if (mine > 0 && __any_sync(0xffffffffu, grow)) {
-                    ok = tr_wait(&o_full[s], (tiles_done - 1) & 1, p.err, ok, lane);
-                    tc_fence_after();
+                    for (int c = 4; c < 124; c += 8)
 #pragma unroll
-                    for (int c0 = 0; c0 < D; c0 += 32) {
-                        float o[32];
-                        uint32_t u[32];
-                        tmem_ld32(to + c0, o);
+                        for (int i = 0; i < 4; ++i)
+                            t4[i] = fmaxf(t4[i], fmaxf(__uint_as_float(v[c + i]), __uint_as_float(v[c + 4 + i])));
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(o[i] * f);
-                        tmem_st32(to + c0, u);
+                    for (int i = 0; i < 4; ++i) t4[i] = fmaxf(t4[i], __uint_as_float(v[124 + i]));
+                    const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+                    // The maximum is moved, and O scaled, only where it has grown by more than
+                    // 2^kTrLazy: sums then stay below 2^kTrLazy * keys, far inside fp32.
+                    const bool grow = top > m && (top - m) * sl > kTrLazy;
+                    float f = 1.f;
+                    if (grow) {
+                        f = m == -INFINITY ? 1.f : fast_exp2((m - top) * sl);   // from -inf: O and l are zero
+                        m = top;
                     }
-                }
-                const float ms = m == -INFINITY ? 0.f : m * sl;
-                float sum = 0.f;
+                    if (mine > 0 && __any_sync(0xffffffffu, grow)) {
+                        ok = tr_wait(&o_full[s], (tiles_done - 1) & 1, p.err, ok, lane);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c0 = 0; c0 < D; c0 += 32) {
+                            float o[32];
+                            uint32_t u[32];
+                            tmem_ld32(to + c0, o);
 #pragma unroll
-                for (int c0 = 0; c0 < 128; c0 += 64) {
-                    uint32_t u[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float a = fast_exp2(fmaf(__uint_as_float(v[c0 + 2 * i]), sl, -ms));
-                        const float b = fast_exp2(fmaf(__uint_as_float(v[c0 + 2 * i + 1]), sl, -ms));
-                        sum += a + b;
-                        u[i] = pack_bf16(a, b);
+                            for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(o[i] * f);
+                            tmem_st32(to + c0, u);
+                        }
                     }
-                    tmem_st32(ts + c0 / 2, u);
+                    const float ms = m == -INFINITY ? 0.f : m * sl;
+                    const uint64_t sl2 = pair(sl, sl), ms2 = pair(-ms, -ms);
+                    uint64_t sum2[2] = {0, 0};
+#pragma unroll
+                    for (int c0 = 0; c0 < 128; c0 += 32) {
+                        uint32_t u[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 x = apart(fma2(pair(v[c0 + 2 * i], v[c0 + 2 * i + 1]), sl2, ms2));
+                            const float a = fast_exp2(x.x), b = fast_exp2(x.y);
+                            sum2[i & 1] = add2(sum2[i & 1], pair(a, b));
+                            u[i] = pack_bf16(a, b);
+                        }
+                        tmem_st16(ts + c0 / 2, u);
+                    }
+                    const float2 sum = apart(add2(sum2[0], sum2[1]));
+                    l = l * f + (sum.x + sum.y);
                 }
-                l = l * f + sum;
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();

@@ -117,13 +117,11 @@ def test_binding_refuses_tensors_of_the_host(lib):
 
 
 def test_binding_refuses_layouts_it_cannot_pass_on(lib, monkeypatch):
-    """Token rows need dense heads and one stride; shapes have to agree.  The device checks, which
-    come first, are taken out, and a library that answers nothing stands in for the calls."""
+    """Token rows need dense heads and one stride; shapes have to agree."""
     import torch
     cpu = torch.device("cpu")
-    monkeypatch.setattr(binding, "_need", lambda *a, **k: None)
     x = torch.zeros((3, 5, 6, 64), dtype=torch.bfloat16)
-    monkeypatch.setattr(torch.Tensor, "is_cuda", True, raising=False)
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True, raising=False)   # the device check comes first
     assert binding._tokens(x, "x", cpu, 3, 5, 64) == (6, 384)
     assert binding._tokens(x[:, :, 2:4], "x", cpu, 3, 5, 64) == (2, 384)
     assert binding._tokens(x[:1, :1], "x", cpu, 1, 1, 64) == (6, 384)
@@ -133,9 +131,11 @@ def test_binding_refuses_layouts_it_cannot_pass_on(lib, monkeypatch):
             binding._tokens(bad, "x", cpu, bad.shape[0], bad.shape[1], 64)
     with pytest.raises(TypeError):
         binding._tokens(x.float(), "x", cpu, 3, 5, 64)
+    i = torch.int32
     with pytest.raises(ValueError, match="block_table"):
-        binding._paged_cache(x, x, torch.zeros((2, 4), dtype=torch.int32), torch.zeros(3, dtype=torch.int32), 3, cpu)
-    with pytest.raises(ValueError, match="seq_len"):
-        binding._paged_cache(x, x, torch.zeros((3, 4), dtype=torch.int32), torch.zeros(2, dtype=torch.int32), 3, cpu)
+        binding._paged_cache(x, x, torch.zeros((2, 4), dtype=i), 3, cpu)
     with pytest.raises(ValueError, match="v_pages"):
-        binding._paged_cache(x, x[1:], torch.zeros((3, 4), dtype=torch.int32), torch.zeros(3, dtype=torch.int32), 3, cpu)
+        binding._paged_cache(x, x[1:], torch.zeros((3, 4), dtype=i), 3, cpu)
+    with pytest.raises(ValueError, match="k_pages"):
+        binding._paged_cache(x[None], x[None], torch.zeros((3, 4), dtype=i), 3, cpu)
+    assert binding._paged_cache(x[None], x[None], torch.zeros((3, 4), dtype=i), 3, cpu, 5)[3:] == (5, 3, 4, 6, 64)
