@@ -111,8 +111,8 @@ int *device_error_word() {
     return cache[dev];
 }
 
-bool encode_tmap_bf16_4d(CUtensorMap *map, const void *base, const uint64_t dims[4], const uint64_t strides[3],
-                         const uint32_t box[4]) {
+bool encode_tmap_bf16(CUtensorMap *map, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
+                      const uint32_t *box) {
     static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
@@ -124,14 +124,24 @@ bool encode_tmap_bf16_4d(CUtensorMap *map, const void *base, const uint64_t dims
             encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     });
     if (!encode) return false;
-    cuuint64_t gd[4] = {dims[0], dims[1], dims[2], dims[3]};
-    cuuint64_t gs[3] = {strides[0], strides[1], strides[2]};
-    cuuint32_t bx[4] = {box[0], box[1], box[2], box[3]};
-    cuuint32_t es[4] = {1, 1, 1, 1};
-    CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), gd, gs, bx, es,
+    if (rank < 2 || rank > 5) return false;
+    cuuint64_t gd[5], gs[4];
+    cuuint32_t bx[5], es[5];
+    for (int i = 0; i < rank; ++i) {
+        gd[i] = dims[i];
+        bx[i] = box[i];
+        es[i] = 1;
+        if (i + 1 < rank) gs[i] = strides[i];
+    }
+    CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), gd, gs, bx, es,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
+}
+
+bool encode_tmap_bf16_4d(CUtensorMap *map, const void *base, const uint64_t dims[4], const uint64_t strides[3],
+                         const uint32_t box[4]) {
+    return encode_tmap_bf16(map, base, 4, dims, strides, box);
 }
 
 }  // namespace magicdec_host

@@ -159,6 +159,17 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *tm, in
         : "memory");
 }
 
+// The same for a 5-D box.
+__device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *tm, int c0, int c1, int c2, int c3, int c4,
+                                            uint64_t *bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar)),
+        "l"(policy)
+        : "memory");
+}
+
 // Prefetch one tiled 4-D box into L2 (no shared memory, no barrier: a hint).
 __device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap *tm, int c0, int c1, int c2, int c3) {
     asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
@@ -414,8 +425,12 @@ int max_smem_optin();
 // Device address of the library's error word on the current device.
 int *device_error_word();
 
-// Encode a 4-D bf16 tensor map (dims innermost first, byte strides of dims
-// 1..3) with 128-byte swizzle and zero fill out of bounds.  False on failure.
+// Encode a bf16 tensor map of 2 to 5 dimensions (innermost first, byte strides
+// of all but the first) with 128-byte swizzle and zero fill out of bounds.
+// False on failure.
+bool encode_tmap_bf16(CUtensorMap *map, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
+                      const uint32_t *box);
+// The same for 4 dimensions.
 bool encode_tmap_bf16_4d(CUtensorMap *map, const void *base, const uint64_t dims[4], const uint64_t strides[3],
                          const uint32_t box[4]);
 

@@ -12,7 +12,8 @@
 // HBM busy while the tensor cores idle, above, the other way round.
 //
 // A row tile is 128 rows: NB = 128 / G whole nodes.  A CTA holds two streams,
-// each with its own S, O (TMEM) and softmax warpgroup, one thread per row:
+// each with its own S, O (TMEM) and two softmax warpgroups, one per half of the
+// keys of a tile (a thread: one row, 64 keys):
 //   one row tile  (n <= NB): the streams take the even and odd key tiles, so one
 //     softmax runs while the other's products do; their O are merged at the end;
 //   two row tiles (n > NB):  each stream owns a row tile and sees every key tile;
@@ -26,17 +27,18 @@
 // does not own whole goes to the workspace as (O, max, sum) and is joined by a
 // second kernel in a fixed order.  No atomics: results do not change from run to run.
 //
-// Roles (384 threads): warp 0 issues the TMA boxes, warp 1 the MMAs, warps 4-7
-// and 8-11 are the two softmax warpgroups, which take over the registers that the
-// first one gives up.  Every wait is bounded; after one that
+// Roles (640 threads): warp 0 issues the TMA boxes, warp 1 the MMAs, warps 4-11
+// and 12-19 are the softmax of the two streams, which take over registers that the
+// first warpgroup gives up.  Every wait is bounded; after one that
 // gave up (error 1) the roles run on without waiting, so that all of them end.
 #include "common.cuh"
 
 namespace magicdec {
 
-constexpr int kTrThreads = 384;
+constexpr int kTrThreads = 640;
 constexpr int kTrKeys = 128;                  // keys per tile
 constexpr int kTrBox = kTrKeys * 128;         // 128 rows x 64 channels (16 KB)
+constexpr int kTrBoxRows = 64;                // most rows of a TMA box
 constexpr int kTrMaxNodes = 256;
 constexpr int kTrOut = 256;                   // first TMEM column of O (S: 0 and 128)
 constexpr float kTrLazy = 8.0f;               // log2 growth of a row's maximum that is put up with
@@ -60,20 +62,36 @@ struct TreeAttnParams {
     int ppt;               // pages per key tile (pages of at most 128 rows), else 0
     int tpp;               // key tiles per page (larger pages)
     int grid;
+    int br;                // rows of a box
+    int by8;               // pages of a multiple of 8 rows: copied by 5-D boxes
+    uint32_t sbo, hoff;    // bytes between groups of 8 rows, and between 64-channel halves, of a K or V tile
     float scale_log2;      // log2(e) / sqrt(d)
 };
 
 __device__ __forceinline__ int tr_clamp(int v, int hi) { return v < 0 ? 0 : (v > hi ? hi : v); }
 
 // ---------------------------------------------------------------- tcgen05 forms
-// V as the B operand [keys x channels], channels contiguous (MN-major): rows of
-// 64 channels (128 bytes), 8 keys per swizzle atom, 1024 bytes between groups of 8
-// keys (SBO) and one box between groups of 64 channels (LBO).
-__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr) {
+// A K or V tile in shared memory: rows of 64 channels (128 bytes, swizzled), groups of
+// 8 rows `sbo` apart, the two halves of 128 channels `hoff` apart.  Pages of a multiple of
+// 8 rows are copied whole, [group][half][8 rows], by one box; other pages half by half,
+// [half][rows].
+// K is K-major: a row is a key's channels, the reduction runs along it.
+__device__ __forceinline__ uint64_t desc_k(uint32_t saddr, uint32_t sbo) {
     uint64_t d = 0;
     d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-    d |= (uint64_t)(kTrBox >> 4) << 16;
-    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1u << 16;                   // leading byte offset (unused for swizzled K-major)
+    d |= (uint64_t)(sbo >> 4) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)2u << 61;
+    return d;
+}
+// V is MN-major: the reduction runs over the rows, 64 channels of a row lie together,
+// the next 64 the leading byte offset further.
+__device__ __forceinline__ uint64_t desc_v(uint32_t saddr, uint32_t sbo, uint32_t hoff) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)(hoff >> 4) << 16;
+    d |= (uint64_t)(sbo >> 4) << 32;
     d |= (uint64_t)1u << 46;
     d |= (uint64_t)2u << 61;
     return d;
@@ -90,39 +108,34 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
         : "memory");
 }
 
-// 32 columns of this thread's TMEM lane without the completion wait of tmem_ld32.
 #define TR_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), \
     "=r"(r[i + 6]), "=r"(r[i + 7])
 #define TR_W8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), \
     "r"(r[i + 6]), "r"(r[i + 7])
 
-// All 128 columns of S: four loads and their completion in one statement, so that
-// no use of a register can be moved before the wait.
-__device__ __forceinline__ void tmem_ld128(uint32_t taddr, uint32_t (&r)[128]) {
+// 64 columns of S: two loads and their completion in one statement, so that no use
+// of a register can be moved before the wait.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%128];\n\t"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,"
-        "%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%129];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,%80,"
-        "%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95}, [%130];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,"
-        "%110,%111,%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%131];\n\t"
+        "%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : TR_R8(r, 0), TR_R8(r, 8), TR_R8(r, 16), TR_R8(r, 24), TR_R8(r, 32), TR_R8(r, 40), TR_R8(r, 48), TR_R8(r, 56),
-          TR_R8(r, 64), TR_R8(r, 72), TR_R8(r, 80), TR_R8(r, 88), TR_R8(r, 96), TR_R8(r, 104), TR_R8(r, 112),
-          TR_R8(r, 120)
-        : "r"(taddr), "r"(taddr + 32), "r"(taddr + 64), "r"(taddr + 96)
+        : TR_R8(r, 0), TR_R8(r, 8), TR_R8(r, 16), TR_R8(r, 24), TR_R8(r, 32), TR_R8(r, 40), TR_R8(r, 48), TR_R8(r, 56)
+        : "r"(taddr), "r"(taddr + 32)
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-        TR_W8(r, 0), TR_W8(r, 8), TR_W8(r, 16), TR_W8(r, 24)
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : TR_R8(r, 0), TR_R8(r, 8)
+        : "r"(taddr)
         : "memory");
 }
+
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
@@ -132,10 +145,38 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Registers per thread from here on, for the whole warpgroup.  384 threads start with
-// 168 each; 80 + 208 + 208 is within 3 * 168.
-__device__ __forceinline__ void regs_give() { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); }
-__device__ __forceinline__ void regs_take() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
+// One thread of a converged warp, the same each time.  The compiler knows a branch on it
+// for uniform, and keeps descriptors in uniform registers: with a branch on the lane
+// number it moved them there one by one, 150 cycles a product instead of the 64 that it
+// takes (8 products: 1250 -> 560 cycles).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(x));
+    return x != 0;
+}
+
+// Registers per thread from here on, for the whole warpgroup.  640 threads start with
+// 96 each; 64 + 4 * 104 is 5 * 96.
+__device__ __forceinline__ void regs_give() { asm volatile("setmaxnreg.dec.sync.aligned.u32 64;"); }
+__device__ __forceinline__ void regs_take() { asm volatile("setmaxnreg.inc.sync.aligned.u32 104;"); }
+
+// Whether x holds for any of the 64 threads of two warps; a barrier for them, too.
+__device__ __forceinline__ bool pair_any(int id, bool x) {
+    int got;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.s32 p, %2, 0;\n\t"
+        "barrier.cta.red.or.pred q, %1, 64, p;\n\t"
+        "selp.s32 %0, 1, 0, q;\n\t}"
+        : "=r"(got)
+        : "r"(id), "r"((int)x)
+        : "memory");
+    return got != 0;
+}
 
 // Two fp32 values in one 64-bit register: one instruction for both.
 __device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
@@ -247,8 +288,8 @@ struct TrSmem {
     static constexpr int HALVES = D / 64;
     static constexpr int OPER = HALVES * kTrBox;                         // a K or V tile, or a row tile of Q
     static constexpr int STAGES = D == 128 ? 5 : 10;
-    static constexpr int BYTES = 1024 + RT * OPER + STAGES * OPER + 2 * kTrMaxNodes + (RT == 1 ? 2 * 128 * 8 : 0) +
-                                 (2 * STAGES + 9) * 8 + 64;
+    static constexpr int XCH = 2 * 2 * 128 * 4 + (RT == 1 ? 2 * 128 * 4 : 0);
+    static constexpr int BYTES = RT * OPER + STAGES * OPER + 2 * kTrMaxNodes + XCH + (2 * STAGES + 9) * 8 + 16;
 };
 
 // Position in the ring of the K and V tile j of a run of cnt.  With one row tile the
@@ -258,11 +299,28 @@ __device__ __forceinline__ int ring_k(int j, int) { return RT == 1 ? (j < 2 ? j 
 template <int RT>
 __device__ __forceinline__ int ring_v(int j, int cnt) { return RT == 1 ? min(2 * j + 2, cnt + j) : 2 * j + 1; }
 
-// Lane 0 waits (bounded) and the warp agrees on the outcome; once a wait has given
-// up, the later ones return at once.
+// Bounded wait.  The clock is read only now and then: a read takes as long as the whole
+// wait does on the path from one product to the next (both sides measured: 32 trees of 64
+// nodes over 32k).
+__device__ __forceinline__ bool tr_poll(uint64_t *bar, uint32_t parity, int *err) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 1; i < kMaxPolls; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 1023u) == 0) {
+            const uint64_t t = globaltimer();
+            if (t0 == 0) t0 = t;
+            else if (t - t0 > kMaxWaitNs) break;
+        }
+    }
+    raise_error(err, kErrTimeout);
+    return false;
+}
+
+// Lane 0 waits and the warp agrees on the outcome; once a wait has given up, the later
+// ones return at once.
 __device__ __forceinline__ bool tr_wait(uint64_t *bar, uint32_t parity, int *err, bool ok, int lane) {
     int got = ok ? 1 : 0;
-    if (ok && lane == 0) got = mbar_wait(bar, parity, err) ? 1 : 0;
+    if (ok && lane == 0) got = tr_poll(bar, parity, err) ? 1 : 0;
     return __shfl_sync(0xffffffffu, got, 0) != 0;
 }
 
@@ -272,12 +330,12 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                      const __grid_constant__ CUtensorMap tmv, const TreeAttnParams p) {
     using L = TrSmem<D, RT>;
     constexpr int HALVES = L::HALVES, OPER = L::OPER, NST = L::STAGES, KS = D / 16;
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t smem[];      // swizzled tiles start at multiples of 1024
     uint8_t *qbuf = smem, *ring = smem + RT * OPER;
     uint8_t *par = ring + NST * OPER;                                    // [2][kTrMaxNodes]
-    float2 *xstat = reinterpret_cast<float2 *>(par + 2 * kTrMaxNodes);   // [2][128], one row tile only
-    uint64_t *full = reinterpret_cast<uint64_t *>(par + 2 * kTrMaxNodes + (RT == 1 ? 2 * 128 * 8 : 0));
+    float *xch = reinterpret_cast<float *>(par + 2 * kTrMaxNodes);       // [stream][half][128]
+    float *xmax = xch + 2 * 2 * 128;                                     // [stream][128], one row tile only
+    uint64_t *full = reinterpret_cast<uint64_t *>(par + 2 * kTrMaxNodes + L::XCH);
     uint64_t *empty = full + NST;
     uint64_t *q_full = empty + NST, *q_empty = q_full + 1;
     uint64_t *s_full = q_empty + 1, *p_full = s_full + 2, *o_full = p_full + 2;   // [2] each
@@ -285,6 +343,11 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
     int *found = reinterpret_cast<int *>(tmem_slot + 1);                 // b0, off0, run length
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (smem_u32(smem) & 1023u) {
+        if (tid == 0) raise_error(p.err, kErrState);
+        pdl_wait();
+        return;
+    }
 
     if (tid == 0) {
         for (int s = 0; s < NST; ++s) {
@@ -296,7 +359,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         mbar_init(mma_done, 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&s_full[s], 1);
-            mbar_init(&p_full[s], 4);
+            mbar_init(&p_full[s], 8);
             mbar_init(&o_full[s], 1);
         }
         mbar_fence_init();
@@ -391,33 +454,28 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 const uint32_t st = slot % NST, ph = (slot / NST) & 1;
                 uint8_t *dst = ring + st * OPER;
                 const int pg0 = t.p0 / p.page_size;
-                const int pages = p.ppt ? (t.rows + p.page_size - 1) / p.page_size : 1;
-                // The lane's page number is on its way while the warp waits for the ring.
-                int id = lane < pages ? ld_dep(table + pg0 + lane) : 0;
+                // Boxes of br rows: a page each, or parts of one page.  The lane's page number is
+                // on its way while the warp waits for the ring.
+                const int boxes = (t.rows + p.br - 1) / p.br, r0 = t.p0 - pg0 * p.page_size;
+                const bool pages = p.br == p.page_size;
+                int id = lane < boxes ? ld_dep(table + pg0 + (pages ? lane : 0)) : 0;
                 ok = tr_wait(&empty[st], ph ^ 1, p.err, ok, lane);
                 if (!ok) break;
                 const CUtensorMap *tm = is_v ? &tmv : &tmk;
-                if (p.ppt) {
-                    if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(pages * HALVES * p.page_size * 128));
-                    __syncwarp();
-                    for (int g = lane; g < pages; g += 32) {
-                        if (g >= 32) id = ld_dep(table + pg0 + g);
-                        if (id < 0 || id >= p.n_pages) {       // such a page is filled with zeros
-                            raise_error(p.err, kErrPage);
-                            id = p.n_pages;
-                        }
-                        for (int hf = 0; hf < HALVES; ++hf)
-                            tma_load_4d(dst + hf * kTrBox + g * p.page_size * 128, tm, hf * 64, r.h, 0, id, &full[st],
-                                        pol);
-                    }
-                } else if (lane == 0) {
-                    mbar_arrive_expect_tx(&full[st], OPER);
-                    if (id < 0 || id >= p.n_pages) {
+                if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(boxes * p.br * HALVES * 128));
+                __syncwarp();
+                for (int g = lane; g < boxes; g += 32) {
+                    if (g >= 32) id = ld_dep(table + pg0 + (pages ? g : 0));
+                    if (id < 0 || id >= p.n_pages) {       // such a page is filled with zeros
                         raise_error(p.err, kErrPage);
                         id = p.n_pages;
                     }
-                    for (int hf = 0; hf < HALVES; ++hf)
-                        tma_load_4d(dst + hf * kTrBox, tm, hf * 64, r.h, t.p0 - pg0 * p.page_size, id, &full[st], pol);
+                    const int at = g * p.br, pr = pages ? 0 : r0 + at;      // row in the tile, in the page
+                    if (p.by8)
+                        tma_load_5d(dst + at / 8 * (HALVES * 1024), tm, 0, 0, r.h * HALVES, pr / 8, id, &full[st], pol);
+                    else
+                        for (int hf = 0; hf < HALVES; ++hf)
+                            tma_load_4d(dst + hf * kTrBox + at * 128, tm, hf * 64, r.h, pr, id, &full[st], pol);
                 }
             }
             if (!ok) break;
@@ -437,30 +495,41 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         const uint32_t qb = smem_u32(qbuf), rb0 = smem_u32(ring);
         uint32_t slot0 = 0, runs = 0, done[2] = {0, 0};                  // done: tiles of each stream
 
+        const uint64_t kdesc = desc_k(rb0, p.sbo), vdesc = desc_v(rb0, p.sbo, p.hoff), qdesc = umma_desc_sw128(qb);
+        const uint32_t khalf = p.hoff >> 4, vstep = 2 * p.sbo >> 4;      // descriptor units of 16 bytes
+        auto stage = [&](uint32_t slot) {                                // of a ring slot, in the same units
+            return (uint64_t)__shfl_sync(0xffffffffu, (slot % NST) * (OPER >> 4), 0);
+        };
         auto scores = [&](int s, uint32_t slot) {                        // S_s = Q K^T
-            if (lane == 0) {
-                const uint32_t k = rb0 + (slot % NST) * OPER, q = qb + (RT == 2 ? s : 0) * OPER;
+            const uint64_t k = kdesc + stage(slot), q = qdesc + (RT == 2 ? s : 0) * (OPER >> 4);
+            if (elect_one()) {
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
-                    umma_bf16(tmem + s * 128, umma_desc_sw128(q + (ks >> 2) * kTrBox + (ks & 3) * 32),
-                              umma_desc_sw128(k + (ks >> 2) * kTrBox + (ks & 3) * 32), idesc_s, ks > 0);
+                    umma_bf16(tmem + s * 128, q + (ks >> 2) * (kTrBox >> 4) + (ks & 3) * 2,
+                              k + (ks >> 2) * khalf + (ks & 3) * 2, idesc_s, ks > 0);
                 umma_commit(&s_full[s]);
             }
             __syncwarp();
         };
         auto values = [&](int s, uint32_t slot, int rows, bool first) {  // O_s (+)= P V
-            if (lane == 0) {
-                const uint32_t v = rb0 + (slot % NST) * OPER;
-                const int steps = (rows + 15) / 16;
-                for (int ks = 0; ks < steps; ++ks)
-                    umma_bf16_ts(tmem + kTrOut + s * D, tmem + s * 128 + ks * 8, desc_mn_sw128(v + ks * 16 * 128),
-                                 idesc_o, !(first && ks == 0));
+            const uint64_t v = vdesc + stage(slot);
+            const uint32_t o = tmem + kTrOut + s * D, a = tmem + s * 128;
+            if (elect_one()) {
+                if (rows > kTrKeys - 16) {
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        umma_bf16_ts(o, a + ks * 8, v + ks * vstep, idesc_o, ks > 0 || !first);
+                } else {
+                    for (int ks = 0; ks * 16 < rows; ++ks)
+                        umma_bf16_ts(o, a + ks * 8, v + ks * vstep, idesc_o, ks > 0 || !first);
+                }
                 umma_commit(&o_full[s]);
             }
             __syncwarp();
         };
         auto release = [&](uint32_t slot) {
-            if (lane == 0) umma_commit(&empty[slot % NST]);
+            const uint32_t st = __shfl_sync(0xffffffffu, slot % NST, 0);
+            if (elect_one()) umma_commit(&empty[st]);
             __syncwarp();
         };
         auto arrived = [&](uint32_t slot) {
@@ -475,7 +544,9 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             uint8_t *v = ring + (slot % NST) * OPER;
             for (int i = lane; i < HALVES * (end - rows) * 8; i += 32) {
                 const int hf = i / ((end - rows) * 8), e = i - hf * (end - rows) * 8;
-                *reinterpret_cast<uint4 *>(v + hf * kTrBox + rows * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+                const int row = rows + e / 8;
+                *reinterpret_cast<uint4 *>(v + hf * p.hoff + (row >> 3) * p.sbo + (row & 7) * 128 + (e & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -493,7 +564,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     scores(j, slot0 + ring_k<RT>(j, cnt));
                     release(slot0 + ring_k<RT>(j, cnt));
                 }
-                if (cnt <= 2 && lane == 0) umma_commit(q_empty);
+                if (cnt <= 2 && elect_one()) umma_commit(q_empty);
                 for (int j = 0; j < cnt && ok; ++j) {
                     const int s = j & 1;
                     const uint32_t vs = slot0 + ring_v<RT>(j, cnt);
@@ -512,7 +583,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                         if (!ok) break;
                         scores(s, ks);
                         release(ks);
-                        if (j + 3 == cnt && lane == 0) umma_commit(q_empty);
+                        if (j + 3 == cnt && elect_one()) umma_commit(q_empty);
                     }
                 }
             } else {
@@ -521,7 +592,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 scores(0, slot0);
                 if (second) scores(1, slot0);
                 release(slot0);
-                if (cnt == 1 && lane == 0) umma_commit(q_empty);
+                if (cnt == 1 && elect_one()) umma_commit(q_empty);
                 for (int j = 0; j < cnt && ok; ++j) {
                     const uint32_t vs = slot0 + ring_v<RT>(j, cnt), ks = slot0 + ring_k<RT>(j + 1, cnt);
                     const int rows = tile_at(p, r.t0 + j, r.s.total).rows;
@@ -543,14 +614,15 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     release(vs);
                     if (j + 1 < cnt) {
                         release(ks);
-                        if (j + 2 == cnt && lane == 0) umma_commit(q_empty);
+                        if (j + 2 == cnt && elect_one()) umma_commit(q_empty);
                     }
                 }
             }
             slot0 += 2 * cnt;
         }
         // The products in flight end before the shared memory and TMEM that they use go.
-        if (lane == 0) {
+        __syncwarp();
+        if (elect_one()) {
             umma_commit(mma_done);
             mbar_wait(mma_done, 0, p.err);
         }
@@ -559,20 +631,21 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     } else {
         regs_take();
         // -------------------------------------------------------- softmax warpgroups
-        const int s = (warp - 4) >> 2;                       // stream
-        const int quad = warp & 3;                           // TMEM lanes 32 * quad ..
+        const int s = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1;    // stream, half of a tile's keys
+        const int quad = warp & 3;                                      // TMEM lanes 32 * quad ..
         const int row = 32 * quad + lane;
+        const int pair_bar = 1 + s * 4 + quad;                          // the two warps of 32 rows
         const uint32_t lane_addr = (uint32_t)(32 * quad) << 16;
         const uint32_t ts = tmem + lane_addr + s * 128, to = tmem + lane_addr + kTrOut + s * D;
-        const int wt = tid - 128 - s * 128;                  // thread of the warpgroup
-        const int node_r = row / p.G;                        // node within the row tile
+        const int wt = tid - 128 - s * 256;                             // thread of the stream
+        const int node_r = row / p.G;                                   // node within the row tile
         const float sl = p.scale_log2;
         uint8_t *mypar = par + s * kTrMaxNodes;
+        float *mine_x = xch + (s * 2 + half) * 128 + row, *other_x = xch + (s * 2 + 1 - half) * 128 + row;
         uint32_t tiles_done = 0;
         int par_b = -1;
         bool first_run = true;
         while (walk.next(p, r)) {
-            const bool whole = r.cnt == r.s.tiles;
             const int base = (r.rb * RT + (RT == 2 ? s : 0)) * p.NB;      // first node of the row tile
             const int node = node_r < p.NB && base + node_r < r.s.nodes ? base + node_r : -1;
             const bool active = RT == 1 || base < r.s.nodes;
@@ -580,42 +653,44 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             if (p.parent && par_b != r.b) {
                 // parent + 1 of every node in a byte (0: none); a parent that is not before its
                 // node counts as none.
-                named_bar_sync(2 + s, 128);
-                for (int i = wt; i < r.s.nodes; i += 128) {
-                    const int pi = checked(ld_dep(p.parent + (long long)r.b * p.n + i), -1, i - 1, p.err);
-                    mypar[i] = (uint8_t)(pi >= 0 && pi < i ? pi + 1 : 0);
+                named_bar_sync(9 + s, 256);
+                if (wt < r.s.nodes) {
+                    const int pi = checked(ld_dep(p.parent + (long long)r.b * p.n + wt), -1, wt - 1, p.err);
+                    mypar[wt] = (uint8_t)(pi >= 0 && pi < wt ? pi + 1 : 0);
                 }
-                named_bar_sync(2 + s, 128);
+                named_bar_sync(9 + s, 256);
                 par_b = r.b;
             }
-            float m = -INFINITY, l = 0.f;
+            float m = -INFINITY, l = 0.f;                    // m: of the row, l: of this half's keys
             int mine = 0;                                    // tiles of this run that this stream had
             for (int j = RT == 1 ? s : 0; active && j < r.cnt; j += RT == 1 ? 2 : 1) {
                 const Tile t = tile_at(p, r.t0 + j, r.s.total);
                 ok = tr_wait(&s_full[s], tiles_done & 1, p.err, ok, lane);
                 tc_fence_after();
                 if (live) {
-                    uint32_t v[128];
-                    tmem_ld128(ts, v);
+                    uint32_t v[64];
+                    tmem_ld64(ts + half * 64, v);
                     if (t.rows < kTrKeys || t.p0 + t.rows > r.s.len) {
-                        uint32_t see[4];
+                        const int k0 = t.p0 + half * 64;                  // position of this half's first key
+                        const int rows = t.rows - half * 64;
+                        uint32_t see[2];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int c = min(r.s.len - t.p0, t.rows) - 32 * k;
+                        for (int k = 0; k < 2; ++k) {
+                            const int c = min(r.s.len - k0, rows) - 32 * k;
                             see[k] = node < 0 || c <= 0 ? 0u : c >= 32 ? 0xffffffffu : (1u << c) - 1u;
                         }
-                        if (node >= 0 && t.p0 + t.rows > r.s.len) {
+                        if (node >= 0 && k0 + rows > r.s.len) {
                             for (int a = node; a >= 0; a = p.parent ? (int)mypar[a] - 1 : a - 1) {
-                                const int off = r.s.len + a - t.p0;
-                                if (off >= 0 && off < t.rows) {
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k)
-                                        if ((off >> 5) == k) see[k] |= 1u << (off & 31);
+                                const int off = r.s.len + a - k0;
+                                if (off < 0) break;                       // ancestors come before their nodes
+                                if (off < rows && off < 64) {
+                                    if (off < 32) see[0] |= 1u << off;
+                                    else see[1] |= 1u << (off - 32);
                                 }
                             }
                         }
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
+                        for (int k = 0; k < 2; ++k) {
                             if (__all_sync(0xffffffffu, see[k] == 0xffffffffu)) continue;
 #pragma unroll
                             for (int c = 0; c < 32; ++c)
@@ -627,39 +702,44 @@ __global__ void __launch_bounds__(kTrThreads, 1)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) t4[c] = __uint_as_float(v[c]);
 #pragma unroll
-                    for (int c = 4; c < 124; c += 8)
+                    for (int c = 4; c < 60; c += 8)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             t4[i] = fmaxf(t4[i], fmaxf(__uint_as_float(v[c + i]), __uint_as_float(v[c + 4 + i])));
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) t4[i] = fmaxf(t4[i], __uint_as_float(v[124 + i]));
-                    const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+                    for (int i = 0; i < 4; ++i) t4[i] = fmaxf(t4[i], __uint_as_float(v[60 + i]));
+                    float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
                     // The maximum is moved, and O scaled, only where it has grown by more than
-                    // 2^kTrLazy: sums then stay below 2^kTrLazy * keys, far inside fp32.
-                    const bool grow = top > m && (top - m) * sl > kTrLazy;
+                    // 2^kTrLazy: sums then stay below 2^kTrLazy * keys, far inside fp32.  Both
+                    // halves of a row have to agree; the barrier also puts the loads of S by
+                    // both before the stores of P over it.
                     float f = 1.f;
-                    if (grow) {
-                        f = m == -INFINITY ? 1.f : fast_exp2((m - top) * sl);   // from -inf: O and l are zero
-                        m = top;
-                    }
-                    if (mine > 0 && __any_sync(0xffffffffu, grow)) {
-                        ok = tr_wait(&o_full[s], (tiles_done - 1) & 1, p.err, ok, lane);
-                        tc_fence_after();
+                    if (pair_any(pair_bar, top > m && (top - m) * sl > kTrLazy)) {
+                        *mine_x = top;
+                        named_bar_sync(pair_bar, 64);
+                        top = fmaxf(top, *other_x);
+                        if (top > m && (top - m) * sl > kTrLazy) {
+                            f = m == -INFINITY ? 1.f : fast_exp2((m - top) * sl);   // from -inf: O and l are zero
+                            m = top;
+                        }
+                        if (mine > 0) {
+                            ok = tr_wait(&o_full[s], (tiles_done - 1) & 1, p.err, ok, lane);
+                            tc_fence_after();
 #pragma unroll 1
-                        for (int c0 = 0; c0 < D; c0 += 32) {
-                            float o[32];
-                            uint32_t u[32];
-                            tmem_ld32(to + c0, o);
+                            for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(to + c0, o);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(o[i] * f);
-                            tmem_st32(to + c0, u);
+                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                tmem_st16(to + c0, o);
+                            }
                         }
                     }
                     const float ms = m == -INFINITY ? 0.f : m * sl;
                     const uint64_t sl2 = pair(sl, sl), ms2 = pair(-ms, -ms);
                     uint64_t sum2[2] = {0, 0};
 #pragma unroll
-                    for (int c0 = 0; c0 < 128; c0 += 32) {
+                    for (int c0 = 0; c0 < 64; c0 += 32) {
                         uint32_t u[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
@@ -668,12 +748,12 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                             sum2[i & 1] = add2(sum2[i & 1], pair(a, b));
                             u[i] = pack_bf16(a, b);
                         }
-                        tmem_st16(ts + c0 / 2, u);
+                        tmem_st16(ts + half * 32 + c0 / 2, u);
                     }
                     const float2 sum = apart(add2(sum2[0], sum2[1]));
                     l = l * f + (sum.x + sum.y);
+                    tmem_wait_st();
                 }
-                tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[s]);
@@ -682,63 +762,76 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             }
             // The end of the run: O / l if the run is the whole list entry, else a partial.
             if (mine > 0) ok = tr_wait(&o_full[s], (tiles_done - 1) & 1, p.err, ok, lane);
-            tc_fence_after();
             const int part = 2 * blockIdx.x + (first_run ? 0 : 1);
             first_run = false;
-            float w0 = 1.f, w1 = 0.f, mm = m, ll = l;
-            int c_lo = 0, c_hi = D;
+            // The halves' sums, and with one row tile both streams' maxima: each warp then
+            // joins what it needs for its share of the channels.
             if (RT == 1) {
-                // Each warpgroup joins both streams for one half of the channels.
-                xstat[s * 128 + row] = make_float2(m, l);
+                named_bar_sync(11, 512);
+                *mine_x = l;
+                if (half == 0) xmax[s * 128 + row] = m;
                 tc_fence_before();
-                named_bar_sync(1, 256);
-                tc_fence_after();
-                const float2 e = xstat[row], o = xstat[128 + row];
-                mm = fmaxf(e.x, o.x);
-                const float mu = mm == -INFINITY ? 0.f : mm;
-                w0 = fast_exp2((e.x - mu) * sl);
-                w1 = r.cnt > 1 ? fast_exp2((o.x - mu) * sl) : 0.f;
-                ll = w0 * e.y + (r.cnt > 1 ? w1 * o.y : 0.f);
-                c_lo = s * (D / 2);
-                c_hi = c_lo + D / 2;
+                named_bar_sync(11, 512);
+            } else {
+                named_bar_sync(pair_bar, 64);
+                *mine_x = l;
+                named_bar_sync(pair_bar, 64);
             }
+            tc_fence_after();
+            float w0 = 1.f, w1 = 0.f, mm = m, ll;
+            if (RT == 1) {
+                const float m0 = xmax[row], m1 = r.cnt > 1 ? xmax[128 + row] : -INFINITY;
+                mm = fmaxf(m0, m1);
+                const float mu = mm == -INFINITY ? 0.f : mm;
+                w0 = fast_exp2((m0 - mu) * sl);
+                w1 = fast_exp2((m1 - mu) * sl);
+                ll = w0 * (xch[row] + xch[128 + row]);
+                if (r.cnt > 1) ll += w1 * (xch[256 + row] + xch[384 + row]);
+            } else {
+                ll = xch[s * 256 + row] + xch[s * 256 + 128 + row];
+            }
+            const bool whole = r.cnt == r.s.tiles;
             const float inv = ll > 0.f ? 1.f / ll : 0.f;
             uint16_t *dst = p.out + (((long long)r.b * p.n + node) * p.H_q + r.h * p.G + (row - node_r * p.G)) * D;
             const int rt = RT == 2 ? s : 0;
             float4 *pd = p.part + ((long long)part * RT + rt) * (D / 4) * 128 + row;
-            for (int c0 = c_lo; active && c0 < c_hi; c0 += 32) {
-                float o[32];
-                if (RT == 1) {
-                    float o1[32];
-                    tmem_ld32(tmem + lane_addr + kTrOut + c0, o);
-                    if (r.cnt > 1) tmem_ld32(tmem + lane_addr + kTrOut + D + c0, o1);
+            constexpr int SHARE = RT == 1 ? D / 4 : D / 2;               // channels of a warp
+            const int c_lo = RT == 1 ? (s * 2 + half) * SHARE : half * SHARE;
+#pragma unroll 1
+            for (int c0 = c_lo; live && c0 < c_lo + SHARE; c0 += 16) {
+                uint32_t o[16];
+                float x[16];
+                tmem_ld16((RT == 1 ? tmem + lane_addr + kTrOut : to) + c0, o);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = r.cnt > 1 ? w0 * o[i] + w1 * o1[i] : w0 * o[i];
-                } else {
-                    tmem_ld32(to + c0, o);
+                for (int i = 0; i < 16; ++i) x[i] = w0 * __uint_as_float(o[i]);
+                if (RT == 1 && r.cnt > 1) {
+                    tmem_ld16(tmem + lane_addr + kTrOut + D + c0, o);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] += w1 * __uint_as_float(o[i]);
                 }
                 if (node < 0) continue;
                 if (whole) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        uint4 x;
-                        x.x = pack_bf16(o[i] * inv, o[i + 1] * inv);
-                        x.y = pack_bf16(o[i + 2] * inv, o[i + 3] * inv);
-                        x.z = pack_bf16(o[i + 4] * inv, o[i + 5] * inv);
-                        x.w = pack_bf16(o[i + 6] * inv, o[i + 7] * inv);
-                        *reinterpret_cast<uint4 *>(dst + c0 + i) = x;
+                    for (int i = 0; i < 16; i += 8) {
+                        uint4 y;
+                        y.x = pack_bf16(x[i] * inv, x[i + 1] * inv);
+                        y.y = pack_bf16(x[i + 2] * inv, x[i + 3] * inv);
+                        y.z = pack_bf16(x[i + 4] * inv, x[i + 5] * inv);
+                        y.w = pack_bf16(x[i + 6] * inv, x[i + 7] * inv);
+                        *reinterpret_cast<uint4 *>(dst + c0 + i) = y;
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        pd[(c0 + i) / 4 * 128] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    for (int i = 0; i < 16; i += 4)
+                        pd[(c0 + i) / 4 * 128] = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
                 }
             }
-            if (!whole && node >= 0 && (RT == 2 || s == 0))
+            if (!whole && node >= 0 && c_lo == 0)
                 p.stat[(long long)part * RT * 128 + rt * 128 + row] = make_float2(mm, ll);
             tc_fence_before();
-            if (RT == 1) named_bar_sync(1, 256);       // both O are free for the next run
-            else __syncwarp();
+            // O is free for the next run, whose first P says so: with one row tile, once all
+            // warps have read both.
+            if (RT == 1) named_bar_sync(11, 512);
         }
     }
     tc_fence_before();
@@ -864,19 +957,33 @@ magicdec_status launch_tree_attn(const magicdec_paged_shape &s, int n, const uin
     w += tr_align(slots * RT * 128 * sizeof(float2));
     p.part = reinterpret_cast<float4 *>(w);
 
-    // The pool as (d, H_kv, page_size, n_pages), boxes of 64 channels x a page (or 128
-    // rows of it); queries as (d, H_q, n, B), one box = NB nodes of a KV head's group.
+    // Queries as (d, H_q, n, B), one box = NB nodes of a KV head's group.  The pool with
+    // pages of a multiple of 8 rows as (64 channels, 8 rows, halves of all heads, groups of 8
+    // rows, pages): one box is a page (or 64 rows of it) of one KV head, its channels read
+    // together and its rows laid out for the tensor cores.  Other pages as (d, H_kv,
+    // page_size, n_pages), boxes of 64 channels x a page (or 64 rows).
     CUtensorMap tmq, tmk, tmv;
-    const int D = s.d;
-    const uint64_t kd[4] = {(uint64_t)D, (uint64_t)s.H_kv, (uint64_t)s.page_size, (uint64_t)s.n_pages};
-    const uint64_t ks[3] = {(uint64_t)D * 2, (uint64_t)s.H_kv * D * 2, (uint64_t)s.page_size * s.H_kv * D * 2};
-    const uint32_t kb[4] = {64, 1, (uint32_t)(s.page_size < kTrKeys ? s.page_size : kTrKeys), 1};
+    const int D = s.d, HV = D / 64;
+    p.by8 = s.page_size % 8 == 0;
+    p.sbo = p.by8 ? HV * 1024 : 1024;
+    p.hoff = p.by8 ? 1024 : kTrBox;
+    const uint64_t row = (uint64_t)s.H_kv * D * 2;
+    p.br = s.page_size < kTrBoxRows ? s.page_size : kTrBoxRows;
+    const uint32_t span = (uint32_t)p.br;
+    const uint64_t kd4[4] = {(uint64_t)D, (uint64_t)s.H_kv, (uint64_t)s.page_size, (uint64_t)s.n_pages};
+    const uint64_t ks4[3] = {(uint64_t)D * 2, row, s.page_size * row};
+    const uint32_t kb4[4] = {64, 1, span, 1};
+    const uint64_t kd5[5] = {64, 8, (uint64_t)s.H_kv * HV, (uint64_t)s.page_size / 8, (uint64_t)s.n_pages};
+    const uint64_t ks5[4] = {row, 128, 8 * row, s.page_size * row};
+    const uint32_t kb5[5] = {64, 8, (uint32_t)HV, span / 8, 1};
     const uint64_t qd[4] = {(uint64_t)D, (uint64_t)s.H_q, (uint64_t)n, (uint64_t)s.B};
     const uint64_t qs[3] = {(uint64_t)D * 2, (uint64_t)s.H_q * D * 2, (uint64_t)n * s.H_q * D * 2};
     const uint32_t qbx[4] = {64, (uint32_t)p.G, (uint32_t)p.NB, 1};
-    if (!magicdec_host::encode_tmap_bf16_4d(&tmk, kp, kd, ks, kb) ||
-        !magicdec_host::encode_tmap_bf16_4d(&tmv, vp, kd, ks, kb) ||
-        !magicdec_host::encode_tmap_bf16_4d(&tmq, q, qd, qs, qbx))
+    auto pool = [&](CUtensorMap *m, const uint16_t *x) {
+        return p.by8 ? magicdec_host::encode_tmap_bf16(m, x, 5, kd5, ks5, kb5)
+                     : magicdec_host::encode_tmap_bf16(m, x, 4, kd4, ks4, kb4);
+    };
+    if (!pool(&tmk, kp) || !pool(&tmv, vp) || !magicdec_host::encode_tmap_bf16_4d(&tmq, q, qd, qs, qbx))
         return MAGICDEC_ERR_CUDA;
     if (D == 128)
         return RT == 1 ? launch_tree_t<128, 1>(tmq, tmk, tmv, p, st) : launch_tree_t<128, 2>(tmq, tmk, tmv, p, st);
