@@ -27,7 +27,7 @@
 // does not own whole goes to the workspace as (O, max, sum) and is joined by a
 // second kernel in a fixed order.  No atomics: results do not change from run to run.
 //
-// Roles (640 threads): warp 0 issues the TMA boxes, warp 1 the MMAs, warps 4-11
+// Roles (640 threads): warps 0, 2 and 3 issue the TMA boxes, warp 1 the MMAs, warps 4-11
 // and 12-19 are the softmax of the two streams, which take over registers that the
 // first warpgroup gives up.  Every wait is bounded; after one that
 // gave up (error 1) the roles run on without waiting, so that all of them end.
@@ -38,7 +38,6 @@ namespace magicdec {
 constexpr int kTrThreads = 640;
 constexpr int kTrKeys = 128;                  // keys per tile
 constexpr int kTrBox = kTrKeys * 128;         // 128 rows x 64 channels (16 KB)
-constexpr int kTrBoxRows = 64;                // most rows of a TMA box
 constexpr int kTrMaxNodes = 256;
 constexpr int kTrOut = 256;                   // first TMEM column of O (S: 0 and 128)
 constexpr float kTrLazy = 8.0f;               // log2 growth of a row's maximum that is put up with
@@ -420,16 +419,19 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     Run r;
     bool ok = true;
 
-    if (warp == 0) {
+    if (warp < 4 && warp != 1) {
         regs_give();
-        // ------------------------------------------------------------- TMA producer
+        // ------------------------------------------------------------ TMA producers
+        // Three warps, every third slot of the ring each: a box of the lanes' loop takes 60
+        // cycles to issue, which with small pages is as long as its data need.
+        const uint32_t pw = warp == 0 ? 0 : warp - 1;
         const uint64_t pol = p.n > RT * p.NB ? policy_evict_normal() : policy_evict_first();
         uint32_t slot = 0, runs = 0;                 // ring slots issued, runs begun
         while (walk.next(p, r)) {
-            ok = tr_wait(q_empty, (runs & 1) ^ 1, p.err, ok, lane);
-            if (!ok) break;
             const int tiles_q = RT == 2 && r.rb * 2 * p.NB + p.NB < r.s.nodes ? 2 : 1;
-            if (lane == 0) {
+            if (pw == 0) ok = tr_wait(q_empty, (runs & 1) ^ 1, p.err, ok, lane);
+            if (!ok) break;
+            if (pw == 0 && lane == 0) {
                 mbar_arrive_expect_tx(q_full, (uint32_t)(tiles_q * HALVES * p.NB * p.G * 128));
                 for (int t = 0; t < tiles_q; ++t)
                     for (int hf = 0; hf < HALVES; ++hf)
@@ -440,6 +442,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             const int32_t *table = p.table + (long long)r.b * p.max_pages;
             // K and V boxes in the order of the products.
             for (int i = 0; i < 2 * r.cnt; ++i, ++slot) {
+                if (slot % 3 != pw) continue;
                 int j, is_v;
                 if (RT == 1) {
                     if (i < 2 && i < r.cnt) { j = i; is_v = 0; }
@@ -483,9 +486,10 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         // No copy may be in flight when the CTA ends.
         __syncwarp();
         if (lane == 0) {
-            if (runs) mbar_wait(q_full, (runs - 1) & 1, p.err);
+            if (pw == 0 && runs) mbar_wait(q_full, (runs - 1) & 1, p.err);
             const uint32_t last = min(slot, (uint32_t)NST);
-            for (uint32_t i = slot - last; i < slot; ++i) mbar_wait(&full[i % NST], (i / NST) & 1, p.err);
+            for (uint32_t i = slot - last; i < slot; ++i)
+                if (i % 3 == pw) mbar_wait(&full[i % NST], (i / NST) & 1, p.err);
         }
     } else if (warp == 1) {
         regs_give();
@@ -626,8 +630,6 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             umma_commit(mma_done);
             mbar_wait(mma_done, 0, p.err);
         }
-    } else if (warp < 4) {
-        regs_give();
     } else {
         regs_take();
         // -------------------------------------------------------- softmax warpgroups
@@ -959,16 +961,16 @@ magicdec_status launch_tree_attn(const magicdec_paged_shape &s, int n, const uin
 
     // Queries as (d, H_q, n, B), one box = NB nodes of a KV head's group.  The pool with
     // pages of a multiple of 8 rows as (64 channels, 8 rows, halves of all heads, groups of 8
-    // rows, pages): one box is a page (or 64 rows of it) of one KV head, its channels read
+    // rows, pages): one box is a page (or 128 rows of it) of one KV head, its channels read
     // together and its rows laid out for the tensor cores.  Other pages as (d, H_kv,
-    // page_size, n_pages), boxes of 64 channels x a page (or 64 rows).
+    // page_size, n_pages), boxes of 64 channels x a page (or 128 rows).
     CUtensorMap tmq, tmk, tmv;
     const int D = s.d, HV = D / 64;
     p.by8 = s.page_size % 8 == 0;
     p.sbo = p.by8 ? HV * 1024 : 1024;
     p.hoff = p.by8 ? 1024 : kTrBox;
     const uint64_t row = (uint64_t)s.H_kv * D * 2;
-    p.br = s.page_size < kTrBoxRows ? s.page_size : kTrBoxRows;
+    p.br = s.page_size < kTrKeys ? s.page_size : kTrKeys;
     const uint32_t span = (uint32_t)p.br;
     const uint64_t kd4[4] = {(uint64_t)D, (uint64_t)s.H_kv, (uint64_t)s.page_size, (uint64_t)s.n_pages};
     const uint64_t ks4[3] = {(uint64_t)D * 2, row, s.page_size * row};
