@@ -13,13 +13,14 @@
 //
 // A row tile is 128 rows: NB = 128 / G whole nodes.  A CTA holds two streams,
 // each with its own S, O (TMEM) and two softmax warpgroups, one per half of the
-// keys of a tile (a thread: one row, 64 keys):
+// keys (a thread: one row, 32 keys at a time):
 //   one row tile  (n <= NB): the streams take the even and odd key tiles, so one
 //     softmax runs while the other's products do; their O are merged at the end;
 //   two row tiles (n > NB):  each stream owns a row tile and sees every key tile;
 //     K and V are read once for both (further pairs of tiles: other work items).
-// P overwrites S's columns as bf16 (the A operand of the second product comes
-// from TMEM).  P in bf16 costs a relative 2^-9 per probability, as much as the
+// A stream's S is in two parts of 64 keys, so that the scores of one are computed
+// while the softmax is at the other.  P overwrites S's columns as bf16 (the A operand
+// of the second product comes from TMEM).  P in bf16 is off by at most 2^-8 relative, as the
 // rounding of the output; sums, maxima and O are fp32.
 //
 // Work: the key tiles of all (sequence, KV head, row block), as one list, cut
@@ -27,9 +28,8 @@
 // does not own whole goes to the workspace as (O, max, sum) and is joined by a
 // second kernel in a fixed order.  No atomics: results do not change from run to run.
 //
-// Roles (640 threads): warps 0, 2 and 3 issue the TMA boxes, warp 1 the MMAs, warps 4-11
-// and 12-19 are the softmax of the two streams, which take over registers that the
-// first warpgroup gives up.  Every wait is bounded; after one that
+// Roles (640 threads): warps 0 and 3 issue the TMA boxes, warps 1 and 2 the MMAs, warps
+// 4-11 and 12-19 are the softmax of the two streams.  Every wait is bounded; after one that
 // gave up (error 1) the roles run on without waiting, so that all of them end.
 #include "common.cuh"
 
@@ -112,20 +112,15 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
 #define TR_W8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), \
     "r"(r[i + 6]), "r"(r[i + 7])
 
-// 64 columns of S: two loads and their completion in one statement, so that no use
-// of a register can be moved before the wait.
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
+__device__ __forceinline__ void tmem_ld32u(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,"
-        "%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : TR_R8(r, 0), TR_R8(r, 8), TR_R8(r, 16), TR_R8(r, 24), TR_R8(r, 32), TR_R8(r, 40), TR_R8(r, 48), TR_R8(r, 56)
-        : "r"(taddr), "r"(taddr + 32)
+        : TR_R8(r, 0), TR_R8(r, 8), TR_R8(r, 16), TR_R8(r, 24)
+        : "r"(taddr)
         : "memory");
 }
-
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
@@ -145,9 +140,8 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // One thread of a converged warp, the same each time.  The compiler knows a branch on it
-// for uniform, and keeps descriptors in uniform registers: with a branch on the lane
-// number it moved them there one by one, 150 cycles a product instead of the 64 that it
-// takes (8 products: 1250 -> 560 cycles).
+// for that of a single thread; with a branch on the lane number a product took 150 cycles
+// to issue instead of the 64 that it takes to run (8 products: 1250 -> 560 cycles).
 __device__ __forceinline__ bool elect_one() {
     uint32_t x;
     asm volatile(
@@ -157,11 +151,6 @@ __device__ __forceinline__ bool elect_one() {
         : "=r"(x));
     return x != 0;
 }
-
-// Registers per thread from here on, for the whole warpgroup.  640 threads start with
-// 96 each; 64 + 4 * 104 is 5 * 96.
-__device__ __forceinline__ void regs_give() { asm volatile("setmaxnreg.dec.sync.aligned.u32 64;"); }
-__device__ __forceinline__ void regs_take() { asm volatile("setmaxnreg.inc.sync.aligned.u32 104;"); }
 
 // Whether x holds for any of the 64 threads of two warps; a barrier for them, too.
 __device__ __forceinline__ bool pair_any(int id, bool x) {
@@ -175,6 +164,12 @@ __device__ __forceinline__ bool pair_any(int id, bool x) {
         : "r"(id), "r"((int)x)
         : "memory");
     return got != 0;
+}
+
+__device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+    return d;
 }
 
 // Two fp32 values in one 64-bit register: one instruction for both.
@@ -286,17 +281,15 @@ template <int D, int RT>
 struct TrSmem {
     static constexpr int HALVES = D / 64;
     static constexpr int OPER = HALVES * kTrBox;                         // a K or V tile, or a row tile of Q
-    static constexpr int STAGES = D == 128 ? 5 : 10;
-    static constexpr int XCH = 2 * 2 * 128 * 4 + (RT == 1 ? 2 * 128 * 4 : 0);
-    static constexpr int BYTES = RT * OPER + STAGES * OPER + 2 * kTrMaxNodes + XCH + (2 * STAGES + 9) * 8 + 16;
+    // Stages of a ring.  With one row tile a ring for each stream, so that a ring has one
+    // reader, and stays in order, whichever stream is ahead; else one ring for both, which
+    // frees a stage when both have read it.
+    static constexpr int RINGS = RT == 1 ? 2 : 1;
+    static constexpr int STAGES = (RT == 1 ? 3 : 5) * (D == 128 ? 1 : 2);
+    static constexpr int XCH = 2 * 2 * 128 * 4;
+    static constexpr int BYTES =
+        RT * OPER + RINGS * STAGES * OPER + 2 * kTrMaxNodes + XCH + (2 * RINGS * STAGES + 16) * 8 + 16;
 };
-
-// Position in the ring of the K and V tile j of a run of cnt.  With one row tile the
-// products are issued K0 K1 | V0 K2 | V1 K3 | ..., with two K0 | V0 K1 | V1 K2 ...
-template <int RT>
-__device__ __forceinline__ int ring_k(int j, int) { return RT == 1 ? (j < 2 ? j : 2 * j - 1) : 2 * j; }
-template <int RT>
-__device__ __forceinline__ int ring_v(int j, int cnt) { return RT == 1 ? min(2 * j + 2, cnt + j) : 2 * j + 1; }
 
 // Bounded wait.  The clock is read only now and then: a read takes as long as the whole
 // wait does on the path from one product to the next (both sides measured: 32 trees of 64
@@ -315,6 +308,12 @@ __device__ __forceinline__ bool tr_poll(uint64_t *bar, uint32_t parity, int *err
     return false;
 }
 
+// A number that a generic lambda takes as a compile-time constant.
+template <int N>
+struct Const {
+    __device__ constexpr operator int() const { return N; }
+};
+
 // Lane 0 waits and the warp agrees on the outcome; once a wait has given up, the later
 // ones return at once.
 __device__ __forceinline__ bool tr_wait(uint64_t *bar, uint32_t parity, int *err, bool ok, int lane) {
@@ -328,18 +327,18 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv, const TreeAttnParams p) {
     using L = TrSmem<D, RT>;
-    constexpr int HALVES = L::HALVES, OPER = L::OPER, NST = L::STAGES, KS = D / 16;
+    constexpr int HALVES = L::HALVES, OPER = L::OPER, NST = L::STAGES, ALL = L::RINGS * NST, KS = D / 16;
+    constexpr int STEP = RT == 1 ? 2 : 1;                  // tiles from one of a stream to its next
     extern __shared__ __align__(1024) uint8_t smem[];      // swizzled tiles start at multiples of 1024
     uint8_t *qbuf = smem, *ring = smem + RT * OPER;
-    uint8_t *par = ring + NST * OPER;                                    // [2][kTrMaxNodes]
+    uint8_t *par = ring + ALL * OPER;                                    // [2][kTrMaxNodes]
     float *xch = reinterpret_cast<float *>(par + 2 * kTrMaxNodes);       // [stream][half][128]
-    float *xmax = xch + 2 * 2 * 128;                                     // [stream][128], one row tile only
     uint64_t *full = reinterpret_cast<uint64_t *>(par + 2 * kTrMaxNodes + L::XCH);
-    uint64_t *empty = full + NST;
-    uint64_t *q_full = empty + NST, *q_empty = q_full + 1;
-    uint64_t *s_full = q_empty + 1, *p_full = s_full + 2, *o_full = p_full + 2;   // [2] each
-    uint64_t *mma_done = o_full + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
+    uint64_t *empty = full + ALL;
+    uint64_t *q_full = empty + ALL, *q_empty = q_full + 1;
+    uint64_t *s_full = q_empty + 1, *p_full = s_full + 4, *o_full = p_full + 4;   // [stream][half tile]
+    uint64_t *mma_done = o_full + 4;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 2);
     int *found = reinterpret_cast<int *>(tmem_slot + 1);                 // b0, off0, run length
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (smem_u32(smem) & 1023u) {
@@ -349,14 +348,15 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     }
 
     if (tid == 0) {
-        for (int s = 0; s < NST; ++s) {
+        for (int s = 0; s < ALL; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&empty[s], RT);
         }
         mbar_init(q_full, 1);
-        mbar_init(q_empty, 1);
-        mbar_init(mma_done, 1);
-        for (int s = 0; s < 2; ++s) {
+        mbar_init(q_empty, 2);
+        mbar_init(&mma_done[0], 1);
+        mbar_init(&mma_done[1], 1);
+        for (int s = 0; s < 4; ++s) {
             mbar_init(&s_full[s], 1);
             mbar_init(&p_full[s], 8);
             mbar_init(&o_full[s], 1);
@@ -419,14 +419,18 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     Run r;
     bool ok = true;
 
-    if (warp < 4 && warp != 1) {
-        regs_give();
+    if (warp == 0 || warp == 3) {
         // ------------------------------------------------------------ TMA producers
-        // Three warps, every third slot of the ring each: a box of the lanes' loop takes 60
-        // cycles to issue, which with small pages is as long as its data need.
-        const uint32_t pw = warp == 0 ? 0 : warp - 1;
+        // A warp for each stream's ring, or every other slot of the one ring: a box of the
+        // lanes' loop takes 60 cycles to issue, which with small pages is as long as its data
+        // need.  (Waits on a parity are right only for a reader at most one phase away: of two
+        // warps on one ring, a slot two turns back is read by both streams before the other
+        // warp, which has seen the release of a later one, can be here.)
+        const uint32_t pw = warp == 0 ? 0 : 1;
         const uint64_t pol = p.n > RT * p.NB ? policy_evict_normal() : policy_evict_first();
-        uint32_t slot = 0, runs = 0;                 // ring slots issued, runs begun
+        uint8_t *buf = ring + (RT == 1 ? pw : 0) * (NST * OPER);
+        uint64_t *full_r = full + (RT == 1 ? pw : 0) * NST, *empty_r = empty + (RT == 1 ? pw : 0) * NST;
+        uint32_t slot = 0, runs = 0;                 // ring slots passed, runs begun
         while (walk.next(p, r)) {
             const int tiles_q = RT == 2 && r.rb * 2 * p.NB + p.NB < r.s.nodes ? 2 : 1;
             if (pw == 0) ok = tr_wait(q_empty, (runs & 1) ^ 1, p.err, ok, lane);
@@ -440,32 +444,24 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             }
             ++runs;
             const int32_t *table = p.table + (long long)r.b * p.max_pages;
-            // K and V boxes in the order of the products.
-            for (int i = 0; i < 2 * r.cnt; ++i, ++slot) {
-                if (slot % 3 != pw) continue;
-                int j, is_v;
-                if (RT == 1) {
-                    if (i < 2 && i < r.cnt) { j = i; is_v = 0; }
-                    else if (r.cnt == 1) { j = 0; is_v = 1; }
-                    else if (i >= 2 * r.cnt - 2) { j = i - r.cnt; is_v = 1; }
-                    else { is_v = (i & 1) == 0; j = is_v ? (i - 2) / 2 : (i + 1) / 2; }
-                } else {
-                    j = i >> 1;
-                    is_v = i & 1;
-                }
+            // K and V in turn, as the products need them.
+            const int j0 = RT == 1 ? pw : 0, mine = (r.cnt - j0 + STEP - 1) / STEP;
+            for (int i = 0; i < 2 * mine; ++i, ++slot) {
+                if (RT == 2 && (slot & 1) != pw) continue;
+                const int j = j0 + (i >> 1) * STEP, is_v = i & 1;
                 const Tile t = tile_at(p, r.t0 + j, r.s.total);
                 const uint32_t st = slot % NST, ph = (slot / NST) & 1;
-                uint8_t *dst = ring + st * OPER;
+                uint8_t *dst = buf + st * OPER;
                 const int pg0 = t.p0 / p.page_size;
                 // Boxes of br rows: a page each, or parts of one page.  The lane's page number is
                 // on its way while the warp waits for the ring.
                 const int boxes = (t.rows + p.br - 1) / p.br, r0 = t.p0 - pg0 * p.page_size;
                 const bool pages = p.br == p.page_size;
                 int id = lane < boxes ? ld_dep(table + pg0 + (pages ? lane : 0)) : 0;
-                ok = tr_wait(&empty[st], ph ^ 1, p.err, ok, lane);
+                ok = tr_wait(&empty_r[st], ph ^ 1, p.err, ok, lane);
                 if (!ok) break;
                 const CUtensorMap *tm = is_v ? &tmv : &tmk;
-                if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(boxes * p.br * HALVES * 128));
+                if (lane == 0) mbar_arrive_expect_tx(&full_r[st], (uint32_t)(boxes * p.br * HALVES * 128));
                 __syncwarp();
                 for (int g = lane; g < boxes; g += 32) {
                     if (g >= 32) id = ld_dep(table + pg0 + (pages ? g : 0));
@@ -475,10 +471,10 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     }
                     const int at = g * p.br, pr = pages ? 0 : r0 + at;      // row in the tile, in the page
                     if (p.by8)
-                        tma_load_5d(dst + at / 8 * (HALVES * 1024), tm, 0, 0, r.h * HALVES, pr / 8, id, &full[st], pol);
+                        tma_load_5d(dst + at / 8 * (HALVES * 1024), tm, 0, 0, r.h * HALVES, pr / 8, id, &full_r[st], pol);
                     else
                         for (int hf = 0; hf < HALVES; ++hf)
-                            tma_load_4d(dst + hf * kTrBox + at * 128, tm, hf * 64, r.h, pr, id, &full[st], pol);
+                            tma_load_4d(dst + hf * kTrBox + at * 128, tm, hf * 64, r.h, pr, id, &full_r[st], pol);
                 }
             }
             if (!ok) break;
@@ -489,149 +485,133 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             if (pw == 0 && runs) mbar_wait(q_full, (runs - 1) & 1, p.err);
             const uint32_t last = min(slot, (uint32_t)NST);
             for (uint32_t i = slot - last; i < slot; ++i)
-                if (i % 3 == pw) mbar_wait(&full[i % NST], (i / NST) & 1, p.err);
+                if (RT == 1 || (i & 1) == pw) mbar_wait(&full_r[i % NST], (i / NST) & 1, p.err);
         }
-    } else if (warp == 1) {
-        regs_give();
-        // -------------------------------------------------------------- MMA issuer
-        const uint32_t idesc_s = umma_idesc_bf16(128, kTrKeys);
-        const uint32_t idesc_o = umma_idesc_bf16(128, D) | (1u << 16);   // B (V) is MN-major
-        const uint32_t qb = smem_u32(qbuf), rb0 = smem_u32(ring);
-        uint32_t slot0 = 0, runs = 0, done[2] = {0, 0};                  // done: tiles of each stream
+    } else if (warp < 4) {
+        // ------------------------------------------------------------- MMA issuers
+        // A warp, and of it one thread, per stream.  A stream's S has two halves of 64 keys,
+        // each with its own barriers: while the softmax is at one, the scores of the other's
+        // next tile are computed.  The queue of products is short, and what a thread does
+        // between two products takes as long as several of them; so the streams have a thread
+        // each, and one's products run while the other waits for its next P.
+        const int s = warp - 1;
+        if (elect_one()) {
+            const uint32_t idesc_s = umma_idesc_bf16(128, kTrKeys / 2);
+            const uint32_t idesc_o = umma_idesc_bf16(128, D) | (1u << 16);      // B (V) is MN-major
+            uint8_t *buf = ring + (RT == 1 ? s : 0) * (NST * OPER);
+            uint64_t *full_r = full + (RT == 1 ? s : 0) * NST, *empty_r = empty + (RT == 1 ? s : 0) * NST;
+            const uint32_t rb0 = smem_u32(buf), ts = tmem + s * 128, to = tmem + kTrOut + s * D;
+            const uint64_t kdesc = desc_k(rb0, p.sbo), vdesc = desc_v(rb0, p.sbo, p.hoff);
+            const uint64_t qdesc = umma_desc_sw128(smem_u32(qbuf)) + (RT == 2 ? s : 0) * (OPER >> 4);
+            // in descriptor units of 16 bytes: between halves of a key, 16 keys, 64 keys
+            const uint32_t khalf = p.hoff >> 4, step16 = 2 * p.sbo >> 4, step64 = 8 * p.sbo >> 4;
+            uint32_t slot = 0, runs = 0, done0 = 0, done1 = 0;                 // done: uses of a P
 
-        const uint64_t kdesc = desc_k(rb0, p.sbo), vdesc = desc_v(rb0, p.sbo, p.hoff), qdesc = umma_desc_sw128(qb);
-        const uint32_t khalf = p.hoff >> 4, vstep = 2 * p.sbo >> 4;      // descriptor units of 16 bytes
-        auto stage = [&](uint32_t slot) {                                // of a ring slot, in the same units
-            return (uint64_t)__shfl_sync(0xffffffffu, (slot % NST) * (OPER >> 4), 0);
-        };
-        auto scores = [&](int s, uint32_t slot) {                        // S_s = Q K^T
-            const uint64_t k = kdesc + stage(slot), q = qdesc + (RT == 2 ? s : 0) * (OPER >> 4);
-            if (elect_one()) {
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                if (ok) ok = tr_poll(bar, parity, p.err);
+                return ok;
+            };
+            auto arrived = [&](uint32_t slot) { return wait(&full_r[slot % NST], (slot / NST) & 1); };
+            // S = Q K^T of 64 keys
+            auto scores = [&](auto h, uint32_t st) {
+                const uint64_t k = kdesc + st * (OPER >> 4) + h * step64;
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
-                    umma_bf16(tmem + s * 128, q + (ks >> 2) * (kTrBox >> 4) + (ks & 3) * 2,
+                    umma_bf16(ts + h * 64, qdesc + (ks >> 2) * (kTrBox >> 4) + (ks & 3) * 2,
                               k + (ks >> 2) * khalf + (ks & 3) * 2, idesc_s, ks > 0);
-                umma_commit(&s_full[s]);
-            }
-            __syncwarp();
-        };
-        auto values = [&](int s, uint32_t slot, int rows, bool first) {  // O_s (+)= P V
-            const uint64_t v = vdesc + stage(slot);
-            const uint32_t o = tmem + kTrOut + s * D, a = tmem + s * 128;
-            if (elect_one()) {
-                if (rows > kTrKeys - 16) {
+                umma_commit(&s_full[s * 2 + h]);
+            };
+            // O (+)= P V of 64 keys, as soon as P is there
+            auto weigh = [&](auto h, uint32_t st, int rows, bool first) {
+                if (!wait(&p_full[s * 2 + h], (h ? done1 : done0) & 1)) return false;
+                tc_fence_after();
+                if (h) ++done1;
+                else ++done0;
+                const uint64_t v = vdesc + st * (OPER >> 4) + h * step64;
+                if (rows - h * 64 > 48) {
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        umma_bf16_ts(o, a + ks * 8, v + ks * vstep, idesc_o, ks > 0 || !first);
+                    for (int ks = 0; ks < 4; ++ks)
+                        umma_bf16_ts(to, ts + h * 64 + ks * 8, v + ks * step16, idesc_o, ks > 0 || !first);
                 } else {
-                    for (int ks = 0; ks * 16 < rows; ++ks)
-                        umma_bf16_ts(o, a + ks * 8, v + ks * vstep, idesc_o, ks > 0 || !first);
+                    for (int ks = 0; ks * 16 < rows - h * 64; ++ks)
+                        umma_bf16_ts(to, ts + h * 64 + ks * 8, v + ks * step16, idesc_o, ks > 0 || !first);
                 }
-                umma_commit(&o_full[s]);
-            }
-            __syncwarp();
-        };
-        auto release = [&](uint32_t slot) {
-            const uint32_t st = __shfl_sync(0xffffffffu, slot % NST, 0);
-            if (elect_one()) umma_commit(&empty[st]);
-            __syncwarp();
-        };
-        auto arrived = [&](uint32_t slot) {
-            ok = tr_wait(&full[slot % NST], (slot / NST) & 1, p.err, ok, lane);
-            tc_fence_after();
-        };
-        // Rows of V behind the sequence's last position may hold anything, and 0 * NaN is
-        // NaN: those that the last step of 16 keys still reads are set to zero.
-        auto clear_tail = [&](uint32_t slot, int rows) {
-            const int end = (rows + 15) & ~15;
-            if (rows == end) return;
-            uint8_t *v = ring + (slot % NST) * OPER;
-            for (int i = lane; i < HALVES * (end - rows) * 8; i += 32) {
-                const int hf = i / ((end - rows) * 8), e = i - hf * (end - rows) * 8;
-                const int row = rows + e / 8;
-                *reinterpret_cast<uint4 *>(v + hf * p.hoff + (row >> 3) * p.sbo + (row & 7) * 128 + (e & 7) * 16) =
-                    make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-        };
-        while (ok && walk.next(p, r)) {
-            ok = tr_wait(q_full, runs & 1, p.err, ok, lane);
-            tc_fence_after();
-            ++runs;
-            const bool second = RT == 2 && r.rb * 2 * p.NB + p.NB < r.s.nodes;
-            const int cnt = r.cnt;
-            if (RT == 1) {
-                for (int j = 0; j < 2 && j < cnt && ok; ++j) {
-                    arrived(slot0 + ring_k<RT>(j, cnt));
-                    if (!ok) break;
-                    scores(j, slot0 + ring_k<RT>(j, cnt));
-                    release(slot0 + ring_k<RT>(j, cnt));
+                umma_commit(&o_full[s * 2 + h]);
+                return true;
+            };
+            // Rows of V behind the sequence's last position may hold anything, and 0 * NaN is
+            // NaN: those that the last step of 16 keys still reads are set to zero (by either
+            // stream's thread before its own products: the same zeros).
+            auto clear_tail = [&](uint32_t st, int rows) {
+                const int end = (rows + 15) & ~15;
+                if (rows == end) return;
+                uint8_t *v = buf + st * OPER;
+                for (int row = rows; row < end; ++row)
+                    for (int i = 0; i < HALVES * 8; ++i)
+                        *reinterpret_cast<uint4 *>(v + (i >> 3) * p.hoff + (row >> 3) * p.sbo + (row & 7) * 128 +
+                                                   (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+            };
+            const Const<0> c0{};
+            const Const<1> c1{};
+            while (ok && walk.next(p, r)) {
+                if (!wait(q_full, runs & 1)) break;
+                ++runs;
+                const int cnt = r.cnt, j0 = RT == 1 ? s : 0;
+                auto rows_at = [&](int j) { return j < cnt ? tile_at(p, r.t0 + j, r.s.total).rows : 0; };
+                if (RT == 2 && s == 1 && r.rb * 2 * p.NB + p.NB >= r.s.nodes) {
+                    // No node in this stream's row tile: its part of every release, in step with the ring.
+                    for (int i = 0; i < 2 * cnt; ++i) {
+                        if (!arrived(slot)) break;
+                        mbar_arrive(&empty_r[slot % NST]);
+                        ++slot;
+                    }
+                    mbar_arrive(q_empty);
+                    continue;
                 }
-                if (cnt <= 2 && elect_one()) umma_commit(q_empty);
-                for (int j = 0; j < cnt && ok; ++j) {
-                    const int s = j & 1;
-                    const uint32_t vs = slot0 + ring_v<RT>(j, cnt);
-                    const int rows = tile_at(p, r.t0 + j, r.s.total).rows;
-                    arrived(vs);
-                    if (ok) clear_tail(vs, rows);
-                    ok = tr_wait(&p_full[s], done[s] & 1, p.err, ok, lane);
-                    tc_fence_after();
-                    if (!ok) break;
-                    values(s, vs, rows, j < 2);
-                    ++done[s];
-                    release(vs);
-                    if (j + 2 < cnt) {
-                        const uint32_t ks = slot0 + ring_k<RT>(j + 2, cnt);
-                        arrived(ks);
-                        if (!ok) break;
-                        scores(s, ks);
-                        release(ks);
-                        if (j + 3 == cnt && elect_one()) umma_commit(q_empty);
-                    }
+                int rows = rows_at(j0);
+                if (rows > 0) {
+                    const uint32_t st = slot % NST;
+                    if (!arrived(slot)) break;
+                    scores(c0, st);
+                    if (rows > 64) scores(c1, st);
+                    umma_commit(&empty_r[st]);
+                    ++slot;
                 }
-            } else {
-                arrived(slot0);
-                if (!ok) break;
-                scores(0, slot0);
-                if (second) scores(1, slot0);
-                release(slot0);
-                if (cnt == 1 && elect_one()) umma_commit(q_empty);
-                for (int j = 0; j < cnt && ok; ++j) {
-                    const uint32_t vs = slot0 + ring_v<RT>(j, cnt), ks = slot0 + ring_k<RT>(j + 1, cnt);
-                    const int rows = tile_at(p, r.t0 + j, r.s.total).rows;
-                    arrived(vs);
-                    if (ok) clear_tail(vs, rows);
-                    for (int s = 0; s < (second ? 2 : 1) && ok; ++s) {
-                        ok = tr_wait(&p_full[s], done[s] & 1, p.err, ok, lane);
-                        tc_fence_after();
-                        if (!ok) break;
-                        values(s, vs, rows, j == 0);
-                        ++done[s];
-                        if (j + 1 < cnt) {
-                            if (s == 0) arrived(ks);
-                            if (!ok) break;
-                            scores(s, ks);
-                        }
+                if (j0 + STEP >= cnt) {
+                    if (rows > 0) umma_commit(q_empty);
+                    else mbar_arrive(q_empty);
+                }
+                for (int j = j0; j < cnt; j += STEP) {
+                    const int next = rows_at(j + STEP);        // rows of the next tile
+                    const uint32_t vst = slot % NST, kst = (slot + 1) % NST;
+                    if (!arrived(slot)) break;
+                    clear_tail(vst, rows);
+                    if (!weigh(c0, vst, rows, j == j0)) break;
+                    if (rows <= 64) umma_commit(&empty_r[vst]);
+                    if (next > 0) {
+                        if (!arrived(slot + 1)) break;
+                        scores(c0, kst);
                     }
-                    if (!ok) break;
-                    release(vs);
-                    if (j + 1 < cnt) {
-                        release(ks);
-                        if (j + 2 == cnt && elect_one()) umma_commit(q_empty);
+                    if (rows > 64) {
+                        if (!weigh(c1, vst, rows, false)) break;
+                        umma_commit(&empty_r[vst]);
                     }
+                    if (next > 64) scores(c1, kst);
+                    if (next > 0) {
+                        umma_commit(&empty_r[kst]);
+                        if (j + 2 * STEP >= cnt) umma_commit(q_empty);
+                    }
+                    rows = next;
+                    slot += next > 0 ? 2 : 1;
                 }
             }
-            slot0 += 2 * cnt;
+            // The products in flight end before the shared memory and TMEM that they use go.
+            umma_commit(&mma_done[s]);
+            mbar_wait(&mma_done[s], 0, p.err);
         }
-        // The products in flight end before the shared memory and TMEM that they use go.
         __syncwarp();
-        if (elect_one()) {
-            umma_commit(mma_done);
-            mbar_wait(mma_done, 0, p.err);
-        }
     } else {
-        regs_take();
         // -------------------------------------------------------- softmax warpgroups
         const int s = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1;    // stream, half of a tile's keys
         const int quad = warp & 3;                                      // TMEM lanes 32 * quad ..
@@ -644,7 +624,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         const float sl = p.scale_log2;
         uint8_t *mypar = par + s * kTrMaxNodes;
         float *mine_x = xch + (s * 2 + half) * 128 + row, *other_x = xch + (s * 2 + 1 - half) * 128 + row;
-        uint32_t tiles_done = 0;
+        uint32_t used[2] = {0, 0};                                      // of this stream's two S
         int par_b = -1;
         bool first_run = true;
         while (walk.next(p, r)) {
@@ -664,114 +644,113 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 par_b = r.b;
             }
             float m = -INFINITY, l = 0.f;                    // m: of the row, l: of this half's keys
-            int mine = 0;                                    // tiles of this run that this stream had
+            uint32_t before[2] = {used[0], used[1]};         // uses of the two S before this run
             for (int j = RT == 1 ? s : 0; active && j < r.cnt; j += RT == 1 ? 2 : 1) {
                 const Tile t = tile_at(p, r.t0 + j, r.s.total);
-                ok = tr_wait(&s_full[s], tiles_done & 1, p.err, ok, lane);
-                tc_fence_after();
-                if (live) {
-                    uint32_t v[64];
-                    tmem_ld64(ts + half * 64, v);
-                    if (t.rows < kTrKeys || t.p0 + t.rows > r.s.len) {
-                        const int k0 = t.p0 + half * 64;                  // position of this half's first key
-                        const int rows = t.rows - half * 64;
-                        uint32_t see[2];
+                const bool edge = t.rows < kTrKeys || t.p0 + t.rows > r.s.len;
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int c = min(r.s.len - k0, rows) - 32 * k;
-                            see[k] = node < 0 || c <= 0 ? 0u : c >= 32 ? 0xffffffffu : (1u << c) - 1u;
+                for (int h = 0; h < 2; ++h) {
+                    if (h == 1 && t.rows <= 64) break;
+                    ok = tr_wait(&s_full[s * 2 + h], used[h] & 1, p.err, ok, lane);
+                    tc_fence_after();
+                    if (live) {
+                        uint32_t v[32];
+                        tmem_ld32u(ts + h * 64 + half * 32, v);
+                        if (edge) {
+                            const int c0 = h * 64 + half * 32;                // this thread's first key of the tile
+                            const int k0 = t.p0 + c0, rows = t.rows - c0;
+                            const int c = min(r.s.len - k0, rows);
+                            uint32_t see = node < 0 || c <= 0 ? 0u : c >= 32 ? 0xffffffffu : (1u << c) - 1u;
+                            if (node >= 0 && k0 + rows > r.s.len) {
+                                for (int a = node; a >= 0; a = p.parent ? (int)mypar[a] - 1 : a - 1) {
+                                    const int off = r.s.len + a - k0;
+                                    if (off < 0) break;                       // ancestors come before their nodes
+                                    if (off < rows && off < 32) see |= 1u << off;
+                                }
+                            }
+                            if (!__all_sync(0xffffffffu, see == 0xffffffffu)) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (!((see >> i) & 1u)) v[i] = 0xff800000u;
+                            }
                         }
-                        if (node >= 0 && k0 + rows > r.s.len) {
-                            for (int a = node; a >= 0; a = p.parent ? (int)mypar[a] - 1 : a - 1) {
-                                const int off = r.s.len + a - k0;
-                                if (off < 0) break;                       // ancestors come before their nodes
-                                if (off < rows && off < 64) {
-                                    if (off < 32) see[0] |= 1u << off;
-                                    else see[1] |= 1u << (off - 32);
+                        // Four chains, so that one maximum does not wait for the last.
+                        float t4[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) t4[i] = __uint_as_float(v[i]);
+#pragma unroll
+                        for (int i = 4; i < 28; i += 8)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) t4[k] = max3(t4[k], v[i + k], v[i + 4 + k]);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) t4[k] = fmaxf(t4[k], __uint_as_float(v[28 + k]));
+                        float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+                        // The maximum is moved, and O scaled, only where it has grown by more than
+                        // 2^kTrLazy: sums then stay below 2^kTrLazy * keys, far inside fp32.  Both
+                        // halves of a row have to agree; the barrier also puts the loads of S by
+                        // both before the stores of P over it.
+                        float f = 1.f;
+                        if (pair_any(pair_bar, top > m && (top - m) * sl > kTrLazy)) {
+                            *mine_x = top;
+                            named_bar_sync(pair_bar, 64);
+                            top = fmaxf(top, *other_x);
+                            if (top > m && (top - m) * sl > kTrLazy) {
+                                f = m == -INFINITY ? 1.f : fast_exp2((m - top) * sl);   // from -inf: O and l are zero
+                                m = top;
+                            }
+                            // This S being there, the product over the last P in its place is done;
+                            // the one over the other's may be under way.
+                            if (used[1 - h] != before[1 - h])
+                                ok = tr_wait(&o_full[s * 2 + 1 - h], (used[1 - h] - 1) & 1, p.err, ok, lane);
+                            tc_fence_after();
+                            if (used[0] != before[0]) {
+#pragma unroll 1
+                                for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 16) {
+                                    uint32_t o[16];
+                                    tmem_ld16(to + c0, o);
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                    tmem_st16(to + c0, o);
                                 }
                             }
                         }
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            if (__all_sync(0xffffffffu, see[k] == 0xffffffffu)) continue;
-#pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                if (!((see[k] >> c) & 1u)) v[32 * k + c] = 0xff800000u;
-                        }
-                    }
-                    // Four chains, so that one maximum does not wait for the last.
-                    float t4[4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) t4[c] = __uint_as_float(v[c]);
-#pragma unroll
-                    for (int c = 4; c < 60; c += 8)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            t4[i] = fmaxf(t4[i], fmaxf(__uint_as_float(v[c + i]), __uint_as_float(v[c + 4 + i])));
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) t4[i] = fmaxf(t4[i], __uint_as_float(v[60 + i]));
-                    float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-                    // The maximum is moved, and O scaled, only where it has grown by more than
-                    // 2^kTrLazy: sums then stay below 2^kTrLazy * keys, far inside fp32.  Both
-                    // halves of a row have to agree; the barrier also puts the loads of S by
-                    // both before the stores of P over it.
-                    float f = 1.f;
-                    if (pair_any(pair_bar, top > m && (top - m) * sl > kTrLazy)) {
-                        *mine_x = top;
-                        named_bar_sync(pair_bar, 64);
-                        top = fmaxf(top, *other_x);
-                        if (top > m && (top - m) * sl > kTrLazy) {
-                            f = m == -INFINITY ? 1.f : fast_exp2((m - top) * sl);   // from -inf: O and l are zero
-                            m = top;
-                        }
-                        if (mine > 0) {
-                            ok = tr_wait(&o_full[s], (tiles_done - 1) & 1, p.err, ok, lane);
-                            tc_fence_after();
-#pragma unroll 1
-                            for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 16) {
-                                uint32_t o[16];
-                                tmem_ld16(to + c0, o);
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                tmem_st16(to + c0, o);
-                            }
-                        }
-                    }
-                    const float ms = m == -INFINITY ? 0.f : m * sl;
-                    const uint64_t sl2 = pair(sl, sl), ms2 = pair(-ms, -ms);
-                    uint64_t sum2[2] = {0, 0};
-#pragma unroll
-                    for (int c0 = 0; c0 < 64; c0 += 32) {
+                        const float ms = m == -INFINITY ? 0.f : m * sl;
+                        const uint64_t sl2 = pair(sl, sl), ms2 = pair(-ms, -ms);
+                        uint64_t sum2[2] = {0, 0};
                         uint32_t u[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const float2 x = apart(fma2(pair(v[c0 + 2 * i], v[c0 + 2 * i + 1]), sl2, ms2));
+                            const float2 x = apart(fma2(pair(v[2 * i], v[2 * i + 1]), sl2, ms2));
                             const float a = fast_exp2(x.x), b = fast_exp2(x.y);
                             sum2[i & 1] = add2(sum2[i & 1], pair(a, b));
                             u[i] = pack_bf16(a, b);
                         }
-                        tmem_st16(ts + half * 32 + c0 / 2, u);
+                        tmem_st16(ts + h * 64 + half * 16, u);
+                        const float2 sum = apart(add2(sum2[0], sum2[1]));
+                        l = l * f + (sum.x + sum.y);
+                        tmem_wait_st();
                     }
-                    const float2 sum = apart(add2(sum2[0], sum2[1]));
-                    l = l * f + (sum.x + sum.y);
-                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[s * 2 + h]);
+                    ++used[h];
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[s]);
-                ++tiles_done;
-                ++mine;
             }
             // The end of the run: O / l if the run is the whole list entry, else a partial.
-            if (mine > 0) ok = tr_wait(&o_full[s], (tiles_done - 1) & 1, p.err, ok, lane);
+            for (int h = 0; h < 2; ++h)
+                if (used[h] != before[h]) ok = tr_wait(&o_full[s * 2 + h], (used[h] - 1) & 1, p.err, ok, lane);
             const int part = 2 * blockIdx.x + (first_run ? 0 : 1);
             first_run = false;
             // The halves' sums, and with one row tile both streams' maxima: each warp then
             // joins what it needs for its share of the channels.
             if (RT == 1) {
-                named_bar_sync(11, 512);
-                *mine_x = l;
-                if (half == 0) xmax[s * 128 + row] = m;
+                named_bar_sync(pair_bar, 64);
+                if (half == 1) *mine_x = l;
+                named_bar_sync(pair_bar, 64);
+                if (half == 0) {                             // a row's sum, and its maximum
+                    *mine_x = l + *other_x;
+                    *other_x = m;
+                }
                 tc_fence_before();
                 named_bar_sync(11, 512);
             } else {
@@ -782,13 +761,13 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             tc_fence_after();
             float w0 = 1.f, w1 = 0.f, mm = m, ll;
             if (RT == 1) {
-                const float m0 = xmax[row], m1 = r.cnt > 1 ? xmax[128 + row] : -INFINITY;
+                const float m0 = xch[128 + row], m1 = r.cnt > 1 ? xch[384 + row] : -INFINITY;
                 mm = fmaxf(m0, m1);
                 const float mu = mm == -INFINITY ? 0.f : mm;
                 w0 = fast_exp2((m0 - mu) * sl);
                 w1 = fast_exp2((m1 - mu) * sl);
-                ll = w0 * (xch[row] + xch[128 + row]);
-                if (r.cnt > 1) ll += w1 * (xch[256 + row] + xch[384 + row]);
+                ll = w0 * xch[row];
+                if (r.cnt > 1) ll += w1 * xch[256 + row];
             } else {
                 ll = xch[s * 256 + row] + xch[s * 256 + 128 + row];
             }
