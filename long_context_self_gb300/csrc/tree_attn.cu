@@ -291,14 +291,22 @@ struct TrSmem {
         RT * OPER + RINGS * STAGES * OPER + 2 * kTrMaxNodes + XCH + (2 * RINGS * STAGES + 16) * 8 + 16;
 };
 
-// Bounded wait.  The clock is read only now and then: a read takes as long as the whole
-// wait does on the path from one product to the next (both sides measured: 32 trees of 64
-// nodes over 32k).
+// Bounded wait.  A poll may sleep until the phase is over, or for 20 us: a warp that
+// spins takes issue slots from those with work (half of all that were issued, before).  The
+// clock is read only now and then: a read takes as long as a wait between two products does.
 __device__ __forceinline__ bool tr_poll(uint64_t *bar, uint32_t parity, int *err) {
     uint64_t t0 = 0;
     for (uint32_t i = 1; i < kMaxPolls; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 1023u) == 0) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+            : "memory");
+        if (done) return true;
+        if ((i & 63u) == 0) {
             const uint64_t t = globaltimer();
             if (t0 == 0) t0 = t;
             else if (t - t0 > kMaxWaitNs) break;
