@@ -294,18 +294,21 @@ struct TrSmem {
 // Bounded wait.  A poll may sleep until the phase is over, or for 20 us: a warp that
 // spins takes issue slots from those with work (half of all that were issued, before).  The
 // clock is read only now and then: a read takes as long as a wait between two products does.
-__device__ __forceinline__ bool tr_poll(uint64_t *bar, uint32_t parity, int *err) {
+__device__ __forceinline__ bool tr_try(uint64_t *bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    return done != 0;
+}
+__device__ __noinline__ bool tr_poll_on(uint64_t *bar, uint32_t parity, int *err) {
     uint64_t t0 = 0;
     for (uint32_t i = 1; i < kMaxPolls; ++i) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
-            : "memory");
-        if (done) return true;
+        if (tr_try(bar, parity)) return true;
         if ((i & 63u) == 0) {
             const uint64_t t = globaltimer();
             if (t0 == 0) t0 = t;
@@ -315,6 +318,9 @@ __device__ __forceinline__ bool tr_poll(uint64_t *bar, uint32_t parity, int *err
     raise_error(err, kErrTimeout);
     return false;
 }
+__device__ __forceinline__ bool tr_poll(uint64_t *bar, uint32_t parity, int *err) {
+    return tr_try(bar, parity) || tr_poll_on(bar, parity, err);
+}
 
 // A number that a generic lambda takes as a compile-time constant.
 template <int N>
@@ -322,11 +328,12 @@ struct Const {
     __device__ constexpr operator int() const { return N; }
 };
 
-// Lane 0 waits and the warp agrees on the outcome; once a wait has given up, the later
-// ones return at once.
+// A warp's wait, with one outcome for all lanes; once a wait has given up, the later ones
+// return at once.
 __device__ __forceinline__ bool tr_wait(uint64_t *bar, uint32_t parity, int *err, bool ok, int lane) {
+    if (__all_sync(0xffffffffu, ok && tr_try(bar, parity))) return true;
     int got = ok ? 1 : 0;
-    if (ok && lane == 0) got = tr_poll(bar, parity, err) ? 1 : 0;
+    if (ok && lane == 0) got = tr_poll_on(bar, parity, err) ? 1 : 0;
     return __shfl_sync(0xffffffffu, got, 0) != 0;
 }
 
@@ -651,9 +658,10 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 named_bar_sync(9 + s, 256);
                 par_b = r.b;
             }
-            float m = -INFINITY, l = 0.f;                    // m: of the row, l: of this half's keys
-            uint32_t before[2] = {used[0], used[1]};         // uses of the two S before this run
-            for (int j = RT == 1 ? s : 0; active && j < r.cnt; j += RT == 1 ? 2 : 1) {
+            // m: the maximum that O and l are held at, ms: m * sl, grown: a score above it moves m.
+            float m = -INFINITY, ms = 0.f, grown = -INFINITY, l = 0.f;
+            const uint32_t before[2] = {used[0], used[1]};   // uses of the two S before this run
+            for (int j = RT == 1 ? s : 0; active && j < r.cnt; j += STEP) {
                 const Tile t = tile_at(p, r.t0 + j, r.s.total);
                 const bool edge = t.rows < kTrKeys || t.p0 + t.rows > r.s.len;
 #pragma unroll
@@ -665,6 +673,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                         uint32_t v[32];
                         tmem_ld32u(ts + h * 64 + half * 32, v);
                         if (edge) {
+                            asm volatile("");                                 // a branch, not selects in every tile
                             const int c0 = h * 64 + half * 32;                // this thread's first key of the tile
                             const int k0 = t.p0 + c0, rows = t.rows - c0;
                             const int c = min(r.s.len - k0, rows);
@@ -685,26 +694,28 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                         // Four chains, so that one maximum does not wait for the last.
                         float t4[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) t4[i] = __uint_as_float(v[i]);
+                        for (int k = 0; k < 4; ++k) t4[k] = fmaxf(__uint_as_float(v[k]), __uint_as_float(v[4 + k]));
 #pragma unroll
-                        for (int i = 4; i < 28; i += 8)
+                        for (int i = 8; i < 32; i += 8)
 #pragma unroll
                             for (int k = 0; k < 4; ++k) t4[k] = max3(t4[k], v[i + k], v[i + 4 + k]);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) t4[k] = fmaxf(t4[k], __uint_as_float(v[28 + k]));
-                        float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+                        float top = fmaxf(max3(t4[0], __float_as_uint(t4[1]), __float_as_uint(t4[2])), t4[3]);
                         // The maximum is moved, and O scaled, only where it has grown by more than
                         // 2^kTrLazy: sums then stay below 2^kTrLazy * keys, far inside fp32.  Both
                         // halves of a row have to agree; the barrier also puts the loads of S by
                         // both before the stores of P over it.
-                        float f = 1.f;
-                        if (pair_any(pair_bar, top > m && (top - m) * sl > kTrLazy)) {
+                        if (pair_any(pair_bar, top > grown)) {
+                            asm volatile("");
                             *mine_x = top;
                             named_bar_sync(pair_bar, 64);
                             top = fmaxf(top, *other_x);
-                            if (top > m && (top - m) * sl > kTrLazy) {
+                            float f = 1.f;
+                            if (top > grown) {
                                 f = m == -INFINITY ? 1.f : fast_exp2((m - top) * sl);   // from -inf: O and l are zero
                                 m = top;
+                                ms = m * sl;
+                                grown = m + kTrLazy / sl;
+                                l *= f;
                             }
                             // This S being there, the product over the last P in its place is done;
                             // the one over the other's may be under way.
@@ -722,7 +733,6 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                                 }
                             }
                         }
-                        const float ms = m == -INFINITY ? 0.f : m * sl;
                         const uint64_t sl2 = pair(sl, sl), ms2 = pair(-ms, -ms);
                         uint64_t sum2[2] = {0, 0};
                         uint32_t u[16];
@@ -735,7 +745,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                         }
                         tmem_st16(ts + h * 64 + half * 16, u);
                         const float2 sum = apart(add2(sum2[0], sum2[1]));
-                        l = l * f + (sum.x + sum.y);
+                        l += sum.x + sum.y;
                         tmem_wait_st();
                     }
                     tc_fence_before();
