@@ -661,97 +661,104 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             // m: the maximum that O and l are held at, ms: m * sl, grown: a score above it moves m.
             float m = -INFINITY, ms = 0.f, grown = -INFINITY, l = 0.f;
             const uint32_t before[2] = {used[0], used[1]};   // uses of the two S before this run
+            // One half of a tile; `edge`: not every row sees all of its keys (compiled apart, as
+            // what it does to S costs the other tiles 30 instructions).
+            auto half_tile = [&](const Tile &t, auto h, auto edge) {
+                ok = tr_wait(&s_full[s * 2 + h], used[h] & 1, p.err, ok, lane);
+                tc_fence_after();
+                if (live) {
+                    uint32_t v[32];
+                    tmem_ld32u(ts + h * 64 + half * 32, v);
+                    if (edge) {
+                        const int first = h * 64 + half * 32;             // this thread's first key of the tile
+                        const int k0 = t.p0 + first, rows = t.rows - first;
+                        const int c = min(r.s.len - k0, rows);
+                        uint32_t see = node < 0 || c <= 0 ? 0u : c >= 32 ? 0xffffffffu : (1u << c) - 1u;
+                        if (node >= 0 && k0 + rows > r.s.len) {
+                            for (int a = node; a >= 0; a = p.parent ? (int)mypar[a] - 1 : a - 1) {
+                                const int off = r.s.len + a - k0;
+                                if (off < 0) break;                       // ancestors come before their nodes
+                                if (off < rows && off < 32) see |= 1u << off;
+                            }
+                        }
+                        if (!__all_sync(0xffffffffu, see == 0xffffffffu)) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!((see >> i) & 1u)) v[i] = 0xff800000u;
+                        }
+                    }
+                    // Four chains, so that one maximum does not wait for the last.
+                    float t4[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) t4[k] = fmaxf(__uint_as_float(v[k]), __uint_as_float(v[4 + k]));
+#pragma unroll
+                    for (int i = 8; i < 32; i += 8)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) t4[k] = max3(t4[k], v[i + k], v[i + 4 + k]);
+                    float top = fmaxf(max3(t4[0], __float_as_uint(t4[1]), __float_as_uint(t4[2])), t4[3]);
+                    // The maximum is moved, and O scaled, only where it has grown by more than
+                    // 2^kTrLazy: sums then stay below 2^kTrLazy * keys, far inside fp32.  Both
+                    // halves of a row have to agree; the barrier also puts the loads of S by
+                    // both before the stores of P over it.
+                    if (pair_any(pair_bar, top > grown)) {
+                        asm volatile("");
+                        *mine_x = top;
+                        named_bar_sync(pair_bar, 64);
+                        top = fmaxf(top, *other_x);
+                        float f = 1.f;
+                        if (top > grown) {
+                            f = m == -INFINITY ? 1.f : fast_exp2((m - top) * sl);   // from -inf: O and l are zero
+                            m = top;
+                            ms = m * sl;
+                            grown = m + kTrLazy / sl;
+                            l *= f;
+                        }
+                        // This S being there, the product over the last P in its place is done;
+                        // the one over the other's may be under way.
+                        if (used[1 - h] != before[1 - h])
+                            ok = tr_wait(&o_full[s * 2 + 1 - h], (used[1 - h] - 1) & 1, p.err, ok, lane);
+                        tc_fence_after();
+                        if (used[0] != before[0]) {
+#pragma unroll 1
+                            for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(to + c, o);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                tmem_st16(to + c, o);
+                            }
+                        }
+                    }
+                    const uint64_t sl2 = pair(sl, sl), ms2 = pair(-ms, -ms);
+                    uint64_t sum2[2] = {0, 0};
+                    uint32_t u[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 x = apart(fma2(pair(v[2 * i], v[2 * i + 1]), sl2, ms2));
+                        const float a = fast_exp2(x.x), b = fast_exp2(x.y);
+                        sum2[i & 1] = add2(sum2[i & 1], pair(a, b));
+                        u[i] = pack_bf16(a, b);
+                    }
+                    tmem_st16(ts + h * 64 + half * 16, u);
+                    const float2 sum = apart(add2(sum2[0], sum2[1]));
+                    l += sum.x + sum.y;
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[s * 2 + h]);
+                ++used[h];
+            };
+            const Const<0> c0{};
+            const Const<1> c1{};
             for (int j = RT == 1 ? s : 0; active && j < r.cnt; j += STEP) {
                 const Tile t = tile_at(p, r.t0 + j, r.s.total);
-                const bool edge = t.rows < kTrKeys || t.p0 + t.rows > r.s.len;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (h == 1 && t.rows <= 64) break;
-                    ok = tr_wait(&s_full[s * 2 + h], used[h] & 1, p.err, ok, lane);
-                    tc_fence_after();
-                    if (live) {
-                        uint32_t v[32];
-                        tmem_ld32u(ts + h * 64 + half * 32, v);
-                        if (edge) {
-                            asm volatile("");                                 // a branch, not selects in every tile
-                            const int c0 = h * 64 + half * 32;                // this thread's first key of the tile
-                            const int k0 = t.p0 + c0, rows = t.rows - c0;
-                            const int c = min(r.s.len - k0, rows);
-                            uint32_t see = node < 0 || c <= 0 ? 0u : c >= 32 ? 0xffffffffu : (1u << c) - 1u;
-                            if (node >= 0 && k0 + rows > r.s.len) {
-                                for (int a = node; a >= 0; a = p.parent ? (int)mypar[a] - 1 : a - 1) {
-                                    const int off = r.s.len + a - k0;
-                                    if (off < 0) break;                       // ancestors come before their nodes
-                                    if (off < rows && off < 32) see |= 1u << off;
-                                }
-                            }
-                            if (!__all_sync(0xffffffffu, see == 0xffffffffu)) {
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    if (!((see >> i) & 1u)) v[i] = 0xff800000u;
-                            }
-                        }
-                        // Four chains, so that one maximum does not wait for the last.
-                        float t4[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) t4[k] = fmaxf(__uint_as_float(v[k]), __uint_as_float(v[4 + k]));
-#pragma unroll
-                        for (int i = 8; i < 32; i += 8)
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) t4[k] = max3(t4[k], v[i + k], v[i + 4 + k]);
-                        float top = fmaxf(max3(t4[0], __float_as_uint(t4[1]), __float_as_uint(t4[2])), t4[3]);
-                        // The maximum is moved, and O scaled, only where it has grown by more than
-                        // 2^kTrLazy: sums then stay below 2^kTrLazy * keys, far inside fp32.  Both
-                        // halves of a row have to agree; the barrier also puts the loads of S by
-                        // both before the stores of P over it.
-                        if (pair_any(pair_bar, top > grown)) {
-                            asm volatile("");
-                            *mine_x = top;
-                            named_bar_sync(pair_bar, 64);
-                            top = fmaxf(top, *other_x);
-                            float f = 1.f;
-                            if (top > grown) {
-                                f = m == -INFINITY ? 1.f : fast_exp2((m - top) * sl);   // from -inf: O and l are zero
-                                m = top;
-                                ms = m * sl;
-                                grown = m + kTrLazy / sl;
-                                l *= f;
-                            }
-                            // This S being there, the product over the last P in its place is done;
-                            // the one over the other's may be under way.
-                            if (used[1 - h] != before[1 - h])
-                                ok = tr_wait(&o_full[s * 2 + 1 - h], (used[1 - h] - 1) & 1, p.err, ok, lane);
-                            tc_fence_after();
-                            if (used[0] != before[0]) {
-#pragma unroll 1
-                                for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 16) {
-                                    uint32_t o[16];
-                                    tmem_ld16(to + c0, o);
-#pragma unroll
-                                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                    tmem_st16(to + c0, o);
-                                }
-                            }
-                        }
-                        const uint64_t sl2 = pair(sl, sl), ms2 = pair(-ms, -ms);
-                        uint64_t sum2[2] = {0, 0};
-                        uint32_t u[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float2 x = apart(fma2(pair(v[2 * i], v[2 * i + 1]), sl2, ms2));
-                            const float a = fast_exp2(x.x), b = fast_exp2(x.y);
-                            sum2[i & 1] = add2(sum2[i & 1], pair(a, b));
-                            u[i] = pack_bf16(a, b);
-                        }
-                        tmem_st16(ts + h * 64 + half * 16, u);
-                        const float2 sum = apart(add2(sum2[0], sum2[1]));
-                        l += sum.x + sum.y;
-                        tmem_wait_st();
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_full[s * 2 + h]);
-                    ++used[h];
+                if (t.rows == kTrKeys && t.p0 + t.rows <= r.s.len) {
+                    half_tile(t, c0, c0);
+                    half_tile(t, c1, c0);
+                } else {
+                    half_tile(t, c0, c1);
+                    if (t.rows > 64) half_tile(t, c1, c1);
                 }
             }
             // The end of the run: O / l if the run is the whole list entry, else a partial.
