@@ -40,7 +40,7 @@ constexpr int kTrKeys = 128;                  // keys per tile
 constexpr int kTrBox = kTrKeys * 128;         // 128 rows x 64 channels (16 KB)
 constexpr int kTrMaxNodes = 256;
 constexpr int kTrOut = 256;                   // first TMEM column of O (S: 0 and 128)
-constexpr float kTrLazy = 8.0f;               // log2 growth of a row's maximum that is put up with
+constexpr float kTrLazy = 24.0f;              // log2 growth of a row's maximum that is put up with
 
 // What the joining kernel has to know of a sequence: its first entry in the list
 // of work, the number of its key tiles and its nodes.  Entry B holds the run length.
@@ -697,9 +697,11 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                         for (int k = 0; k < 4; ++k) t4[k] = max3(t4[k], v[i + k], v[i + 4 + k]);
                     float top = fmaxf(max3(t4[0], __float_as_uint(t4[1]), __float_as_uint(t4[2])), t4[3]);
                     // The maximum is moved, and O scaled, only where it has grown by more than
-                    // 2^kTrLazy: sums then stay below 2^kTrLazy * keys, far inside fp32.  Both
-                    // halves of a row have to agree; the barrier also puts the loads of S by
-                    // both before the stores of P over it.
+                    // 2^kTrLazy: probabilities are then up to 2^24 instead of 1, which costs a
+                    // floating sum nothing (its relative errors stay, and 2^24 * keys * |v| is
+                    // inside fp32 for every |v| below 2^80), and a scaling takes as long as the
+                    // half tile itself.  Both halves of a row have to agree; the barrier also puts
+                    // the loads of S by both before the stores of P over it.
                     if (pair_any(pair_bar, top > grown)) {
                         asm volatile("");
                         *mine_x = top;
