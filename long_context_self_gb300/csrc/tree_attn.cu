@@ -31,6 +31,8 @@
 // Roles (640 threads): warps 0 and 3 issue the TMA boxes, warps 1 and 2 the MMAs, warps
 // 4-11 and 12-19 are the softmax of the two streams.  Every wait is bounded; after one that
 // gave up (error 1) the roles run on without waiting, so that all of them end.
+#include <climits>
+
 #include "common.cuh"
 
 namespace magicdec {
@@ -239,6 +241,11 @@ __device__ __forceinline__ Seq seq_at(const TreeAttnParams &p, int b) {
     return s;
 }
 
+// x / d, in 32 bits where they suffice (a 64-bit division is a hundred instructions).
+__device__ __forceinline__ long long quotient(long long x, int d) {
+    return x <= 0xffffffffll ? (long long)((uint32_t)x / (uint32_t)d) : x / d;
+}
+
 // A run of tiles of one (sequence, KV head, row block).
 struct Run {
     int b, h, rb, t0, cnt;
@@ -249,14 +256,8 @@ struct Run {
 template <int RT>
 struct Walk {
     int b, off;             // off: tiles of sequence b already passed, over its heads and blocks
-    long long left;
+    int left;               // tiles of the run
     Seq s;
-    __device__ __forceinline__ void start(const TreeAttnParams &p, int b0, int off0, long long n) {
-        b = b0;
-        off = off0;
-        left = n;
-        if (left > 0) s = seq_at<RT>(p, b);
-    }
     __device__ __forceinline__ bool next(const TreeAttnParams &p, Run &r) {
         if (left <= 0) return false;
         while (off >= s.tiles * s.blocks * p.H_kv) {
@@ -267,10 +268,10 @@ struct Walk {
         const int item = off / s.tiles;
         r.b = b;
         r.s = s;
-        r.h = item / s.blocks;
+        r.h = s.blocks == 1 ? item : item / s.blocks;
         r.rb = item - r.h * s.blocks;
         r.t0 = off - item * s.tiles;
-        r.cnt = (int)min((long long)(s.tiles - r.t0), left);
+        r.cnt = min(s.tiles - r.t0, left);
         off += r.cnt;
         left -= r.cnt;
         return true;
@@ -288,7 +289,7 @@ struct TrSmem {
     static constexpr int STAGES = (RT == 1 ? 3 : 5) * (D == 128 ? 1 : 2);
     static constexpr int XCH = 2 * 2 * 128 * 4;
     static constexpr int BYTES =
-        RT * OPER + RINGS * STAGES * OPER + 2 * kTrMaxNodes + XCH + (2 * RINGS * STAGES + 16) * 8 + 16;
+        RT * OPER + RINGS * STAGES * OPER + 2 * kTrMaxNodes + XCH + (2 * RINGS * STAGES + 16) * 8 + 48;
 };
 
 // Bounded wait.  A poll may sleep until the phase is over, or for 20 us: a warp that
@@ -354,7 +355,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     uint64_t *s_full = q_empty + 1, *p_full = s_full + 4, *o_full = p_full + 4;   // [stream][half tile]
     uint64_t *mma_done = o_full + 4;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 2);
-    int *found = reinterpret_cast<int *>(tmem_slot + 1);                 // b0, off0, run length
+    int *found = reinterpret_cast<int *>(tmem_slot + 1);                 // where this CTA begins: see the list of work
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (smem_u32(smem) & 1023u) {
         if (tid == 0) raise_error(p.err, kErrState);
@@ -386,16 +387,19 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     pdl_trigger();
     pdl_wait();
 
-    // The list of work: prefix sums over the sequences, this CTA's run of tiles, and the
-    // sequence that it begins in.
+    // The list of work: prefix sums over the sequences (a thread has one of them, or with more
+    // than kTrThreads several in a row), this CTA's run of tiles, and the sequence that it
+    // begins in.
+    Walk<RT> walk;
     {
         long long *wsum = reinterpret_cast<long long *>(par);
-        const int per = (p.B + kTrThreads - 1) / kTrThreads;
+        const int per = p.B <= kTrThreads ? 1 : (p.B + kTrThreads - 1) / kTrThreads;
         const int ba = min(p.B, tid * per), bz = min(p.B, ba + per);
+        Seq sq{};
         long long mine = 0;
         for (int b = ba; b < bz; ++b) {
-            const Seq s = seq_at<RT>(p, b);
-            mine += (long long)s.tiles * s.blocks * p.H_kv;
+            sq = seq_at<RT>(p, b);
+            mine += (long long)(sq.tiles * sq.blocks) * p.H_kv;
         }
         long long incl = mine;
 #pragma unroll
@@ -406,20 +410,27 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         if (lane == 31) wsum[warp] = incl;
         __syncthreads();
         long long before = incl - mine, all = 0;
+#pragma unroll
         for (int w = 0; w < kTrThreads / 32; ++w) {
-            if (w < warp) before += wsum[w];
-            all += wsum[w];
+            const long long x = wsum[w];
+            if (w < warp) before += x;
+            all += x;
         }
-        const long long run = max(1ll, (all + p.grid - 1) / p.grid);
+        const long long run = max(1ll, quotient(all + p.grid - 1, p.grid));
         const long long t0 = blockIdx.x * run;
         for (int b = ba; b < bz; ++b) {
-            const Seq s = seq_at<RT>(p, b);
-            const long long w = (long long)s.tiles * s.blocks * p.H_kv;
-            if (blockIdx.x == 0) p.seq[b] = TreeSeq{before, s.tiles, s.nodes};
+            if (per > 1) sq = seq_at<RT>(p, b);
+            const long long w = (long long)(sq.tiles * sq.blocks) * p.H_kv;
+            if (blockIdx.x == 0) p.seq[b] = TreeSeq{before, sq.tiles, sq.nodes};
             if (t0 >= before && t0 < before + w) {
                 found[0] = b;
                 found[1] = (int)(t0 - before);
                 found[2] = (int)min(run, all - t0);
+                found[3] = sq.len;
+                found[4] = sq.nodes;
+                found[5] = sq.total;
+                found[6] = sq.tiles;
+                found[7] = sq.blocks;
             }
             before += w;
         }
@@ -429,8 +440,10 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    Walk<RT> walk;
-    walk.start(p, found[0], found[1], found[2]);
+    walk.b = found[0];
+    walk.off = found[1];
+    walk.left = found[2];
+    walk.s = Seq{found[3], found[4], found[5], found[6], found[7]};
     Run r;
     bool ok = true;
 
@@ -461,6 +474,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             const int32_t *table = p.table + (long long)r.b * p.max_pages;
             // K and V in turn, as the products need them.
             const int j0 = RT == 1 ? pw : 0, mine = (r.cnt - j0 + STEP - 1) / STEP;
+            int id = 0;
             for (int i = 0; i < 2 * mine; ++i, ++slot) {
                 if (RT == 2 && (slot & 1) != pw) continue;
                 const int j = j0 + (i >> 1) * STEP, is_v = i & 1;
@@ -472,7 +486,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 // on its way while the warp waits for the ring.
                 const int boxes = (t.rows + p.br - 1) / p.br, r0 = t.p0 - pg0 * p.page_size;
                 const bool pages = p.br == p.page_size;
-                int id = lane < boxes ? ld_dep(table + pg0 + (pages ? lane : 0)) : 0;
+                if (RT == 2 || !is_v || boxes > 32) id = lane < boxes ? ld_dep(table + pg0 + (pages ? lane : 0)) : 0;
                 ok = tr_wait(&empty_r[st], ph ^ 1, p.err, ok, lane);
                 if (!ok) break;
                 const CUtensorMap *tm = is_v ? &tmv : &tmk;
@@ -876,28 +890,27 @@ __global__ void __launch_bounds__(kTjThreads) tree_attn_join_kernel(const TreeAt
     const int blocks = (s.nodes + RT * p.NB - 1) / (RT * p.NB);
     const int tile = node / p.NB, rb = tile / RT, rt = tile - rb * RT;
     const long long t0 = s.first + (long long)(h * blocks + rb) * s.tiles, t1 = t0 + s.tiles - 1;
-    const int c0 = (int)(t0 / run), c1 = (int)(t1 / run);
+    const int c0 = (int)quotient(t0, (int)run), c1 = (int)quotient(t1, (int)run);
     if (c0 == c1) return;                              // one CTA had it whole and wrote it
     const int row = (node - tile * p.NB) * p.G + g;
     const int first = 2 * c0 + (t0 == c0 * run ? 0 : 1);
     const float sl = p.scale_log2;
     const long long srow = rt * 128 + row;
-    float top = p.stat[(long long)first * RT * 128 + srow].x;
-    for (int c = c0 + 1; c <= c1; ++c) top = fmaxf(top, p.stat[(long long)2 * c * RT * 128 + srow].x);
-    const float mu = top == -INFINITY ? 0.f : top;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
+    float top = -INFINITY, sum = 0.f;
 #pragma unroll 4
     for (int c = c0; c <= c1; ++c) {
         const long long slot = c == c0 ? first : 2 * c;
         const float2 e = p.stat[slot * RT * 128 + srow];
         const float4 o = p.part[((slot * RT + rt) * (D / 4) + c4) * 128 + row];
-        const float w = fast_exp2((e.x - mu) * sl);
-        sum += w * e.y;
-        acc.x += w * o.x;
-        acc.y += w * o.y;
-        acc.z += w * o.z;
-        acc.w += w * o.w;
+        const float m = fmaxf(top, e.x), mu = m == -INFINITY ? 0.f : m;
+        const float f = fast_exp2((top - mu) * sl), w = fast_exp2((e.x - mu) * sl);
+        top = m;
+        sum = sum * f + w * e.y;
+        acc.x = acc.x * f + w * o.x;
+        acc.y = acc.y * f + w * o.y;
+        acc.z = acc.z * f + w * o.z;
+        acc.w = acc.w * f + w * o.w;
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
     *dst = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
@@ -913,6 +926,14 @@ size_t tree_attn_workspace_bytes(const magicdec_paged_shape &s, int n) {
     const size_t slots = 2 * (size_t)magicdec_host::sm_count();
     return tr_align(((size_t)s.B + 1) * sizeof(TreeSeq)) + tr_align(slots * RT * 128 * sizeof(float2)) +
            slots * RT * 128 * s.d * 4;
+}
+
+// The list of work is counted in 32 bits within a sequence and within a CTA's run.
+static bool tr_counts(const TreeAttnParams &p) {
+    const long long cap = (long long)p.page_size * p.max_pages;
+    const long long tiles = p.ppt ? (cap + p.ppt * p.page_size - 1) / (p.ppt * p.page_size) : (long long)p.max_pages * p.tpp;
+    const long long work = tiles * p.H_kv * ((p.n + p.NB - 1) / p.NB);
+    return work <= INT_MAX && work * p.B / p.grid < INT_MAX;
 }
 
 template <int D, int RT>
@@ -956,6 +977,7 @@ magicdec_status launch_tree_attn(const magicdec_paged_shape &s, int n, const uin
     p.tpp = (s.page_size + kTrKeys - 1) / kTrKeys;
     p.scale_log2 = kLog2e / sqrtf((float)s.d);
     p.grid = magicdec_host::sm_count();
+    if (!tr_counts(p)) return MAGICDEC_ERR_UNSUPPORTED;
     const int RT = tr_row_tiles(n, p.G);
     const size_t slots = 2 * (size_t)p.grid;
     uint8_t *w = static_cast<uint8_t *>(ws);
