@@ -10,6 +10,7 @@ raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -559,13 +560,17 @@ def magicdec_spec_accept(target: torch.Tensor, draft: Optional[torch.Tensor], dr
 # little: one pass over a tensor's properties where all is well, the words where it is not.
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
 def _at(t, name, dtype, dev, shape) -> int:
     """The address of a dense tensor of this type, device and shape; raises for any other."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
-            and t.is_contiguous()):
-        _need_shape(t, name, dtype, dev, shape)
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev.index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need_shape(t, name, dtype, dev, shape)
     return t.data_ptr()
 
 
@@ -580,20 +585,13 @@ def _cuda_device(t, name, dtype):
     return t.device
 
 
-def _launch(name, dev, stream, call):
-    """call(address of the stream) with the tensors' device, and the stream, as the current ones."""
-    raw = _raw_stream(dev.index)
-    if (stream is None or getattr(stream, "cuda_stream", stream) == raw) and _current_device() == dev.index:
-        _check(name, call(raw))
-        return
-    if stream is None:
-        with torch.cuda.device(dev):
-            _check(name, call(raw))
-        return
-    if not hasattr(stream, "cuda_stream"):
+@contextlib.contextmanager
+def _on(dev, stream):
+    """The tensors' device, and the stream of the call, as the current ones."""
+    if stream is not None and not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=dev)
-    with torch.cuda.stream(stream):
-        _check(name, call(stream.cuda_stream))
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        yield
 
 
 def paged_shape(B, H_q, H_kv, d, page_size, n_pages, max_pages) -> PagedShape:
@@ -603,27 +601,26 @@ def paged_shape(B, H_q, H_kv, d, page_size, n_pages, max_pages) -> PagedShape:
 def _paged_cache(k_pages, v_pages, block_table, B, dev, dims=4):
     """Checks of the pool and its table; their addresses and (page_size, n_pages, max_pages, H_kv, d)."""
     shape = getattr(k_pages, "shape", ())
-    if len(shape) not in (4, dims):
+    if len(shape) != 4 and len(shape) != dims:
         raise ValueError(f"k_pages must be [n_pages, page_size, H_kv, d]{' or [layers, ...]' if dims == 5 else ''}")
-    kp = _at(k_pages, "k_pages", torch.bfloat16, dev, shape)
-    vp = _at(v_pages, "v_pages", torch.bfloat16, dev, shape)
+    kp = _at(k_pages, "k_pages", _BF16, dev, shape)
+    vp = _at(v_pages, "v_pages", _BF16, dev, shape)
     ts = getattr(block_table, "shape", ())
     if len(ts) != 2 or ts[0] != B:
         raise ValueError(f"block_table must be [{B}, max_pages]")
-    table = _at(block_table, "block_table", torch.int32, dev, ts)
-    n_pages, page_size, H_kv, d = shape[-4:]
-    return kp, vp, table, page_size, n_pages, ts[1], H_kv, d
+    return (kp, vp, _at(block_table, "block_table", _I32, dev, ts), shape[-3], shape[-4], ts[1], shape[-2], shape[-1])
 
 
 def _tokens(t, name, dev, B, n, d):
     """Checks of token rows [B, n, H, d] with dense heads and one stride between tokens; (H, stride)."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16:
+    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16:
         raise TypeError(f"{name} must be a torch.bfloat16 tensor")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != n or t.shape[3] != d:
-        raise ValueError(f"{name} must have shape ({B}, {n}, H, {d}), got {tuple(t.shape)}")
-    H = t.shape[2]
+    shape = t.shape
+    if len(shape) != 4 or shape[0] != B or shape[1] != n or shape[3] != d:
+        raise ValueError(f"{name} must have shape ({B}, {n}, H, {d}), got {tuple(shape)}")
+    H = shape[2]
     sb, sn, sh, sd = t.stride()
     # The stride between tokens; a dimension of one element has none of its own.
     stride = sn if n > 1 else sb if B > 1 else H * d
@@ -640,7 +637,11 @@ def magicdec_paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tenso
     """Append k, v [B, n, H_kv, d] (token-strided views allowed) at slots seq_len + i of the paged cache
     k_pages / v_pages [n_pages, page_size, H_kv, d], k rotated by inv_freq [rot_dim / 2] fp32 (None: not);
     q [B, n, H_q, d] is rotated into q_out, which is returned (None without q)."""
-    dev = _cuda_device(k, "k", torch.bfloat16)
+    dev = _cuda_device(k, "k", _BF16)
+    if stream is not None or _current_device() != dev.index:
+        with _on(dev, stream):
+            return magicdec_paged_append(k, v, k_pages, v_pages, block_table, seq_len, inv_freq, q, n_new, parent,
+                                         interleaved, q_out)
     if k.dim() != 4:
         raise ValueError("k must be [B, n, H_kv, d]")
     B, n, H_kv, d = k.shape
@@ -651,28 +652,25 @@ def magicdec_paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tenso
     H_v, vs = _tokens(v, "v", dev, B, n, d)
     if H_v != H_kv:
         raise ValueError("k and v have different numbers of heads")
-    H_q, qs = _tokens(q, "q", dev, B, n, d) if q is not None else (H_kv, 0)
-    if q is None and q_out is not None:
+    H_q, qs, qp, qo = H_kv, 0, None, None
+    if q is not None:
+        H_q, qs = _tokens(q, "q", dev, B, n, d)
+        qp = q.data_ptr()
+        if q_out is None:
+            q_out = torch.empty((B, n, H_q, d), dtype=_BF16, device=dev)
+        qo = _at(q_out, "q_out", _BF16, dev, (B, n, H_q, d))
+    elif q_out is not None:
         raise ValueError("q_out without q")
-    length = _at(seq_len, "seq_len", torch.int32, dev, (B,))
-    count = None if n_new is None else _at(n_new, "n_new", torch.int32, dev, (B,))
-    par = None if parent is None else _at(parent, "parent", torch.int32, dev, (B, n))
     inv, rot = None, 0
     if inv_freq is not None:
-        inv = _at(inv_freq, "inv_freq", torch.float32, dev, (inv_freq.numel(),))
-        rot = 2 * inv_freq.numel()
-    if q_out is not None:
-        _at(q_out, "q_out", torch.bfloat16, dev, (B, n, H_q, d))
-
-    def call(st):
-        nonlocal q_out
-        if q is not None and q_out is None:
-            q_out = torch.empty((B, n, H_q, d), dtype=torch.bfloat16, device=dev)
-        return (_lib or lib()).magicdec_paged_append(
-            PagedShape(B, H_q, H_kv, d, page_size, n_pages, max_pages), n, None if q is None else q.data_ptr(), qs,
-            k.data_ptr(), ks, v.data_ptr(), vs, length, count, par, inv, rot, 1 if interleaved else 0, table,
-            None if q is None else q_out.data_ptr(), kp, vp, st)
-    _launch("magicdec_paged_append", dev, stream, call)
+        rot = inv_freq.numel()
+        inv = _at(inv_freq, "inv_freq", _F32, dev, (rot,))
+        rot *= 2
+    _check("magicdec_paged_append", (_lib or lib()).magicdec_paged_append(
+        PagedShape(B, H_q, H_kv, d, page_size, n_pages, max_pages), n, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs,
+        _at(seq_len, "seq_len", _I32, dev, (B,)), None if n_new is None else _at(n_new, "n_new", _I32, dev, (B,)),
+        None if parent is None else _at(parent, "parent", _I32, dev, (B, n)), inv, rot, 1 if interleaved else 0, table,
+        qo, kp, vp, _raw_stream(dev.index)))
     return q_out
 
 
@@ -692,33 +690,33 @@ def magicdec_tree_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Te
     """q [B, n, H_q, d] over the paged cache k_pages / v_pages [n_pages, page_size, H_kv, d] through
     block_table [B, max_pages]: node i sees positions [0, seq_len) and the slots seq_len + a of its
     ancestors a (parent [B, n], None: a chain) and itself -> out [B, n, H_q, d] bf16."""
-    dev = _cuda_device(q, "q", torch.bfloat16)
-    if q.dim() != 4:
+    dev = _cuda_device(q, "q", _BF16)
+    if stream is not None or _current_device() != dev.index:
+        with _on(dev, stream):
+            return magicdec_tree_attn(q, k_pages, v_pages, block_table, seq_len, parent, n_nodes, out, ws)
+    qs = q.shape
+    if len(qs) != 4:
         raise ValueError("q must be [B, n, H_q, d]")
-    B, n, H_q, d = q.shape
-    qp = _at(q, "q", torch.bfloat16, dev, (B, n, H_q, d))
+    B, n, H_q, d = qs
     kp, vp, table, page_size, n_pages, max_pages, H_kv, d_c = _paged_cache(k_pages, v_pages, block_table, B, dev)
     if d_c != d:
         raise ValueError("q and k_pages disagree: q [B, n, H_q, d], k_pages [n_pages, page_size, H_kv, d]")
-    length = _at(seq_len, "seq_len", torch.int32, dev, (B,))
-    par = None if parent is None else _at(parent, "parent", torch.int32, dev, (B, n))
-    count = None if n_nodes is None else _at(n_nodes, "n_nodes", torch.int32, dev, (B,))
-    if out is not None:
-        _at(out, "out", torch.bfloat16, dev, (B, n, H_q, d))
-    if ws is not None and (ws.device != dev or not ws.is_contiguous()):
+    qp = _at(q, "q", _BF16, dev, qs)
+    length = _at(seq_len, "seq_len", _I32, dev, (B,))
+    par = None if parent is None else _at(parent, "parent", _I32, dev, (B, n))
+    count = None if n_nodes is None else _at(n_nodes, "n_nodes", _I32, dev, (B,))
+    if out is None:
+        out = torch.empty(qs, dtype=_BF16, device=dev)
+    op = _at(out, "out", _BF16, dev, qs)
+    if ws is None:
+        # No contents are kept between calls, so it comes from torch's allocator each time.
+        ws = torch.empty(_tree_ws_bytes(dev.index, B, H_q, H_kv, d, page_size, n_pages, max_pages, n),
+                         dtype=torch.uint8, device=dev)
+    elif ws.device != dev or not ws.is_contiguous():
         raise ValueError(f"ws must be contiguous and on {dev}")
-    dims = (B, H_q, H_kv, d, page_size, n_pages, max_pages)
-
-    def call(st):
-        nonlocal out, ws
-        if out is None:
-            out = torch.empty((B, n, H_q, d), dtype=torch.bfloat16, device=dev)
-        if ws is None:
-            # No contents are kept between calls, so it comes from torch's allocator each time.
-            ws = torch.empty(_tree_ws_bytes(dev.index, *dims, n), dtype=torch.uint8, device=dev)
-        return (_lib or lib()).magicdec_tree_attn(PagedShape(*dims), n, qp, kp, vp, table, length, count, par,
-                                                  out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), st)
-    _launch("magicdec_tree_attn", dev, stream, call)
+    _check("magicdec_tree_attn", (_lib or lib()).magicdec_tree_attn(
+        PagedShape(B, H_q, H_kv, d, page_size, n_pages, max_pages), n, qp, kp, vp, table, length, count, par, op,
+        ws.data_ptr(), ws.nbytes, _raw_stream(dev.index)))
     return out
 
 
@@ -727,29 +725,24 @@ def magicdec_tree_accept(target: torch.Tensor, tok: torch.Tensor, parent: Option
                          path: Optional[torch.Tensor] = None, out_tok: Optional[torch.Tensor] = None, stream=None):
     """Greedy acceptance down the tree: target [B, n, V] f32, tok [B, n] int32 ->
     (n_acc [B], path [B, n], out_tok [B, n]) int32."""
-    dev = _cuda_device(target, "target", torch.float32)
+    dev = _cuda_device(target, "target", _F32)
+    if stream is not None or _current_device() != dev.index:
+        with _on(dev, stream):
+            return magicdec_tree_accept(target, tok, parent, n_nodes, n_acc, path, out_tok)
     if target.dim() != 3:
         raise ValueError("target must be [B, n, V]")
     B, n, V = target.shape
-    logits = _at(target, "target", torch.float32, dev, (B, n, V))
-    tk = _at(tok, "tok", torch.int32, dev, (B, n))
-    par = None if parent is None else _at(parent, "parent", torch.int32, dev, (B, n))
-    count = None if n_nodes is None else _at(n_nodes, "n_nodes", torch.int32, dev, (B,))
-    for name, t, shape in (("n_acc", n_acc, (B,)), ("path", path, (B, n)), ("out_tok", out_tok, (B, n))):
-        if t is not None:
-            _at(t, name, torch.int32, dev, shape)
-
-    def call(st):
-        nonlocal n_acc, path, out_tok
-        if n_acc is None:
-            n_acc = torch.empty((B,), dtype=torch.int32, device=dev)
-        if path is None:
-            path = torch.empty((B, n), dtype=torch.int32, device=dev)
-        if out_tok is None:
-            out_tok = torch.empty((B, n), dtype=torch.int32, device=dev)
-        return (_lib or lib()).magicdec_tree_accept(B, n, V, logits, tk, par, count, n_acc.data_ptr(),
-                                                    path.data_ptr(), out_tok.data_ptr(), st)
-    _launch("magicdec_tree_accept", dev, stream, call)
+    if n_acc is None:
+        n_acc = torch.empty((B,), dtype=_I32, device=dev)
+    if path is None:
+        path = torch.empty((B, n), dtype=_I32, device=dev)
+    if out_tok is None:
+        out_tok = torch.empty((B, n), dtype=_I32, device=dev)
+    _check("magicdec_tree_accept", (_lib or lib()).magicdec_tree_accept(
+        B, n, V, _at(target, "target", _F32, dev, (B, n, V)), _at(tok, "tok", _I32, dev, (B, n)),
+        None if parent is None else _at(parent, "parent", _I32, dev, (B, n)),
+        None if n_nodes is None else _at(n_nodes, "n_nodes", _I32, dev, (B,)), _at(n_acc, "n_acc", _I32, dev, (B,)),
+        _at(path, "path", _I32, dev, (B, n)), _at(out_tok, "out_tok", _I32, dev, (B, n)), _raw_stream(dev.index)))
     return n_acc, path, out_tok
 
 
@@ -757,14 +750,15 @@ def magicdec_tree_commit(k_pages: torch.Tensor, v_pages: torch.Tensor, block_tab
                          seq_len: torch.Tensor, path: torch.Tensor, n_acc: torch.Tensor, stream=None) -> None:
     """Move the rows of the accepted path [B, n] (magicdec_tree_accept) to slots seq_len + 0 .. n_acc, in
     place, in k_pages / v_pages [n_pages, page_size, H_kv, d] or [layers, n_pages, page_size, H_kv, d]."""
-    dev = _cuda_device(path, "path", torch.int32)
+    dev = _cuda_device(path, "path", _I32)
+    if stream is not None or _current_device() != dev.index:
+        with _on(dev, stream):
+            return magicdec_tree_commit(k_pages, v_pages, block_table, seq_len, path, n_acc)
     if path.dim() != 2:
         raise ValueError("path must be [B, n]")
     B, n = path.shape
-    way = _at(path, "path", torch.int32, dev, (B, n))
     kp, vp, table, page_size, n_pages, max_pages, H_kv, d = _paged_cache(k_pages, v_pages, block_table, B, dev, 5)
-    length = _at(seq_len, "seq_len", torch.int32, dev, (B,))
-    acc = _at(n_acc, "n_acc", torch.int32, dev, (B,))
-    layers = k_pages.shape[0] if k_pages.dim() == 5 else 1
-    _launch("magicdec_tree_commit", dev, stream, lambda st: (_lib or lib()).magicdec_tree_commit(
-        PagedShape(B, H_kv, H_kv, d, page_size, n_pages, max_pages), n, layers, length, way, acc, table, kp, vp, st))
+    _check("magicdec_tree_commit", (_lib or lib()).magicdec_tree_commit(
+        PagedShape(B, H_kv, H_kv, d, page_size, n_pages, max_pages), n, k_pages.shape[0] if k_pages.dim() == 5 else 1,
+        _at(seq_len, "seq_len", _I32, dev, (B,)), _at(path, "path", _I32, dev, (B, n)),
+        _at(n_acc, "n_acc", _I32, dev, (B,)), table, kp, vp, _raw_stream(dev.index)))

@@ -10,6 +10,7 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 #include "../../include/magicdec.h"
@@ -421,6 +422,19 @@ inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 
 int sm_count();
 // Opt-in maximum dynamic shared memory per block of the current device.
 int max_smem_optin();
+
+// Allow kernel K `bytes` of dynamic shared memory on the current device; asked of the
+// runtime once per device.
+template <auto K>
+inline bool allow_smem_once(int bytes) {
+    static std::atomic<unsigned long long> done{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    if (done.load(std::memory_order_relaxed) >> dev & 1) return true;
+    if (cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    done.fetch_or(1ull << dev, std::memory_order_relaxed);
+    return true;
+}
 
 // Device address of the library's error word on the current device.
 int *device_error_word();

@@ -55,8 +55,9 @@ struct TreeAttnParams {
     const int32_t *len, *n_nodes, *parent, *table;
     uint16_t *out;
     TreeSeq *seq;          // workspace: [B + 1]
-    float2 *stat;          // workspace: [2 * grid][RT * 128] (max, sum)
-    float4 *part;          // workspace: [2 * grid][RT][d / 4][128]
+    float2 *stat;          // workspace: [2 * grid][RT * rr] (max, sum)
+    float4 *part;          // workspace: [2 * grid][RT][d / 4][rr]
+    int rr;                // rows of a row tile in the workspace
     int *err;
     int B, H_q, H_kv, G, n, page_size, n_pages, max_pages;
     int NB;                // nodes per row tile
@@ -816,7 +817,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             const float inv = ll > 0.f ? 1.f / ll : 0.f;
             uint16_t *dst = p.out + (((long long)r.b * p.n + node) * p.H_q + r.h * p.G + (row - node_r * p.G)) * D;
             const int rt = RT == 2 ? s : 0;
-            float4 *pd = p.part + ((long long)part * RT + rt) * (D / 4) * 128 + row;
+            float4 *pd = p.part + ((long long)part * RT + rt) * (D / 4) * p.rr + row;
             constexpr int SHARE = RT == 1 ? D / 4 : D / 2;               // channels of a warp
             const int c_lo = RT == 1 ? (s * 2 + half) * SHARE : half * SHARE;
 #pragma unroll 1
@@ -845,11 +846,11 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 } else {
 #pragma unroll
                     for (int i = 0; i < 16; i += 4)
-                        pd[(c0 + i) / 4 * 128] = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                        pd[(c0 + i) / 4 * p.rr] = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
                 }
             }
             if (!whole && node >= 0 && c_lo == 0)
-                p.stat[(long long)part * RT * 128 + rt * 128 + row] = make_float2(mm, ll);
+                p.stat[((long long)part * RT + rt) * p.rr + row] = make_float2(mm, ll);
             tc_fence_before();
             // O is free for the next run, whose first P says so: with one row tile, once all
             // warps have read both.
@@ -895,14 +896,13 @@ __global__ void __launch_bounds__(kTjThreads) tree_attn_join_kernel(const TreeAt
     const int row = (node - tile * p.NB) * p.G + g;
     const int first = 2 * c0 + (t0 == c0 * run ? 0 : 1);
     const float sl = p.scale_log2;
-    const long long srow = rt * 128 + row;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float top = -INFINITY, sum = 0.f;
 #pragma unroll 4
     for (int c = c0; c <= c1; ++c) {
         const long long slot = c == c0 ? first : 2 * c;
-        const float2 e = p.stat[slot * RT * 128 + srow];
-        const float4 o = p.part[((slot * RT + rt) * (D / 4) + c4) * 128 + row];
+        const float2 e = p.stat[(slot * RT + rt) * p.rr + row];
+        const float4 o = p.part[((slot * RT + rt) * (D / 4) + c4) * p.rr + row];
         const float m = fmaxf(top, e.x), mu = m == -INFINITY ? 0.f : m;
         const float f = fast_exp2((top - mu) * sl), w = fast_exp2((e.x - mu) * sl);
         top = m;
@@ -921,11 +921,13 @@ static size_t tr_align(size_t x) { return (x + 255) & ~(size_t)255; }
 
 static int tr_row_tiles(int n, int G) { return n <= 128 / G ? 1 : 2; }
 
+// Rows of a row tile in the workspace: those of one short tile, in pairs of 64-byte segments.
+static int tr_part_rows(int n, int G) { return n <= 128 / G ? (n * G + 7) / 8 * 8 : 128; }
+
 size_t tree_attn_workspace_bytes(const magicdec_paged_shape &s, int n) {
-    const int RT = tr_row_tiles(n, s.H_q / s.H_kv);
-    const size_t slots = 2 * (size_t)magicdec_host::sm_count();
-    return tr_align(((size_t)s.B + 1) * sizeof(TreeSeq)) + tr_align(slots * RT * 128 * sizeof(float2)) +
-           slots * RT * 128 * s.d * 4;
+    const int G = s.H_q / s.H_kv;
+    const size_t rows = 2 * (size_t)magicdec_host::sm_count() * tr_row_tiles(n, G) * tr_part_rows(n, G);
+    return tr_align(((size_t)s.B + 1) * sizeof(TreeSeq)) + tr_align(rows * sizeof(float2)) + rows * s.d * 4;
 }
 
 // The list of work is counted in 32 bits within a sequence and within a CTA's run.
@@ -942,8 +944,7 @@ static magicdec_status launch_tree_t(const CUtensorMap &tmq, const CUtensorMap &
     auto kern = tree_attn_kernel<D, RT>;
     constexpr int smem = TrSmem<D, RT>::BYTES;
     static_assert(smem <= 227 * 1024, "shared memory of one CTA");
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return MAGICDEC_ERR_CUDA;
+    if (!magicdec_host::allow_smem_once<tree_attn_kernel<D, RT>>(smem)) return MAGICDEC_ERR_CUDA;
     magicdec_status s =
         magicdec_host::launch_pdl(kern, dim3((unsigned)p.grid), dim3(kTrThreads), smem, st, tmq, tmk, tmv, p);
     if (s != MAGICDEC_OK) return s;
@@ -984,7 +985,8 @@ magicdec_status launch_tree_attn(const magicdec_paged_shape &s, int n, const uin
     p.seq = reinterpret_cast<TreeSeq *>(w);
     w += tr_align(((size_t)s.B + 1) * sizeof(TreeSeq));
     p.stat = reinterpret_cast<float2 *>(w);
-    w += tr_align(slots * RT * 128 * sizeof(float2));
+    p.rr = tr_part_rows(n, p.G);
+    w += tr_align(slots * RT * p.rr * sizeof(float2));
     p.part = reinterpret_cast<float4 *>(w);
 
     // Queries as (d, H_q, n, B), one box = NB nodes of a KV head's group.  The pool with
