@@ -112,7 +112,7 @@ int *device_error_word() {
 }
 
 bool encode_tmap_bf16(CUtensorMap *map, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
-                      const uint32_t *box) {
+                      const uint32_t *box, int fetch) {
     static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
@@ -134,14 +134,15 @@ bool encode_tmap_bf16(CUtensorMap *map, const void *base, int rank, const uint64
         if (i + 1 < rank) gs[i] = strides[i];
     }
     CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), gd, gs, bx, es,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        fetch <= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
 
 bool encode_tmap_bf16_4d(CUtensorMap *map, const void *base, const uint64_t dims[4], const uint64_t strides[3],
                          const uint32_t box[4]) {
-    return encode_tmap_bf16(map, base, 4, dims, strides, box);
+    return encode_tmap_bf16(map, base, 4, dims, strides, box, 256);
 }
 
 }  // namespace magicdec_host

@@ -423,17 +423,25 @@ int sm_count();
 // Opt-in maximum dynamic shared memory per block of the current device.
 int max_smem_optin();
 
-// Allow kernel K `bytes` of dynamic shared memory on the current device; asked of the
-// runtime once per device.
-template <auto K>
-inline bool allow_smem_once(int bytes) {
+// Set attribute A of kernel K on the current device; asked of the runtime once per device.
+template <auto K, cudaFuncAttribute A>
+inline bool set_attribute_once(int value) {
     static std::atomic<unsigned long long> done{0};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
     if (done.load(std::memory_order_relaxed) >> dev & 1) return true;
-    if (cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    if (cudaFuncSetAttribute(K, A, value) != cudaSuccess) return false;
     done.fetch_or(1ull << dev, std::memory_order_relaxed);
     return true;
+}
+// Allow kernel K `bytes` of dynamic shared memory, or clusters of 16 CTAs.
+template <auto K>
+inline bool allow_smem_once(int bytes) {
+    return set_attribute_once<K, cudaFuncAttributeMaxDynamicSharedMemorySize>(bytes);
+}
+template <auto K>
+inline bool allow_wide_cluster_once() {
+    return set_attribute_once<K, cudaFuncAttributeNonPortableClusterSizeAllowed>(1);
 }
 
 // Device address of the library's error word on the current device.
@@ -441,9 +449,10 @@ int *device_error_word();
 
 // Encode a bf16 tensor map of 2 to 5 dimensions (innermost first, byte strides
 // of all but the first) with 128-byte swizzle and zero fill out of bounds.
-// False on failure.
+// L2 fetches `fetch` bytes (128 or 256) where a copy touches one of them.  False
+// on failure.
 bool encode_tmap_bf16(CUtensorMap *map, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
-                      const uint32_t *box);
+                      const uint32_t *box, int fetch);
 // The same for 4 dimensions.
 bool encode_tmap_bf16_4d(CUtensorMap *map, const void *base, const uint64_t dims[4], const uint64_t strides[3],
                          const uint32_t box[4]);

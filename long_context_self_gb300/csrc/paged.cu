@@ -53,27 +53,31 @@ struct AppendParams {
     int B, n, H_q, H_kv, d, rot, page_size, n_pages, max_pages;
 };
 
-// (a, b) -> (a cos - b sin, a sin + b cos) on two packed bf16 pairs; products and
-// sums in fp32, one rounding of each result to bf16.
-__device__ __forceinline__ void turn2(uint32_t &a, uint32_t &b, float2 c0, float2 c1) {
-    const float a0 = __uint_as_float(a << 16), a1 = __uint_as_float(a & 0xffff0000u);
-    const float b0 = __uint_as_float(b << 16), b1 = __uint_as_float(b & 0xffff0000u);
-    a = pack_bf16(a0 * c0.x - b0 * c0.y, a1 * c1.x - b1 * c1.y);
-    b = pack_bf16(a0 * c0.y + b0 * c0.x, a1 * c1.y + b1 * c1.x);
-}
+__device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
-// One pair held in one word: (lo, hi) -> (lo cos - hi sin, lo sin + hi cos).
-__device__ __forceinline__ uint32_t turn1(uint32_t x, float2 c) {
-    const float a = __uint_as_float(x << 16), b = __uint_as_float(x & 0xffff0000u);
+// One pair held in one word: (lo, hi) -> (lo cos - hi sin, lo sin + hi cos).  Products and
+// sums in fp32, one rounding of each result to bf16.
+__device__ __forceinline__ uint32_t turn_pair(uint32_t x, float2 c) {
+    const float a = bf_lo(x), b = bf_hi(x);
     return pack_bf16(a * c.x - b * c.y, a * c.y + b * c.x);
 }
+// Two channels and, `sign` times, the two that they are paired with: x cos + sign * y sin.
+__device__ __forceinline__ uint32_t turn_with(uint32_t x, uint32_t y, float4 c, float sign) {
+    return pack_bf16(bf_lo(x) * c.x + sign * (bf_lo(y) * c.y), bf_hi(x) * c.z + sign * (bf_hi(y) * c.w));
+}
 
-// A CTA takes T consecutive tokens of one sequence.  First the rot / 2 angles of
-// each token, once for all its heads; then its 16-byte vectors, one item of a
-// thread at a time.
-template <int T, bool INTER>
+// A CTA takes T consecutive tokens of one sequence and goes over their head rows (q, k and v
+// rows of d channels), VPH = d / 8 lanes a row, one 16-byte vector a lane: a row is read and
+// written whole, and the channels rotated with one another come from another lane of the row.
+// The first rows' loads are under way while the lengths, the table and the angles (once per
+// token, for all its heads) are read and computed.  Bound: HBM, 4 (H_q + 2 H_kv) d bytes a
+// token.
+template <int T, int VPH, bool INTER>
 __global__ void __launch_bounds__(kApThreads) paged_append_kernel(const AppendParams p) {
-    __shared__ float2 cs[T][64];
+    constexpr int ROWS = kApThreads / VPH;      // rows of a pass
+    constexpr int AHEAD = 4;                    // passes loaded together
+    __shared__ __align__(16) float2 cs[T][VPH * 4];
     __shared__ int par[kApMaxTree];
     __shared__ long long dst[T];
     __shared__ int posn[T];
@@ -84,93 +88,103 @@ __global__ void __launch_bounds__(kApThreads) paged_append_kernel(const AppendPa
     const int len = pg_clamp(checked(ld_dep(p.len + b), 0, cap, p.err), cap);
     const int cnt = p.n_new ? pg_clamp(checked(ld_dep(p.n_new + b), 0, p.n, p.err), p.n) : p.n;
     if (i0 >= cnt) return;
+    const int nt = min(T, cnt - i0);
+    const int nq = p.q_out ? p.H_q : 0, R = nq + 2 * p.H_kv;         // rows of a token
+    const int c = tid % VPH, total = nt * R;
+    const long long tok0 = (long long)b * p.n + i0;
+    auto load = [&](int w) {                                        // vector c of row w % R of token w / R
+        const int t = T == 1 ? 0 : w / R, r = w - t * R;
+        const uint16_t *src = r < nq ? p.q + (tok0 + t) * p.q_stride + r * p.d
+                              : r < nq + p.H_kv ? p.k + (tok0 + t) * p.k_stride + (r - nq) * p.d
+                                                : p.v + (tok0 + t) * p.v_stride + (r - nq - p.H_kv) * p.d;
+        return ld_once_u4(reinterpret_cast<const uint4 *>(src) + c);
+    };
+    uint4 x[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+        const int w = tid / VPH + k * ROWS;
+        if (w < total) x[k] = load(w);
+    }
     if (p.parent)
         for (int i = tid; i < min(i0 + T, p.n); i += kApThreads)
             par[i] = checked(ld_dep(p.parent + (long long)b * p.n + i), -1, i - 1, p.err);
-    __syncthreads();
-    const int nt = min(T, cnt - i0);
-    if (tid < nt) {
-        const int i = i0 + tid;
-        int depth = i;
-        if (p.parent) {
-            depth = 0;
-            for (int j = i; par[j] >= 0 && par[j] < j; j = par[j]) ++depth;
-        }
-        posn[tid] = depth;
-        dst[tid] = pool_row(p.table + (long long)b * p.max_pages, (long long)len + i, p.page_size, p.n_pages,
+    if (tid < nt)
+        dst[tid] = pool_row(p.table + (long long)b * p.max_pages, (long long)len + i0 + tid, p.page_size, p.n_pages,
                             p.max_pages, p.err);
+    if (p.parent) {
+        __syncthreads();
+        if (tid < nt) {
+            int depth = 0;
+            for (int j = i0 + tid; par[j] >= 0 && par[j] < j; j = par[j]) ++depth;
+            posn[tid] = depth;
+        }
+        __syncthreads();
     }
-    __syncthreads();
     // The angle position * inv_freq reaches 1e5 radians and more, where fp32 would
     // lose the low bits of the turn: the product in turns is formed and reduced in
     // fp64, and the fraction handed to the fp32 sine and cosine.
     const int half = p.rot / 2;
     for (int w = tid; w < nt * half; w += kApThreads) {
         const int t = w / half, f = w - t * half;
-        const double turns = ((double)len + posn[t]) * ((double)ld_dep_f(p.inv_freq + f) * 0.15915494309189535);
-        float s, c;
-        sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
-        cs[t][f] = make_float2(c, s);
+        const int at = p.parent ? posn[t] : i0 + t;
+        const double turns = ((double)len + at) * ((double)ld_dep_f(p.inv_freq + f) * 0.15915494309189535);
+        float s, co;
+        sincospif((float)(2.0 * (turns - rint(turns))), &s, &co);
+        cs[t][f] = make_float2(co, s);
     }
     __syncthreads();
-    const int vph = p.d / 8;                                    // 16-byte vectors per head
-    const int rv = p.rot / 8;                                   // of them rotated
-    const int per = INTER ? vph : vph - rv / 2;                 // items per rotated head
-    const int nq = p.q_out ? p.H_q : 0;
-    const int rot_items = (nq + p.H_kv) * per, items = rot_items + p.H_kv * vph;
-    for (int w = tid; w < nt * items; w += kApThreads) {
-        const int t = w / items;
-        int it = w - t * items;
-        const long long tok = (long long)b * p.n + i0 + t;
-        if (it >= rot_items) {                                  // a value vector: copied
-            it -= rot_items;
-            if (dst[t] < 0) continue;
-            const uint4 x = ld_once_u4(reinterpret_cast<const uint4 *>(p.v + tok * p.v_stride) + it);
-            reinterpret_cast<uint4 *>(p.vp + dst[t] * p.H_kv * p.d)[it] = x;
-            continue;
+    const int rv = p.rot / 8;                                       // rotated vectors of a row
+    const int lane = tid & 31, other = c < rv / 2 ? lane + rv / 2 : lane - rv / 2;
+    const float sign = c < rv / 2 ? -1.f : 1.f;
+    const int f0 = INTER ? c * 4 : (c < rv / 2 ? c : c - rv / 2) * 8;
+    // Every lane of a warp takes part in a pass's exchange; a row that is not there is not stored.
+    for (int w0 = tid / VPH; w0 - tid / VPH < total; w0 += AHEAD * ROWS) {
+        if (w0 != tid / VPH) {
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k)
+                if (w0 + k * ROWS < total) x[k] = load(w0 + k * ROWS);
         }
-        int h = it / per;
-        const int c = it - h * per;
-        const bool is_q = h < nq;
-        const uint4 *src;
-        uint4 *out;
-        if (is_q) {
-            src = reinterpret_cast<const uint4 *>(p.q + tok * p.q_stride) + h * vph;
-            out = reinterpret_cast<uint4 *>(p.q_out + tok * p.H_q * p.d) + h * vph;
-        } else {
-            if (dst[t] < 0) continue;
-            h -= nq;
-            src = reinterpret_cast<const uint4 *>(p.k + tok * p.k_stride) + h * vph;
-            out = reinterpret_cast<uint4 *>(p.kp + dst[t] * p.H_kv * p.d) + h * vph;
-        }
-        if (INTER) {
-            uint4 x = ld_once_u4(src + c);
-            if (c < rv) {
-                const float2 *a = &cs[t][c * 4];
-                x = make_uint4(turn1(x.x, a[0]), turn1(x.y, a[1]), turn1(x.z, a[2]), turn1(x.w, a[3]));
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const int w = w0 + k * ROWS;
+            if (w - tid / VPH >= total) break;                      // the same for the whole block
+            const int t = T == 1 ? 0 : min(w / R, nt - 1), r = w - t * R;
+            uint4 o = x[k];
+            const bool turned = c < rv && r < nq + p.H_kv;
+            if (INTER) {
+                if (turned) {
+                    const float2 *a = &cs[t][f0];
+                    o = make_uint4(turn_pair(o.x, a[0]), turn_pair(o.y, a[1]), turn_pair(o.z, a[2]), turn_pair(o.w, a[3]));
+                }
+            } else {
+                uint4 y;
+                y.x = __shfl_sync(0xffffffffu, x[k].x, other & 31);
+                y.y = __shfl_sync(0xffffffffu, x[k].y, other & 31);
+                y.z = __shfl_sync(0xffffffffu, x[k].z, other & 31);
+                y.w = __shfl_sync(0xffffffffu, x[k].w, other & 31);
+                if (turned) {
+                    const float4 *a = reinterpret_cast<const float4 *>(&cs[t][f0]);
+                    o = make_uint4(turn_with(o.x, y.x, a[0], sign), turn_with(o.y, y.y, a[1], sign),
+                                   turn_with(o.z, y.z, a[2], sign), turn_with(o.w, y.w, a[3], sign));
+                }
             }
-            out[c] = x;
-        } else if (c < rv / 2) {
-            uint4 x = ld_once_u4(src + c), y = ld_once_u4(src + c + rv / 2);
-            const float2 *a = &cs[t][c * 8];
-            turn2(x.x, y.x, a[0], a[1]);
-            turn2(x.y, y.y, a[2], a[3]);
-            turn2(x.z, y.z, a[4], a[5]);
-            turn2(x.w, y.w, a[6], a[7]);
-            out[c] = x;
-            out[c + rv / 2] = y;
-        } else {
-            out[c + rv / 2] = ld_once_u4(src + c + rv / 2);
+            if (w >= total) continue;
+            if (r < nq) {
+                reinterpret_cast<uint4 *>(p.q_out + ((tok0 + t) * p.H_q + r) * p.d)[c] = o;
+            } else if (dst[t] >= 0) {
+                const int h = r - nq;
+                uint16_t *out = h < p.H_kv ? p.kp + (dst[t] * p.H_kv + h) * p.d : p.vp + (dst[t] * p.H_kv + h - p.H_kv) * p.d;
+                reinterpret_cast<uint4 *>(out)[c] = o;
+            }
         }
     }
 }
 
-template <int T>
+template <int T, int VPH>
 static magicdec_status launch_append_t(const AppendParams &p, int interleaved, cudaStream_t st) {
     const dim3 grid((unsigned)((p.n + T - 1) / T), (unsigned)p.B);
-    if (interleaved)
-        return magicdec_host::launch_pdl(paged_append_kernel<T, true>, grid, dim3(kApThreads), 0, st, p);
-    return magicdec_host::launch_pdl(paged_append_kernel<T, false>, grid, dim3(kApThreads), 0, st, p);
+    return magicdec_host::launch_pdl(interleaved ? paged_append_kernel<T, VPH, true> : paged_append_kernel<T, VPH, false>,
+                                     grid, dim3(kApThreads), 0, st, p);
 }
 
 magicdec_status launch_paged_append(const magicdec_paged_shape &s, int n, const uint16_t *q, long long q_stride,
@@ -203,7 +217,11 @@ magicdec_status launch_paged_append(const magicdec_paged_shape &s, int n, const 
     p.page_size = s.page_size;
     p.n_pages = s.n_pages;
     p.max_pages = s.max_pages;
-    return launch_append_t<1>(p, interleaved, st);
+    // Four tokens a CTA pay for its way in (angles, table, tree) once the GPU has CTAs enough
+    // without splitting further.
+    if ((long long)s.B * n >= 8ll * magicdec_host::sm_count())
+        return s.d == 128 ? launch_append_t<4, 16>(p, interleaved, st) : launch_append_t<4, 8>(p, interleaved, st);
+    return s.d == 128 ? launch_append_t<1, 16>(p, interleaved, st) : launch_append_t<1, 8>(p, interleaved, st);
 }
 
 // ---------------------------------------------------------------------- commit
@@ -214,7 +232,7 @@ struct CommitParams {
     uint4 *kp, *vp;                  // [layers, n_pages, page_size, H_kv, d] as 16-byte vectors
     const int32_t *len, *path, *n_acc, *table;
     int *err;
-    int B, n, row_vecs, page_size, n_pages, max_pages;
+    int B, n, layers, row_vecs, page_size, n_pages, max_pages;
 };
 
 // Slot len + i takes the row of slot len + path[i], i = 0 .. n_acc, in every
@@ -257,9 +275,15 @@ __global__ void __launch_bounds__(kCmThreads) tree_commit_kernel(const CommitPar
     }
     __syncthreads();
     const int nm = moves;
-    const long long layer = (long long)blockIdx.y * p.n_pages * p.page_size * p.row_vecs;
-    for (int c = blockIdx.z * kCmThreads + tid; c < 2 * p.row_vecs; c += gridDim.z * kCmThreads) {
-        uint4 *base = (c < p.row_vecs ? p.kp + c : p.vp + (c - p.row_vecs)) + layer;
+    if (nm == 0) return;
+    const long long layer = (long long)p.n_pages * p.page_size * p.row_vecs;
+    const int cols = 2 * p.row_vecs;
+    // Columns of the layers blockIdx.y, blockIdx.y + gridDim.y, ...
+    const int layers = (p.layers - (int)blockIdx.y + (int)gridDim.y - 1) / (int)gridDim.y;
+    for (int w = tid; w < layers * cols; w += kCmThreads) {
+        const int l = w / cols, c = w - l * cols;
+        uint4 *base = (c < p.row_vecs ? p.kp + c : p.vp + (c - p.row_vecs)) +
+                      ((long long)blockIdx.y + (long long)l * gridDim.y) * layer;
         for (int i = 0; i < nm; i += kCmBatch) {
             uint4 x[kCmBatch];
 #pragma unroll
@@ -289,10 +313,12 @@ magicdec_status launch_tree_commit(const magicdec_paged_shape &s, int n, int lay
     p.page_size = s.page_size;
     p.n_pages = s.n_pages;
     p.max_pages = s.max_pages;
-    const int splits = (2 * p.row_vecs + kCmThreads - 1) / kCmThreads;
-    return magicdec_host::launch_pdl(tree_commit_kernel,
-                                     dim3((unsigned)s.B, (unsigned)layers, (unsigned)(splits < 8 ? splits : 8)),
-                                     dim3(kCmThreads), 0, st, p);
+    p.layers = layers;
+    // A CTA takes several layers of a sequence, as long as there are some eight CTAs an SM.
+    const int want = (8 * magicdec_host::sm_count() + s.B - 1) / s.B;
+    const int groups = layers < want ? layers : want;
+    return magicdec_host::launch_pdl(tree_commit_kernel, dim3((unsigned)s.B, (unsigned)groups), dim3(kCmThreads), 0, st,
+                                     p);
 }
 
 }  // namespace magicdec

@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kTaThreads) tree_accept_kernel(const TreeAccep
         const float4 *vec = reinterpret_cast<const float4 *>(row + pre);
         Best best{-INFINITY, 0xffffffffu};
         if (rank == 0 && tid < pre) best.see(ld_dep_f(row + tid), tid);
-#pragma unroll 4
+#pragma unroll 8
         for (int i = v0 + tid; i < v1; i += kTaThreads) {
             const float4 x = ld_dep_f4(vec + i);
             const uint32_t e = pre + 4 * i;
@@ -155,7 +155,10 @@ magicdec_status launch_tree_accept(int B, int n, int V, const float *target, con
     p.err = magicdec_host::device_error_word();
     p.n = n;
     p.V = V;
-    int C = 8;
+    // As many CTAs a row as there are places for all sequences at once (four CTAs an SM).
+    int C = kTaMaxCluster;
+    while (C > 1 && (long long)B * C > 4ll * magicdec_host::sm_count()) C /= 2;
+    if (!magicdec_host::allow_wide_cluster_once<tree_accept_kernel>()) return MAGICDEC_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)B * C);
     cfg.blockDim = dim3(kTaThreads);

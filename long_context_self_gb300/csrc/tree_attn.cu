@@ -44,17 +44,16 @@ constexpr int kTrMaxNodes = 256;
 constexpr int kTrOut = 256;                   // first TMEM column of O (S: 0 and 128)
 constexpr float kTrLazy = 24.0f;              // log2 growth of a row's maximum that is put up with
 
-// What the joining kernel has to know of a sequence: its first entry in the list
-// of work, the number of its key tiles and its nodes.  Entry B holds the run length.
-struct TreeSeq {
-    long long first;
-    int tiles, nodes;
+// Where a CTA's part of the list begins, for the joining kernel: a list entry, its first
+// tile there, its tiles and its sequence's nodes, and the length of a run.
+struct TreeStart {
+    int b, h, rb, t0, tiles, nodes, run, pad;
 };
 
 struct TreeAttnParams {
     const int32_t *len, *n_nodes, *parent, *table;
     uint16_t *out;
-    TreeSeq *seq;          // workspace: [B + 1]
+    TreeStart *start;      // workspace: [grid]
     float2 *stat;          // workspace: [2 * grid][RT * rr] (max, sum)
     float4 *part;          // workspace: [2 * grid][RT][d / 4][rr]
     int rr;                // rows of a row tile in the workspace
@@ -422,7 +421,6 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         for (int b = ba; b < bz; ++b) {
             if (per > 1) sq = seq_at<RT>(p, b);
             const long long w = (long long)(sq.tiles * sq.blocks) * p.H_kv;
-            if (blockIdx.x == 0) p.seq[b] = TreeSeq{before, sq.tiles, sq.nodes};
             if (t0 >= before && t0 < before + w) {
                 found[0] = b;
                 found[1] = (int)(t0 - before);
@@ -432,10 +430,13 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 found[5] = sq.total;
                 found[6] = sq.tiles;
                 found[7] = sq.blocks;
+                const int item = found[1] / sq.tiles, h = item / sq.blocks;
+                p.start[blockIdx.x] = TreeStart{b, h, item - h * sq.blocks, found[1] - item * sq.tiles, sq.tiles,
+                                                sq.nodes, (int)run, 0};
             }
             before += w;
         }
-        if (blockIdx.x == 0 && tid == 0) p.seq[p.B] = TreeSeq{run, 0, 0};
+        if (t0 >= all && tid == 0) p.start[blockIdx.x] = TreeStart{};
     }
     tc_fence_before();
     __syncthreads();
@@ -866,43 +867,47 @@ __global__ void __launch_bounds__(kTrThreads, 1)
 }
 
 // ------------------------------------------------------------------ the joining
-// One thread: four channels of one row, over the CTAs that had a run of its list
-// entry, in the order of the list.  Rows that belong to no entry (nodes past the
-// sequence's count) are set to zero.
+// `per` blocks for every border between two CTAs' runs: where it is the first inside a list
+// entry, they join that entry's partials, in the order of the list.  PL neighbouring warps
+// share the partials of 32 * (8 / PL) items of four channels of a row.  With few entries, each
+// in many parts, and few items, PL = 8 keeps the chain of loads short (one token over 2k, 16
+// parts: 4 us less); with many items it would be blocks without number (64 nodes, 8 sequences
+// of 8k: 38,656 blocks, 32 us more), and PL = 1 keeps them few.  A block for every
+// sequence then sets the rows of the nodes that it does not have to zero.
 constexpr int kTjThreads = 256;
 
-template <int RT>
-__global__ void __launch_bounds__(kTjThreads) tree_attn_join_kernel(const TreeAttnParams p, int D) {
+template <int RT, int PL>
+__global__ void __launch_bounds__(kTjThreads) tree_attn_join_kernel(const TreeAttnParams p, int D, int per) {
+    __shared__ float4 xo[PL > 1 ? kTjThreads : 1];
+    __shared__ float2 xs[PL > 1 ? kTjThreads : 1];
     pdl_trigger();
     pdl_wait();
-    const int b = blockIdx.z, h = blockIdx.y;
-    const int R = p.n * p.G;
-    const int it = blockIdx.x * kTjThreads + threadIdx.x;
-    if (it >= R * (D / 4)) return;
-    const int c4 = it / R, gr = it - c4 * R;
-    const int node = gr / p.G, g = gr - node * p.G;
-    const TreeSeq s = p.seq[b];
-    uint2 *dst = reinterpret_cast<uint2 *>(p.out + (((long long)b * p.n + node) * p.H_q + h * p.G + g) * D) + c4;
-    if (node >= s.nodes || s.tiles == 0) {
-        *dst = make_uint2(0, 0);
+    const int tid = threadIdx.x, borders = (p.grid - 1) * per;
+    if ((int)blockIdx.x >= borders) {
+        const int b = blockIdx.x - borders;
+        const int nodes = tr_clamp(ld_dep(p.n_nodes + b), p.n);
+        const long long row = (long long)p.H_q * D / 8;
+        uint4 *o = reinterpret_cast<uint4 *>(p.out) + (long long)b * p.n * row;
+        for (long long i = nodes * row + tid; i < p.n * row; i += kTjThreads) o[i] = make_uint4(0, 0, 0, 0);
         return;
     }
-    const long long run = p.seq[p.B].first;
-    const int blocks = (s.nodes + RT * p.NB - 1) / (RT * p.NB);
-    const int tile = node / p.NB, rb = tile / RT, rt = tile - rb * RT;
-    const long long t0 = s.first + (long long)(h * blocks + rb) * s.tiles, t1 = t0 + s.tiles - 1;
-    const int c0 = (int)quotient(t0, (int)run), c1 = (int)quotient(t1, (int)run);
-    if (c0 == c1) return;                              // one CTA had it whole and wrote it
-    const int row = (node - tile * p.NB) * p.G + g;
-    const int first = 2 * c0 + (t0 == c0 * run ? 0 : 1);
+    const int c1 = 1 + blockIdx.x / per;
+    const TreeStart s = p.start[c1];
+    if (s.t0 == 0 || s.t0 > s.run) return;             // no entry is cut here, or not for the first time
+    constexpr int ITEMS = kTjThreads / PL;
+    const int it = (blockIdx.x % per) * ITEMS + tid % ITEMS, pl = tid / ITEMS;
+    const int base = s.rb * RT * p.NB;                 // first node of the entry
+    const int rows = min(s.nodes - base, RT * p.NB) * p.G;
+    const bool real = it < rows * (D / 4);
+    if (PL == 1 && !real) return;
+    const int c4 = real ? it / rows : 0, gr = real ? it - c4 * rows : 0;
+    const int rt = RT == 2 && gr >= p.NB * p.G ? 1 : 0, row = gr - rt * p.NB * p.G;
+    const int first = 2 * (c1 - 1) + (s.t0 == s.run ? 0 : 1);      // the partial before the border
+    const int parts = 1 + (s.tiles - s.t0 + s.run - 1) / s.run;
     const float sl = p.scale_log2;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float top = -INFINITY, sum = 0.f;
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-        const long long slot = c == c0 ? first : 2 * c;
-        const float2 e = p.stat[(slot * RT + rt) * p.rr + row];
-        const float4 o = p.part[((slot * RT + rt) * (D / 4) + c4) * p.rr + row];
+    auto add = [&](float2 e, float4 o) {
         const float m = fmaxf(top, e.x), mu = m == -INFINITY ? 0.f : m;
         const float f = fast_exp2((top - mu) * sl), w = fast_exp2((e.x - mu) * sl);
         top = m;
@@ -911,9 +916,24 @@ __global__ void __launch_bounds__(kTjThreads) tree_attn_join_kernel(const TreeAt
         acc.y = acc.y * f + w * o.y;
         acc.z = acc.z * f + w * o.z;
         acc.w = acc.w * f + w * o.w;
+    };
+#pragma unroll 4
+    for (int k = pl; k < parts; k += PL) {
+        const long long slot = k == 0 ? first : 2 * (c1 + k - 1);
+        add(p.stat[(slot * RT + rt) * p.rr + row], p.part[((slot * RT + rt) * (D / 4) + c4) * p.rr + row]);
+    }
+    if (PL > 1) {
+        xs[tid] = make_float2(top, sum);
+        xo[tid] = acc;
+        __syncthreads();
+        if (pl > 0 || !real) return;
+        for (int k = 1; k < PL; ++k) add(xs[k * ITEMS + tid], xo[k * ITEMS + tid]);
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    *dst = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    const int local = gr / p.G;
+    uint16_t *dst = p.out + (((long long)s.b * p.n + base + local) * p.H_q + s.h * p.G + (gr - local * p.G)) * D + c4 * 4;
+    *reinterpret_cast<uint2 *>(dst) =
+        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
 }
 
 // ------------------------------------------------------------------- host side
@@ -927,7 +947,7 @@ static int tr_part_rows(int n, int G) { return n <= 128 / G ? (n * G + 7) / 8 * 
 size_t tree_attn_workspace_bytes(const magicdec_paged_shape &s, int n) {
     const int G = s.H_q / s.H_kv;
     const size_t rows = 2 * (size_t)magicdec_host::sm_count() * tr_row_tiles(n, G) * tr_part_rows(n, G);
-    return tr_align(((size_t)s.B + 1) * sizeof(TreeSeq)) + tr_align(rows * sizeof(float2)) + rows * s.d * 4;
+    return tr_align(magicdec_host::sm_count() * sizeof(TreeStart)) + tr_align(rows * sizeof(float2)) + rows * s.d * 4;
 }
 
 // The list of work is counted in 32 bits within a sequence and within a CTA's run.
@@ -948,11 +968,13 @@ static magicdec_status launch_tree_t(const CUtensorMap &tmq, const CUtensorMap &
     magicdec_status s =
         magicdec_host::launch_pdl(kern, dim3((unsigned)p.grid), dim3(kTrThreads), smem, st, tmq, tmk, tmv, p);
     if (s != MAGICDEC_OK) return s;
-    const int items = p.n * p.G * (D / 4);
-    return magicdec_host::launch_pdl(tree_attn_join_kernel<RT>,
-                                     dim3((unsigned)((items + kTjThreads - 1) / kTjThreads), (unsigned)p.H_kv,
-                                          (unsigned)p.B),
-                                     dim3(kTjThreads), 0, st, p, D);
+    const int items = (p.n < RT * p.NB ? p.n : RT * p.NB) * p.G * (D / 4);
+    const bool few = items <= 512 && 2 * (long long)p.B * p.H_kv <= p.grid;
+    const int block = few ? kTjThreads / 8 : kTjThreads;
+    const int per = (items + block - 1) / block;
+    return magicdec_host::launch_pdl(few ? tree_attn_join_kernel<RT, 8> : tree_attn_join_kernel<RT, 1>,
+                                     dim3((unsigned)((p.grid - 1) * per + (p.n_nodes ? p.B : 0))), dim3(kTjThreads), 0,
+                                     st, p, D, per);
 }
 
 magicdec_status launch_tree_attn(const magicdec_paged_shape &s, int n, const uint16_t *q, const uint16_t *kp,
@@ -982,8 +1004,8 @@ magicdec_status launch_tree_attn(const magicdec_paged_shape &s, int n, const uin
     const int RT = tr_row_tiles(n, p.G);
     const size_t slots = 2 * (size_t)p.grid;
     uint8_t *w = static_cast<uint8_t *>(ws);
-    p.seq = reinterpret_cast<TreeSeq *>(w);
-    w += tr_align(((size_t)s.B + 1) * sizeof(TreeSeq));
+    p.start = reinterpret_cast<TreeStart *>(w);
+    w += tr_align(p.grid * sizeof(TreeStart));
     p.stat = reinterpret_cast<float2 *>(w);
     p.rr = tr_part_rows(n, p.G);
     w += tr_align(slots * RT * p.rr * sizeof(float2));
@@ -1012,8 +1034,8 @@ magicdec_status launch_tree_attn(const magicdec_paged_shape &s, int n, const uin
     const uint64_t qs[3] = {(uint64_t)D * 2, (uint64_t)s.H_q * D * 2, (uint64_t)n * s.H_q * D * 2};
     const uint32_t qbx[4] = {64, (uint32_t)p.G, (uint32_t)p.NB, 1};
     auto pool = [&](CUtensorMap *m, const uint16_t *x) {
-        return p.by8 ? magicdec_host::encode_tmap_bf16(m, x, 5, kd5, ks5, kb5)
-                     : magicdec_host::encode_tmap_bf16(m, x, 4, kd4, ks4, kb4);
+        return p.by8 ? magicdec_host::encode_tmap_bf16(m, x, 5, kd5, ks5, kb5, D * 2)
+                     : magicdec_host::encode_tmap_bf16(m, x, 4, kd4, ks4, kb4, D * 2);
     };
     if (!pool(&tmk, kp) || !pool(&tmv, vp) || !magicdec_host::encode_tmap_bf16_4d(&tmq, q, qd, qs, qbx))
         return MAGICDEC_ERR_CUDA;
