@@ -40,7 +40,6 @@ __device__ __forceinline__ long long pool_row(const int32_t *table_row, long lon
 }
 
 // ---------------------------------------------------------------------- append
-constexpr int kApThreads = 256;
 constexpr int kApMaxTree = 256;      // nodes of an explicit tree
 
 struct AppendParams {
@@ -62,129 +61,117 @@ __device__ __forceinline__ uint32_t turn_pair(uint32_t x, float2 c) {
     const float a = bf_lo(x), b = bf_hi(x);
     return pack_bf16(a * c.x - b * c.y, a * c.y + b * c.x);
 }
-// Two channels and, `sign` times, the two that they are paired with: x cos + sign * y sin.
-__device__ __forceinline__ uint32_t turn_with(uint32_t x, uint32_t y, float4 c, float sign) {
-    return pack_bf16(bf_lo(x) * c.x + sign * (bf_lo(y) * c.y), bf_hi(x) * c.z + sign * (bf_hi(y) * c.w));
+// Two channels of the first half (x) and the two that they are paired with (y).
+__device__ __forceinline__ void turn_halves(uint32_t &x, uint32_t &y, float2 c0, float2 c1) {
+    const float a0 = bf_lo(x), a1 = bf_hi(x), b0 = bf_lo(y), b1 = bf_hi(y);
+    x = pack_bf16(a0 * c0.x - b0 * c0.y, a1 * c1.x - b1 * c1.y);
+    y = pack_bf16(a0 * c0.y + b0 * c0.x, a1 * c1.y + b1 * c1.x);
 }
 
-// A CTA takes T consecutive tokens of one sequence and goes over their head rows (q, k and v
-// rows of d channels), VPH = d / 8 lanes a row, one 16-byte vector a lane: a row is read and
-// written whole, and the channels rotated with one another come from another lane of the row.
-// The first rows' loads are under way while the lengths, the table and the angles (once per
-// token, for all its heads) are read and computed.  Bound: HBM, 4 (H_q + 2 H_kv) d bytes a
-// token.
-template <int T, int VPH, bool INTER>
-__global__ void __launch_bounds__(kApThreads) paged_append_kernel(const AppendParams p) {
-    constexpr int ROWS = kApThreads / VPH;      // rows of a pass
-    constexpr int AHEAD = 4;                    // passes loaded together
-    __shared__ __align__(16) float2 cs[T][VPH * 4];
+// A CTA of NT threads takes a token, LR = d / 16 lanes one of its head rows (q, k and v rows
+// of d channels) at a time, two 16-byte vectors a lane: the two whose channels are rotated
+// with one another, or two neighbours.  A lane keeps to its channels, so its 8 angles stay in
+// registers for all rows (read from shared memory for every row, they bounded the kernel: 35 us
+// for 4096 tokens of 48 rows).  The first rows' loads are under way while the lengths, the
+// table, the tree and the angles (once per token) are read and computed.  Bound: HBM,
+// 4 (H_q + 2 H_kv) d bytes a token.  Small CTAs, because what a token needs first is a chain of
+// loads that only other CTAs' rows can cover: 4096 tokens in CTAs of 64, 128 or 256 threads (1, 2
+// or 4 tokens) take 17.7, 21.1 and 23.9 us, of 14.9 us at the measured copy rate.
+template <int NT, int LR, bool INTER>
+__global__ void __launch_bounds__(NT) paged_append_kernel(const AppendParams p) {
+    constexpr int ROWS = NT / LR;               // rows of a pass
+    constexpr int AHEAD = 2;                    // passes loaded together
+    __shared__ float2 cs[LR * 8];               // room for d / 2 angles
     __shared__ int par[kApMaxTree];
-    __shared__ long long dst[T];
-    __shared__ int posn[T];
-    const int b = blockIdx.y, i0 = blockIdx.x * T, tid = threadIdx.x;
+    const int b = blockIdx.y, i = blockIdx.x, tid = threadIdx.x;
     pdl_trigger();
     pdl_wait();
     const int cap = p.page_size * p.max_pages;
     const int len = pg_clamp(checked(ld_dep(p.len + b), 0, cap, p.err), cap);
     const int cnt = p.n_new ? pg_clamp(checked(ld_dep(p.n_new + b), 0, p.n, p.err), p.n) : p.n;
-    if (i0 >= cnt) return;
-    const int nt = min(T, cnt - i0);
-    const int nq = p.q_out ? p.H_q : 0, R = nq + 2 * p.H_kv;         // rows of a token
-    const int c = tid % VPH, total = nt * R;
-    const long long tok0 = (long long)b * p.n + i0;
-    auto load = [&](int w) {                                        // vector c of row w % R of token w / R
-        const int t = T == 1 ? 0 : w / R, r = w - t * R;
-        const uint16_t *src = r < nq ? p.q + (tok0 + t) * p.q_stride + r * p.d
-                              : r < nq + p.H_kv ? p.k + (tok0 + t) * p.k_stride + (r - nq) * p.d
-                                                : p.v + (tok0 + t) * p.v_stride + (r - nq - p.H_kv) * p.d;
-        return ld_once_u4(reinterpret_cast<const uint4 *>(src) + c);
+    if (i >= cnt) return;
+    const int nq = p.q_out ? p.H_q : 0, R = nq + 2 * p.H_kv;        // rows of the token
+    const long long tok = (long long)b * p.n + i;
+    const int l = tid % LR, pairs = p.rot / 16;                     // pairs: lanes of a row that rotate halves
+    const bool halves = !INTER && l < pairs;
+    const int v0 = halves ? l : 2 * l, v1 = halves ? l + pairs : 2 * l + 1;   // the lane's vectors
+    auto load = [&](int r, uint4 (&x)[2]) {
+        const uint16_t *src = r < nq ? p.q + tok * p.q_stride + r * p.d
+                              : r < nq + p.H_kv ? p.k + tok * p.k_stride + (r - nq) * p.d
+                                                : p.v + tok * p.v_stride + (r - nq - p.H_kv) * p.d;
+        x[0] = ld_once_u4(reinterpret_cast<const uint4 *>(src) + v0);
+        x[1] = ld_once_u4(reinterpret_cast<const uint4 *>(src) + v1);
     };
-    uint4 x[AHEAD];
+    uint4 x[AHEAD][2];
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k) {
-        const int w = tid / VPH + k * ROWS;
-        if (w < total) x[k] = load(w);
-    }
-    if (p.parent)
-        for (int i = tid; i < min(i0 + T, p.n); i += kApThreads)
-            par[i] = checked(ld_dep(p.parent + (long long)b * p.n + i), -1, i - 1, p.err);
-    if (tid < nt)
-        dst[tid] = pool_row(p.table + (long long)b * p.max_pages, (long long)len + i0 + tid, p.page_size, p.n_pages,
-                            p.max_pages, p.err);
+    for (int k = 0; k < AHEAD; ++k)
+        if (tid / LR + k * ROWS < R) load(tid / LR + k * ROWS, x[k]);
+    const long long dst = pool_row(p.table + (long long)b * p.max_pages, (long long)len + i, p.page_size, p.n_pages,
+                                   p.max_pages, tid == 0 ? p.err : nullptr);
+    int at = i;                                                     // position after len
     if (p.parent) {
+        for (int j = tid; j <= i; j += NT)
+            par[j] = checked(ld_dep(p.parent + (long long)b * p.n + j), -1, j - 1, p.err);
         __syncthreads();
-        if (tid < nt) {
-            int depth = 0;
-            for (int j = i0 + tid; par[j] >= 0 && par[j] < j; j = par[j]) ++depth;
-            posn[tid] = depth;
-        }
-        __syncthreads();
+        at = 0;
+        for (int j = i; par[j] >= 0 && par[j] < j; j = par[j]) ++at;
     }
     // The angle position * inv_freq reaches 1e5 radians and more, where fp32 would
     // lose the low bits of the turn: the product in turns is formed and reduced in
     // fp64, and the fraction handed to the fp32 sine and cosine.
-    const int half = p.rot / 2;
-    for (int w = tid; w < nt * half; w += kApThreads) {
-        const int t = w / half, f = w - t * half;
-        const int at = p.parent ? posn[t] : i0 + t;
+    for (int f = tid; f < p.rot / 2; f += NT) {
         const double turns = ((double)len + at) * ((double)ld_dep_f(p.inv_freq + f) * 0.15915494309189535);
-        float s, co;
-        sincospif((float)(2.0 * (turns - rint(turns))), &s, &co);
-        cs[t][f] = make_float2(co, s);
+        float s, c;
+        sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
+        cs[f] = make_float2(c, s);
     }
     __syncthreads();
-    const int rv = p.rot / 8;                                       // rotated vectors of a row
-    const int lane = tid & 31, other = c < rv / 2 ? lane + rv / 2 : lane - rv / 2;
-    const float sign = c < rv / 2 ? -1.f : 1.f;
-    const int f0 = INTER ? c * 4 : (c < rv / 2 ? c : c - rv / 2) * 8;
-    // Every lane of a warp takes part in a pass's exchange; a row that is not there is not stored.
-    for (int w0 = tid / VPH; w0 - tid / VPH < total; w0 += AHEAD * ROWS) {
-        if (w0 != tid / VPH) {
+    // Interleaved, a vector has 4 angles; the halves' vectors share 8.
+    const bool turned = INTER ? v0 * 8 < p.rot : halves;            // rot is a multiple of 16: both vectors or none
+    float2 a[8];
+    if (turned)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) a[k] = cs[l * 8 + k];
+    for (int r0 = tid / LR; r0 < R; r0 += AHEAD * ROWS) {
+        if (r0 >= AHEAD * ROWS) {
 #pragma unroll
             for (int k = 0; k < AHEAD; ++k)
-                if (w0 + k * ROWS < total) x[k] = load(w0 + k * ROWS);
+                if (r0 + k * ROWS < R) load(r0 + k * ROWS, x[k]);
         }
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
-            const int w = w0 + k * ROWS;
-            if (w - tid / VPH >= total) break;                      // the same for the whole block
-            const int t = T == 1 ? 0 : min(w / R, nt - 1), r = w - t * R;
-            uint4 o = x[k];
-            const bool turned = c < rv && r < nq + p.H_kv;
-            if (INTER) {
-                if (turned) {
-                    const float2 *a = &cs[t][f0];
-                    o = make_uint4(turn_pair(o.x, a[0]), turn_pair(o.y, a[1]), turn_pair(o.z, a[2]), turn_pair(o.w, a[3]));
-                }
-            } else {
-                uint4 y;
-                y.x = __shfl_sync(0xffffffffu, x[k].x, other & 31);
-                y.y = __shfl_sync(0xffffffffu, x[k].y, other & 31);
-                y.z = __shfl_sync(0xffffffffu, x[k].z, other & 31);
-                y.w = __shfl_sync(0xffffffffu, x[k].w, other & 31);
-                if (turned) {
-                    const float4 *a = reinterpret_cast<const float4 *>(&cs[t][f0]);
-                    o = make_uint4(turn_with(o.x, y.x, a[0], sign), turn_with(o.y, y.y, a[1], sign),
-                                   turn_with(o.z, y.z, a[2], sign), turn_with(o.w, y.w, a[3], sign));
+            const int r = r0 + k * ROWS;
+            if (r >= R) break;
+            uint4 y = x[k][0], z = x[k][1];
+            if (turned && r < nq + p.H_kv) {
+                if (INTER) {
+                    y = make_uint4(turn_pair(y.x, a[0]), turn_pair(y.y, a[1]), turn_pair(y.z, a[2]), turn_pair(y.w, a[3]));
+                    z = make_uint4(turn_pair(z.x, a[4]), turn_pair(z.y, a[5]), turn_pair(z.z, a[6]), turn_pair(z.w, a[7]));
+                } else {
+                    turn_halves(y.x, z.x, a[0], a[1]);
+                    turn_halves(y.y, z.y, a[2], a[3]);
+                    turn_halves(y.z, z.z, a[4], a[5]);
+                    turn_halves(y.w, z.w, a[6], a[7]);
                 }
             }
-            if (w >= total) continue;
+            uint16_t *out;
             if (r < nq) {
-                reinterpret_cast<uint4 *>(p.q_out + ((tok0 + t) * p.H_q + r) * p.d)[c] = o;
-            } else if (dst[t] >= 0) {
+                out = p.q_out + (tok * p.H_q + r) * p.d;
+            } else {
+                if (dst < 0) continue;
                 const int h = r - nq;
-                uint16_t *out = h < p.H_kv ? p.kp + (dst[t] * p.H_kv + h) * p.d : p.vp + (dst[t] * p.H_kv + h - p.H_kv) * p.d;
-                reinterpret_cast<uint4 *>(out)[c] = o;
+                out = h < p.H_kv ? p.kp + (dst * p.H_kv + h) * p.d : p.vp + (dst * p.H_kv + h - p.H_kv) * p.d;
             }
+            reinterpret_cast<uint4 *>(out)[v0] = y;
+            reinterpret_cast<uint4 *>(out)[v1] = z;
         }
     }
 }
 
-template <int T, int VPH>
+template <int NT, int LR>
 static magicdec_status launch_append_t(const AppendParams &p, int interleaved, cudaStream_t st) {
-    const dim3 grid((unsigned)((p.n + T - 1) / T), (unsigned)p.B);
-    return magicdec_host::launch_pdl(interleaved ? paged_append_kernel<T, VPH, true> : paged_append_kernel<T, VPH, false>,
-                                     grid, dim3(kApThreads), 0, st, p);
+    return magicdec_host::launch_pdl(interleaved ? paged_append_kernel<NT, LR, true> : paged_append_kernel<NT, LR, false>,
+                                     dim3((unsigned)p.n, (unsigned)p.B), dim3(NT), 0, st, p);
 }
 
 magicdec_status launch_paged_append(const magicdec_paged_shape &s, int n, const uint16_t *q, long long q_stride,
@@ -217,11 +204,11 @@ magicdec_status launch_paged_append(const magicdec_paged_shape &s, int n, const 
     p.page_size = s.page_size;
     p.n_pages = s.n_pages;
     p.max_pages = s.max_pages;
-    // Four tokens a CTA pay for its way in (angles, table, tree) once the GPU has CTAs enough
-    // without splitting further.
-    if ((long long)s.B * n >= 8ll * magicdec_host::sm_count())
-        return s.d == 128 ? launch_append_t<4, 16>(p, interleaved, st) : launch_append_t<4, 8>(p, interleaved, st);
-    return s.d == 128 ? launch_append_t<1, 16>(p, interleaved, st) : launch_append_t<1, 8>(p, interleaved, st);
+    // Larger CTAs while there are fewer tokens than SMs: then a token's own rows take longest (one
+    // token of 48 rows: 2.7 us with 256 threads, 3.7 us with 64).
+    if ((long long)s.B * n >= magicdec_host::sm_count())
+        return s.d == 128 ? launch_append_t<64, 8>(p, interleaved, st) : launch_append_t<64, 4>(p, interleaved, st);
+    return s.d == 128 ? launch_append_t<256, 8>(p, interleaved, st) : launch_append_t<256, 4>(p, interleaved, st);
 }
 
 // ---------------------------------------------------------------------- commit

@@ -16,6 +16,8 @@ namespace magicdec {
 constexpr int kTaThreads = 512;
 constexpr int kTaMaxCluster = 16;
 constexpr int kTaMaxNodes = 256;
+constexpr int kTaPerSm = 3;             // CTAs an SM holds
+constexpr int kTaAhead = 4;             // loads of a thread under way
 static_assert(kTaMaxNodes <= kTaThreads, "one thread holds a node's token and parent");
 
 struct TreeAcceptParams {
@@ -47,25 +49,20 @@ __device__ __forceinline__ void st_cluster_u64(uint64_t *p, uint32_t rank, uint6
 }
 
 // Order-preserving key: larger value first, then the smaller index.  -0 counts
-// as +0 (they compare equal, so the smaller index has to win).
+// as +0 (they compare equal, so the smaller index has to win); 0 stands for no
+// value above -infinity.
 __device__ __forceinline__ uint64_t best_key(float v, uint32_t idx) {
     const uint32_t u = __float_as_uint(v + 0.0f);
     const uint32_t o = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-    return ((uint64_t)o << 32) | (uint32_t)~idx;
+    return v > -INFINITY ? ((uint64_t)o << 32) | (uint32_t)~idx : 0;
+}
+// The largest key of a warp, as two 32-bit reductions.
+__device__ __forceinline__ uint64_t warp_best(uint64_t key) {
+    const uint32_t hi = (uint32_t)(key >> 32), top = __reduce_max_sync(0xffffffffu, hi);
+    return ((uint64_t)top << 32) | __reduce_max_sync(0xffffffffu, hi == top ? (uint32_t)key : 0u);
 }
 
-struct Best {
-    float v;
-    uint32_t idx;
-    __device__ __forceinline__ void see(float x, uint32_t i) {
-        if (x > v || idx == 0xffffffffu) {       // a thread meets its indices in ascending order
-            v = x;
-            idx = i;
-        }
-    }
-};
-
-__global__ void __launch_bounds__(kTaThreads) tree_accept_kernel(const TreeAcceptParams p) {
+__global__ void __launch_bounds__(kTaThreads, kTaPerSm) tree_accept_kernel(const TreeAcceptParams p) {
     __shared__ uint64_t slot[2][kTaMaxCluster];
     __shared__ uint64_t wbest[kTaThreads / 32];
     __shared__ int wnext[kTaMaxNodes / 32];
@@ -90,35 +87,51 @@ __global__ void __launch_bounds__(kTaThreads) tree_accept_kernel(const TreeAccep
         const int pre = min(p.V, (4 - mis) & 3), nv = (p.V - pre) / 4, post = pre + nv * 4;
         const int v0 = (int)((long long)nv * rank / C), v1 = (int)((long long)nv * (rank + 1) / C);
         const float4 *vec = reinterpret_cast<const float4 *>(row + pre);
-        Best best{-INFINITY, 0xffffffffu};
-        if (rank == 0 && tid < pre) best.see(ld_dep_f(row + tid), tid);
-#pragma unroll 8
-        for (int i = v0 + tid; i < v1; i += kTaThreads) {
-            const float4 x = ld_dep_f4(vec + i);
-            const uint32_t e = pre + 4 * i;
-            best.see(x.x, e);
-            best.see(x.y, e + 1);
-            best.see(x.z, e + 2);
-            best.see(x.w, e + 3);
-        }
-        if (rank == C - 1 && tid < p.V - post) best.see(ld_dep_f(row + post + tid), post + tid);
-        uint64_t key = best.idx == 0xffffffffu ? 0 : best_key(best.v, best.idx);
+        // The largest of a thread's vectors, the first of equal ones.
+        float best = -INFINITY;
+        float4 at = make_float4(best, best, best, best);
+        int vi = 0;
+        auto see = [&](float4 x, int i) {
+            const float m = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w));
+            if (m > best) {
+                best = m;
+                at = x;
+                vi = i;
+            }
+        };
+        int i = v0 + tid;
+        for (; i + (kTaAhead - 1) * kTaThreads < v1; i += kTaAhead * kTaThreads) {
+            float4 x[kTaAhead];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
+            for (int k = 0; k < kTaAhead; ++k) x[k] = ld_dep_f4(vec + i + k * kTaThreads);
+#pragma unroll
+            for (int k = 0; k < kTaAhead; ++k) see(x[k], i + k * kTaThreads);
+        }
+        {
+            float4 x[kTaAhead];
+#pragma unroll
+            for (int k = 0; k < kTaAhead - 1; ++k)
+                if (i + k * kTaThreads < v1) x[k] = ld_dep_f4(vec + i + k * kTaThreads);
+#pragma unroll
+            for (int k = 0; k < kTaAhead - 1; ++k)
+                if (i + k * kTaThreads < v1) see(x[k], i + k * kTaThreads);
+        }
+        const uint32_t first = pre + 4 * vi;
+        uint64_t key = best_key(best, first + (at.x == best ? 0 : at.y == best ? 1 : at.z == best ? 2 : 3));
+        if (rank == 0 && tid < pre) key = max(key, best_key(ld_dep_f(row + tid), tid));
+        if (rank == C - 1 && tid < p.V - post) key = max(key, best_key(ld_dep_f(row + post + tid), post + tid));
+        key = warp_best(key);
         if (lane == 0) wbest[warp] = key;
         __syncthreads();
         if (warp == 0) {
-            key = lane < kTaThreads / 32 ? wbest[lane] : 0;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
+            key = warp_best(lane < kTaThreads / 32 ? wbest[lane] : 0);
             if (lane < C) st_cluster_u64(&slot[level & 1][rank], lane, key);
         }
         // One barrier per level: a slot is written again two levels on, after the next
         // barrier, which no CTA reaches before it has read this level's slots.
         cluster_sync();
-        key = slot[level & 1][0];
-        for (uint32_t c = 1; c < C; ++c) key = max(key, slot[level & 1][c]);
-        const int t = (int)~(uint32_t)key;
+        key = warp_best(lane < C ? slot[level & 1][lane] : 0);
+        const int t = key ? (int)~(uint32_t)key : 0;            // nothing above -infinity: all are equal
         const bool go = tid < nn && my_par == u && my_tok == t;
         const unsigned m = __ballot_sync(0xffffffffu, go);
         if (lane == 0 && warp < kTaMaxNodes / 32) wnext[warp] = m ? warp * 32 + __ffs(m) - 1 : -1;
@@ -155,9 +168,9 @@ magicdec_status launch_tree_accept(int B, int n, int V, const float *target, con
     p.err = magicdec_host::device_error_word();
     p.n = n;
     p.V = V;
-    // As many CTAs a row as there are places for all sequences at once (four CTAs an SM).
+    // As many CTAs a row as there are places for all sequences at once (kTaPerSm CTAs an SM).
     int C = kTaMaxCluster;
-    while (C > 1 && (long long)B * C > 4ll * magicdec_host::sm_count()) C /= 2;
+    while (C > 1 && (long long)B * C > (long long)kTaPerSm * magicdec_host::sm_count()) C /= 2;
     if (!magicdec_host::allow_wide_cluster_once<tree_accept_kernel>()) return MAGICDEC_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)B * C);

@@ -689,7 +689,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                         const int first = h * 64 + half * 32;             // this thread's first key of the tile
                         const int k0 = t.p0 + first, rows = t.rows - first;
                         const int c = min(r.s.len - k0, rows);
-                        uint32_t see = node < 0 || c <= 0 ? 0u : c >= 32 ? 0xffffffffu : (1u << c) - 1u;
+                        // (a row without a node may see anything: it is not used)
+                        uint32_t see = node < 0 || c >= 32 ? 0xffffffffu : c <= 0 ? 0u : (1u << c) - 1u;
                         if (node >= 0 && k0 + rows > r.s.len) {
                             for (int a = node; a >= 0; a = p.parent ? (int)mypar[a] - 1 : a - 1) {
                                 const int off = r.s.len + a - k0;
