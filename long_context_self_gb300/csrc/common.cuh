@@ -171,6 +171,18 @@ __device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *tm, in
         : "memory");
 }
 
+// 64 channels of 4 rows of a 2-D tensor map whose box is one row: any rows, one
+// behind the last is zero; they land one after the other, 128 bytes each.
+__device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *tm, int c0, const int (&row)[4], uint64_t *bar,
+                                            uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]),
+        "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
 // Prefetch one tiled 4-D box into L2 (no shared memory, no barrier: a hint).
 __device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap *tm, int c0, int c1, int c2, int c3) {
     asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(

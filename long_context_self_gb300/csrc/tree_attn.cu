@@ -64,6 +64,7 @@ struct TreeAttnParams {
     int tpp;               // key tiles per page (larger pages)
     int grid;
     int br;                // rows of a box
+    int by4;               // pages of fewer than 4 rows: 4 rows of any pages at a time
     int by8;               // pages of a multiple of 8 rows: copied by 5-D boxes
     uint32_t sbo, hoff;    // bytes between groups of 8 rows, and between 64-channel halves, of a K or V tile
     float scale_log2;      // log2(e) / sqrt(d)
@@ -488,6 +489,30 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 // on its way while the warp waits for the ring.
                 const int boxes = (t.rows + p.br - 1) / p.br, r0 = t.p0 - pg0 * p.page_size;
                 const bool pages = p.br == p.page_size;
+                if (p.by4) {
+                    // A lane's 4 rows; one behind the tile or outside the pool is past the pool's last.
+                    int rows[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int at = lane * 4 + k, pg = (t.p0 + at) / p.page_size;
+                        rows[k] = p.n_pages * p.page_size;
+                        if (at < t.rows) {
+                            const int q = ld_dep(table + pg);
+                            if (q < 0 || q >= p.n_pages) raise_error(p.err, kErrPage);
+                            else rows[k] = q * p.page_size + t.p0 + at - pg * p.page_size;
+                        }
+                    }
+                    ok = tr_wait(&empty_r[st], ph ^ 1, p.err, ok, lane);
+                    if (!ok) break;
+                    const int fours = (t.rows + 3) / 4;
+                    if (lane == 0) mbar_arrive_expect_tx(&full_r[st], (uint32_t)(fours * HALVES * 512));
+                    __syncwarp();
+                    if (lane < fours)
+                        for (int hf = 0; hf < HALVES; ++hf)
+                            tma_gather4(dst + hf * kTrBox + lane * 512, is_v ? &tmv : &tmk, (r.h * HALVES + hf) * 64, rows,
+                                        &full_r[st], pol);
+                    continue;
+                }
                 if (RT == 2 || !is_v || boxes > 32) id = lane < boxes ? ld_dep(table + pg0 + (pages ? lane : 0)) : 0;
                 ok = tr_wait(&empty_r[st], ph ^ 1, p.err, ok, lane);
                 if (!ok) break;
@@ -1016,10 +1041,13 @@ magicdec_status launch_tree_attn(const magicdec_paged_shape &s, int n, const uin
     // pages of a multiple of 8 rows as (64 channels, 8 rows, halves of all heads, groups of 8
     // rows, pages): one box is a page (or 128 rows of it) of one KV head, its channels read
     // together and its rows laid out for the tensor cores.  Other pages as (d, H_kv,
-    // page_size, n_pages), boxes of 64 channels x a page (or 128 rows).
+    // page_size, n_pages), boxes of 64 channels x a page (or 128 rows); pages of 1 to 3 rows as
+    // one list of rows, 4 of them a copy (32 sequences of 32k, 8 nodes, pages of 1, 2 and 3 rows:
+    // 4.2, 2.2 and 1.8 ms with a box a page, 1.6 ms so; of 4 rows: 1.15 ms with boxes).
     CUtensorMap tmq, tmk, tmv;
     const int D = s.d, HV = D / 64;
     p.by8 = s.page_size % 8 == 0;
+    p.by4 = s.page_size < 4 && (long long)s.n_pages * s.page_size < INT_MAX;
     p.sbo = p.by8 ? HV * 1024 : 1024;
     p.hoff = p.by8 ? 1024 : kTrBox;
     const uint64_t row = (uint64_t)s.H_kv * D * 2;
@@ -1028,6 +1056,8 @@ magicdec_status launch_tree_attn(const magicdec_paged_shape &s, int n, const uin
     const uint64_t kd4[4] = {(uint64_t)D, (uint64_t)s.H_kv, (uint64_t)s.page_size, (uint64_t)s.n_pages};
     const uint64_t ks4[3] = {(uint64_t)D * 2, row, s.page_size * row};
     const uint32_t kb4[4] = {64, 1, span, 1};
+    const uint64_t kd2[2] = {(uint64_t)s.H_kv * D, (uint64_t)s.n_pages * s.page_size};
+    const uint32_t kb2[2] = {64, 1};
     const uint64_t kd5[5] = {64, 8, (uint64_t)s.H_kv * HV, (uint64_t)s.page_size / 8, (uint64_t)s.n_pages};
     const uint64_t ks5[4] = {row, 128, 8 * row, s.page_size * row};
     const uint32_t kb5[5] = {64, 8, (uint32_t)HV, span / 8, 1};
@@ -1035,8 +1065,9 @@ magicdec_status launch_tree_attn(const magicdec_paged_shape &s, int n, const uin
     const uint64_t qs[3] = {(uint64_t)D * 2, (uint64_t)s.H_q * D * 2, (uint64_t)n * s.H_q * D * 2};
     const uint32_t qbx[4] = {64, (uint32_t)p.G, (uint32_t)p.NB, 1};
     auto pool = [&](CUtensorMap *m, const uint16_t *x) {
-        return p.by8 ? magicdec_host::encode_tmap_bf16(m, x, 5, kd5, ks5, kb5, D * 2)
-                     : magicdec_host::encode_tmap_bf16(m, x, 4, kd4, ks4, kb4, D * 2);
+        return p.by4   ? magicdec_host::encode_tmap_bf16(m, x, 2, kd2, &row, kb2, D * 2)
+               : p.by8 ? magicdec_host::encode_tmap_bf16(m, x, 5, kd5, ks5, kb5, D * 2)
+                       : magicdec_host::encode_tmap_bf16(m, x, 4, kd4, ks4, kb4, D * 2);
     };
     if (!pool(&tmk, kp) || !pool(&tmv, vp) || !magicdec_host::encode_tmap_bf16_4d(&tmq, q, qd, qs, qbx))
         return MAGICDEC_ERR_CUDA;
