@@ -199,24 +199,38 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 
 // ------------------------------------------------------------------ work list
-// Key tile tj of a sequence: its first position and its rows that hold positions.
+// A key tile of a sequence: its first position and its rows that hold positions.
 struct Tile {
     int p0, rows;
 };
-__device__ __forceinline__ Tile tile_at(const TreeAttnParams &p, int tj, int total) {
-    Tile t;
-    int span;
-    if (p.ppt) {
-        span = p.ppt * p.page_size;
-        t.p0 = tj * span;
-    } else {
-        const int pg = tj / p.tpp, r0 = (tj - pg * p.tpp) * kTrKeys;
-        t.p0 = pg * p.page_size + r0;
-        span = min(kTrKeys, p.page_size - r0);
+// Walks over key tiles; a division only where it begins.
+struct TileWalk {
+    int tj, pg, part;       // the tile; with pages of several tiles, its page and its place there
+    __device__ __forceinline__ TileWalk(const TreeAttnParams &p, int tj_) : tj(tj_), pg(0), part(0) {
+        if (!p.ppt) {
+            pg = tj / p.tpp;
+            part = tj - pg * p.tpp;
+        }
     }
-    t.rows = min(span, total - t.p0);
-    return t;
-}
+    __device__ __forceinline__ void step(const TreeAttnParams &p, int n) {
+        tj += n;
+        if (!p.ppt)
+            for (part += n; part >= p.tpp; part -= p.tpp) ++pg;
+    }
+    __device__ __forceinline__ Tile at(const TreeAttnParams &p, int total) const {
+        Tile t;
+        int span;
+        if (p.ppt) {
+            span = p.ppt * p.page_size;
+            t.p0 = tj * span;
+        } else {
+            t.p0 = pg * p.page_size + part * kTrKeys;
+            span = min(kTrKeys, p.page_size - part * kTrKeys);
+        }
+        t.rows = min(span, total - t.p0);
+        return t;
+    }
+};
 __device__ __forceinline__ int tiles_of(const TreeAttnParams &p, int total) {
     if (p.ppt) {
         const int span = p.ppt * p.page_size;
@@ -478,10 +492,12 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             // K and V in turn, as the products need them.
             const int j0 = RT == 1 ? pw : 0, mine = (r.cnt - j0 + STEP - 1) / STEP;
             int id = 0;
+            TileWalk tile(p, r.t0 + j0);
             for (int i = 0; i < 2 * mine; ++i, ++slot) {
+                if (i && (i & 1) == 0) tile.step(p, STEP);
                 if (RT == 2 && (slot & 1) != pw) continue;
-                const int j = j0 + (i >> 1) * STEP, is_v = i & 1;
-                const Tile t = tile_at(p, r.t0 + j, r.s.total);
+                const int is_v = i & 1;
+                const Tile t = tile.at(p, r.s.total);
                 const uint32_t st = slot % NST, ph = (slot / NST) & 1;
                 uint8_t *dst = buf + st * OPER;
                 const int pg0 = t.p0 / p.page_size;
@@ -614,7 +630,14 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 if (!wait(q_full, runs & 1)) break;
                 ++runs;
                 const int cnt = r.cnt, j0 = RT == 1 ? s : 0;
-                auto rows_at = [&](int j) { return j < cnt ? tile_at(p, r.t0 + j, r.s.total).rows : 0; };
+                TileWalk tile(p, r.t0 + j0);
+                int tj = j0;
+                auto next_rows = [&]() {                       // of this stream's next tile, 0 behind the last
+                    const int rows = tj < cnt ? tile.at(p, r.s.total).rows : 0;
+                    tj += STEP;
+                    tile.step(p, STEP);
+                    return rows;
+                };
                 if (RT == 2 && s == 1 && r.rb * 2 * p.NB + p.NB >= r.s.nodes) {
                     // No node in this stream's row tile: its part of every release, in step with the ring.
                     for (int i = 0; i < 2 * cnt; ++i) {
@@ -625,7 +648,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     mbar_arrive(q_empty);
                     continue;
                 }
-                int rows = rows_at(j0);
+                int rows = next_rows(), next = next_rows();    // of the tile at hand and the one after it
                 if (rows > 0) {
                     const uint32_t st = slot % NST;
                     if (!arrived(slot)) break;
@@ -638,10 +661,10 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     if (rows > 0) umma_commit(q_empty);
                     else mbar_arrive(q_empty);
                 }
+                uint32_t vst = slot % NST, kst = (slot + 1) % NST;
+                bool in = false;                               // the tile's V is known to be there
                 for (int j = j0; j < cnt; j += STEP) {
-                    const int next = rows_at(j + STEP);        // rows of the next tile
-                    const uint32_t vst = slot % NST, kst = (slot + 1) % NST;
-                    if (!arrived(slot)) break;
+                    if (!in && !arrived(slot)) break;
                     clear_tail(vst, rows);
                     if (!weigh(c0, vst, rows, j == j0)) break;
                     if (rows <= 64) umma_commit(&empty_r[vst]);
@@ -649,6 +672,10 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                         if (!arrived(slot + 1)) break;
                         scores(c0, kst);
                     }
+                    // While the tensor cores have these: what the next tile needs.
+                    const int after = next_rows();
+                    const uint32_t slot1 = slot + (next > 0 ? 2 : 1), vst1 = slot1 % NST, kst1 = (slot1 + 1) % NST;
+                    in = next > 0 && mbar_try_wait(&full_r[vst1], (slot1 / NST) & 1);
                     if (rows > 64) {
                         if (!weigh(c1, vst, rows, false)) break;
                         umma_commit(&empty_r[vst]);
@@ -656,10 +683,13 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     if (next > 64) scores(c1, kst);
                     if (next > 0) {
                         umma_commit(&empty_r[kst]);
-                        if (j + 2 * STEP >= cnt) umma_commit(q_empty);
+                        if (after == 0) umma_commit(q_empty);
                     }
                     rows = next;
-                    slot += next > 0 ? 2 : 1;
+                    next = after;
+                    slot = slot1;
+                    vst = vst1;
+                    kst = kst1;
                 }
             }
             // The products in flight end before the shared memory and TMEM that they use go.
@@ -795,8 +825,9 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             };
             const Const<0> c0{};
             const Const<1> c1{};
-            for (int j = RT == 1 ? s : 0; active && j < r.cnt; j += STEP) {
-                const Tile t = tile_at(p, r.t0 + j, r.s.total);
+            TileWalk tile(p, r.t0 + (RT == 1 ? s : 0));
+            for (int j = RT == 1 ? s : 0; active && j < r.cnt; j += STEP, tile.step(p, STEP)) {
+                const Tile t = tile.at(p, r.s.total);
                 if (t.rows == kTrKeys && t.p0 + t.rows <= r.s.len) {
                     half_tile(t, c0, c0);
                     half_tile(t, c1, c0);
