@@ -83,6 +83,7 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const AppendParams p) 
     constexpr int AHEAD = 2;                    // passes loaded together
     __shared__ float2 cs[LR * 8];               // room for d / 2 angles
     __shared__ int par[kApMaxTree];
+    __shared__ unsigned turns[kApMaxTree / 32];
     const int b = blockIdx.y, i = blockIdx.x, tid = threadIdx.x;
     pdl_trigger();
     pdl_wait();
@@ -110,11 +111,25 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const AppendParams p) 
                                    p.max_pages, tid == 0 ? p.err : nullptr);
     int at = i;                                                     // position after len
     if (p.parent) {
-        for (int j = tid; j <= i; j += NT)
-            par[j] = checked(ld_dep(p.parent + (long long)b * p.n + j), -1, j - 1, p.err);
+        // The depth, by stretches of nodes each of which follows the one before it (a bit where
+        // one does not): a chain is a single one.
+        for (int j = tid; j < (i / 32 + 1) * 32; j += NT) {
+            const int q = j <= i ? checked(ld_dep(p.parent + (long long)b * p.n + j), -1, j - 1, p.err) : -1;
+            par[j] = q;
+            const unsigned m = __ballot_sync(0xffffffffu, j == 0 || q != j - 1);
+            if (tid % 32 == 0) turns[j / 32] = m;
+        }
         __syncthreads();
         at = 0;
-        for (int j = i; par[j] >= 0 && par[j] < j; j = par[j]) ++at;
+        for (int j = i; j >= 0;) {
+            int w = j / 32;
+            unsigned m = turns[w] & (0xffffffffu >> (31 - (j & 31)));
+            while (m == 0 && w > 0) m = turns[--w];
+            const int z = m ? w * 32 + 31 - __clz(m) : 0;
+            at += j - z + 1;
+            j = par[z] < z ? par[z] : -1;
+        }
+        --at;
     }
     // The angle position * inv_freq reaches 1e5 radians and more, where fp32 would
     // lose the low bits of the turn: the product in turns is formed and reduced in

@@ -256,6 +256,15 @@ __device__ __forceinline__ Seq seq_at(const TreeAttnParams &p, int b) {
     return s;
 }
 
+// The first node of the stretch that ends at node a and in which each one's parent is the
+// node before it: the last bit up to a, of which the first node has one.
+__device__ __forceinline__ int stretch(const uint32_t *turns, int a) {
+    int w = a >> 5;
+    uint32_t m = turns[w] & (0xffffffffu >> (31 - (a & 31)));
+    while (m == 0 && w > 0) m = turns[--w];
+    return m ? w * 32 + 31 - __clz(m) : 0;
+}
+
 // x / d, in 32 bits where they suffice (a 64-bit division is a hundred instructions).
 __device__ __forceinline__ long long quotient(long long x, int d) {
     return x <= 0xffffffffll ? (long long)((uint32_t)x / (uint32_t)d) : x / d;
@@ -304,7 +313,8 @@ struct TrSmem {
     static constexpr int STAGES = (RT == 1 ? 3 : 5) * (D == 128 ? 1 : 2);
     static constexpr int XCH = 2 * 2 * 128 * 4;
     static constexpr int BYTES =
-        RT * OPER + RINGS * STAGES * OPER + 2 * kTrMaxNodes + XCH + (2 * RINGS * STAGES + 16) * 8 + 48;
+        RT * OPER + RINGS * STAGES * OPER + 2 * kTrMaxNodes + 2 * kTrMaxNodes / 8 + XCH +
+        (2 * RINGS * STAGES + 16) * 8 + 48;
 };
 
 // Bounded wait.  A poll may sleep until the phase is over, or for 20 us: a warp that
@@ -363,8 +373,9 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem[];      // swizzled tiles start at multiples of 1024
     uint8_t *qbuf = smem, *ring = smem + RT * OPER;
     uint8_t *par = ring + ALL * OPER;                                    // [2][kTrMaxNodes]
-    float *xch = reinterpret_cast<float *>(par + 2 * kTrMaxNodes);       // [stream][half][128]
-    uint64_t *full = reinterpret_cast<uint64_t *>(par + 2 * kTrMaxNodes + L::XCH);
+    uint32_t *turns = reinterpret_cast<uint32_t *>(par + 2 * kTrMaxNodes);   // [2][kTrMaxNodes / 32]
+    float *xch = reinterpret_cast<float *>(turns + 2 * kTrMaxNodes / 32);       // [stream][half][128]
+    uint64_t *full = reinterpret_cast<uint64_t *>(xch) + L::XCH / 8;
     uint64_t *empty = full + ALL;
     uint64_t *q_full = empty + ALL, *q_empty = q_full + 1;
     uint64_t *s_full = q_empty + 1, *p_full = s_full + 4, *o_full = p_full + 4;   // [stream][half tile]
@@ -709,6 +720,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         const int node_r = row / p.G;                                   // node within the row tile
         const float sl = p.scale_log2;
         uint8_t *mypar = par + s * kTrMaxNodes;
+        uint32_t *myturns = turns + s * (kTrMaxNodes / 32);
         float *mine_x = xch + (s * 2 + half) * 128 + row, *other_x = xch + (s * 2 + 1 - half) * 128 + row;
         uint32_t used[2] = {0, 0};                                      // of this stream's two S
         int par_b = -1;
@@ -719,13 +731,14 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             const bool active = RT == 1 || base < r.s.nodes;
             const bool live = __any_sync(0xffffffffu, node >= 0);         // the warp has rows
             if (p.parent && par_b != r.b) {
-                // parent + 1 of every node in a byte (0: none); a parent that is not before its
-                // node counts as none.
+                // parent + 1 of every node in a byte (0: none; a parent that is not before its
+                // node counts as none), and a bit where it is not the node just before.
                 named_bar_sync(9 + s, 256);
-                if (wt < r.s.nodes) {
-                    const int pi = checked(ld_dep(p.parent + (long long)r.b * p.n + wt), -1, wt - 1, p.err);
-                    mypar[wt] = (uint8_t)(pi >= 0 && pi < wt ? pi + 1 : 0);
-                }
+                const int pi = wt < r.s.nodes
+                                   ? checked(ld_dep(p.parent + (long long)r.b * p.n + wt), -1, wt - 1, p.err) : -1;
+                mypar[wt] = (uint8_t)(pi >= 0 && pi < wt ? pi + 1 : 0);
+                const uint32_t turn = __ballot_sync(0xffffffffu, wt == 0 || pi != wt - 1);
+                if (lane == 0) myturns[wt >> 5] = turn;
                 named_bar_sync(9 + s, 256);
                 par_b = r.b;
             }
@@ -747,10 +760,14 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                         // (a row without a node may see anything: it is not used)
                         uint32_t see = node < 0 || c >= 32 ? 0xffffffffu : c <= 0 ? 0u : (1u << c) - 1u;
                         if (node >= 0 && k0 + rows > r.s.len) {
-                            for (int a = node; a >= 0; a = p.parent ? (int)mypar[a] - 1 : a - 1) {
-                                const int off = r.s.len + a - k0;
-                                if (off < 0) break;                       // ancestors come before their nodes
-                                if (off < rows && off < 32) see |= 1u << off;
+                            // A node's ancestors in stretches of neighbours: a chain is a single one.
+                            const int last = min(rows, 32) - 1;
+                            for (int a = node; a >= 0;) {
+                                const int z = p.parent ? stretch(myturns, a) : 0;
+                                const int lo = max(r.s.len + z - k0, 0), hi = min(r.s.len + a - k0, last);
+                                if (lo <= hi) see |= (0xffffffffu >> (31 - hi)) & (0xffffffffu << lo);
+                                if (r.s.len + z <= k0) break;             // what is further up lies before these keys
+                                a = p.parent ? (int)mypar[z] - 1 : -1;
                             }
                         }
                         if (!__all_sync(0xffffffffu, see == 0xffffffffu)) {
