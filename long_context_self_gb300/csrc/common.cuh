@@ -115,6 +115,37 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, int *e
     return false;
 }
 
+// The same wait for warps that have others with work beside them: a poll may sleep until
+// the phase is over, or for 20 us (a warp that spins takes their issue slots: half of all in
+// tree attention), and the clock is read only now and then.
+__device__ __forceinline__ bool mbar_try_sleep(uint64_t *bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    return done != 0;
+}
+static __device__ __noinline__ bool mbar_poll_on(uint64_t *bar, uint32_t parity, int *err) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 1; i < kMaxPolls; ++i) {
+        if (mbar_try_sleep(bar, parity)) return true;
+        if ((i & 63u) == 0) {
+            const uint64_t t = globaltimer();
+            if (t0 == 0) t0 = t;
+            else if (t - t0 > kMaxWaitNs) break;
+        }
+    }
+    raise_error(err, kErrTimeout);
+    return false;
+}
+__device__ __forceinline__ bool mbar_poll(uint64_t *bar, uint32_t parity, int *err) {
+    return mbar_try_sleep(bar, parity) || mbar_poll_on(bar, parity, err);
+}
+
 // ------------------------------------------------------------- bulk copies
 // One contiguous global -> shared copy through the TMA engine, completing on
 // `bar` with a byte count.  dst/src 16-byte aligned, bytes a multiple of 16.

@@ -265,6 +265,25 @@ __device__ __forceinline__ int stretch(const uint32_t *turns, int a) {
     return m ? w * 32 + 31 - __clz(m) : 0;
 }
 
+// The 32 keys that a node sees, as bits: `prefix` of them (or more, or none) lie before the
+// nodes' slots, `rows` hold anything; of the nodes' it sees its ancestors and itself.  A
+// function of its own, so that its registers are not taken from the tiles that do not call it
+// (32 trees of 64 over 32k: 800 us inline, 770 us so).
+__device__ __noinline__ uint32_t seen(int prefix, int rows, int node, const uint8_t *par, const uint32_t *turns) {
+    const int c = min(prefix, rows);
+    uint32_t see = node < 0 || c >= 32 ? 0xffffffffu : c <= 0 ? 0u : (1u << c) - 1u;
+    // A node's ancestors in stretches of neighbours: a chain is a single one.
+    const int last = min(rows, 32) - 1;
+    for (int a = node; a >= 0;) {
+        const int z = par ? stretch(turns, a) : 0;
+        const int lo = max(prefix + z, 0), hi = min(prefix + a, last);
+        if (lo <= hi) see |= (0xffffffffu >> (31 - hi)) & (0xffffffffu << lo);
+        if (prefix + z <= 0) break;                        // what is further up lies before these keys
+        a = par ? (int)par[z] - 1 : -1;
+    }
+    return see;
+}
+
 // x / d, in 32 bits where they suffice (a 64-bit division is a hundred instructions).
 __device__ __forceinline__ long long quotient(long long x, int d) {
     return x <= 0xffffffffll ? (long long)((uint32_t)x / (uint32_t)d) : x / d;
@@ -317,37 +336,6 @@ struct TrSmem {
         (2 * RINGS * STAGES + 16) * 8 + 48;
 };
 
-// Bounded wait.  A poll may sleep until the phase is over, or for 20 us: a warp that
-// spins takes issue slots from those with work (half of all that were issued, before).  The
-// clock is read only now and then: a read takes as long as a wait between two products does.
-__device__ __forceinline__ bool tr_try(uint64_t *bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
-        : "memory");
-    return done != 0;
-}
-__device__ __noinline__ bool tr_poll_on(uint64_t *bar, uint32_t parity, int *err) {
-    uint64_t t0 = 0;
-    for (uint32_t i = 1; i < kMaxPolls; ++i) {
-        if (tr_try(bar, parity)) return true;
-        if ((i & 63u) == 0) {
-            const uint64_t t = globaltimer();
-            if (t0 == 0) t0 = t;
-            else if (t - t0 > kMaxWaitNs) break;
-        }
-    }
-    raise_error(err, kErrTimeout);
-    return false;
-}
-__device__ __forceinline__ bool tr_poll(uint64_t *bar, uint32_t parity, int *err) {
-    return tr_try(bar, parity) || tr_poll_on(bar, parity, err);
-}
-
 // A number that a generic lambda takes as a compile-time constant.
 template <int N>
 struct Const {
@@ -357,9 +345,9 @@ struct Const {
 // A warp's wait, with one outcome for all lanes; once a wait has given up, the later ones
 // return at once.
 __device__ __forceinline__ bool tr_wait(uint64_t *bar, uint32_t parity, int *err, bool ok, int lane) {
-    if (__all_sync(0xffffffffu, ok && tr_try(bar, parity))) return true;
+    if (__all_sync(0xffffffffu, ok && mbar_try_sleep(bar, parity))) return true;
     int got = ok ? 1 : 0;
-    if (ok && lane == 0) got = tr_poll_on(bar, parity, err) ? 1 : 0;
+    if (ok && lane == 0) got = mbar_poll_on(bar, parity, err) ? 1 : 0;
     return __shfl_sync(0xffffffffu, got, 0) != 0;
 }
 
@@ -591,7 +579,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             uint32_t slot = 0, runs = 0, done0 = 0, done1 = 0;                 // done: uses of a P
 
             auto wait = [&](uint64_t *bar, uint32_t parity) {
-                if (ok) ok = tr_poll(bar, parity, p.err);
+                if (ok) ok = mbar_poll(bar, parity, p.err);
                 return ok;
             };
             auto arrived = [&](uint32_t slot) { return wait(&full_r[slot % NST], (slot / NST) & 1); };
@@ -755,21 +743,13 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     tmem_ld32u(ts + h * 64 + half * 32, v);
                     if (edge) {
                         const int first = h * 64 + half * 32;             // this thread's first key of the tile
-                        const int k0 = t.p0 + first, rows = t.rows - first;
-                        const int c = min(r.s.len - k0, rows);
-                        // (a row without a node may see anything: it is not used)
-                        uint32_t see = node < 0 || c >= 32 ? 0xffffffffu : c <= 0 ? 0u : (1u << c) - 1u;
-                        if (node >= 0 && k0 + rows > r.s.len) {
-                            // A node's ancestors in stretches of neighbours: a chain is a single one.
-                            const int last = min(rows, 32) - 1;
-                            for (int a = node; a >= 0;) {
-                                const int z = p.parent ? stretch(myturns, a) : 0;
-                                const int lo = max(r.s.len + z - k0, 0), hi = min(r.s.len + a - k0, last);
-                                if (lo <= hi) see |= (0xffffffffu >> (31 - hi)) & (0xffffffffu << lo);
-                                if (r.s.len + z <= k0) break;             // what is further up lies before these keys
-                                a = p.parent ? (int)mypar[z] - 1 : -1;
-                            }
-                        }
+                        // Before the nodes' slots only the tile's end counts.  (A row without a node may
+                        // see anything: it is not used.)
+                        const int prefix = r.s.len - (t.p0 + first), rows = t.rows - first;
+                        uint32_t see = node < 0 || rows >= 32 ? 0xffffffffu : rows <= 0 ? 0u : (1u << rows) - 1u;
+                        if (rows > prefix)
+                            see = seen(prefix, rows, node, p.parent ? par + s * kTrMaxNodes : nullptr,
+                                       turns + s * (kTrMaxNodes / 32));
                         if (!__all_sync(0xffffffffu, see == 0xffffffffu)) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
