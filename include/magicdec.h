@@ -81,7 +81,9 @@ MAGICDEC_API const char *magicdec_status_string(int status);
  * range-checking build (libmagicdec_debug.so, compiled with
  * MAGICDEC_DEBUG_CHECKS) value 4 means a kernel read a sequence length
  * outside [0, capacity] or a gather index outside [0, L_cap) other than the
- * -1 padding mark; that build still clamps or skips the value as documented
+ * -1 padding mark (in the calls on trees also a node count outside [0, n], a
+ * parent that is not before its node, or a path entry or n_acc that names no
+ * node); that build still clamps or skips the value as documented
  * for each call, so its outputs equal the release build's, which records
  * nothing for it.  The first error since the last read is kept.  Returns MAGICDEC_OK or
  * MAGICDEC_ERR_CUDA. */

@@ -5,6 +5,8 @@
 // [B, max_pages]: position s of sequence b is row s % page_size of page
 // table[b, s / page_size].  A dense cache [B, L_cap, H_kv, d] is the pool with
 // page_size = L_cap, max_pages = 1 and table[b, 0] = b.
+#include <climits>
+
 #include "common.cuh"
 
 namespace magicdec {
@@ -114,7 +116,7 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const AppendParams p) 
         // The depth, by stretches of nodes each of which follows the one before it (a bit where
         // one does not): a chain is a single one.
         for (int j = tid; j < (i / 32 + 1) * 32; j += NT) {
-            const int q = j <= i ? checked(ld_dep(p.parent + (long long)b * p.n + j), -1, j - 1, p.err) : -1;
+            const int q = j <= i ? checked(ld_dep(p.parent + (long long)b * p.n + j), INT_MIN, j - 1, p.err) : -1;
             par[j] = q;
             const unsigned m = __ballot_sync(0xffffffffu, j == 0 || q != j - 1);
             if (tid % 32 == 0) turns[j / 32] = m;
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(kCmThreads) tree_commit_kernel(const CommitPar
     pdl_wait();
     const int cap = p.page_size * p.max_pages;
     const int len = pg_clamp(checked(ld_dep(p.len + b), 0, cap, p.err), cap);
-    const int rows = min(max(ld_dep(p.n_acc + b), -1), p.n - 1) + 1;
+    const int rows = min(max(checked(ld_dep(p.n_acc + b), -1, p.n - 1, p.err), -1), p.n - 1) + 1;
     if (tid < 32) {
         const int32_t *table = p.table + (long long)b * p.max_pages;
         int found = 0;

@@ -9,6 +9,8 @@
 // A cluster of CTAs shares a row: each takes a slice, and the slices' best keys
 // (value, then lower index, packed in 64 bits) are exchanged through distributed
 // shared memory with one cluster barrier per level.
+#include <climits>
+
 #include "common.cuh"
 
 namespace magicdec {
@@ -75,7 +77,7 @@ __global__ void __launch_bounds__(kTaThreads, kTaPerSm) tree_accept_kernel(const
     int my_tok = -1, my_par = -1;
     if (tid < nn) {
         my_tok = ld_dep(p.tok + (long long)b * p.n + tid);
-        my_par = p.parent ? checked(ld_dep(p.parent + (long long)b * p.n + tid), -1, tid - 1, p.err) : tid - 1;
+        my_par = p.parent ? checked(ld_dep(p.parent + (long long)b * p.n + tid), INT_MIN, tid - 1, p.err) : tid - 1;
         if (my_par >= tid) my_par = -1;
     }
     int32_t *path = p.path + (long long)b * p.n, *out = p.out_tok + (long long)b * p.n;

@@ -723,7 +723,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 // node counts as none), and a bit where it is not the node just before.
                 named_bar_sync(9 + s, 256);
                 const int pi = wt < r.s.nodes
-                                   ? checked(ld_dep(p.parent + (long long)r.b * p.n + wt), -1, wt - 1, p.err) : -1;
+                                   ? checked(ld_dep(p.parent + (long long)r.b * p.n + wt), INT_MIN, wt - 1, p.err) : -1;
                 mypar[wt] = (uint8_t)(pi >= 0 && pi < wt ? pi + 1 : 0);
                 const uint32_t turn = __ballot_sync(0xffffffffu, wt == 0 || pi != wt - 1);
                 if (lane == 0) myturns[wt >> 5] = turn;

@@ -1,9 +1,10 @@
 """Time one entry point of libmagicdec on a named synthetic workload.
 
     python -m long_context_self_gb300.microbench <entry> [--workload NAME] [--batch B] [--gamma G]
-                                                 [--reps N] [--warmup W] [--budget K]
+                                                 [--reps N] [--warmup W] [--budget K] [--nodes N] [--page P]
 
-entry: verify | draft | topk | pq | pq_build | accept | accept_greedy | snapkv | gather | draft_cache
+entry: verify | draft | topk | pq | pq_build | accept | accept_greedy | snapkv | gather | draft_cache |
+       paged_append | tree_attn | tree_accept | tree_commit
 
 Inputs come from ``synth`` (seeded, resident on the GPU before timing); each
 call is launched `reps` times back to back after `warmup` untimed calls and
@@ -41,7 +42,8 @@ def _time(fn: Callable[[], object], reps: int, warmup: int) -> float:
 def main(argv=None) -> None:
     ap = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
     ap.add_argument("entry", choices=["verify", "draft", "topk", "pq", "pq_build", "accept", "accept_greedy", "snapkv",
-                                      "gather", "draft_cache"])
+                                      "gather", "draft_cache", "paged_append", "tree_attn", "tree_accept",
+                                      "tree_commit"])
     ap.add_argument("--pq-centroids", type=int, default=256)
     ap.add_argument("--pq-iters", type=int, default=2)
     ap.add_argument("--workload", default="llama8b_b128_l32k", choices=sorted(synth.WORKLOADS))
@@ -49,6 +51,8 @@ def main(argv=None) -> None:
     ap.add_argument("--gamma", type=int, default=0, help="override the workload's draft length (verify: gamma+1 rows)")
     ap.add_argument("--reps", type=int, default=5)
     ap.add_argument("--warmup", type=int, default=2)
+    ap.add_argument("--nodes", type=int, default=16, help="nodes of a drafted tree (paged_append, tree_*)")
+    ap.add_argument("--page", type=int, default=16, help="rows of a cache page (paged_append, tree_*)")
     ap.add_argument("--budget", type=int, default=0, help="draft / Top-K / SnapKV budget (default: the workload's)")
     args = ap.parse_args(argv)
 
@@ -141,6 +145,44 @@ def main(argv=None) -> None:
         fn = cycle
         nbytes = 2.0 * w.gamma * w.B * w.H_kv * w.d * 2 * 2 * 2
         info.update(cap=cap, gamma=w.gamma)
+    elif args.entry in ("paged_append", "tree_attn", "tree_commit"):
+        n, page = args.nodes, args.page
+        mp = -(-(w.L + n) // page)
+        table = torch.randperm(w.B * mp, device=dev).view(w.B, mp).to(torch.int32)
+        gen = synth.gen(dev, w.seed * 13 + 1)
+        kp = synth.randn_bf16((w.B * mp, page, w.H_kv, w.d), gen, dev)
+        vp = synth.randn_bf16((w.B * mp, page, w.H_kv, w.d), gen, dev)
+        parent = ((torch.arange(n, device=dev) + 1) // 2 - 1).to(torch.int32).expand(w.B, n).contiguous()
+        q = synth.randn_bf16((w.B, n, w.H_q, w.d), gen, dev)
+        row = w.H_kv * w.d * 2
+        if args.entry == "tree_attn":
+            out = torch.empty_like(q)
+            fn = lambda: mb.magicdec_tree_attn(q, kp, vp, table, sl, parent=parent, out=out)
+            nbytes = 2.0 * w.B * (w.L + n) * row + 2.0 * q.numel() * 2
+            info["tflop"] = 4.0 * w.B * n * w.L * w.H_q * w.d / 1e12
+        elif args.entry == "paged_append":
+            k, v = (synth.randn_bf16((w.B, n, w.H_kv, w.d), gen, dev) for _ in range(2))
+            inv = (500000.0 ** (-torch.arange(0, w.d, 2, dtype=torch.float64, device=dev) / w.d)).float()
+            out = torch.empty_like(q)
+            fn = lambda: mb.magicdec_paged_append(k, v, kp, vp, table, sl, inv, q=q, parent=parent, q_out=out)
+            nbytes = 4.0 * q.numel() + 4.0 * w.B * n * row
+        else:
+            acc = min(w.gamma, n - 1)
+            path = torch.full((w.B, n), -1, dtype=torch.int32, device=dev)
+            path[:, 0], path[:, 1:acc + 1] = 0, torch.arange(n - acc, n, dtype=torch.int32, device=dev)
+            n_acc = torch.full((w.B,), acc, dtype=torch.int32, device=dev)
+            fn = lambda: mb.magicdec_tree_commit(kp, vp, table, sl, path, n_acc)
+            nbytes = 4.0 * w.B * acc * row
+        info.update(nodes=n, page=page)
+    elif args.entry == "tree_accept":
+        n = args.nodes
+        target = torch.randn((w.B, n, w.V), device=dev, generator=synth.gen(dev, w.seed * 13 + 2))
+        parent = ((torch.arange(n, device=dev) + 1) // 2 - 1).to(torch.int32).expand(w.B, n).contiguous()
+        tok = target.argmax(-1).gather(1, parent.clamp(min=0).long()).to(torch.int32)    # the first child is accepted
+        fn = lambda: mb.magicdec_tree_accept(target, tok, parent=parent)
+        levels = int(fn()[0][0]) + 1
+        nbytes = 4.0 * w.B * levels * w.V
+        info.update(nodes=n, V=w.V, levels=levels)
     elif args.entry in ("accept", "accept_greedy"):
         greedy = args.entry == "accept_greedy"
         target, draft, tok, u_acc, u_res = synth.logits(w, dev)

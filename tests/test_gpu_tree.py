@@ -478,3 +478,101 @@ def test_step_captured_in_a_graph_and_on_side_streams():
     handle = _step(_step_inputs(93), stream=streams[0].cuda_stream)
     torch.cuda.synchronize()
     assert torch.equal(handle[0][1], ref[0][0][1])
+
+
+# ------------------------------------------------------------- far pages, debug build
+def test_pages_past_32_bit_offsets():
+    """A pool of more than 2^31 elements: the last pages are appended to, attended to and moved."""
+    H_q, H_kv, d, page, n = 8, 8, 128, 64, 5
+    n_pages = (1 << 31) // (page * H_kv * d) + 40
+    kp, vp = (torch.empty((n_pages, page, H_kv, d), dtype=BF16, device=DEV) for _ in range(2))
+    lens = [100, 30]
+    table = torch.tensor([[n_pages - 1, n_pages - 7], [n_pages - 3, n_pages - 2]], dtype=I32, device=DEV)
+    for pg in table.flatten().tolist():
+        kp[pg], vp[pg] = randn((page, H_kv, d), pg), randn((page, H_kv, d), pg + 1)
+    q, k, v = randn((2, n, H_q, d), 101), randn((2, n, H_kv, d), 102), randn((2, n, H_kv, d), 103)
+    mb.magicdec_paged_append(k, v, kp, vp, table, i32(lens), None)
+    small = torch.cat((kp[table.flatten().long()], torch.zeros_like(kp[:1]))), torch.cat(
+        (vp[table.flatten().long()], torch.zeros_like(vp[:1])))
+    near = torch.arange(4, dtype=I32, device=DEV).view(2, 2)
+    for b in range(2):
+        rows = rows_of(near, b, lens[b] + torch.arange(n), page).to(DEV)
+        assert torch.equal(small[0].view(-1, H_kv, d)[rows], k[b]) and torch.equal(small[1].view(-1, H_kv, d)[rows], v[b])
+    got = mb.magicdec_tree_attn(q, kp, vp, table, i32(lens))
+    within(got, *attn_ref(q, *small, near, lens, None, None))
+    mb.magicdec_tree_commit(kp, vp, table, i32(lens), i32([[0, 2, 4, -1, -1], [0, 3, -1, -1, -1]]), i32([2, 1]))
+    for b, (dst, src) in enumerate((((1, 2), (2, 4)), ((1,), (3,)))):
+        at = rows_of(table, b, lens[b] + torch.tensor(dst), page).to(DEV)
+        assert torch.equal(vp.view(-1, H_kv, d)[at], v[b, list(src)])
+
+
+@pytest.mark.parametrize("page,H_q,H_kv,d,n", [(2, 8, 2, 128, 40), (3, 16, 2, 64, 5), (1, 8, 1, 128, 20),
+                                               (4, 8, 2, 128, 9), (5, 8, 2, 64, 33), (128, 8, 2, 128, 33),
+                                               (136, 8, 2, 128, 33), (40, 4, 4, 128, 129)])
+def test_attention_more_page_sizes(page, H_q, H_kv, d, n):
+    lens = [515, 0, 129]
+    kp, vp, table = make_cache(lens, n, page, H_kv, d, 111, DEV, poison=True)
+    q, parent = randn((3, n, H_q, d), 112), make_tree(3, n, "random", 113)
+    got = mb.magicdec_tree_attn(q, kp, vp, table, i32(lens), parent=parent.to(DEV))
+    within(got, *attn_ref(q, kp, vp, table, lens, parent, None))
+    table[1, 0] = kp.shape[0]                       # outside the pool: zeros, and reported
+    mb.magicdec_tree_attn(q, kp, vp, table, i32(lens), parent=parent.to(DEV))
+    assert mb.magicdec_device_error() == 5
+
+
+DEBUG_CHILD = """
+import json, sys, torch
+sys.path.insert(0, {tests!r}); sys.path.insert(0, {root!r})
+from long_context_self_gb300 import binding as mb
+from tree_util import make_cache, make_tree
+D = torch.device("cuda:0")
+i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=D)
+B, n, H, d, page = 2, 6, 2, 64, 16
+kp, vp, table = make_cache([60, 60], 4, page, H, d, 1, D)             # 64 slots
+q = torch.ones((B, n, 4, d), dtype=torch.bfloat16, device=D)
+k = torch.ones((B, n, H, d), dtype=torch.bfloat16, device=D)
+good = make_tree(B, n, "forest", 2).to(D)
+bad = good.clone(); bad[1, 3] = 5
+target = torch.randn((B, n, 50), device=D)
+tok = torch.zeros((B, n), dtype=torch.int32, device=D)
+path = i32([[0, 2, -1, -1, -1, -1], [0, -1, -1, -1, -1, -1]])
+err = mb.magicdec_device_error
+def tell(f):
+    f(); return err()
+res = dict(lib=mb.lib()._name.rsplit("/", 1)[-1])
+res["in"] = [tell(lambda: mb.magicdec_paged_append(k, k, kp, vp, table, i32([10, 20]), parent=good, n_new=i32([6, 0]))),
+             tell(lambda: mb.magicdec_tree_attn(q, kp, vp, table, i32([10, 20]), parent=good, n_nodes=i32([6, 0]))),
+             tell(lambda: mb.magicdec_tree_accept(target, tok, parent=good, n_nodes=i32([6, 0]))),
+             tell(lambda: mb.magicdec_tree_commit(kp, vp, table, i32([10, 20]), path, i32([1, -1])))]
+res["out"] = [tell(lambda: mb.magicdec_paged_append(k, k, kp, vp, table, i32([10, 20]), parent=bad)),
+              tell(lambda: mb.magicdec_paged_append(k, k, kp, vp, table, i32([10, -1]), n_new=i32([1, 7]))),
+              tell(lambda: mb.magicdec_tree_attn(q, kp, vp, table, i32([10, 65]))),
+              tell(lambda: mb.magicdec_tree_attn(q, kp, vp, table, i32([10, 20]), n_nodes=i32([7, 1]))),
+              tell(lambda: mb.magicdec_tree_attn(q, kp, vp, table, i32([10, 20]), parent=bad)),
+              tell(lambda: mb.magicdec_tree_accept(target, tok, parent=bad)),
+              tell(lambda: mb.magicdec_tree_accept(target, tok, n_nodes=i32([-1, 6]))),
+              tell(lambda: mb.magicdec_tree_commit(kp, vp, table, i32([10, 20]), path, i32([6, 0]))),
+              tell(lambda: mb.magicdec_tree_commit(kp, vp, table, i32([10, 20]), path - 9, i32([1, 0])))]
+print(json.dumps(res))
+"""
+
+
+def test_range_checking_build_records_and_release_build_does_not():
+    import json
+    import os
+    import subprocess
+    import sys
+    from long_context_self_gb300 import build
+    build.build(debug=True)
+    tests = os.path.dirname(os.path.abspath(__file__))
+    code = DEBUG_CHILD.format(tests=tests, root=os.path.dirname(tests))
+    for library, name, out in (("debug", "libmagicdec_debug.so", 4), (None, "libmagicdec.so", 0)):
+        env = {k: v for k, v in os.environ.items() if k != "MAGICDEC_LIBRARY"}
+        if library:
+            env["MAGICDEC_LIBRARY"] = library
+        r = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, timeout=600)
+        assert r.returncode == 0, r.stderr[-3000:]
+        res = json.loads(r.stdout.strip().splitlines()[-1])
+        assert res["lib"] == name
+        assert res["in"] == [0] * 4, res
+        assert res["out"] == [out] * 9, res
