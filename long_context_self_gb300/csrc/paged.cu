@@ -98,12 +98,14 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const AppendParams p) 
     const int l = tid % LR, pairs = p.rot / 16;                     // pairs: lanes of a row that rotate halves
     const bool halves = !INTER && l < pairs;
     const int v0 = halves ? l : 2 * l, v1 = halves ? l + pairs : 2 * l + 1;   // the lane's vectors
+    // Row r of the token: a base, from which r is counted, for each of the three kinds.
+    const int nk = nq + p.H_kv;
+    const uint16_t *qb = p.q + tok * p.q_stride, *kb = p.k + tok * p.k_stride - nq * p.d,
+                   *vb = p.v + tok * p.v_stride - nk * p.d;
     auto load = [&](int r, uint4 (&x)[2]) {
-        const uint16_t *src = r < nq ? p.q + tok * p.q_stride + r * p.d
-                              : r < nq + p.H_kv ? p.k + tok * p.k_stride + (r - nq) * p.d
-                                                : p.v + tok * p.v_stride + (r - nq - p.H_kv) * p.d;
-        x[0] = ld_once_u4(reinterpret_cast<const uint4 *>(src) + v0);
-        x[1] = ld_once_u4(reinterpret_cast<const uint4 *>(src) + v1);
+        const uint4 *src = reinterpret_cast<const uint4 *>((r < nq ? qb : r < nk ? kb : vb) + r * p.d);
+        x[0] = ld_once_u4(src + v0);
+        x[1] = ld_once_u4(src + v1);
     };
     uint4 x[AHEAD][2];
 #pragma unroll
@@ -149,6 +151,8 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const AppendParams p) 
     if (turned)
 #pragma unroll
         for (int k = 0; k < 8; ++k) a[k] = cs[l * 8 + k];
+    uint16_t *qo = p.q_out + tok * p.H_q * p.d, *ko = p.kp + dst * p.H_kv * p.d - nq * p.d,
+             *vo = p.vp + dst * p.H_kv * p.d - nk * p.d;
     for (int r0 = tid / LR; r0 < R; r0 += AHEAD * ROWS) {
         if (r0 >= AHEAD * ROWS) {
 #pragma unroll
@@ -160,7 +164,7 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const AppendParams p) 
             const int r = r0 + k * ROWS;
             if (r >= R) break;
             uint4 y = x[k][0], z = x[k][1];
-            if (turned && r < nq + p.H_kv) {
+            if (turned && r < nk) {
                 if (INTER) {
                     y = make_uint4(turn_pair(y.x, a[0]), turn_pair(y.y, a[1]), turn_pair(y.z, a[2]), turn_pair(y.w, a[3]));
                     z = make_uint4(turn_pair(z.x, a[4]), turn_pair(z.y, a[5]), turn_pair(z.z, a[6]), turn_pair(z.w, a[7]));
@@ -171,16 +175,10 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const AppendParams p) 
                     turn_halves(y.w, z.w, a[6], a[7]);
                 }
             }
-            uint16_t *out;
-            if (r < nq) {
-                out = p.q_out + (tok * p.H_q + r) * p.d;
-            } else {
-                if (dst < 0) continue;
-                const int h = r - nq;
-                out = h < p.H_kv ? p.kp + (dst * p.H_kv + h) * p.d : p.vp + (dst * p.H_kv + h - p.H_kv) * p.d;
-            }
-            reinterpret_cast<uint4 *>(out)[v0] = y;
-            reinterpret_cast<uint4 *>(out)[v1] = z;
+            if (r >= nq && dst < 0) continue;
+            uint4 *out = reinterpret_cast<uint4 *>((r < nq ? qo : r < nk ? ko : vo) + r * p.d);
+            out[v0] = y;
+            out[v1] = z;
         }
     }
 }
