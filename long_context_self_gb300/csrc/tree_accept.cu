@@ -9,6 +9,12 @@
 // A cluster of CTAs shares a row: each takes a slice, and the slices' best keys
 // (value, then lower index, packed in 64 bits) are exchanged through distributed
 // shared memory with one cluster barrier per level.
+//
+// Bound: HBM while all sequences are at it, a chain of latencies (a row's loads, two
+// reductions, the barrier: about 2 us) when few are.  V = 128,256, 128 sequences that accept 0
+// to 4 nodes: 46 us, of 29 us at the measured copy rate; one sequence, V = 152,064, 4 levels:
+// 8.7 us.  Copies through shared memory in place of the loads, 96 KB a CTA under way, measured
+// slower (55 us): what a CTA does for a piece of 16 KB costs more than the loads' latency.
 #include <climits>
 
 #include "common.cuh"
@@ -19,6 +25,7 @@ constexpr int kTaThreads = 512;
 constexpr int kTaMaxCluster = 16;
 constexpr int kTaMaxNodes = 256;
 constexpr int kTaPerSm = 3;             // CTAs an SM holds
+constexpr int kTaAsk = 1024;            // 16-byte vectors of a prefetch
 constexpr int kTaAhead = 4;             // loads of a thread under way
 static_assert(kTaMaxNodes <= kTaThreads, "one thread holds a node's token and parent");
 
@@ -89,6 +96,13 @@ __global__ void __launch_bounds__(kTaThreads, kTaPerSm) tree_accept_kernel(const
         const int pre = min(p.V, (4 - mis) & 3), nv = (p.V - pre) / 4, post = pre + nv * 4;
         const int v0 = (int)((long long)nv * rank / C), v1 = (int)((long long)nv * (rank + 1) / C);
         const float4 *vec = reinterpret_cast<const float4 *>(row + pre);
+        // The slice is on its way to L2 as a whole while the threads load it bit by bit, as long
+        // as the rows under way are few enough: with clusters of 4 and more (V = 128,256: 16, 50
+        // and 100 sequences 16.9, 24.3 and 35.5 us without, 15.4, 21.0 and 32.7 us with it); with
+        // 128 sequences it costs (45.7 and 50.6 us).
+        if (C >= 4)
+            for (int at = v0 + tid * kTaAsk; at < v1; at += kTaThreads * kTaAsk)
+                bulk_prefetch_l2(vec + at, (uint32_t)min(kTaAsk, v1 - at) * 16);
         // The largest of a thread's vectors, the first of equal ones.
         float best = -INFINITY;
         float4 at = make_float4(best, best, best, best);
