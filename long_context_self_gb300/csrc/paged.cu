@@ -82,7 +82,7 @@ __device__ __forceinline__ void turn_halves(uint32_t &x, uint32_t &y, float2 c0,
 template <int NT, int LR, bool INTER>
 __global__ void __launch_bounds__(NT) paged_append_kernel(const AppendParams p) {
     constexpr int ROWS = NT / LR;               // rows of a pass
-    constexpr int AHEAD = 2;                    // passes loaded together
+    constexpr int AHEAD = 3;                    // passes loaded together
     __shared__ float2 cs[LR * 8];               // room for d / 2 angles
     __shared__ int par[kApMaxTree];
     __shared__ unsigned turns[kApMaxTree / 32];

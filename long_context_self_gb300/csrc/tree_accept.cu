@@ -12,7 +12,7 @@
 //
 // Bound: HBM while all sequences are at it, a chain of latencies (a row's loads, two
 // reductions, the barrier: about 2 us) when few are.  V = 128,256, 128 sequences that accept 0
-// to 4 nodes: 39 us, of 29 us at the measured copy rate; one sequence, V = 152,064, 4 levels:
+// to 4 nodes: 44 us, of 29 us at the measured copy rate; one sequence, V = 152,064, 4 levels:
 // 8.7 us.  Copies through shared memory in place of the loads, 96 KB a CTA under way, measured
 // slower (55 us, where the loads alone took 46): what a CTA does for a piece of 16 KB costs more than the loads' latency.
 #include <climits>
@@ -24,7 +24,7 @@ namespace magicdec {
 constexpr int kTaThreads = 512;
 constexpr int kTaMaxCluster = 16;
 constexpr int kTaMaxNodes = 256;
-constexpr int kTaPerSm = 3;             // CTAs an SM gets (it holds 2: sequences that end early make room)
+constexpr int kTaPerSm = 2;             // CTAs an SM holds
 constexpr int kTaAsk = 2048;            // 16-byte vectors of a prefetch
 constexpr int kTaAhead = 4;             // loads of a thread under way
 static_assert(kTaMaxNodes <= kTaThreads, "one thread holds a node's token and parent");
@@ -71,7 +71,7 @@ __device__ __forceinline__ uint64_t warp_best(uint64_t key) {
     return ((uint64_t)top << 32) | __reduce_max_sync(0xffffffffu, hi == top ? (uint32_t)key : 0u);
 }
 
-__global__ void __launch_bounds__(kTaThreads, 2) tree_accept_kernel(const TreeAcceptParams p) {
+__global__ void __launch_bounds__(kTaThreads, kTaPerSm) tree_accept_kernel(const TreeAcceptParams p) {
     __shared__ uint64_t slot[2][kTaMaxCluster];
     __shared__ uint64_t wbest[kTaThreads / 32];
     __shared__ int wnext[kTaMaxNodes / 32];
@@ -96,11 +96,11 @@ __global__ void __launch_bounds__(kTaThreads, 2) tree_accept_kernel(const TreeAc
         const int pre = min(p.V, (4 - mis) & 3), nv = (p.V - pre) / 4, post = pre + nv * 4;
         const int v0 = (int)((long long)nv * rank / C), v1 = (int)((long long)nv * (rank + 1) / C);
         const float4 *vec = reinterpret_cast<const float4 *>(row + pre);
-        // The slice is on its way to L2 as a whole while the threads load it bit by bit: few
-        // sequences get far down, and what they get of the memory hangs on how much of their rows
-        // is under way (V = 128,256: 16, 50, 100 and 128 sequences 16.9, 24.3, 35.5 and 45.7 us
-        // without, 15.8, 22.5, 33.2 and 38.9 us with it; 400, a CTA each, gain nothing).
-        if (C >= 2)
+        // The slice is on its way to L2 as a whole while the threads load it bit by bit, as long
+        // as there are few sequences, whose rate hangs on how much of a row is under way
+        // (V = 128,256, logits from HBM: 16 and 50 sequences 18.6 and 28.8 us without, 16.2 and
+        // 26.9 us with it; 128 sequences 44.3 and 46.6 us).
+        if (C >= 4)
             for (int at = v0 + tid * kTaAsk; at < v1; at += kTaThreads * kTaAsk)
                 bulk_prefetch_l2(vec + at, (uint32_t)min(kTaAsk, v1 - at) * 16);
         // The largest of a thread's vectors, the first of equal ones.
@@ -184,8 +184,8 @@ magicdec_status launch_tree_accept(int B, int n, int V, const float *target, con
     p.err = magicdec_host::device_error_word();
     p.n = n;
     p.V = V;
-    // As many CTAs a row as there are places for, kTaPerSm on an SM (128 sequences, 2, 3 and 4 on an
-    // SM: 40.1, 38.9 and 42.2 us; 100 sequences: 35.9, 33.2 and 33.4 us; 75: 25.8, 25.8, 31.4 us).
+    // As many CTAs a row as there are places for (with more, 50 sequences take 26.9 us instead of
+    // 24.5, 128 take 48.9 instead of 44.3).
     int C = kTaMaxCluster;
     while (C > 1 && (long long)B * C > (long long)kTaPerSm * magicdec_host::sm_count()) C /= 2;
     if (!magicdec_host::allow_wide_cluster_once<tree_accept_kernel>()) return MAGICDEC_ERR_CUDA;
