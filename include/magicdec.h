@@ -404,9 +404,10 @@ MAGICDEC_API magicdec_status magicdec_spec_accept(int B, int gamma, int V, const
  * sequence b is row s % page_size of page block_table[b, s / page_size].  Any
  * page_size >= 1.  A dense cache [B, L_cap, H_kv, d] is the pool with n_pages =
  * B, page_size = L_cap, max_pages = 1 and block_table[b, 0] = b.  The capacity of
- * a sequence is page_size * max_pages slots (at most INT_MAX).  Only entries of
- * the slots that a call reads or writes are looked at; one outside [0, n_pages)
- * sets the device error word to 5, and nothing outside the pool is touched.
+ * a sequence is page_size * max_pages slots (at most INT_MAX - 255; B at most 4096,
+ * H_q at most 65535; MAGICDEC_ERR_SHAPE beyond).  Only entries of the slots that a
+ * call reads or writes are looked at; one outside [0, n_pages) sets the device error
+ * word to 5, and nothing outside the pool is touched.
  *
  * A tree: len[b] positions of sequence b are committed.  Its node i (a drafted
  * token; node 0 is the last emitted one, whose K and V are not in the cache yet)

@@ -154,10 +154,11 @@ static bool shape_ok(const magicdec_kv_shape &s) {
            s.L_cap > 0 && s.B <= 4096;
 }
 
+// The kernels count slots in 32 bits, up to a tile behind the last one, and a token's elements.
 static bool paged_ok(const magicdec_paged_shape &s) {
-    return s.B > 0 && s.B <= 4096 && s.H_q > 0 && s.H_kv > 0 && s.H_kv <= 65535 && s.H_q % s.H_kv == 0 &&
+    return s.B > 0 && s.B <= 4096 && s.H_q > 0 && s.H_q <= 65535 && s.H_kv > 0 && s.H_q % s.H_kv == 0 &&
            (s.d == 64 || s.d == 128) && s.page_size > 0 && s.n_pages > 0 && s.max_pages > 0 &&
-           (long long)s.page_size * s.max_pages <= INT_MAX;
+           (long long)s.page_size * s.max_pages <= INT_MAX - 255;
 }
 
 constexpr int kTreeMaxNodes = 256;

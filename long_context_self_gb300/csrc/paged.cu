@@ -316,9 +316,11 @@ magicdec_status launch_tree_commit(const magicdec_paged_shape &s, int n, int lay
     p.n_pages = s.n_pages;
     p.max_pages = s.max_pages;
     p.layers = layers;
-    // A CTA takes several layers of a sequence, as long as there are some eight CTAs an SM.
+    // A CTA takes several layers of a sequence, as long as there are some eight CTAs an SM, and no
+    // more columns than it counts in 32 bits.
     const int want = (8 * magicdec_host::sm_count() + s.B - 1) / s.B;
-    const int groups = layers < want ? layers : want;
+    const int most = INT_MAX / 2 / (2 * p.row_vecs), least = (layers + most - 1) / most;
+    const int groups = layers < want ? layers : (want < least ? least : want);
     return magicdec_host::launch_pdl(tree_commit_kernel, dim3((unsigned)s.B, (unsigned)groups), dim3(kCmThreads), 0, st,
                                      p);
 }

@@ -25,7 +25,8 @@ def shape(**kw):
 
 
 BAD_SHAPES = [dict(B=0), dict(B=4097), dict(H_q=0), dict(H_kv=0), dict(H_q=9), dict(d=96), dict(page_size=0),
-              dict(n_pages=0), dict(max_pages=0), dict(page_size=1 << 16, max_pages=1 << 15), dict(H_q=65536, H_kv=65536)]
+              dict(n_pages=0), dict(max_pages=0), dict(page_size=1 << 16, max_pages=1 << 15), dict(H_q=65536, H_kv=65536),
+              dict(page_size=(1 << 31) - 255, max_pages=1), dict(H_q=65536)]
 
 
 def append(lib, s=None, n=4, q=FAKE, qs=1024, k=FAKE, ks=256, v=FAKE, vs=256, length=FAKE, n_new=NULL, parent=NULL,
