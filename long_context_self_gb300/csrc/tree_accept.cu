@@ -12,7 +12,7 @@
 //
 // Bound: HBM while all sequences are at it, a chain of latencies (a row's loads, two
 // reductions, the barrier: about 2 us) when few are.  V = 128,256, 128 sequences that accept 0
-// to 4 nodes: 44 us, of 29 us at the measured copy rate; one sequence, V = 152,064, 4 levels:
+// to 4 nodes: 41.5 us, of 29 us at the measured copy rate; one sequence, V = 152,064, 4 levels:
 // 8.7 us.  Copies through shared memory in place of the loads, 96 KB a CTA under way, measured
 // slower (55 us, where the loads alone took 46): what a CTA does for a piece of 16 KB costs more than the loads' latency.
 #include <climits>
@@ -99,8 +99,11 @@ __global__ void __launch_bounds__(kTaThreads, kTaPerSm) tree_accept_kernel(const
         // The slice is on its way to L2 as a whole while the threads load it bit by bit, as long
         // as there are few sequences, whose rate hangs on how much of a row is under way
         // (V = 128,256, logits from HBM: 16 and 50 sequences 18.6 and 28.8 us without, 16.2 and
-        // 26.9 us with it; 128 sequences 44.3 and 46.6 us).
-        if (C >= 4)
+        // 26.9 us with it; 128 sequences 44.3 and 46.6 us), or deep in the trees, where most
+        // sequences have ended (100, 128 and 200 sequences that accept 0 to 4 nodes: 40.9, 44.3
+        // and 71.1 us without, 38.4, 41.5 and 69.5 us with it from level 3 on; 37.7, 42.1 and
+        // 71.1 us from level 2 on).
+        if (C >= 4 || level >= 3)
             for (int at = v0 + tid * kTaAsk; at < v1; at += kTaThreads * kTaAsk)
                 bulk_prefetch_l2(vec + at, (uint32_t)min(kTaAsk, v1 - at) * 16);
         // The largest of a thread's vectors, the first of equal ones.
