@@ -60,8 +60,8 @@ struct TreeAttnParams {
     int *err;
     int B, H_q, H_kv, G, n, page_size, n_pages, max_pages;
     int NB;                // nodes per row tile
-    int ppt;               // pages per key tile (pages of at most 128 rows), else 0
-    int tpp;               // key tiles per page (larger pages)
+    int span;              // keys of a tile, where tiles run on over the pages, else 0
+    int tpp;               // key tiles per page, where each page begins with one
     int grid;
     int br;                // rows of a box
     int by4;               // pages of fewer than 4 rows: 4 rows of any pages at a time
@@ -207,21 +207,21 @@ struct Tile {
 struct TileWalk {
     int tj, pg, part;       // the tile; with pages of several tiles, its page and its place there
     __device__ __forceinline__ TileWalk(const TreeAttnParams &p, int tj_) : tj(tj_), pg(0), part(0) {
-        if (!p.ppt) {
+        if (!p.span) {
             pg = tj / p.tpp;
             part = tj - pg * p.tpp;
         }
     }
     __device__ __forceinline__ void step(const TreeAttnParams &p, int n) {
         tj += n;
-        if (!p.ppt)
+        if (!p.span)
             for (part += n; part >= p.tpp; part -= p.tpp) ++pg;
     }
     __device__ __forceinline__ Tile at(const TreeAttnParams &p, int total) const {
         Tile t;
         int span;
-        if (p.ppt) {
-            span = p.ppt * p.page_size;
+        if (p.span) {
+            span = p.span;
             t.p0 = tj * span;
         } else {
             t.p0 = pg * p.page_size + part * kTrKeys;
@@ -232,10 +232,7 @@ struct TileWalk {
     }
 };
 __device__ __forceinline__ int tiles_of(const TreeAttnParams &p, int total) {
-    if (p.ppt) {
-        const int span = p.ppt * p.page_size;
-        return (total + span - 1) / span;
-    }
+    if (p.span) return (total + p.span - 1) / p.span;
     const int full = total / p.page_size;
     return full * p.tpp + (total - full * p.page_size + kTrKeys - 1) / kTrKeys;
 }
@@ -490,7 +487,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             const int32_t *table = p.table + (long long)r.b * p.max_pages;
             // K and V in turn, as the products need them.
             const int j0 = RT == 1 ? pw : 0, mine = (r.cnt - j0 + STEP - 1) / STEP;
-            int id = 0;
+            int id = 0, pr = 0;                          // of the lane's box: its page, and its first row there
             TileWalk tile(p, r.t0 + j0);
             for (int i = 0; i < 2 * mine; ++i, ++slot) {
                 if (i && (i & 1) == 0) tile.step(p, STEP);
@@ -499,11 +496,6 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 const Tile t = tile.at(p, r.s.total);
                 const uint32_t st = slot % NST, ph = (slot / NST) & 1;
                 uint8_t *dst = buf + st * OPER;
-                const int pg0 = t.p0 / p.page_size;
-                // Boxes of br rows: a page each, or parts of one page.  The lane's page number is
-                // on its way while the warp waits for the ring.
-                const int boxes = (t.rows + p.br - 1) / p.br, r0 = t.p0 - pg0 * p.page_size;
-                const bool pages = p.br == p.page_size;
                 if (p.by4) {
                     // A lane's 4 rows; one behind the tile or outside the pool is past the pool's last.
                     int rows[4];
@@ -528,19 +520,27 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                                         &full_r[st], pol);
                     continue;
                 }
-                if (RT == 2 || !is_v || boxes > 32) id = lane < boxes ? ld_dep(table + pg0 + (pages ? lane : 0)) : 0;
+                // Boxes of br rows, each inside a page.  The lane's page number is on its way while
+                // the warp waits for the ring.
+                const int boxes = (t.rows + p.br - 1) / p.br;
+                auto locate = [&](int g) {
+                    const int at = t.p0 + g * p.br, pg = at / p.page_size;
+                    id = ld_dep(table + pg);
+                    pr = at - pg * p.page_size;
+                };
+                if ((RT == 2 || !is_v || boxes > 32) && lane < boxes) locate(lane);
                 ok = tr_wait(&empty_r[st], ph ^ 1, p.err, ok, lane);
                 if (!ok) break;
                 const CUtensorMap *tm = is_v ? &tmv : &tmk;
                 if (lane == 0) mbar_arrive_expect_tx(&full_r[st], (uint32_t)(boxes * p.br * HALVES * 128));
                 __syncwarp();
                 for (int g = lane; g < boxes; g += 32) {
-                    if (g >= 32) id = ld_dep(table + pg0 + (pages ? g : 0));
+                    if (g >= 32) locate(g);
                     if (id < 0 || id >= p.n_pages) {       // such a page is filled with zeros
                         raise_error(p.err, kErrPage);
                         id = p.n_pages;
                     }
-                    const int at = g * p.br, pr = pages ? 0 : r0 + at;      // row in the tile, in the page
+                    const int at = g * p.br;                           // row in the tile
                     if (p.by8)
                         tma_load_5d(dst + at / 8 * (HALVES * 1024), tm, 0, 0, r.h * HALVES, pr / 8, id, &full_r[st], pol);
                     else
@@ -1007,7 +1007,7 @@ size_t tree_attn_workspace_bytes(const magicdec_paged_shape &s, int n) {
 // The list of work is counted in 32 bits within a sequence and within a CTA's run.
 static bool tr_counts(const TreeAttnParams &p) {
     const long long cap = (long long)p.page_size * p.max_pages;
-    const long long tiles = p.ppt ? (cap + p.ppt * p.page_size - 1) / (p.ppt * p.page_size) : (long long)p.max_pages * p.tpp;
+    const long long tiles = p.span ? (cap + p.span - 1) / p.span : (long long)p.max_pages * p.tpp;
     const long long work = tiles * p.H_kv * ((p.n + p.NB - 1) / p.NB);
     return work <= INT_MAX && work * p.B / p.grid < INT_MAX;
 }
@@ -1050,8 +1050,23 @@ magicdec_status launch_tree_attn(const magicdec_paged_shape &s, int n, const uin
     p.n_pages = s.n_pages;
     p.max_pages = s.max_pages;
     p.NB = 128 / p.G;
-    p.ppt = s.page_size <= kTrKeys ? kTrKeys / s.page_size : 0;
+    // Tiles and boxes.  A tile is of whole pages, or a part of one page, copied by boxes of a page
+    // or of 64 rows (boxes of 128 rows, 16 trees of 8 over 30k at d = 128: 327 us, of 64: 299).
+    // Where that leaves too much of the tiles empty, and pages are of a multiple of 8 rows, tiles
+    // run on over the pages, in boxes of the largest power of 2 rows that divides a page; how
+    // much is too much hangs on the bytes of such a box, as the copy engine takes 70 cycles for
+    // even the smallest (24 ragged sequences of up to 36k, 13 nodes, d = 64: boxes of 8 rows 242
+    // us whatever the page, of 16 rows 198, of 64 rows 172; pages of 48 rows in twos 228).
+    p.by8 = s.page_size % 8 == 0;
     p.tpp = (s.page_size + kTrKeys - 1) / kTrKeys;
+    p.span = s.page_size <= kTrKeys ? kTrKeys / s.page_size * s.page_size : 0;
+    p.br = s.page_size < kTrKeys / 2 ? s.page_size : kTrKeys / 2;
+    const int even = s.page_size & -s.page_size, bytes = even * s.d * 2;
+    const long long used = p.span ? p.span : s.page_size, room = p.span ? kTrKeys : (long long)p.tpp * kTrKeys;
+    if (p.by8 && used * 16 < room * (bytes >= 4096 ? 15 : bytes >= 2048 ? 14 : 12)) {
+        p.span = kTrKeys;
+        p.br = even < p.br ? even : p.br;
+    }
     p.scale_log2 = kLog2e / sqrtf((float)s.d);
     p.grid = magicdec_host::sm_count();
     if (!tr_counts(p)) return MAGICDEC_ERR_UNSUPPORTED;
@@ -1074,21 +1089,19 @@ magicdec_status launch_tree_attn(const magicdec_paged_shape &s, int n, const uin
     // 4.2, 2.2 and 1.8 ms with a box a page, 1.6 ms so; of 4 rows: 1.15 ms with boxes).
     CUtensorMap tmq, tmk, tmv;
     const int D = s.d, HV = D / 64;
-    p.by8 = s.page_size % 8 == 0;
     p.by4 = s.page_size < 4 && (long long)s.n_pages * s.page_size < INT_MAX;
     p.sbo = p.by8 ? HV * 1024 : 1024;
     p.hoff = p.by8 ? 1024 : kTrBox;
     const uint64_t row = (uint64_t)s.H_kv * D * 2;
-    p.br = s.page_size < kTrKeys ? s.page_size : kTrKeys;
-    const uint32_t span = (uint32_t)p.br;
+    const uint32_t br = (uint32_t)p.br;
     const uint64_t kd4[4] = {(uint64_t)D, (uint64_t)s.H_kv, (uint64_t)s.page_size, (uint64_t)s.n_pages};
     const uint64_t ks4[3] = {(uint64_t)D * 2, row, s.page_size * row};
-    const uint32_t kb4[4] = {64, 1, span, 1};
+    const uint32_t kb4[4] = {64, 1, br, 1};
     const uint64_t kd2[2] = {(uint64_t)s.H_kv * D, (uint64_t)s.n_pages * s.page_size};
     const uint32_t kb2[2] = {64, 1};
     const uint64_t kd5[5] = {64, 8, (uint64_t)s.H_kv * HV, (uint64_t)s.page_size / 8, (uint64_t)s.n_pages};
     const uint64_t ks5[4] = {row, 128, 8 * row, s.page_size * row};
-    const uint32_t kb5[5] = {64, 8, (uint32_t)HV, span / 8, 1};
+    const uint32_t kb5[5] = {64, 8, (uint32_t)HV, br / 8, 1};
     const uint64_t qd[4] = {(uint64_t)D, (uint64_t)s.H_q, (uint64_t)n, (uint64_t)s.B};
     const uint64_t qs[3] = {(uint64_t)D * 2, (uint64_t)s.H_q * D * 2, (uint64_t)n * s.H_q * D * 2};
     const uint32_t qbx[4] = {64, (uint32_t)p.G, (uint32_t)p.NB, 1};

@@ -520,6 +520,18 @@ def test_attention_more_page_sizes(page, H_q, H_kv, d, n):
     assert mb.magicdec_device_error() == 5
 
 
+@pytest.mark.parametrize("page", [8, 24, 56, 72, 80, 96, 104, 125, 129, 192, 250, 264, 1000])
+@pytest.mark.parametrize("H_q,H_kv,d,n", [(6, 2, 64, 7), (8, 2, 128, 40)])
+def test_attention_tiles_over_pages(page, H_q, H_kv, d, n):
+    """Tiles that run on over the pages' ends, and those that begin anew with each page."""
+    lens, counts = [1207, 1, 2 * page, 129], [n, n, n, 1]
+    kp, vp, table = make_cache(lens, n, page, H_kv, d, 121, DEV, poison=True, counts=counts)
+    q, parent = randn((4, n, H_q, d), 122), make_tree(4, n, "random", 123)
+    got = mb.magicdec_tree_attn(q, kp, vp, table, i32(lens), parent=parent.to(DEV), n_nodes=i32(counts))
+    within(got, *attn_ref(q, kp, vp, table, lens, parent, counts))
+    assert mb.magicdec_device_error() == 0
+
+
 DEBUG_CHILD = """
 import json, sys, torch
 sys.path.insert(0, {tests!r}); sys.path.insert(0, {root!r})
