@@ -1082,9 +1082,9 @@ magicdec_status launch_tree_attn(const magicdec_paged_shape &s, int n, const uin
 
     // Queries as (d, H_q, n, B), one box = NB nodes of a KV head's group.  The pool with
     // pages of a multiple of 8 rows as (64 channels, 8 rows, halves of all heads, groups of 8
-    // rows, pages): one box is a page (or 128 rows of it) of one KV head, its channels read
+    // rows, pages): one box is a page (or a part of it) of one KV head, its channels read
     // together and its rows laid out for the tensor cores.  Other pages as (d, H_kv,
-    // page_size, n_pages), boxes of 64 channels x a page (or 128 rows); pages of 1 to 3 rows as
+    // page_size, n_pages), boxes of 64 channels x a page (or 64 rows); pages of 1 to 3 rows as
     // one list of rows, 4 of them a copy (32 sequences of 32k, 8 nodes, pages of 1, 2 and 3 rows:
     // 4.2, 2.2 and 1.8 ms with a box a page, 1.6 ms so; of 4 rows: 1.15 ms with boxes).
     CUtensorMap tmq, tmk, tmv;
