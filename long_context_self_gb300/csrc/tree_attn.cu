@@ -930,8 +930,11 @@ __global__ void __launch_bounds__(kTrThreads, 1)
 // sequence then sets the rows of the nodes that it does not have to zero.
 constexpr int kTjThreads = 256;
 
-template <int RT, int PL>
+// A thread has W * 4 channels of a row: 8 for PL = 1, so that its stores are 16 bytes (4 channels,
+// 8 and 16: 32 trees of 64 over 8k 221, 216 and 215 us, chain of 200 over 8k 217, 211 and 214).
+template <int RT, int PL, int W>
 __global__ void __launch_bounds__(kTjThreads) tree_attn_join_kernel(const TreeAttnParams p, int D, int per) {
+    static_assert(PL == 1 || W == 1, "partials are shared out for 4 channels a thread");
     __shared__ float4 xo[PL > 1 ? kTjThreads : 1];
     __shared__ float2 xs[PL > 1 ? kTjThreads : 1];
     pdl_trigger();
@@ -952,42 +955,57 @@ __global__ void __launch_bounds__(kTjThreads) tree_attn_join_kernel(const TreeAt
     const int it = (blockIdx.x % per) * ITEMS + tid % ITEMS, pl = tid / ITEMS;
     const int base = s.rb * RT * p.NB;                 // first node of the entry
     const int rows = min(s.nodes - base, RT * p.NB) * p.G;
-    const bool real = it < rows * (D / 4);
+    const bool real = it < rows * (D / (4 * W));
     if (PL == 1 && !real) return;
-    const int c4 = real ? it / rows : 0, gr = real ? it - c4 * rows : 0;
+    const int cw = real ? it / rows : 0, c4 = cw * W, gr = real ? it - cw * rows : 0;
     const int rt = RT == 2 && gr >= p.NB * p.G ? 1 : 0, row = gr - rt * p.NB * p.G;
     const int first = 2 * (c1 - 1) + (s.t0 == s.run ? 0 : 1);      // the partial before the border
     const int parts = 1 + (s.tiles - s.t0 + s.run - 1) / s.run;
     const float sl = p.scale_log2;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 acc[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     float top = -INFINITY, sum = 0.f;
-    auto add = [&](float2 e, float4 o) {
+    auto add = [&](float2 e, const float4 *o) {
         const float m = fmaxf(top, e.x), mu = m == -INFINITY ? 0.f : m;
         const float f = fast_exp2((top - mu) * sl), w = fast_exp2((e.x - mu) * sl);
         top = m;
         sum = sum * f + w * e.y;
-        acc.x = acc.x * f + w * o.x;
-        acc.y = acc.y * f + w * o.y;
-        acc.z = acc.z * f + w * o.z;
-        acc.w = acc.w * f + w * o.w;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            acc[i].x = acc[i].x * f + w * o[i].x;
+            acc[i].y = acc[i].y * f + w * o[i].y;
+            acc[i].z = acc[i].z * f + w * o[i].z;
+            acc[i].w = acc[i].w * f + w * o[i].w;
+        }
     };
-#pragma unroll 4
+#pragma unroll(W > 1 ? 2 : 4)
     for (int k = pl; k < parts; k += PL) {
         const long long slot = k == 0 ? first : 2 * (c1 + k - 1);
-        add(p.stat[(slot * RT + rt) * p.rr + row], p.part[((slot * RT + rt) * (D / 4) + c4) * p.rr + row]);
+        const float4 *src = p.part + ((slot * RT + rt) * (D / 4) + c4) * p.rr + row;
+        float4 o[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) o[i] = src[i * p.rr];
+        add(p.stat[(slot * RT + rt) * p.rr + row], o);
     }
     if (PL > 1) {
         xs[tid] = make_float2(top, sum);
-        xo[tid] = acc;
+        xo[tid] = acc[0];
         __syncthreads();
         if (pl > 0 || !real) return;
-        for (int k = 1; k < PL; ++k) add(xs[k * ITEMS + tid], xo[k * ITEMS + tid]);
+        for (int k = 1; k < PL; ++k) add(xs[k * ITEMS + tid], &xo[k * ITEMS + tid]);
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
     const int local = gr / p.G;
     uint16_t *dst = p.out + (((long long)s.b * p.n + base + local) * p.H_q + s.h * p.G + (gr - local * p.G)) * D + c4 * 4;
-    *reinterpret_cast<uint2 *>(dst) =
-        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    uint2 y[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+        y[i] = make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv), pack_bf16(acc[i].z * inv, acc[i].w * inv));
+    if (W == 1) *reinterpret_cast<uint2 *>(dst) = y[0];
+#pragma unroll
+    for (int i = 0; i + 1 < W; i += 2)
+        reinterpret_cast<uint4 *>(dst)[i / 2] = make_uint4(y[i].x, y[i].y, y[i + 1].x, y[i + 1].y);
 }
 
 // ------------------------------------------------------------------- host side
@@ -1024,9 +1042,9 @@ static magicdec_status launch_tree_t(const CUtensorMap &tmq, const CUtensorMap &
     if (s != MAGICDEC_OK) return s;
     const int items = (p.n < RT * p.NB ? p.n : RT * p.NB) * p.G * (D / 4);
     const bool few = items <= 512 && 2 * (long long)p.B * p.H_kv <= p.grid;
-    const int block = few ? kTjThreads / 8 : kTjThreads;
+    const int block = few ? kTjThreads / 8 : kTjThreads * 2;
     const int per = (items + block - 1) / block;
-    return magicdec_host::launch_pdl(few ? tree_attn_join_kernel<RT, 8> : tree_attn_join_kernel<RT, 1>,
+    return magicdec_host::launch_pdl(few ? tree_attn_join_kernel<RT, 8, 1> : tree_attn_join_kernel<RT, 1, 2>,
                                      dim3((unsigned)((p.grid - 1) * per + (p.n_nodes ? p.B : 0))), dim3(kTjThreads), 0,
                                      st, p, D, per);
 }
