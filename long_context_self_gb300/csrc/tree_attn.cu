@@ -923,7 +923,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
 // ------------------------------------------------------------------ the joining
 // `per` blocks for every border between two CTAs' runs: where it is the first inside a list
 // entry, they join that entry's partials, in the order of the list.  PL neighbouring warps
-// share the partials of 32 * (8 / PL) items of four channels of a row.  With few entries, each
+// share the partials of 32 * (8 / PL) items, channels of a row.  With few entries, each
 // in many parts, and few items, PL = 8 keeps the chain of loads short (one token over 2k, 16
 // parts: 4 us less); with many items it would be blocks without number (64 nodes, 8 sequences
 // of 8k: 38,656 blocks, 32 us more), and PL = 1 keeps them few.  A block for every

@@ -316,6 +316,21 @@ def test_accept(B, n, V, tree, counts):
         assert torch.equal(a.cpu(), r)
 
 
+@pytest.mark.parametrize("B,V", [(130, 10007), (320, 4098)])
+def test_accept_full_depth_in_large_batches(B, V):
+    """Every level of a chain, with few CTAs a row."""
+    n = 7
+    g = gen(73)
+    target = torch.randn((B, n, V), generator=g)
+    tok = torch.zeros((B, n), dtype=I32)
+    tok[:, 1:] = target.argmax(-1)[:, :-1].to(I32)
+    tok[::5, 4] = -1                                  # some end at level 3
+    got = mb.magicdec_tree_accept(target.to(DEV), tok.to(DEV))
+    for a, r in zip(got, accept_ref(target, tok, None, None)):
+        assert torch.equal(a.cpu(), r)
+    assert got[0][:6].tolist() == [3, 6, 6, 6, 6, 3]
+
+
 def test_accept_infinite_logits_and_chain():
     B, n, V = 2, 4, 37
     target = torch.full((B, n, V), -float("inf"))
