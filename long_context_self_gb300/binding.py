@@ -598,6 +598,15 @@ def paged_shape(B, H_q, H_kv, d, page_size, n_pages, max_pages) -> PagedShape:
     return PagedShape(int(B), int(H_q), int(H_kv), int(d), int(page_size), int(n_pages), int(max_pages))
 
 
+_paged = functools.lru_cache(maxsize=1024)(PagedShape)         # passed by value, never written
+
+
+def _fits(name, size) -> None:
+    """Sizes are passed as C ints, to which ctypes would cut larger ones short."""
+    if size > 0x7FFFFFFF:
+        raise ValueError(f"{name} is {size}, past 2**31 - 1")
+
+
 def _paged_cache(k_pages, v_pages, block_table, B, dev, dims=4):
     """Checks of the pool and its table; their addresses and (page_size, n_pages, max_pages, H_kv, d)."""
     shape = getattr(k_pages, "shape", ())
@@ -608,6 +617,7 @@ def _paged_cache(k_pages, v_pages, block_table, B, dev, dims=4):
     ts = getattr(block_table, "shape", ())
     if len(ts) != 2 or ts[0] != B:
         raise ValueError(f"block_table must be [{B}, max_pages]")
+    _fits("max_pages", ts[1])
     return (kp, vp, _at(block_table, "block_table", _I32, dev, ts), shape[-3], shape[-4], ts[1], shape[-2], shape[-1])
 
 
@@ -667,7 +677,7 @@ def magicdec_paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tenso
         inv = _at(inv_freq, "inv_freq", _F32, dev, (rot,))
         rot *= 2
     _check("magicdec_paged_append", (_lib or lib()).magicdec_paged_append(
-        PagedShape(B, H_q, H_kv, d, page_size, n_pages, max_pages), n, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs,
+        _paged(B, H_q, H_kv, d, page_size, n_pages, max_pages), n, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs,
         _at(seq_len, "seq_len", _I32, dev, (B,)), None if n_new is None else _at(n_new, "n_new", _I32, dev, (B,)),
         None if parent is None else _at(parent, "parent", _I32, dev, (B, n)), inv, rot, 1 if interleaved else 0, table,
         qo, kp, vp, _raw_stream(dev.index)))
@@ -715,7 +725,7 @@ def magicdec_tree_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Te
     elif ws.device != dev or not ws.is_contiguous():
         raise ValueError(f"ws must be contiguous and on {dev}")
     _check("magicdec_tree_attn", (_lib or lib()).magicdec_tree_attn(
-        PagedShape(B, H_q, H_kv, d, page_size, n_pages, max_pages), n, qp, kp, vp, table, length, count, par, op,
+        _paged(B, H_q, H_kv, d, page_size, n_pages, max_pages), n, qp, kp, vp, table, length, count, par, op,
         ws.data_ptr(), ws.nbytes, _raw_stream(dev.index)))
     return out
 
@@ -732,6 +742,8 @@ def magicdec_tree_accept(target: torch.Tensor, tok: torch.Tensor, parent: Option
     if target.dim() != 3:
         raise ValueError("target must be [B, n, V]")
     B, n, V = target.shape
+    _fits("n", n)
+    _fits("V", V)
     if n_acc is None:
         n_acc = torch.empty((B,), dtype=_I32, device=dev)
     if path is None:
@@ -757,8 +769,9 @@ def magicdec_tree_commit(k_pages: torch.Tensor, v_pages: torch.Tensor, block_tab
     if path.dim() != 2:
         raise ValueError("path must be [B, n]")
     B, n = path.shape
+    _fits("n", n)
     kp, vp, table, page_size, n_pages, max_pages, H_kv, d = _paged_cache(k_pages, v_pages, block_table, B, dev, 5)
     _check("magicdec_tree_commit", (_lib or lib()).magicdec_tree_commit(
-        PagedShape(B, H_kv, H_kv, d, page_size, n_pages, max_pages), n, k_pages.shape[0] if k_pages.dim() == 5 else 1,
+        _paged(B, H_kv, H_kv, d, page_size, n_pages, max_pages), n, k_pages.shape[0] if k_pages.dim() == 5 else 1,
         _at(seq_len, "seq_len", _I32, dev, (B,)), _at(path, "path", _I32, dev, (B, n)),
         _at(n_acc, "n_acc", _I32, dev, (B,)), table, kp, vp, _raw_stream(dev.index)))

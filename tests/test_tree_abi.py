@@ -140,3 +140,15 @@ def test_binding_refuses_layouts_it_cannot_pass_on(lib, monkeypatch):
     with pytest.raises(ValueError, match="k_pages"):
         binding._paged_cache(x[None], x[None], torch.zeros((3, 4), dtype=i), 3, cpu)
     assert binding._paged_cache(x[None], x[None], torch.zeros((3, 4), dtype=i), 3, cpu, 5)[3:] == (5, 3, 4, 6, 64)
+
+
+def test_binding_refuses_sizes_that_ctypes_would_cut_short(monkeypatch):
+    import torch
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True, raising=False)
+    cpu = torch.device("cpu")
+    x = torch.zeros((3, 5, 6, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="max_pages is 4294967299"):
+        binding._paged_cache(x, x, torch.empty((3, (1 << 32) + 3), dtype=torch.int32, device="meta"), 3, cpu)
+    binding._fits("V", (1 << 31) - 1)
+    with pytest.raises(ValueError, match="V is 2147483648"):
+        binding._fits("V", 1 << 31)
