@@ -47,10 +47,20 @@ __device__ __forceinline__ uint32_t cluster_size() {
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+// The two halves of a cluster barrier, for whole warps.
+__device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
-// Store to the same shared-memory variable of CTA `rank` of the cluster.
+__device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    cluster_arrive();
+    cluster_wait();
+}
+// Store to the same shared-memory variable of CTA `rank` of the cluster, which has to be known to run.
 __device__ __forceinline__ void st_cluster_u64(uint64_t *p, uint32_t rank, uint64_t v) {
     uint32_t a;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
@@ -77,6 +87,9 @@ __global__ void __launch_bounds__(kTaThreads, kTaPerSm) tree_accept_kernel(const
     __shared__ int wnext[kTaMaxNodes / 32];
     const uint32_t rank = cluster_rank(), C = cluster_size();
     const int b = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // Every CTA says here that it runs.  Another one's shared memory is there only from then on, so
+    // the first store to it waits for all of them; the first row's loads lie between.
+    cluster_arrive();
     pdl_trigger();
     pdl_wait();
     const int raw = p.n_nodes ? checked(ld_dep(p.n_nodes + b), 0, p.n, p.err) : p.n;
@@ -140,6 +153,7 @@ __global__ void __launch_bounds__(kTaThreads, kTaPerSm) tree_accept_kernel(const
         if (rank == 0 && tid < pre) key = max(key, best_key(ld_dep_f(row + tid), tid));
         if (rank == C - 1 && tid < p.V - post) key = max(key, best_key(ld_dep_f(row + post + tid), post + tid));
         key = warp_best(key);
+        if (level == 0) cluster_wait();                         // from now on all CTAs of the cluster run
         if (lane == 0) wbest[warp] = key;
         __syncthreads();
         if (warp == 0) {
@@ -164,6 +178,7 @@ __global__ void __launch_bounds__(kTaThreads, kTaPerSm) tree_accept_kernel(const
         u = next;
         ++level;
     }
+    if (level == 0) cluster_wait();                             // no nodes: the arrival's other half
     if (rank == 0) {
         if (tid == 0) p.n_acc[b] = level - 1;
         for (int i = level + tid; i < p.n; i += kTaThreads) {
