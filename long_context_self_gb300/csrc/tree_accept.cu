@@ -11,10 +11,11 @@
 // shared memory with one cluster barrier per level.
 //
 // Bound: HBM while all sequences are at it, a chain of latencies (a row's loads, two
-// reductions, the barrier: about 2 us) when few are.  V = 128,256, 128 sequences that accept 0
-// to 4 nodes: 41.5 us, of 29 us at the measured copy rate; one sequence, V = 152,064, 4 levels:
-// 8.7 us.  Copies through shared memory in place of the loads, 96 KB a CTA under way, measured
-// slower (55 us, where the loads alone took 46): what a CTA does for a piece of 16 KB costs more than the loads' latency.
+// reductions, the barrier: about 2 us) when few are.  V = 128,256, logits from HBM, 128
+// sequences that accept 0 to 4 nodes: 43.9 us on the GPU, of 29 us at the measured copy rate;
+// 6 nodes each: 76 us, of 68; one sequence, V = 152,064, four rows: 9.3 us.  Copies through
+// shared memory in place of the loads, 96 KB a CTA under way, measured slower (55 us, where the
+// loads alone then took 46): what a CTA does for a piece of 16 KB costs more than the loads' latency.
 #include <climits>
 
 #include "common.cuh"
@@ -110,13 +111,13 @@ __global__ void __launch_bounds__(kTaThreads, kTaPerSm) tree_accept_kernel(const
         const int v0 = (int)((long long)nv * rank / C), v1 = (int)((long long)nv * (rank + 1) / C);
         const float4 *vec = reinterpret_cast<const float4 *>(row + pre);
         // The slice is on its way to L2 as a whole while the threads load it bit by bit, as long
-        // as there are few sequences, whose rate hangs on how much of a row is under way
-        // (V = 128,256, logits from HBM: 16 and 50 sequences 18.6 and 28.8 us without, 16.2 and
-        // 26.9 us with it; 128 sequences 44.3 and 46.6 us), or deep in the trees, where most
-        // sequences have ended (100, 128 and 200 sequences that accept 0 to 4 nodes: 40.9, 44.3
-        // and 71.1 us without, 38.4, 41.5 and 69.5 us with it from level 3 on; 37.7, 42.1 and
-        // 71.1 us from level 2 on).
-        if (C >= 4 || level >= 3)
+        // as there are few sequences, whose rate hangs on how much of a row is under way.  With,
+        // and without it (V = 128,256, us on the GPU, logits from HBM, of sequences that accept
+        // 0 to 4 nodes evenly, 6 each, none): 16 sequences 18.4, 40.6, 6.6 and 18.9, 41.6, 7.2;
+        // 50 sequences 25.5, 38.0, 7.8 and 27.0, 41.7, 7.5; 76 sequences 33.8, 74.5, 13.5 and
+        // 34.4, 81.2, 13.2; 100 sequences, two CTAs a row, 40.5, 69.2, 13.1 and 40.4, 65.3, 11.1;
+        // 128 sequences 46.3, 85.8, 14.9 and 43.8, 75.8, 12.7.
+        if (C >= 4)
             for (int at = v0 + tid * kTaAsk; at < v1; at += kTaThreads * kTaAsk)
                 bulk_prefetch_l2(vec + at, (uint32_t)min(kTaAsk, v1 - at) * 16);
         // The largest of a thread's vectors, the first of equal ones.
@@ -202,8 +203,10 @@ magicdec_status launch_tree_accept(int B, int n, int V, const float *target, con
     p.err = magicdec_host::device_error_word();
     p.n = n;
     p.V = V;
-    // As many CTAs a row as there are places for (with more, 50 sequences take 26.9 us instead of
-    // 24.5, 128 take 48.9 instead of 44.3).
+    // As many CTAs a row as there are places for.  So, and with twice as many (inputs as above):
+    // 38 sequences 20.5, 49.9, 9.3 and 33.0, 63.8, 11.6 us; 50 sequences 25.5, 38.0, 7.8 and
+    // 27.7, 54.6, 9.9; 128 sequences 44.0, 76.1, 12.8 and 48.6, 87.0, 16.8; 200 sequences 70.6,
+    // 116.7, 18.9 and 66.3, 137.2, 21.8.
     int C = kTaMaxCluster;
     while (C > 1 && (long long)B * C > (long long)kTaPerSm * magicdec_host::sm_count()) C /= 2;
     if (!magicdec_host::allow_wide_cluster_once<tree_accept_kernel>()) return MAGICDEC_ERR_CUDA;
