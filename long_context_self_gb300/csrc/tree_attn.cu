@@ -784,6 +784,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                             grown = m + kTrLazy / sl;
                             l *= f;
                         }
+                        __syncwarp();                        // TMEM is read and written by whole warps
                         // This S being there, the product over the last P in its place is done;
                         // the one over the other's may be under way.
                         if (used[1 - h] != before[1 - h])
@@ -887,25 +888,28 @@ __global__ void __launch_bounds__(kTrThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) x[i] += w1 * __uint_as_float(o[i]);
                 }
-                if (node < 0) continue;
-                if (whole) {
+                if (node >= 0) {
+                    if (whole) {
 #pragma unroll
-                    for (int i = 0; i < 16; i += 8) {
-                        uint4 y;
-                        y.x = pack_bf16(x[i] * inv, x[i + 1] * inv);
-                        y.y = pack_bf16(x[i + 2] * inv, x[i + 3] * inv);
-                        y.z = pack_bf16(x[i + 4] * inv, x[i + 5] * inv);
-                        y.w = pack_bf16(x[i + 6] * inv, x[i + 7] * inv);
-                        *reinterpret_cast<uint4 *>(dst + c0 + i) = y;
+                        for (int i = 0; i < 16; i += 8) {
+                            uint4 y;
+                            y.x = pack_bf16(x[i] * inv, x[i + 1] * inv);
+                            y.y = pack_bf16(x[i + 2] * inv, x[i + 3] * inv);
+                            y.z = pack_bf16(x[i + 4] * inv, x[i + 5] * inv);
+                            y.w = pack_bf16(x[i + 6] * inv, x[i + 7] * inv);
+                            *reinterpret_cast<uint4 *>(dst + c0 + i) = y;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4)
+                            pd[(c0 + i) / 4 * p.rr] = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
                     }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4)
-                        pd[(c0 + i) / 4 * p.rr] = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
                 }
+                __syncwarp();                                // TMEM is read by whole warps
             }
             if (!whole && node >= 0 && c_lo == 0)
                 p.stat[((long long)part * RT + rt) * p.rr + row] = make_float2(mm, ll);
+            __syncwarp();
             tc_fence_before();
             // O is free for the next run, whose first P says so: with one row tile, once all
             // warps have read both.

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from long_context_self_gb300 import binding as mb
-from tree_util import accept_ref, gen, make_tree
+from tree_util import accept_ref, attn_ref, gen, make_cache, make_tree, rows_of
 
 pytestmark = pytest.mark.gpu
 
@@ -31,6 +31,34 @@ def i32(x):
 
 def randn(shape, seed):
     return torch.randn(shape, generator=gen(seed)).to(BF16).to(DEV)
+
+
+def within(got, ref, tol):
+    assert torch.isfinite(got).all()
+    over = ((got.double() - ref).abs() - tol).max().item()
+    assert over <= 0, f"off by {over:.3e} more than the bound"
+
+
+# ------------------------------------------------------------------- attention
+@pytest.mark.parametrize("page", [16, 130])      # 130: every other tile has two keys
+@pytest.mark.parametrize("H_q,H_kv,d,n", [(1, 1, 128, 1), (3, 1, 64, 1), (31, 1, 128, 1), (33, 1, 64, 1), (5, 1, 128, 13),
+                                          (97, 1, 128, 1), (127, 1, 64, 1), (3, 1, 128, 43), (5, 1, 64, 51),
+                                          (2, 2, 128, 129), (1, 1, 64, 161)])
+def test_attention_rows_that_leave_warps_part_empty(H_q, H_kv, d, n, page):
+    """Warps some of whose rows have no node, whose rows' maxima grow at different tiles; a sequence
+    that one CTA has whole and one that several join."""
+    lens = [9, 4001]
+    kp, vp, table = make_cache(lens, n, page, H_kv, d, 211, DEV, poison=True)
+    # Every 97th key is 3 times as long, so maxima move late and for some rows only.  Scores reach
+    # 3 * |q| |k| / sqrt(d), about 40: fp32 products of that size are off by less than
+    # 128 * 2^-24 * 3 * sum |q k| / sqrt(d) < 2^-12, inside the bound's 2^-10.
+    for b in range(2):
+        at = torch.arange(0, lens[b], 97)
+        x = kp.view(-1, H_kv, d)
+        x[rows_of(table, b, at, page).to(DEV)] *= 3
+    q, parent = randn((2, n, H_q, d), 212), make_tree(2, n, "random", 213)
+    got = mb.magicdec_tree_attn(q, kp, vp, table, i32(lens), parent=parent.to(DEV))
+    within(got, *attn_ref(q, kp, vp, table, lens, parent, None))
 
 
 # ---------------------------------------------------------------------- accept
