@@ -481,8 +481,8 @@ MAGICDEC_API size_t magicdec_tree_attn_workspace_size(magicdec_paged_shape shape
  *       nothing (no node sees them)
  *   ws  workspace of magicdec_tree_attn_workspace_size(shape, n) bytes; no initial
  *       contents needed
- * Pool rows outside [0, len + n_nodes) may hold anything, NaN included.  A page
- * outside the pool counts as keys and values of zero (device error 5).
+ * Pool rows outside [0, len + n_nodes) may hold anything, NaN included; a node's
+ * own rows reach it and its descendants only, whatever they hold.  A page outside the pool counts as keys and values of zero (device error 5).
  * Supported: n <= 256, H_q/H_kv <= 128 (MAGICDEC_ERR_UNSUPPORTED beyond).
  * Errors: NULL pointers, bad shape, n <= 0, alignment, workspace too small.
  */

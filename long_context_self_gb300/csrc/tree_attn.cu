@@ -52,6 +52,7 @@ struct TreeStart {
 
 struct TreeAttnParams {
     const int32_t *len, *n_nodes, *parent, *table;
+    const uint16_t *vp;    // the pool of V, for add_back
     uint16_t *out;
     TreeStart *start;      // workspace: [grid]
     float2 *stat;          // workspace: [2 * grid][RT * rr] (max, sum)
@@ -281,6 +282,73 @@ __device__ __noinline__ uint32_t seen(int prefix, int rows, int node, const uint
     return see;
 }
 
+// A node's V may hold infinities and NaN, of which the nodes that do not see it must have
+// nothing; but a masked probability is a product with zero, and 0 * inf is NaN.  So in the tiles
+// that hold nodes' slots those values are taken out of shared memory before the product
+// (take_out), and a run whose CTA met any adds them, of the nodes that a row does see, to the
+// row's sums at its end, from the pool (add_back): a product with a probability above zero is
+// the same infinity, or NaN.  What it costs the tiles that are looked through (ragged d = 64,
+// 24 entries of up to 9k: 68.7 -> 70.0 us; chain of 200 over 8k: 220 -> 224; others nothing) is
+// mostly behind the softmax of their first half, while their V arrives.
+
+// Whether either bf16 of a word is not finite: 0x8000 in its place, else 0.
+__device__ __forceinline__ uint32_t not_finite(uint32_t x) { return ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+// All bits of the bf16 whose top bit is set in `m`.
+__device__ __forceinline__ uint32_t whole_halves(uint32_t m) { return (m >> 15) * 0xffffu; }
+
+// Rows [lo, hi) of a V tile, by the 256 threads of a stream; `met` is set if there were any, before
+// they are taken out, so that the other stream, which then does not find them, knows.
+template <int HALVES>
+__device__ __forceinline__ void take_out(uint8_t *v, int lo, int hi, uint32_t sbo, uint32_t hoff, int thread,
+                                         volatile int *met) {
+    bool any = false;
+#pragma unroll 1
+    for (int i = thread; i < (hi - lo) * HALVES * 8; i += 256) {
+        const int row = lo + i / (HALVES * 8), c = i % (HALVES * 8);
+        uint4 *at = reinterpret_cast<uint4 *>(v + (c >> 3) * hoff + (row >> 3) * sbo + (row & 7) * 128 + (c & 7) * 16);
+        uint4 x = *at;
+        const uint4 m = make_uint4(not_finite(x.x), not_finite(x.y), not_finite(x.z), not_finite(x.w));
+        if (m.x | m.y | m.z | m.w) {
+            *met = 1;
+            __threadfence_block();
+            x.x &= ~whole_halves(m.x);
+            x.y &= ~whole_halves(m.y);
+            x.z &= ~whole_halves(m.z);
+            x.w &= ~whole_halves(m.w);
+            *at = x;
+            any = true;
+        }
+    }
+    if (any) fence_proxy_async_smem();
+}
+
+// 16 channels, as pairs of bf16: the sum of the values that are not finite over the nodes that
+// `node` sees and whose slots lie in [from, to).  A function of its own, as it is hardly ever called.
+struct Channels16 {
+    uint32_t x[8];
+};
+__device__ __noinline__ Channels16 add_back(const uint16_t *v, long long stride, const int32_t *table, int page_size,
+                                            int n_pages, int len, int from, int to, int node, const uint8_t *par) {
+    Channels16 r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.x[i] = 0;
+    for (int a = node; a >= 0; a = par ? (int)par[a] - 1 : a - 1) {
+        const int slot = len + a;
+        if (slot < from || slot >= to) continue;
+        const int pg = slot / page_size, id = table[pg];
+        if (id < 0 || id >= n_pages) continue;                 // zeros
+        const uint32_t *x =
+            reinterpret_cast<const uint32_t *>(v + ((long long)id * page_size + slot - pg * page_size) * stride);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t y = x[i] & whole_halves(not_finite(x[i]));
+            r.x[i] = pack_bf16(__uint_as_float(r.x[i] << 16) + __uint_as_float(y << 16),
+                               __uint_as_float(r.x[i] & 0xffff0000u) + __uint_as_float(y & 0xffff0000u));
+        }
+    }
+    return r;
+}
+
 // x / d, in 32 bits where they suffice (a 64-bit division is a hundred instructions).
 __device__ __forceinline__ long long quotient(long long x, int d) {
     return x <= 0xffffffffll ? (long long)((uint32_t)x / (uint32_t)d) : x / d;
@@ -367,6 +435,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     uint64_t *mma_done = o_full + 4;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 2);
     int *found = reinterpret_cast<int *>(tmem_slot + 1);                 // where this CTA begins: see the list of work
+    volatile int *met = found + 8;                                       // a node's V was not finite: see take_out
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (smem_u32(smem) & 1023u) {
         if (tid == 0) raise_error(p.err, kErrState);
@@ -393,6 +462,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         prefetch_tensormap(&tmk);
         prefetch_tensormap(&tmv);
         found[2] = 0;
+        *met = 0;
     }
     if (warp == 1) tmem_alloc(tmem_slot, 512);
     pdl_trigger();
@@ -711,6 +781,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         uint32_t *myturns = turns + s * (kTrMaxNodes / 32);
         float *mine_x = xch + (s * 2 + half) * 128 + row, *other_x = xch + (s * 2 + 1 - half) * 128 + row;
         uint32_t used[2] = {0, 0};                                      // of this stream's two S
+        uint32_t idle = 0;                                              // tiles that this stream passed by
         int par_b = -1;
         bool first_run = true;
         while (walk.next(p, r)) {
@@ -816,6 +887,11 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     l += sum.x + sum.y;
                     tmem_wait_st();
                 }
+                if (edge && h == 0 && r.s.nodes > 1 && t.p0 + t.rows > r.s.len) {   // a node sees itself
+                    const uint32_t slot = 2 * (used[0] + idle) + 1, at = (RT == 1 ? s : 0) * NST + slot % NST;
+                    ok = tr_wait(&full[at], (slot / NST) & 1, p.err, ok, lane);    // the tile's V
+                    if (ok) take_out<HALVES>(ring + at * OPER, max(r.s.len - t.p0, 0), t.rows, p.sbo, p.hoff, wt, met);
+                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[s * 2 + h]);
@@ -834,6 +910,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     if (t.rows > 64) half_tile(t, c1, c1);
                 }
             }
+            if (!active) idle += r.cnt;
             // The end of the run: O / l if the run is the whole list entry, else a partial.
             for (int h = 0; h < 2; ++h)
                 if (used[h] != before[h]) ok = tr_wait(&o_full[s * 2 + h], (used[h] - 1) & 1, p.err, ok, lane);
@@ -889,6 +966,16 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     for (int i = 0; i < 16; ++i) x[i] += w1 * __uint_as_float(o[i]);
                 }
                 if (node >= 0) {
+                    if (*met) {
+                        const Tile e = TileWalk(p, r.t0 + r.cnt - 1).at(p, r.s.total);
+                        const Channels16 z =
+                            add_back(p.vp + r.h * D + c0, (long long)p.H_kv * D, p.table + (long long)r.b * p.max_pages,
+                                     p.page_size, p.n_pages, r.s.len, TileWalk(p, r.t0).at(p, r.s.total).p0,
+                                     e.p0 + e.rows, node, p.parent ? mypar : nullptr);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            x[i] += __uint_as_float(i & 1 ? z.x[i / 2] & 0xffff0000u : z.x[i / 2] << 16);
+                    }
                     if (whole) {
 #pragma unroll
                         for (int i = 0; i < 16; i += 8) {
@@ -1061,6 +1148,7 @@ magicdec_status launch_tree_attn(const magicdec_paged_shape &s, int n, const uin
     p.n_nodes = n_nodes;
     p.parent = parent;
     p.table = table;
+    p.vp = vp;
     p.out = out;
     p.err = magicdec_host::device_error_word();
     p.B = s.B;

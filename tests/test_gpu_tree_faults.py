@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from long_context_self_gb300 import binding as mb
-from tree_util import accept_ref, attn_ref, gen, make_cache, make_tree, rows_of
+from tree_util import accept_ref, ancestors, attn_ref, gen, make_cache, make_tree, rows_of
 
 pytestmark = pytest.mark.gpu
 
@@ -59,6 +59,75 @@ def test_attention_rows_that_leave_warps_part_empty(H_q, H_kv, d, n, page):
     q, parent = randn((2, n, H_q, d), 212), make_tree(2, n, "random", 213)
     got = mb.magicdec_tree_attn(q, kp, vp, table, i32(lens), parent=parent.to(DEV))
     within(got, *attn_ref(q, kp, vp, table, lens, parent, None))
+
+
+@pytest.mark.parametrize("H_q,H_kv,d,n,lens,page,tree,counts", [
+    (8, 2, 128, 2, [0, 127, 300], 16, "chain", None),
+    (8, 2, 128, 13, [0, 1, 121, 700], 16, "random", [13, 2, 7, 13]),       # one row tile
+    (8, 2, 64, 13, [120, 64, 9001], 48, "star", None),
+    (8, 2, 64, 20, [250, 3], 100, None, None),                             # a causal block
+    (8, 2, 128, 6, [500, 3], 7, "random", None),
+    (8, 2, 64, 40, [301, 2], 1, "forest", None),
+    (8, 2, 128, 40, [30000, 90], 64, "random", None),                      # two row tiles, joined
+    (32, 8, 128, 64, [2000, 64, 0], 16, "random", [64, 33, 50]),
+    (16, 4, 128, 256, [700, 5], 256, "random", None),                      # several pairs of row tiles
+    (8, 8, 64, 200, [250], 16, None, None),
+])
+def test_attention_values_that_a_node_does_not_see(H_q, H_kv, d, n, lens, page, tree, counts):
+    """A node's keys and values reach itself and its descendants only, whatever they are: infinities
+    in single channels, of both signs, NaN in a whole row, a NaN key."""
+    B = len(lens)
+    kp, vp, table = make_cache(lens, n, page, H_kv, d, 221, DEV, poison=True, counts=counts)
+    q = randn((B, n, H_q, d), 222)
+    parent = None if tree is None else make_tree(B, n, tree, 223)
+    kx, vx = kp.view(-1, H_kv, d), vp.view(-1, H_kv, d)
+    k0, v0 = kp.clone(), vp.clone()                           # the same with zeros in their place
+    k0x, v0x = k0.view(-1, H_kv, d), v0.view(-1, H_kv, d)
+    more = torch.zeros((B, n, H_kv, d), dtype=torch.float64)  # what each node's own values add
+    key = torch.zeros((B, n, H_kv), dtype=torch.bool)
+    for b in range(B):
+        m = n if counts is None else counts[b]
+        rows = rows_of(table, b, lens[b] + torch.arange(m), page)
+        picks = torch.randperm(m, generator=gen(224 + b))
+        for what, i in enumerate(picks[: max(1, m // 3)].tolist()):
+            h = (what // 4) % H_kv
+            if what % 4 == 3:
+                kx[rows[i], h, 5] = float("nan")
+                k0x[rows[i], h, 5] = 0
+                key[b, i, h] = True
+                continue
+            at = slice(None) if what % 4 == 2 else slice(what % 11, None, 17 + what)
+            x = (float("inf"), -float("inf"), float("nan"))[what % 4]
+            vx[rows[i], h, at] = x
+            v0x[rows[i], h, at] = 0
+            more[b, i, h, at] = x
+    got = mb.magicdec_tree_attn(q, kp, vp, table, i32(lens), parent=None if parent is None else parent.to(DEV),
+                                n_nodes=i32(counts)).cpu()
+    ref, tol = (x.cpu() for x in attn_ref(q, k0, v0, table, lens, parent, counts))
+    G = H_q // H_kv
+    for b in range(B):
+        for i in range(n if counts is None else counts[b]):
+            path = ancestors(None if parent is None else parent[b].tolist(), i)
+            ref[b, i] += more[b, path].sum(0).repeat_interleave(G, 0)
+            ref[b, i][key[b, path].any(0).repeat_interleave(G)] = float("nan")
+    assert torch.equal(torch.isnan(got), torch.isnan(ref))
+    far = torch.isinf(ref)
+    assert torch.equal(torch.isinf(got), far) and torch.equal(got[far].double(), ref[far])
+    fine = torch.isfinite(ref)
+    assert ((got.double() - ref).abs() - tol)[fine].max() <= 0
+
+
+def test_attention_row_that_sees_nothing_beside_values_that_are_not_finite():
+    """Roots past the capacity of an empty sequence: zero, whatever the nodes inside it hold."""
+    H_q, H_kv, d, n = 4, 2, 128, 6
+    kp, vp = randn((2, 4, H_kv, d), 231), randn((2, 4, H_kv, d), 232)
+    vp[0, 1], vp[0, 3] = float("nan"), float("inf")
+    table = torch.tensor([[0], [1]], dtype=I32, device=DEV)
+    parent = i32([[-1, -1, 0, -1, -1, -1]] * 2)
+    got = mb.magicdec_tree_attn(randn((2, n, H_q, d), 233), kp, vp, table, i32([0, 0]), parent=parent)
+    assert (got[:, 4:] == 0).all() and torch.isfinite(got[1]).all()
+    assert torch.isfinite(got[0, [0, 2]]).all()
+    assert torch.isnan(got[0, 1]).all() and (got[0, 3] == float("inf")).all()
 
 
 # ---------------------------------------------------------------------- accept
