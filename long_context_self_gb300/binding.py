@@ -617,7 +617,9 @@ def _paged_cache(k_pages, v_pages, block_table, B, dev, dims=4):
     ts = getattr(block_table, "shape", ())
     if len(ts) != 2 or ts[0] != B:
         raise ValueError(f"block_table must be [{B}, max_pages]")
-    _fits("max_pages", ts[1])
+    if max(*ts, *shape) > 0x7FFFFFFF:
+        for name, size in (("B", B), ("max_pages", ts[1]), *((f"k_pages.shape[{i}]", x) for i, x in enumerate(shape))):
+            _fits(name, size)
     return (kp, vp, _at(block_table, "block_table", _I32, dev, ts), shape[-3], shape[-4], ts[1], shape[-2], shape[-1])
 
 
@@ -742,6 +744,7 @@ def magicdec_tree_accept(target: torch.Tensor, tok: torch.Tensor, parent: Option
     if target.dim() != 3:
         raise ValueError("target must be [B, n, V]")
     B, n, V = target.shape
+    _fits("B", B)
     _fits("n", n)
     _fits("V", V)
     if n_acc is None:
