@@ -590,6 +590,8 @@ def _on(dev, stream):
     """The tensors' device, and the stream of the call, as the current ones."""
     if stream is not None and not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
     with torch.cuda.device(dev), torch.cuda.stream(stream):
         yield
 

@@ -26,3 +26,26 @@ def test_batches_that_ctypes_would_cut_short(stand_in):
     kp = empty(B, 1, 1, 64, t=torch.bfloat16)
     with pytest.raises(ValueError, match=r"k_pages.shape\[0\] is"):
         binding.magicdec_tree_commit(kp, kp, empty(2, 1), empty(2), empty(2, 1), empty(2))
+
+
+def test_a_stream_of_another_device(stand_in):
+    """It would become the current one with its device, and the call would go to the tensors'
+    device's own current stream."""
+    class Stream:
+        cuda_stream, device = 7, torch.device("cuda", 1)
+
+    class Here(Stream):
+        device = torch.device("meta")
+
+    x, p = empty(2, 4, 8, 128, t=torch.bfloat16), empty(20, 16, 8, 128, t=torch.bfloat16)
+    lens = empty(2)
+    calls = (lambda s: binding.magicdec_paged_append(x, x, p, p, empty(2, 10), lens, stream=s),
+             lambda s: binding.magicdec_tree_attn(x, p, p, empty(2, 10), lens, stream=s),
+             lambda s: binding.magicdec_tree_accept(empty(2, 4, 9, t=torch.float32), empty(2, 4), stream=s),
+             lambda s: binding.magicdec_tree_commit(p, p, empty(2, 10), lens, empty(2, 4), lens, stream=s))
+    for call in calls:
+        with pytest.raises(ValueError, match="stream is on cuda:1"):
+            call(Stream())
+        with pytest.raises(Exception) as e:                 # goes on to select the device, of which there is none
+            call(Here())
+        assert "stream is on" not in str(e.value)
