@@ -416,6 +416,8 @@ magicdec_status magicdec_paged_append(magicdec_paged_shape shape, int n, const u
 static magicdec_status tree_shape(const magicdec_paged_shape &shape, int n) {
     if (!paged_ok(shape) || n <= 0) return MAGICDEC_ERR_SHAPE;
     if (n > kTreeMaxNodes || shape.H_q / shape.H_kv > 128) return MAGICDEC_ERR_UNSUPPORTED;
+    // Such pages are gathered by rows of the pool, which are counted in 32 bits.
+    if (shape.page_size < 4 && (long long)shape.n_pages * shape.page_size >= INT_MAX) return MAGICDEC_ERR_UNSUPPORTED;
     return MAGICDEC_OK;
 }
 

@@ -590,27 +590,24 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                                         &full_r[st], pol);
                     continue;
                 }
-                // Boxes of br rows, each inside a page.  The lane's page number is on its way while
-                // the warp waits for the ring.
-                const int boxes = (t.rows + p.br - 1) / p.br;
-                auto locate = [&](int g) {
-                    const int at = t.p0 + g * p.br, pg = at / p.page_size;
+                // Boxes of br rows, each inside a page, at most one a lane (pages of fewer than 4 rows go
+                // the way above).  The lane's page number is on its way while the warp waits for the ring.
+                const int boxes = (t.rows + p.br - 1) / p.br, at = lane * p.br;      // row in the tile
+                if ((RT == 2 || !is_v) && lane < boxes) {
+                    const int pos = t.p0 + at, pg = pos / p.page_size;
                     id = ld_dep(table + pg);
-                    pr = at - pg * p.page_size;
-                };
-                if ((RT == 2 || !is_v || boxes > 32) && lane < boxes) locate(lane);
+                    pr = pos - pg * p.page_size;
+                }
                 ok = tr_wait(&empty_r[st], ph ^ 1, p.err, ok, lane);
                 if (!ok) break;
                 const CUtensorMap *tm = is_v ? &tmv : &tmk;
                 if (lane == 0) mbar_arrive_expect_tx(&full_r[st], (uint32_t)(boxes * p.br * HALVES * 128));
                 __syncwarp();
-                for (int g = lane; g < boxes; g += 32) {
-                    if (g >= 32) locate(g);
+                if (lane < boxes) {
                     if (id < 0 || id >= p.n_pages) {       // such a page is filled with zeros
                         raise_error(p.err, kErrPage);
                         id = p.n_pages;
                     }
-                    const int at = g * p.br;                           // row in the tile
                     if (p.by8)
                         tma_load_5d(dst + at / 8 * (HALVES * 1024), tm, 0, 0, r.h * HALVES, pr / 8, id, &full_r[st], pol);
                     else
@@ -1199,7 +1196,7 @@ magicdec_status launch_tree_attn(const magicdec_paged_shape &s, int n, const uin
     // 4.2, 2.2 and 1.8 ms with a box a page, 1.6 ms so; of 4 rows: 1.15 ms with boxes).
     CUtensorMap tmq, tmk, tmv;
     const int D = s.d, HV = D / 64;
-    p.by4 = s.page_size < 4 && (long long)s.n_pages * s.page_size < INT_MAX;
+    p.by4 = s.page_size < 4;
     p.sbo = p.by8 ? HV * 1024 : 1024;
     p.hoff = p.by8 ? 1024 : kTrBox;
     const uint64_t row = (uint64_t)s.H_kv * D * 2;

@@ -49,3 +49,20 @@ def test_a_stream_of_another_device(stand_in):
         with pytest.raises(Exception) as e:                 # goes on to select the device, of which there is none
             call(Here())
         assert "stream is on" not in str(e.value)
+
+
+def test_pools_of_single_rows_past_32_bits():
+    """Pages of 1 to 3 rows are gathered by their rows' numbers in the pool."""
+    from long_context_self_gb300 import build
+    build.build()
+    lib, P = binding.lib(), binding.ctypes.c_void_p
+    for page in (1, 2, 3):
+        most = ((1 << 31) - 2) // page
+        for n_pages, ok in ((most, True), (most + 1, page * (most + 1) < (1 << 31) - 1)):
+            s = binding.paged_shape(1, 8, 1, 64, page, n_pages, 10)
+            size = lib.magicdec_tree_attn_workspace_size(s, 4)
+            assert (size > 0) == ok
+            if not ok:
+                x = P(0x10000)
+                assert lib.magicdec_tree_attn(s, 4, x, x, x, x, x, P(0), P(0), x, x, 1 << 40, P(0)) == -5
+    assert lib.magicdec_tree_attn_workspace_size(binding.paged_shape(1, 8, 1, 64, 4, 1 << 30, 10), 4) > 0
