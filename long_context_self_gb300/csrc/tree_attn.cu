@@ -840,7 +840,6 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     // half tile itself.  Both halves of a row have to agree; the barrier also puts
                     // the loads of S by both before the stores of P over it.
                     if (pair_any(pair_bar, top > grown)) {
-                        asm volatile("");
                         *mine_x = top;
                         named_bar_sync(pair_bar, 64);
                         top = fmaxf(top, *other_x);
