@@ -498,7 +498,9 @@ MAGICDEC_API magicdec_status magicdec_tree_attn(magicdec_paged_shape shape, int 
  * Greedy acceptance down the tree.  From node u = 0: t = argmax target[b, u], ties
  * to the smaller token; the walk goes on to the lowest node whose parent is u and
  * whose token is t, and ends where there is none.
- *   target [B, n, V] fp32 logits of the target at every node (-inf allowed)
+ *   target [B, n, V] fp32 logits of the target at every node; infinities are values
+ *          like others, NaN counts as -inf, and of a row of nothing else token 0 is
+ *          the argmax
  *   tok    [B, n] int32: the nodes' tokens (tok[b, 0] is not looked at)
  * Outputs: n_acc [B]: nodes accepted after node 0, -1 for a sequence without nodes
  *   (so that len + n_acc + 1 is its next length in every case); path [B, n]: node 0

@@ -147,3 +147,30 @@ def test_accept_small_vocabulary(B, V):
     for _ in range(20):
         for a, r in zip(mb.magicdec_tree_accept(*args), ref):
             assert torch.equal(a.cpu(), r)
+
+
+@pytest.mark.parametrize("B,V", [(3, 37), (40, 4099), (160, 1030)])
+def test_accept_infinities_and_nan(B, V):
+    """NaN counts as -inf, wherever in a row and in how many of its values; infinities as themselves."""
+    n = 6
+    g = gen(241)
+    target = torch.randn((B, n, V), generator=g)
+    inf, nan = float("inf"), float("nan")
+    target[0::3, 0, ::2] = nan
+    target[0::3, 1] = nan
+    target[0::3, 2, 1:] = nan
+    target[0::3, 2, 0] = -inf
+    target[1::3, 0, V // 2] = inf
+    target[1::3, 0, V - 1] = inf
+    target[1::3, 1, 0] = nan
+    target[1::3, 1, V - 1] = 1e30
+    target[2::3, :2] = -inf
+    target[2::3, 1, 3] = nan
+    target[2::3, 1, V - 2] = -3e38
+    plain = torch.where(torch.isnan(target), -inf, target)
+    tok = torch.zeros((B, n), dtype=I32)
+    tok[:, 1:] = torch.where(plain == plain.amax(-1, keepdim=True), torch.arange(V), V).amin(-1)[:, :-1].to(I32)
+    ref = accept_ref(plain, tok, None, None)
+    assert (ref[0] == n - 1).all()
+    for a, r in zip(mb.magicdec_tree_accept(target.to(DEV), tok.to(DEV)), ref):
+        assert torch.equal(a.cpu(), r)
