@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from long_context_self_gb300 import binding as mb
-from tree_util import accept_ref, ancestors, attn_ref, gen, make_cache, make_tree, rows_of
+from tree_util import accept_ref, ancestors, attn_ref, gen, make_cache, make_tree, rope_ref, rows_of
 
 pytestmark = pytest.mark.gpu
 
@@ -174,3 +174,86 @@ def test_accept_infinities_and_nan(B, V):
     assert (ref[0] == n - 1).all()
     for a, r in zip(mb.magicdec_tree_accept(target.to(DEV), tok.to(DEV)), ref):
         assert torch.equal(a.cpu(), r)
+
+
+# ----------------------------------------------------------------- steps of all
+@pytest.mark.parametrize("page", [None, 16])
+def test_steps_from_a_prompt(page):
+    """A ragged prompt's append, then steps of append, attention, acceptance, commit and the next
+    lengths, over a dense cache (page None: one page a sequence) or pages.  Every row of K and V is
+    followed: as the append writes it (against the rotation's 64-bit form), and bit for bit through the
+    commits.  Over the dense cache a StreamingLLM draft cache takes the accepted positions in."""
+    B, n, H_q, H_kv, d, V, layers, P, steps = 3, 12, 8, 2, 128, 41, 2, 70, 4
+    L_cap = P + steps * n
+    g = gen(251)
+    ps = L_cap if page is None else page
+    mp = -(-L_cap // ps)
+    pages = torch.arange(B) if page is None else torch.randperm(B * mp + 3, generator=g)[: B * mp]
+    table = pages.view(B, mp).to(I32).to(DEV)
+    shape = (layers, B if page is None else B * mp + 3, ps, H_kv, d)
+    kp, vp = (torch.full(shape, float("nan"), dtype=BF16, device=DEV) for _ in range(2))
+    inv = (10000.0 ** (-torch.arange(0, d, 2, dtype=torch.float64) / d)).float().to(DEV)
+    lens = [P, 1, 33]
+    rows = [rows_of(table, b, torch.arange(L_cap), ps).to(DEV) for b in range(B)]
+
+    def append(m, length, seed, **kw):
+        x = [randn((B, m, H, d), seed + j) for j, H in enumerate((H_q, H_kv, H_kv))]
+        out = []
+        for layer in range(layers):
+            k, v = x[1].roll(layer, -1), x[2].roll(layer, -1)
+            q = mb.magicdec_paged_append(k, v, kp[layer], vp[layer], table, i32(length), inv, q=x[0], **kw)
+            out.append((q, k, v))
+        return out
+
+    def check_rows(new, length, depth, counts):
+        for layer, (_, k, v) in enumerate(new):
+            for b in range(B):
+                at = rows[b][length[b]:length[b] + counts[b]]
+                pos = (length[b] + depth[b, :counts[b]]).to(DEV)
+                within(kp[layer].view(-1, H_kv, d)[at], *rope_ref(k[b, :counts[b]], pos, inv, False))
+                assert torch.equal(vp[layer].view(-1, H_kv, d)[at], v[b, :counts[b]])
+
+    check_rows(append(P, [0] * B, 252, n_new=i32(lens)), [0] * B, torch.arange(P).expand(B, P), lens)
+    ring, sinks = 16, 4
+    if page is None:
+        kc, vc = (torch.full((B, H_kv, sinks + ring, d), float("nan"), dtype=BF16, device=DEV) for _ in range(2))
+        origin, zero = i32([sinks] * B), i32([0] * B)
+        mb.magicdec_draft_cache_update(kp[0], vp[0], kc, vc, zero, zero, i32(lens), origin, None, ring)
+    total = 0
+    for step in range(steps):
+        parent = make_tree(B, n, "random", 260 + step)
+        depth = torch.tensor([[len(ancestors(parent[b].tolist(), i)) - 1 for i in range(n)] for b in range(B)])
+        new = append(n, lens, 270 + 10 * step, parent=parent.to(DEV))
+        check_rows(new, lens, depth, [n] * B)
+        for layer, (q, _, _) in enumerate(new):
+            got = mb.magicdec_tree_attn(q, kp[layer], vp[layer], table, i32(lens), parent=parent.to(DEV))
+            within(got, *attn_ref(q, kp[layer], vp[layer], table, lens, parent, None))
+        target = torch.randn((B, n, V), generator=g)
+        tok = target.argmax(-1).gather(1, parent.clamp(min=0).long())
+        tok = torch.where(torch.rand((B, n), generator=g) < 0.8, tok, 0).to(I32)
+        n_acc, path, out = mb.magicdec_tree_accept(target.to(DEV), tok.to(DEV), parent=parent.to(DEV))
+        ref = accept_ref(target, tok, parent, None)
+        assert torch.equal(n_acc.cpu(), ref[0]) and torch.equal(path.cpu(), ref[1]) and torch.equal(out.cpu(), ref[2])
+        moved = []
+        for x in (kp, vp):
+            x = x.clone().view(layers, -1, H_kv, d)
+            for b in range(B):
+                m = int(ref[0][b]) + 1
+                x[:, rows[b][lens[b]:lens[b] + m]] = x[:, rows[b][lens[b] + ref[1][b, :m].long()]].clone()
+            moved.append(x)
+        mb.magicdec_tree_commit(kp, vp, table, i32(lens), path, n_acc)
+        for x, y in zip((kp, vp), moved):
+            assert torch.equal(x.view(layers, -1, H_kv, d).view(torch.int16), y.view(torch.int16))
+        now, _ = mb.magicdec_step_lengths(i32(lens), 0, L_cap, n_acc=n_acc)
+        if page is None:
+            mb.magicdec_draft_cache_update(kp[0], vp[0], kc, vc, i32(lens), i32(lens), now, origin, None, ring)
+        lens = [ln + int(a) + 1 for ln, a in zip(lens, ref[0])]
+        total += int(ref[0].sum())
+        assert now.tolist() == lens
+        if page is None:
+            for b, ln in enumerate(lens):
+                pos = torch.cat((torch.arange(min(ln, sinks)), torch.arange(max(sinks, ln - ring), ln)))
+                slot = torch.where(pos < sinks, pos, sinks + (pos - sinks) % ring)
+                assert torch.equal(kc[b][:, slot].transpose(0, 1), kp[0, b, pos])
+                assert torch.equal(vc[b][:, slot].transpose(0, 1), vp[0, b, pos])
+    assert total > 4
