@@ -484,8 +484,9 @@ MAGICDEC_API size_t magicdec_tree_attn_workspace_size(magicdec_paged_shape shape
  * Pool rows outside [0, len + n_nodes) may hold anything, NaN included; a node's
  * own rows reach it and its descendants only, whatever they hold.  A page outside
  * the pool counts as keys and values of zero (device error 5).
- * Supported: n <= 256, H_q/H_kv <= 128, and below 4 rows a page fewer than INT_MAX
- * rows in the pool (MAGICDEC_ERR_UNSUPPORTED beyond).
+ * Supported: n <= 256, H_q/H_kv <= 128, below 4 rows a page fewer than INT_MAX rows
+ * in the pool, and a capacity whose tiles of 128 keys, counted for every KV head and
+ * every 128 H_kv / H_q nodes, fit 32 bits (MAGICDEC_ERR_UNSUPPORTED beyond).
  * Errors: NULL pointers, bad shape, n <= 0, alignment, workspace too small.
  */
 MAGICDEC_API magicdec_status magicdec_tree_attn(magicdec_paged_shape shape, int n, const uint16_t *q,

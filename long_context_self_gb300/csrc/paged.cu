@@ -73,12 +73,13 @@ __device__ __forceinline__ void turn_halves(uint32_t &x, uint32_t &y, float2 c0,
 // A CTA of NT threads takes a token, LR = d / 16 lanes one of its head rows (q, k and v rows
 // of d channels) at a time, two 16-byte vectors a lane: the two whose channels are rotated
 // with one another, or two neighbours.  A lane keeps to its channels, so its 8 angles stay in
-// registers for all rows (read from shared memory for every row, they bounded the kernel: 35 us
-// for 4096 tokens of 48 rows).  The first rows' loads are under way while the lengths, the
+// registers for all rows (read from shared memory for every row, they bounded the kernel: twice
+// the time for 4096 tokens of 48 rows).  The first rows' loads are under way while the lengths, the
 // table, the tree and the angles (once per token) are read and computed.  Bound: HBM,
 // 4 (H_q + 2 H_kv) d bytes a token.  Small CTAs, because what a token needs first is a chain of
-// loads that only other CTAs' rows can cover: 4096 tokens in CTAs of 64, 128 or 256 threads (1, 2
-// or 4 tokens) take 17.7, 21.1 and 23.9 us, of 14.9 us at the measured copy rate.
+// loads that only other CTAs' rows can cover: 4096 tokens, each in a CTA of 64, 128 or 256
+// threads, take 21.5, 23.0 and 38.0 us with inputs from HBM, 17.7, 19.5 and 34.2 with inputs in
+// L2, of 14.9 us at the measured copy rate.
 template <int NT, int LR, bool INTER>
 __global__ void __launch_bounds__(NT) paged_append_kernel(const AppendParams p) {
     constexpr int ROWS = NT / LR;               // rows of a pass
@@ -220,7 +221,7 @@ magicdec_status launch_paged_append(const magicdec_paged_shape &s, int n, const 
     p.n_pages = s.n_pages;
     p.max_pages = s.max_pages;
     // Larger CTAs while there are fewer tokens than SMs: then a token's own rows take longest (one
-    // token of 48 rows: 2.7 us with 256 threads, 3.7 us with 64).
+    // token of 48 rows: 2.7 us with 256 threads, 3.5 us with 64).
     if ((long long)s.B * n >= magicdec_host::sm_count())
         return s.d == 128 ? launch_append_t<64, 8>(p, interleaved, st) : launch_append_t<64, 4>(p, interleaved, st);
     return s.d == 128 ? launch_append_t<256, 8>(p, interleaved, st) : launch_append_t<256, 4>(p, interleaved, st);

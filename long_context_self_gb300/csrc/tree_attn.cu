@@ -288,7 +288,7 @@ __device__ __noinline__ uint32_t seen(int prefix, int rows, int node, const uint
 // (take_out), and a run whose CTA met any adds them, of the nodes that a row does see, to the
 // row's sums at its end, from the pool (add_back): a product with a probability above zero is
 // the same infinity, or NaN.  What it costs the tiles that are looked through (ragged d = 64,
-// 24 entries of up to 9k: 68.7 -> 70.0 us; chain of 200 over 8k: 220 -> 224; others nothing) is
+// 24 sequences of up to 9k: 65.9 -> 67.4 us; chain of 200 over 8k: 225.1 -> 227.6; others nothing) is
 // mostly behind the softmax of their first half, while their V arrives.
 
 // Whether either bf16 of a word is not finite: 0x8000 in its place, else 0.
