@@ -72,6 +72,9 @@ def test_attention_rows_that_leave_warps_part_empty(H_q, H_kv, d, n, page):
     (32, 8, 128, 64, [2000, 64, 0], 16, "random", [64, 33, 50]),
     (16, 4, 128, 256, [700, 5], 256, "random", None),                      # several pairs of row tiles
     (8, 8, 64, 200, [250], 16, None, None),
+    # many entries a CTA, with one row tile, and with two of which the second is often empty
+    (8, 2, 128, 20, [b * 37 % 300 for b in range(300)], 16, "random", [b * 29 % 21 for b in range(300)]),
+    (8, 2, 64, 48, [b * 37 % 300 for b in range(300)], 24, "random", [b * 29 % 49 for b in range(300)]),
 ])
 def test_attention_values_that_a_node_does_not_see(H_q, H_kv, d, n, lens, page, tree, counts):
     """A node's keys and values reach itself and its descendants only, whatever they are: infinities
