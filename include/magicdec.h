@@ -466,6 +466,34 @@ MAGICDEC_API magicdec_status magicdec_paged_append(magicdec_paged_shape shape, i
                                                    uint16_t *q_out, uint16_t *k_pages, uint16_t *v_pages,
                                                    void *stream);
 
+/*
+ * Append as magicdec_paged_append, for models that norm every query and key head before
+ * the rotation, and for tokens whose positions have several axes (time, height and width
+ * of images and video).  A query head x becomes x / sqrt(mean(x^2) + eps) * q_weight over
+ * its d channels, a key head likewise with k_weight, then is rotated; norm and rotation
+ * in fp32, with one rounding to bf16 at the end.
+ *   q_weight, k_weight (nullable, each) [d] bf16: NULL leaves the query (key) heads as
+ *            they are
+ *   eps      above zero and finite, if there is a weight
+ *   pos      (nullable) [B, n, n_axes] int32: token i of sequence b has these positions
+ *            instead of those counted from len; not with parent.  Slots go by len as before
+ *   axis     (nullable if n_axes == 1) [rot_dim / 2] int32: pair f turns by the angle
+ *            pos[b, i, axis[f]] * inv_freq[f]; an entry outside [0, n_axes) counts as 0 (and,
+ *            in the range-checking build, sets error 4)
+ * Everything else as there, the errors too; further ones: MAGICDEC_ERR_NULL for n_axes > 1
+ * without axis, MAGICDEC_ERR_SHAPE for eps not above zero or not finite beside a weight, pos
+ * together with parent, n_axes <= 0 with pos, or axis without pos, MAGICDEC_ERR_ALIGN for
+ * weights off a 16-byte boundary, MAGICDEC_ERR_UNSUPPORTED for n_axes > 64.
+ */
+MAGICDEC_API magicdec_status magicdec_norm_append(magicdec_paged_shape shape, int n, const uint16_t *q,
+                                                  long long q_stride, const uint16_t *k, long long k_stride,
+                                                  const uint16_t *v, long long v_stride, const uint16_t *q_weight,
+                                                  const uint16_t *k_weight, float eps, const int32_t *len,
+                                                  const int32_t *n_new, const int32_t *parent, const int32_t *pos,
+                                                  int n_axes, const int32_t *axis, const float *inv_freq, int rot_dim,
+                                                  int interleaved, const int32_t *block_table, uint16_t *q_out,
+                                                  uint16_t *k_pages, uint16_t *v_pages, void *stream);
+
 /* Workspace bytes magicdec_tree_attn needs for this shape and node count on the
  * current device (0 for a shape that it refuses). */
 MAGICDEC_API size_t magicdec_tree_attn_workspace_size(magicdec_paged_shape shape, int n);
@@ -494,6 +522,41 @@ MAGICDEC_API magicdec_status magicdec_tree_attn(magicdec_paged_shape shape, int 
                                                 const int32_t *block_table, const int32_t *len,
                                                 const int32_t *n_nodes, const int32_t *parent, uint16_t *out, void *ws,
                                                 size_t ws_bytes, void *stream);
+
+/* Workspace bytes magicdec_prefix_attn needs for this shape, number of prefixes and node
+ * count on the current device (0 for a shape that it refuses). */
+MAGICDEC_API size_t magicdec_prefix_attn_workspace_size(magicdec_paged_shape shape, int n_prefixes, int n);
+
+/*
+ * Attention as magicdec_tree_attn for a batch whose sequences share long prefixes (samples of
+ * one prompt, a system prompt of all): a prefix's keys and values are read once for all
+ * sequences behind it.  The sequences [first[g], first[g+1]) follow prefix g, which is the
+ * prefix_len[g] positions of the pages prefix_table[g]; each one's own slots, counted from 0, are
+ * those of block_table, and len, n_nodes and parent are as in magicdec_tree_attn.  Node i of
+ * sequence b attends to its prefix, to its own positions [0, len[b]), and to the slots of its
+ * ancestors and itself.  Keys are taken as they are: rotate them (magicdec_norm_append with pos,
+ * magicdec_paged_append) by the position that counts the prefix in.
+ *   prefix_table [n_prefixes, max_prefix_pages] int32, of the same pool;  prefix_len [n_prefixes]
+ *            int32, clamped to [0, page_size * max_prefix_pages]
+ *   first    [n_prefixes + 1] int32, ascending, clamped to [0, B]; sequences outside all groups
+ *            have no prefix; NULL with n_prefixes == 1: all sequences follow the one prefix.  Of
+ *            entries that do not ascend the rows come out unspecified
+ *   q   [B, n, H_q, d] bf16;  out [B, n, H_q, d] bf16: rows of nodes i >= n_nodes[b] are zero, as
+ *       is a row that sees nothing
+ *   ws  workspace of magicdec_prefix_attn_workspace_size(shape, n_prefixes, n) bytes; no initial
+ *       contents needed
+ * Pool rows that no node sees may hold anything, and a node's own rows reach it and its descendants only;
+ * a page outside the pool counts as keys and values of zero (device error 5).
+ * Supported, errors: as magicdec_tree_attn, the prefixes' capacity and their tiles with those of all
+ * B n nodes included; n_prefixes at most 4096, one unless first is given; MAGICDEC_ERR_SHAPE for
+ * n_prefixes <= 0 or max_prefix_pages <= 0.
+ */
+MAGICDEC_API magicdec_status magicdec_prefix_attn(magicdec_paged_shape shape, int n_prefixes, int max_prefix_pages, int n,
+                                                  const uint16_t *q, const uint16_t *k_pages, const uint16_t *v_pages,
+                                                  const int32_t *prefix_table, const int32_t *prefix_len,
+                                                  const int32_t *first, const int32_t *block_table,
+                                                  const int32_t *len, const int32_t *n_nodes, const int32_t *parent,
+                                                  uint16_t *out, void *ws, size_t ws_bytes, void *stream);
 
 /*
  * Greedy acceptance down the tree.  From node u = 0: t = argmax target[b, u], ties
@@ -530,6 +593,62 @@ MAGICDEC_API magicdec_status magicdec_tree_commit(magicdec_paged_shape shape, in
                                                   const int32_t *path, const int32_t *n_acc,
                                                   const int32_t *block_table, uint16_t *k_pages, uint16_t *v_pages,
                                                   void *stream);
+
+/*
+ * A draft cache that keeps its heavy hitters (no counterpart in the paper, which drafts over
+ * static selections: the rows kept here follow what the attention finds heavy while it
+ * drafts).  Rows of K and V lie in kc, vc [B, H_kv, cap, d] as in the compact draft cache,
+ * draft_len[b] of them in use, in any order; beside each row its accumulated attention
+ * weight, weight [B, H_kv, cap] fp32, and the position of its token, pos [B, H_kv, cap]
+ * int32.  A step appends a token's rows behind the others (magicdec_draft_cache_update),
+ * attends with magicdec_heavy_attn, and, when the rows have outgrown the budget, drops those
+ * of least weight with magicdec_heavy_evict.
+ */
+
+/*
+ * Attention of n_q query tokens over the draft cache, whose last n_q rows are the tokens'
+ * own; every row's weight grows by the attention that it got.  Token i sees rows
+ * 0 .. len - n_q + i, len = draft_len[b] clamped to [0, cap]; softmax scale 1/sqrt(d); query
+ * head hq reads KV head hq / (H_q/H_kv).  weight[b, h, j] += the probabilities of row j
+ * summed over the tokens and the H_q/H_kv query heads of KV head h.
+ *   q [B, n_q, H_q, d] bf16;  kc, vc [B, H_kv, cap, d] bf16;  shape.L_cap is cap
+ *   out [B, n_q, H_q, d] bf16: zero rows for tokens that see nothing
+ *   next_pos (nullable) [B] int32: the last n_q rows are new: what weight and pos hold there
+ *            is replaced, pos by next_pos[b] + i, the weight by this call's alone.  NULL: pos is not
+ *            looked at (and may be NULL), and all weights are added to
+ * Rows at or past len may hold anything, NaN included, and are left as they are; a token's own
+ * row reaches it and later tokens only, whatever it holds.  Probabilities are summed in fp32, in
+ * an order that is the same from run to run.
+ * Supported: (H_q/H_kv) * n_q <= 32, and rows whose scores, 4 (H_q/H_kv) n_q bytes each, fit
+ * the shared memory of 16 CTAs (a cap of 229,888 for 4 query rows, of 28,672 for 32;
+ * MAGICDEC_ERR_UNSUPPORTED beyond).
+ * Errors: NULL pointers, bad shape, n_q <= 0, alignment (q, kc, vc, out).
+ */
+MAGICDEC_API magicdec_status magicdec_heavy_attn(magicdec_kv_shape shape, int n_q, const uint16_t *q,
+                                                 const uint16_t *kc, const uint16_t *vc, const int32_t *draft_len,
+                                                 const int32_t *next_pos, float *weight, int32_t *pos, uint16_t *out,
+                                                 void *stream);
+
+/*
+ * Eviction, all layers in one call: of every (layer, sequence, KV head) with more than
+ * `budget` rows, `budget` stay: those whose position is below n_sink or at least
+ * seq_len[b] - n_recent, and of the others the ones of largest weight (equal weights: the
+ * smaller position, then the smaller row; protected rows count as of infinite weight).
+ * Rows that stay and lie at or past the budget move, in ascending order, into the places below
+ * it of rows that went, with their weight and position; all others stay where they are.
+ *   kc, vc [layers, B, H_kv, cap, d] bf16, weight, pos [layers, B, H_kv, cap]; shape.L_cap is
+ *   cap, shape.H_q is not looked at beyond being a multiple of H_kv
+ *   draft_len [B] int32, for all layers;  seq_len [B] int32: positions of the sequence so far
+ *   draft_len_out [B] int32 out: min(draft_len clamped to [0, cap], budget); not draft_len itself
+ * What rows at or past the new length hold is left as it was.  No weight may be NaN.
+ * Errors: NULL pointers, bad shape, layers <= 0, budget <= 0, n_sink or n_recent < 0, or their
+ * sum above the budget, draft_len_out == draft_len, alignment (kc, vc);
+ * MAGICDEC_ERR_UNSUPPORTED when layers > 65535 or cap > 1048576.
+ */
+MAGICDEC_API magicdec_status magicdec_heavy_evict(magicdec_kv_shape shape, int layers, const int32_t *draft_len,
+                                                  const int32_t *seq_len, int budget, int n_sink, int n_recent,
+                                                  uint16_t *kc, uint16_t *vc, float *weight, int32_t *pos,
+                                                  int32_t *draft_len_out, void *stream);
 
 #ifdef __cplusplus
 }

@@ -47,6 +47,7 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _L = ctypes.c_longlong
 _S = ctypes.c_size_t
+_F = ctypes.c_float
 
 _SIGNATURES = {
     "magicdec_status_string": ([_I], ctypes.c_char_p),
@@ -71,10 +72,16 @@ _SIGNATURES = {
     "magicdec_spec_accept_workspace_size": ([_I, _I, _I], _S),
     "magicdec_spec_accept": ([_I, _I, _I, _P, _P, _P, _P, _P, _I, _P, _P, _P, _P, _S, _P], _I),
     "magicdec_paged_append": ([PagedShape, _I, _P, _L, _P, _L, _P, _L, _P, _P, _P, _P, _I, _I, _P, _P, _P, _P, _P], _I),
+    "magicdec_norm_append": ([PagedShape, _I, _P, _L, _P, _L, _P, _L, _P, _P, _F, _P, _P, _P, _P, _I, _P, _P, _I, _I, _P,
+                              _P, _P, _P, _P], _I),
     "magicdec_tree_attn_workspace_size": ([PagedShape, _I], _S),
     "magicdec_tree_attn": ([PagedShape, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S, _P], _I),
+    "magicdec_prefix_attn_workspace_size": ([PagedShape, _I, _I], _S),
+    "magicdec_prefix_attn": ([PagedShape, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S, _P], _I),
     "magicdec_tree_accept": ([_I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P], _I),
     "magicdec_tree_commit": ([PagedShape, _I, _I, _P, _P, _P, _P, _P, _P, _P], _I),
+    "magicdec_heavy_attn": ([KVShape, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P], _I),
+    "magicdec_heavy_evict": ([KVShape, _I, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P], _I),
 }
 
 EXPORTED = tuple(_SIGNATURES)
@@ -601,6 +608,7 @@ def paged_shape(B, H_q, H_kv, d, page_size, n_pages, max_pages) -> PagedShape:
 
 
 _paged = functools.lru_cache(maxsize=1024)(PagedShape)         # passed by value, never written
+_kv = functools.lru_cache(maxsize=1024)(KVShape)
 
 
 def _fits(name, size) -> None:
@@ -643,19 +651,9 @@ def _tokens(t, name, dev, B, n, d):
     return H, stride
 
 
-def magicdec_paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
-                          block_table: torch.Tensor, seq_len: torch.Tensor, inv_freq: Optional[torch.Tensor] = None,
-                          q: Optional[torch.Tensor] = None, n_new: Optional[torch.Tensor] = None,
-                          parent: Optional[torch.Tensor] = None, interleaved: bool = False,
-                          q_out: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
-    """Append k, v [B, n, H_kv, d] (token-strided views allowed) at slots seq_len + i of the paged cache
-    k_pages / v_pages [n_pages, page_size, H_kv, d], k rotated by inv_freq [rot_dim / 2] fp32 (None: not);
-    q [B, n, H_q, d] is rotated into q_out, which is returned (None without q)."""
-    dev = _cuda_device(k, "k", _BF16)
-    if stream is not None or _current_device() != dev.index:
-        with _on(dev, stream):
-            return magicdec_paged_append(k, v, k_pages, v_pages, block_table, seq_len, inv_freq, q, n_new, parent,
-                                         interleaved, q_out)
+def _append_args(k, v, k_pages, v_pages, block_table, seq_len, inv_freq, q, n_new, parent, q_out, dev):
+    """Checks of what both appends take: (shape, n, (q, stride, k, stride, v, stride), (len, n_new, parent),
+    (inv_freq, rot_dim), table, q_out's address, kp, vp, q_out)."""
     if k.dim() != 4:
         raise ValueError("k must be [B, n, H_kv, d]")
     B, n, H_kv, d = k.shape
@@ -680,11 +678,65 @@ def magicdec_paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tenso
         rot = inv_freq.numel()
         inv = _at(inv_freq, "inv_freq", _F32, dev, (rot,))
         rot *= 2
+    return (_paged(B, H_q, H_kv, d, page_size, n_pages, max_pages), n,
+            (qp, qs, k.data_ptr(), ks, v.data_ptr(), vs),
+            (_at(seq_len, "seq_len", _I32, dev, (B,)), None if n_new is None else _at(n_new, "n_new", _I32, dev, (B,)),
+             None if parent is None else _at(parent, "parent", _I32, dev, (B, n))), (inv, rot), table, qo, kp, vp, q_out)
+
+
+def magicdec_paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                          block_table: torch.Tensor, seq_len: torch.Tensor, inv_freq: Optional[torch.Tensor] = None,
+                          q: Optional[torch.Tensor] = None, n_new: Optional[torch.Tensor] = None,
+                          parent: Optional[torch.Tensor] = None, interleaved: bool = False,
+                          q_out: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """Append k, v [B, n, H_kv, d] (token-strided views allowed) at slots seq_len + i of the paged cache
+    k_pages / v_pages [n_pages, page_size, H_kv, d], k rotated by inv_freq [rot_dim / 2] fp32 (None: not);
+    q [B, n, H_q, d] is rotated into q_out, which is returned (None without q)."""
+    dev = _cuda_device(k, "k", _BF16)
+    if stream is not None or _current_device() != dev.index:
+        with _on(dev, stream):
+            return magicdec_paged_append(k, v, k_pages, v_pages, block_table, seq_len, inv_freq, q, n_new, parent,
+                                         interleaved, q_out)
+    shape, n, rows, seq, rope, table, qo, kp, vp, q_out = _append_args(k, v, k_pages, v_pages, block_table, seq_len,
+                                                                       inv_freq, q, n_new, parent, q_out, dev)
     _check("magicdec_paged_append", (_lib or lib()).magicdec_paged_append(
-        _paged(B, H_q, H_kv, d, page_size, n_pages, max_pages), n, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs,
-        _at(seq_len, "seq_len", _I32, dev, (B,)), None if n_new is None else _at(n_new, "n_new", _I32, dev, (B,)),
-        None if parent is None else _at(parent, "parent", _I32, dev, (B, n)), inv, rot, 1 if interleaved else 0, table,
-        qo, kp, vp, _raw_stream(dev.index)))
+        shape, n, *rows, *seq, *rope, 1 if interleaved else 0, table, qo, kp, vp, _raw_stream(dev.index)))
+    return q_out
+
+
+def magicdec_norm_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                         block_table: torch.Tensor, seq_len: torch.Tensor, inv_freq: Optional[torch.Tensor] = None,
+                         q: Optional[torch.Tensor] = None, q_weight: Optional[torch.Tensor] = None,
+                         k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                         n_new: Optional[torch.Tensor] = None, parent: Optional[torch.Tensor] = None,
+                         pos: Optional[torch.Tensor] = None, axis: Optional[torch.Tensor] = None,
+                         interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+                         stream=None) -> Optional[torch.Tensor]:
+    """magicdec_paged_append with every query and key head normed before the rotation (x / rms(x) times
+    q_weight / k_weight [d] bf16; None: not) and, with pos [B, n] or [B, n, axes] int32, turned by these
+    positions: pair f by pos[..., axis[f]] * inv_freq[f], axis [rot_dim / 2] int32."""
+    dev = _cuda_device(k, "k", _BF16)
+    if stream is not None or _current_device() != dev.index:
+        with _on(dev, stream):
+            return magicdec_norm_append(k, v, k_pages, v_pages, block_table, seq_len, inv_freq, q, q_weight, k_weight,
+                                        eps, n_new, parent, pos, axis, interleaved, q_out)
+    shape, n, rows, seq, rope, table, qo, kp, vp, q_out = _append_args(k, v, k_pages, v_pages, block_table, seq_len,
+                                                                       inv_freq, q, n_new, parent, q_out, dev)
+    d = (shape.d,)
+    axes, pp, ap = 0, None, None
+    if pos is not None:
+        at = getattr(pos, "shape", ())
+        if len(at) not in (2, 3):
+            raise ValueError("pos must be [B, n] or [B, n, axes]")
+        axes = at[2] if len(at) == 3 else 1
+        _fits("axes", axes)
+        pp = _at(pos, "pos", _I32, dev, (shape.B, n, axes)[:len(at)])
+    if axis is not None:
+        ap = _at(axis, "axis", _I32, dev, (rope[1] // 2,))
+    _check("magicdec_norm_append", (_lib or lib()).magicdec_norm_append(
+        shape, n, *rows, None if q_weight is None else _at(q_weight, "q_weight", _BF16, dev, d),
+        None if k_weight is None else _at(k_weight, "k_weight", _BF16, dev, d), eps, *seq, pp, axes, ap, *rope,
+        1 if interleaved else 0, table, qo, kp, vp, _raw_stream(dev.index)))
     return q_out
 
 
@@ -734,6 +786,64 @@ def magicdec_tree_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Te
     return out
 
 
+def magicdec_prefix_attn_workspace_size(shape: PagedShape, n_prefixes: int, n: int) -> int:
+    return int(lib().magicdec_prefix_attn_workspace_size(shape, int(n_prefixes), int(n)))
+
+
+@functools.lru_cache(maxsize=256)
+def _prefix_ws_bytes(device_index, *args) -> int:
+    return max(256, magicdec_prefix_attn_workspace_size(PagedShape(*args[:-2]), *args[-2:]))
+
+
+def magicdec_prefix_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, prefix_table: torch.Tensor,
+                         prefix_len: torch.Tensor, block_table: torch.Tensor, seq_len: torch.Tensor,
+                         first: Optional[torch.Tensor] = None, parent: Optional[torch.Tensor] = None,
+                         n_nodes: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                         ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """magicdec_tree_attn for sequences behind shared prefixes: sequences first[g] .. first[g+1] - 1 (first [P + 1]
+    int32; None: all of them, behind the one prefix) also see the prefix_len[g] positions of the pages
+    prefix_table[g] ([P, max_prefix_pages] int32), which are read once for all of them; seq_len, block_table,
+    parent and n_nodes are of their own slots behind it -> out [B, n, H_q, d] bf16."""
+    dev = _cuda_device(q, "q", _BF16)
+    if stream is not None or _current_device() != dev.index:
+        with _on(dev, stream):
+            return magicdec_prefix_attn(q, k_pages, v_pages, prefix_table, prefix_len, block_table, seq_len, first,
+                                        parent, n_nodes, out, ws)
+    qs = q.shape
+    if len(qs) != 4:
+        raise ValueError("q must be [B, n, H_q, d]")
+    B, n, H_q, d = qs
+    kp, vp, table, page_size, n_pages, max_pages, H_kv, d_c = _paged_cache(k_pages, v_pages, block_table, B, dev)
+    if d_c != d:
+        raise ValueError("q and k_pages disagree: q [B, n, H_q, d], k_pages [n_pages, page_size, H_kv, d]")
+    ps = getattr(prefix_table, "shape", ())
+    if len(ps) != 2:
+        raise ValueError("prefix_table must be [P, max_prefix_pages]")
+    P, most = ps
+    _fits("P", P)
+    _fits("max_prefix_pages", most)
+    if first is None and P != 1:
+        raise ValueError("several prefixes need first")
+    qp, pt = _at(q, "q", _BF16, dev, qs), _at(prefix_table, "prefix_table", _I32, dev, ps)
+    plen, length = _at(prefix_len, "prefix_len", _I32, dev, (P,)), _at(seq_len, "seq_len", _I32, dev, (B,))
+    fp = None if first is None else _at(first, "first", _I32, dev, (P + 1,))
+    par = None if parent is None else _at(parent, "parent", _I32, dev, (B, n))
+    count = None if n_nodes is None else _at(n_nodes, "n_nodes", _I32, dev, (B,))
+    if out is None:
+        out = torch.empty(qs, dtype=_BF16, device=dev)
+    op = _at(out, "out", _BF16, dev, qs)
+    if ws is None:
+        # No contents are kept between calls, so it comes from torch's allocator each time.
+        ws = torch.empty(_prefix_ws_bytes(dev.index, B, H_q, H_kv, d, page_size, n_pages, max_pages, P, n),
+                         dtype=torch.uint8, device=dev)
+    elif ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous and on {dev}")
+    _check("magicdec_prefix_attn", (_lib or lib()).magicdec_prefix_attn(
+        _paged(B, H_q, H_kv, d, page_size, n_pages, max_pages), P, most, n, qp, kp, vp, pt, plen, fp, table, length, count,
+        par, op, ws.data_ptr(), ws.nbytes, _raw_stream(dev.index)))
+    return out
+
+
 def magicdec_tree_accept(target: torch.Tensor, tok: torch.Tensor, parent: Optional[torch.Tensor] = None,
                          n_nodes: Optional[torch.Tensor] = None, n_acc: Optional[torch.Tensor] = None,
                          path: Optional[torch.Tensor] = None, out_tok: Optional[torch.Tensor] = None, stream=None):
@@ -780,3 +890,75 @@ def magicdec_tree_commit(k_pages: torch.Tensor, v_pages: torch.Tensor, block_tab
         _paged(B, H_kv, H_kv, d, page_size, n_pages, max_pages), n, k_pages.shape[0] if k_pages.dim() == 5 else 1,
         _at(seq_len, "seq_len", _I32, dev, (B,)), _at(path, "path", _I32, dev, (B, n)),
         _at(n_acc, "n_acc", _I32, dev, (B,)), table, kp, vp, _raw_stream(dev.index)))
+
+
+# ------------------------------------------- draft cache that keeps its heavy hitters
+def _draft_cache(kc, vc, weight, pos, dev, dims=4):
+    """Checks of a draft cache kc, vc [.., B, H_kv, cap, d] and its rows' weights and positions; their
+    addresses (pos may be None) and the shape."""
+    shape = getattr(kc, "shape", ())
+    if len(shape) != 4 and len(shape) != dims:
+        raise ValueError(f"kc must be [B, H_kv, cap, d]{' or [layers, ...]' if dims == 5 else ''}")
+    if max(shape) > 0x7FFFFFFF:
+        for i, x in enumerate(shape):
+            _fits(f"kc.shape[{i}]", x)
+    return (_at(kc, "kc", _BF16, dev, shape), _at(vc, "vc", _BF16, dev, shape),
+            _at(weight, "weight", _F32, dev, shape[:-1]),
+            None if pos is None else _at(pos, "pos", _I32, dev, shape[:-1]), shape)
+
+
+def magicdec_heavy_attn(q: torch.Tensor, kc: torch.Tensor, vc: torch.Tensor, weight: torch.Tensor,
+                        draft_len: torch.Tensor, pos: Optional[torch.Tensor] = None,
+                        next_pos: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                        stream=None) -> torch.Tensor:
+    """q [B, n, H_q, d] over the draft cache kc, vc [B, H_kv, cap, d], of which draft_len [B] rows are in use
+    and the last n are the tokens' own -> out [B, n, H_q, d] bf16.  weight [B, H_kv, cap] f32 grows, in place, by
+    every row's probabilities; with next_pos [B] the last n rows are new: their weight begins at this call, and
+    their pos [B, H_kv, cap] int32 becomes next_pos + i."""
+    dev = _cuda_device(q, "q", _BF16)
+    if stream is not None or _current_device() != dev.index:
+        with _on(dev, stream):
+            return magicdec_heavy_attn(q, kc, vc, weight, draft_len, pos, next_pos, out)
+    qs = q.shape
+    if len(qs) != 4:
+        raise ValueError("q must be [B, n, H_q, d]")
+    B, n, H_q, d = qs
+    _fits("n", n)
+    _fits("H_q", H_q)
+    kp, vp, wp, pp, (B_c, H_kv, cap, d_c) = _draft_cache(kc, vc, weight, pos, dev)
+    if B_c != B or d_c != d:
+        raise ValueError("q and kc disagree: q [B, n, H_q, d], kc [B, H_kv, cap, d]")
+    if next_pos is not None and pos is None:
+        raise ValueError("next_pos without pos")
+    if out is None:
+        out = torch.empty(qs, dtype=_BF16, device=dev)
+    _check("magicdec_heavy_attn", (_lib or lib()).magicdec_heavy_attn(
+        _kv(B, H_q, H_kv, d, cap), n, _at(q, "q", _BF16, dev, qs), kp, vp, _at(draft_len, "draft_len", _I32, dev, (B,)),
+        None if next_pos is None else _at(next_pos, "next_pos", _I32, dev, (B,)), wp, pp, _at(out, "out", _BF16, dev, qs),
+        _raw_stream(dev.index)))
+    return out
+
+
+def magicdec_heavy_evict(kc: torch.Tensor, vc: torch.Tensor, weight: torch.Tensor, pos: torch.Tensor,
+                         draft_len: torch.Tensor, seq_len: torch.Tensor, budget: int, n_sink: int = 0,
+                         n_recent: int = 0, draft_len_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Evict, in place, the rows of least weight of kc, vc [B, H_kv, cap, d] or [layers, B, H_kv, cap, d] (weight
+    f32 and pos int32 without the last dimension) until `budget` are left; those with pos < n_sink or pos >=
+    seq_len - n_recent stay.  Returns draft_len_out [B] = min(draft_len, budget)."""
+    dev = _cuda_device(kc, "kc", _BF16)
+    if stream is not None or _current_device() != dev.index:
+        with _on(dev, stream):
+            return magicdec_heavy_evict(kc, vc, weight, pos, draft_len, seq_len, budget, n_sink, n_recent, draft_len_out)
+    if pos is None:
+        raise TypeError("pos must be a torch.Tensor")
+    kp, vp, wp, pp, shape = _draft_cache(kc, vc, weight, pos, dev, 5)
+    B, H_kv, cap, d = shape[-4:]
+    for name, x in (("budget", budget), ("n_sink", n_sink), ("n_recent", n_recent)):
+        _fits(name, x)
+    if draft_len_out is None:
+        draft_len_out = torch.empty((B,), dtype=_I32, device=dev)
+    _check("magicdec_heavy_evict", (_lib or lib()).magicdec_heavy_evict(
+        _kv(B, H_kv, H_kv, d, cap), shape[0] if len(shape) == 5 else 1, _at(draft_len, "draft_len", _I32, dev, (B,)),
+        _at(seq_len, "seq_len", _I32, dev, (B,)), int(budget), int(n_sink), int(n_recent), kp, vp, wp, pp,
+        _at(draft_len_out, "draft_len_out", _I32, dev, (B,)), _raw_stream(dev.index)))
+    return draft_len_out

@@ -3,6 +3,7 @@
 // contract of every entry point are in include/magicdec.h.
 #include <cudaTypedefs.h>
 
+#include <cfloat>
 #include <climits>
 #include <cstdlib>
 #include <mutex>
@@ -48,10 +49,22 @@ magicdec_status launch_paged_append(const magicdec_paged_shape &s, int n, const 
                                     const int32_t *len, const int32_t *n_new, const int32_t *parent,
                                     const float *inv_freq, int rot_dim, int interleaved, const int32_t *table,
                                     uint16_t *q_out, uint16_t *kp, uint16_t *vp, cudaStream_t st);
+magicdec_status launch_norm_append(const magicdec_paged_shape &s, int n, const uint16_t *q, long long q_stride,
+                                   const uint16_t *k, long long k_stride, const uint16_t *v, long long v_stride,
+                                   const uint16_t *q_weight, const uint16_t *k_weight, float eps, const int32_t *len,
+                                   const int32_t *n_new, const int32_t *parent, const int32_t *pos, int axes,
+                                   const int32_t *axis, const float *inv_freq, int rot_dim, int interleaved,
+                                   const int32_t *table, uint16_t *q_out, uint16_t *kp, uint16_t *vp, cudaStream_t st);
 size_t tree_attn_workspace_bytes(const magicdec_paged_shape &s, int n);
 magicdec_status launch_tree_attn(const magicdec_paged_shape &s, int n, const uint16_t *q, const uint16_t *kp,
                                  const uint16_t *vp, const int32_t *table, const int32_t *len, const int32_t *n_nodes,
                                  const int32_t *parent, uint16_t *out, void *ws, cudaStream_t st);
+size_t prefix_attn_workspace_bytes(const magicdec_paged_shape &s, int P, int n);
+magicdec_status launch_prefix_attn(const magicdec_paged_shape &s, int P, int pmax, int n, const uint16_t *q,
+                                   const uint16_t *kp, const uint16_t *vp, const int32_t *ptable, const int32_t *plen,
+                                   const int32_t *first, const int32_t *table, const int32_t *len,
+                                   const int32_t *n_nodes, const int32_t *parent, uint16_t *out, void *ws,
+                                   cudaStream_t st);
 magicdec_status launch_tree_accept(int B, int n, int V, const float *target, const int32_t *tok,
                                    const int32_t *parent, const int32_t *n_nodes, int32_t *n_acc, int32_t *path,
                                    int32_t *out_tok, cudaStream_t st);
@@ -59,6 +72,12 @@ magicdec_status launch_tree_commit(const magicdec_paged_shape &s, int n, int lay
                                    const int32_t *path, const int32_t *n_acc, const int32_t *table, uint16_t *kp,
                                    uint16_t *vp, cudaStream_t st);
 
+magicdec_status launch_heavy_attn(int B, int H_q, int H_kv, int D, int cap, int n, const uint16_t *q,
+                                  const uint16_t *k, const uint16_t *v, const int32_t *len, const int32_t *next_pos,
+                                  float *weight, int32_t *pos, uint16_t *out, cudaStream_t st);
+magicdec_status launch_heavy_evict(int layers, int B, int H_kv, int D, int cap, const int32_t *len,
+                                   const int32_t *seq_len, int budget, int n_sink, int n_recent, uint16_t *kc,
+                                   uint16_t *vc, float *weight, int32_t *pos, int32_t *len_out, cudaStream_t st);
 // The library's device error word (one per device that loads the library).
 __device__ int g_error_word;
 }  // namespace magicdec
@@ -393,12 +412,12 @@ magicdec_status magicdec_spec_accept(int B, int gamma, int V, const float *targe
                                         n_acc, out_tok, n_ambiguous, ws, static_cast<cudaStream_t>(stream));
 }
 
-magicdec_status magicdec_paged_append(magicdec_paged_shape shape, int n, const uint16_t *q, long long q_stride,
-                                      const uint16_t *k, long long k_stride, const uint16_t *v, long long v_stride,
-                                      const int32_t *len, const int32_t *n_new, const int32_t *parent,
-                                      const float *inv_freq, int rot_dim, int interleaved,
-                                      const int32_t *block_table, uint16_t *q_out, uint16_t *k_pages,
-                                      uint16_t *v_pages, void *stream) {
+// What both appends refuse.
+static magicdec_status append_args(const magicdec_paged_shape &shape, int n, const uint16_t *q, long long q_stride,
+                                   const uint16_t *k, long long k_stride, const uint16_t *v, long long v_stride,
+                                   const int32_t *len, const int32_t *parent, const float *inv_freq, int rot_dim,
+                                   const int32_t *block_table, const uint16_t *q_out, const uint16_t *k_pages,
+                                   const uint16_t *v_pages) {
     if (!k || !v || !len || !block_table || !k_pages || !v_pages || (!q) != (!q_out) || (rot_dim > 0 && !inv_freq))
         return MAGICDEC_ERR_NULL;
     if (!paged_ok(shape) || n <= 0 || rot_dim < 0 || rot_dim > shape.d || (rot_dim & 1)) return MAGICDEC_ERR_SHAPE;
@@ -408,9 +427,41 @@ magicdec_status magicdec_paged_append(magicdec_paged_shape shape, int n, const u
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_pages) ||
         !aligned16(v_pages) || k_stride % 8 || v_stride % 8 || (q && q_stride % 8))
         return MAGICDEC_ERR_ALIGN;
+    return MAGICDEC_OK;
+}
+
+magicdec_status magicdec_paged_append(magicdec_paged_shape shape, int n, const uint16_t *q, long long q_stride,
+                                      const uint16_t *k, long long k_stride, const uint16_t *v, long long v_stride,
+                                      const int32_t *len, const int32_t *n_new, const int32_t *parent,
+                                      const float *inv_freq, int rot_dim, int interleaved,
+                                      const int32_t *block_table, uint16_t *q_out, uint16_t *k_pages,
+                                      uint16_t *v_pages, void *stream) {
+    const magicdec_status s = append_args(shape, n, q, q_stride, k, k_stride, v, v_stride, len, parent, inv_freq,
+                                          rot_dim, block_table, q_out, k_pages, v_pages);
+    if (s != MAGICDEC_OK) return s;
     return magicdec::launch_paged_append(shape, n, q, q_stride, k, k_stride, v, v_stride, len, n_new, parent, inv_freq,
                                          rot_dim, interleaved, block_table, q_out, k_pages, v_pages,
                                          static_cast<cudaStream_t>(stream));
+}
+
+magicdec_status magicdec_norm_append(magicdec_paged_shape shape, int n, const uint16_t *q, long long q_stride,
+                                     const uint16_t *k, long long k_stride, const uint16_t *v, long long v_stride,
+                                     const uint16_t *q_weight, const uint16_t *k_weight, float eps, const int32_t *len,
+                                     const int32_t *n_new, const int32_t *parent, const int32_t *pos, int n_axes,
+                                     const int32_t *axis, const float *inv_freq, int rot_dim, int interleaved,
+                                     const int32_t *block_table, uint16_t *q_out, uint16_t *k_pages,
+                                     uint16_t *v_pages, void *stream) {
+    const magicdec_status s = append_args(shape, n, q, q_stride, k, k_stride, v, v_stride, len, parent, inv_freq,
+                                          rot_dim, block_table, q_out, k_pages, v_pages);
+    if (s != MAGICDEC_OK) return s;
+    if (pos ? parent || n_axes <= 0 : axis != nullptr) return MAGICDEC_ERR_SHAPE;
+    if (pos && n_axes > 1 && !axis) return MAGICDEC_ERR_NULL;
+    if ((q_weight || k_weight) && !(eps > 0.f && eps <= FLT_MAX)) return MAGICDEC_ERR_SHAPE;
+    if (pos && n_axes > 64) return MAGICDEC_ERR_UNSUPPORTED;
+    if (!aligned16(q_weight) || !aligned16(k_weight)) return MAGICDEC_ERR_ALIGN;
+    return magicdec::launch_norm_append(shape, n, q, q_stride, k, k_stride, v, v_stride, q_weight, k_weight, eps, len,
+                                        n_new, parent, pos, n_axes, axis, inv_freq, rot_dim, interleaved, block_table,
+                                        q_out, k_pages, v_pages, static_cast<cudaStream_t>(stream));
 }
 
 static magicdec_status tree_shape(const magicdec_paged_shape &shape, int n) {
@@ -439,6 +490,32 @@ magicdec_status magicdec_tree_attn(magicdec_paged_shape shape, int n, const uint
                                       static_cast<cudaStream_t>(stream));
 }
 
+size_t magicdec_prefix_attn_workspace_size(magicdec_paged_shape shape, int n_prefixes, int n) {
+    if (tree_shape(shape, n) != MAGICDEC_OK || n_prefixes <= 0 || n_prefixes > 4096) return 0;
+    return magicdec::prefix_attn_workspace_bytes(shape, n_prefixes, n);
+}
+
+magicdec_status magicdec_prefix_attn(magicdec_paged_shape shape, int n_prefixes, int max_prefix_pages, int n,
+                                     const uint16_t *q, const uint16_t *k_pages, const uint16_t *v_pages,
+                                     const int32_t *prefix_table, const int32_t *prefix_len, const int32_t *first,
+                                     const int32_t *block_table, const int32_t *len, const int32_t *n_nodes,
+                                     const int32_t *parent, uint16_t *out, void *ws, size_t ws_bytes, void *stream) {
+    if (!q || !k_pages || !v_pages || !prefix_table || !prefix_len || !block_table || !len || !out || !ws)
+        return MAGICDEC_ERR_NULL;
+    const magicdec_status s = tree_shape(shape, n);
+    if (s != MAGICDEC_OK) return s;
+    if (n_prefixes <= 0 || max_prefix_pages <= 0 || (long long)shape.page_size * max_prefix_pages > INT_MAX - 255)
+        return MAGICDEC_ERR_SHAPE;
+    if (n_prefixes > 1 && !first) return MAGICDEC_ERR_NULL;
+    if (n_prefixes > 4096) return MAGICDEC_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) || !aligned16(ws))
+        return MAGICDEC_ERR_ALIGN;
+    if (ws_bytes < magicdec::prefix_attn_workspace_bytes(shape, n_prefixes, n)) return MAGICDEC_ERR_WORKSPACE;
+    return magicdec::launch_prefix_attn(shape, n_prefixes, max_prefix_pages, n, q, k_pages, v_pages, prefix_table,
+                                        prefix_len, first, block_table, len, n_nodes, parent, out, ws,
+                                        static_cast<cudaStream_t>(stream));
+}
+
 magicdec_status magicdec_tree_accept(int B, int n, int V, const float *target_logits, const int32_t *tok,
                                      const int32_t *parent, const int32_t *n_nodes, int32_t *n_acc, int32_t *path,
                                      int32_t *out_tok, void *stream) {
@@ -458,6 +535,31 @@ magicdec_status magicdec_tree_commit(magicdec_paged_shape shape, int n, int laye
     if (n > kTreeMaxNodes || layers > 65535) return MAGICDEC_ERR_UNSUPPORTED;
     if (!aligned16(k_pages) || !aligned16(v_pages)) return MAGICDEC_ERR_ALIGN;
     return magicdec::launch_tree_commit(shape, n, layers, len, path, n_acc, block_table, k_pages, v_pages,
+                                        static_cast<cudaStream_t>(stream));
+}
+
+magicdec_status magicdec_heavy_attn(magicdec_kv_shape shape, int n_q, const uint16_t *q, const uint16_t *kc,
+                                    const uint16_t *vc, const int32_t *draft_len, const int32_t *next_pos,
+                                    float *weight, int32_t *pos, uint16_t *out, void *stream) {
+    if (!q || !kc || !vc || !draft_len || !weight || !out || (next_pos && !pos)) return MAGICDEC_ERR_NULL;
+    if (!shape_ok(shape) || n_q <= 0) return MAGICDEC_ERR_SHAPE;
+    if ((long long)(shape.H_q / shape.H_kv) * n_q > 32 || shape.H_kv > 65535) return MAGICDEC_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(kc) || !aligned16(vc) || !aligned16(out)) return MAGICDEC_ERR_ALIGN;
+    return magicdec::launch_heavy_attn(shape.B, shape.H_q, shape.H_kv, shape.d, shape.L_cap, n_q, q, kc, vc, draft_len,
+                                       next_pos, weight, pos, out, static_cast<cudaStream_t>(stream));
+}
+
+magicdec_status magicdec_heavy_evict(magicdec_kv_shape shape, int layers, const int32_t *draft_len,
+                                     const int32_t *seq_len, int budget, int n_sink, int n_recent, uint16_t *kc,
+                                     uint16_t *vc, float *weight, int32_t *pos, int32_t *draft_len_out, void *stream) {
+    if (!draft_len || !seq_len || !kc || !vc || !weight || !pos || !draft_len_out) return MAGICDEC_ERR_NULL;
+    if (!shape_ok(shape) || layers <= 0 || budget <= 0 || n_sink < 0 || n_recent < 0 ||
+        (long long)n_sink + n_recent > budget || draft_len_out == draft_len)
+        return MAGICDEC_ERR_SHAPE;
+    if (layers > 65535) return MAGICDEC_ERR_UNSUPPORTED;
+    if (!aligned16(kc) || !aligned16(vc)) return MAGICDEC_ERR_ALIGN;
+    return magicdec::launch_heavy_evict(layers, shape.B, shape.H_kv, shape.d, shape.L_cap, draft_len, seq_len, budget,
+                                        n_sink, n_recent, kc, vc, weight, pos, draft_len_out,
                                         static_cast<cudaStream_t>(stream));
 }
 

@@ -1,10 +1,11 @@
-// paged.cu -- appending rotated keys and values to a paged KV cache, and moving
-// the rows of an accepted path to their final slots (sm_103a).
+// paged.cu -- appending rotated (and normed) keys and values to a paged KV cache, and
+// moving the rows of an accepted path to their final slots (sm_103a).
 //
 // A cache is a pool [n_pages, page_size, H_kv, d] and a block table
 // [B, max_pages]: position s of sequence b is row s % page_size of page
 // table[b, s / page_size].  A dense cache [B, L_cap, H_kv, d] is the pool with
 // page_size = L_cap, max_pages = 1 and table[b, 0] = b.
+#include <cfloat>
 #include <climits>
 
 #include "common.cuh"
@@ -52,6 +53,11 @@ struct AppendParams {
     uint16_t *q_out, *kp, *vp;
     int *err;
     int B, n, H_q, H_kv, d, rot, page_size, n_pages, max_pages;
+    // of the normed form
+    const uint16_t *qw, *kw;         // [d] weights of the norms, or NULL: heads not normed
+    const int32_t *pos, *axis;       // [B, n, axes] positions, or NULL; [rot / 2] axis of a pair, or NULL: axis 0
+    float eps;
+    int axes;
 };
 
 __device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }
@@ -70,6 +76,46 @@ __device__ __forceinline__ void turn_halves(uint32_t &x, uint32_t &y, float2 c0,
     y = pack_bf16(a0 * c0.y + b0 * c0.x, a1 * c1.y + b1 * c1.x);
 }
 
+// The 16 channels of two words of 8, in fp32.
+__device__ __forceinline__ void unpack16(uint4 y, uint4 z, float (&f)[16]) {
+    const uint32_t w[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        f[2 * k] = bf_lo(w[k]);
+        f[2 * k + 1] = bf_hi(w[k]);
+    }
+}
+
+// Squares of a head's d channels, summed over its LR lanes of 16 channels each.
+template <int LR>
+__device__ __forceinline__ float squares(const float (&f)[16], unsigned lanes) {
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) s = fmaf(f[k], f[k], s);
+#pragma unroll
+    for (int o = LR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(lanes, s, o);
+    return s;
+}
+
+// x / sqrt(mean(x^2) + eps) * w over a head's channels, this lane's 16 of them, in fp32 (the one
+// rounding to bf16 comes behind the rotation).  Heads whose squares leave fp32 are scaled down
+// first: eps, at most 2^128, is nothing beside them.
+template <int LR>
+__device__ __forceinline__ void norm_head(float (&f)[16], uint4 w0, uint4 w1, float eps, unsigned lanes) {
+    float s = squares<LR>(f, lanes), e = eps;
+    if (s > FLT_MAX) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) f[k] *= 0x1p-70f;
+        s = squares<LR>(f, lanes);
+        e *= 0x1p-140f;
+    }
+    const float inv = rsqrtf(fmaf(s, 1.f / (LR * 16), e));
+    float w[16];
+    unpack16(w0, w1, w);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) f[k] *= inv * w[k];
+}
+
 // A CTA of NT threads takes a token, LR = d / 16 lanes one of its head rows (q, k and v rows
 // of d channels) at a time, two 16-byte vectors a lane: the two whose channels are rotated
 // with one another, or two neighbours.  A lane keeps to its channels, so its 8 angles stay in
@@ -80,7 +126,10 @@ __device__ __forceinline__ void turn_halves(uint32_t &x, uint32_t &y, float2 c0,
 // loads that only other CTAs' rows can cover: 4096 tokens, each in a CTA of 64, 128 or 256
 // threads, take 21.5, 23.0 and 38.0 us with inputs from HBM, 17.7, 19.5 and 34.2 with inputs in
 // L2, of 14.9 us at the measured copy rate.
-template <int NT, int LR, bool INTER>
+//
+// NORM: query and key heads are normed before the rotation, in the registers that hold them: a
+// lane's 16 squares and log2(LR) shuffles a row, beside loads that bound the kernel as before.
+template <int NT, int LR, bool INTER, bool NORM>
 __global__ void __launch_bounds__(NT) paged_append_kernel(const AppendParams p) {
     constexpr int ROWS = NT / LR;               // rows of a pass
     constexpr int AHEAD = 3;                    // passes loaded together
@@ -140,7 +189,12 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const AppendParams p) 
     // lose the low bits of the turn: the product in turns is formed and reduced in
     // fp64, and the fraction handed to the fp32 sine and cosine.
     for (int f = tid; f < p.rot / 2; f += NT) {
-        const double turns = ((double)len + at) * ((double)ld_dep_f(p.inv_freq + f) * 0.15915494309189535);
+        double where = (double)len + at;
+        if (NORM && p.pos) {
+            const int ax = p.axis ? checked(ld_dep(p.axis + f), 0, p.axes - 1, p.err) : 0;
+            where = ld_dep(p.pos + tok * p.axes + (ax < 0 || ax >= p.axes ? 0 : ax));
+        }
+        const double turns = where * ((double)ld_dep_f(p.inv_freq + f) * 0.15915494309189535);
         float s, c;
         sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
         cs[f] = make_float2(c, s);
@@ -152,6 +206,18 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const AppendParams p) 
     if (turned)
 #pragma unroll
         for (int k = 0; k < 8; ++k) a[k] = cs[l * 8 + k];
+    uint4 qw0{}, qw1{}, kw0{}, kw1{};                               // this lane's channels of the weights
+    const unsigned lanes = (LR == 8 ? 0xffu : 0xfu) << (tid % 32 / LR * LR);     // of a row
+    if (NORM) {
+        if (p.qw && nq) {
+            qw0 = ld_dep_u4(reinterpret_cast<const uint4 *>(p.qw) + v0);
+            qw1 = ld_dep_u4(reinterpret_cast<const uint4 *>(p.qw) + v1);
+        }
+        if (p.kw) {
+            kw0 = ld_dep_u4(reinterpret_cast<const uint4 *>(p.kw) + v0);
+            kw1 = ld_dep_u4(reinterpret_cast<const uint4 *>(p.kw) + v1);
+        }
+    }
     uint16_t *qo = p.q_out + tok * p.H_q * p.d, *ko = p.kp + dst * p.H_kv * p.d - nq * p.d,
              *vo = p.vp + dst * p.H_kv * p.d - nk * p.d;
     for (int r0 = tid / LR; r0 < R; r0 += AHEAD * ROWS) {
@@ -165,7 +231,22 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const AppendParams p) 
             const int r = r0 + k * ROWS;
             if (r >= R) break;
             uint4 y = x[k][0], z = x[k][1];
-            if (turned && r < nk) {
+            if (NORM && r < nk && (r < nq ? p.qw : p.kw)) {
+                float h[16];
+                unpack16(y, z, h);
+                norm_head<LR>(h, r < nq ? qw0 : kw0, r < nq ? qw1 : kw1, p.eps, lanes);
+                if (turned)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int c = INTER ? 2 * j : j, e = INTER ? 2 * j + 1 : j + 8;
+                        const float lo = h[c], hi = h[e];
+                        h[c] = lo * a[j].x - hi * a[j].y;
+                        h[e] = lo * a[j].y + hi * a[j].x;
+                    }
+                y = make_uint4(pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3]), pack_bf16(h[4], h[5]), pack_bf16(h[6], h[7]));
+                z = make_uint4(pack_bf16(h[8], h[9]), pack_bf16(h[10], h[11]), pack_bf16(h[12], h[13]),
+                               pack_bf16(h[14], h[15]));
+            } else if (turned && r < nk) {
                 if (INTER) {
                     y = make_uint4(turn_pair(y.x, a[0]), turn_pair(y.y, a[1]), turn_pair(y.z, a[2]), turn_pair(y.w, a[3]));
                     z = make_uint4(turn_pair(z.x, a[4]), turn_pair(z.y, a[5]), turn_pair(z.z, a[6]), turn_pair(z.w, a[7]));
@@ -185,17 +266,37 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const AppendParams p) 
 }
 
 template <int NT, int LR>
-static magicdec_status launch_append_t(const AppendParams &p, int interleaved, cudaStream_t st) {
-    return magicdec_host::launch_pdl(interleaved ? paged_append_kernel<NT, LR, true> : paged_append_kernel<NT, LR, false>,
-                                     dim3((unsigned)p.n, (unsigned)p.B), dim3(NT), 0, st, p);
+static magicdec_status launch_append_t(const AppendParams &p, int interleaved, bool norm, cudaStream_t st) {
+    auto kern = norm ? (interleaved ? paged_append_kernel<NT, LR, true, true> : paged_append_kernel<NT, LR, false, true>)
+                     : (interleaved ? paged_append_kernel<NT, LR, true, false> : paged_append_kernel<NT, LR, false, false>);
+    return magicdec_host::launch_pdl(kern, dim3((unsigned)p.n, (unsigned)p.B), dim3(NT), 0, st, p);
 }
 
-magicdec_status launch_paged_append(const magicdec_paged_shape &s, int n, const uint16_t *q, long long q_stride,
-                                    const uint16_t *k, long long k_stride, const uint16_t *v, long long v_stride,
-                                    const int32_t *len, const int32_t *n_new, const int32_t *parent,
-                                    const float *inv_freq, int rot_dim, int interleaved, const int32_t *table,
-                                    uint16_t *q_out, uint16_t *kp, uint16_t *vp, cudaStream_t st) {
+static magicdec_status launch_append(AppendParams &p, const magicdec_paged_shape &s, int interleaved, bool norm,
+                                     cudaStream_t st) {
+    p.err = magicdec_host::device_error_word();
+    p.B = s.B;
+    p.H_q = s.H_q;
+    p.H_kv = s.H_kv;
+    p.d = s.d;
+    p.page_size = s.page_size;
+    p.n_pages = s.n_pages;
+    p.max_pages = s.max_pages;
+    // Larger CTAs while there are fewer tokens than SMs: then a token's own rows take longest (one
+    // token of 48 rows: 2.7 us with 256 threads, 3.5 us with 64).
+    if ((long long)s.B * p.n >= magicdec_host::sm_count())
+        return s.d == 128 ? launch_append_t<64, 8>(p, interleaved, norm, st)
+                          : launch_append_t<64, 4>(p, interleaved, norm, st);
+    return s.d == 128 ? launch_append_t<256, 8>(p, interleaved, norm, st)
+                      : launch_append_t<256, 4>(p, interleaved, norm, st);
+}
+
+static AppendParams append_params(int n, const uint16_t *q, long long q_stride, const uint16_t *k, long long k_stride,
+                                  const uint16_t *v, long long v_stride, const int32_t *len, const int32_t *n_new,
+                                  const int32_t *parent, const float *inv_freq, int rot_dim, const int32_t *table,
+                                  uint16_t *q_out, uint16_t *kp, uint16_t *vp) {
     AppendParams p{};
+    p.n = n;
     p.q = q;
     p.k = k;
     p.v = v;
@@ -207,24 +308,38 @@ magicdec_status launch_paged_append(const magicdec_paged_shape &s, int n, const 
     p.parent = parent;
     p.table = table;
     p.inv_freq = inv_freq;
+    p.rot = rot_dim;
     p.q_out = q_out;
     p.kp = kp;
     p.vp = vp;
-    p.err = magicdec_host::device_error_word();
-    p.B = s.B;
-    p.n = n;
-    p.H_q = s.H_q;
-    p.H_kv = s.H_kv;
-    p.d = s.d;
-    p.rot = rot_dim;
-    p.page_size = s.page_size;
-    p.n_pages = s.n_pages;
-    p.max_pages = s.max_pages;
-    // Larger CTAs while there are fewer tokens than SMs: then a token's own rows take longest (one
-    // token of 48 rows: 2.7 us with 256 threads, 3.5 us with 64).
-    if ((long long)s.B * n >= magicdec_host::sm_count())
-        return s.d == 128 ? launch_append_t<64, 8>(p, interleaved, st) : launch_append_t<64, 4>(p, interleaved, st);
-    return s.d == 128 ? launch_append_t<256, 8>(p, interleaved, st) : launch_append_t<256, 4>(p, interleaved, st);
+    return p;
+}
+
+magicdec_status launch_paged_append(const magicdec_paged_shape &s, int n, const uint16_t *q, long long q_stride,
+                                    const uint16_t *k, long long k_stride, const uint16_t *v, long long v_stride,
+                                    const int32_t *len, const int32_t *n_new, const int32_t *parent,
+                                    const float *inv_freq, int rot_dim, int interleaved, const int32_t *table,
+                                    uint16_t *q_out, uint16_t *kp, uint16_t *vp, cudaStream_t st) {
+    AppendParams p = append_params(n, q, q_stride, k, k_stride, v, v_stride, len, n_new, parent, inv_freq, rot_dim, table,
+                                   q_out, kp, vp);
+    return launch_append(p, s, interleaved, false, st);
+}
+
+magicdec_status launch_norm_append(const magicdec_paged_shape &s, int n, const uint16_t *q, long long q_stride,
+                                   const uint16_t *k, long long k_stride, const uint16_t *v, long long v_stride,
+                                   const uint16_t *q_weight, const uint16_t *k_weight, float eps, const int32_t *len,
+                                   const int32_t *n_new, const int32_t *parent, const int32_t *pos, int axes,
+                                   const int32_t *axis, const float *inv_freq, int rot_dim, int interleaved,
+                                   const int32_t *table, uint16_t *q_out, uint16_t *kp, uint16_t *vp, cudaStream_t st) {
+    AppendParams p = append_params(n, q, q_stride, k, k_stride, v, v_stride, len, n_new, parent, inv_freq, rot_dim, table,
+                                   q_out, kp, vp);
+    p.qw = q_weight;
+    p.kw = k_weight;
+    p.eps = eps;
+    p.pos = pos;
+    p.axis = axis;
+    p.axes = axes;
+    return launch_append(p, s, interleaved, true, st);
 }
 
 // ---------------------------------------------------------------------- commit

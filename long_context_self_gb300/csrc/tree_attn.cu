@@ -28,6 +28,12 @@
 // does not own whole goes to the workspace as (O, max, sum) and is joined by a
 // second kernel in a fixed order.  No atomics: results do not change from run to run.
 //
+// Behind shared prefixes (template parameter PRE) the list begins with the prefixes: an entry
+// "sequence" of which the rows of all sequences of a group are the nodes, B n G rows a KV
+// head, so that a prefix's K and V are read once for a row block of any of them; the sequences'
+// own slots follow.  Every entry's part goes to the workspace, and a joining kernel of its own
+// puts a row's parts together.
+//
 // Roles (640 threads): warps 0 and 3 issue the TMA boxes, warps 1 and 2 the MMAs, warps
 // 4-11 and 12-19 are the softmax of the two streams.  Every wait is bounded; after one that
 // gave up (error 1) the roles run on without waiting, so that all of them end.
@@ -50,6 +56,12 @@ struct TreeStart {
     int b, h, rb, t0, tiles, nodes, run, pad;
 };
 
+// Where an entry of the list of PRE begins, its tiles and blocks; one more holds the length of a run.
+struct PreEntry {
+    long long start;
+    int tiles, blocks;
+};
+
 struct TreeAttnParams {
     const int32_t *len, *n_nodes, *parent, *table;
     const uint16_t *vp;    // the pool of V, for add_back
@@ -69,6 +81,13 @@ struct TreeAttnParams {
     int by8;               // pages of a multiple of 8 rows: copied by 5-D boxes
     uint32_t sbo, hoff;    // bytes between groups of 8 rows, and between 64-channel halves, of a K or V tile
     float scale_log2;      // log2(e) / sqrt(d)
+    // PRE only
+    const int32_t *plen, *first, *ptable;
+    PreEntry *entry;       // workspace: [P + B + 1]
+    float2 *pstat;         // workspace: a prefix's parts, [slots][RT * 128]
+    float4 *ppart;         // workspace: [slots][RT][d / 4][128]
+    int P, pmax;           // prefixes; pages of a row of ptable
+    int own_rt, own_blocks;   // of a sequence's own slots: row tiles of a part, blocks at most
 };
 
 __device__ __forceinline__ int tr_clamp(int v, int hi) { return v < 0 ? 0 : (v > hi ? hi : v); }
@@ -241,10 +260,34 @@ __device__ __forceinline__ int tiles_of(const TreeAttnParams &p, int total) {
 // A sequence as the roles see it.
 struct Seq {
     int len, nodes, total, tiles, blocks;   // blocks: pairs of row tiles (one: a single tile)
+    int row0;                               // PRE: its first row of queries, over all sequences
 };
-template <int RT>
+// The sequences [lo, hi) behind prefix g.
+struct Group {
+    int lo, hi;
+};
+__device__ __forceinline__ Group group_at(const TreeAttnParams &p, int g) {
+    if (!p.first) return Group{0, p.B};
+    return Group{tr_clamp(checked(ld_dep(p.first + g), 0, p.B, p.err), p.B),
+                 tr_clamp(checked(ld_dep(p.first + g + 1), 0, p.B, p.err), p.B)};
+}
+template <int RT, bool PRE>
 __device__ __forceinline__ Seq seq_at(const TreeAttnParams &p, int b) {
     Seq s;
+    if (PRE) {
+        if (b < p.P) {
+            const Group g = group_at(p, b);
+            const int most = p.page_size * p.pmax;
+            s.row0 = g.lo * p.n;
+            s.nodes = max(g.hi - g.lo, 0) * p.n;
+            s.len = s.total = s.nodes ? tr_clamp(checked(ld_dep(p.plen + b), 0, most, p.err), most) : 0;
+            s.tiles = tiles_of(p, s.total);
+            s.blocks = (s.nodes + RT * p.NB - 1) / (RT * p.NB);
+            return s;
+        }
+        b -= p.P;
+        s.row0 = b * p.n;
+    }
     const int cap = p.page_size * p.max_pages;
     s.len = tr_clamp(checked(ld_dep(p.len + b), 0, cap, p.err), cap);
     s.nodes = p.n_nodes ? tr_clamp(checked(ld_dep(p.n_nodes + b), 0, p.n, p.err), p.n) : p.n;
@@ -361,7 +404,7 @@ struct Run {
 };
 
 // Walks a CTA's part of the list; every role has its own.
-template <int RT>
+template <int RT, bool PRE>
 struct Walk {
     int b, off;             // off: tiles of sequence b already passed, over its heads and blocks
     int left;               // tiles of the run
@@ -369,9 +412,9 @@ struct Walk {
     __device__ __forceinline__ bool next(const TreeAttnParams &p, Run &r) {
         if (left <= 0) return false;
         while (off >= s.tiles * s.blocks * p.H_kv) {
-            if (++b >= p.B) return false;
+            if (++b >= (PRE ? p.P : 0) + p.B) return false;
             off = 0;
-            s = seq_at<RT>(p, b);
+            s = seq_at<RT, PRE>(p, b);
         }
         const int item = off / s.tiles;
         r.b = b;
@@ -385,6 +428,15 @@ struct Walk {
         return true;
     }
 };
+
+// PRE: an entry's parts lie at this number and the CTA's added, one for each CTA that has some of it,
+// and no two entries' meet: along the list either grows.  Prefixes are numbered by their first
+// rows, of which RT * NB make a block; sequences by their own blocks at most.
+template <int RT>
+__device__ __forceinline__ long long pre_slot(const TreeAttnParams &p, int e, int h, int rb, int blocks, int row0) {
+    if (e < p.P) return (long long)(row0 / (RT * p.NB) + e) * p.H_kv + h * blocks + rb;
+    return ((long long)(e - p.P) * p.H_kv + h) * p.own_blocks + rb;
+}
 
 template <int D, int RT>
 struct TrSmem {
@@ -416,10 +468,11 @@ __device__ __forceinline__ bool tr_wait(uint64_t *bar, uint32_t parity, int *err
     return __shfl_sync(0xffffffffu, got, 0) != 0;
 }
 
-template <int D, int RT>
+template <int D, int RT, bool PRE>
 __global__ void __launch_bounds__(kTrThreads, 1)
     tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                     const __grid_constant__ CUtensorMap tmv, const TreeAttnParams p) {
+                     const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmg,
+                     const TreeAttnParams p) {
     using L = TrSmem<D, RT>;
     constexpr int HALVES = L::HALVES, OPER = L::OPER, NST = L::STAGES, ALL = L::RINGS * NST, KS = D / 16;
     constexpr int STEP = RT == 1 ? 2 : 1;                  // tiles from one of a stream to its next
@@ -435,7 +488,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     uint64_t *mma_done = o_full + 4;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 2);
     int *found = reinterpret_cast<int *>(tmem_slot + 1);                 // where this CTA begins: see the list of work
-    volatile int *met = found + 8;                                       // a node's V was not finite: see take_out
+    volatile int *met = found + 9;                                       // a node's V was not finite: see take_out
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (smem_u32(smem) & 1023u) {
         if (tid == 0) raise_error(p.err, kErrState);
@@ -471,15 +524,16 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     // The list of work: prefix sums over the sequences (a thread has one of them, or with more
     // than kTrThreads several in a row), this CTA's run of tiles, and the sequence that it
     // begins in.
-    Walk<RT> walk;
+    Walk<RT, PRE> walk;
+    const int first_own = PRE ? p.P : 0;                                 // list entries of the prefixes
     {
         long long *wsum = reinterpret_cast<long long *>(par);
-        const int per = p.B <= kTrThreads ? 1 : (p.B + kTrThreads - 1) / kTrThreads;
-        const int ba = min(p.B, tid * per), bz = min(p.B, ba + per);
+        const int entries = first_own + p.B, per = entries <= kTrThreads ? 1 : (entries + kTrThreads - 1) / kTrThreads;
+        const int ba = min(entries, tid * per), bz = min(entries, ba + per);
         Seq sq{};
         long long mine = 0;
         for (int b = ba; b < bz; ++b) {
-            sq = seq_at<RT>(p, b);
+            sq = seq_at<RT, PRE>(p, b);
             mine += (long long)(sq.tiles * sq.blocks) * p.H_kv;
         }
         long long incl = mine;
@@ -500,8 +554,9 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         const long long run = max(1ll, quotient(all + p.grid - 1, p.grid));
         const long long t0 = blockIdx.x * run;
         for (int b = ba; b < bz; ++b) {
-            if (per > 1) sq = seq_at<RT>(p, b);
+            if (per > 1) sq = seq_at<RT, PRE>(p, b);
             const long long w = (long long)(sq.tiles * sq.blocks) * p.H_kv;
+            if (PRE && blockIdx.x == 0) p.entry[b] = PreEntry{before, sq.tiles, sq.blocks};
             if (t0 >= before && t0 < before + w) {
                 found[0] = b;
                 found[1] = (int)(t0 - before);
@@ -511,13 +566,19 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 found[5] = sq.total;
                 found[6] = sq.tiles;
                 found[7] = sq.blocks;
+                if (PRE) found[8] = sq.row0;
                 const int item = found[1] / sq.tiles, h = item / sq.blocks;
-                p.start[blockIdx.x] = TreeStart{b, h, item - h * sq.blocks, found[1] - item * sq.tiles, sq.tiles,
-                                                sq.nodes, (int)run, 0};
+                if (!PRE)
+                    p.start[blockIdx.x] = TreeStart{b, h, item - h * sq.blocks, found[1] - item * sq.tiles, sq.tiles,
+                                                    sq.nodes, (int)run, 0};
             }
             before += w;
         }
-        if (t0 >= all && tid == 0) p.start[blockIdx.x] = TreeStart{};
+        if (PRE) {
+            if (blockIdx.x == 0 && tid == 0) p.entry[entries] = PreEntry{run, 0, 0};
+        } else if (t0 >= all && tid == 0) {
+            p.start[blockIdx.x] = TreeStart{};
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -526,7 +587,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     walk.b = found[0];
     walk.off = found[1];
     walk.left = found[2];
-    walk.s = Seq{found[3], found[4], found[5], found[6], found[7]};
+    walk.s = Seq{found[3], found[4], found[5], found[6], found[7], PRE ? found[8] : 0};
     Run r;
     bool ok = true;
 
@@ -538,7 +599,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         // warps on one ring, a slot two turns back is read by both streams before the other
         // warp, which has seen the release of a later one, can be here.)
         const uint32_t pw = warp == 0 ? 0 : 1;
-        const uint64_t pol = p.n > RT * p.NB ? policy_evict_normal() : policy_evict_first();
+        const uint64_t keep = policy_evict_normal(), once = policy_evict_first();
         uint8_t *buf = ring + (RT == 1 ? pw : 0) * (NST * OPER);
         uint64_t *full_r = full + (RT == 1 ? pw : 0) * NST, *empty_r = empty + (RT == 1 ? pw : 0) * NST;
         uint32_t slot = 0, runs = 0;                 // ring slots passed, runs begun
@@ -546,15 +607,19 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             const int tiles_q = RT == 2 && r.rb * 2 * p.NB + p.NB < r.s.nodes ? 2 : 1;
             if (pw == 0) ok = tr_wait(q_empty, (runs & 1) ^ 1, p.err, ok, lane);
             if (!ok) break;
+            const bool pre = PRE && r.b < first_own;
+            const uint64_t pol = (PRE ? r.s.blocks > 1 : p.n > RT * p.NB) ? keep : once;
             if (pw == 0 && lane == 0) {
                 mbar_arrive_expect_tx(q_full, (uint32_t)(tiles_q * HALVES * p.NB * p.G * 128));
                 for (int t = 0; t < tiles_q; ++t)
                     for (int hf = 0; hf < HALVES; ++hf)
-                        tma_load_4d(qbuf + t * OPER + hf * kTrBox, &tmq, hf * 64, r.h * p.G, (r.rb * RT + t) * p.NB, r.b,
-                                    q_full, policy_evict_normal());
+                        tma_load_4d(qbuf + t * OPER + hf * kTrBox, pre ? &tmg : &tmq, hf * 64, r.h * p.G,
+                                    (r.rb * RT + t) * p.NB + (pre ? r.s.row0 : 0), pre ? 0 : r.b - first_own, q_full,
+                                    policy_evict_normal());
             }
             ++runs;
-            const int32_t *table = p.table + (long long)r.b * p.max_pages;
+            const int32_t *table = pre ? p.ptable + (long long)r.b * p.pmax
+                                       : p.table + (long long)(r.b - first_own) * p.max_pages;
             // K and V in turn, as the products need them.
             const int j0 = RT == 1 ? pw : 0, mine = (r.cnt - j0 + STEP - 1) / STEP;
             int id = 0, pr = 0;                          // of the lane's box: its page, and its first row there
@@ -786,12 +851,13 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             const int node = node_r < p.NB && base + node_r < r.s.nodes ? base + node_r : -1;
             const bool active = RT == 1 || base < r.s.nodes;
             const bool live = __any_sync(0xffffffffu, node >= 0);         // the warp has rows
-            if (p.parent && par_b != r.b) {
+            if (p.parent && par_b != r.b && (!PRE || r.b >= first_own)) {
                 // parent + 1 of every node in a byte (0: none; a parent that is not before its
                 // node counts as none), and a bit where it is not the node just before.
                 named_bar_sync(9 + s, 256);
                 const int pi = wt < r.s.nodes
-                                   ? checked(ld_dep(p.parent + (long long)r.b * p.n + wt), INT_MIN, wt - 1, p.err) : -1;
+                                   ? checked(ld_dep(p.parent + (long long)(r.b - first_own) * p.n + wt), INT_MIN, wt - 1, p.err)
+                                   : -1;
                 mypar[wt] = (uint8_t)(pi >= 0 && pi < wt ? pi + 1 : 0);
                 const uint32_t turn = __ballot_sync(0xffffffffu, wt == 0 || pi != wt - 1);
                 if (lane == 0) myturns[wt >> 5] = turn;
@@ -942,11 +1008,15 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             } else {
                 ll = xch[s * 256 + row] + xch[s * 256 + 128 + row];
             }
-            const bool whole = r.cnt == r.s.tiles;
+            const bool whole = !PRE && r.cnt == r.s.tiles, pre = PRE && r.b < first_own;
             const float inv = ll > 0.f ? 1.f / ll : 0.f;
             uint16_t *dst = p.out + (((long long)r.b * p.n + node) * p.H_q + r.h * p.G + (row - node_r * p.G)) * D;
             const int rt = RT == 2 ? s : 0;
-            float4 *pd = p.part + ((long long)part * RT + rt) * (D / 4) * p.rr + row;
+            const int rr = pre ? 128 : p.rr;
+            const long long tile_at = PRE ? (pre_slot<RT>(p, r.b, r.h, r.rb, r.s.blocks, r.s.row0) + blockIdx.x) *
+                                                    (pre ? RT : p.own_rt) + rt
+                                          : (long long)part * RT + rt;
+            float4 *pd = (pre ? p.ppart : p.part) + tile_at * (D / 4) * rr + row;
             constexpr int SHARE = RT == 1 ? D / 4 : D / 2;               // channels of a warp
             const int c_lo = RT == 1 ? (s * 2 + half) * SHARE : half * SHARE;
 #pragma unroll 1
@@ -962,10 +1032,10 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     for (int i = 0; i < 16; ++i) x[i] += w1 * __uint_as_float(o[i]);
                 }
                 if (node >= 0) {
-                    if (*met) {
+                    if (*met && !pre) {
                         const Tile e = TileWalk(p, r.t0 + r.cnt - 1).at(p, r.s.total);
                         const Channels16 z =
-                            add_back(p.vp + r.h * D + c0, (long long)p.H_kv * D, p.table + (long long)r.b * p.max_pages,
+                            add_back(p.vp + r.h * D + c0, (long long)p.H_kv * D, p.table + (long long)(r.b - first_own) * p.max_pages,
                                      p.page_size, p.n_pages, r.s.len, TileWalk(p, r.t0).at(p, r.s.total).p0,
                                      e.p0 + e.rows, node, p.parent ? mypar : nullptr);
 #pragma unroll
@@ -985,13 +1055,13 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     } else {
 #pragma unroll
                         for (int i = 0; i < 16; i += 4)
-                            pd[(c0 + i) / 4 * p.rr] = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                            pd[(c0 + i) / 4 * rr] = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
                     }
                 }
                 __syncwarp();                                // TMEM is read by whole warps
             }
             if (!whole && node >= 0 && c_lo == 0)
-                p.stat[((long long)part * RT + rt) * p.rr + row] = make_float2(mm, ll);
+                (pre ? p.pstat : p.stat)[tile_at * rr + row] = make_float2(mm, ll);
             __syncwarp();
             tc_fence_before();
             // O is free for the next run, whose first P says so: with one row tile, once all
@@ -1095,6 +1165,89 @@ __global__ void __launch_bounds__(kTjThreads) tree_attn_join_kernel(const TreeAt
         reinterpret_cast<uint4 *>(dst)[i / 2] = make_uint4(y[i].x, y[i].y, y[i + 1].x, y[i + 1].y);
 }
 
+// ------------------------------------------- the joining behind shared prefixes
+// A block joins 32 neighbouring query rows (b, i, g) of a KV head, of each the parts of its group's
+// prefix and of its own slots, in the order of the list.  PL = 1: its 8 warps share the channels, 8
+// of a row a thread at a time; PL = 8: a block has 8 channels of the rows, and its warps share the
+// parts (few rows, each in many parts, as one warp's chain of loads would be all that runs).
+template <int RT, int PL>
+__global__ void __launch_bounds__(kTjThreads) tree_attn_pre_join_kernel(const TreeAttnParams p, int D) {
+    __shared__ float4 xo[PL > 1 ? 2 * kTjThreads : 1];
+    __shared__ float2 xs[PL > 1 ? kTjThreads : 1];
+    pdl_trigger();
+    pdl_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.y;
+    const int rows = p.B * p.n * p.G, at = blockIdx.x * 32 + lane;
+    const bool real = at < rows;
+    const int flat = real ? at / p.G : 0, g = real ? at - flat * p.G : 0, b = flat / p.n, i = flat - b * p.n;
+    const int nodes = !real ? 0 : p.n_nodes ? tr_clamp(ld_dep(p.n_nodes + b), p.n) : p.n;
+    const long long run = p.entry[p.P + p.B].start;
+    // The parts of the row: in the entry of a prefix, and in that of the sequence.
+    long long slot[2] = {0, 0};          // number of the first part's row tile
+    int parts[2] = {0, 0}, row[2] = {0, 0};
+    auto locate = [&](int k, int e, int node, int row0, int rts) {
+        const PreEntry x = p.entry[e];
+        if (x.tiles == 0) return;
+        const int rb = node / (RT * p.NB), local = node - rb * RT * p.NB, rt = local / p.NB;
+        const long long t0 = x.start + (long long)(h * x.blocks + rb) * x.tiles;
+        const long long c0 = quotient(t0, (int)run), c1 = quotient(t0 + x.tiles - 1, (int)run);
+        parts[k] = (int)(c1 - c0) + 1;
+        slot[k] = (pre_slot<RT>(p, e, h, rb, x.blocks, row0) + c0) * rts + rt;
+        row[k] = (local - rt * p.NB) * p.G + g;
+    };
+    if (i < nodes) {
+        // The last group that begins at b or before; an empty one begins where the next does.
+        int lo = 0, hi = p.first ? p.P : 1;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (tr_clamp(ld_dep(p.first + mid), p.B) <= b) lo = mid;
+            else hi = mid;
+        }
+        const Group q = group_at(p, lo);
+        if (q.lo <= b && b < q.hi) locate(0, lo, (b - q.lo) * p.n + i, q.lo * p.n, RT);
+        locate(1, p.P + b, i, b * p.n, p.own_rt);
+    }
+    const float sl = p.scale_log2;
+    uint16_t *dst = p.out + ((long long)flat * p.H_q + h * p.G + g) * D;
+    for (int c = PL > 1 ? blockIdx.z : warp; c < D / 8; c += PL > 1 ? D : kTjThreads / 32) {
+        float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+        float top = -INFINITY, sum = 0.f;
+        auto add = [&](float2 e, float4 x, float4 y) {
+            const float m = fmaxf(top, e.x), mu = m == -INFINITY ? 0.f : m;
+            const float f = fast_exp2((top - mu) * sl), w = fast_exp2((e.x - mu) * sl);
+            top = m;
+            sum = sum * f + w * e.y;
+            acc[0] = make_float4(acc[0].x * f + w * x.x, acc[0].y * f + w * x.y, acc[0].z * f + w * x.z, acc[0].w * f + w * x.w);
+            acc[1] = make_float4(acc[1].x * f + w * y.x, acc[1].y * f + w * y.y, acc[1].z * f + w * y.z, acc[1].w * f + w * y.w);
+        };
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int rr = k ? p.rr : 128, rts = k ? p.own_rt : RT;
+            const float2 *stat = k ? p.stat : p.pstat;
+            const float4 *part = k ? p.part : p.ppart;
+#pragma unroll 4
+            for (int j = PL > 1 ? warp : 0; j < parts[k]; j += PL) {
+                const long long s = slot[k] + (long long)j * rts;
+                const float4 *src = part + (s * (D / 4) + 2 * c) * rr + row[k];
+                add(stat[s * rr + row[k]], src[0], src[rr]);
+            }
+        }
+        if (PL > 1) {
+            xs[tid] = make_float2(top, sum);
+            xo[2 * tid] = acc[0];
+            xo[2 * tid + 1] = acc[1];
+            __syncthreads();
+            if (warp > 0) return;
+            for (int w = 1; w < PL; ++w) add(xs[w * 32 + lane], xo[2 * (w * 32 + lane)], xo[2 * (w * 32 + lane) + 1]);
+        }
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        if (real)
+            *reinterpret_cast<uint4 *>(dst + c * 8) =
+                make_uint4(pack_bf16(acc[0].x * inv, acc[0].y * inv), pack_bf16(acc[0].z * inv, acc[0].w * inv),
+                           pack_bf16(acc[1].x * inv, acc[1].y * inv), pack_bf16(acc[1].z * inv, acc[1].w * inv));
+    }
+}
+
 // ------------------------------------------------------------------- host side
 static size_t tr_align(size_t x) { return (x + 255) & ~(size_t)255; }
 
@@ -1120,12 +1273,12 @@ static bool tr_counts(const TreeAttnParams &p) {
 template <int D, int RT>
 static magicdec_status launch_tree_t(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv,
                                      const TreeAttnParams &p, cudaStream_t st) {
-    auto kern = tree_attn_kernel<D, RT>;
+    auto kern = tree_attn_kernel<D, RT, false>;
     constexpr int smem = TrSmem<D, RT>::BYTES;
     static_assert(smem <= 227 * 1024, "shared memory of one CTA");
-    if (!magicdec_host::allow_smem_once<tree_attn_kernel<D, RT>>(smem)) return MAGICDEC_ERR_CUDA;
+    if (!magicdec_host::allow_smem_once<tree_attn_kernel<D, RT, false>>(smem)) return MAGICDEC_ERR_CUDA;
     magicdec_status s =
-        magicdec_host::launch_pdl(kern, dim3((unsigned)p.grid), dim3(kTrThreads), smem, st, tmq, tmk, tmv, p);
+        magicdec_host::launch_pdl(kern, dim3((unsigned)p.grid), dim3(kTrThreads), smem, st, tmq, tmk, tmv, tmq, p);
     if (s != MAGICDEC_OK) return s;
     const int items = (p.n < RT * p.NB ? p.n : RT * p.NB) * p.G * (D / 4);
     const bool few = items <= 512 && 2 * (long long)p.B * p.H_kv <= p.grid;
@@ -1136,22 +1289,13 @@ static magicdec_status launch_tree_t(const CUtensorMap &tmq, const CUtensorMap &
                                      st, p, D, per);
 }
 
-magicdec_status launch_tree_attn(const magicdec_paged_shape &s, int n, const uint16_t *q, const uint16_t *kp,
-                                 const uint16_t *vp, const int32_t *table, const int32_t *len, const int32_t *n_nodes,
-                                 const int32_t *parent, uint16_t *out, void *ws, cudaStream_t st) {
-    TreeAttnParams p{};
-    p.len = len;
-    p.n_nodes = n_nodes;
-    p.parent = parent;
-    p.table = table;
-    p.vp = vp;
-    p.out = out;
+// What follows from the shape of the pool and the heads.
+static void set_tiles(TreeAttnParams &p, const magicdec_paged_shape &s) {
     p.err = magicdec_host::device_error_word();
     p.B = s.B;
     p.H_q = s.H_q;
     p.H_kv = s.H_kv;
     p.G = s.H_q / s.H_kv;
-    p.n = n;
     p.page_size = s.page_size;
     p.n_pages = s.n_pages;
     p.max_pages = s.max_pages;
@@ -1175,6 +1319,57 @@ magicdec_status launch_tree_attn(const magicdec_paged_shape &s, int n, const uin
     }
     p.scale_log2 = kLog2e / sqrtf((float)s.d);
     p.grid = magicdec_host::sm_count();
+    p.by4 = s.page_size < 4;
+    p.sbo = p.by8 ? s.d / 64 * 1024 : 1024;
+    p.hoff = p.by8 ? 1024 : kTrBox;
+}
+
+static bool set_maps(const TreeAttnParams &p, const magicdec_paged_shape &s, const uint16_t *q, const uint16_t *kp,
+                     const uint16_t *vp, CUtensorMap *tmq, CUtensorMap *tmk, CUtensorMap *tmv, CUtensorMap *tmg) {
+    // Queries as (d, H_q, n, B), one box = NB nodes of a KV head's group; tmg, if
+    // given, takes the rows of all sequences for those of one.  The pool with
+    // pages of a multiple of 8 rows as (64 channels, 8 rows, halves of all heads, groups of 8
+    // rows, pages): one box is a page (or a part of it) of one KV head, its channels read
+    // together and its rows laid out for the tensor cores.  Other pages as (d, H_kv,
+    // page_size, n_pages), boxes of 64 channels x a page (or 64 rows); pages of 1 to 3 rows as
+    // one list of rows, 4 of them a copy (32 sequences of 32k, 8 nodes, pages of 1, 2 and 3 rows:
+    // 4.2, 2.2 and 1.8 ms with a box a page, 1.6 ms so; of 4 rows: 1.15 ms with boxes).
+    const int D = s.d, HV = D / 64;
+    const uint64_t row = (uint64_t)s.H_kv * D * 2;
+    const uint32_t br = (uint32_t)p.br;
+    const uint64_t kd4[4] = {(uint64_t)D, (uint64_t)s.H_kv, (uint64_t)s.page_size, (uint64_t)s.n_pages};
+    const uint64_t ks4[3] = {(uint64_t)D * 2, row, s.page_size * row};
+    const uint32_t kb4[4] = {64, 1, br, 1};
+    const uint64_t kd2[2] = {(uint64_t)s.H_kv * D, (uint64_t)s.n_pages * s.page_size};
+    const uint32_t kb2[2] = {64, 1};
+    const uint64_t kd5[5] = {64, 8, (uint64_t)s.H_kv * HV, (uint64_t)s.page_size / 8, (uint64_t)s.n_pages};
+    const uint64_t ks5[4] = {row, 128, 8 * row, s.page_size * row};
+    const uint32_t kb5[5] = {64, 8, (uint32_t)HV, br / 8, 1};
+    const uint64_t qd[4] = {(uint64_t)D, (uint64_t)s.H_q, (uint64_t)p.n, (uint64_t)s.B};
+    const uint64_t qs[3] = {(uint64_t)D * 2, (uint64_t)s.H_q * D * 2, (uint64_t)p.n * s.H_q * D * 2};
+    const uint32_t qbx[4] = {64, (uint32_t)p.G, (uint32_t)p.NB, 1};
+    auto pool = [&](CUtensorMap *m, const uint16_t *x) {
+        return p.by4   ? magicdec_host::encode_tmap_bf16(m, x, 2, kd2, &row, kb2, D * 2)
+               : p.by8 ? magicdec_host::encode_tmap_bf16(m, x, 5, kd5, ks5, kb5, D * 2)
+                       : magicdec_host::encode_tmap_bf16(m, x, 4, kd4, ks4, kb4, D * 2);
+    };
+    const uint64_t gd[4] = {(uint64_t)D, (uint64_t)s.H_q, (uint64_t)s.B * p.n, 1};
+    return pool(tmk, kp) && pool(tmv, vp) && magicdec_host::encode_tmap_bf16_4d(tmq, q, qd, qs, qbx) &&
+           (!tmg || magicdec_host::encode_tmap_bf16_4d(tmg, q, gd, qs, qbx));
+}
+
+magicdec_status launch_tree_attn(const magicdec_paged_shape &s, int n, const uint16_t *q, const uint16_t *kp,
+                                 const uint16_t *vp, const int32_t *table, const int32_t *len, const int32_t *n_nodes,
+                                 const int32_t *parent, uint16_t *out, void *ws, cudaStream_t st) {
+    TreeAttnParams p{};
+    p.len = len;
+    p.n_nodes = n_nodes;
+    p.parent = parent;
+    p.table = table;
+    p.vp = vp;
+    p.out = out;
+    p.n = n;
+    set_tiles(p, s);
     if (!tr_counts(p)) return MAGICDEC_ERR_UNSUPPORTED;
     const int RT = tr_row_tiles(n, p.G);
     const size_t slots = 2 * (size_t)p.grid;
@@ -1186,41 +1381,110 @@ magicdec_status launch_tree_attn(const magicdec_paged_shape &s, int n, const uin
     w += tr_align(slots * RT * p.rr * sizeof(float2));
     p.part = reinterpret_cast<float4 *>(w);
 
-    // Queries as (d, H_q, n, B), one box = NB nodes of a KV head's group.  The pool with
-    // pages of a multiple of 8 rows as (64 channels, 8 rows, halves of all heads, groups of 8
-    // rows, pages): one box is a page (or a part of it) of one KV head, its channels read
-    // together and its rows laid out for the tensor cores.  Other pages as (d, H_kv,
-    // page_size, n_pages), boxes of 64 channels x a page (or 64 rows); pages of 1 to 3 rows as
-    // one list of rows, 4 of them a copy (32 sequences of 32k, 8 nodes, pages of 1, 2 and 3 rows:
-    // 4.2, 2.2 and 1.8 ms with a box a page, 1.6 ms so; of 4 rows: 1.15 ms with boxes).
     CUtensorMap tmq, tmk, tmv;
-    const int D = s.d, HV = D / 64;
-    p.by4 = s.page_size < 4;
-    p.sbo = p.by8 ? HV * 1024 : 1024;
-    p.hoff = p.by8 ? 1024 : kTrBox;
-    const uint64_t row = (uint64_t)s.H_kv * D * 2;
-    const uint32_t br = (uint32_t)p.br;
-    const uint64_t kd4[4] = {(uint64_t)D, (uint64_t)s.H_kv, (uint64_t)s.page_size, (uint64_t)s.n_pages};
-    const uint64_t ks4[3] = {(uint64_t)D * 2, row, s.page_size * row};
-    const uint32_t kb4[4] = {64, 1, br, 1};
-    const uint64_t kd2[2] = {(uint64_t)s.H_kv * D, (uint64_t)s.n_pages * s.page_size};
-    const uint32_t kb2[2] = {64, 1};
-    const uint64_t kd5[5] = {64, 8, (uint64_t)s.H_kv * HV, (uint64_t)s.page_size / 8, (uint64_t)s.n_pages};
-    const uint64_t ks5[4] = {row, 128, 8 * row, s.page_size * row};
-    const uint32_t kb5[5] = {64, 8, (uint32_t)HV, br / 8, 1};
-    const uint64_t qd[4] = {(uint64_t)D, (uint64_t)s.H_q, (uint64_t)n, (uint64_t)s.B};
-    const uint64_t qs[3] = {(uint64_t)D * 2, (uint64_t)s.H_q * D * 2, (uint64_t)n * s.H_q * D * 2};
-    const uint32_t qbx[4] = {64, (uint32_t)p.G, (uint32_t)p.NB, 1};
-    auto pool = [&](CUtensorMap *m, const uint16_t *x) {
-        return p.by4   ? magicdec_host::encode_tmap_bf16(m, x, 2, kd2, &row, kb2, D * 2)
-               : p.by8 ? magicdec_host::encode_tmap_bf16(m, x, 5, kd5, ks5, kb5, D * 2)
-                       : magicdec_host::encode_tmap_bf16(m, x, 4, kd4, ks4, kb4, D * 2);
-    };
-    if (!pool(&tmk, kp) || !pool(&tmv, vp) || !magicdec_host::encode_tmap_bf16_4d(&tmq, q, qd, qs, qbx))
-        return MAGICDEC_ERR_CUDA;
-    if (D == 128)
+    if (!set_maps(p, s, q, kp, vp, &tmq, &tmk, &tmv, nullptr)) return MAGICDEC_ERR_CUDA;
+    if (s.d == 128)
         return RT == 1 ? launch_tree_t<128, 1>(tmq, tmk, tmv, p, st) : launch_tree_t<128, 2>(tmq, tmk, tmv, p, st);
     return RT == 1 ? launch_tree_t<64, 1>(tmq, tmk, tmv, p, st) : launch_tree_t<64, 2>(tmq, tmk, tmv, p, st);
+}
+
+// ------------------------------------------------- behind shared prefixes: host side
+// One row tile a CTA while a group's rows fit one on average and a sequence's do; else two, which
+// read K and V once for 256 rows.
+static int pre_row_tiles(int B, int P, int n, int G) {
+    const int NB = 128 / G;
+    return n <= NB && (long long)((B + P - 1) / P) * n <= NB ? 1 : 2;
+}
+
+struct PreSizes {
+    int RT, own_rt, own_blocks, rr;
+    long long pslots, slots;
+};
+static PreSizes pre_sizes(const magicdec_paged_shape &s, int P, int n) {
+    PreSizes z;
+    const int G = s.H_q / s.H_kv, NB = 128 / G;
+    z.RT = pre_row_tiles(s.B, P, n, G);
+    z.own_rt = tr_row_tiles(n, G);
+    z.own_blocks = (n + z.RT * NB - 1) / (z.RT * NB);
+    z.rr = tr_part_rows(n, G);
+    z.pslots = ((long long)s.B * n / (z.RT * NB) + P) * s.H_kv + magicdec_host::sm_count();
+    z.slots = (long long)s.B * s.H_kv * z.own_blocks + magicdec_host::sm_count();
+    return z;
+}
+
+size_t prefix_attn_workspace_bytes(const magicdec_paged_shape &s, int P, int n) {
+    const PreSizes z = pre_sizes(s, P, n);
+    const size_t prows = (size_t)z.pslots * z.RT * 128, rows = (size_t)z.slots * z.own_rt * z.rr;
+    return tr_align(((size_t)P + s.B + 1) * sizeof(PreEntry)) + tr_align(prows * sizeof(float2)) +
+           tr_align(rows * sizeof(float2)) + (prows + rows) * s.d * 4;
+}
+
+template <int D, int RT>
+static magicdec_status launch_prefix_t(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv,
+                                       const CUtensorMap &tmg, const TreeAttnParams &p, cudaStream_t st) {
+    auto kern = tree_attn_kernel<D, RT, true>;
+    constexpr int smem = TrSmem<D, RT>::BYTES;
+    if (!magicdec_host::allow_smem_once<tree_attn_kernel<D, RT, true>>(smem)) return MAGICDEC_ERR_CUDA;
+    magicdec_status s =
+        magicdec_host::launch_pdl(kern, dim3((unsigned)p.grid), dim3(kTrThreads), smem, st, tmq, tmk, tmv, tmg, p);
+    if (s != MAGICDEC_OK) return s;
+    const unsigned blocks = (unsigned)(((long long)p.B * p.n * p.G + 31) / 32);
+    // Parts shared out while the blocks of whole rows would not fill the GPU.
+    if ((long long)blocks * p.H_kv <= p.grid)
+        return magicdec_host::launch_pdl(tree_attn_pre_join_kernel<RT, 8>, dim3(blocks, (unsigned)p.H_kv, D / 8),
+                                         dim3(kTjThreads), 0, st, p, D);
+    return magicdec_host::launch_pdl(tree_attn_pre_join_kernel<RT, 1>, dim3(blocks, (unsigned)p.H_kv), dim3(kTjThreads), 0,
+                                     st, p, D);
+}
+
+magicdec_status launch_prefix_attn(const magicdec_paged_shape &s, int P, int pmax, int n, const uint16_t *q,
+                                   const uint16_t *kp, const uint16_t *vp, const int32_t *ptable, const int32_t *plen,
+                                   const int32_t *first, const int32_t *table, const int32_t *len,
+                                   const int32_t *n_nodes, const int32_t *parent, uint16_t *out, void *ws,
+                                   cudaStream_t st) {
+    TreeAttnParams p{};
+    p.len = len;
+    p.n_nodes = n_nodes;
+    p.parent = parent;
+    p.table = table;
+    p.vp = vp;
+    p.out = out;
+    p.n = n;
+    set_tiles(p, s);
+    p.plen = plen;
+    p.first = first;
+    p.ptable = ptable;
+    p.P = P;
+    p.pmax = pmax;
+    // The list is counted in 32 bits within an entry and within a CTA's run.
+    auto tiles = [&](long long pages) {
+        return p.span ? (pages * p.page_size + p.span - 1) / p.span : pages * p.tpp;
+    };
+    const PreSizes z = pre_sizes(s, P, n);
+    const long long rows = (long long)s.B * n;
+    const double work = (double)tiles(pmax) * s.H_kv * (double)((rows + p.NB - 1) / p.NB);
+    const double own = (double)tiles(s.max_pages) * s.H_kv * ((n + p.NB - 1) / p.NB);
+    if (work > INT_MAX || own > INT_MAX || (work * P + own * s.B) / p.grid >= INT_MAX / 2) return MAGICDEC_ERR_UNSUPPORTED;
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    const size_t prows = (size_t)z.pslots * z.RT * 128, orows = (size_t)z.slots * z.own_rt * z.rr;
+    p.entry = reinterpret_cast<PreEntry *>(w);
+    w += tr_align(((size_t)P + s.B + 1) * sizeof(PreEntry));
+    p.pstat = reinterpret_cast<float2 *>(w);
+    w += tr_align(prows * sizeof(float2));
+    p.stat = reinterpret_cast<float2 *>(w);
+    w += tr_align(orows * sizeof(float2));
+    p.ppart = reinterpret_cast<float4 *>(w);
+    p.part = reinterpret_cast<float4 *>(w + prows * s.d * 4);
+    p.rr = z.rr;
+    p.own_rt = z.own_rt;
+    p.own_blocks = z.own_blocks;
+    CUtensorMap tmq, tmk, tmv, tmg;
+    if (!set_maps(p, s, q, kp, vp, &tmq, &tmk, &tmv, &tmg)) return MAGICDEC_ERR_CUDA;
+    if (s.d == 128)
+        return z.RT == 1 ? launch_prefix_t<128, 1>(tmq, tmk, tmv, tmg, p, st)
+                         : launch_prefix_t<128, 2>(tmq, tmk, tmv, tmg, p, st);
+    return z.RT == 1 ? launch_prefix_t<64, 1>(tmq, tmk, tmv, tmg, p, st)
+                     : launch_prefix_t<64, 2>(tmq, tmk, tmv, tmg, p, st);
 }
 
 }  // namespace magicdec
