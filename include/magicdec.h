@@ -619,9 +619,7 @@ MAGICDEC_API magicdec_status magicdec_tree_commit(magicdec_paged_shape shape, in
  * Rows at or past len may hold anything, NaN included, and are left as they are; a token's own
  * row reaches it and later tokens only, whatever it holds.  Probabilities are summed in fp32, in
  * an order that is the same from run to run.
- * Supported: (H_q/H_kv) * n_q <= 32, and rows whose scores, 4 (H_q/H_kv) n_q bytes each, fit
- * the shared memory of 16 CTAs (a cap of 229,888 for 4 query rows, of 28,672 for 32;
- * MAGICDEC_ERR_UNSUPPORTED beyond).
+ * Supported: (H_q/H_kv) * n_q <= 32 and H_kv <= 65535 (MAGICDEC_ERR_UNSUPPORTED beyond).
  * Errors: NULL pointers, bad shape, n_q <= 0, alignment (q, kc, vc, out).
  */
 MAGICDEC_API magicdec_status magicdec_heavy_attn(magicdec_kv_shape shape, int n_q, const uint16_t *q,

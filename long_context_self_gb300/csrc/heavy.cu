@@ -14,23 +14,26 @@ namespace magicdec {
 // ----------------------------------------------------------------- attention
 // Bound: HBM, 4 d + 8 bytes a cache row (K, V, the weight read and written) for 4 d R flops.
 // A row's weight needs the whole softmax's maximum and sum, which are known when all keys have
-// been seen; so the scores stay on chip until then: a cluster of C CTAs takes a (sequence, KV
-// head), each a stretch of its keys and keeps their R scores in shared memory.  Then the CTAs
-// exchange (max, sum), every row's weight is written once, and the O of all warps are summed in
-// a fixed order.  No workspace, no atomics, one launch.
+// been seen.  So a cluster of C CTAs takes a (sequence, KV head), each a stretch of its keys, and
+// after one pass over K and V the CTAs exchange (max, sum); then every row's weight is written
+// once, from the scores, which stay in shared memory until then, or, where they would take too
+// much of it (R = 25 and 1500 keys a CTA: 150 KB), are computed again from a second pass over K,
+// out of L2 (AGAIN).  The O of all warps are summed in a fixed order.  No workspace, no
+// atomics, one launch.
 //
-// A warp takes 16 keys at a time, straight from global memory into the fragments of
-// mma.sync (m16n8k16): the order of the channels inside a product and of the output's
-// columns is free, so that a lane's fragments are whole 16-byte words of a K row (channels
-// 8 (lane % 4) .. of every 32) and of a V row (channels 8 (lane / 4) .. of every 64).  The
-// products are a few percent of the time; what counts is the bytes under way: the K of the
-// warp's next keys and the V of these.
-constexpr int kHvWarps = 4;
-constexpr int kHvThreads = kHvWarps * 32;
+// A producer warp keeps a ring of stages filled by TMA, 64 keys' K and V each; consumer warps take 16
+// keys of a stage (with more than 16 query rows, two warps the same keys for 16 rows each) through
+// ldmatrix and mma.sync (m16n8k16): at R <= 32 the products are a few percent of the time, and a
+// 128-row tcgen05 tile would be empty but for R rows.  Keys straight from global memory into the
+// fragments, without shared memory, left too few bytes under way (128 sequences over 2053 rows, R = 4:
+// 207 us; 16 over up to 12,001, R = 25: 229 us).
+constexpr int kHvKeys = 64;          // keys of a stage
+constexpr int kHvHalf = kHvKeys * 128;   // bytes of 64 channels of them
+constexpr int kHvStages = 8;         // stages of a ring at most
 constexpr float kHvLazy = 24.0f;     // log2 growth of a row's maximum that is put up with
 
 struct HeavyParams {
-    const uint16_t *q, *k, *v;
+    const uint16_t *q;
     uint16_t *out;
     float *weight;
     int32_t *pos;
@@ -38,6 +41,7 @@ struct HeavyParams {
     int *err;
     int B, H_q, H_kv, G, n, cap, R;
     int stride;                      // floats between two query rows' scores
+    int stages;                      // of the ring
     float scale_log2;                // log2(e) / sqrt(d)
 };
 
@@ -75,302 +79,433 @@ __device__ __forceinline__ float4 hv_ld4(uint32_t a) {
                  : "memory");
     return v;
 }
+// A warp's wait, with one outcome for all lanes; once one has given up, the later ones return at once.
+__device__ __forceinline__ bool hv_wait(uint64_t *bar, uint32_t parity, int *err, bool ok, int lane) {
+    if (__all_sync(0xffffffffu, ok && mbar_try_sleep(bar, parity))) return true;
+    int got = ok ? 1 : 0;
+    if (ok && lane == 0) got = mbar_poll_on(bar, parity, err) ? 1 : 0;
+    return __shfl_sync(0xffffffffu, got, 0) != 0;
+}
 
-// A 16-byte load of K or V.  With two row tiles two warps read the same keys, the second from L1.
-template <int MT>
-__device__ __forceinline__ uint4 hv_ld(const uint4 *p) {
-    if (MT == 1) return ld_dep_u4(p);
-    uint4 v;
-    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p)
-                 : "memory");
-    return v;
+// D(16x8) += A(16x16) B(16x8); with 8 real rows (HR = 1) the lower half of A and of D is not there.
+template <int HR>
+__device__ __forceinline__ void hv_mma(float (&c)[2 * HR], const uint32_t (&a)[2 * HR], uint32_t b0, uint32_t b1) {
+    if constexpr (HR == 2) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    } else {
+        asm volatile(
+            "{\n\t.reg .f32 x, y;\n\t"
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,x,y}, {%2,%3,%4,%5}, {%6,%7}, "
+            "{%0,%1,%8,%8};\n\t}"
+            : "+f"(c[0]), "+f"(c[1])
+            : "r"(a[0]), "r"(0u), "r"(a[1]), "r"(0u), "r"(b0), "r"(b1), "f"(0.f));
+    }
 }
 
 // ROWS: query rows of a warp's tile that can be real, 8 or 16; MT: row tiles (a warp has one).
-template <int D, int ROWS, int MT>
-__global__ void __launch_bounds__(kHvThreads, ROWS == 8 ? 3 : 2) heavy_attn_kernel(const HeavyParams p) {
-    constexpr int SP = D / 32;                          // spans of 32 channels
-    constexpr int HV = D / 64;                          // halves of 64 channels
+template <int D, int ROWS, int MT, bool AGAIN>
+__global__ void __launch_bounds__(128 * MT + 32, MT == 2 ? 1 : 2)
+    heavy_attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                      const __grid_constant__ CUtensorMap tmk16, const __grid_constant__ CUtensorMap tmv16,
+                      const HeavyParams p) {
+    constexpr int CW = 4 * MT, NT = CW * 32 + 32;       // consumer warps; threads
+    constexpr int KS = D / 16, HV = D / 64, NB = D / 8;
     constexpr int HR = ROWS / 8;                        // rows of a lane: lane / 4, and 8 more
-    constexpr int KW = kHvWarps / MT;                   // warps that share the keys
-    extern __shared__ __align__(16) uint8_t smem[];
-    float *scores = reinterpret_cast<float *>(smem);    // [R][stride]; later the warps' O
-    __shared__ float2 wstat[kHvWarps][16];              // of a warp's rows: (max, sum)
+    constexpr int OPER = HV * kHvHalf, STAGE = 2 * OPER;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *ring = smem;
+    float *scores = reinterpret_cast<float *>(smem + p.stages * STAGE);     // [R][stride]; later the warps' O
+    __shared__ uint64_t full[kHvStages], empty[kHvStages];
+    __shared__ float2 wstat[CW][16];                    // of a warp's rows: (max, sum)
     __shared__ float2 cstat[32];                        // of this CTA
     __shared__ float2 all[32];                          // of the cluster: (max, 1 / sum)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int lq = lane & 3, lr = lane >> 2;
     const int b = blockIdx.z, h = blockIdx.y;
     const uint32_t rank = hv_rank(), C = hv_ctas();
-    const int mt = warp % MT, kw = warp / MT;
     const float sl = p.scale_log2;
+    if (tid == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], CW);
+        }
+        mbar_fence_init();
+        prefetch_tensormap(&tmk);
+        prefetch_tensormap(&tmv);
+    }
     pdl_trigger();
     pdl_wait();
+    __syncthreads();
     const int len0 = checked(ld_dep(p.len + b), 0, p.cap, p.err);
     const int len = len0 < 0 ? 0 : (len0 > p.cap ? p.cap : len0);
     // This CTA's keys: [k0, k1), in groups of 16.
     const int per = ((len + (int)C - 1) / (int)C + 15) & ~15;
-    const int k0 = min(len, (int)rank * per), k1 = min(len, k0 + per);
+    const int k0 = min(len, (int)rank * per), k1 = min(len, k0 + per), tiles = (k1 - k0 + kHvKeys - 1) / kHvKeys;
     const long long row0 = ((long long)b * p.H_kv + h) * p.cap;
-    const uint4 *kb = reinterpret_cast<const uint4 *>(p.k + row0 * D);
-    const uint4 *vb = reinterpret_cast<const uint4 *>(p.v + row0 * D);
+    const int first_new = p.next_pos ? len - p.n : INT_MAX;
+    bool ok = smem_u32(smem) % 1024 == 0;
+    if (!ok && tid == 0) raise_error(p.err, kErrState);
 
-    // The lane's query rows (i * G + g: token i, head g of the group), and how many keys they see.
-    uint4 qf[SP][HR];
-    int see[HR];
-#pragma unroll
-    for (int e = 0; e < HR; ++e) {
-        const int r = mt * 16 + lr + 8 * e, i = r / p.G;
-        see[e] = r < p.R ? len - p.n + 1 + i : 0;
-        const uint4 *src = reinterpret_cast<const uint4 *>(
-            p.q + (((long long)b * p.n + i) * p.H_q + h * p.G + (r - i * p.G)) * D);
-#pragma unroll
-        for (int s = 0; s < SP; ++s) qf[s][e] = r < p.R ? ld_dep_u4(src + s * 4 + lq) : make_uint4(0, 0, 0, 0);
-    }
-    float o[HV][8][2 * HR];                             // [half][channel][columns, rows]
-#pragma unroll
-    for (int f = 0; f < HV; ++f)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int e = 0; e < 2 * HR; ++e) o[f][j][e] = 0.f;
-    float m[HR], l[HR];
-#pragma unroll
-    for (int e = 0; e < HR; ++e) {
-        m[e] = -INFINITY;
-        l[e] = 0.f;
-    }
-
-    // D(16x8) += A(16x16) B(16x8); with 8 real rows the lower half of A and of D is not there.
-    auto mma = [&](float *c, const uint32_t a0, const uint32_t a1, const uint32_t a2, const uint32_t a3, uint32_t b0,
-                   uint32_t b1) {
-        if (HR == 2) {
-            asm volatile(
-                "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                "{%0,%1,%2,%3};"
-                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2 * HR - 2]), "+f"(c[2 * HR - 1])
-                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-        } else {
-            asm volatile(
-                "{\n\t.reg .f32 x, y;\n\t"
-                "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,x,y}, {%2,%3,%4,%5}, {%6,%7}, "
-                "{%0,%1,%8,%8};\n\t}"
-                : "+f"(c[0]), "+f"(c[1])
-                : "r"(a0), "r"(0u), "r"(a2), "r"(0u), "r"(b0), "r"(b1), "f"(0.f));
-        }
-    };
-    uint4 kf[2][SP];
-    auto load_k = [&](int g) {                          // keys g .. g + 15; a row behind the last reads as zeros
-#pragma unroll
-        for (int nb = 0; nb < 2; ++nb) {
-            const int key = g + nb * 8 + lr;
-#pragma unroll
-            for (int s = 0; s < SP; ++s)
-                kf[nb][s] = key < k1 ? hv_ld<MT>(kb + (long long)key * (D / 8) + s * 4 + lq) : make_uint4(0, 0, 0, 0);
-        }
-    };
-    // The scores' place: row r of this warp's tile, key g.
-    float *my = scores + (long long)(mt * 16 + lr) * p.stride - k0;
-    int g = k0 + 16 * kw;
-    if (g < k1) load_k(g);
-    for (; g < k1; g += 16 * KW) {
-        uint4 vf[4][HV];                                // V of keys 2 lq, 2 lq + 1, 2 lq + 8, 2 lq + 9
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const int key = g + 2 * lq + (x & 1) + (x >> 1) * 8;
-#pragma unroll
-            for (int f = 0; f < HV; ++f)
-                vf[x][f] = key < k1 ? hv_ld<MT>(vb + (long long)key * (D / 8) + f * 8 + lr) : make_uint4(0, 0, 0, 0);
-        }
-        float s[2][2 * HR];
-#pragma unroll
-        for (int nb = 0; nb < 2; ++nb) {
-#pragma unroll
-            for (int e = 0; e < 2 * HR; ++e) s[nb][e] = 0.f;
-#pragma unroll
-            for (int c = 0; c < SP; ++c) {
-                const uint4 &a = qf[c][0], &a8 = qf[c][HR - 1];
-                mma(s[nb], a.x, a8.x, a.y, a8.y, kf[nb][c].x, kf[nb][c].y);
-                mma(s[nb], a.z, a8.z, a.w, a8.w, kf[nb][c].z, kf[nb][c].w);
-            }
-        }
-        if (g + 16 * KW < k1) load_k(g + 16 * KW);
-        // Keys that not every row sees: behind the last one, or of the block's own tokens.
-        const bool edge = g + 16 > len - p.n + 1 || g + 16 > k1;
-        float top[HR];
-#pragma unroll
-        for (int e = 0; e < HR; ++e) top[e] = -INFINITY;
-#pragma unroll
-        for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-            for (int e = 0; e < HR; ++e) {
-                float &x = s[nb][2 * e], &y = s[nb][2 * e + 1];
-                x *= sl;
-                y *= sl;
-                if (edge) {
-                    const int key = g + nb * 8 + 2 * lq;
-                    if (key >= min(see[e], k1)) x = -INFINITY;
-                    if (key + 1 >= min(see[e], k1)) y = -INFINITY;
-                }
-                if (mt * 16 + lr + 8 * e < p.R)
-                    *reinterpret_cast<float2 *>(my + (long long)(8 * e) * p.stride + g + nb * 8 + 2 * lq) =
-                        make_float2(x, y);
-                top[e] = fmaxf(top[e], fmaxf(x, y));
-            }
-        // The maximum moves, and O and the sum are scaled, only where it has grown by more than
-        // 2^kHvLazy: weights up to 2^24 instead of 1 cost a floating sum nothing.
-        bool move = false;
-#pragma unroll
-        for (int e = 0; e < HR; ++e) {
-            top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
-            top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
-            move |= top[e] > m[e] + kHvLazy || (m[e] == -INFINITY && top[e] > m[e]);
-        }
-        if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-            for (int e = 0; e < HR; ++e) {
-                const float to = fmaxf(m[e], top[e]);
-                const float f = to == -INFINITY ? 1.f : fast_exp2(m[e] - to);
-                m[e] = to;
-                l[e] *= f;
-#pragma unroll
-                for (int x = 0; x < HV; ++x)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        o[x][j][2 * e] *= f;
-                        o[x][j][2 * e + 1] *= f;
+    // The producer's part of a pass: tiles [from, to) of it, of which the first is the ring's `slot`.
+    const uint64_t once = policy_evict_first(), keep = policy_evict_normal();
+    auto produce = [&](int from, int to, uint32_t slot, bool v_too) {
+        for (int t = from; ok && t < to; ++t, ++slot) {
+            const uint32_t st = slot % p.stages;
+            ok = mbar_poll(&empty[st], (slot / p.stages & 1) ^ 1, p.err);
+            if (!ok) return;
+            const int key = k0 + t * kHvKeys, groups = (min(kHvKeys, k1 - key) + 15) / 16;
+            uint8_t *to_k = ring + st * STAGE;
+            const uint64_t pol = AGAIN && v_too ? keep : once;
+            mbar_arrive_expect_tx(&full[st], (uint32_t)(groups * (v_too ? 2 : 1) * HV * 2048));
+            for (int f = 0; f < HV; ++f) {
+                if (groups == 4) {
+                    tma_load_4d(to_k + f * kHvHalf, &tmk, f * 64, key, h, b, &full[st], pol);
+                    if (v_too) tma_load_4d(to_k + OPER + f * kHvHalf, &tmv, f * 64, key, h, b, &full[st], once);
+                } else {
+                    for (int g = 0; g < groups; ++g) {
+                        tma_load_4d(to_k + f * kHvHalf + g * 2048, &tmk16, f * 64, key + g * 16, h, b, &full[st], pol);
+                        if (v_too)
+                            tma_load_4d(to_k + OPER + f * kHvHalf + g * 2048, &tmv16, f * 64, key + g * 16, h, b,
+                                        &full[st], once);
                     }
+                }
             }
         }
-        // P in bf16 for the second product: off by at most 2^-9 of itself, as the output's
-        // rounding; the sum is of the unrounded values.
-        uint32_t a[2][2] = {{0, 0}, {0, 0}};
+    };
+    const int ahead = AGAIN ? min(p.stages, tiles) : 0; // tiles of the second pass that fit the ring beside no other
+    const int mt = MT == 1 ? 0 : warp % MT, kw = warp / MT;
+    float o[NB][2 * HR];
+    float m[HR], l[HR];
+    uint32_t qf[KS][2 * HR];
+    // The fragments of query rows 16 tile .. (row i * G + g: token i, head g of the group).
+    auto load_q = [&](int tile, uint32_t (&to)[KS][2 * HR]) {
 #pragma unroll
         for (int e = 0; e < HR; ++e) {
-            const float mu = m[e] == -INFINITY ? 0.f : m[e];
+            const int r = tile * 16 + lr + 8 * e, i = r / p.G;
+            const unsigned *src = reinterpret_cast<const unsigned *>(
+                p.q + (((long long)b * p.n + i) * p.H_q + h * p.G + (r - i * p.G)) * D);
 #pragma unroll
-            for (int nb = 0; nb < 2; ++nb) {
-                const float x = fast_exp2(s[nb][2 * e] - mu), y = fast_exp2(s[nb][2 * e + 1] - mu);
-                s[nb][2 * e] = x;
-                s[nb][2 * e + 1] = y;
-                l[e] += x + y;
-                a[nb][e] = pack_bf16(x, y);
+            for (int s = 0; s < KS; ++s) {
+                to[s][e] = r < p.R ? ld_dep_u32(src + s * 8 + lq) : 0u;
+                to[s][HR + e] = r < p.R ? ld_dep_u32(src + s * 8 + 4 + lq) : 0u;
             }
         }
-        if (p.n > 1 && g + 16 > len - p.n + 1) {
-            // Keys of the block's own tokens, which earlier tokens must not see whatever they hold
-            // (0 * inf is NaN): by scalars, and only where a row sees them.
-            const int last = min(16, k1 - g);
-            for (int x = 0; x < last; ++x) {
-                const int key = g + x, from = (lane & ~3) | ((x & 7) >> 1);
-                float w[HR];
+    };
+    // Query row r sees keys below this.
+    auto seen = [&](int r) { return r < p.R ? min(len - p.n + 1 + r / p.G, k1) : 0; };
+    // 8 keys' fragments for 32 channels, or 16 keys' for 16: rows r .. of the K tile at `at`.
+    auto k_addr = [&](uint32_t at, int row, int chunk) {
+        return at + (uint32_t)(chunk >> 3) * kHvHalf + swz128(row, chunk & 7);
+    };
+
+    if (warp == CW) {
+        if (lane == 0) {
+            produce(0, tiles, 0, true);
+            if (AGAIN) produce(0, ahead, tiles, false);
+        }
+        __syncwarp();
+    } else {
+        load_q(mt, qf);
+        int see[HR];
 #pragma unroll
-                for (int e = 0; e < HR; ++e) {
-                    const float even = x < 8 ? s[0][2 * e] : s[1][2 * e], odd = x < 8 ? s[0][2 * e + 1] : s[1][2 * e + 1];
-                    w[e] = __shfl_sync(0xffffffffu, x & 1 ? odd : even, from);
+        for (int e = 0; e < HR; ++e) {
+            see[e] = seen(mt * 16 + lr + 8 * e);
+            m[e] = -INFINITY;
+            l[e] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+            for (int e = 0; e < 2 * HR; ++e) o[j][e] = 0.f;
+        // The scores' place: row r of this warp's tile, key g.
+        float *my = scores + (long long)(mt * 16 + lr) * p.stride - k0;
+        const int x4 = lane >> 3, r0 = 16 * kw;
+        for (int t = 0; t < tiles; ++t) {
+            const uint32_t st = (uint32_t)t % p.stages, kt = smem_u32(ring + st * STAGE), vt = kt + OPER;
+            ok = hv_wait(&full[st], (uint32_t)t / p.stages & 1, p.err, ok, lane);
+            const int g = k0 + t * kHvKeys + r0;
+            if (g < k1) {
+                // Two chains of products a score, so that half as many wait for one another.
+                float s[2][2 * HR], s2[2][2 * HR];
+#pragma unroll
+                for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                    for (int e = 0; e < 2 * HR; ++e) s[nb][e] = s2[nb][e] = 0.f;
+#pragma unroll
+                for (int c = 0; c < KS; ++c) {
+                    uint32_t f0, f1, f2, f3;
+                    ldsm_x4(k_addr(kt, r0 + (x4 >> 1) * 8 + (lane & 7), c * 2 + (x4 & 1)), f0, f1, f2, f3);
+                    hv_mma<HR>(c & 1 ? s2[0] : s[0], qf[c], f0, f1);
+                    hv_mma<HR>(c & 1 ? s2[1] : s[1], qf[c], f2, f3);
                 }
+                // Keys that not every row sees: behind the last one, or of the block's own tokens.
+                const bool edge = g + 16 > len - p.n + 1 || g + 16 > k1;
+                float top[HR];
 #pragma unroll
-                for (int f = 0; f < HV; ++f)
+                for (int e = 0; e < HR; ++e) top[e] = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {       // 8 channels of column 2 lq + c
-                        const uint4 y = hv_ld<MT>(vb + (long long)key * (D / 8) + f * 8 + 2 * lq + c);
-                        const uint32_t z[4] = {y.x, y.y, y.z, y.w};
+                for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float vj = __uint_as_float(j & 1 ? z[j / 2] & 0xffff0000u : z[j / 2] << 16);
+                    for (int e = 0; e < HR; ++e) {
+                        float &x = s[nb][2 * e], &y = s[nb][2 * e + 1];
+                        x = (x + s2[nb][2 * e]) * sl;
+                        y = (y + s2[nb][2 * e + 1]) * sl;
+                        if (edge) {
+                            const int key = g + nb * 8 + 2 * lq;
+                            if (key >= see[e]) x = -INFINITY;
+                            if (key + 1 >= see[e]) y = -INFINITY;
+                        }
+                        if (!AGAIN && mt * 16 + lr + 8 * e < p.R)
+                            *reinterpret_cast<float2 *>(my + (long long)(8 * e) * p.stride + g + nb * 8 + 2 * lq) =
+                                make_float2(x, y);
+                        top[e] = fmaxf(top[e], fmaxf(x, y));
+                    }
+                // The maximum moves, and O and the sum are scaled, only where it has grown by more than
+                // 2^kHvLazy: weights up to 2^24 instead of 1 cost a floating sum nothing.
+                bool move = false;
 #pragma unroll
-                            for (int e = 0; e < HR; ++e)
-                                if (key < see[e]) o[f][j][2 * e + c] = fmaf(w[e], vj, o[f][j][2 * e + c]);
+                for (int e = 0; e < HR; ++e) move |= top[e] > m[e] + kHvLazy;
+                if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                    for (int e = 0; e < HR; ++e) {
+                        top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+                        top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+                        const float to = fmaxf(m[e], top[e]);
+                        const float f = to == -INFINITY ? 1.f : fast_exp2(m[e] - to);
+                        m[e] = to;
+                        l[e] *= f;
+#pragma unroll
+                        for (int j = 0; j < NB; ++j) {
+                            o[j][2 * e] *= f;
+                            o[j][2 * e + 1] *= f;
                         }
                     }
+                }
+                // P in bf16 for the second product: off by at most 2^-8 of itself, as the output's
+                // rounding; the sum is of the unrounded values.
+                uint32_t a[2 * HR];
+#pragma unroll
+                for (int e = 0; e < HR; ++e) {
+                    const float mu = m[e] == -INFINITY ? 0.f : m[e];
+#pragma unroll
+                    for (int nb = 0; nb < 2; ++nb) {
+                        const float x = fast_exp2(s[nb][2 * e] - mu), y = fast_exp2(s[nb][2 * e + 1] - mu);
+                        s[nb][2 * e] = x;
+                        s[nb][2 * e + 1] = y;
+                        l[e] += x + y;
+                        a[nb * HR + e] = pack_bf16(x, y);
+                    }
+                }
+                if (p.n > 1 && g + 16 > len - p.n + 1) {
+                    // Keys of the block's own tokens, which earlier tokens must not see whatever they hold
+                    // (0 * inf is NaN): by scalars, and only where a row sees them.
+                    const int last = min(16, k1 - g);
+                    for (int x = 0; x < last; ++x) {
+                        const int from = (lane & ~3) | ((x & 7) >> 1);
+                        float w[HR];
+#pragma unroll
+                        for (int e = 0; e < HR; ++e) {
+                            const float even = x < 8 ? s[0][2 * e] : s[1][2 * e];
+                            const float odd = x < 8 ? s[0][2 * e + 1] : s[1][2 * e + 1];
+                            w[e] = __shfl_sync(0xffffffffu, x & 1 ? odd : even, from);
+                        }
+                        const uint8_t *v = ring + st * STAGE + OPER;
+#pragma unroll
+                        for (int j = 0; j < NB; ++j) {
+                            const uint32_t z = *reinterpret_cast<const uint32_t *>(v + (j >> 3) * kHvHalf +
+                                                                                   swz128(r0 + x, j & 7) + 4 * lq);
+#pragma unroll
+                            for (int e = 0; e < HR; ++e)
+                                if (g + x < see[e]) {
+                                    o[j][2 * e] = fmaf(w[e], __uint_as_float(z << 16), o[j][2 * e]);
+                                    o[j][2 * e + 1] = fmaf(w[e], __uint_as_float(z & 0xffff0000u), o[j][2 * e + 1]);
+                                }
+                        }
+                    }
+                } else {
+                    if (g + 16 > k1) {
+                        // Rows of V behind the last may hold anything, and 0 * NaN is NaN: zeros.
+                        for (int i = lane; i < (g + 16 - k1) * HV * 8; i += 32) {
+                            const int row = r0 + 15 - i / (HV * 8), c = i % (HV * 8);
+                            *reinterpret_cast<uint4 *>(ring + st * STAGE + OPER + (c >> 3) * kHvHalf + swz128(row, c & 7)) =
+                                make_uint4(0, 0, 0, 0);
+                        }
+                        __syncwarp();
+                    }
+#pragma unroll
+                    for (int j = 0; j < NB; j += 2) {
+                        uint32_t f0, f1, f2, f3;
+                        ldsm_x4_trans(k_addr(vt, r0 + (x4 & 1) * 8 + (lane & 7), j + (x4 >> 1)), f0, f1, f2, f3);
+                        hv_mma<HR>(o[j], a, f0, f1);
+                        hv_mma<HR>(o[j + 1], a, f2, f3);
+                    }
+                }
             }
-            continue;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[st]);
         }
+        // The warps' maxima and sums.
 #pragma unroll
-        for (int f = 0; f < HV; ++f) {
-            const uint32_t v0[4] = {vf[0][f].x, vf[0][f].y, vf[0][f].z, vf[0][f].w};
-            const uint32_t v1[4] = {vf[1][f].x, vf[1][f].y, vf[1][f].z, vf[1][f].w};
-            const uint32_t v8[4] = {vf[2][f].x, vf[2][f].y, vf[2][f].z, vf[2][f].w};
-            const uint32_t v9[4] = {vf[3][f].x, vf[3][f].y, vf[3][f].z, vf[3][f].w};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {               // two keys' values of a channel side by side
-                const uint32_t pick = j & 1 ? 0x7632u : 0x5410u;
-                mma(o[f][j], a[0][0], a[0][HR - 1], a[1][0], a[1][HR - 1], __byte_perm(v0[j / 2], v1[j / 2], pick),
-                    __byte_perm(v8[j / 2], v9[j / 2], pick));
-            }
+        for (int e = 0; e < HR; ++e) {
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+            if (lq == 0) wstat[warp][lr + 8 * e] = make_float2(m[e], l[e]);
         }
-    }
-
-    // The warps' maxima and sums, the CTA's, the cluster's.
-#pragma unroll
-    for (int e = 0; e < HR; ++e) {
-        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-        if (lq == 0) wstat[warp][lr + 8 * e] = make_float2(m[e], l[e]);
     }
     __syncthreads();
+    // The CTA's, the cluster's.
     auto join = [](float2 &s, float2 x) {
         const float mx = fmaxf(s.x, x.x), mu = mx == -INFINITY ? 0.f : mx;
         s = make_float2(mx, s.y * fast_exp2(s.x - mu) + x.y * fast_exp2(x.x - mu));
     };
     if (tid < p.R) {
         float2 s = make_float2(-INFINITY, 0.f);
-        for (int w = 0; w < KW; ++w) join(s, wstat[w * MT + tid / 16][tid % 16]);
+        for (int w = 0; w < CW / MT; ++w) join(s, wstat[w * MT + tid / 16][tid % 16]);
         cstat[tid] = s;
     }
     if (C > 1) hv_cluster_sync();
-    if (tid < p.R) {
+    if (tid < 32) {
         float2 s = make_float2(-INFINITY, 0.f);
-        if (C > 1)
-            for (uint32_t c = 0; c < C; ++c) join(s, hv_ld2(hv_at(&cstat[tid], c)));
-        else
-            s = cstat[tid];
+        if (tid < p.R) {
+            if (C > 1)
+                for (uint32_t c = 0; c < C; ++c) join(s, hv_ld2(hv_at(&cstat[tid], c)));
+            else
+                s = cstat[tid];
+        }
         all[tid] = make_float2(s.x == -INFINITY ? 0.f : s.x, s.y > 0.f ? 1.f / s.y : 0.f);
     }
     __syncthreads();
 
-    // Every row's weight, summed over the query rows in their order.
-    const int first_new = p.next_pos ? len - p.n : INT_MAX;
-    for (int j = k0 + tid; j < k1; j += kHvThreads) {
-        float *w = p.weight + row0 + j;
-        float sum = 0.f;
-        const float old = j >= first_new ? 0.f : *w;
-        for (int r = 0; r < p.R; ++r) sum = fmaf(fast_exp2(scores[(long long)r * p.stride + j - k0] - all[r].x), all[r].y, sum);
-        *w = old + sum;
+    // Every row's weight.
+    auto add_weight = [&](int j, float old, float sum) {
+        p.weight[row0 + j] = (j >= first_new ? 0.f : old) + sum;
         if (j >= first_new) p.pos[row0 + j] = ld_dep(p.next_pos + b) + (j - first_new);
+    };
+    if (!AGAIN) {
+        // Summed over the query rows in their order.
+        for (int j = k0 + tid; j < k1; j += NT) {
+            const float old = p.weight[row0 + j];
+            float sum = 0.f;
+            for (int r = 0; r < p.R; ++r)
+                sum = fmaf(fast_exp2(scores[(long long)r * p.stride + j - k0] - all[r].x), all[r].y, sum);
+            add_weight(j, old, sum);
+        }
+        __syncthreads();
     }
-    __syncthreads();
-
-    // O of the warps, in the softmax's own scale: to shared memory, then summed over the warps
-    // and over the CTAs, each of which has a share of the channels.
-    float *osum = scores;                               // [KW][R][D]
+    // O of the warps, in the softmax's own scale.
+    float *osum = scores;                               // [CW / MT][R][D]
+    if (warp < CW) {
 #pragma unroll
-    for (int e = 0; e < HR; ++e) {
-        const int r = mt * 16 + lr + 8 * e;
-        if (r >= p.R) continue;
-        const float f = m[e] == -INFINITY ? 0.f : fast_exp2(m[e] - all[r].x) * all[r].y;
-        float *to = osum + ((long long)kw * p.R + r) * D;
+        for (int e = 0; e < HR; ++e) {
+            const int r = mt * 16 + lr + 8 * e;
+            if (r >= p.R) continue;
+            const float f = m[e] == -INFINITY ? 0.f : fast_exp2(m[e] - all[r].x) * all[r].y;
+            float *to = osum + ((long long)kw * p.R + r) * D + 2 * lq;
 #pragma unroll
-        for (int x = 0; x < HV; ++x)
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int j = 0; j < 8; j += 4)
-                    *reinterpret_cast<float4 *>(to + x * 64 + (2 * lq + c) * 8 + j) =
-                        make_float4(o[x][j][2 * e + c] * f, o[x][j + 1][2 * e + c] * f, o[x][j + 2][2 * e + c] * f,
-                                    o[x][j + 3][2 * e + c] * f);
+            for (int j = 0; j < NB; ++j)
+                *reinterpret_cast<float2 *>(to + j * 8) = make_float2(o[j][2 * e] * f, o[j][2 * e + 1] * f);
+        }
     }
+    if (AGAIN) {
+        // The second pass over K: a warp has 64 / CW keys of a stage and all query rows.
+        constexpr int KN = kHvKeys / CW / 8;            // in groups of 8
+        if (warp == CW) {
+            if (lane == 0) {
+                produce(ahead, tiles, tiles + ahead, false);
+                // No copy may be in flight when the CTA ends.
+                for (int t = max(0, 2 * tiles - p.stages); t < 2 * tiles; ++t)
+                    mbar_poll(&full[t % p.stages], (uint32_t)t / p.stages & 1, p.err);
+            }
+            __syncwarp();
+        } else {
+            uint32_t q2[MT][KS][2 * HR];
+            float2 at[MT][HR];
+            int see[MT][HR];
+#pragma unroll
+            for (int x = 0; x < MT; ++x) {
+                load_q(x, q2[x]);
+#pragma unroll
+                for (int e = 0; e < HR; ++e) {
+                    at[x][e] = all[x * 16 + lr + 8 * e];
+                    see[x][e] = seen(x * 16 + lr + 8 * e);
+                }
+            }
+            for (int t = 0; t < tiles; ++t) {
+                const uint32_t slot = tiles + t, st = slot % p.stages, kt = smem_u32(ring + st * STAGE);
+                const int g = k0 + t * kHvKeys + warp * 8 * KN;
+                float old[KN][2];
+#pragma unroll
+                for (int nb = 0; nb < KN; ++nb)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int key = g + nb * 8 + 2 * lq + x;
+                        old[nb][x] = lr == 0 && key < k1 ? p.weight[row0 + key] : 0.f;
+                    }
+                ok = hv_wait(&full[st], slot / p.stages & 1, p.err, ok, lane);
+                if (g < k1) {
+#pragma unroll
+                    for (int nb = 0; nb < KN; ++nb) {
+                        float s[MT][2 * HR];
+#pragma unroll
+                        for (int x = 0; x < MT; ++x)
+#pragma unroll
+                            for (int e = 0; e < 2 * HR; ++e) s[x][e] = 0.f;
+#pragma unroll
+                        for (int c = 0; c < KS; c += 2) {
+                            uint32_t f0, f1, f2, f3;
+                            ldsm_x4(k_addr(kt, warp * 8 * KN + nb * 8 + (lane & 7), c * 2 + (lane >> 3)), f0, f1, f2, f3);
+#pragma unroll
+                            for (int x = 0; x < MT; ++x) {
+                                hv_mma<HR>(s[x], q2[x][c], f0, f1);
+                                hv_mma<HR>(s[x], q2[x][c + 1], f2, f3);
+                            }
+                        }
+                        const int key = g + nb * 8 + 2 * lq;
+                        float w0 = 0.f, w1 = 0.f;
+#pragma unroll
+                        for (int x = 0; x < MT; ++x)
+#pragma unroll
+                            for (int e = 0; e < HR; ++e) {
+                                if (key < see[x][e]) w0 = fmaf(fast_exp2(s[x][2 * e] * sl - at[x][e].x), at[x][e].y, w0);
+                                if (key + 1 < see[x][e])
+                                    w1 = fmaf(fast_exp2(s[x][2 * e + 1] * sl - at[x][e].x), at[x][e].y, w1);
+                            }
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) {
+                            w0 += __shfl_xor_sync(0xffffffffu, w0, d);
+                            w1 += __shfl_xor_sync(0xffffffffu, w1, d);
+                        }
+                        if (lr == 0) {
+                            if (key < k1) add_weight(key, old[nb][0], w0);
+                            if (key + 1 < k1) add_weight(key + 1, old[nb][1], w1);
+                        }
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[st]);
+            }
+        }
+    } else if (warp == CW && lane == 0) {
+        for (int t = max(0, tiles - p.stages); t < tiles; ++t)
+            mbar_poll(&full[t % p.stages], (uint32_t)t / p.stages & 1, p.err);
+    }
+    __syncwarp();
+    // O summed over the warps and the CTAs, each of which has a share of the channels.
     if (C > 1) hv_cluster_sync();
     else __syncthreads();
     const int vecs = p.R * (D / 4), share = (vecs + (int)C - 1) / (int)C;
-    for (int i = (int)rank * share + tid; i < min(vecs, (int)(rank + 1) * share); i += kHvThreads) {
+    for (int i = (int)rank * share + tid; i < min(vecs, (int)(rank + 1) * share); i += NT) {
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         for (uint32_t c = 0; c < C; ++c) {
             const uint32_t base = hv_at(osum, c);
 #pragma unroll
-            for (int w = 0; w < KW; ++w) {
+            for (int w = 0; w < CW / MT; ++w) {
                 const float4 x = hv_ld4(base + (uint32_t)(w * vecs + i) * 16);
                 s.x += x.x;
                 s.y += x.y;
@@ -386,41 +521,82 @@ __global__ void __launch_bounds__(kHvThreads, ROWS == 8 ? 3 : 2) heavy_attn_kern
 }
 
 // ----------------------------------------------------------------- host side
-constexpr int kHvMaxCluster = 16;
+constexpr int kHvMaxCluster = 8;
+constexpr int kHvScores = 40 * 1024;     // scores of a CTA that stay in shared memory
 
-// Shared memory of a CTA whose cluster is C wide: the scores of its keys, or later the warps' O.
-static size_t hv_smem(int cap, int R, int D, int C, int *stride) {
-    const int warps = R <= 16 ? kHvWarps : kHvWarps / 2;
-    const long long per = (((long long)cap + C - 1) / C + 15) / 16 * 16;
+struct HeavyPlan {
+    int C, stages, stride;
+    size_t smem;
+    bool again;
+};
+
+static HeavyPlan heavy_plan(int pairs, int cap, int R, int D) {
+    HeavyPlan z;
+    // How wide a cluster: a CTA's stages take the time of HBM's share of an SM (two CTAs an SM, or one at
+    // half the time), and some 6 us go by before and after them; CTAs come in waves, the last one
+    // part full.  128 sequences of 2053 rows, 8 heads, R = 4, clusters of 1, 2, 4 and 8: 184, 195, 216 and
+    // 331 us; 16 of up to 12,001, R = 25: 257, 178, 176 and 265.
+    const double slots = (R > 16 ? 1.0 : 2.0) * magicdec_host::sm_count();
+    double best = 0;
+    z.C = 1;
+    for (int C = 1; C <= kHvMaxCluster; C *= 2) {
+        const double waves = pairs * C / slots + 0.5;
+        const double t = (waves > 1 ? waves : 1) * (((cap + C - 1) / C + kHvKeys - 1) / kHvKeys * 1.4 + 6.0);
+        if (C == 1 || t < best) {
+            best = t;
+            z.C = C;
+        }
+    }
+    const long long per = (((long long)cap + z.C - 1) / z.C + 15) / 16 * 16;
     // 8 floats more than a multiple of 32: neighbouring rows' scores lie in other banks.
-    const long long st = (per + 23) / 32 * 32 + 8;
-    *stride = (int)st;
-    const long long a = st * R * 4, o = (long long)warps * R * D * 4;
-    return (size_t)(a > o ? a : o);
+    const long long stride = (per + 23) / 32 * 32 + 8, scores = stride * R * 4, o = 4ll * R * D * 4;
+    z.again = scores > kHvScores;
+    z.stride = z.again ? 0 : (int)stride;
+    const long long rest = (z.again || o > scores ? o : scores), stage = D / 64 * 2ll * kHvHalf;
+    // Two CTAs an SM (one with more than 16 query rows, whose registers fill it).
+    const long long room = (R > 16 ? magicdec_host::max_smem_optin() : magicdec_host::max_smem_optin() / 2) - 4096 - rest;
+    long long stages = room / stage, tiles = (per + kHvKeys - 1) / kHvKeys * (z.again ? 2 : 1);
+    if (stages > kHvStages) stages = kHvStages;
+    if (stages > tiles) stages = tiles;
+    z.stages = (int)(stages < 1 ? 1 : stages);
+    z.smem = (size_t)(z.stages * stage + rest);
+    return z;
 }
 
-template <int D, int ROWS, int MT>
-static magicdec_status launch_heavy_t(const HeavyParams &p, int C, size_t smem, cudaStream_t st) {
-    auto kern = heavy_attn_kernel<D, ROWS, MT>;
-    if (!magicdec_host::allow_smem_once<heavy_attn_kernel<D, ROWS, MT>>(magicdec_host::max_smem_optin() - 2048) ||
-        !magicdec_host::allow_wide_cluster_once<heavy_attn_kernel<D, ROWS, MT>>())
+template <int D, int ROWS, int MT, bool AGAIN>
+static magicdec_status launch_heavy_t(const CUtensorMap (&tm)[4], const HeavyParams &p, const HeavyPlan &z,
+                                      cudaStream_t st) {
+    if (!magicdec_host::allow_smem_once<heavy_attn_kernel<D, ROWS, MT, AGAIN>>(magicdec_host::max_smem_optin() - 3072))
         return MAGICDEC_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)C, (unsigned)p.H_kv, (unsigned)p.B);
-    cfg.blockDim = dim3(kHvThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.gridDim = dim3((unsigned)z.C, (unsigned)p.H_kv, (unsigned)p.B);
+    cfg.blockDim = dim3(128 * MT + 32);
+    cfg.dynamicSmemBytes = z.smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = C;
+    attr[1].val.clusterDim.x = z.C;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return MAGICDEC_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, heavy_attn_kernel<D, ROWS, MT, AGAIN>, tm[0], tm[1], tm[2], tm[3], p) != cudaSuccess)
+        return MAGICDEC_ERR_CUDA;
     return magicdec_host::launch_status();
+}
+
+template <int D>
+static magicdec_status launch_heavy_d(const CUtensorMap (&tm)[4], const HeavyParams &p, const HeavyPlan &z,
+                                      cudaStream_t st) {
+    if (z.again)
+        return p.R <= 8    ? launch_heavy_t<D, 8, 1, true>(tm, p, z, st)
+               : p.R <= 16 ? launch_heavy_t<D, 16, 1, true>(tm, p, z, st)
+                           : launch_heavy_t<D, 16, 2, true>(tm, p, z, st);
+    return p.R <= 8    ? launch_heavy_t<D, 8, 1, false>(tm, p, z, st)
+           : p.R <= 16 ? launch_heavy_t<D, 16, 1, false>(tm, p, z, st)
+                       : launch_heavy_t<D, 16, 2, false>(tm, p, z, st);
 }
 
 magicdec_status launch_heavy_attn(int B, int H_q, int H_kv, int D, int cap, int n, const uint16_t *q,
@@ -428,8 +604,6 @@ magicdec_status launch_heavy_attn(int B, int H_q, int H_kv, int D, int cap, int 
                                   float *weight, int32_t *pos, uint16_t *out, cudaStream_t st) {
     HeavyParams p{};
     p.q = q;
-    p.k = k;
-    p.v = v;
     p.out = out;
     p.weight = weight;
     p.pos = pos;
@@ -444,32 +618,40 @@ magicdec_status launch_heavy_attn(int B, int H_q, int H_kv, int D, int cap, int 
     p.cap = cap;
     p.R = n * p.G;
     p.scale_log2 = kLog2e / sqrtf((float)D);
-    // As wide a cluster as it takes to have 8 CTAs an SM in all, with 64 keys each at least, and for
-    // the scores to leave room for three CTAs an SM.
-    const int limit = magicdec_host::max_smem_optin() - 2048;
-    int C = 1;
-    while (C < 8 && (long long)B * H_kv * C < 8ll * magicdec_host::sm_count() && cap > C * 64) C *= 2;
-    size_t smem = hv_smem(cap, p.R, D, C, &p.stride);
-    while (C < kHvMaxCluster && smem > 72 * 1024) smem = hv_smem(cap, p.R, D, C *= 2, &p.stride);
-    if (smem > (size_t)limit) return MAGICDEC_ERR_UNSUPPORTED;
-    if (D == 128)
-        return p.R <= 8 ? launch_heavy_t<128, 8, 1>(p, C, smem, st)
-                        : p.R <= 16 ? launch_heavy_t<128, 16, 1>(p, C, smem, st) : launch_heavy_t<128, 16, 2>(p, C, smem, st);
-    return p.R <= 8 ? launch_heavy_t<64, 8, 1>(p, C, smem, st)
-                    : p.R <= 16 ? launch_heavy_t<64, 16, 1>(p, C, smem, st) : launch_heavy_t<64, 16, 2>(p, C, smem, st);
+    const HeavyPlan z = heavy_plan(B * H_kv, cap, p.R, D);
+    p.stride = z.stride;
+    p.stages = z.stages;
+    // (channels, rows, heads, sequences), boxes of 64 channels of a stage's rows, and of 16 for its end.
+    CUtensorMap tm[4];
+    const uint64_t dims[4] = {(uint64_t)D, (uint64_t)cap, (uint64_t)H_kv, (uint64_t)B};
+    const uint64_t row = (uint64_t)D * 2, strides[3] = {row, cap * row, (uint64_t)H_kv * cap * row};
+    const uint32_t box[4] = {64, kHvKeys, 1, 1}, box16[4] = {64, 16, 1, 1};
+    if (!magicdec_host::encode_tmap_bf16_4d(&tm[0], k, dims, strides, box) ||
+        !magicdec_host::encode_tmap_bf16_4d(&tm[1], v, dims, strides, box) ||
+        !magicdec_host::encode_tmap_bf16_4d(&tm[2], k, dims, strides, box16) ||
+        !magicdec_host::encode_tmap_bf16_4d(&tm[3], v, dims, strides, box16))
+        return MAGICDEC_ERR_CUDA;
+    return D == 128 ? launch_heavy_d<128>(tm, p, z, st) : launch_heavy_d<64>(tm, p, z, st);
 }
 
 // ------------------------------------------------------------------ eviction
 // Of a (layer, sequence, KV head)'s len rows the `budget` with the largest key stay.  A row's
 // key is its weight, infinity for the protected ones; equal keys: the smaller position stays, then
-// the smaller row.  Seen from the other end, the E = len - budget least go; the border is found
-// digit by digit over (weight, position, row), most significant first, from counts of the rows
-// that agree with the border so far.  Rows that stay behind the budget then fill the holes below
-// it, in ascending order of both, so that a step that evicts E rows moves at most E.
-// Bound: 8 bytes a row (weight, position) from HBM, in practice the chain of a CTA's passes.
+// the smaller row.  Seen from the other end, the E = len - budget least go.  Rows that stay behind
+// the budget then fill the holes below it, in ascending order of both, so that a step that evicts E
+// rows moves at most E.
+// Bound: 8 bytes a row (weight, position) from HBM; in practice the chain of loads, searches and
+// moves of a (layer, sequence, KV head), which only others can cover.  So one warp takes it where its
+// keys are few (kEvWarpRows; keys in shared memory, reductions and lists inside the warp, no barrier of
+// a CTA), and 8 warps where they are many.  The border is found by searches over all keys: for few rows
+// the least key not yet taken, again and again, for many the key's bits from the top, each with the
+// count of the keys below (one digit of 8 bits at a time with counts by shared-memory atomics: 87 us
+// for 32 layers of 16 sequences of 1029 rows, see DESIGN for the times since).
 constexpr int kEvThreads = 256;
-constexpr int kEvMoves = 512;            // moves listed at a time
-constexpr int kEvBits = 8;
+constexpr int kEvWarps = kEvThreads / 32;
+constexpr int kEvWarpRows = 2048;        // rows of a warp's own
+constexpr int kEvMoves = 64;             // moves listed at a time, a warp
+constexpr int kEvTake = 16;              // rows to go that are taken one after another
 
 struct EvictParams {
     uint4 *kc, *vc;
@@ -479,6 +661,7 @@ struct EvictParams {
     int32_t *len_out;
     int *err;
     int B, H_kv, cap, vecs, budget, n_sink, n_recent;
+    long long items;                     // layers * B * H_kv
     int keep;                            // rows whose keys fit shared memory
 };
 
@@ -488,105 +671,166 @@ __device__ __forceinline__ uint32_t ev_key(float w) {
     return x & 0x80000000u ? ~x : x | 0x80000000u;
 }
 
+// NW: warps of an item (1: a CTA has kEvWarps items).
+template <int NW>
 __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictParams p) {
-    extern __shared__ uint32_t kept[];                       // keys of the first p.keep rows
-    __shared__ int hist[1 << kEvBits];
-    __shared__ int found[2];                                 // the border's digit, rows below it
-    __shared__ int src[kEvMoves], dst[kEvMoves];
-    __shared__ int wsum[2][kEvThreads / 32];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h = blockIdx.x, b = blockIdx.y;
+    constexpr int T = NW * 32, LIST = kEvMoves * NW;
+    extern __shared__ uint32_t shared[];
+    __shared__ int lists[2 * kEvMoves * kEvWarps];
+    __shared__ uint2 xch[2][kEvWarps];
+    const int tid = threadIdx.x % T, warp = tid >> 5, lane = tid & 31, sub = threadIdx.x / T;
+    const int words = (p.cap + 31) / 32;
+    uint32_t *kept = shared + sub * (p.keep + words), *gone = kept + p.keep;
+    int *src = lists + sub * 2 * LIST, *dst = src + LIST;
     pdl_trigger();
     pdl_wait();
+    const long long item = (long long)blockIdx.x * (kEvWarps / NW) + sub;
+    if (item >= p.items) return;
+    const int b = (int)(item / p.H_kv % p.B);
     const int len0 = checked(ld_dep(p.len + b), 0, p.cap, p.err);
     const int len = len0 < 0 ? 0 : (len0 > p.cap ? p.cap : len0);
-    if (h == 0 && blockIdx.z == 0 && tid == 0) p.len_out[b] = min(len, p.budget);
-    int E = len - p.budget;                                  // rows to go
+    if (item < (long long)p.B * p.H_kv && item % p.H_kv == 0 && tid == 0) p.len_out[b] = min(len, p.budget);
+    const int E = len - p.budget;                            // rows to go
     if (E <= 0) return;
-    const long long row0 = (((long long)blockIdx.z * p.B + b) * p.H_kv + h) * p.cap;
+    const long long row0 = item * p.cap;
     float *weight = p.weight + row0;
     int32_t *pos = p.pos + row0;
     const long long recent = (long long)ld_dep(p.seq_len + b) - p.n_recent;
-    auto fresh = [&](int j) {
-        const int at = ld_dep(pos + j);
-        return at < p.n_sink || at >= recent ? ev_key(INFINITY) : ev_key(__uint_as_float(ld_dep_u32(
-                                                   reinterpret_cast<const unsigned *>(weight + j))));
+    auto sync = [] {
+        if (NW == 1) __syncwarp();
+        else __syncthreads();
     };
-    for (int j = tid; j < min(len, p.keep); j += kEvThreads) kept[j] = fresh(j);
-    auto key = [&](int j) { return j < p.keep ? kept[j] : fresh(j); };
-    // What goes first: small weights, large positions, high rows.
-    auto part = [&](int word, int j) {
-        return word == 0 ? key(j) : word == 1 ? ~((uint32_t)ld_dep(pos + j) ^ 0x80000000u) : ~(uint32_t)j;
-    };
-    uint32_t border[3] = {0, 0, 0};
-    int words = 3;                                           // words of the border that count
-    bool whole = false;                                      // everything that agrees with the border goes
-    uint32_t mask = 0;                                       // digits of the current word that are settled
-    int left = E;
-    for (int word = 0; word < 3 && !whole; ++word) {
-        mask = 0;
-        for (int shift = 32 - kEvBits; shift >= 0 && !whole; shift -= kEvBits) {
-            __syncthreads();
-            for (int i = tid; i < 1 << kEvBits; i += kEvThreads) hist[i] = 0;
-            __syncthreads();
-            for (int j = tid; j < len; j += kEvThreads) {
-                bool same = true;
-                for (int w = 0; w < word && same; ++w) same = part(w, j) == border[w];
-                if (!same) continue;
-                const uint32_t x = part(word, j);
-                if ((x & mask) == (border[word] & mask)) atomicAdd(&hist[x >> shift & ((1 << kEvBits) - 1)], 1);
-            }
-            __syncthreads();
-            // The digit at which the running count reaches `left`.
-            const int c = hist[tid];
-            int incl = c;
+    auto key_of = [&](int at, float w) { return at < p.n_sink || at >= recent ? ev_key(INFINITY) : ev_key(w); };
+    auto weight_at = [&](int j) { return __uint_as_float((uint32_t)ld_dep(reinterpret_cast<const int *>(weight) + j)); };
+    // Keys, 8 rows of a thread under way at a time.
+    const int mine = min(len, p.keep);
+    for (int j0 = tid; j0 < mine; j0 += 8 * T) {
+        int at[8];
+        float w[8];
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += x;
+        for (int k = 0; k < 8; ++k)
+            if (j0 + k * T < mine) {
+                at[k] = ld_dep(pos + j0 + k * T);
+                w[k] = weight_at(j0 + k * T);
             }
-            if (lane == 31) wsum[0][warp] = incl;
-            __syncthreads();
-            for (int w = 0; w < warp; ++w) incl += wsum[0][w];
-            if (incl >= left && incl - c < left) {
-                found[0] = tid;
-                found[1] = incl - c;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (j0 + k * T < mine) kept[j0 + k * T] = key_of(at[k], w[k]);
+    }
+    sync();
+    auto key = [&](int j) { return j < p.keep ? kept[j] : key_of(ld_dep(pos + j), weight_at(j)); };
+
+    // Sums, and least values with the sum of their counts, over the item's threads.
+    int turn = 0;                                            // of the two buffers, which take turns
+    auto sum_all = [&](int x) {
+        x = __reduce_add_sync(0xffffffffu, x);
+        if (NW > 1) {
+            if (lane == 0) xch[turn][warp].x = (uint32_t)x;
+            sync();
+            x = 0;
+            for (int w = 0; w < NW; ++w) x += (int)xch[turn][w].x;
+            turn ^= 1;
+        }
+        return x;
+    };
+    auto least_all = [&](uint32_t x, int n) {
+        uint2 r;
+        r.x = __reduce_min_sync(0xffffffffu, x);
+        r.y = __reduce_add_sync(0xffffffffu, x == r.x ? n : 0);
+        if (NW > 1) {
+            if (lane == 0) xch[turn][warp] = r;
+            sync();
+            r = xch[turn][0];
+            for (int w = 1; w < NW; ++w) {
+                const uint2 o = xch[turn][w];
+                if (o.x < r.x) r = o;
+                else if (o.x == r.x) r.y += o.y;
             }
-            __syncthreads();
-            const int digit = found[0];
-            border[word] |= (uint32_t)digit << shift;
-            mask |= (uint32_t)((1 << kEvBits) - 1) << shift;
-            left -= found[1];
-            whole = hist[digit] == left;
-            words = word + 1;
+            turn ^= 1;
+        }
+        return r;
+    };
+    // The value at which the count of `part` over the rows for which `in` holds reaches `left`, which
+    // becomes what is still to be taken of the rows of that value; returns how many those are.
+    auto border = [&](auto part, auto in, int &left, uint32_t &at) {
+        if (left <= kEvTake) {
+            for (bool begun = false;; begun = true) {
+                uint32_t low = 0xffffffffu;
+                int n = 0;
+                for (int j = tid; j < len; j += T) {
+                    if (!in(j)) continue;
+                    const uint32_t x = part(j);
+                    if (begun && x <= at) continue;
+                    if (x < low) {
+                        low = x;
+                        n = 0;
+                    }
+                    n += x == low;
+                }
+                const uint2 r = least_all(low, n);
+                at = r.x;
+                if ((int)r.y >= left) return (int)r.y;
+                left -= (int)r.y;
+            }
+        }
+        at = 0;
+        for (int bit = 31; bit >= 0; --bit) {
+            const uint32_t top = at | (1u << bit);           // rows below it, of those that are not below `at`
+            int n = 0;
+            for (int j = tid; j < len; j += T) {
+                if (!in(j)) continue;
+                const uint32_t x = part(j);
+                n += x >= at && x < top;
+            }
+            n = sum_all(n);
+            if (n < left) {
+                left -= n;
+                at = top;
+            }
+        }
+        int n = 0;
+        for (int j = tid; j < len; j += T) n += in(j) && part(j) == at;
+        return sum_all(n);
+    };
+    // What goes first: small weights, large positions, high rows.
+    auto place = [&](int j) { return ~((uint32_t)ld_dep(pos + j) ^ 0x80000000u); };
+    auto any = [](int) { return true; };
+    int left = E;
+    uint32_t w_at = 0, p_at = 0, r_at = 0;                   // borders: rows at them go, too
+    const bool tied = border(key, any, left, w_at) != left;  // not all rows of that weight go
+    bool twins = false;                                      // nor all of that position among them
+    if (tied) {
+        auto tie = [&](int j) { return key(j) == w_at; };
+        twins = border(place, tie, left, p_at) != left;
+        if (twins) {
+            auto twin = [&](int j) { return key(j) == w_at && place(j) == p_at; };
+            border([](int j) { return ~(uint32_t)j; }, twin, left, r_at);
         }
     }
-    static_assert(kEvThreads == 1 << kEvBits, "a thread has a digit");
-    // Whether row j goes: below the border, or in agreement with it as far as it was settled.
-    auto goes = [&](int j) {
-        for (int w = 0; w < words; ++w) {
-            const uint32_t m = w + 1 == words ? mask : 0xffffffffu;
-            const uint32_t x = part(w, j) & m, y = border[w] & m;
-            if (x != y) return x < y;
-        }
-        return true;
-    };
     // One bit a row, so that weights and positions may move afterwards.
-    uint32_t *gone = kept + p.keep;
     const int nw = (len + 31) / 32;
-    for (int w = warp; w < nw; w += kEvThreads / 32) {
+    for (int w = warp; w < nw; w += NW) {
         const int j = w * 32 + lane;
-        const unsigned m = __ballot_sync(0xffffffffu, j < len && goes(j));
+        bool go = false;
+        if (j < len) {
+            const uint32_t x = key(j);
+            go = x < w_at;
+            if (x == w_at) {
+                const uint32_t y = tied ? place(j) : 0;
+                go = y < p_at || (y == p_at && (!twins || ~(uint32_t)j <= r_at));
+            }
+        }
+        const unsigned m = __ballot_sync(0xffffffffu, go);
         if (lane == 0) gone[w] = m;
     }
-    __syncthreads();
-    // Holes below the budget and the rows to fill them, listed kEvMoves at a time.
-    const int per = 2 * p.vecs, rows = kEvThreads / per, c = tid % per;   // threads of a row of K and V
+    sync();
+    // Holes below the budget and the rows to fill them, listed LIST at a time.
+    const int per = 2 * p.vecs, rows = T / per, c = tid % per;   // threads of a row of K and V
     uint4 *base = (c < p.vecs ? p.kc + c : p.vc + (c - p.vecs)) + row0 * p.vecs;
-    for (int done = 0, holes = 1; done < holes; done += kEvMoves) {
+    for (int done = 0, holes = 1; done < holes; done += LIST) {
         holes = 0;
         int late = 0;                                        // found so far, alike in all threads
-        for (int w0 = 0; w0 < nw; w0 += kEvThreads) {
+        for (int w0 = 0; w0 < nw; w0 += T) {
             const int w = w0 + tid;
             unsigned hole = 0, stay = 0;
             if (w < nw) {
@@ -606,45 +850,66 @@ __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictPara
                     is += y;
                 }
             }
-            if (lane == 31) {
-                wsum[0][warp] = ih;
-                wsum[1][warp] = is;
-            }
-            __syncthreads();
             int ah = holes + ih - ch, as = late + is - cs;
-            for (int x = 0; x < kEvThreads / 32; ++x) {
-                if (x < warp) {
-                    ah += wsum[0][x];
-                    as += wsum[1][x];
+            if (NW == 1) {
+                holes += __shfl_sync(0xffffffffu, ih, 31);
+                late += __shfl_sync(0xffffffffu, is, 31);
+            } else {
+                if (lane == 31) xch[turn][warp] = make_uint2(ih, is);
+                sync();
+                for (int x = 0; x < NW; ++x) {
+                    const uint2 y = xch[turn][x];
+                    if (x < warp) {
+                        ah += (int)y.x;
+                        as += (int)y.y;
+                    }
+                    holes += (int)y.x;
+                    late += (int)y.y;
                 }
-                holes += wsum[0][x];
-                late += wsum[1][x];
+                turn ^= 1;
             }
             for (; hole; hole &= hole - 1, ++ah)
-                if (ah >= done && ah < done + kEvMoves) dst[ah - done] = w * 32 + __ffs(hole) - 1;
+                if (ah >= done && ah < done + LIST) dst[ah - done] = w * 32 + __ffs(hole) - 1;
             for (; stay; stay &= stay - 1, ++as)
-                if (as >= done && as < done + kEvMoves) src[as - done] = w * 32 + __ffs(stay) - 1;
-            __syncthreads();
+                if (as >= done && as < done + LIST) src[as - done] = w * 32 + __ffs(stay) - 1;
         }
-        const int moves = min(holes - done, kEvMoves);       // there are as many holes as rows to fill them
-        for (int i = tid / per; i < moves; i += rows)
-            base[(long long)dst[i] * p.vecs] = ld_dep_u4(base + (long long)src[i] * p.vecs);
-        for (int i = tid; i < moves; i += kEvThreads) {
-            weight[dst[i]] = weight[src[i]];
-            pos[dst[i]] = pos[src[i]];
+        sync();
+        const int moves = min(holes - done, LIST);           // there are as many holes as rows to fill them
+        constexpr int AHEAD = 4;                             // rows under way
+        for (int i = tid / per; i < moves; i += AHEAD * rows) {
+            uint4 x[AHEAD];
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k)
+                if (i + k * rows < moves) x[k] = ld_dep_u4(base + (long long)src[i + k * rows] * p.vecs);
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k)
+                if (i + k * rows < moves) base[(long long)dst[i + k * rows] * p.vecs] = x[k];
         }
-        __syncthreads();
+        for (int i = tid; i < moves; i += T) {
+            weight[dst[i]] = weight_at(src[i]);
+            pos[dst[i]] = ld_dep(pos + src[i]);
+        }
+        sync();
     }
 }
 
 constexpr int kEvKeep = 24 * 1024;       // keys in shared memory at most
 constexpr int kEvMaxRows = 1 << 20;
 
+template <int NW>
+static magicdec_status launch_evict_t(EvictParams &p, cudaStream_t st) {
+    const int sets = kEvWarps / NW, smem = sets * (p.keep + (p.cap + 31) / 32) * 4;      // at most 192 KB
+    if (!magicdec_host::allow_smem_once<heavy_evict_kernel<NW>>(200 * 1024)) return MAGICDEC_ERR_CUDA;
+    return magicdec_host::launch_pdl(heavy_evict_kernel<NW>, dim3((unsigned)((p.items + sets - 1) / sets)),
+                                     dim3(kEvThreads), (size_t)smem, st, p);
+}
+
 magicdec_status launch_heavy_evict(int layers, int B, int H_kv, int D, int cap, const int32_t *len,
                                    const int32_t *seq_len, int budget, int n_sink, int n_recent, uint16_t *kc,
                                    uint16_t *vc, float *weight, int32_t *pos, int32_t *len_out, cudaStream_t st) {
-    if (cap > kEvMaxRows) return MAGICDEC_ERR_UNSUPPORTED;
     EvictParams p{};
+    p.items = (long long)layers * B * H_kv;
+    if (cap > kEvMaxRows || p.items > INT_MAX) return MAGICDEC_ERR_UNSUPPORTED;
     p.kc = reinterpret_cast<uint4 *>(kc);
     p.vc = reinterpret_cast<uint4 *>(vc);
     p.weight = weight;
@@ -661,10 +926,9 @@ magicdec_status launch_heavy_evict(int layers, int B, int H_kv, int D, int cap, 
     p.n_sink = n_sink;
     p.n_recent = n_recent;
     p.keep = cap < kEvKeep ? cap : cap <= kEvMaxRows / 2 ? kEvKeep : kEvKeep / 2;
-    const int smem = (p.keep + (cap + 31) / 32) * 4;         // at most 192 KB
-    if (!magicdec_host::allow_smem_once<heavy_evict_kernel>(200 * 1024)) return MAGICDEC_ERR_CUDA;
-    return magicdec_host::launch_pdl(heavy_evict_kernel, dim3((unsigned)H_kv, (unsigned)B, (unsigned)layers),
-                                     dim3(kEvThreads), (size_t)smem, st, p);
+    // A warp an item, while its CTAs are not fewer than SMs or its rows so few that more warps gain nothing.
+    const bool narrow = cap <= kEvWarpRows && (cap <= 256 || p.items >= magicdec_host::sm_count());
+    return narrow ? launch_evict_t<1>(p, st) : launch_evict_t<kEvWarps>(p, st);
 }
 
 }  // namespace magicdec

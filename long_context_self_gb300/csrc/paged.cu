@@ -129,13 +129,14 @@ __device__ __forceinline__ void norm_head(float (&f)[16], uint4 w0, uint4 w1, fl
 //
 // NORM: query and key heads are normed before the rotation, in the registers that hold them: a
 // lane's 16 squares and log2(LR) shuffles a row, beside loads that bound the kernel as before.
-template <int NT, int LR, bool INTER, bool NORM>
-__global__ void __launch_bounds__(NT) paged_append_kernel(const AppendParams p) {
+template <int NT, int LR, bool INTER, bool NORM, int MINB = NT == 64 ? 12 : 3>
+__global__ void __launch_bounds__(NT, NORM ? MINB : 1) paged_append_kernel(const AppendParams p) {
     constexpr int ROWS = NT / LR;               // rows of a pass
     constexpr int AHEAD = 3;                    // passes loaded together
     __shared__ float2 cs[LR * 8];               // room for d / 2 angles
     __shared__ int par[kApMaxTree];
     __shared__ unsigned turns[kApMaxTree / 32];
+    __shared__ uint4 weight[NORM ? 4 * LR : 1];  // of query heads, then of key heads
     const int b = blockIdx.y, i = blockIdx.x, tid = threadIdx.x;
     pdl_trigger();
     pdl_wait();
@@ -161,6 +162,11 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const AppendParams p) 
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k)
         if (tid / LR + k * ROWS < R) load(tid / LR + k * ROWS, x[k]);
+    const unsigned lanes = (LR == 8 ? 0xffu : 0xfu) << (tid % 32 / LR * LR);     // of a row
+    if (NORM && tid < 4 * LR) {                                     // seen behind the angles' barrier
+        const uint16_t *w = tid < 2 * LR ? p.qw : p.kw;
+        if (w) weight[tid] = ld_dep_u4(reinterpret_cast<const uint4 *>(w) + tid % (2 * LR));
+    }
     const long long dst = pool_row(p.table + (long long)b * p.max_pages, (long long)len + i, p.page_size, p.n_pages,
                                    p.max_pages, tid == 0 ? p.err : nullptr);
     int at = i;                                                     // position after len
@@ -206,18 +212,6 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const AppendParams p) 
     if (turned)
 #pragma unroll
         for (int k = 0; k < 8; ++k) a[k] = cs[l * 8 + k];
-    uint4 qw0{}, qw1{}, kw0{}, kw1{};                               // this lane's channels of the weights
-    const unsigned lanes = (LR == 8 ? 0xffu : 0xfu) << (tid % 32 / LR * LR);     // of a row
-    if (NORM) {
-        if (p.qw && nq) {
-            qw0 = ld_dep_u4(reinterpret_cast<const uint4 *>(p.qw) + v0);
-            qw1 = ld_dep_u4(reinterpret_cast<const uint4 *>(p.qw) + v1);
-        }
-        if (p.kw) {
-            kw0 = ld_dep_u4(reinterpret_cast<const uint4 *>(p.kw) + v0);
-            kw1 = ld_dep_u4(reinterpret_cast<const uint4 *>(p.kw) + v1);
-        }
-    }
     uint16_t *qo = p.q_out + tok * p.H_q * p.d, *ko = p.kp + dst * p.H_kv * p.d - nq * p.d,
              *vo = p.vp + dst * p.H_kv * p.d - nk * p.d;
     for (int r0 = tid / LR; r0 < R; r0 += AHEAD * ROWS) {
@@ -234,7 +228,8 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const AppendParams p) 
             if (NORM && r < nk && (r < nq ? p.qw : p.kw)) {
                 float h[16];
                 unpack16(y, z, h);
-                norm_head<LR>(h, r < nq ? qw0 : kw0, r < nq ? qw1 : kw1, p.eps, lanes);
+                const uint4 *w = weight + (r < nq ? 0 : 2 * LR);
+                norm_head<LR>(h, w[v0], w[v1], p.eps, lanes);
                 if (turned)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {

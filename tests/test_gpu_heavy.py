@@ -81,6 +81,10 @@ ATTN = [
     (8, 2, 128, 1, 20000, [20000, 1, 7777]),
     (10, 2, 128, 5, 12001, [12001, 3000]),
     (2, 1, 64, 1, 100003, [100003]),
+    (4, 1, 128, 1, 300001, [300001, 12345]),
+    (16, 2, 64, 4, 30001, [30001, 3]),
+    (16, 2, 128, 1, 30001, [29999, 3]),
+    (6, 2, 64, 5, 30001, [30001, 6]),
     # more pairs than fill the GPU
     (16, 8, 64, 1, 130, [(b * 37) % 131 for b in range(200)]),
     # lengths out of range are clamped

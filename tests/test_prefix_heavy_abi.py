@@ -98,8 +98,7 @@ def test_heavy_attention_refusals(lib):
     for bad in BAD_DENSE:
         assert call(s=dense(**bad)) == SHAPE, bad
     assert call(n=0) == call(n=-1) == SHAPE
-    for s, n in ((dense(), 9), (dense(H_q=33, H_kv=1), 1), (dense(), 1 << 30), (dense(H_q=65536, H_kv=65536), 1),
-                 (dense(H_q=4, H_kv=1, L_cap=229889), 1), (dense(H_q=32, H_kv=1, L_cap=28673), 1)):
+    for s, n in ((dense(), 9), (dense(H_q=33, H_kv=1), 1), (dense(), 1 << 30), (dense(H_q=65536, H_kv=65536), 1)):
         assert call(s=s, n=n) == UNSUPPORTED, (s.L_cap, n)
     for name in ("q", "kc", "vc", "out"):
         assert call(**{name: ODD}) == ALIGN, name
