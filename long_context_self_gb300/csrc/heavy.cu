@@ -119,6 +119,8 @@ __global__ void __launch_bounds__(128 * MT + 32, MT == 2 ? 1 : 2)
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *ring = smem;
     float *scores = reinterpret_cast<float *>(smem + p.stages * STAGE);     // [R][stride]; later the warps' O
+    constexpr int QHALF = MT * ROWS * 128;              // bytes of 64 channels of the query rows
+    __shared__ __align__(1024) uint8_t qs[HV * QHALF];
     __shared__ uint64_t full[kHvStages], empty[kHvStages];
     __shared__ float2 wstat[CW][16];                    // of a warp's rows: (max, sum)
     __shared__ float2 cstat[32];                        // of this CTA
@@ -139,6 +141,13 @@ __global__ void __launch_bounds__(128 * MT + 32, MT == 2 ? 1 : 2)
     }
     pdl_trigger();
     pdl_wait();
+    // The query rows (row i * G + g: token i, head g of the group), swizzled as the keys.
+    for (int x = tid; x < MT * ROWS * (D / 8); x += NT) {
+        const int r = x / (D / 8), c = x % (D / 8), i = r / p.G;
+        const uint16_t *src = p.q + (((long long)b * p.n + i) * p.H_q + h * p.G + (r - i * p.G)) * D + c * 8;
+        *reinterpret_cast<uint4 *>(qs + (c >> 3) * QHALF + swz128(r, c & 7)) =
+            r < p.R ? ld_dep_u4(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
+    }
     __syncthreads();
     const int len0 = checked(ld_dep(p.len + b), 0, p.cap, p.err);
     const int len = len0 < 0 ? 0 : (len0 > p.cap ? p.cap : len0);
@@ -181,27 +190,21 @@ __global__ void __launch_bounds__(128 * MT + 32, MT == 2 ? 1 : 2)
     float o[NB][2 * HR];
     float m[HR], l[HR];
     uint32_t qf[KS][2 * HR];
-    // The fragments of query rows 16 tile .. (row i * G + g: token i, head g of the group).
+    // The fragments of query rows 16 tile .. , as mma.sync takes them.
     auto load_q = [&](int tile, uint32_t (&to)[KS][2 * HR]) {
+        const uint32_t at = smem_u32(qs) + (uint32_t)tile * 2048;
 #pragma unroll
-        for (int e = 0; e < HR; ++e) {
-            const int r = tile * 16 + lr + 8 * e, i = r / p.G;
-            const unsigned *src = reinterpret_cast<const unsigned *>(
-                p.q + (((long long)b * p.n + i) * p.H_q + h * p.G + (r - i * p.G)) * D);
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                to[s][e] = r < p.R ? ld_dep_u32(src + s * 8 + lq) : 0u;
-                to[s][HR + e] = r < p.R ? ld_dep_u32(src + s * 8 + 4 + lq) : 0u;
-            }
+        for (int c = 0; c < KS; c += 3 - HR) {
+            if constexpr (HR == 2)
+                ldsm_x4(at + (uint32_t)(c >> 2) * QHALF + swz128(lane & 15, (c & 3) * 2 + (lane >> 4)), to[c][0], to[c][1],
+                        to[c][2], to[c][3]);
+            else
+                ldsm_x4(at + (uint32_t)(c >> 2) * QHALF + swz128(lane & 7, (c & 3) * 2 + (lane >> 3)), to[c][0], to[c][1],
+                        to[c + 1][0], to[c + 1][1]);
         }
     };
     // Query row r sees keys below this.
     auto seen = [&](int r) { return r < p.R ? min(len - p.n + 1 + r / p.G, k1) : 0; };
-    // 8 keys' fragments for 32 channels, or 16 keys' for 16: rows r .. of the K tile at `at`.
-    auto k_addr = [&](uint32_t at, int row, int chunk) {
-        return at + (uint32_t)(chunk >> 3) * kHvHalf + swz128(row, chunk & 7);
-    };
-
     if (warp == CW) {
         if (lane == 0) {
             produce(0, tiles, 0, true);
@@ -223,7 +226,11 @@ __global__ void __launch_bounds__(128 * MT + 32, MT == 2 ? 1 : 2)
             for (int e = 0; e < 2 * HR; ++e) o[j][e] = 0.f;
         // The scores' place: row r of this warp's tile, key g.
         float *my = scores + (long long)(mt * 16 + lr) * p.stride - k0;
+        // A lane's address in a K tile, and in a V tile: 16-byte chunk c of its row is at c * 16 away from
+        // chunk 0 in the sense of an exclusive or (8 chunks a half).
         const int x4 = lane >> 3, r0 = 16 * kw;
+        const uint32_t k_lane = swz128(r0 + (x4 >> 1) * 8 + (lane & 7), x4 & 1);
+        const uint32_t v_lane = swz128(r0 + (x4 & 1) * 8 + (lane & 7), x4 >> 1);
         for (int t = 0; t < tiles; ++t) {
             const uint32_t st = (uint32_t)t % p.stages, kt = smem_u32(ring + st * STAGE), vt = kt + OPER;
             ok = hv_wait(&full[st], (uint32_t)t / p.stages & 1, p.err, ok, lane);
@@ -238,7 +245,7 @@ __global__ void __launch_bounds__(128 * MT + 32, MT == 2 ? 1 : 2)
 #pragma unroll
                 for (int c = 0; c < KS; ++c) {
                     uint32_t f0, f1, f2, f3;
-                    ldsm_x4(k_addr(kt, r0 + (x4 >> 1) * 8 + (lane & 7), c * 2 + (x4 & 1)), f0, f1, f2, f3);
+                    ldsm_x4(((kt + k_lane) ^ ((c & 3) * 32)) + (c >> 2) * kHvHalf, f0, f1, f2, f3);
                     hv_mma<HR>(c & 1 ? s2[0] : s[0], qf[c], f0, f1);
                     hv_mma<HR>(c & 1 ? s2[1] : s[1], qf[c], f2, f3);
                 }
@@ -339,7 +346,7 @@ __global__ void __launch_bounds__(128 * MT + 32, MT == 2 ? 1 : 2)
 #pragma unroll
                     for (int j = 0; j < NB; j += 2) {
                         uint32_t f0, f1, f2, f3;
-                        ldsm_x4_trans(k_addr(vt, r0 + (x4 & 1) * 8 + (lane & 7), j + (x4 >> 1)), f0, f1, f2, f3);
+                        ldsm_x4_trans(((vt + v_lane) ^ ((j & 7) * 16)) + (j >> 3) * kHvHalf, f0, f1, f2, f3);
                         hv_mma<HR>(o[j], a, f0, f1);
                         hv_mma<HR>(o[j + 1], a, f2, f3);
                     }
@@ -435,6 +442,7 @@ __global__ void __launch_bounds__(128 * MT + 32, MT == 2 ? 1 : 2)
                     see[x][e] = seen(x * 16 + lr + 8 * e);
                 }
             }
+            const uint32_t k_lane = swz128(warp * 8 * KN + (lane & 7), lane >> 3);
             for (int t = 0; t < tiles; ++t) {
                 const uint32_t slot = tiles + t, st = slot % p.stages, kt = smem_u32(ring + st * STAGE);
                 const int g = k0 + t * kHvKeys + warp * 8 * KN;
@@ -458,7 +466,7 @@ __global__ void __launch_bounds__(128 * MT + 32, MT == 2 ? 1 : 2)
 #pragma unroll
                         for (int c = 0; c < KS; c += 2) {
                             uint32_t f0, f1, f2, f3;
-                            ldsm_x4(k_addr(kt, warp * 8 * KN + nb * 8 + (lane & 7), c * 2 + (lane >> 3)), f0, f1, f2, f3);
+                            ldsm_x4(((kt + k_lane + nb * 1024) ^ ((c & 3) * 32)) + (c >> 2) * kHvHalf, f0, f1, f2, f3);
 #pragma unroll
                             for (int x = 0; x < MT; ++x) {
                                 hv_mma<HR>(s[x], q2[x][c], f0, f1);
@@ -523,6 +531,7 @@ __global__ void __launch_bounds__(128 * MT + 32, MT == 2 ? 1 : 2)
 // ----------------------------------------------------------------- host side
 constexpr int kHvMaxCluster = 8;
 constexpr int kHvScores = 40 * 1024;     // scores of a CTA that stay in shared memory
+constexpr int kHvStatic = 11 * 1024;     // room for the query rows and what else is not sized by the call
 
 struct HeavyPlan {
     int C, stages, stride;
@@ -554,7 +563,8 @@ static HeavyPlan heavy_plan(int pairs, int cap, int R, int D) {
     z.stride = z.again ? 0 : (int)stride;
     const long long rest = (z.again || o > scores ? o : scores), stage = D / 64 * 2ll * kHvHalf;
     // Two CTAs an SM (one with more than 16 query rows, whose registers fill it).
-    const long long room = (R > 16 ? magicdec_host::max_smem_optin() : magicdec_host::max_smem_optin() / 2) - 4096 - rest;
+    const long long room = (R > 16 ? magicdec_host::max_smem_optin() - kHvStatic
+                                   : magicdec_host::max_smem_optin() / 2 - kHvStatic * 3 / 4) - rest;
     long long stages = room / stage, tiles = (per + kHvKeys - 1) / kHvKeys * (z.again ? 2 : 1);
     if (stages > kHvStages) stages = kHvStages;
     if (stages > tiles) stages = tiles;
@@ -566,7 +576,7 @@ static HeavyPlan heavy_plan(int pairs, int cap, int R, int D) {
 template <int D, int ROWS, int MT, bool AGAIN>
 static magicdec_status launch_heavy_t(const CUtensorMap (&tm)[4], const HeavyParams &p, const HeavyPlan &z,
                                       cudaStream_t st) {
-    if (!magicdec_host::allow_smem_once<heavy_attn_kernel<D, ROWS, MT, AGAIN>>(magicdec_host::max_smem_optin() - 3072))
+    if (!magicdec_host::allow_smem_once<heavy_attn_kernel<D, ROWS, MT, AGAIN>>(magicdec_host::max_smem_optin() - kHvStatic))
         return MAGICDEC_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)z.C, (unsigned)p.H_kv, (unsigned)p.B);
