@@ -7,7 +7,7 @@
 #include <cfloat>
 #include <climits>
 
-#include "common.cuh"
+#include "few_rows.cuh"
 
 namespace magicdec {
 
@@ -30,7 +30,6 @@ namespace magicdec {
 constexpr int kHvKeys = 64;          // keys of a stage
 constexpr int kHvHalf = kHvKeys * 128;   // bytes of 64 channels of them
 constexpr int kHvStages = 8;         // stages of a ring at most
-constexpr float kHvLazy = 24.0f;     // log2 growth of a row's maximum that is put up with
 
 struct HeavyParams {
     const uint16_t *q;
@@ -44,67 +43,6 @@ struct HeavyParams {
     int stages;                      // of the ring
     float scale_log2;                // log2(e) / sqrt(d)
 };
-
-__device__ __forceinline__ uint32_t hv_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t hv_ctas() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void hv_cluster_sync() {
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The address of `p` in the shared memory of CTA `rank` of the cluster, and loads from there.
-__device__ __forceinline__ uint32_t hv_at(const void *p, uint32_t rank) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-    return a;
-}
-__device__ __forceinline__ float2 hv_ld2(uint32_t a) {
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ float4 hv_ld4(uint32_t a) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(a)
-                 : "memory");
-    return v;
-}
-// A warp's wait, with one outcome for all lanes; once one has given up, the later ones return at once.
-__device__ __forceinline__ bool hv_wait(uint64_t *bar, uint32_t parity, int *err, bool ok, int lane) {
-    if (__all_sync(0xffffffffu, ok && mbar_try_sleep(bar, parity))) return true;
-    int got = ok ? 1 : 0;
-    if (ok && lane == 0) got = mbar_poll_on(bar, parity, err) ? 1 : 0;
-    return __shfl_sync(0xffffffffu, got, 0) != 0;
-}
-
-// D(16x8) += A(16x16) B(16x8); with 8 real rows (HR = 1) the lower half of A and of D is not there.
-template <int HR>
-__device__ __forceinline__ void hv_mma(float (&c)[2 * HR], const uint32_t (&a)[2 * HR], uint32_t b0, uint32_t b1) {
-    if constexpr (HR == 2) {
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-            "{%0,%1,%2,%3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    } else {
-        asm volatile(
-            "{\n\t.reg .f32 x, y;\n\t"
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,x,y}, {%2,%3,%4,%5}, {%6,%7}, "
-            "{%0,%1,%8,%8};\n\t}"
-            : "+f"(c[0]), "+f"(c[1])
-            : "r"(a[0]), "r"(0u), "r"(a[1]), "r"(0u), "r"(b0), "r"(b1), "f"(0.f));
-    }
-}
 
 // ROWS: query rows of a warp's tile that can be real, 8 or 16; MT: row tiles (a warp has one).
 template <int D, int ROWS, int MT, bool AGAIN>
@@ -128,7 +66,7 @@ __global__ void __launch_bounds__(128 * MT + 32, MT == 2 ? 1 : 2)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int lq = lane & 3, lr = lane >> 2;
     const int b = blockIdx.z, h = blockIdx.y;
-    const uint32_t rank = hv_rank(), C = hv_ctas();
+    const uint32_t rank = few_rank(), C = few_ctas();
     const float sl = p.scale_log2;
     if (tid == 0) {
         for (int s = 0; s < p.stages; ++s) {
@@ -233,7 +171,7 @@ __global__ void __launch_bounds__(128 * MT + 32, MT == 2 ? 1 : 2)
         const uint32_t v_lane = swz128(r0 + (x4 & 1) * 8 + (lane & 7), x4 >> 1);
         for (int t = 0; t < tiles; ++t) {
             const uint32_t st = (uint32_t)t % p.stages, kt = smem_u32(ring + st * STAGE), vt = kt + OPER;
-            ok = hv_wait(&full[st], (uint32_t)t / p.stages & 1, p.err, ok, lane);
+            ok = few_wait(&full[st], (uint32_t)t / p.stages & 1, p.err, ok, lane);
             const int g = k0 + t * kHvKeys + r0;
             if (g < k1) {
                 // Two chains of products a score, so that half as many wait for one another.
@@ -246,8 +184,8 @@ __global__ void __launch_bounds__(128 * MT + 32, MT == 2 ? 1 : 2)
                 for (int c = 0; c < KS; ++c) {
                     uint32_t f0, f1, f2, f3;
                     ldsm_x4(((kt + k_lane) ^ ((c & 3) * 32)) + (c >> 2) * kHvHalf, f0, f1, f2, f3);
-                    hv_mma<HR>(c & 1 ? s2[0] : s[0], qf[c], f0, f1);
-                    hv_mma<HR>(c & 1 ? s2[1] : s[1], qf[c], f2, f3);
+                    few_mma<HR>(c & 1 ? s2[0] : s[0], qf[c], f0, f1);
+                    few_mma<HR>(c & 1 ? s2[1] : s[1], qf[c], f2, f3);
                 }
                 // Keys that not every row sees: behind the last one, or of the block's own tokens.
                 const bool edge = g + 16 > len - p.n + 1 || g + 16 > k1;
@@ -272,10 +210,10 @@ __global__ void __launch_bounds__(128 * MT + 32, MT == 2 ? 1 : 2)
                         top[e] = fmaxf(top[e], fmaxf(x, y));
                     }
                 // The maximum moves, and O and the sum are scaled, only where it has grown by more than
-                // 2^kHvLazy: weights up to 2^24 instead of 1 cost a floating sum nothing.
+                // 2^kFewLazy: weights up to 2^24 instead of 1 cost a floating sum nothing.
                 bool move = false;
 #pragma unroll
-                for (int e = 0; e < HR; ++e) move |= top[e] > m[e] + kHvLazy;
+                for (int e = 0; e < HR; ++e) move |= top[e] > m[e] + kFewLazy;
                 if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
                     for (int e = 0; e < HR; ++e) {
@@ -347,8 +285,8 @@ __global__ void __launch_bounds__(128 * MT + 32, MT == 2 ? 1 : 2)
                     for (int j = 0; j < NB; j += 2) {
                         uint32_t f0, f1, f2, f3;
                         ldsm_x4_trans(((vt + v_lane) ^ ((j & 7) * 16)) + (j >> 3) * kHvHalf, f0, f1, f2, f3);
-                        hv_mma<HR>(o[j], a, f0, f1);
-                        hv_mma<HR>(o[j + 1], a, f2, f3);
+                        few_mma<HR>(o[j], a, f0, f1);
+                        few_mma<HR>(o[j + 1], a, f2, f3);
                     }
                 }
             }
@@ -375,12 +313,12 @@ __global__ void __launch_bounds__(128 * MT + 32, MT == 2 ? 1 : 2)
         for (int w = 0; w < CW / MT; ++w) join(s, wstat[w * MT + tid / 16][tid % 16]);
         cstat[tid] = s;
     }
-    if (C > 1) hv_cluster_sync();
+    if (C > 1) few_cluster_sync();
     if (tid < 32) {
         float2 s = make_float2(-INFINITY, 0.f);
         if (tid < p.R) {
             if (C > 1)
-                for (uint32_t c = 0; c < C; ++c) join(s, hv_ld2(hv_at(&cstat[tid], c)));
+                for (uint32_t c = 0; c < C; ++c) join(s, few_ld2(few_at(&cstat[tid], c)));
             else
                 s = cstat[tid];
         }
@@ -454,7 +392,7 @@ __global__ void __launch_bounds__(128 * MT + 32, MT == 2 ? 1 : 2)
                         const int key = g + nb * 8 + 2 * lq + x;
                         old[nb][x] = lr == 0 && key < k1 ? p.weight[row0 + key] : 0.f;
                     }
-                ok = hv_wait(&full[st], slot / p.stages & 1, p.err, ok, lane);
+                ok = few_wait(&full[st], slot / p.stages & 1, p.err, ok, lane);
                 if (g < k1) {
 #pragma unroll
                     for (int nb = 0; nb < KN; ++nb) {
@@ -469,8 +407,8 @@ __global__ void __launch_bounds__(128 * MT + 32, MT == 2 ? 1 : 2)
                             ldsm_x4(((kt + k_lane + nb * 1024) ^ ((c & 3) * 32)) + (c >> 2) * kHvHalf, f0, f1, f2, f3);
 #pragma unroll
                             for (int x = 0; x < MT; ++x) {
-                                hv_mma<HR>(s[x], q2[x][c], f0, f1);
-                                hv_mma<HR>(s[x], q2[x][c + 1], f2, f3);
+                                few_mma<HR>(s[x], q2[x][c], f0, f1);
+                                few_mma<HR>(s[x], q2[x][c + 1], f2, f3);
                             }
                         }
                         const int key = g + nb * 8 + 2 * lq;
@@ -505,16 +443,16 @@ __global__ void __launch_bounds__(128 * MT + 32, MT == 2 ? 1 : 2)
     }
     __syncwarp();
     // O summed over the warps and the CTAs, each of which has a share of the channels.
-    if (C > 1) hv_cluster_sync();
+    if (C > 1) few_cluster_sync();
     else __syncthreads();
     const int vecs = p.R * (D / 4), share = (vecs + (int)C - 1) / (int)C;
     for (int i = (int)rank * share + tid; i < min(vecs, (int)(rank + 1) * share); i += NT) {
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         for (uint32_t c = 0; c < C; ++c) {
-            const uint32_t base = hv_at(osum, c);
+            const uint32_t base = few_at(osum, c);
 #pragma unroll
             for (int w = 0; w < CW / MT; ++w) {
-                const float4 x = hv_ld4(base + (uint32_t)(w * vecs + i) * 16);
+                const float4 x = few_ld4(base + (uint32_t)(w * vecs + i) * 16);
                 s.x += x.x;
                 s.y += x.y;
                 s.z += x.z;
@@ -525,7 +463,7 @@ __global__ void __launch_bounds__(128 * MT + 32, MT == 2 ? 1 : 2)
         *reinterpret_cast<uint2 *>(p.out + (((long long)b * p.n + t) * p.H_q + h * p.G + (r - t * p.G)) * D + c4 * 4) =
             make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
     }
-    if (C > 1) hv_cluster_sync();                       // no CTA ends while another reads its O
+    if (C > 1) few_cluster_sync();                       // no CTA ends while another reads its O
 }
 
 // ----------------------------------------------------------------- host side

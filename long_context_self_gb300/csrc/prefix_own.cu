@@ -1,0 +1,385 @@
+// prefix_own.cu -- attention of up to 32 query rows of a KV head over a sequence's own slots behind
+// a shared prefix, joined with the prefix's parts (sm_103a).
+//
+// A cluster of C CTAs takes a (sequence, KV head), each a stretch of its slots; at the end the
+// CTAs exchange (max, sum), sum the warps' O in a fixed order, add the parts that
+// tree_attn_kernel left of the prefix, and write the output: no parts of their own go through
+// memory.  Bound: HBM, 4 d bytes a slot and KV head.  Many small CTAs, two or more an SM, so that
+// one's way in and out runs beside another's keys: as entries of tree_attn_kernel's list, a CTA an
+// SM with one entry after another, each took some 8 us (1024 of 1 slot 60 us, of 500 slots 131 us).
+//
+// All warps fill the ring, 16 bytes a thread from any rows of the pool (page sizes need no
+// care, rows that hold nothing are filled with zeros), and take 16 keys of a stage of 64
+// through ldmatrix and mma.sync, with more than 16 query rows two warps the same keys.
+//
+// The kernel before it in the stream is tree_attn_kernel, which lets it begin when all of
+// its CTAs have waited for what was before them: everything but the prefixes' parts is there.
+#include <climits>
+
+#include "few_rows.cuh"
+#include "prefix.cuh"
+
+namespace magicdec {
+
+constexpr int kPoKeys = 64;              // keys of a stage
+constexpr int kPoHalf = kPoKeys * 128;   // bytes of 64 channels of them
+constexpr int kPoMaxCluster = 8;
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// ROWS: query rows of a warp's tile that can be real, 8 or 16; MT: row tiles (a warp has one).
+template <int D, int ROWS, int MT>
+struct PoShape {
+    static constexpr int WARPS = 4 * MT, NT = WARPS * 32;
+    static constexpr int HV = D / 64, OPER = HV * kPoHalf, STAGE = 2 * OPER;
+    // Two CTAs an SM; with 32 rows of 128 channels, whose registers fill it, one.
+    static constexpr int PER_SM = MT == 2 && D == 128 ? 1 : 2;
+    static constexpr int STAGES = D == 128 ? (PER_SM == 1 ? 6 : 3) : 6;
+    static constexpr int QHALF = MT * ROWS * 128;
+    static constexpr int BYTES = STAGES * STAGE + HV * QHALF;
+    static_assert(4 * MT * ROWS * D * 4 <= STAGES * STAGE, "the warps' O take the ring's place");
+};
+
+template <int D, int ROWS, int MT>
+__global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>::PER_SM)
+    prefix_own_kernel(const PreOwn p) {
+    using L = PoShape<D, ROWS, MT>;
+    constexpr int NT = L::NT, OPER = L::OPER, STAGE = L::STAGE, NST = L::STAGES, QHALF = L::QHALF;
+    constexpr int KS = D / 16, NB = D / 8, HR = ROWS / 8, VR = D / 8;   // VR: 16-byte words of a row
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *ring = smem, *qs = smem + NST * STAGE;
+    __shared__ long long rows_at[2][kPoKeys];           // of a tile's keys: element of the pool, or -1
+    __shared__ int par[32];
+    __shared__ uint32_t sees[32];                       // of a node's slots: itself and its ancestors
+    __shared__ float2 wstat[L::WARPS][16];              // of a warp's rows: (max, sum)
+    __shared__ float2 cstat[32];                        // of this CTA
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int lq = lane & 3, lr = lane >> 2;
+    const int b = blockIdx.z, h = blockIdx.y, n = p.pre.n, G = p.pre.G, R = n * G;
+    const uint32_t rank = few_rank(), C = few_ctas();
+    const float sl = p.scale_log2;
+    pdl_trigger();
+    // Not behind a wait: see above.
+    const int cap = p.page_size * p.max_pages;
+    const int len = pre_clamp(checked(ld_dep(p.len + b), 0, cap, p.err), cap);
+    const int nodes = p.n_nodes ? pre_clamp(checked(ld_dep(p.n_nodes + b), 0, n, p.err), n) : n;
+    const int total = nodes ? (nodes > cap - len ? cap : len + nodes) : 0;
+    // This CTA's keys: [k0, k1), in groups of 16.
+    const int per = ((total + (int)C - 1) / (int)C + 15) & ~15;
+    const int k0 = min(total, (int)rank * per), k1 = min(total, k0 + per), tiles = (k1 - k0 + kPoKeys - 1) / kPoKeys;
+    // The query rows (row i * G + g: node i, head g of the group), swizzled as the keys.
+    for (int x = tid; x < MT * ROWS * VR; x += NT) {
+        const int r = x / VR, c = x % VR, i = r / G;
+        const uint16_t *src = p.q + (((long long)b * n + i) * p.H_q + h * G + (r - i * G)) * D + c * 8;
+        *reinterpret_cast<uint4 *>(qs + (c >> 3) * QHALF + swz128(r, c & 7)) =
+            r < R ? ld_dep_u4(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
+    }
+    if (p.parent && tid < n)
+        par[tid] = checked(ld_dep(p.parent + (long long)b * n + tid), INT_MIN, tid - 1, p.err);
+    // Where a tile's keys lie; one outside the pool is zeros.
+    const int32_t *table = p.table + (long long)b * p.max_pages;
+    auto look_up = [&](int t) {
+        if (tid < kPoKeys) {
+            const int key = k0 + t * kPoKeys + tid;
+            long long at = -1;
+            if (key < k1) {
+                const int pg = key / p.page_size, id = ld_dep(table + pg);
+                if (id < 0 || id >= p.n_pages) raise_error(p.err, kErrPage);
+                else at = (((long long)id * p.page_size + (key - pg * p.page_size)) * p.pre.H_kv + h) * D;
+            }
+            rows_at[t & 1][tid] = at;
+        }
+    };
+    auto load = [&](int t) {
+        if (t < tiles) {
+            const uint32_t to = smem_u32(ring + t % NST * STAGE);
+#pragma unroll
+            for (int x = 0; x < kPoKeys * VR; x += NT) {
+                const int r = (x + tid) / VR, c = (x + tid) % VR;
+                const long long at = rows_at[t & 1][r];
+                const long long from = (at < 0 ? 0 : at) + c * 8;
+                const uint32_t dst = to + (uint32_t)(c >> 3) * kPoHalf + swz128(r, c & 7);
+                copy16(dst, p.k + from, at >= 0);
+                copy16(dst + OPER, p.v + from, at >= 0);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    look_up(0);
+    __syncthreads();
+    if (tid < n) {
+        uint32_t m = 0;
+        for (int a = tid; a >= 0;) {
+            m |= 1u << a;
+            const int q = p.parent ? par[a] : a - 1;
+            a = q < a ? q : -1;
+        }
+        sees[tid] = m;
+    }
+#pragma unroll 1
+    for (int t = 0; t + 1 < NST; ++t) {
+        look_up(t + 1);
+        load(t);
+        __syncthreads();
+    }
+
+    const int mt = MT == 1 ? 0 : warp % MT, kw = warp / MT;
+    uint32_t qf[KS][2 * HR];
+    float o[NB][2 * HR], m[HR], l[HR];
+    uint32_t anc[HR];
+#pragma unroll
+    for (int e = 0; e < HR; ++e) {
+        const int r = mt * 16 + lr + 8 * e;
+        anc[e] = r < R ? sees[r / G] : 0u;
+        m[e] = -INFINITY;
+        l[e] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int e = 0; e < 2 * HR; ++e) o[j][e] = 0.f;
+#pragma unroll
+    for (int c = 0; c < KS; c += 3 - HR) {
+        const uint32_t at = smem_u32(qs) + (uint32_t)mt * 2048 + (uint32_t)(c >> 2) * QHALF;
+        if constexpr (HR == 2)
+            ldsm_x4(at + swz128(lane & 15, (c & 3) * 2 + (lane >> 4)), qf[c][0], qf[c][1], qf[c][2], qf[c][3]);
+        else
+            ldsm_x4(at + swz128(lane & 7, (c & 3) * 2 + (lane >> 3)), qf[c][0], qf[c][1], qf[c + 1][0], qf[c + 1][1]);
+    }
+    // A lane's address in a K tile, and in a V tile: 16-byte chunk c of its row is at c * 16 away from
+    // chunk 0 in the sense of an exclusive or (8 chunks a half).
+    const int x4 = lane >> 3, r0 = 16 * kw;
+    const uint32_t k_lane = swz128(r0 + (x4 >> 1) * 8 + (lane & 7), x4 & 1);
+    const uint32_t v_lane = swz128(r0 + (x4 & 1) * 8 + (lane & 7), x4 >> 1);
+    for (int t = 0; t < tiles; ++t) {
+        copies_wait<NST - 2>();
+        __syncthreads();                                // tile t is there, and all are done with tile t - 1
+        load(t + NST - 1);
+        look_up(t + NST);
+        const uint32_t kt = smem_u32(ring + t % NST * STAGE), vt = kt + OPER;
+        const int g = k0 + t * kPoKeys + r0;
+        if (g >= k1) continue;
+        // Two chains of products a score, so that half as many wait for one another.
+        float s[2][2 * HR], s2[2][2 * HR];
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2 * HR; ++e) s[nb][e] = s2[nb][e] = 0.f;
+#pragma unroll
+        for (int c = 0; c < KS; ++c) {
+            uint32_t f0, f1, f2, f3;
+            ldsm_x4(((kt + k_lane) ^ ((c & 3) * 32)) + (c >> 2) * kPoHalf, f0, f1, f2, f3);
+            few_mma<HR>(c & 1 ? s2[0] : s[0], qf[c], f0, f1);
+            few_mma<HR>(c & 1 ? s2[1] : s[1], qf[c], f2, f3);
+        }
+        // Keys that not every row sees: behind the last one, or of the nodes.
+        const bool edge = g + 16 > len || g + 16 > k1;
+        auto hidden = [&](int key, uint32_t mask) {
+            return key >= k1 || (key >= len && !(mask >> (key - len) & 1u));
+        };
+        float top[HR];
+#pragma unroll
+        for (int e = 0; e < HR; ++e) top[e] = -INFINITY;
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+            for (int e = 0; e < HR; ++e) {
+                float &x = s[nb][2 * e], &y = s[nb][2 * e + 1];
+                x = (x + s2[nb][2 * e]) * sl;
+                y = (y + s2[nb][2 * e + 1]) * sl;
+                if (edge) {
+                    const int key = g + nb * 8 + 2 * lq;
+                    if (hidden(key, anc[e])) x = -INFINITY;
+                    if (hidden(key + 1, anc[e])) y = -INFINITY;
+                }
+                top[e] = fmaxf(top[e], fmaxf(x, y));
+            }
+        // The maximum moves, and O and the sum are scaled, only where it has grown by more than
+        // 2^kFewLazy: weights up to 2^24 instead of 1 cost a floating sum nothing.
+        bool move = false;
+#pragma unroll
+        for (int e = 0; e < HR; ++e) move |= top[e] > m[e] + kFewLazy;
+        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+            for (int e = 0; e < HR; ++e) {
+                top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+                top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+                const float to = fmaxf(m[e], top[e]);
+                const float f = to == -INFINITY ? 1.f : fast_exp2(m[e] - to);
+                m[e] = to;
+                l[e] *= f;
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    o[j][2 * e] *= f;
+                    o[j][2 * e + 1] *= f;
+                }
+            }
+        }
+        // P in bf16 for the second product: off by at most 2^-8 of itself, as the output's
+        // rounding; the sum is of the unrounded values.
+        uint32_t a[2 * HR];
+#pragma unroll
+        for (int e = 0; e < HR; ++e) {
+            const float mu = m[e] == -INFINITY ? 0.f : m[e];
+#pragma unroll
+            for (int nb = 0; nb < 2; ++nb) {
+                const float x = fast_exp2(s[nb][2 * e] - mu), y = fast_exp2(s[nb][2 * e + 1] - mu);
+                s[nb][2 * e] = x;
+                s[nb][2 * e + 1] = y;
+                l[e] += x + y;
+                a[nb * HR + e] = pack_bf16(x, y);
+            }
+        }
+        if (n > 1 && g + 16 > len) {
+            // Keys of nodes, which others than their descendants must not see whatever they hold
+            // (0 * inf is NaN): by scalars, and only where a row sees them.
+            const int last = min(16, k1 - g);
+            for (int x = 0; x < last; ++x) {
+                const int from = (lane & ~3) | ((x & 7) >> 1);
+                float w[HR];
+#pragma unroll
+                for (int e = 0; e < HR; ++e) {
+                    const float even = x < 8 ? s[0][2 * e] : s[1][2 * e];
+                    const float odd = x < 8 ? s[0][2 * e + 1] : s[1][2 * e + 1];
+                    w[e] = __shfl_sync(0xffffffffu, x & 1 ? odd : even, from);
+                }
+                const uint8_t *v = ring + t % NST * STAGE + OPER;
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    const uint32_t z =
+                        *reinterpret_cast<const uint32_t *>(v + (j >> 3) * kPoHalf + swz128(r0 + x, j & 7) + 4 * lq);
+#pragma unroll
+                    for (int e = 0; e < HR; ++e)
+                        if (!hidden(g + x, anc[e])) {
+                            o[j][2 * e] = fmaf(w[e], __uint_as_float(z << 16), o[j][2 * e]);
+                            o[j][2 * e + 1] = fmaf(w[e], __uint_as_float(z & 0xffff0000u), o[j][2 * e + 1]);
+                        }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NB; j += 2) {
+                uint32_t f0, f1, f2, f3;
+                ldsm_x4_trans(((vt + v_lane) ^ ((j & 7) * 16)) + (j >> 3) * kPoHalf, f0, f1, f2, f3);
+                few_mma<HR>(o[j], a, f0, f1);
+                few_mma<HR>(o[j + 1], a, f2, f3);
+            }
+        }
+    }
+    // The warps' maxima and sums, and the CTA's.
+#pragma unroll
+    for (int e = 0; e < HR; ++e) {
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+        if (lq == 0) wstat[warp][lr + 8 * e] = make_float2(m[e], l[e]);
+    }
+    copies_wait<0>();
+    __syncthreads();
+    auto join = [](float2 &s, float2 x) {
+        const float mx = fmaxf(s.x, x.x), mu = mx == -INFINITY ? 0.f : mx;
+        s = make_float2(mx, s.y * fast_exp2(s.x - mu) + x.y * fast_exp2(x.x - mu));
+    };
+    if (tid < R) {
+        float2 s = make_float2(-INFINITY, 0.f);
+        for (int w = 0; w < L::WARPS / MT; ++w) join(s, wstat[w * MT + tid / 16][tid % 16]);
+        cstat[tid] = s;
+    }
+    __syncthreads();
+    // The warps' O, at the CTA's maximum.
+    float *osum = reinterpret_cast<float *>(ring);      // [WARPS / MT][R][D]
+#pragma unroll
+    for (int e = 0; e < HR; ++e) {
+        const int r = mt * 16 + lr + 8 * e;
+        if (r >= R) continue;
+        const float f = m[e] == -INFINITY ? 0.f : fast_exp2(m[e] - cstat[r].x);
+        float *to = osum + (kw * R + r) * D + 2 * lq;
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            *reinterpret_cast<float2 *>(to + j * 8) = make_float2(o[j][2 * e] * f, o[j][2 * e + 1] * f);
+    }
+    if (C > 1) few_cluster_sync();
+    else __syncthreads();
+    // The CTAs' O, each a share of the channels, with the prefix's parts.
+    pdl_wait();
+    const int vecs = R * (D / 4), share = (vecs + (int)C - 1) / (int)C;
+    for (int i = (int)rank * share + tid; i < min(vecs, (int)(rank + 1) * share); i += NT) {
+        const int r = i / (D / 4), c4 = i - r * (D / 4), t = r / G;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float2 st = make_float2(-INFINITY, 0.f);
+        auto add = [&](float2 x, float4 y) {
+            const float mx = fmaxf(st.x, x.x), mu = mx == -INFINITY ? 0.f : mx;
+            const float f = fast_exp2(st.x - mu), w = fast_exp2(x.x - mu);
+            st = make_float2(mx, st.y * f + x.y * w);
+            acc = make_float4(acc.x * f + y.x * w, acc.y * f + y.y * w, acc.z * f + y.z * w, acc.w * f + y.w * w);
+        };
+        if (t < nodes) {
+            const RowParts parts = pre_parts(p.pre, b, t, r - t * G, h);
+#pragma unroll 4
+            for (int k = 0; k < parts.count; ++k) {
+                const long long at = parts.tile + (long long)k * parts.step;
+                const float2 x = p.pre.stat[at * 128 + parts.row];
+                add(make_float2(x.x * sl, x.y), p.pre.part[(at * (D / 4) + c4) * 128 + parts.row]);
+            }
+            for (uint32_t c = 0; c < C; ++c) {
+                const uint32_t base = few_at(osum, c);
+                float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < L::WARPS / MT; ++w) {
+                    const float4 x = few_ld4(base + (uint32_t)(w * vecs + i) * 16);
+                    s = make_float4(s.x + x.x, s.y + x.y, s.z + x.z, s.w + x.w);
+                }
+                add(few_ld2(few_at(&cstat[r], c)), s);
+            }
+        }
+        const float inv = st.y > 0.f ? 1.f / st.y : 0.f;
+        *reinterpret_cast<uint2 *>(p.out + (((long long)b * n + t) * p.H_q + h * G + (r - t * G)) * D + c4 * 4) =
+            make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    }
+    if (C > 1) few_cluster_sync();                      // no CTA ends while another reads its O
+}
+
+template <int D, int ROWS, int MT>
+static magicdec_status launch_own_t(const PreOwn &p, cudaStream_t st) {
+    using L = PoShape<D, ROWS, MT>;
+    if (!magicdec_host::allow_smem_once<prefix_own_kernel<D, ROWS, MT>>(L::BYTES)) return MAGICDEC_ERR_CUDA;
+    // As many CTAs a (sequence, KV head) as there are places for, with 64 slots each at least.
+    const int slots = L::PER_SM * magicdec_host::sm_count();
+    const long long cap = (long long)p.page_size * p.max_pages;
+    int C = 1;
+    while (C < kPoMaxCluster && 2ll * C * p.pre.B * p.pre.H_kv <= slots && cap > C * kPoKeys) C *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)C, (unsigned)p.pre.H_kv, (unsigned)p.pre.B);
+    cfg.blockDim = dim3(L::NT);
+    cfg.dynamicSmemBytes = L::BYTES;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, prefix_own_kernel<D, ROWS, MT>, p) != cudaSuccess) return MAGICDEC_ERR_CUDA;
+    return magicdec_host::launch_status();
+}
+
+magicdec_status launch_prefix_own(const PreOwn &p, int D, cudaStream_t st) {
+    const int R = p.pre.n * p.pre.G;
+    if (D == 128)
+        return R <= 8    ? launch_own_t<128, 8, 1>(p, st)
+               : R <= 16 ? launch_own_t<128, 16, 1>(p, st)
+                         : launch_own_t<128, 16, 2>(p, st);
+    return R <= 8 ? launch_own_t<64, 8, 1>(p, st)
+           : R <= 16 ? launch_own_t<64, 16, 1>(p, st)
+                     : launch_own_t<64, 16, 2>(p, st);
+}
+
+}  // namespace magicdec

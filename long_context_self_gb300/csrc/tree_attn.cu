@@ -39,7 +39,7 @@
 // gave up (error 1) the roles run on without waiting, so that all of them end.
 #include <climits>
 
-#include "common.cuh"
+#include "prefix.cuh"
 
 namespace magicdec {
 
@@ -54,12 +54,6 @@ constexpr float kTrLazy = 24.0f;              // log2 growth of a row's maximum 
 // tile there, its tiles and its sequence's nodes, and the length of a run.
 struct TreeStart {
     int b, h, rb, t0, tiles, nodes, run, pad;
-};
-
-// Where an entry of the list of PRE begins, its tiles and blocks; one more holds the length of a run.
-struct PreEntry {
-    long long start;
-    int tiles, blocks;
 };
 
 struct TreeAttnParams {
@@ -82,11 +76,10 @@ struct TreeAttnParams {
     uint32_t sbo, hoff;    // bytes between groups of 8 rows, and between 64-channel halves, of a K or V tile
     float scale_log2;      // log2(e) / sqrt(d)
     // PRE only
-    const int32_t *plen, *first, *ptable;
-    PreEntry *entry;       // workspace: [P + B + 1]
-    float2 *pstat;         // workspace: a prefix's parts, [slots][RT * 128]
-    float4 *ppart;         // workspace: [slots][RT][d / 4][128]
-    int P, pmax;           // prefixes; pages of a row of ptable
+    PreParts pre;          // the parts of prefixes, in the workspace
+    const int32_t *plen, *ptable;
+    int pmax;              // pages of a row of ptable
+    int own;               // sequences in the list: B, or none where another kernel takes their own slots
     int own_rt, own_blocks;   // of a sequence's own slots: row tiles of a part, blocks at most
 };
 
@@ -262,21 +255,12 @@ struct Seq {
     int len, nodes, total, tiles, blocks;   // blocks: pairs of row tiles (one: a single tile)
     int row0;                               // PRE: its first row of queries, over all sequences
 };
-// The sequences [lo, hi) behind prefix g.
-struct Group {
-    int lo, hi;
-};
-__device__ __forceinline__ Group group_at(const TreeAttnParams &p, int g) {
-    if (!p.first) return Group{0, p.B};
-    return Group{tr_clamp(checked(ld_dep(p.first + g), 0, p.B, p.err), p.B),
-                 tr_clamp(checked(ld_dep(p.first + g + 1), 0, p.B, p.err), p.B)};
-}
 template <int RT, bool PRE>
 __device__ __forceinline__ Seq seq_at(const TreeAttnParams &p, int b) {
     Seq s;
     if (PRE) {
-        if (b < p.P) {
-            const Group g = group_at(p, b);
+        if (b < p.pre.P) {
+            const Group g = group_at(p.pre.first, p.B, b, p.err);
             const int most = p.page_size * p.pmax;
             s.row0 = g.lo * p.n;
             s.nodes = max(g.hi - g.lo, 0) * p.n;
@@ -285,7 +269,7 @@ __device__ __forceinline__ Seq seq_at(const TreeAttnParams &p, int b) {
             s.blocks = (s.nodes + RT * p.NB - 1) / (RT * p.NB);
             return s;
         }
-        b -= p.P;
+        b -= p.pre.P;
         s.row0 = b * p.n;
     }
     const int cap = p.page_size * p.max_pages;
@@ -392,9 +376,10 @@ __device__ __noinline__ Channels16 add_back(const uint16_t *v, long long stride,
     return r;
 }
 
-// x / d, in 32 bits where they suffice (a 64-bit division is a hundred instructions).
-__device__ __forceinline__ long long quotient(long long x, int d) {
-    return x <= 0xffffffffll ? (long long)((uint32_t)x / (uint32_t)d) : x / d;
+// What an entry's row block takes of the list.
+template <bool PRE>
+__device__ __forceinline__ int list_tiles(const Seq &s) {
+    return PRE && s.tiles ? s.tiles + kTrEntry : s.tiles;
 }
 
 // A run of tiles of one (sequence, KV head, row block).
@@ -411,31 +396,38 @@ struct Walk {
     Seq s;
     __device__ __forceinline__ bool next(const TreeAttnParams &p, Run &r) {
         if (left <= 0) return false;
-        while (off >= s.tiles * s.blocks * p.H_kv) {
-            if (++b >= (PRE ? p.P : 0) + p.B) return false;
-            off = 0;
-            s = seq_at<RT, PRE>(p, b);
+        for (;;) {
+            while (off >= list_tiles<PRE>(s) * s.blocks * p.H_kv) {
+                if (++b >= (PRE ? p.pre.P + p.own : p.B)) return false;
+                off = 0;
+                s = seq_at<RT, PRE>(p, b);
+            }
+            const int tiles = list_tiles<PRE>(s), item = off / tiles;
+            r.b = b;
+            r.s = s;
+            r.h = s.blocks == 1 ? item : item / s.blocks;
+            r.rb = item - r.h * s.blocks;
+            const int at = off - item * tiles, n = min(tiles - at, left);
+            off += n;
+            left -= n;
+            if (!PRE) {
+                r.t0 = at;
+                r.cnt = n;
+                return true;
+            }
+            r.t0 = max(at - kTrEntry, 0);
+            r.cnt = max(at + n - kTrEntry, 0) - r.t0;
+            if (r.cnt > 0) return true;
+            if (left <= 0) return false;
         }
-        const int item = off / s.tiles;
-        r.b = b;
-        r.s = s;
-        r.h = s.blocks == 1 ? item : item / s.blocks;
-        r.rb = item - r.h * s.blocks;
-        r.t0 = off - item * s.tiles;
-        r.cnt = min(s.tiles - r.t0, left);
-        off += r.cnt;
-        left -= r.cnt;
-        return true;
     }
 };
 
-// PRE: an entry's parts lie at this number and the CTA's added, one for each CTA that has some of it,
-// and no two entries' meet: along the list either grows.  Prefixes are numbered by their first
-// rows, of which RT * NB make a block; sequences by their own blocks at most.
+// Number of an entry's parts: see pre_slot; a sequence's by its own blocks at most.
 template <int RT>
-__device__ __forceinline__ long long pre_slot(const TreeAttnParams &p, int e, int h, int rb, int blocks, int row0) {
-    if (e < p.P) return (long long)(row0 / (RT * p.NB) + e) * p.H_kv + h * blocks + rb;
-    return ((long long)(e - p.P) * p.H_kv + h) * p.own_blocks + rb;
+__device__ __forceinline__ long long part_slot(const TreeAttnParams &p, int e, int h, int rb, int blocks, int row0) {
+    if (e < p.pre.P) return pre_slot(row0, e, h, rb, blocks, p.H_kv, RT * p.NB);
+    return ((long long)(e - p.pre.P) * p.H_kv + h) * p.own_blocks + rb;
 }
 
 template <int D, int RT>
@@ -518,23 +510,26 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         *met = 0;
     }
     if (warp == 1) tmem_alloc(tmem_slot, 512);
-    pdl_trigger();
+    // The kernel behind PRE reads what was there before this one without waiting for its end.
+    if (!PRE) pdl_trigger();
     pdl_wait();
+    if (PRE) pdl_trigger();
 
     // The list of work: prefix sums over the sequences (a thread has one of them, or with more
     // than kTrThreads several in a row), this CTA's run of tiles, and the sequence that it
     // begins in.
     Walk<RT, PRE> walk;
-    const int first_own = PRE ? p.P : 0;                                 // list entries of the prefixes
+    const int first_own = PRE ? p.pre.P : 0;                                 // list entries of the prefixes
     {
         long long *wsum = reinterpret_cast<long long *>(par);
-        const int entries = first_own + p.B, per = entries <= kTrThreads ? 1 : (entries + kTrThreads - 1) / kTrThreads;
+        PreEntry *entry = const_cast<PreEntry *>(p.pre.entry);
+        const int entries = PRE ? first_own + p.own : p.B, per = entries <= kTrThreads ? 1 : (entries + kTrThreads - 1) / kTrThreads;
         const int ba = min(entries, tid * per), bz = min(entries, ba + per);
         Seq sq{};
         long long mine = 0;
         for (int b = ba; b < bz; ++b) {
             sq = seq_at<RT, PRE>(p, b);
-            mine += (long long)(sq.tiles * sq.blocks) * p.H_kv;
+            mine += (long long)(list_tiles<PRE>(sq) * sq.blocks) * p.H_kv;
         }
         long long incl = mine;
 #pragma unroll
@@ -555,8 +550,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         const long long t0 = blockIdx.x * run;
         for (int b = ba; b < bz; ++b) {
             if (per > 1) sq = seq_at<RT, PRE>(p, b);
-            const long long w = (long long)(sq.tiles * sq.blocks) * p.H_kv;
-            if (PRE && blockIdx.x == 0) p.entry[b] = PreEntry{before, sq.tiles, sq.blocks};
+            const long long w = (long long)(list_tiles<PRE>(sq) * sq.blocks) * p.H_kv;
+            if (PRE && blockIdx.x == 0) entry[b] = PreEntry{before, sq.tiles, sq.blocks};
             if (t0 >= before && t0 < before + w) {
                 found[0] = b;
                 found[1] = (int)(t0 - before);
@@ -567,15 +562,16 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 found[6] = sq.tiles;
                 found[7] = sq.blocks;
                 if (PRE) found[8] = sq.row0;
-                const int item = found[1] / sq.tiles, h = item / sq.blocks;
-                if (!PRE)
+                if (!PRE) {
+                    const int item = found[1] / sq.tiles, h = item / sq.blocks;
                     p.start[blockIdx.x] = TreeStart{b, h, item - h * sq.blocks, found[1] - item * sq.tiles, sq.tiles,
                                                     sq.nodes, (int)run, 0};
+                }
             }
             before += w;
         }
         if (PRE) {
-            if (blockIdx.x == 0 && tid == 0) p.entry[entries] = PreEntry{run, 0, 0};
+            if (blockIdx.x == 0 && tid == 0) *const_cast<PreEntry *>(p.pre.run) = PreEntry{run, 0, 0};
         } else if (t0 >= all && tid == 0) {
             p.start[blockIdx.x] = TreeStart{};
         }
@@ -1013,10 +1009,10 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             uint16_t *dst = p.out + (((long long)r.b * p.n + node) * p.H_q + r.h * p.G + (row - node_r * p.G)) * D;
             const int rt = RT == 2 ? s : 0;
             const int rr = pre ? 128 : p.rr;
-            const long long tile_at = PRE ? (pre_slot<RT>(p, r.b, r.h, r.rb, r.s.blocks, r.s.row0) + blockIdx.x) *
+            const long long tile_at = PRE ? (part_slot<RT>(p, r.b, r.h, r.rb, r.s.blocks, r.s.row0) + blockIdx.x) *
                                                     (pre ? RT : p.own_rt) + rt
                                           : (long long)part * RT + rt;
-            float4 *pd = (pre ? p.ppart : p.part) + tile_at * (D / 4) * rr + row;
+            float4 *pd = (pre ? const_cast<float4 *>(p.pre.part) : p.part) + tile_at * (D / 4) * rr + row;
             constexpr int SHARE = RT == 1 ? D / 4 : D / 2;               // channels of a warp
             const int c_lo = RT == 1 ? (s * 2 + half) * SHARE : half * SHARE;
 #pragma unroll 1
@@ -1061,7 +1057,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 __syncwarp();                                // TMEM is read by whole warps
             }
             if (!whole && node >= 0 && c_lo == 0)
-                (pre ? p.pstat : p.stat)[tile_at * rr + row] = make_float2(mm, ll);
+                (pre ? const_cast<float2 *>(p.pre.stat) : p.stat)[tile_at * rr + row] = make_float2(mm, ll);
             __syncwarp();
             tc_fence_before();
             // O is free for the next run, whose first P says so: with one row tile, once all
@@ -1181,31 +1177,18 @@ __global__ void __launch_bounds__(kTjThreads) tree_attn_pre_join_kernel(const Tr
     const bool real = at < rows;
     const int flat = real ? at / p.G : 0, g = real ? at - flat * p.G : 0, b = flat / p.n, i = flat - b * p.n;
     const int nodes = !real ? 0 : p.n_nodes ? tr_clamp(ld_dep(p.n_nodes + b), p.n) : p.n;
-    const long long run = p.entry[p.P + p.B].start;
     // The parts of the row: in the entry of a prefix, and in that of the sequence.
-    long long slot[2] = {0, 0};          // number of the first part's row tile
-    int parts[2] = {0, 0}, row[2] = {0, 0};
-    auto locate = [&](int k, int e, int node, int row0, int rts) {
-        const PreEntry x = p.entry[e];
-        if (x.tiles == 0) return;
-        const int rb = node / (RT * p.NB), local = node - rb * RT * p.NB, rt = local / p.NB;
-        const long long t0 = x.start + (long long)(h * x.blocks + rb) * x.tiles;
-        const long long c0 = quotient(t0, (int)run), c1 = quotient(t0 + x.tiles - 1, (int)run);
-        parts[k] = (int)(c1 - c0) + 1;
-        slot[k] = (pre_slot<RT>(p, e, h, rb, x.blocks, row0) + c0) * rts + rt;
-        row[k] = (local - rt * p.NB) * p.G + g;
-    };
+    RowParts piece[2] = {RowParts{0, 0, 1, 0}, RowParts{0, 0, 1, 0}};
     if (i < nodes) {
-        // The last group that begins at b or before; an empty one begins where the next does.
-        int lo = 0, hi = p.first ? p.P : 1;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (tr_clamp(ld_dep(p.first + mid), p.B) <= b) lo = mid;
-            else hi = mid;
+        piece[0] = pre_parts(p.pre, b, i, g, h);
+        const PreEntry x = p.pre.entry[p.pre.P + b];
+        if (x.tiles) {
+            const int rb = i / (RT * p.NB), local = i - rb * RT * p.NB, rt = local / p.NB, run = (int)p.pre.run->start;
+            const long long t0 = x.start + (long long)(h * x.blocks + rb) * (x.tiles + kTrEntry) + kTrEntry;
+            const long long c0 = quotient(t0, run), c1 = quotient(t0 + x.tiles - 1, run);
+            piece[1] = RowParts{(part_slot<RT>(p, p.pre.P + b, h, rb, x.blocks, 0) + c0) * p.own_rt + rt, (int)(c1 - c0) + 1,
+                              p.own_rt, (local - rt * p.NB) * p.G + g};
         }
-        const Group q = group_at(p, lo);
-        if (q.lo <= b && b < q.hi) locate(0, lo, (b - q.lo) * p.n + i, q.lo * p.n, RT);
-        locate(1, p.P + b, i, b * p.n, p.own_rt);
     }
     const float sl = p.scale_log2;
     uint16_t *dst = p.out + ((long long)flat * p.H_q + h * p.G + g) * D;
@@ -1222,14 +1205,14 @@ __global__ void __launch_bounds__(kTjThreads) tree_attn_pre_join_kernel(const Tr
         };
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const int rr = k ? p.rr : 128, rts = k ? p.own_rt : RT;
-            const float2 *stat = k ? p.stat : p.pstat;
-            const float4 *part = k ? p.part : p.ppart;
+            const int rr = k ? p.rr : 128;
+            const float2 *stat = k ? p.stat : p.pre.stat;
+            const float4 *part = k ? p.part : p.pre.part;
 #pragma unroll 4
-            for (int j = PL > 1 ? warp : 0; j < parts[k]; j += PL) {
-                const long long s = slot[k] + (long long)j * rts;
-                const float4 *src = part + (s * (D / 4) + 2 * c) * rr + row[k];
-                add(stat[s * rr + row[k]], src[0], src[rr]);
+            for (int j = PL > 1 ? warp : 0; j < piece[k].count; j += PL) {
+                const long long s = piece[k].tile + (long long)j * piece[k].step;
+                const float4 *src = part + (s * (D / 4) + 2 * c) * rr + piece[k].row;
+                add(stat[s * rr + piece[k].row], src[0], src[rr]);
             }
         }
         if (PL > 1) {
@@ -1396,19 +1379,23 @@ static int pre_row_tiles(int B, int P, int n, int G) {
     return n <= NB && (long long)((B + P - 1) / P) * n <= NB ? 1 : 2;
 }
 
+// Up to this many query rows of a sequence's KV head, its own slots are another kernel's (prefix_own.cu).
+constexpr int kTrOwnRows = 32;
+
 struct PreSizes {
-    int RT, own_rt, own_blocks, rr;
+    int RT, own, own_rt, own_blocks, rr;       // own: sequences in the list
     long long pslots, slots;
 };
 static PreSizes pre_sizes(const magicdec_paged_shape &s, int P, int n) {
     PreSizes z;
     const int G = s.H_q / s.H_kv, NB = 128 / G;
     z.RT = pre_row_tiles(s.B, P, n, G);
+    z.own = n * G > kTrOwnRows ? s.B : 0;
     z.own_rt = tr_row_tiles(n, G);
     z.own_blocks = (n + z.RT * NB - 1) / (z.RT * NB);
     z.rr = tr_part_rows(n, G);
     z.pslots = ((long long)s.B * n / (z.RT * NB) + P) * s.H_kv + magicdec_host::sm_count();
-    z.slots = (long long)s.B * s.H_kv * z.own_blocks + magicdec_host::sm_count();
+    z.slots = z.own ? (long long)s.B * s.H_kv * z.own_blocks + magicdec_host::sm_count() : 0;
     return z;
 }
 
@@ -1421,13 +1408,33 @@ size_t prefix_attn_workspace_bytes(const magicdec_paged_shape &s, int P, int n) 
 
 template <int D, int RT>
 static magicdec_status launch_prefix_t(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv,
-                                       const CUtensorMap &tmg, const TreeAttnParams &p, cudaStream_t st) {
+                                       const CUtensorMap &tmg, const TreeAttnParams &p, const uint16_t *q,
+                                       const uint16_t *k, cudaStream_t st) {
     auto kern = tree_attn_kernel<D, RT, true>;
     constexpr int smem = TrSmem<D, RT>::BYTES;
     if (!magicdec_host::allow_smem_once<tree_attn_kernel<D, RT, true>>(smem)) return MAGICDEC_ERR_CUDA;
     magicdec_status s =
         magicdec_host::launch_pdl(kern, dim3((unsigned)p.grid), dim3(kTrThreads), smem, st, tmq, tmk, tmv, tmg, p);
     if (s != MAGICDEC_OK) return s;
+    if (!p.own) {
+        PreOwn x{};
+        x.pre = p.pre;
+        x.q = q;
+        x.k = k;
+        x.v = p.vp;
+        x.out = p.out;
+        x.len = p.len;
+        x.n_nodes = p.n_nodes;
+        x.parent = p.parent;
+        x.table = p.table;
+        x.err = p.err;
+        x.H_q = p.H_q;
+        x.page_size = p.page_size;
+        x.n_pages = p.n_pages;
+        x.max_pages = p.max_pages;
+        x.scale_log2 = p.scale_log2;
+        return launch_prefix_own(x, D, st);
+    }
     const unsigned blocks = (unsigned)(((long long)p.B * p.n * p.G + 31) / 32);
     // Parts shared out while the blocks of whole rows would not fill the GPU.
     if ((long long)blocks * p.H_kv <= p.grid)
@@ -1452,9 +1459,7 @@ magicdec_status launch_prefix_attn(const magicdec_paged_shape &s, int P, int pma
     p.n = n;
     set_tiles(p, s);
     p.plen = plen;
-    p.first = first;
     p.ptable = ptable;
-    p.P = P;
     p.pmax = pmax;
     // The list is counted in 32 bits within an entry and within a CTA's run.
     auto tiles = [&](long long pages) {
@@ -1462,18 +1467,28 @@ magicdec_status launch_prefix_attn(const magicdec_paged_shape &s, int P, int pma
     };
     const PreSizes z = pre_sizes(s, P, n);
     const long long rows = (long long)s.B * n;
-    const double work = (double)tiles(pmax) * s.H_kv * (double)((rows + p.NB - 1) / p.NB);
-    const double own = (double)tiles(s.max_pages) * s.H_kv * ((n + p.NB - 1) / p.NB);
+    const double work = (double)(tiles(pmax) + kTrEntry) * s.H_kv * (double)((rows + p.NB - 1) / p.NB);
+    const double own = (double)(tiles(s.max_pages) + kTrEntry) * s.H_kv * ((n + p.NB - 1) / p.NB);
     if (work > INT_MAX || own > INT_MAX || (work * P + own * s.B) / p.grid >= INT_MAX / 2) return MAGICDEC_ERR_UNSUPPORTED;
     uint8_t *w = static_cast<uint8_t *>(ws);
     const size_t prows = (size_t)z.pslots * z.RT * 128, orows = (size_t)z.slots * z.own_rt * z.rr;
-    p.entry = reinterpret_cast<PreEntry *>(w);
+    p.own = z.own;
+    p.pre.entry = reinterpret_cast<PreEntry *>(w);
+    p.pre.run = p.pre.entry + P + s.B;
     w += tr_align(((size_t)P + s.B + 1) * sizeof(PreEntry));
-    p.pstat = reinterpret_cast<float2 *>(w);
+    p.pre.stat = reinterpret_cast<float2 *>(w);
     w += tr_align(prows * sizeof(float2));
     p.stat = reinterpret_cast<float2 *>(w);
     w += tr_align(orows * sizeof(float2));
-    p.ppart = reinterpret_cast<float4 *>(w);
+    p.pre.part = reinterpret_cast<float4 *>(w);
+    p.pre.first = first;
+    p.pre.P = P;
+    p.pre.B = s.B;
+    p.pre.n = n;
+    p.pre.G = p.G;
+    p.pre.H_kv = s.H_kv;
+    p.pre.NB = p.NB;
+    p.pre.RT = z.RT;
     p.part = reinterpret_cast<float4 *>(w + prows * s.d * 4);
     p.rr = z.rr;
     p.own_rt = z.own_rt;
@@ -1481,10 +1496,10 @@ magicdec_status launch_prefix_attn(const magicdec_paged_shape &s, int P, int pma
     CUtensorMap tmq, tmk, tmv, tmg;
     if (!set_maps(p, s, q, kp, vp, &tmq, &tmk, &tmv, &tmg)) return MAGICDEC_ERR_CUDA;
     if (s.d == 128)
-        return z.RT == 1 ? launch_prefix_t<128, 1>(tmq, tmk, tmv, tmg, p, st)
-                         : launch_prefix_t<128, 2>(tmq, tmk, tmv, tmg, p, st);
-    return z.RT == 1 ? launch_prefix_t<64, 1>(tmq, tmk, tmv, tmg, p, st)
-                     : launch_prefix_t<64, 2>(tmq, tmk, tmv, tmg, p, st);
+        return z.RT == 1 ? launch_prefix_t<128, 1>(tmq, tmk, tmv, tmg, p, q, kp, st)
+                         : launch_prefix_t<128, 2>(tmq, tmk, tmv, tmg, p, q, kp, st);
+    return z.RT == 1 ? launch_prefix_t<64, 1>(tmq, tmk, tmv, tmg, p, q, kp, st)
+                     : launch_prefix_t<64, 2>(tmq, tmk, tmv, tmg, p, q, kp, st);
 }
 
 }  // namespace magicdec
