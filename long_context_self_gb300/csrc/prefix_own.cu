@@ -38,9 +38,8 @@ template <int D, int ROWS, int MT>
 struct PoShape {
     static constexpr int WARPS = 4 * MT, NT = WARPS * 32;
     static constexpr int HV = D / 64, OPER = HV * kPoHalf, STAGE = 2 * OPER;
-    // Two CTAs an SM; with 32 rows of 128 channels, whose registers fill it, one.
-    static constexpr int PER_SM = MT == 2 && D == 128 ? 1 : 2;
-    static constexpr int STAGES = D == 128 ? (PER_SM == 1 ? 6 : 3) : 6;
+    static constexpr int PER_SM = 2;                    // CTAs
+    static constexpr int STAGES = D == 128 ? 3 : 6;
     static constexpr int QHALF = MT * ROWS * 128;
     static constexpr int BYTES = STAGES * STAGE + HV * QHALF;
     static_assert(4 * MT * ROWS * D * 4 <= STAGES * STAGE, "the warps' O take the ring's place");
@@ -59,6 +58,7 @@ __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>
     __shared__ uint32_t sees[32];                       // of a node's slots: itself and its ancestors
     __shared__ float2 wstat[L::WARPS][16];              // of a warp's rows: (max, sum)
     __shared__ float2 cstat[32];                        // of this CTA
+    __shared__ RowParts parts_of[32];                   // of the prefix
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int lq = lane & 3, lr = lane >> 2;
     const int b = blockIdx.z, h = blockIdx.y, n = p.pre.n, G = p.pre.G, R = n * G;
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>
     }
 
     const int mt = MT == 1 ? 0 : warp % MT, kw = warp / MT;
-    uint32_t qf[KS][2 * HR];
+    uint32_t qf[HR == 1 ? KS : 1][2 * HR];
     float o[NB][2 * HR], m[HR], l[HR];
     uint32_t anc[HR];
 #pragma unroll
@@ -144,14 +144,13 @@ __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>
     for (int j = 0; j < NB; ++j)
 #pragma unroll
         for (int e = 0; e < 2 * HR; ++e) o[j][e] = 0.f;
+    // The queries' fragments: kept with 8 rows, else from shared memory for every 16 keys (they would
+    // take the registers of a second CTA on the SM).
+    const uint32_t q_lane = smem_u32(qs) + (uint32_t)mt * 2048 + (HR == 2 ? swz128(lane & 15, lane >> 4) : swz128(lane & 7, lane >> 3));
+    if constexpr (HR == 1)
 #pragma unroll
-    for (int c = 0; c < KS; c += 3 - HR) {
-        const uint32_t at = smem_u32(qs) + (uint32_t)mt * 2048 + (uint32_t)(c >> 2) * QHALF;
-        if constexpr (HR == 2)
-            ldsm_x4(at + swz128(lane & 15, (c & 3) * 2 + (lane >> 4)), qf[c][0], qf[c][1], qf[c][2], qf[c][3]);
-        else
-            ldsm_x4(at + swz128(lane & 7, (c & 3) * 2 + (lane >> 3)), qf[c][0], qf[c][1], qf[c + 1][0], qf[c + 1][1]);
-    }
+        for (int c = 0; c < KS; c += 2)
+            ldsm_x4((q_lane ^ ((c & 3) * 32)) + (c >> 2) * QHALF, qf[c][0], qf[c][1], qf[c + 1][0], qf[c + 1][1]);
     // A lane's address in a K tile, and in a V tile: 16-byte chunk c of its row is at c * 16 away from
     // chunk 0 in the sense of an exclusive or (8 chunks a half).
     const int x4 = lane >> 3, r0 = 16 * kw;
@@ -175,8 +174,10 @@ __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>
         for (int c = 0; c < KS; ++c) {
             uint32_t f0, f1, f2, f3;
             ldsm_x4(((kt + k_lane) ^ ((c & 3) * 32)) + (c >> 2) * kPoHalf, f0, f1, f2, f3);
-            few_mma<HR>(c & 1 ? s2[0] : s[0], qf[c], f0, f1);
-            few_mma<HR>(c & 1 ? s2[1] : s[1], qf[c], f2, f3);
+            uint32_t(&f)[2 * HR] = qf[HR == 1 ? c : 0];
+            if constexpr (HR == 2) ldsm_x4((q_lane ^ ((c & 3) * 32)) + (c >> 2) * QHALF, f[0], f[1], f[2], f[3]);
+            few_mma<HR>(c & 1 ? s2[0] : s[0], f, f0, f1);
+            few_mma<HR>(c & 1 ? s2[1] : s[1], f, f2, f3);
         }
         // Keys that not every row sees: behind the last one, or of the nodes.
         const bool edge = g + 16 > len || g + 16 > k1;
@@ -307,6 +308,11 @@ __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>
     else __syncthreads();
     // The CTAs' O, each a share of the channels, with the prefix's parts.
     pdl_wait();
+    if (tid < R) {
+        const int t = tid / G;
+        parts_of[tid] = t < nodes ? pre_parts(p.pre, b, t, tid - t * G, h) : RowParts{0, 0, 1, 0};
+    }
+    __syncthreads();
     const int vecs = R * (D / 4), share = (vecs + (int)C - 1) / (int)C;
     for (int i = (int)rank * share + tid; i < min(vecs, (int)(rank + 1) * share); i += NT) {
         const int r = i / (D / 4), c4 = i - r * (D / 4), t = r / G;
@@ -319,7 +325,7 @@ __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>
             acc = make_float4(acc.x * f + y.x * w, acc.y * f + y.y * w, acc.z * f + y.z * w, acc.w * f + y.w * w);
         };
         if (t < nodes) {
-            const RowParts parts = pre_parts(p.pre, b, t, r - t * G, h);
+            const RowParts parts = parts_of[r];
 #pragma unroll 4
             for (int k = 0; k < parts.count; ++k) {
                 const long long at = parts.tile + (long long)k * parts.step;
