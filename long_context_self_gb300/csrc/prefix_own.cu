@@ -82,16 +82,21 @@ __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>
     }
     if (p.parent && tid < n)
         par[tid] = checked(ld_dep(p.parent + (long long)b * n + tid), INT_MIN, tid - 1, p.err);
-    // Where a tile's keys lie; one outside the pool is zeros.
+    // Where a tile's keys lie; one outside the pool is zeros.  The page is asked for before a tile's
+    // products and its number used behind them.
     const int32_t *table = p.table + (long long)b * p.max_pages;
+    int page = -1;
+    auto ask = [&](int t) {
+        const int key = k0 + t * kPoKeys + tid;
+        if (tid < kPoKeys && key < k1) page = ld_dep(table + key / p.page_size);
+    };
     auto look_up = [&](int t) {
         if (tid < kPoKeys) {
             const int key = k0 + t * kPoKeys + tid;
             long long at = -1;
             if (key < k1) {
-                const int pg = key / p.page_size, id = ld_dep(table + pg);
-                if (id < 0 || id >= p.n_pages) raise_error(p.err, kErrPage);
-                else at = (((long long)id * p.page_size + (key - pg * p.page_size)) * p.pre.H_kv + h) * D;
+                if (page < 0 || page >= p.n_pages) raise_error(p.err, kErrPage);
+                else at = (((long long)page * p.page_size + key % p.page_size) * p.pre.H_kv + h) * D;
             }
             rows_at[t & 1][tid] = at;
         }
@@ -111,6 +116,7 @@ __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    ask(0);
     look_up(0);
     __syncthreads();
     if (tid < n) {
@@ -124,8 +130,9 @@ __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>
     }
 #pragma unroll 1
     for (int t = 0; t + 1 < NST; ++t) {
-        look_up(t + 1);
+        ask(t + 1);
         load(t);
+        look_up(t + 1);
         __syncthreads();
     }
 
@@ -159,11 +166,14 @@ __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>
     for (int t = 0; t < tiles; ++t) {
         copies_wait<NST - 2>();
         __syncthreads();                                // tile t is there, and all are done with tile t - 1
+        ask(t + NST);
         load(t + NST - 1);
-        look_up(t + NST);
         const uint32_t kt = smem_u32(ring + t % NST * STAGE), vt = kt + OPER;
         const int g = k0 + t * kPoKeys + r0;
-        if (g >= k1) continue;
+        if (g >= k1) {                                  // nothing for this warp
+            look_up(t + NST);
+            continue;
+        }
         // Two chains of products a score, so that half as many wait for one another.
         float s[2][2 * HR], s2[2][2 * HR];
 #pragma unroll
@@ -272,6 +282,7 @@ __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>
                 few_mma<HR>(o[j + 1], a, f2, f3);
             }
         }
+        look_up(t + NST);
     }
     // The warps' maxima and sums, and the CTA's.
 #pragma unroll
