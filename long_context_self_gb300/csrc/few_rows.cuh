@@ -69,4 +69,22 @@ __device__ __forceinline__ void few_mma(float (&c)[2 * HR], const uint32_t (&a)[
     }
 }
 
+// Bits of the bf16 of a word that are not finite: the carry of an exponent of ones tells.
+__device__ __forceinline__ uint32_t few_odd_bits(uint32_t x) {
+    return ((((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u) >> 15) * 0xffffu;
+}
+
+// Whether any value of rows [row, row + rows) of a tile of V is not finite: 64-channel halves `half`
+// bytes apart, rows of 128 bytes, swizzled.  By a warp.
+template <int HV>
+__device__ __forceinline__ bool few_not_finite(const uint8_t *v, int half, int row, int rows, int lane) {
+    uint32_t any = 0;
+    for (int i = lane; i < rows * HV * 8; i += 32) {
+        const int r = row + i / (HV * 8), c = i % (HV * 8);
+        const uint4 x = *reinterpret_cast<const uint4 *>(v + (c >> 3) * half + swz128(r, c & 7));
+        any |= few_odd_bits(x.x) | few_odd_bits(x.y) | few_odd_bits(x.z) | few_odd_bits(x.w);
+    }
+    return __any_sync(0xffffffffu, any != 0);
+}
+
 }  // namespace magicdec

@@ -245,49 +245,56 @@ __global__ void __launch_bounds__(128 * MT + 32, MT == 2 ? 1 : 2)
                         a[nb * HR + e] = pack_bf16(x, y);
                     }
                 }
-                if (p.n > 1 && g + 16 > len - p.n + 1) {
-                    // Keys of the block's own tokens, which earlier tokens must not see whatever they hold
-                    // (0 * inf is NaN): by scalars, and only where a row sees them.
-                    const int last = min(16, k1 - g);
+                if (g + 16 > k1) {
+                    // Rows of V behind the last may hold anything, and 0 * NaN is NaN: zeros.
+                    for (int i = lane; i < (g + 16 - k1) * HV * 8; i += 32) {
+                        const int row = r0 + 15 - i / (HV * 8), c = i % (HV * 8);
+                        *reinterpret_cast<uint4 *>(ring + st * STAGE + OPER + (c >> 3) * kHvHalf + swz128(row, c & 7)) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                    __syncwarp();
+                }
+                // Infinities and NaN among the V of the block's own tokens, which earlier ones must not see
+                // (0 * inf is NaN), are left out of the product and added by scalars where a row sees them.
+                const int last = min(16, k1 - g);
+                const uint8_t *v = ring + st * STAGE + OPER;
+                const bool odd = p.n > 1 && g + 16 > len - p.n + 1 && few_not_finite<HV>(v, kHvHalf, r0, last, lane);
+                if (odd) {
                     for (int x = 0; x < last; ++x) {
                         const int from = (lane & ~3) | ((x & 7) >> 1);
                         float w[HR];
 #pragma unroll
                         for (int e = 0; e < HR; ++e) {
-                            const float even = x < 8 ? s[0][2 * e] : s[1][2 * e];
-                            const float odd = x < 8 ? s[0][2 * e + 1] : s[1][2 * e + 1];
-                            w[e] = __shfl_sync(0xffffffffu, x & 1 ? odd : even, from);
+                            const float w0 = x < 8 ? s[0][2 * e] : s[1][2 * e];
+                            const float w1 = x < 8 ? s[0][2 * e + 1] : s[1][2 * e + 1];
+                            w[e] = __shfl_sync(0xffffffffu, x & 1 ? w1 : w0, from);
                         }
-                        const uint8_t *v = ring + st * STAGE + OPER;
 #pragma unroll
                         for (int j = 0; j < NB; ++j) {
-                            const uint32_t z = *reinterpret_cast<const uint32_t *>(v + (j >> 3) * kHvHalf +
-                                                                                   swz128(r0 + x, j & 7) + 4 * lq);
+                            uint32_t z =
+                                *reinterpret_cast<const uint32_t *>(v + (j >> 3) * kHvHalf + swz128(r0 + x, j & 7) + 4 * lq);
+                            z &= few_odd_bits(z);
 #pragma unroll
                             for (int e = 0; e < HR; ++e)
-                                if (g + x < see[e]) {
+                                if (z && g + x < see[e]) {
                                     o[j][2 * e] = fmaf(w[e], __uint_as_float(z << 16), o[j][2 * e]);
                                     o[j][2 * e + 1] = fmaf(w[e], __uint_as_float(z & 0xffff0000u), o[j][2 * e + 1]);
                                 }
                         }
                     }
-                } else {
-                    if (g + 16 > k1) {
-                        // Rows of V behind the last may hold anything, and 0 * NaN is NaN: zeros.
-                        for (int i = lane; i < (g + 16 - k1) * HV * 8; i += 32) {
-                            const int row = r0 + 15 - i / (HV * 8), c = i % (HV * 8);
-                            *reinterpret_cast<uint4 *>(ring + st * STAGE + OPER + (c >> 3) * kHvHalf + swz128(row, c & 7)) =
-                                make_uint4(0, 0, 0, 0);
-                        }
-                        __syncwarp();
-                    }
+                }
 #pragma unroll
-                    for (int j = 0; j < NB; j += 2) {
-                        uint32_t f0, f1, f2, f3;
-                        ldsm_x4_trans(((vt + v_lane) ^ ((j & 7) * 16)) + (j >> 3) * kHvHalf, f0, f1, f2, f3);
-                        few_mma<HR>(o[j], a, f0, f1);
-                        few_mma<HR>(o[j + 1], a, f2, f3);
+                for (int j = 0; j < NB; j += 2) {
+                    uint32_t f0, f1, f2, f3;
+                    ldsm_x4_trans(((vt + v_lane) ^ ((j & 7) * 16)) + (j >> 3) * kHvHalf, f0, f1, f2, f3);
+                    if (odd) {
+                        f0 &= ~few_odd_bits(f0);
+                        f1 &= ~few_odd_bits(f1);
+                        f2 &= ~few_odd_bits(f2);
+                        f3 &= ~few_odd_bits(f3);
                     }
+                    few_mma<HR>(o[j], a, f0, f1);
+                    few_mma<HR>(o[j + 1], a, f2, f3);
                 }
             }
             fence_proxy_async_smem();

@@ -247,40 +247,45 @@ __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>
                 a[nb * HR + e] = pack_bf16(x, y);
             }
         }
-        if (n > 1 && g + 16 > len) {
-            // Keys of nodes, which others than their descendants must not see whatever they hold
-            // (0 * inf is NaN): by scalars, and only where a row sees them.
-            const int last = min(16, k1 - g);
+        // Infinities and NaN among the V of nodes, which others than their descendants must not see
+        // (0 * inf is NaN), are left out of the product and added by scalars where a row sees them.
+        const int last = min(16, k1 - g);
+        const uint8_t *v = ring + t % NST * STAGE + OPER;
+        const bool odd = n > 1 && g + 16 > len && few_not_finite<L::HV>(v, kPoHalf, r0, last, lane);
+        if (odd) {
             for (int x = 0; x < last; ++x) {
                 const int from = (lane & ~3) | ((x & 7) >> 1);
                 float w[HR];
 #pragma unroll
                 for (int e = 0; e < HR; ++e) {
-                    const float even = x < 8 ? s[0][2 * e] : s[1][2 * e];
-                    const float odd = x < 8 ? s[0][2 * e + 1] : s[1][2 * e + 1];
-                    w[e] = __shfl_sync(0xffffffffu, x & 1 ? odd : even, from);
+                    const float w0 = x < 8 ? s[0][2 * e] : s[1][2 * e], w1 = x < 8 ? s[0][2 * e + 1] : s[1][2 * e + 1];
+                    w[e] = __shfl_sync(0xffffffffu, x & 1 ? w1 : w0, from);
                 }
-                const uint8_t *v = ring + t % NST * STAGE + OPER;
 #pragma unroll
                 for (int j = 0; j < NB; ++j) {
-                    const uint32_t z =
-                        *reinterpret_cast<const uint32_t *>(v + (j >> 3) * kPoHalf + swz128(r0 + x, j & 7) + 4 * lq);
+                    uint32_t z = *reinterpret_cast<const uint32_t *>(v + (j >> 3) * kPoHalf + swz128(r0 + x, j & 7) + 4 * lq);
+                    z &= few_odd_bits(z);
 #pragma unroll
                     for (int e = 0; e < HR; ++e)
-                        if (!hidden(g + x, anc[e])) {
+                        if (z && !hidden(g + x, anc[e])) {
                             o[j][2 * e] = fmaf(w[e], __uint_as_float(z << 16), o[j][2 * e]);
                             o[j][2 * e + 1] = fmaf(w[e], __uint_as_float(z & 0xffff0000u), o[j][2 * e + 1]);
                         }
                 }
             }
-        } else {
+        }
 #pragma unroll
-            for (int j = 0; j < NB; j += 2) {
-                uint32_t f0, f1, f2, f3;
-                ldsm_x4_trans(((vt + v_lane) ^ ((j & 7) * 16)) + (j >> 3) * kPoHalf, f0, f1, f2, f3);
-                few_mma<HR>(o[j], a, f0, f1);
-                few_mma<HR>(o[j + 1], a, f2, f3);
+        for (int j = 0; j < NB; j += 2) {
+            uint32_t f0, f1, f2, f3;
+            ldsm_x4_trans(((vt + v_lane) ^ ((j & 7) * 16)) + (j >> 3) * kPoHalf, f0, f1, f2, f3);
+            if (odd) {
+                f0 &= ~few_odd_bits(f0);
+                f1 &= ~few_odd_bits(f1);
+                f2 &= ~few_odd_bits(f2);
+                f3 &= ~few_odd_bits(f3);
             }
+            few_mma<HR>(o[j], a, f0, f1);
+            few_mma<HR>(o[j + 1], a, f2, f3);
         }
         look_up(t + NST);
     }
