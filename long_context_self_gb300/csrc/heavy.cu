@@ -495,7 +495,8 @@ static HeavyPlan heavy_plan(int pairs, int cap, int R, int D) {
     z.C = 1;
     for (int C = 1; C <= kHvMaxCluster; C *= 2) {
         const double waves = pairs * C / slots + 0.5;
-        const double t = (waves > 1 ? waves : 1) * (((cap + C - 1) / C + kHvKeys - 1) / kHvKeys * 1.4 + 6.0);
+        const bool twice = ((long long)cap + C - 1) / C * R * 4 > kHvScores;
+        const double t = (waves > 1 ? waves : 1) * (((cap + C - 1) / C + kHvKeys - 1) / kHvKeys * (twice ? 2.2 : 1.4) + 6.0);
         if (C == 1 || t < best) {
             best = t;
             z.C = C;
@@ -617,9 +618,11 @@ struct EvictParams {
     int *err;
     int B, H_kv, cap, vecs, budget, n_sink, n_recent;
     long long items;                     // layers * B * H_kv
-    int keep;                            // rows whose keys fit shared memory
+    int keep;                            // rows whose keys fit shared memory, a multiple of 4
+    int wide;                            // rows of weights and positions begin at 16 bytes
 };
 
+// A thread's rows: 4 neighbours of every 4 T, so that keys are written and searched 16 bytes at a time.
 // Order of fp32 as unsigned integers; both zeros are one.
 __device__ __forceinline__ uint32_t ev_key(float w) {
     const uint32_t x = __float_as_uint(w + 0.f);
@@ -630,12 +633,12 @@ __device__ __forceinline__ uint32_t ev_key(float w) {
 template <int NW>
 __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictParams p) {
     constexpr int T = NW * 32, LIST = kEvMoves * NW;
-    extern __shared__ uint32_t shared[];
+    extern __shared__ __align__(16) uint32_t shared[];
     __shared__ int lists[2 * kEvMoves * kEvWarps];
     __shared__ uint2 xch[2][kEvWarps];
     const int tid = threadIdx.x % T, warp = tid >> 5, lane = tid & 31, sub = threadIdx.x / T;
     const int words = (p.cap + 31) / 32;
-    uint32_t *kept = shared + sub * (p.keep + words), *gone = kept + p.keep;
+    uint32_t *kept = shared + sub * (p.keep + (words + 3) / 4 * 4), *gone = kept + p.keep;
     int *src = lists + sub * 2 * LIST, *dst = src + LIST;
     pdl_trigger();
     pdl_wait();
@@ -657,20 +660,34 @@ __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictPara
     };
     auto key_of = [&](int at, float w) { return at < p.n_sink || at >= recent ? ev_key(INFINITY) : ev_key(w); };
     auto weight_at = [&](int j) { return __uint_as_float((uint32_t)ld_dep(reinterpret_cast<const int *>(weight) + j)); };
-    // Keys, 8 rows of a thread under way at a time.
+    // Keys, those of 16 rows of a thread under way at a time; behind the last one the largest value.
     const int mine = min(len, p.keep);
-    for (int j0 = tid; j0 < mine; j0 += 8 * T) {
-        int at[8];
-        float w[8];
+    auto place_of = [](int at) { return ~((uint32_t)at ^ 0x80000000u); };
+    for (int j0 = 4 * tid; j0 < mine; j0 += 16 * T) {
+        int4 at[4];
+        float4 w[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (j0 + k * T < mine) {
-                at[k] = ld_dep(pos + j0 + k * T);
-                w[k] = weight_at(j0 + k * T);
+        for (int k = 0; k < 4; ++k) {
+            const int j = j0 + k * 4 * T;
+            if (j + 3 < mine && p.wide) {
+                const uint4 x = ld_dep_u4(reinterpret_cast<const uint4 *>(pos + j));
+                at[k] = make_int4(x.x, x.y, x.z, x.w);
+                w[k] = ld_dep_f4(reinterpret_cast<const float4 *>(weight + j));
+            } else if (j < mine) {
+                at[k] = make_int4(ld_dep(pos + j), j + 1 < mine ? ld_dep(pos + j + 1) : 0,
+                                  j + 2 < mine ? ld_dep(pos + j + 2) : 0, j + 3 < mine ? ld_dep(pos + j + 3) : 0);
+                w[k] = make_float4(weight_at(j), j + 1 < mine ? weight_at(j + 1) : 0.f,
+                                   j + 2 < mine ? weight_at(j + 2) : 0.f, j + 3 < mine ? weight_at(j + 3) : 0.f);
             }
+        }
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (j0 + k * T < mine) kept[j0 + k * T] = key_of(at[k], w[k]);
+        for (int k = 0; k < 4; ++k) {
+            const int j = j0 + k * 4 * T;
+            if (j < mine)
+                *reinterpret_cast<uint4 *>(kept + j) =
+                    make_uint4(key_of(at[k].x, w[k].x), j + 1 < mine ? key_of(at[k].y, w[k].y) : ~0u,
+                               j + 2 < mine ? key_of(at[k].z, w[k].z) : ~0u, j + 3 < mine ? key_of(at[k].w, w[k].w) : ~0u);
+        }
     }
     sync();
     auto key = [&](int j) { return j < p.keep ? kept[j] : key_of(ld_dep(pos + j), weight_at(j)); };
@@ -748,11 +765,36 @@ __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictPara
         return sum_all(n);
     };
     // What goes first: small weights, large positions, high rows.
-    auto place = [&](int j) { return ~((uint32_t)ld_dep(pos + j) ^ 0x80000000u); };
+    auto place = [&](int j) { return place_of(ld_dep(pos + j)); };
     auto any = [](int) { return true; };
+    // The same over the keys alone, where all of them are in shared memory and few go: each search counts
+    // the last least key's rows and finds the next.
+    auto border_kept = [&](int &left, uint32_t &at) {
+        uint32_t low = ~0u;
+        for (int j = 4 * tid; j < len; j += 4 * T) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(kept + j);
+            low = min(min(low, min(x.x, x.y)), min(x.z, x.w));
+        }
+        at = least_all(low, 0).x;
+        for (;;) {
+            uint32_t next = ~0u;
+            int n = 0;
+            for (int j = 4 * tid; j < len; j += 4 * T) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(kept + j);
+                n += (x.x == at) + (x.y == at) + (x.z == at) + (x.w == at);
+                next = min(min(next, min(x.x > at ? x.x : ~0u, x.y > at ? x.y : ~0u)),
+                           min(x.z > at ? x.z : ~0u, x.w > at ? x.w : ~0u));
+            }
+            n = sum_all(n);
+            if (n >= left) return n;
+            left -= n;
+            at = least_all(next, 0).x;
+        }
+    };
     int left = E;
     uint32_t w_at = 0, p_at = 0, r_at = 0;                   // borders: rows at them go, too
-    const bool tied = border(key, any, left, w_at) != left;  // not all rows of that weight go
+    const bool tied = (E <= kEvTake && len <= p.keep ? border_kept(left, w_at) : border(key, any, left, w_at)) !=
+                      left;                                  // not all rows of that weight go
     bool twins = false;                                      // nor all of that position among them
     if (tied) {
         auto tie = [&](int j) { return key(j) == w_at; };
@@ -830,7 +872,7 @@ __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictPara
         }
         sync();
         const int moves = min(holes - done, LIST);           // there are as many holes as rows to fill them
-        constexpr int AHEAD = 4;                             // rows under way
+        constexpr int AHEAD = 6;                             // rows under way
         for (int i = tid / per; i < moves; i += AHEAD * rows) {
             uint4 x[AHEAD];
 #pragma unroll
@@ -853,7 +895,7 @@ constexpr int kEvMaxRows = 1 << 20;
 
 template <int NW>
 static magicdec_status launch_evict_t(EvictParams &p, cudaStream_t st) {
-    const int sets = kEvWarps / NW, smem = sets * (p.keep + (p.cap + 31) / 32) * 4;      // at most 192 KB
+    const int sets = kEvWarps / NW, smem = sets * (p.keep + (p.cap + 127) / 128 * 4) * 4;      // at most 192 KB
     if (!magicdec_host::allow_smem_once<heavy_evict_kernel<NW>>(200 * 1024)) return MAGICDEC_ERR_CUDA;
     return magicdec_host::launch_pdl(heavy_evict_kernel<NW>, dim3((unsigned)((p.items + sets - 1) / sets)),
                                      dim3(kEvThreads), (size_t)smem, st, p);
@@ -880,7 +922,8 @@ magicdec_status launch_heavy_evict(int layers, int B, int H_kv, int D, int cap, 
     p.budget = budget;
     p.n_sink = n_sink;
     p.n_recent = n_recent;
-    p.keep = cap < kEvKeep ? cap : cap <= kEvMaxRows / 2 ? kEvKeep : kEvKeep / 2;
+    p.wide = cap % 4 == 0 && magicdec_host::aligned16(weight) && magicdec_host::aligned16(pos);
+    p.keep = cap < kEvKeep ? (cap + 3) / 4 * 4 : cap <= kEvMaxRows / 2 ? kEvKeep : kEvKeep / 2;
     // A warp an item, while its CTAs are not fewer than SMs or its rows so few that more warps gain nothing.
     const bool narrow = cap <= kEvWarpRows && (cap <= 256 || p.items >= magicdec_host::sm_count());
     return narrow ? launch_evict_t<1>(p, st) : launch_evict_t<kEvWarps>(p, st);
