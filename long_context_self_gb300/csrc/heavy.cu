@@ -663,6 +663,7 @@ __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictPara
     // Keys, those of 16 rows of a thread under way at a time; behind the last one the largest value.
     const int mine = min(len, p.keep);
     auto place_of = [](int at) { return ~((uint32_t)at ^ 0x80000000u); };
+    uint32_t low = ~0u;                                      // this thread's least key
     for (int j0 = 4 * tid; j0 < mine; j0 += 16 * T) {
         int4 at[4];
         float4 w[4];
@@ -683,14 +684,94 @@ __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictPara
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int j = j0 + k * 4 * T;
-            if (j < mine)
-                *reinterpret_cast<uint4 *>(kept + j) =
+            if (j < mine) {
+                const uint4 x =
                     make_uint4(key_of(at[k].x, w[k].x), j + 1 < mine ? key_of(at[k].y, w[k].y) : ~0u,
                                j + 2 < mine ? key_of(at[k].z, w[k].z) : ~0u, j + 3 < mine ? key_of(at[k].w, w[k].w) : ~0u);
+                *reinterpret_cast<uint4 *>(kept + j) = x;
+                low = min(min(low, min(x.x, x.y)), min(x.z, x.w));
+            }
         }
     }
     sync();
     auto key = [&](int j) { return j < p.keep ? kept[j] : key_of(ld_dep(pos + j), weight_at(j)); };
+
+    // The listed rows' moves: K, V, weight and position of row src[i] to row dst[i].
+    const int per = 2 * p.vecs, rows = T / per, c = tid % per;   // threads of a row of K and V
+    uint4 *base = (c < p.vecs ? p.kc + c : p.vc + (c - p.vecs)) + row0 * p.vecs;
+    auto move_rows = [&](int moves) {
+        constexpr int AHEAD = 6;                             // rows under way
+        for (int i = tid; i < moves; i += T) {
+            const float w = weight_at(src[i]);
+            const int at = ld_dep(pos + src[i]);
+            weight[dst[i]] = w;
+            pos[dst[i]] = at;
+        }
+        for (int i = tid / per; i < moves; i += AHEAD * rows) {
+            uint4 x[AHEAD];
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k)
+                if (i + k * rows < moves) x[k] = ld_dep_u4(base + (long long)src[i + k * rows] * p.vecs);
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k)
+                if (i + k * rows < moves) base[(long long)dst[i + k * rows] * p.vecs] = x[k];
+        }
+    };
+    if (NW == 1 && E <= kEvTake && len <= p.keep) {
+        // Few rows to go.  The E-th least of the lanes' least keys bounds the E-th least key from above;
+        // hardly more than E keys lie at or below it, and are ranked by comparing each with all.
+        uint32_t rest = low, bound = 0;
+        for (int k = 0; k < E; ++k) {
+            bound = __reduce_min_sync(0xffffffffu, rest);
+            if (lane == __ffs(__ballot_sync(0xffffffffu, rest == bound)) - 1) rest = ~0u;
+        }
+        int found = 0;
+        for (int j0 = 0; j0 < len; j0 += 128) {
+            const int j = j0 + 4 * lane;
+            const uint4 x = j < len ? *reinterpret_cast<const uint4 *>(kept + j) : make_uint4(~0u, ~0u, ~0u, ~0u);
+            if (!__any_sync(0xffffffffu, min(min(x.x, x.y), min(x.z, x.w)) <= bound)) continue;
+            const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const bool in = j + k < len && y[k] <= bound;
+                const unsigned m = __ballot_sync(0xffffffffu, in);
+                const int to = found + __popc(m & ((1u << lane) - 1u));
+                if (in && to < 32) src[to] = j + k;
+                found += __popc(m);
+            }
+        }
+        __syncwarp();
+        if (found <= 32) {
+            const bool in = lane < found;
+            const int row = in ? src[lane] : -1;
+            const uint32_t x = in ? kept[row] : ~0u;
+            const unsigned alike = __match_any_sync(0xffffffffu, x);
+            uint32_t y = 0;                                  // positions only where weights are alike
+            if (__any_sync(0xffffffffu, in && (alike & (alike - 1)))) y = in ? place_of(ld_dep(pos + row)) : 0;
+            int rank = 0;
+            for (int k = 0; k < found; ++k) {
+                const uint32_t x2 = __shfl_sync(0xffffffffu, x, k), y2 = __shfl_sync(0xffffffffu, y, k);
+                const int row2 = __shfl_sync(0xffffffffu, row, k);
+                rank += x2 < x || (x2 == x && (y2 < y || (y2 == y && row2 > row)));
+            }
+            const bool go = in && rank < E, hole = go && row < p.budget;
+            // Of the E rows from the budget on, those that do not go, ascending, into the holes, ascending.
+            bool stay = lane < E;
+            int before = 0;
+            for (unsigned m = __ballot_sync(0xffffffffu, go); m; m &= m - 1) {
+                const int row2 = __shfl_sync(0xffffffffu, row, __ffs(m) - 1);
+                stay = stay && row2 != p.budget + lane;
+                before += row2 < row;
+            }
+            const unsigned ms = __ballot_sync(0xffffffffu, stay);
+            __syncwarp();                                    // src has been read
+            if (hole) dst[before] = row;
+            if (stay) src[__popc(ms & ((1u << lane) - 1u))] = p.budget + lane;
+            __syncwarp();
+            move_rows(__popc(ms));
+            return;
+        }
+    }
 
     // Sums, and least values with the sum of their counts, over the item's threads.
     int turn = 0;                                            // of the two buffers, which take turns
@@ -767,34 +848,9 @@ __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictPara
     // What goes first: small weights, large positions, high rows.
     auto place = [&](int j) { return place_of(ld_dep(pos + j)); };
     auto any = [](int) { return true; };
-    // The same over the keys alone, where all of them are in shared memory and few go: each search counts
-    // the last least key's rows and finds the next.
-    auto border_kept = [&](int &left, uint32_t &at) {
-        uint32_t low = ~0u;
-        for (int j = 4 * tid; j < len; j += 4 * T) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(kept + j);
-            low = min(min(low, min(x.x, x.y)), min(x.z, x.w));
-        }
-        at = least_all(low, 0).x;
-        for (;;) {
-            uint32_t next = ~0u;
-            int n = 0;
-            for (int j = 4 * tid; j < len; j += 4 * T) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(kept + j);
-                n += (x.x == at) + (x.y == at) + (x.z == at) + (x.w == at);
-                next = min(min(next, min(x.x > at ? x.x : ~0u, x.y > at ? x.y : ~0u)),
-                           min(x.z > at ? x.z : ~0u, x.w > at ? x.w : ~0u));
-            }
-            n = sum_all(n);
-            if (n >= left) return n;
-            left -= n;
-            at = least_all(next, 0).x;
-        }
-    };
     int left = E;
     uint32_t w_at = 0, p_at = 0, r_at = 0;                   // borders: rows at them go, too
-    const bool tied = (E <= kEvTake && len <= p.keep ? border_kept(left, w_at) : border(key, any, left, w_at)) !=
-                      left;                                  // not all rows of that weight go
+    const bool tied = border(key, any, left, w_at) != left;  // not all rows of that weight go
     bool twins = false;                                      // nor all of that position among them
     if (tied) {
         auto tie = [&](int j) { return key(j) == w_at; };
@@ -822,8 +878,6 @@ __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictPara
     }
     sync();
     // Holes below the budget and the rows to fill them, listed LIST at a time.
-    const int per = 2 * p.vecs, rows = T / per, c = tid % per;   // threads of a row of K and V
-    uint4 *base = (c < p.vecs ? p.kc + c : p.vc + (c - p.vecs)) + row0 * p.vecs;
     for (int done = 0, holes = 1; done < holes; done += LIST) {
         holes = 0;
         int late = 0;                                        // found so far, alike in all threads
@@ -872,20 +926,7 @@ __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictPara
         }
         sync();
         const int moves = min(holes - done, LIST);           // there are as many holes as rows to fill them
-        constexpr int AHEAD = 6;                             // rows under way
-        for (int i = tid / per; i < moves; i += AHEAD * rows) {
-            uint4 x[AHEAD];
-#pragma unroll
-            for (int k = 0; k < AHEAD; ++k)
-                if (i + k * rows < moves) x[k] = ld_dep_u4(base + (long long)src[i + k * rows] * p.vecs);
-#pragma unroll
-            for (int k = 0; k < AHEAD; ++k)
-                if (i + k * rows < moves) base[(long long)dst[i + k * rows] * p.vecs] = x[k];
-        }
-        for (int i = tid; i < moves; i += T) {
-            weight[dst[i]] = weight_at(src[i]);
-            pos[dst[i]] = ld_dep(pos + src[i]);
-        }
+        move_rows(moves);
         sync();
     }
 }
@@ -924,9 +965,7 @@ magicdec_status launch_heavy_evict(int layers, int B, int H_kv, int D, int cap, 
     p.n_recent = n_recent;
     p.wide = cap % 4 == 0 && magicdec_host::aligned16(weight) && magicdec_host::aligned16(pos);
     p.keep = cap < kEvKeep ? (cap + 3) / 4 * 4 : cap <= kEvMaxRows / 2 ? kEvKeep : kEvKeep / 2;
-    // A warp an item, while its CTAs are not fewer than SMs or its rows so few that more warps gain nothing.
-    const bool narrow = cap <= kEvWarpRows && (cap <= 256 || p.items >= magicdec_host::sm_count());
-    return narrow ? launch_evict_t<1>(p, st) : launch_evict_t<kEvWarps>(p, st);
+    return cap <= kEvWarpRows ? launch_evict_t<1>(p, st) : launch_evict_t<kEvWarps>(p, st);
 }
 
 }  // namespace magicdec
