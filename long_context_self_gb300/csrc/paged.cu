@@ -76,22 +76,48 @@ __device__ __forceinline__ void turn_halves(uint32_t &x, uint32_t &y, float2 c0,
     y = pack_bf16(a0 * c0.y + b0 * c0.x, a1 * c1.y + b1 * c1.x);
 }
 
-// The 16 channels of two words of 8, in fp32.
-__device__ __forceinline__ void unpack16(uint4 y, uint4 z, float (&f)[16]) {
-    const uint32_t w[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+// A lane's 16 channels in fp32, two in a register pair: lo[k] and hi[k] are what pairs 2k and 2k + 1 of
+// the rotation turn, whether those are halves (two words that hold neighbours) or interleaved.
+struct Head16 {
+    uint64_t lo[4], hi[4];
+};
+template <bool INTER>
+__device__ __forceinline__ Head16 unpack16(uint4 y, uint4 z) {
+    const uint32_t a[4] = {y.x, y.y, y.z, y.w}, b[4] = {z.x, z.y, z.z, z.w};
+    Head16 h;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        f[2 * k] = bf_lo(w[k]);
-        f[2 * k + 1] = bf_hi(w[k]);
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t v = INTER ? (k < 2 ? a[2 * k] : b[2 * k - 4]) : a[k], w = INTER ? (k < 2 ? a[2 * k + 1] : b[2 * k - 3]) : b[k];
+        h.lo[k] = INTER ? pair(bf_lo(v), bf_lo(w)) : pair(bf_lo(v), bf_hi(v));
+        h.hi[k] = INTER ? pair(bf_hi(v), bf_hi(w)) : pair(bf_lo(w), bf_hi(w));
     }
+    return h;
+}
+template <bool INTER>
+__device__ __forceinline__ void pack16(const Head16 &h, uint4 &y, uint4 &z) {
+    uint32_t a[4], b[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 l = apart(h.lo[k]), e = apart(h.hi[k]);
+        uint32_t &v = INTER ? (k < 2 ? a[2 * k] : b[2 * k - 4]) : a[k], &w = INTER ? (k < 2 ? a[2 * k + 1] : b[2 * k - 3]) : b[k];
+        v = INTER ? pack_bf16(l.x, e.x) : pack_bf16(l.x, l.y);
+        w = INTER ? pack_bf16(l.y, e.y) : pack_bf16(e.x, e.y);
+    }
+    y = make_uint4(a[0], a[1], a[2], a[3]);
+    z = make_uint4(b[0], b[1], b[2], b[3]);
 }
 
 // Squares of a head's d channels, summed over its LR lanes of 16 channels each.
 template <int LR>
-__device__ __forceinline__ float squares(const float (&f)[16], unsigned lanes) {
-    float s = 0.f;
+__device__ __forceinline__ float squares(const Head16 &h, unsigned lanes) {
+    uint64_t a = 0, b = 0;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) s = fmaf(f[k], f[k], s);
+    for (int k = 0; k < 4; ++k) {
+        a = fma2(h.lo[k], h.lo[k], a);
+        b = fma2(h.hi[k], h.hi[k], b);
+    }
+    const float2 c = apart(add2(a, b));
+    float s = c.x + c.y;
 #pragma unroll
     for (int o = LR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(lanes, s, o);
     return s;
@@ -101,19 +127,25 @@ __device__ __forceinline__ float squares(const float (&f)[16], unsigned lanes) {
 // rounding to bf16 comes behind the rotation).  Heads whose squares leave fp32 are scaled down
 // first: eps, at most 2^128, is nothing beside them.
 template <int LR>
-__device__ __forceinline__ void norm_head(float (&f)[16], uint4 w0, uint4 w1, float eps, unsigned lanes) {
-    float s = squares<LR>(f, lanes), e = eps;
+__device__ __forceinline__ void norm_head(Head16 &h, const Head16 &w, float eps, unsigned lanes) {
+    float s = squares<LR>(h, lanes), e = eps;
     if (s > FLT_MAX) {
+        const uint64_t down = pair(0x1p-70f, 0x1p-70f);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) f[k] *= 0x1p-70f;
-        s = squares<LR>(f, lanes);
+        for (int k = 0; k < 4; ++k) {
+            h.lo[k] = mul2(h.lo[k], down);
+            h.hi[k] = mul2(h.hi[k], down);
+        }
+        s = squares<LR>(h, lanes);
         e *= 0x1p-140f;
     }
     const float inv = rsqrtf(fmaf(s, 1.f / (LR * 16), e));
-    float w[16];
-    unpack16(w0, w1, w);
+    const uint64_t i2 = pair(inv, inv);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) f[k] *= inv * w[k];
+    for (int k = 0; k < 4; ++k) {
+        h.lo[k] = mul2(h.lo[k], mul2(i2, w.lo[k]));
+        h.hi[k] = mul2(h.hi[k], mul2(i2, w.hi[k]));
+    }
 }
 
 // A CTA of NT threads takes a token, LR = d / 16 lanes one of its head rows (q, k and v rows
@@ -128,11 +160,15 @@ __device__ __forceinline__ void norm_head(float (&f)[16], uint4 w0, uint4 w1, fl
 // L2, of 14.9 us at the measured copy rate.
 //
 // NORM: query and key heads are normed before the rotation, in the registers that hold them: a
-// lane's 16 squares and log2(LR) shuffles a row, beside loads that bound the kernel as before.
+// lane's 16 squares and log2(LR) shuffles a row.  That is twice the instructions, and a row's chain is
+// longer, so what counts is how many CTAs fit: two passes under way instead of three, the next
+// loaded as soon as one is taken, the weights in shared memory, fp32 arithmetic by pairs, 80 registers
+// (MINB = 12 CTAs of 64 threads an SM).  128 trees of 32 with inputs from HBM: 27.8 us, with three
+// passes 31, one by one and in single fp32 34; 32,000 prompt tokens of 48 rows 140, 163 and 174 us.
 template <int NT, int LR, bool INTER, bool NORM, int MINB = NT == 64 ? 12 : 3>
-__global__ void __launch_bounds__(NT, NORM ? MINB : 1) paged_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(NT, NORM ? MINB : 0) paged_append_kernel(const AppendParams p) {
     constexpr int ROWS = NT / LR;               // rows of a pass
-    constexpr int AHEAD = 3;                    // passes loaded together
+    constexpr int AHEAD = NORM ? 2 : 3;         // passes under way
     __shared__ float2 cs[LR * 8];               // room for d / 2 angles
     __shared__ int par[kApMaxTree];
     __shared__ unsigned turns[kApMaxTree / 32];
@@ -215,7 +251,7 @@ __global__ void __launch_bounds__(NT, NORM ? MINB : 1) paged_append_kernel(const
     uint16_t *qo = p.q_out + tok * p.H_q * p.d, *ko = p.kp + dst * p.H_kv * p.d - nq * p.d,
              *vo = p.vp + dst * p.H_kv * p.d - nk * p.d;
     for (int r0 = tid / LR; r0 < R; r0 += AHEAD * ROWS) {
-        if (r0 >= AHEAD * ROWS) {
+        if (!NORM && r0 >= AHEAD * ROWS) {
 #pragma unroll
             for (int k = 0; k < AHEAD; ++k)
                 if (r0 + k * ROWS < R) load(r0 + k * ROWS, x[k]);
@@ -225,22 +261,20 @@ __global__ void __launch_bounds__(NT, NORM ? MINB : 1) paged_append_kernel(const
             const int r = r0 + k * ROWS;
             if (r >= R) break;
             uint4 y = x[k][0], z = x[k][1];
+            if (NORM && r + AHEAD * ROWS < R) load(r + AHEAD * ROWS, x[k]);
             if (NORM && r < nk && (r < nq ? p.qw : p.kw)) {
-                float h[16];
-                unpack16(y, z, h);
+                Head16 h = unpack16<INTER>(y, z);
                 const uint4 *w = weight + (r < nq ? 0 : 2 * LR);
-                norm_head<LR>(h, w[v0], w[v1], p.eps, lanes);
+                norm_head<LR>(h, unpack16<INTER>(w[v0], w[v1]), p.eps, lanes);
                 if (turned)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int c = INTER ? 2 * j : j, e = INTER ? 2 * j + 1 : j + 8;
-                        const float lo = h[c], hi = h[e];
-                        h[c] = lo * a[j].x - hi * a[j].y;
-                        h[e] = lo * a[j].y + hi * a[j].x;
+                    for (int j = 0; j < 4; ++j) {
+                        const uint64_t c = pair(a[2 * j].x, a[2 * j + 1].x), e = pair(a[2 * j].y, a[2 * j + 1].y);
+                        const uint64_t lo = h.lo[j], hi = h.hi[j];
+                        h.lo[j] = fma2(lo, c, mul2(hi, pair(-a[2 * j].y, -a[2 * j + 1].y)));
+                        h.hi[j] = fma2(lo, e, mul2(hi, c));
                     }
-                y = make_uint4(pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3]), pack_bf16(h[4], h[5]), pack_bf16(h[6], h[7]));
-                z = make_uint4(pack_bf16(h[8], h[9]), pack_bf16(h[10], h[11]), pack_bf16(h[12], h[13]),
-                               pack_bf16(h[14], h[15]));
+                pack16<INTER>(h, y, z);
             } else if (turned && r < nk) {
                 if (INTER) {
                     y = make_uint4(turn_pair(y.x, a[0]), turn_pair(y.y, a[1]), turn_pair(y.z, a[2]), turn_pair(y.w, a[3]));
