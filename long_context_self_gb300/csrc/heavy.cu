@@ -8,6 +8,7 @@
 #include <climits>
 
 #include "few_rows.cuh"
+#include "heavy.cuh"
 
 namespace magicdec {
 
@@ -30,19 +31,6 @@ namespace magicdec {
 constexpr int kHvKeys = 64;          // keys of a stage
 constexpr int kHvHalf = kHvKeys * 128;   // bytes of 64 channels of them
 constexpr int kHvStages = 8;         // stages of a ring at most
-
-struct HeavyParams {
-    const uint16_t *q;
-    uint16_t *out;
-    float *weight;
-    int32_t *pos;
-    const int32_t *len, *next_pos;
-    int *err;
-    int B, H_q, H_kv, G, n, cap, R;
-    int stride;                      // floats between two query rows' scores
-    int stages;                      // of the ring
-    float scale_log2;                // log2(e) / sqrt(d)
-};
 
 // ROWS: query rows of a warp's tile that can be real, 8 or 16; MT: row tiles (a warp has one).
 template <int D, int ROWS, int MT, bool AGAIN>
@@ -574,6 +562,8 @@ magicdec_status launch_heavy_attn(int B, int H_q, int H_kv, int D, int cap, int 
     p.cap = cap;
     p.R = n * p.G;
     p.scale_log2 = kLog2e / sqrtf((float)D);
+    p.v = v;
+    if (p.R > 8) return launch_heavy_tc(p, D, k, v, st);
     const HeavyPlan z = heavy_plan(B * H_kv, cap, p.R, D);
     p.stride = z.stride;
     p.stages = z.stages;

@@ -40,6 +40,7 @@
 #include <climits>
 
 #include "prefix.cuh"
+#include "tc.cuh"
 
 namespace magicdec {
 
@@ -84,89 +85,6 @@ struct TreeAttnParams {
 };
 
 __device__ __forceinline__ int tr_clamp(int v, int hi) { return v < 0 ? 0 : (v > hi ? hi : v); }
-
-// ---------------------------------------------------------------- tcgen05 forms
-// A K or V tile in shared memory: rows of 64 channels (128 bytes, swizzled), groups of
-// 8 rows `sbo` apart, the two halves of 128 channels `hoff` apart.  Pages of a multiple of
-// 8 rows are copied whole, [group][half][8 rows], by one box; other pages half by half,
-// [half][rows].
-// K is K-major: a row is a key's channels, the reduction runs along it.
-__device__ __forceinline__ uint64_t desc_k(uint32_t saddr, uint32_t sbo) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-    d |= (uint64_t)1u << 16;                   // leading byte offset (unused for swizzled K-major)
-    d |= (uint64_t)(sbo >> 4) << 32;
-    d |= (uint64_t)1u << 46;
-    d |= (uint64_t)2u << 61;
-    return d;
-}
-// V is MN-major: the reduction runs over the rows, 64 channels of a row lie together,
-// the next 64 the leading byte offset further.
-__device__ __forceinline__ uint64_t desc_v(uint32_t saddr, uint32_t sbo, uint32_t hoff) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-    d |= (uint64_t)(hoff >> 4) << 16;
-    d |= (uint64_t)(sbo >> 4) << 32;
-    d |= (uint64_t)1u << 46;
-    d |= (uint64_t)2u << 61;
-    return d;
-}
-
-// D[tmem] (+)= A[tmem] * B[smem], B transposed (MN-major) by the instruction descriptor.
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                             uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-#define TR_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), \
-    "=r"(r[i + 6]), "=r"(r[i + 7])
-#define TR_W8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), \
-    "r"(r[i + 6]), "r"(r[i + 7])
-
-__device__ __forceinline__ void tmem_ld32u(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : TR_R8(r, 0), TR_R8(r, 8), TR_R8(r, 16), TR_R8(r, 24)
-        : "r"(taddr)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : TR_R8(r, 0), TR_R8(r, 8)
-        : "r"(taddr)
-        : "memory");
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-            taddr),
-        TR_W8(r, 0), TR_W8(r, 8)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// One thread of a converged warp, the same each time.  The compiler knows a branch on it
-// for that of a single thread; with a branch on the lane number a product took 150 cycles
-// to issue instead of the 64 that it takes to run (8 products: 1250 -> 560 cycles).
-__device__ __forceinline__ bool elect_one() {
-    uint32_t x;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(x));
-    return x != 0;
-}
 
 // Whether x holds for any of the 64 threads of two warps; a barrier for them, too.
 __device__ __forceinline__ bool pair_any(int id, bool x) {
