@@ -17,49 +17,47 @@ namespace magicdec {
 // A row's weight needs the whole softmax's maximum and sum, which are known when all keys have
 // been seen.  So a cluster of C CTAs takes a (sequence, KV head), each a stretch of its keys, and
 // after one pass over K and V the CTAs exchange (max, sum); then every row's weight is written
-// once, from the scores, which stay in shared memory until then, or, where they would take too
-// much of it (R = 25 and 1500 keys a CTA: 150 KB), are computed again from a second pass over K,
-// out of L2 (AGAIN).  The O of all warps are summed in a fixed order.  No workspace, no
-// atomics, one launch.
+// once, from the scores, which stay in shared memory until then.  The O of all warps are summed in
+// a fixed order.  No workspace, no atomics, one launch.  This is the way of up to 8 query rows whose
+// scores fit; the others' is heavy_tc.cu.
 //
-// A producer warp keeps a ring of stages filled by TMA, 64 keys' K and V each; consumer warps take 16
-// keys of a stage (with more than 16 query rows, two warps the same keys for 16 rows each) through
-// ldmatrix and mma.sync (m16n8k16): at R <= 32 the products are a few percent of the time, and a
-// 128-row tcgen05 tile would be empty but for R rows.  Keys straight from global memory into the
-// fragments, without shared memory, left too few bytes under way (128 sequences over 2053 rows, R = 4:
-// 207 us; 16 over up to 12,001, R = 25: 229 us).
+// A producer warp keeps a ring of stages filled by TMA, 64 keys' K and V each; 4 consumer warps take 16
+// keys of a stage each through ldmatrix and mma.sync (m16n8k16, the lower half of A empty): at 8 rows
+// the products are a few percent of the time.  128 sequences over 2053 rows, R = 4: 184 to 190 us,
+// 5.8 to 6.0 TB/s; with keys straight from global memory into the fragments, which left too few bytes
+// under way, 207; on tcgen05, with the scores computed again, 246.
 constexpr int kHvKeys = 64;          // keys of a stage
 constexpr int kHvHalf = kHvKeys * 128;   // bytes of 64 channels of them
 constexpr int kHvStages = 8;         // stages of a ring at most
+constexpr int kHvRows = 8;           // query rows at most
+constexpr int kHvWarps = 4;          // consumer warps
+constexpr int kHvThreads = kHvWarps * 32 + 32;
 
-// ROWS: query rows of a warp's tile that can be real, 8 or 16; MT: row tiles (a warp has one).
-template <int D, int ROWS, int MT, bool AGAIN>
-__global__ void __launch_bounds__(128 * MT + 32, MT == 2 ? 1 : 2)
+template <int D>
+__global__ void __launch_bounds__(kHvThreads, 2)
     heavy_attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                       const __grid_constant__ CUtensorMap tmk16, const __grid_constant__ CUtensorMap tmv16,
                       const HeavyParams p) {
-    constexpr int CW = 4 * MT, NT = CW * 32 + 32;       // consumer warps; threads
     constexpr int KS = D / 16, HV = D / 64, NB = D / 8;
-    constexpr int HR = ROWS / 8;                        // rows of a lane: lane / 4, and 8 more
     constexpr int OPER = HV * kHvHalf, STAGE = 2 * OPER;
+    constexpr int QHALF = kHvRows * 128;                // bytes of 64 channels of the query rows
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint8_t *ring = smem;
-    float *scores = reinterpret_cast<float *>(smem + p.stages * STAGE);     // [R][stride]; later the warps' O
-    constexpr int QHALF = MT * ROWS * 128;              // bytes of 64 channels of the query rows
+    uint8_t *ring = smem;                               // later the warps' O
+    float *scores = reinterpret_cast<float *>(smem + p.stages * STAGE);     // [R][stride]
     __shared__ __align__(1024) uint8_t qs[HV * QHALF];
     __shared__ uint64_t full[kHvStages], empty[kHvStages];
-    __shared__ float2 wstat[CW][16];                    // of a warp's rows: (max, sum)
-    __shared__ float2 cstat[32];                        // of this CTA
-    __shared__ float2 all[32];                          // of the cluster: (max, 1 / sum)
+    __shared__ float2 wstat[kHvWarps][kHvRows];         // of a warp's keys: (max, sum)
+    __shared__ float2 cstat[kHvRows];                   // of this CTA
+    __shared__ float2 all[kHvRows];                     // of the cluster: (max, 1 / sum)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int lq = lane & 3, lr = lane >> 2;
+    const int lq = lane & 3, lr = lane >> 2;            // fragments: columns 2 lq, row lr
     const int b = blockIdx.z, h = blockIdx.y;
     const uint32_t rank = few_rank(), C = few_ctas();
     const float sl = p.scale_log2;
     if (tid == 0) {
         for (int s = 0; s < p.stages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], CW);
+            mbar_init(&empty[s], kHvWarps);
         }
         mbar_fence_init();
         prefetch_tensormap(&tmk);
@@ -68,7 +66,7 @@ __global__ void __launch_bounds__(128 * MT + 32, MT == 2 ? 1 : 2)
     pdl_trigger();
     pdl_wait();
     // The query rows (row i * G + g: token i, head g of the group), swizzled as the keys.
-    for (int x = tid; x < MT * ROWS * (D / 8); x += NT) {
+    for (int x = tid; x < kHvRows * (D / 8); x += kHvThreads) {
         const int r = x / (D / 8), c = x % (D / 8), i = r / p.G;
         const uint16_t *src = p.q + (((long long)b * p.n + i) * p.H_q + h * p.G + (r - i * p.G)) * D + c * 8;
         *reinterpret_cast<uint4 *>(qs + (c >> 3) * QHALF + swz128(r, c & 7)) =
@@ -81,80 +79,55 @@ __global__ void __launch_bounds__(128 * MT + 32, MT == 2 ? 1 : 2)
     const int per = ((len + (int)C - 1) / (int)C + 15) & ~15;
     const int k0 = min(len, (int)rank * per), k1 = min(len, k0 + per), tiles = (k1 - k0 + kHvKeys - 1) / kHvKeys;
     const long long row0 = ((long long)b * p.H_kv + h) * p.cap;
-    const int first_new = p.next_pos ? len - p.n : INT_MAX;
     bool ok = smem_u32(smem) % 1024 == 0;
     if (!ok && tid == 0) raise_error(p.err, kErrState);
 
-    // The producer's part of a pass: tiles [from, to) of it, of which the first is the ring's `slot`.
-    const uint64_t once = policy_evict_first(), keep = policy_evict_normal();
-    auto produce = [&](int from, int to, uint32_t slot, bool v_too) {
-        for (int t = from; ok && t < to; ++t, ++slot) {
-            const uint32_t st = slot % p.stages;
-            ok = mbar_poll(&empty[st], (slot / p.stages & 1) ^ 1, p.err);
-            if (!ok) return;
-            const int key = k0 + t * kHvKeys, groups = (min(kHvKeys, k1 - key) + 15) / 16;
-            uint8_t *to_k = ring + st * STAGE;
-            const uint64_t pol = AGAIN && v_too ? keep : once;
-            mbar_arrive_expect_tx(&full[st], (uint32_t)(groups * (v_too ? 2 : 1) * HV * 2048));
-            for (int f = 0; f < HV; ++f) {
-                if (groups == 4) {
-                    tma_load_4d(to_k + f * kHvHalf, &tmk, f * 64, key, h, b, &full[st], pol);
-                    if (v_too) tma_load_4d(to_k + OPER + f * kHvHalf, &tmv, f * 64, key, h, b, &full[st], once);
-                } else {
-                    for (int g = 0; g < groups; ++g) {
-                        tma_load_4d(to_k + f * kHvHalf + g * 2048, &tmk16, f * 64, key + g * 16, h, b, &full[st], pol);
-                        if (v_too)
-                            tma_load_4d(to_k + OPER + f * kHvHalf + g * 2048, &tmv16, f * 64, key + g * 16, h, b,
-                                        &full[st], once);
+    if (warp == kHvWarps) {
+        // ------------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            const uint64_t once = policy_evict_first();
+            for (int t = 0; ok && t < tiles; ++t) {
+                const uint32_t st = (uint32_t)t % p.stages;
+                ok = mbar_poll(&empty[st], ((uint32_t)t / p.stages & 1) ^ 1, p.err);
+                if (!ok) break;
+                const int key = k0 + t * kHvKeys, groups = (min(kHvKeys, k1 - key) + 15) / 16;
+                uint8_t *to = ring + st * STAGE;
+                mbar_arrive_expect_tx(&full[st], (uint32_t)(groups * 2 * HV * 2048));
+                for (int f = 0; f < HV; ++f) {
+                    if (groups == 4) {
+                        tma_load_4d(to + f * kHvHalf, &tmk, f * 64, key, h, b, &full[st], once);
+                        tma_load_4d(to + OPER + f * kHvHalf, &tmv, f * 64, key, h, b, &full[st], once);
+                    } else {
+                        for (int g = 0; g < groups; ++g) {
+                            tma_load_4d(to + f * kHvHalf + g * 2048, &tmk16, f * 64, key + g * 16, h, b, &full[st], once);
+                            tma_load_4d(to + OPER + f * kHvHalf + g * 2048, &tmv16, f * 64, key + g * 16, h, b, &full[st],
+                                        once);
+                        }
                     }
                 }
             }
-        }
-    };
-    const int ahead = AGAIN ? min(p.stages, tiles) : 0; // tiles of the second pass that fit the ring beside no other
-    const int mt = MT == 1 ? 0 : warp % MT, kw = warp / MT;
-    float o[NB][2 * HR];
-    float m[HR], l[HR];
-    uint32_t qf[KS][2 * HR];
-    // The fragments of query rows 16 tile .. , as mma.sync takes them.
-    auto load_q = [&](int tile, uint32_t (&to)[KS][2 * HR]) {
-        const uint32_t at = smem_u32(qs) + (uint32_t)tile * 2048;
-#pragma unroll
-        for (int c = 0; c < KS; c += 3 - HR) {
-            if constexpr (HR == 2)
-                ldsm_x4(at + (uint32_t)(c >> 2) * QHALF + swz128(lane & 15, (c & 3) * 2 + (lane >> 4)), to[c][0], to[c][1],
-                        to[c][2], to[c][3]);
-            else
-                ldsm_x4(at + (uint32_t)(c >> 2) * QHALF + swz128(lane & 7, (c & 3) * 2 + (lane >> 3)), to[c][0], to[c][1],
-                        to[c + 1][0], to[c + 1][1]);
-        }
-    };
-    // Query row r sees keys below this.
-    auto seen = [&](int r) { return r < p.R ? min(len - p.n + 1 + r / p.G, k1) : 0; };
-    if (warp == CW) {
-        if (lane == 0) {
-            produce(0, tiles, 0, true);
-            if (AGAIN) produce(0, ahead, tiles, false);
+            // No copy may be in flight when the CTA ends, or when O takes the ring.
+            for (int t = max(0, tiles - p.stages); t < tiles; ++t)
+                mbar_poll(&full[t % p.stages], (uint32_t)t / p.stages & 1, p.err);
         }
         __syncwarp();
-    } else {
-        load_q(mt, qf);
-        int see[HR];
+    }
+    float o[NB][2], m = -INFINITY, l = 0.f;
+    if (warp < kHvWarps) {
+        // Query row r sees keys below this.
+        const int see = lr < p.R ? min(len - p.n + 1 + lr / p.G, k1) : 0;
+        uint32_t qf[KS][2];
 #pragma unroll
-        for (int e = 0; e < HR; ++e) {
-            see[e] = seen(mt * 16 + lr + 8 * e);
-            m[e] = -INFINITY;
-            l[e] = 0.f;
-        }
+        for (int c = 0; c < KS; c += 2)
+            ldsm_x4(smem_u32(qs) + (c >> 2) * QHALF + (swz128(lane & 7, lane >> 3) ^ ((c & 3) * 32)), qf[c][0], qf[c][1],
+                    qf[c + 1][0], qf[c + 1][1]);
 #pragma unroll
-        for (int j = 0; j < NB; ++j)
-#pragma unroll
-            for (int e = 0; e < 2 * HR; ++e) o[j][e] = 0.f;
-        // The scores' place: row r of this warp's tile, key g.
-        float *my = scores + (long long)(mt * 16 + lr) * p.stride - k0;
+        for (int j = 0; j < NB; ++j) o[j][0] = o[j][1] = 0.f;
+        // The scores' place: row lr, key g.
+        float *my = scores + (long long)lr * p.stride - k0;
         // A lane's address in a K tile, and in a V tile: 16-byte chunk c of its row is at c * 16 away from
         // chunk 0 in the sense of an exclusive or (8 chunks a half).
-        const int x4 = lane >> 3, r0 = 16 * kw;
+        const int x4 = lane >> 3, r0 = 16 * warp;
         const uint32_t k_lane = swz128(r0 + (x4 >> 1) * 8 + (lane & 7), x4 & 1);
         const uint32_t v_lane = swz128(r0 + (x4 & 1) * 8 + (lane & 7), x4 >> 1);
         for (int t = 0; t < tiles; ++t) {
@@ -163,75 +136,54 @@ __global__ void __launch_bounds__(128 * MT + 32, MT == 2 ? 1 : 2)
             const int g = k0 + t * kHvKeys + r0;
             if (g < k1) {
                 // Two chains of products a score, so that half as many wait for one another.
-                float s[2][2 * HR], s2[2][2 * HR];
-#pragma unroll
-                for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-                    for (int e = 0; e < 2 * HR; ++e) s[nb][e] = s2[nb][e] = 0.f;
+                float s[2][2] = {}, s2[2][2] = {};
 #pragma unroll
                 for (int c = 0; c < KS; ++c) {
                     uint32_t f0, f1, f2, f3;
                     ldsm_x4(((kt + k_lane) ^ ((c & 3) * 32)) + (c >> 2) * kHvHalf, f0, f1, f2, f3);
-                    few_mma<HR>(c & 1 ? s2[0] : s[0], qf[c], f0, f1);
-                    few_mma<HR>(c & 1 ? s2[1] : s[1], qf[c], f2, f3);
+                    few_mma<1>(c & 1 ? s2[0] : s[0], qf[c], f0, f1);
+                    few_mma<1>(c & 1 ? s2[1] : s[1], qf[c], f2, f3);
                 }
                 // Keys that not every row sees: behind the last one, or of the block's own tokens.
                 const bool edge = g + 16 > len - p.n + 1 || g + 16 > k1;
-                float top[HR];
+                float top = -INFINITY;
 #pragma unroll
-                for (int e = 0; e < HR; ++e) top[e] = -INFINITY;
-#pragma unroll
-                for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-                    for (int e = 0; e < HR; ++e) {
-                        float &x = s[nb][2 * e], &y = s[nb][2 * e + 1];
-                        x = (x + s2[nb][2 * e]) * sl;
-                        y = (y + s2[nb][2 * e + 1]) * sl;
-                        if (edge) {
-                            const int key = g + nb * 8 + 2 * lq;
-                            if (key >= see[e]) x = -INFINITY;
-                            if (key + 1 >= see[e]) y = -INFINITY;
-                        }
-                        if (!AGAIN && mt * 16 + lr + 8 * e < p.R)
-                            *reinterpret_cast<float2 *>(my + (long long)(8 * e) * p.stride + g + nb * 8 + 2 * lq) =
-                                make_float2(x, y);
-                        top[e] = fmaxf(top[e], fmaxf(x, y));
+                for (int nb = 0; nb < 2; ++nb) {
+                    float &x = s[nb][0], &y = s[nb][1];
+                    x = (x + s2[nb][0]) * sl;
+                    y = (y + s2[nb][1]) * sl;
+                    const int key = g + nb * 8 + 2 * lq;
+                    if (edge) {
+                        if (key >= see) x = -INFINITY;
+                        if (key + 1 >= see) y = -INFINITY;
                     }
+                    if (lr < p.R) *reinterpret_cast<float2 *>(my + key) = make_float2(x, y);
+                    top = fmaxf(top, fmaxf(x, y));
+                }
                 // The maximum moves, and O and the sum are scaled, only where it has grown by more than
                 // 2^kFewLazy: weights up to 2^24 instead of 1 cost a floating sum nothing.
-                bool move = false;
+                if (__any_sync(0xffffffffu, top > m + kFewLazy)) {
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    const float to = fmaxf(m, top), f = to == -INFINITY ? 1.f : fast_exp2(m - to);
+                    m = to;
+                    l *= f;
 #pragma unroll
-                for (int e = 0; e < HR; ++e) move |= top[e] > m[e] + kFewLazy;
-                if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-                    for (int e = 0; e < HR; ++e) {
-                        top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
-                        top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
-                        const float to = fmaxf(m[e], top[e]);
-                        const float f = to == -INFINITY ? 1.f : fast_exp2(m[e] - to);
-                        m[e] = to;
-                        l[e] *= f;
-#pragma unroll
-                        for (int j = 0; j < NB; ++j) {
-                            o[j][2 * e] *= f;
-                            o[j][2 * e + 1] *= f;
-                        }
+                    for (int j = 0; j < NB; ++j) {
+                        o[j][0] *= f;
+                        o[j][1] *= f;
                     }
                 }
                 // P in bf16 for the second product: off by at most 2^-8 of itself, as the output's
                 // rounding; the sum is of the unrounded values.
-                uint32_t a[2 * HR];
+                uint32_t a[2];
+                const float mu = m == -INFINITY ? 0.f : m;
 #pragma unroll
-                for (int e = 0; e < HR; ++e) {
-                    const float mu = m[e] == -INFINITY ? 0.f : m[e];
-#pragma unroll
-                    for (int nb = 0; nb < 2; ++nb) {
-                        const float x = fast_exp2(s[nb][2 * e] - mu), y = fast_exp2(s[nb][2 * e + 1] - mu);
-                        s[nb][2 * e] = x;
-                        s[nb][2 * e + 1] = y;
-                        l[e] += x + y;
-                        a[nb * HR + e] = pack_bf16(x, y);
-                    }
+                for (int nb = 0; nb < 2; ++nb) {
+                    s[nb][0] = fast_exp2(s[nb][0] - mu);
+                    s[nb][1] = fast_exp2(s[nb][1] - mu);
+                    l += s[nb][0] + s[nb][1];
+                    a[nb] = pack_bf16(s[nb][0], s[nb][1]);
                 }
                 if (g + 16 > k1) {
                     // Rows of V behind the last may hold anything, and 0 * NaN is NaN: zeros.
@@ -249,25 +201,17 @@ __global__ void __launch_bounds__(128 * MT + 32, MT == 2 ? 1 : 2)
                 const bool odd = p.n > 1 && g + 16 > len - p.n + 1 && few_not_finite<HV>(v, kHvHalf, r0, last, lane);
                 if (odd) {
                     for (int x = 0; x < last; ++x) {
-                        const int from = (lane & ~3) | ((x & 7) >> 1);
-                        float w[HR];
-#pragma unroll
-                        for (int e = 0; e < HR; ++e) {
-                            const float w0 = x < 8 ? s[0][2 * e] : s[1][2 * e];
-                            const float w1 = x < 8 ? s[0][2 * e + 1] : s[1][2 * e + 1];
-                            w[e] = __shfl_sync(0xffffffffu, x & 1 ? w1 : w0, from);
-                        }
+                        const float even = x < 8 ? s[0][0] : s[1][0], next = x < 8 ? s[0][1] : s[1][1];
+                        const float w = __shfl_sync(0xffffffffu, x & 1 ? next : even, (lane & ~3) | ((x & 7) >> 1));
 #pragma unroll
                         for (int j = 0; j < NB; ++j) {
                             uint32_t z =
                                 *reinterpret_cast<const uint32_t *>(v + (j >> 3) * kHvHalf + swz128(r0 + x, j & 7) + 4 * lq);
                             z &= few_odd_bits(z);
-#pragma unroll
-                            for (int e = 0; e < HR; ++e)
-                                if (z && g + x < see[e]) {
-                                    o[j][2 * e] = fmaf(w[e], __uint_as_float(z << 16), o[j][2 * e]);
-                                    o[j][2 * e + 1] = fmaf(w[e], __uint_as_float(z & 0xffff0000u), o[j][2 * e + 1]);
-                                }
+                            if (z && g + x < see) {
+                                o[j][0] = fmaf(w, __uint_as_float(z << 16), o[j][0]);
+                                o[j][1] = fmaf(w, __uint_as_float(z & 0xffff0000u), o[j][1]);
+                            }
                         }
                     }
                 }
@@ -281,266 +225,111 @@ __global__ void __launch_bounds__(128 * MT + 32, MT == 2 ? 1 : 2)
                         f2 &= ~few_odd_bits(f2);
                         f3 &= ~few_odd_bits(f3);
                     }
-                    few_mma<HR>(o[j], a, f0, f1);
-                    few_mma<HR>(o[j + 1], a, f2, f3);
+                    few_mma<1>(o[j], a, f0, f1);
+                    few_mma<1>(o[j + 1], a, f2, f3);
                 }
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[st]);
         }
-        // The warps' maxima and sums.
-#pragma unroll
-        for (int e = 0; e < HR; ++e) {
-            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-            if (lq == 0) wstat[warp][lr + 8 * e] = make_float2(m[e], l[e]);
-        }
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        if (lq == 0) wstat[warp][lr] = make_float2(m, l);
     }
     __syncthreads();
-    // The CTA's, the cluster's.
+    // The warps' maxima and sums, the CTA's, the cluster's.
     auto join = [](float2 &s, float2 x) {
         const float mx = fmaxf(s.x, x.x), mu = mx == -INFINITY ? 0.f : mx;
         s = make_float2(mx, s.y * fast_exp2(s.x - mu) + x.y * fast_exp2(x.x - mu));
     };
-    if (tid < p.R) {
+    if (tid < kHvRows) {
         float2 s = make_float2(-INFINITY, 0.f);
-        for (int w = 0; w < CW / MT; ++w) join(s, wstat[w * MT + tid / 16][tid % 16]);
+        for (int w = 0; w < kHvWarps; ++w) join(s, wstat[w][tid]);
         cstat[tid] = s;
     }
     if (C > 1) few_cluster_sync();
-    if (tid < 32) {
+    if (tid < kHvRows) {
         float2 s = make_float2(-INFINITY, 0.f);
-        if (tid < p.R) {
-            if (C > 1)
-                for (uint32_t c = 0; c < C; ++c) join(s, few_ld2(few_at(&cstat[tid], c)));
-            else
-                s = cstat[tid];
-        }
+        if (C > 1)
+            for (uint32_t c = 0; c < C; ++c) join(s, few_ld2(few_at(&cstat[tid], c)));
+        else
+            s = cstat[tid];
         all[tid] = make_float2(s.x == -INFINITY ? 0.f : s.x, s.y > 0.f ? 1.f / s.y : 0.f);
     }
     __syncthreads();
-
-    // Every row's weight.
-    auto add_weight = [&](int j, float old, float sum) {
+    // Every row's weight, summed over the query rows in their order.
+    const int first_new = p.next_pos ? len - p.n : INT_MAX;
+    for (int j = k0 + tid; j < k1; j += kHvThreads) {
+        const float old = p.weight[row0 + j];
+        float sum = 0.f;
+        for (int r = 0; r < p.R; ++r)
+            sum = fmaf(fast_exp2(scores[(long long)r * p.stride + j - k0] - all[r].x), all[r].y, sum);
         p.weight[row0 + j] = (j >= first_new ? 0.f : old) + sum;
         if (j >= first_new) p.pos[row0 + j] = ld_dep(p.next_pos + b) + (j - first_new);
-    };
-    if (!AGAIN) {
-        // Summed over the query rows in their order.
-        for (int j = k0 + tid; j < k1; j += NT) {
-            const float old = p.weight[row0 + j];
-            float sum = 0.f;
-            for (int r = 0; r < p.R; ++r)
-                sum = fmaf(fast_exp2(scores[(long long)r * p.stride + j - k0] - all[r].x), all[r].y, sum);
-            add_weight(j, old, sum);
-        }
-        __syncthreads();
     }
     // O of the warps, in the softmax's own scale.
-    float *osum = scores;                               // [CW / MT][R][D]
-    if (warp < CW) {
+    float *osum = reinterpret_cast<float *>(ring);      // [kHvWarps][R][D]
+    if (warp < kHvWarps && lr < p.R) {
+        const float f = m == -INFINITY ? 0.f : fast_exp2(m - all[lr].x) * all[lr].y;
+        float *to = osum + (warp * p.R + lr) * D + 2 * lq;
 #pragma unroll
-        for (int e = 0; e < HR; ++e) {
-            const int r = mt * 16 + lr + 8 * e;
-            if (r >= p.R) continue;
-            const float f = m[e] == -INFINITY ? 0.f : fast_exp2(m[e] - all[r].x) * all[r].y;
-            float *to = osum + ((long long)kw * p.R + r) * D + 2 * lq;
-#pragma unroll
-            for (int j = 0; j < NB; ++j)
-                *reinterpret_cast<float2 *>(to + j * 8) = make_float2(o[j][2 * e] * f, o[j][2 * e + 1] * f);
-        }
+        for (int j = 0; j < NB; ++j) *reinterpret_cast<float2 *>(to + j * 8) = make_float2(o[j][0] * f, o[j][1] * f);
     }
-    if (AGAIN) {
-        // The second pass over K: a warp has 64 / CW keys of a stage and all query rows.
-        constexpr int KN = kHvKeys / CW / 8;            // in groups of 8
-        if (warp == CW) {
-            if (lane == 0) {
-                produce(ahead, tiles, tiles + ahead, false);
-                // No copy may be in flight when the CTA ends.
-                for (int t = max(0, 2 * tiles - p.stages); t < 2 * tiles; ++t)
-                    mbar_poll(&full[t % p.stages], (uint32_t)t / p.stages & 1, p.err);
-            }
-            __syncwarp();
-        } else {
-            uint32_t q2[MT][KS][2 * HR];
-            float2 at[MT][HR];
-            int see[MT][HR];
-#pragma unroll
-            for (int x = 0; x < MT; ++x) {
-                load_q(x, q2[x]);
-#pragma unroll
-                for (int e = 0; e < HR; ++e) {
-                    at[x][e] = all[x * 16 + lr + 8 * e];
-                    see[x][e] = seen(x * 16 + lr + 8 * e);
-                }
-            }
-            const uint32_t k_lane = swz128(warp * 8 * KN + (lane & 7), lane >> 3);
-            for (int t = 0; t < tiles; ++t) {
-                const uint32_t slot = tiles + t, st = slot % p.stages, kt = smem_u32(ring + st * STAGE);
-                const int g = k0 + t * kHvKeys + warp * 8 * KN;
-                float old[KN][2];
-#pragma unroll
-                for (int nb = 0; nb < KN; ++nb)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int key = g + nb * 8 + 2 * lq + x;
-                        old[nb][x] = lr == 0 && key < k1 ? p.weight[row0 + key] : 0.f;
-                    }
-                ok = few_wait(&full[st], slot / p.stages & 1, p.err, ok, lane);
-                if (g < k1) {
-#pragma unroll
-                    for (int nb = 0; nb < KN; ++nb) {
-                        float s[MT][2 * HR];
-#pragma unroll
-                        for (int x = 0; x < MT; ++x)
-#pragma unroll
-                            for (int e = 0; e < 2 * HR; ++e) s[x][e] = 0.f;
-#pragma unroll
-                        for (int c = 0; c < KS; c += 2) {
-                            uint32_t f0, f1, f2, f3;
-                            ldsm_x4(((kt + k_lane + nb * 1024) ^ ((c & 3) * 32)) + (c >> 2) * kHvHalf, f0, f1, f2, f3);
-#pragma unroll
-                            for (int x = 0; x < MT; ++x) {
-                                few_mma<HR>(s[x], q2[x][c], f0, f1);
-                                few_mma<HR>(s[x], q2[x][c + 1], f2, f3);
-                            }
-                        }
-                        const int key = g + nb * 8 + 2 * lq;
-                        float w0 = 0.f, w1 = 0.f;
-#pragma unroll
-                        for (int x = 0; x < MT; ++x)
-#pragma unroll
-                            for (int e = 0; e < HR; ++e) {
-                                if (key < see[x][e]) w0 = fmaf(fast_exp2(s[x][2 * e] * sl - at[x][e].x), at[x][e].y, w0);
-                                if (key + 1 < see[x][e])
-                                    w1 = fmaf(fast_exp2(s[x][2 * e + 1] * sl - at[x][e].x), at[x][e].y, w1);
-                            }
-#pragma unroll
-                        for (int d = 4; d < 32; d <<= 1) {
-                            w0 += __shfl_xor_sync(0xffffffffu, w0, d);
-                            w1 += __shfl_xor_sync(0xffffffffu, w1, d);
-                        }
-                        if (lr == 0) {
-                            if (key < k1) add_weight(key, old[nb][0], w0);
-                            if (key + 1 < k1) add_weight(key + 1, old[nb][1], w1);
-                        }
-                    }
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[st]);
-            }
-        }
-    } else if (warp == CW && lane == 0) {
-        for (int t = max(0, tiles - p.stages); t < tiles; ++t)
-            mbar_poll(&full[t % p.stages], (uint32_t)t / p.stages & 1, p.err);
-    }
-    __syncwarp();
-    // O summed over the warps and the CTAs, each of which has a share of the channels.
+    // Summed over the warps and the CTAs, each of which has a share of the channels.
     if (C > 1) few_cluster_sync();
     else __syncthreads();
     const int vecs = p.R * (D / 4), share = (vecs + (int)C - 1) / (int)C;
-    for (int i = (int)rank * share + tid; i < min(vecs, (int)(rank + 1) * share); i += NT) {
+    for (int i = (int)rank * share + tid; i < min(vecs, (int)(rank + 1) * share); i += kHvThreads) {
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         for (uint32_t c = 0; c < C; ++c) {
             const uint32_t base = few_at(osum, c);
 #pragma unroll
-            for (int w = 0; w < CW / MT; ++w) {
+            for (int w = 0; w < kHvWarps; ++w) {
                 const float4 x = few_ld4(base + (uint32_t)(w * vecs + i) * 16);
-                s.x += x.x;
-                s.y += x.y;
-                s.z += x.z;
-                s.w += x.w;
+                s = make_float4(s.x + x.x, s.y + x.y, s.z + x.z, s.w + x.w);
             }
         }
         const int r = i / (D / 4), c4 = i - r * (D / 4), t = r / p.G;
         *reinterpret_cast<uint2 *>(p.out + (((long long)b * p.n + t) * p.H_q + h * p.G + (r - t * p.G)) * D + c4 * 4) =
             make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
     }
-    if (C > 1) few_cluster_sync();                       // no CTA ends while another reads its O
+    if (C > 1) few_cluster_sync();                      // no CTA ends while another reads its O
 }
 
 // ----------------------------------------------------------------- host side
-constexpr int kHvMaxCluster = 8;
-constexpr int kHvScores = 40 * 1024;     // scores of a CTA that stay in shared memory
-constexpr int kHvStatic = 11 * 1024;     // room for the query rows and what else is not sized by the call
+constexpr int kHvScores = 40 * 1024;     // scores of a CTA that stay in shared memory at most
+constexpr int kHvStatic = 8 * 1024;      // room for the query rows and what else is not sized by the call
 
-struct HeavyPlan {
-    int C, stages, stride;
-    size_t smem;
-    bool again;
-};
-
-static HeavyPlan heavy_plan(int pairs, int cap, int R, int D) {
-    HeavyPlan z;
-    // How wide a cluster: a CTA's stages take the time of HBM's share of an SM (two CTAs an SM, or one at
-    // half the time), and some 6 us go by before and after them; CTAs come in waves, the last one
-    // part full.  128 sequences of 2053 rows, 8 heads, R = 4, clusters of 1, 2, 4 and 8: 184, 195, 216 and
-    // 331 us; 16 of up to 12,001, R = 25: 257, 178, 176 and 265.
-    const double slots = (R > 16 ? 1.0 : 2.0) * magicdec_host::sm_count();
-    double best = 0;
-    z.C = 1;
-    for (int C = 1; C <= kHvMaxCluster; C *= 2) {
-        const double waves = pairs * C / slots + 0.5;
-        const bool twice = ((long long)cap + C - 1) / C * R * 4 > kHvScores;
-        const double t = (waves > 1 ? waves : 1) * (((cap + C - 1) / C + kHvKeys - 1) / kHvKeys * (twice ? 2.2 : 1.4) + 6.0);
-        if (C == 1 || t < best) {
-            best = t;
-            z.C = C;
-        }
-    }
-    const long long per = (((long long)cap + z.C - 1) / z.C + 15) / 16 * 16;
-    // 8 floats more than a multiple of 32: neighbouring rows' scores lie in other banks.
-    const long long stride = (per + 23) / 32 * 32 + 8, scores = stride * R * 4, o = 4ll * R * D * 4;
-    z.again = scores > kHvScores;
-    z.stride = z.again ? 0 : (int)stride;
-    const long long rest = (z.again || o > scores ? o : scores), stage = D / 64 * 2ll * kHvHalf;
-    // Two CTAs an SM (one with more than 16 query rows, whose registers fill it).
-    const long long room = (R > 16 ? magicdec_host::max_smem_optin() - kHvStatic
-                                   : magicdec_host::max_smem_optin() / 2 - kHvStatic * 3 / 4) - rest;
-    long long stages = room / stage, tiles = (per + kHvKeys - 1) / kHvKeys * (z.again ? 2 : 1);
-    if (stages > kHvStages) stages = kHvStages;
-    if (stages > tiles) stages = tiles;
-    z.stages = (int)(stages < 1 ? 1 : stages);
-    z.smem = (size_t)(z.stages * stage + rest);
-    return z;
+// The time of a launch by clusters of C, in us, as far as it hangs on C: CTAs come in waves, two an
+// SM, the last one part full; a CTA's tiles take `each`, HBM's share of an SM, and `way` goes by
+// before and after them.
+double heavy_time(long long pairs, int cap, int C, int keys, double each, double way) {
+    const double waves = pairs * C / (2.0 * magicdec_host::sm_count()) + 0.5;
+    return (waves > 1 ? waves : 1) * ((((long long)cap + C - 1) / C + keys - 1) / keys * each + way);
 }
 
-template <int D, int ROWS, int MT, bool AGAIN>
-static magicdec_status launch_heavy_t(const CUtensorMap (&tm)[4], const HeavyParams &p, const HeavyPlan &z,
-                                      cudaStream_t st) {
-    if (!magicdec_host::allow_smem_once<heavy_attn_kernel<D, ROWS, MT, AGAIN>>(magicdec_host::max_smem_optin() - kHvStatic))
+template <int D>
+static magicdec_status launch_heavy_t(const CUtensorMap (&tm)[4], const HeavyParams &p, int C, size_t smem, cudaStream_t st) {
+    if (!magicdec_host::allow_smem_once<heavy_attn_kernel<D>>(magicdec_host::max_smem_optin() / 2))
         return MAGICDEC_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)z.C, (unsigned)p.H_kv, (unsigned)p.B);
-    cfg.blockDim = dim3(128 * MT + 32);
-    cfg.dynamicSmemBytes = z.smem;
+    cfg.gridDim = dim3((unsigned)C, (unsigned)p.H_kv, (unsigned)p.B);
+    cfg.blockDim = dim3(kHvThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = z.C;
+    attr[1].val.clusterDim.x = C;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, heavy_attn_kernel<D, ROWS, MT, AGAIN>, tm[0], tm[1], tm[2], tm[3], p) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, heavy_attn_kernel<D>, tm[0], tm[1], tm[2], tm[3], p) != cudaSuccess)
         return MAGICDEC_ERR_CUDA;
     return magicdec_host::launch_status();
-}
-
-template <int D>
-static magicdec_status launch_heavy_d(const CUtensorMap (&tm)[4], const HeavyParams &p, const HeavyPlan &z,
-                                      cudaStream_t st) {
-    if (z.again)
-        return p.R <= 8    ? launch_heavy_t<D, 8, 1, true>(tm, p, z, st)
-               : p.R <= 16 ? launch_heavy_t<D, 16, 1, true>(tm, p, z, st)
-                           : launch_heavy_t<D, 16, 2, true>(tm, p, z, st);
-    return p.R <= 8    ? launch_heavy_t<D, 8, 1, false>(tm, p, z, st)
-           : p.R <= 16 ? launch_heavy_t<D, 16, 1, false>(tm, p, z, st)
-                       : launch_heavy_t<D, 16, 2, false>(tm, p, z, st);
 }
 
 magicdec_status launch_heavy_attn(int B, int H_q, int H_kv, int D, int cap, int n, const uint16_t *q,
@@ -548,6 +337,7 @@ magicdec_status launch_heavy_attn(int B, int H_q, int H_kv, int D, int cap, int 
                                   float *weight, int32_t *pos, uint16_t *out, cudaStream_t st) {
     HeavyParams p{};
     p.q = q;
+    p.v = v;
     p.out = out;
     p.weight = weight;
     p.pos = pos;
@@ -562,11 +352,31 @@ magicdec_status launch_heavy_attn(int B, int H_q, int H_kv, int D, int cap, int 
     p.cap = cap;
     p.R = n * p.G;
     p.scale_log2 = kLog2e / sqrtf((float)D);
-    p.v = v;
-    if (p.R > 8) return launch_heavy_tc(p, D, k, v, st);
-    const HeavyPlan z = heavy_plan(B * H_kv, cap, p.R, D);
-    p.stride = z.stride;
-    p.stages = z.stages;
+    // Clusters of 1 to 8 whose scores fit, by the time they should take.  128 sequences of 2053 rows, 8
+    // heads, R = 4, clusters of 1, 2, 4 and 8: 184, 195, 216 and 331 us; 16 of up to 12,001 in
+    // clusters of 8, R = 5: 92 us, and on tcgen05, in clusters of 4, 109.
+    int C = 0;
+    double least = 0;
+    for (int c = 1; p.R <= kHvRows && c <= 8; c *= 2) {
+        const long long per = (((long long)cap + c - 1) / c + 15) / 16 * 16;
+        // 8 floats more than a multiple of 32: neighbouring rows' scores lie in other banks.
+        const long long stride = (per + 23) / 32 * 32 + 8;
+        if (stride * p.R * 4 > kHvScores) continue;
+        const double t = heavy_time((long long)B * H_kv, cap, c, kHvKeys, D == 128 ? 1.4 : 0.8, 6.0);
+        if (C == 0 || t < least) {
+            least = t;
+            C = c;
+            p.stride = (int)stride;
+        }
+    }
+    if (C == 0) return launch_heavy_tc(p, D, k, v, st);
+    // The ring takes what two CTAs an SM leave beside the scores, in the end the warps' O.
+    const int stage = D / 64 * 2 * kHvHalf, scores = p.stride * p.R * 4;
+    const int tiles = (((cap + C - 1) / C + 15) / 16 * 16 + kHvKeys - 1) / kHvKeys;
+    p.stages = (magicdec_host::max_smem_optin() / 2 - kHvStatic - scores) / stage;
+    if (p.stages > kHvStages) p.stages = kHvStages;
+    if (p.stages > tiles) p.stages = tiles;
+    static_assert(kHvWarps * kHvRows * 64 * 4 <= 2 * kHvHalf, "a stage has room for the warps' O");
     // (channels, rows, heads, sequences), boxes of 64 channels of a stage's rows, and of 16 for its end.
     CUtensorMap tm[4];
     const uint64_t dims[4] = {(uint64_t)D, (uint64_t)cap, (uint64_t)H_kv, (uint64_t)B};
@@ -577,7 +387,8 @@ magicdec_status launch_heavy_attn(int B, int H_q, int H_kv, int D, int cap, int 
         !magicdec_host::encode_tmap_bf16_4d(&tm[2], k, dims, strides, box16) ||
         !magicdec_host::encode_tmap_bf16_4d(&tm[3], v, dims, strides, box16))
         return MAGICDEC_ERR_CUDA;
-    return D == 128 ? launch_heavy_d<128>(tm, p, z, st) : launch_heavy_d<64>(tm, p, z, st);
+    const size_t smem = (size_t)p.stages * stage + scores;
+    return D == 128 ? launch_heavy_t<128>(tm, p, C, smem, st) : launch_heavy_t<64>(tm, p, C, smem, st);
 }
 
 // ------------------------------------------------------------------ eviction

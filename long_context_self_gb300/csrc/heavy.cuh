@@ -15,11 +15,12 @@ struct HeavyParams {
     int *err;
     int B, H_q, H_kv, G, n, cap, R;
     int stride;                      // floats between two query rows' scores
-    int stages;                      // of the ring
+    int stages;                      // of the ring (both: heavy.cu's way only)
     float scale_log2;                // log2(e) / sqrt(d)
 };
 
-// By 9 to 32 query rows of a KV head.
+double heavy_time(long long pairs, int cap, int C, int keys, double each, double way);
+// By up to 32 query rows of a KV head, the scores computed twice.
 magicdec_status launch_heavy_tc(const HeavyParams &p, int D, const uint16_t *k, const uint16_t *v, cudaStream_t st);
 
 }  // namespace magicdec

@@ -1,13 +1,14 @@
-// heavy_tc.cu -- attention over a heavy-hitter draft cache by 9 to 32 query rows of a KV head, on the
-// fifth-generation tensor cores (tcgen05 + TMEM), sm_103a.  What it computes, and the way of up to 8
-// rows: heavy.cu.
+// heavy_tc.cu -- attention over a heavy-hitter draft cache on the fifth-generation tensor cores
+// (tcgen05 + TMEM), by up to 32 query rows of a KV head (sm_103a).  What it computes, and the way of
+// up to 8 rows whose scores fit shared memory: heavy.cu.
 //
 // With the keys as the 128 rows of a tile, S^T = K Q^T (128 keys x NR query rows) puts a key in a
 // TMEM lane: its thread has the key's scores for all query rows, so that a row's weight is a sum
 // inside one thread, and the running maxima need no shuffles (they are held at values that a score
 // may exceed by 2^24 before any is moved).  O^T += V^T P^T (d channels x NR) takes V as it lies
 // and P from shared memory, 64 bytes a key.  A quarter of the instructions of mma.sync tiles
-// of 16 rows, which bounded these row counts (16 sequences of up to 12,001, R = 25: 166 us).
+// of 16 rows, which bounded 9 rows and more (16 sequences of up to 12,001, R = 25: 166 us by them, 127
+// so, 3.2 TB/s).
 //
 // A row's weight needs the softmax's final maximum and sum: a second pass over K, out of L2, computes
 // the scores again.  CTAs, clusters and exchange as in heavy.cu, two CTAs an SM.
@@ -435,13 +436,12 @@ static magicdec_status launch_ht_t(const CUtensorMap &tmk, const CUtensorMap &tm
 }
 
 magicdec_status launch_heavy_tc(const HeavyParams &p, int D, const uint16_t *k, const uint16_t *v, cudaStream_t st) {
-    // How wide a cluster: a CTA's tiles take the time of HBM's share of an SM, on which there are two,
-    // and some 8 us go by before and after them; CTAs come in waves, the last one part full.
+    // Clusters of 1 to 8, by the time they should take.  16 sequences of up to 12,001 rows, 8 heads,
+    // R = 25, clusters of 1, 2, 4 and 8: 257, 149, 127 and 132 us; 64 of 2053, R = 4: 87, 90, 115 and 184.
     int best = 1;
     double least = 0;
     for (int C = 1; C <= 8; C *= 2) {
-        const double waves = (double)p.B * p.H_kv * C / (2.0 * magicdec_host::sm_count()) + 0.5;
-        const double t = (waves > 1 ? waves : 1) * (((p.cap + C - 1) / C + kHtKeys - 1) / kHtKeys * (D == 128 ? 3.2 : 1.8) + 8.0);
+        const double t = heavy_time((long long)p.B * p.H_kv, p.cap, C, kHtKeys, D == 128 ? 3.2 : 1.8, 12.0);
         if (C == 1 || t < least) {
             least = t;
             best = C;
