@@ -4,7 +4,7 @@
                                                  [--reps N] [--warmup W] [--budget K] [--nodes N] [--page P]
 
 entry: verify | draft | topk | pq | pq_build | accept | accept_greedy | snapkv | gather | draft_cache |
-       paged_append | tree_attn | tree_accept | tree_commit
+       paged_append | norm_append | tree_attn | prefix_attn | tree_accept | tree_commit | heavy_attn | heavy_evict
 
 Inputs come from ``synth`` (seeded, resident on the GPU before timing); each
 call is launched `reps` times back to back after `warmup` untimed calls and
@@ -42,8 +42,8 @@ def _time(fn: Callable[[], object], reps: int, warmup: int) -> float:
 def main(argv=None) -> None:
     ap = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
     ap.add_argument("entry", choices=["verify", "draft", "topk", "pq", "pq_build", "accept", "accept_greedy", "snapkv",
-                                      "gather", "draft_cache", "paged_append", "tree_attn", "tree_accept",
-                                      "tree_commit"])
+                                      "gather", "draft_cache", "paged_append", "norm_append", "tree_attn",
+                                      "prefix_attn", "tree_accept", "tree_commit", "heavy_attn", "heavy_evict"])
     ap.add_argument("--pq-centroids", type=int, default=256)
     ap.add_argument("--pq-iters", type=int, default=2)
     ap.add_argument("--workload", default="llama8b_b128_l32k", choices=sorted(synth.WORKLOADS))
@@ -51,8 +51,10 @@ def main(argv=None) -> None:
     ap.add_argument("--gamma", type=int, default=0, help="override the workload's draft length (verify: gamma+1 rows)")
     ap.add_argument("--reps", type=int, default=5)
     ap.add_argument("--warmup", type=int, default=2)
-    ap.add_argument("--nodes", type=int, default=16, help="nodes of a drafted tree (paged_append, tree_*)")
-    ap.add_argument("--page", type=int, default=16, help="rows of a cache page (paged_append, tree_*)")
+    ap.add_argument("--nodes", type=int, default=16, help="nodes of a drafted tree (*_append, tree_*, prefix_attn), tokens of a "
+                    "block (heavy_attn), rows to go (heavy_evict)")
+    ap.add_argument("--page", type=int, default=16, help="rows of a cache page (*_append, tree_*, prefix_attn)")
+    ap.add_argument("--own", type=int, default=256, help="own positions of a sequence behind the prefix (prefix_attn)")
     ap.add_argument("--budget", type=int, default=0, help="draft / Top-K / SnapKV budget (default: the workload's)")
     args = ap.parse_args(argv)
 
@@ -145,7 +147,7 @@ def main(argv=None) -> None:
         fn = cycle
         nbytes = 2.0 * w.gamma * w.B * w.H_kv * w.d * 2 * 2 * 2
         info.update(cap=cap, gamma=w.gamma)
-    elif args.entry in ("paged_append", "tree_attn", "tree_commit"):
+    elif args.entry in ("paged_append", "norm_append", "tree_attn", "tree_commit"):
         n, page = args.nodes, args.page
         mp = -(-(w.L + n) // page)
         table = torch.randperm(w.B * mp, device=dev).view(w.B, mp).to(torch.int32)
@@ -160,11 +162,16 @@ def main(argv=None) -> None:
             fn = lambda: mb.magicdec_tree_attn(q, kp, vp, table, sl, parent=parent, out=out)
             nbytes = 2.0 * w.B * (w.L + n) * row + 2.0 * q.numel() * 2
             info["tflop"] = 4.0 * w.B * n * w.L * w.H_q * w.d / 1e12
-        elif args.entry == "paged_append":
+        elif args.entry in ("paged_append", "norm_append"):
             k, v = (synth.randn_bf16((w.B, n, w.H_kv, w.d), gen, dev) for _ in range(2))
             inv = (500000.0 ** (-torch.arange(0, w.d, 2, dtype=torch.float64, device=dev) / w.d)).float()
             out = torch.empty_like(q)
-            fn = lambda: mb.magicdec_paged_append(k, v, kp, vp, table, sl, inv, q=q, parent=parent, q_out=out)
+            if args.entry == "norm_append":
+                nw = torch.ones((w.d,), dtype=torch.bfloat16, device=dev)
+                fn = lambda: mb.magicdec_norm_append(k, v, kp, vp, table, sl, inv, q=q, q_weight=nw, k_weight=nw,
+                                                     parent=parent, q_out=out)
+            else:
+                fn = lambda: mb.magicdec_paged_append(k, v, kp, vp, table, sl, inv, q=q, parent=parent, q_out=out)
             nbytes = 4.0 * q.numel() + 4.0 * w.B * n * row
         else:
             acc = min(w.gamma, n - 1)
@@ -174,6 +181,38 @@ def main(argv=None) -> None:
             fn = lambda: mb.magicdec_tree_commit(kp, vp, table, sl, path, n_acc)
             nbytes = 4.0 * w.B * acc * row
         info.update(nodes=n, page=page)
+    elif args.entry == "prefix_attn":
+        n, page = args.nodes, args.page
+        pp, mp = -(-w.L // page), -(-(args.own + n) // page)
+        perm = torch.randperm(pp + w.B * mp, device=dev).to(torch.int32)
+        ptable, table = perm[:pp].view(1, pp).contiguous(), perm[pp:].view(w.B, mp).contiguous()
+        gen = synth.gen(dev, w.seed * 13 + 3)
+        kp = synth.randn_bf16((pp + w.B * mp, page, w.H_kv, w.d), gen, dev)
+        vp = synth.randn_bf16((pp + w.B * mp, page, w.H_kv, w.d), gen, dev)
+        parent = ((torch.arange(n, device=dev) + 1) // 2 - 1).to(torch.int32).expand(w.B, n).contiguous()
+        q = synth.randn_bf16((w.B, n, w.H_q, w.d), gen, dev)
+        out, plen, own = torch.empty_like(q), sl[:1].clone(), torch.full_like(sl, args.own)
+        fn = lambda: mb.magicdec_prefix_attn(q, kp, vp, ptable, plen, table, own, parent=parent, out=out)
+        nbytes = 4.0 * (w.L + w.B * (args.own + n)) * w.H_kv * w.d + 2.0 * q.numel() * 2
+        info.update(nodes=n, page=page, own=args.own, tflop=4.0 * w.B * n * (w.L + args.own) * w.H_q * w.d / 1e12)
+    elif args.entry in ("heavy_attn", "heavy_evict"):
+        n, rows = args.nodes, budget + args.nodes
+        gen = synth.gen(dev, w.seed * 13 + 4)
+        kc, vc = (synth.randn_bf16((w.B, w.H_kv, rows, w.d), gen, dev) for _ in range(2))
+        weight = torch.rand((w.B, w.H_kv, rows), device=dev, generator=gen)
+        pos = torch.arange(rows, dtype=torch.int32, device=dev).expand(w.B, w.H_kv, rows).contiguous()
+        dl = torch.full((w.B,), rows, dtype=torch.int32, device=dev)
+        if args.entry == "heavy_attn":
+            q = synth.randn_bf16((w.B, n, w.H_q, w.d), gen, dev)
+            out = torch.empty_like(q)
+            fn = lambda: mb.magicdec_heavy_attn(q, kc, vc, weight, dl, pos=pos, next_pos=sl, out=out)
+            nbytes = float(w.B) * w.H_kv * rows * (4 * w.d + 8) + 2.0 * q.numel() * 2
+        else:
+            left = torch.empty_like(dl)
+            fn = lambda: mb.magicdec_heavy_evict(kc, vc, weight, pos, dl, sl, budget, n_sink=4, n_recent=budget // 4,
+                                                 draft_len_out=left)
+            nbytes = float(w.B) * w.H_kv * (8 * rows + n * (8 * w.d + 16))
+        info.update(budget=budget, tokens=n)
     elif args.entry == "tree_accept":
         n = args.nodes
         target = torch.randn((w.B, n, w.V), device=dev, generator=synth.gen(dev, w.seed * 13 + 2))
