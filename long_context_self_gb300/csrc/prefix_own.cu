@@ -44,18 +44,19 @@ struct PoShape {
     static constexpr int STAGES = D == 128 ? 3 : 6;
     static constexpr int QHALF = MT * ROWS * 128;
     static constexpr int BYTES = STAGES * STAGE + HV * QHALF;
-    static_assert(4 * MT * ROWS * D * 4 <= STAGES * STAGE, "the warps' O take the ring's place");
+    static constexpr int OROW = D + 8;                  // floats of a row of O: rows lie in other banks
+    static_assert(4 * MT * ROWS * OROW * 4 <= STAGES * STAGE, "the warps' O take the ring's place");
 };
 
 template <int D, int ROWS, int MT>
 __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>::PER_SM)
     prefix_own_kernel(const PreOwn p) {
     using L = PoShape<D, ROWS, MT>;
-    constexpr int NT = L::NT, OPER = L::OPER, STAGE = L::STAGE, NST = L::STAGES, QHALF = L::QHALF;
+    constexpr int NT = L::NT, OPER = L::OPER, STAGE = L::STAGE, NST = L::STAGES, QHALF = L::QHALF, OROW = L::OROW;
     constexpr int KS = D / 16, NB = D / 8, HR = ROWS / 8, VR = D / 8;   // VR: 16-byte words of a row
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *ring = smem, *qs = smem + NST * STAGE;
-    __shared__ long long rows_at[2][kPoKeys];           // of a tile's keys: element of the pool, or -1
+    __shared__ long long rows_at[8][kPoKeys];           // of a tile's keys: element of the pool, or -1
     __shared__ int par[32];
     __shared__ uint32_t sees[32];                       // of a node's slots: itself and its ancestors
     __shared__ float2 wstat[L::WARPS][16];              // of a warp's rows: (max, sum)
@@ -67,40 +68,39 @@ __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>
     const uint32_t rank = few_rank(), C = few_ctas();
     const float sl = p.scale_log2;
     pdl_trigger();
+    // Loads that wait for no others go out together: the query rows (row i * G + g: node i, head g of the
+    // group), the parents, the lengths; then the pages of the first tiles, all at once.
+    constexpr int QV = (MT * ROWS * VR + NT - 1) / NT;  // 16-byte words of the query rows a thread has
+    uint4 qv[QV];
+#pragma unroll
+    for (int x = 0; x < QV; ++x) {
+        const int r = (x * NT + tid) / VR, c = (x * NT + tid) % VR, i = r / G;
+        const uint16_t *src = p.q + (((long long)b * n + i) * p.H_q + h * G + (r - i * G)) * D + c * 8;
+        qv[x] = r < R ? ld_dep_u4(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
+    }
+    const int parent = p.parent && tid < n ? ld_dep(p.parent + (long long)b * n + tid) : tid - 1;
     const int cap = p.page_size * p.max_pages;
-    const int len = pre_clamp(checked(ld_dep(p.len + b), 0, cap, p.err), cap);
-    const int nodes = p.n_nodes ? pre_clamp(checked(ld_dep(p.n_nodes + b), 0, n, p.err), n) : n;
+    const int len_in = ld_dep(p.len + b), nodes_in = p.n_nodes ? ld_dep(p.n_nodes + b) : n;
+    const int len = pre_clamp(checked(len_in, 0, cap, p.err), cap), nodes = pre_clamp(checked(nodes_in, 0, n, p.err), n);
     const int total = nodes ? (nodes > cap - len ? cap : len + nodes) : 0;
     // This CTA's keys: [k0, k1), in groups of 16.
     const int per = ((total + (int)C - 1) / (int)C + 15) & ~15;
     const int k0 = min(total, (int)rank * per), k1 = min(total, k0 + per), tiles = (k1 - k0 + kPoKeys - 1) / kPoKeys;
-    // The query rows (row i * G + g: node i, head g of the group), swizzled as the keys.
-    for (int x = tid; x < MT * ROWS * VR; x += NT) {
-        const int r = x / VR, c = x % VR, i = r / G;
-        const uint16_t *src = p.q + (((long long)b * n + i) * p.H_q + h * G + (r - i * G)) * D + c * 8;
-        *reinterpret_cast<uint4 *>(qs + (c >> 3) * QHALF + swz128(r, c & 7)) =
-            r < R ? ld_dep_u4(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
-    }
-    if (p.parent && tid < n)
-        par[tid] = checked(ld_dep(p.parent + (long long)b * n + tid), INT_MIN, tid - 1, p.err);
-    // Where a tile's keys lie; one outside the pool is zeros.  The page is asked for before a tile's
-    // products and its number used behind them.
+    // Where a key lies; one outside the pool is zeros.  A page is asked for before a tile's products and
+    // its number used behind them.
     const int32_t *table = p.table + (long long)b * p.max_pages;
-    int page = -1;
-    auto ask = [&](int t) {
-        const int key = k0 + t * kPoKeys + tid;
-        if (tid < kPoKeys && key < k1) page = ld_dep(table + key / p.page_size);
+    auto ask = [&](int t, int at) {
+        const int key = k0 + t * kPoKeys + at;
+        return key < k1 ? ld_dep(table + key / p.page_size) : -1;
     };
-    auto look_up = [&](int t) {
-        if (tid < kPoKeys) {
-            const int key = k0 + t * kPoKeys + tid;
-            long long at = -1;
-            if (key < k1) {
-                if (page < 0 || page >= p.n_pages) raise_error(p.err, kErrPage);
-                else at = (((long long)page * p.page_size + key % p.page_size) * p.pre.H_kv + h) * D;
-            }
-            rows_at[t & 1][tid] = at;
+    auto look_up = [&](int t, int at, int page) {
+        const int key = k0 + t * kPoKeys + at;
+        long long row = -1;
+        if (key < k1) {
+            if (page < 0 || page >= p.n_pages) raise_error(p.err, kErrPage);
+            else row = (((long long)page * p.page_size + key % p.page_size) * p.pre.H_kv + h) * D;
         }
+        rows_at[t & 7][at] = row;
     };
     auto load = [&](int t) {
         if (t < tiles) {
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>
 #pragma unroll
             for (int x = 0; x < kPoKeys * VR; x += NT) {
                 const int r = (x + tid) / VR, c = (x + tid) % VR;
-                const long long at = rows_at[t & 1][r];
+                const long long at = rows_at[t & 7][r];
                 const long long from = (at < 0 ? 0 : at) + c * 8;
                 const uint32_t dst = to + (uint32_t)(c >> 3) * kPoHalf + swz128(r, c & 7);
                 copy16(dst, p.k + from, at >= 0);
@@ -117,25 +117,31 @@ __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    ask(0);
-    look_up(0);
+    constexpr int FIRST = (NST * kPoKeys + NT - 1) / NT;
+    int pages[FIRST];
+#pragma unroll
+    for (int x = 0; x < FIRST; ++x) pages[x] = ask((x * NT + tid) / kPoKeys, (x * NT + tid) % kPoKeys);
+#pragma unroll
+    for (int x = 0; x < QV; ++x) {
+        const int r = (x * NT + tid) / VR, c = (x * NT + tid) % VR;
+        if (r < MT * ROWS) *reinterpret_cast<uint4 *>(qs + (c >> 3) * QHALF + swz128(r, c & 7)) = qv[x];
+    }
+    if (tid < n) par[tid] = checked(parent, INT_MIN, tid - 1, p.err);
+#pragma unroll
+    for (int x = 0; x < FIRST; ++x) look_up((x * NT + tid) / kPoKeys, (x * NT + tid) % kPoKeys, pages[x]);
     __syncthreads();
+#pragma unroll 1
+    for (int t = 0; t + 1 < NST; ++t) load(t);
     if (tid < n) {
         uint32_t m = 0;
         for (int a = tid; a >= 0;) {
             m |= 1u << a;
-            const int q = p.parent ? par[a] : a - 1;
+            const int q = par[a];
             a = q < a ? q : -1;
         }
         sees[tid] = m;
     }
-#pragma unroll 1
-    for (int t = 0; t + 1 < NST; ++t) {
-        ask(t + 1);
-        load(t);
-        look_up(t + 1);
-        __syncthreads();
-    }
+    __syncthreads();
 
     const int mt = MT == 1 ? 0 : warp % MT, kw = warp / MT;
     uint32_t qf[HR == 1 ? KS : 1][2 * HR];
@@ -167,12 +173,12 @@ __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>
     for (int t = 0; t < tiles; ++t) {
         copies_wait<NST - 2>();
         __syncthreads();                                // tile t is there, and all are done with tile t - 1
-        ask(t + NST);
+        const int page = tid < kPoKeys ? ask(t + NST, tid) : -1;
         load(t + NST - 1);
         const uint32_t kt = smem_u32(ring + t % NST * STAGE), vt = kt + OPER;
         const int g = k0 + t * kPoKeys + r0;
         if (g >= k1) {                                  // nothing for this warp
-            look_up(t + NST);
+            if (tid < kPoKeys) look_up(t + NST, tid, page);
             continue;
         }
         // Two chains of products a score, so that half as many wait for one another.
@@ -288,7 +294,7 @@ __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>
             few_mma<HR>(o[j], a, f0, f1);
             few_mma<HR>(o[j + 1], a, f2, f3);
         }
-        look_up(t + NST);
+        if (tid < kPoKeys) look_up(t + NST, tid, page);
     }
     // The warps' maxima and sums, and the CTA's.
 #pragma unroll
@@ -309,30 +315,29 @@ __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>
         const float mx = fmaxf(s.x, x.x), mu = mx == -INFINITY ? 0.f : mx;
         s = make_float2(mx, s.y * fast_exp2(s.x - mu) + x.y * fast_exp2(x.x - mu));
     };
-    if (tid < R) {
+    auto of_cta = [&](int r) {
         float2 s = make_float2(-INFINITY, 0.f);
-        for (int w = 0; w < L::WARPS / MT; ++w) join(s, wstat[w * MT + tid / 16][tid % 16]);
-        cstat[tid] = s;
-    }
-    __syncthreads();
+#pragma unroll
+        for (int w = 0; w < L::WARPS / MT; ++w) join(s, wstat[w * MT + r / 16][r % 16]);
+        return s;
+    };
+    if (tid < R) cstat[tid] = of_cta(tid);
     // The warps' O, at the CTA's maximum.
-    float *osum = reinterpret_cast<float *>(ring);      // [WARPS / MT][R][D]
+    float *osum = reinterpret_cast<float *>(ring);      // [WARPS / MT][R][OROW]
 #pragma unroll
     for (int e = 0; e < HR; ++e) {
         const int r = mt * 16 + lr + 8 * e;
         if (r >= R) continue;
-        const float f = m[e] == -INFINITY ? 0.f : fast_exp2(m[e] - cstat[r].x);
-        float *to = osum + (kw * R + r) * D + 2 * lq;
+        const float f = m[e] == -INFINITY ? 0.f : fast_exp2(m[e] - of_cta(r).x);
+        float *to = osum + (kw * R + r) * OROW + 2 * lq;
 #pragma unroll
         for (int j = 0; j < NB; ++j)
             *reinterpret_cast<float2 *>(to + j * 8) = make_float2(o[j][2 * e] * f, o[j][2 * e + 1] * f);
     }
-    if (C > 1) few_cluster_sync();
-    else __syncthreads();
-    // The CTAs' O with the prefix's parts: 4 channels c4 of ITEMS rows a thread at most, whose loads go
-    // side by side; the CTAs take the rows in turn.
+    // The prefix's parts, 4 channels c4 of ITEMS rows a thread at most, whose loads go side by side, then
+    // the CTAs' O; the CTAs take the rows in turn.
     constexpr int ITEMS = MT * ROWS * (D / 4) / NT, STEP = NT / (D / 4);
-    const int c4 = tid % (D / 4), vecs = R * (D / 4);
+    const int c4 = tid % (D / 4);
     int row[ITEMS];
     RowParts parts[ITEMS];
     float4 acc[ITEMS];
@@ -373,21 +378,34 @@ __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>
 #pragma unroll
             for (int x = 0; x < ITEMS; ++x) add(x, make_float2(e[k][x].x * sl, e[k][x].y), y[k][x]);
     }
+    if (C > 1) few_cluster_sync();
+    else __syncthreads();
 #pragma unroll
     for (int x = 0; x < ITEMS; ++x) {
         if (row[x] >= R) continue;
         const int r = row[x], t = r / G;
-        if (t < nodes)
-            for (uint32_t c = 0; c < C; ++c) {
-                const uint32_t base = few_at(osum, c) + (uint32_t)(r * (D / 4) + c4) * 16;
+        if (t < nodes) {
+            if (C == 1) {
                 float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int w = 0; w < L::WARPS / MT; ++w) {
-                    const float4 y = few_ld4(base + (uint32_t)(w * vecs) * 16);
+                    const float4 y = *reinterpret_cast<const float4 *>(osum + (w * R + r) * OROW + c4 * 4);
                     sum = make_float4(sum.x + y.x, sum.y + y.y, sum.z + y.z, sum.w + y.w);
                 }
-                add(x, few_ld2(few_at(&cstat[r], c)), sum);
+                add(x, cstat[r], sum);
+            } else {
+                for (uint32_t c = 0; c < C; ++c) {
+                    const uint32_t base = few_at(osum, c) + (uint32_t)(r * OROW + c4 * 4) * 4;
+                    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int w = 0; w < L::WARPS / MT; ++w) {
+                        const float4 y = few_ld4(base + (uint32_t)(w * R * OROW) * 4);
+                        sum = make_float4(sum.x + y.x, sum.y + y.y, sum.z + y.z, sum.w + y.w);
+                    }
+                    add(x, few_ld2(few_at(&cstat[r], c)), sum);
+                }
             }
+        }
         const float inv = st[x].y > 0.f ? 1.f / st[x].y : 0.f;
         *reinterpret_cast<uint2 *>(p.out + (((long long)b * n + t) * p.H_q + h * G + (r - t * G)) * D + c4 * 4) =
             make_uint2(pack_bf16(acc[x].x * inv, acc[x].y * inv), pack_bf16(acc[x].z * inv, acc[x].w * inv));
