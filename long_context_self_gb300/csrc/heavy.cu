@@ -40,6 +40,7 @@ __global__ void __launch_bounds__(kHvThreads, 2)
                       const HeavyParams p) {
     constexpr int KS = D / 16, HV = D / 64, NB = D / 8;
     constexpr int OPER = HV * kHvHalf, STAGE = 2 * OPER;
+    constexpr int OROW = D + 8;                         // floats of a row of O: rows lie in other banks
     constexpr int QHALF = kHvRows * 128;                // bytes of 64 channels of the query rows
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *ring = smem;                               // later the warps' O
@@ -66,14 +67,13 @@ __global__ void __launch_bounds__(kHvThreads, 2)
     pdl_trigger();
     pdl_wait();
     // The query rows (row i * G + g: token i, head g of the group), swizzled as the keys.
-    for (int x = tid; x < kHvRows * (D / 8); x += kHvThreads) {
-        const int r = x / (D / 8), c = x % (D / 8), i = r / p.G;
-        const uint16_t *src = p.q + (((long long)b * p.n + i) * p.H_q + h * p.G + (r - i * p.G)) * D + c * 8;
-        *reinterpret_cast<uint4 *>(qs + (c >> 3) * QHALF + swz128(r, c & 7)) =
-            r < p.R ? ld_dep_u4(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
-    }
-    __syncthreads();
+    static_assert(kHvRows * (D / 8) <= kHvThreads, "a thread has a 16-byte word of the query rows");
+    const int qr = tid / (D / 8), qc = tid % (D / 8), qi = qr / p.G;
+    const uint16_t *qsrc = p.q + (((long long)b * p.n + qi) * p.H_q + h * p.G + (qr - qi * p.G)) * D + qc * 8;
+    const uint4 qv = qr < p.R ? ld_dep_u4(reinterpret_cast<const uint4 *>(qsrc)) : make_uint4(0, 0, 0, 0);
     const int len0 = checked(ld_dep(p.len + b), 0, p.cap, p.err);
+    if (qr < kHvRows) *reinterpret_cast<uint4 *>(qs + (qc >> 3) * QHALF + swz128(qr, qc & 7)) = qv;
+    __syncthreads();
     const int len = len0 < 0 ? 0 : (len0 > p.cap ? p.cap : len0);
     // This CTA's keys: [k0, k1), in groups of 16.
     const int per = ((len + (int)C - 1) / (int)C + 15) & ~15;
@@ -269,10 +269,10 @@ __global__ void __launch_bounds__(kHvThreads, 2)
         if (j >= first_new) p.pos[row0 + j] = ld_dep(p.next_pos + b) + (j - first_new);
     }
     // O of the warps, in the softmax's own scale.
-    float *osum = reinterpret_cast<float *>(ring);      // [kHvWarps][R][D]
+    float *osum = reinterpret_cast<float *>(ring);      // [kHvWarps][R][OROW]
     if (warp < kHvWarps && lr < p.R) {
         const float f = m == -INFINITY ? 0.f : fast_exp2(m - all[lr].x) * all[lr].y;
-        float *to = osum + (warp * p.R + lr) * D + 2 * lq;
+        float *to = osum + (warp * p.R + lr) * OROW + 2 * lq;
 #pragma unroll
         for (int j = 0; j < NB; ++j) *reinterpret_cast<float2 *>(to + j * 8) = make_float2(o[j][0] * f, o[j][1] * f);
     }
@@ -281,16 +281,20 @@ __global__ void __launch_bounds__(kHvThreads, 2)
     else __syncthreads();
     const int vecs = p.R * (D / 4), share = (vecs + (int)C - 1) / (int)C;
     for (int i = (int)rank * share + tid; i < min(vecs, (int)(rank + 1) * share); i += kHvThreads) {
+        const int r = i / (D / 4), c4 = i - r * (D / 4), t = r / p.G, at = r * OROW + c4 * 4;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         for (uint32_t c = 0; c < C; ++c) {
-            const uint32_t base = few_at(osum, c);
+            const uint32_t base = few_at(osum + at, c);
 #pragma unroll
             for (int w = 0; w < kHvWarps; ++w) {
-                const float4 x = few_ld4(base + (uint32_t)(w * vecs + i) * 16);
-                s = make_float4(s.x + x.x, s.y + x.y, s.z + x.z, s.w + x.w);
+                const float4 x = C == 1 ? *reinterpret_cast<const float4 *>(osum + w * p.R * OROW + at)
+                                        : few_ld4(base + (uint32_t)(w * p.R * OROW) * 4);
+                s.x += x.x;
+                s.y += x.y;
+                s.z += x.z;
+                s.w += x.w;
             }
         }
-        const int r = i / (D / 4), c4 = i - r * (D / 4), t = r / p.G;
         *reinterpret_cast<uint2 *>(p.out + (((long long)b * p.n + t) * p.H_q + h * p.G + (r - t * p.G)) * D + c4 * 4) =
             make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
     }
@@ -376,7 +380,7 @@ magicdec_status launch_heavy_attn(int B, int H_q, int H_kv, int D, int cap, int 
     p.stages = (magicdec_host::max_smem_optin() / 2 - kHvStatic - scores) / stage;
     if (p.stages > kHvStages) p.stages = kHvStages;
     if (p.stages > tiles) p.stages = tiles;
-    static_assert(kHvWarps * kHvRows * 64 * 4 <= 2 * kHvHalf, "a stage has room for the warps' O");
+    static_assert(kHvWarps * kHvRows * (64 + 8) * 4 <= 2 * kHvHalf, "a stage has room for the warps' O");
     // (channels, rows, heads, sequences), boxes of 64 channels of a stage's rows, and of 16 for its end.
     CUtensorMap tm[4];
     const uint64_t dims[4] = {(uint64_t)D, (uint64_t)cap, (uint64_t)H_kv, (uint64_t)B};
