@@ -260,13 +260,25 @@ __global__ void __launch_bounds__(kHvThreads, 2)
     __syncthreads();
     // Every row's weight, summed over the query rows in their order.
     const int first_new = p.next_pos ? len - p.n : INT_MAX;
-    for (int j = k0 + tid; j < k1; j += kHvThreads) {
-        const float old = p.weight[row0 + j];
-        float sum = 0.f;
-        for (int r = 0; r < p.R; ++r)
-            sum = fmaf(fast_exp2(scores[(long long)r * p.stride + j - k0] - all[r].x), all[r].y, sum);
-        p.weight[row0 + j] = (j >= first_new ? 0.f : old) + sum;
-        if (j >= first_new) p.pos[row0 + j] = ld_dep(p.next_pos + b) + (j - first_new);
+    const int first_pos = p.next_pos ? ld_dep(p.next_pos + b) : 0;
+    constexpr int KEYS = 8;                             // a thread's keys whose old weights are loaded together
+    for (int j0 = k0 + tid; j0 < k1; j0 += KEYS * kHvThreads) {
+        float old[KEYS];
+#pragma unroll
+        for (int x = 0; x < KEYS; ++x) {
+            const int j = j0 + x * kHvThreads;
+            old[x] = j < k1 && j < first_new ? p.weight[row0 + j] : 0.f;
+        }
+#pragma unroll
+        for (int x = 0; x < KEYS; ++x) {
+            const int j = j0 + x * kHvThreads;
+            if (j >= k1) break;
+            float sum = 0.f;
+            for (int r = 0; r < p.R; ++r)
+                sum = fmaf(fast_exp2(scores[(long long)r * p.stride + j - k0] - all[r].x), all[r].y, sum);
+            p.weight[row0 + j] = old[x] + sum;
+            if (j >= first_new) p.pos[row0 + j] = first_pos + (j - first_new);
+        }
     }
     // O of the warps, in the softmax's own scale.
     float *osum = reinterpret_cast<float *>(ring);      // [kHvWarps][R][OROW]
