@@ -98,14 +98,21 @@ __global__ void __launch_bounds__(kHtThreads, 2)
     pdl_trigger();
     pdl_wait();
     // The query rows (row i * G + g: token i, head g of the group), K-major and swizzled.
-    for (int x = tid; x < NR * (D / 8); x += kHtThreads) {
-        const int r = x / (D / 8), c = x % (D / 8), i = r / p.G;
+    constexpr int QV = (NR * (D / 8) + kHtThreads - 1) / kHtThreads;     // 16-byte words a thread has
+    uint4 qv[QV];
+#pragma unroll
+    for (int x = 0; x < QV; ++x) {
+        const int r = (x * kHtThreads + tid) / (D / 8), c = (x * kHtThreads + tid) % (D / 8), i = r / p.G;
         const uint16_t *src = p.q + (((long long)b * p.n + i) * p.H_q + h * p.G + (r - i * p.G)) * D + c * 8;
-        *reinterpret_cast<uint4 *>(qs + (c >> 3) * QHALF + swz128(r, c & 7)) =
-            r < p.R ? ld_dep_u4(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
+        qv[x] = r < p.R ? ld_dep_u4(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
+    }
+    const int len0 = checked(ld_dep(p.len + b), 0, p.cap, p.err);
+#pragma unroll
+    for (int x = 0; x < QV; ++x) {
+        const int r = (x * kHtThreads + tid) / (D / 8), c = (x * kHtThreads + tid) % (D / 8);
+        if (r < NR) *reinterpret_cast<uint4 *>(qs + (c >> 3) * QHALF + swz128(r, c & 7)) = qv[x];
     }
     fence_proxy_async_smem();
-    const int len0 = checked(ld_dep(p.len + b), 0, p.cap, p.err);
     const int len = len0 < 0 ? 0 : (len0 > p.cap ? p.cap : len0);
     // This CTA's keys: [k0, k1), in tiles.
     const int per = ((len + (int)C - 1) / (int)C + kHtKeys - 1) / kHtKeys * kHtKeys;
@@ -343,6 +350,7 @@ __global__ void __launch_bounds__(kHtThreads, 2)
                 s = make_float2(mx, s.y * fast_exp2(s.x - mu) + x.y * fast_exp2(x.x - mu));
             }
             all[row] = row < p.R && s.y > 0.f ? make_float2(s.x, 1.f / s.y) : make_float2(0.f, 0.f);
+            moved[row] = tiles == 0 || held[row] == -INFINITY ? 0.f : fast_exp2(held[row] - all[row].x) * all[row].y;
         }
         named_bar_sync(2, 128);
         // O, in the softmax's own scale, to the probabilities' place: [R][D].
@@ -351,16 +359,18 @@ __global__ void __launch_bounds__(kHtThreads, 2)
         float *osum = reinterpret_cast<float *>(pbuf);
         const int chan = D == 128 ? row : 16 * quad + lane;              // 64 rows lie in the first 16 lanes of every 32
         const bool real = D == 128 || lane < 16;
-#pragma unroll 1
+        const bool odd = met;
+#pragma unroll
         for (int c = 0; c < NR; c += 16) {
             uint32_t o[16];
             tmem_ld16(ts + O_COL + c, o);
+            float f[16];
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4 *>(f + i) = *reinterpret_cast<const float4 *>(moved + c + i);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float m = held[c + i];
-                const float f = tiles == 0 || m == -INFINITY ? 0.f : fast_exp2(m - all[c + i].x) * all[c + i].y;
-                float y = f == 0.f ? 0.f : __uint_as_float(o[i]) * f;
-                if (met && real)
+                float y = f[i] == 0.f ? 0.f : __uint_as_float(o[i]) * f[i];
+                if (odd && real)
                     for (int j = max(own, k0); j < k1; ++j) {
                         const uint32_t z = (uint32_t)p.v[(row0 + j) * D + chan] << 16;
                         if ((z & 0x7f800000u) == 0x7f800000u && c + i >= (j - own) * p.G) y += __uint_as_float(z);
