@@ -23,8 +23,8 @@ namespace magicdec {
 //
 // A producer warp keeps a ring of stages filled by TMA, 64 keys' K and V each; 4 consumer warps take 16
 // keys of a stage each through ldmatrix and mma.sync (m16n8k16, the lower half of A empty): at 8 rows
-// the products are a few percent of the time.  128 sequences over 2053 rows, R = 4: 184 to 190 us,
-// 5.8 to 6.0 TB/s; with keys straight from global memory into the fragments, which left too few bytes
+// the products are a few percent of the time.  128 sequences over 2053 rows, R = 4: 181 to 183 us,
+// 6.0 TB/s; with keys straight from global memory into the fragments, which left too few bytes
 // under way, 207; on tcgen05, with the scores computed again, 246.
 constexpr int kHvKeys = 64;          // keys of a stage
 constexpr int kHvHalf = kHvKeys * 128;   // bytes of 64 channels of them
@@ -416,10 +416,11 @@ magicdec_status launch_heavy_attn(int B, int H_q, int H_kv, int D, int cap, int 
 // Bound: 8 bytes a row (weight, position) from HBM; in practice the chain of loads, searches and
 // moves of a (layer, sequence, KV head), which only others can cover.  So one warp takes it where its
 // keys are few (kEvWarpRows; keys in shared memory, reductions and lists inside the warp, no barrier of
-// a CTA), and 8 warps where they are many.  The border is found by searches over all keys: for few rows
-// the least key not yet taken, again and again, for many the key's bits from the top, each with the
-// count of the keys below (one digit of 8 bits at a time with counts by shared-memory atomics: 87 us
-// for 32 layers of 16 sequences of 1029 rows, see DESIGN for the times since).
+// a CTA), and 8 warps where they are many.  A warp from which few rows go ranks the few keys that lie
+// below a bound; else the border is found by searches over all keys: for few rows the least key not yet
+// taken, again and again, for many the key's bits from the top, each with the count of the keys below.
+// 32 layers of 16 sequences, 8 heads, up to 1029 rows of which 5 go: 15.5 us; by such searches 41, by
+// digits of 8 bits counted with shared-memory atomics, 8 warps each, 87.
 constexpr int kEvThreads = 256;
 constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvWarpRows = 2048;        // rows of a warp's own
@@ -665,9 +666,38 @@ __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictPara
     // What goes first: small weights, large positions, high rows.
     auto place = [&](int j) { return place_of(ld_dep(pos + j)); };
     auto any = [](int) { return true; };
+    // The same over the keys alone, where all are in shared memory: their bits from the top, 4 keys a load,
+    // and no further than to where a count is met.
+    auto border_kept = [&](int &left, uint32_t &at) {
+        at = 0;
+        int n = 0;
+        for (int bit = 31; bit >= 0; --bit) {
+            const uint32_t top = at | (1u << bit);
+            n = 0;
+            for (int j = 4 * tid; j < len; j += 4 * T) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(kept + j);
+                n += (x.x - at < top - at) + (x.y - at < top - at) + (x.z - at < top - at) + (x.w - at < top - at);
+            }
+            n = sum_all(n);
+            if (n == left) {                                 // what lies below `top` goes, and nothing else
+                at = top - 1;
+                return left;
+            }
+            if (n < left) {
+                left -= n;
+                at = top;
+            }
+        }
+        n = 0;
+        for (int j = 4 * tid; j < len; j += 4 * T) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(kept + j);
+            n += (x.x == at) + (x.y == at) + (x.z == at) + (x.w == at);
+        }
+        return sum_all(n);
+    };
     int left = E;
     uint32_t w_at = 0, p_at = 0, r_at = 0;                   // borders: rows at them go, too
-    const bool tied = border(key, any, left, w_at) != left;  // not all rows of that weight go
+    const bool tied = (len <= p.keep ? border_kept(left, w_at) : border(key, any, left, w_at)) != left;   // not all rows of that weight go
     bool twins = false;                                      // nor all of that position among them
     if (tied) {
         auto tie = [&](int j) { return key(j) == w_at; };
@@ -698,7 +728,7 @@ __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictPara
     for (int done = 0, holes = 1; done < holes; done += LIST) {
         holes = 0;
         int late = 0;                                        // found so far, alike in all threads
-        for (int w0 = 0; w0 < nw; w0 += T) {
+        for (int w0 = 0; w0 < nw; w0 += T) {                 // a thread has a word
             const int w = w0 + tid;
             unsigned hole = 0, stay = 0;
             if (w < nw) {
@@ -782,7 +812,8 @@ magicdec_status launch_heavy_evict(int layers, int B, int H_kv, int D, int cap, 
     p.n_recent = n_recent;
     p.wide = cap % 4 == 0 && magicdec_host::aligned16(weight) && magicdec_host::aligned16(pos);
     p.keep = cap < kEvKeep ? (cap + 3) / 4 * 4 : cap <= kEvMaxRows / 2 ? kEvKeep : kEvKeep / 2;
-    return cap <= kEvWarpRows ? launch_evict_t<1>(p, st) : launch_evict_t<kEvWarps>(p, st);
+    // A warp an item where few rows can go, as it moves but one at a time.
+    return cap <= kEvWarpRows && cap - budget <= kEvTake ? launch_evict_t<1>(p, st) : launch_evict_t<kEvWarps>(p, st);
 }
 
 }  // namespace magicdec

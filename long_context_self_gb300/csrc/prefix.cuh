@@ -7,7 +7,8 @@
 namespace magicdec {
 
 // List tiles that an entry counts for, in front of its own, for the way in and out of it: CTAs' runs
-// are equal in list tiles.
+// are equal in list tiles.  Without, 1024 entries of one tile behind 32,000 tiles of prefixes all fell
+// to a few CTAs, and the call took 890 us instead of some 500.
 constexpr int kTrEntry = 2;
 
 // Where an entry of the list of work begins, its tiles and blocks; one more behind the last
