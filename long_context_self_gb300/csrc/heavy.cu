@@ -417,10 +417,10 @@ magicdec_status launch_heavy_attn(int B, int H_q, int H_kv, int D, int cap, int 
 // moves of a (layer, sequence, KV head), which only others can cover.  So one warp takes it where its
 // keys are few (kEvWarpRows; keys in shared memory, reductions and lists inside the warp, no barrier of
 // a CTA), and 8 warps where they are many.  A warp from which few rows go ranks the few keys that lie
-// below a bound; else the border is found by searches over all keys: for few rows the least key not yet
-// taken, again and again, for many the key's bits from the top, each with the count of the keys below.
-// 32 layers of 16 sequences, 8 heads, up to 1029 rows of which 5 go: 15.5 us; by such searches 41, by
-// digits of 8 bits counted with shared-memory atomics, 8 warps each, 87.
+// below a bound; a CTA finds the border digit by digit of 8 bits, with counts of the keys of every
+// digit, until a count is met.  Ties go by positions and rows, which are searched: for few rows the least
+// not yet taken, again and again, for many bit by bit.  32 layers of 16 sequences, 8 heads, up to 1029
+// rows of which 5 go: 15.5 us; a CTA each 87.
 constexpr int kEvThreads = 256;
 constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvWarpRows = 2048;        // rows of a warp's own
@@ -454,6 +454,7 @@ __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictPara
     extern __shared__ __align__(16) uint32_t shared[];
     __shared__ int lists[2 * kEvMoves * kEvWarps];
     __shared__ uint2 xch[2][kEvWarps];
+    __shared__ int hist[kEvThreads], digit[2];
     const int tid = threadIdx.x % T, warp = tid >> 5, lane = tid & 31, sub = threadIdx.x / T;
     const int words = (p.cap + 31) / 32;
     uint32_t *kept = shared + sub * (p.keep + (words + 3) / 4 * 4), *gone = kept + p.keep;
@@ -666,38 +667,50 @@ __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictPara
     // What goes first: small weights, large positions, high rows.
     auto place = [&](int j) { return place_of(ld_dep(pos + j)); };
     auto any = [](int) { return true; };
-    // The same over the keys alone, where all are in shared memory: their bits from the top, 4 keys a load,
-    // and no further than to where a count is met.
+    // The same over the keys alone, where a CTA has all of them in shared memory: 8 bits at a time from the
+    // top, with counts of every digit's keys, and no further than to where a count is met.
     auto border_kept = [&](int &left, uint32_t &at) {
         at = 0;
-        int n = 0;
-        for (int bit = 31; bit >= 0; --bit) {
-            const uint32_t top = at | (1u << bit);
-            n = 0;
+        for (int shift = 24;; shift -= 8) {
+            hist[tid] = 0;
+            sync();
+            const uint32_t settled = shift == 24 ? 0u : ~0u << (shift + 8);
             for (int j = 4 * tid; j < len; j += 4 * T) {
                 const uint4 x = *reinterpret_cast<const uint4 *>(kept + j);
-                n += (x.x - at < top - at) + (x.y - at < top - at) + (x.z - at < top - at) + (x.w - at < top - at);
+                const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (j + k < len && ((y[k] ^ at) & settled) == 0) atomicAdd(&hist[y[k] >> shift & 255], 1);
             }
-            n = sum_all(n);
-            if (n == left) {                                 // what lies below `top` goes, and nothing else
-                at = top - 1;
-                return left;
+            sync();
+            const int c = hist[tid];
+            int incl = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += x;
             }
-            if (n < left) {
-                left -= n;
-                at = top;
+            if (lane == 31) xch[turn][warp].x = (uint32_t)incl;
+            sync();
+            for (int w = 0; w < warp; ++w) incl += (int)xch[turn][w].x;
+            turn ^= 1;
+            if (incl >= left && incl - c < left) {
+                digit[0] = tid;
+                digit[1] = incl - c;
             }
+            sync();
+            at |= (uint32_t)digit[0] << shift;
+            left -= digit[1];
+            const int alike = hist[digit[0]];
+            sync();                                          // before the counts are cleared
+            if (alike == left) at |= (1u << shift) - 1u;     // all that agree so far go
+            if (alike == left || shift == 0) return alike;
         }
-        n = 0;
-        for (int j = 4 * tid; j < len; j += 4 * T) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(kept + j);
-            n += (x.x == at) + (x.y == at) + (x.z == at) + (x.w == at);
-        }
-        return sum_all(n);
     };
     int left = E;
     uint32_t w_at = 0, p_at = 0, r_at = 0;                   // borders: rows at them go, too
-    const bool tied = (len <= p.keep ? border_kept(left, w_at) : border(key, any, left, w_at)) != left;   // not all rows of that weight go
+    // Whether not all rows of that weight go.
+    const bool tied = (NW > 1 && len <= p.keep ? border_kept(left, w_at) : border(key, any, left, w_at)) != left;
     bool twins = false;                                      // nor all of that position among them
     if (tied) {
         auto tie = [&](int j) { return key(j) == w_at; };
