@@ -418,8 +418,7 @@ magicdec_status launch_heavy_attn(int B, int H_q, int H_kv, int D, int cap, int 
 // keys are few (kEvWarpRows; keys in shared memory, reductions and lists inside the warp, no barrier of
 // a CTA), and 8 warps where they are many.  A warp from which few rows go ranks the few keys that lie
 // below a bound; a CTA finds the border digit by digit of 8 bits, with counts of the keys of every
-// digit, until a count is met.  Ties go by positions and rows, which are searched: for few rows the least
-// not yet taken, again and again, for many bit by bit.  32 layers of 16 sequences, 8 heads, up to 1029
+// digit, until a count is met.  Positions of ties take the keys' place and are searched likewise.  32 layers of 16 sequences, 8 heads, up to 1029
 // rows of which 5 go: 15.5 us; a CTA each 87.
 constexpr int kEvThreads = 256;
 constexpr int kEvWarps = kEvThreads / 32;
@@ -457,7 +456,9 @@ __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictPara
     __shared__ int hist[kEvThreads], digit[2];
     const int tid = threadIdx.x % T, warp = tid >> 5, lane = tid & 31, sub = threadIdx.x / T;
     const int words = (p.cap + 31) / 32;
-    uint32_t *kept = shared + sub * (p.keep + (words + 3) / 4 * 4), *gone = kept + p.keep;
+    const int words4 = (words + 3) / 4 * 4;
+    // Keys, a bit a row that goes, and, of rows whose keys are here, one a row that is alike.
+    uint32_t *kept = shared + sub * (p.keep + words4 + (p.keep + 127) / 128 * 4), *gone = kept + p.keep, *ties = gone + words4;
     int *src = lists + sub * 2 * LIST, *dst = src + LIST;
     pdl_trigger();
     pdl_wait();
@@ -592,7 +593,7 @@ __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictPara
         }
     }
 
-    // Sums, and least values with the sum of their counts, over the item's threads.
+    // Sums over the item's threads.
     int turn = 0;                                            // of the two buffers, which take turns
     auto sum_all = [&](int x) {
         x = __reduce_add_sync(0xffffffffu, x);
@@ -605,46 +606,10 @@ __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictPara
         }
         return x;
     };
-    auto least_all = [&](uint32_t x, int n) {
-        uint2 r;
-        r.x = __reduce_min_sync(0xffffffffu, x);
-        r.y = __reduce_add_sync(0xffffffffu, x == r.x ? n : 0);
-        if (NW > 1) {
-            if (lane == 0) xch[turn][warp] = r;
-            sync();
-            r = xch[turn][0];
-            for (int w = 1; w < NW; ++w) {
-                const uint2 o = xch[turn][w];
-                if (o.x < r.x) r = o;
-                else if (o.x == r.x) r.y += o.y;
-            }
-            turn ^= 1;
-        }
-        return r;
-    };
     // The value at which the count of `part` over the rows for which `in` holds reaches `left`, which
-    // becomes what is still to be taken of the rows of that value; returns how many those are.
+    // becomes what is still to be taken of the rows of that value; returns how many those are.  Bit by bit,
+    // for rows whose keys do not fit shared memory.
     auto border = [&](auto part, auto in, int &left, uint32_t &at) {
-        if (left <= kEvTake) {
-            for (bool begun = false;; begun = true) {
-                uint32_t low = 0xffffffffu;
-                int n = 0;
-                for (int j = tid; j < len; j += T) {
-                    if (!in(j)) continue;
-                    const uint32_t x = part(j);
-                    if (begun && x <= at) continue;
-                    if (x < low) {
-                        low = x;
-                        n = 0;
-                    }
-                    n += x == low;
-                }
-                const uint2 r = least_all(low, n);
-                at = r.x;
-                if ((int)r.y >= left) return (int)r.y;
-                left -= (int)r.y;
-            }
-        }
         at = 0;
         for (int bit = 31; bit >= 0; --bit) {
             const uint32_t top = at | (1u << bit);           // rows below it, of those that are not below `at`
@@ -664,79 +629,181 @@ __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictPara
         for (int j = tid; j < len; j += T) n += in(j) && part(j) == at;
         return sum_all(n);
     };
-    // What goes first: small weights, large positions, high rows.
-    auto place = [&](int j) { return place_of(ld_dep(pos + j)); };
-    auto any = [](int) { return true; };
-    // The same over the keys alone, where a CTA has all of them in shared memory: 8 bits at a time from the
-    // top, with counts of every digit's keys, and no further than to where a count is met.
-    auto border_kept = [&](int &left, uint32_t &at) {
-        at = 0;
-        for (int shift = 24;; shift -= 8) {
-            hist[tid] = 0;
-            sync();
-            const uint32_t settled = shift == 24 ? 0u : ~0u << (shift + 8);
-            for (int j = 4 * tid; j < len; j += 4 * T) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(kept + j);
-                const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+    // The same over what shared memory holds of the rows, or of those with a bit in `mask`, 4 rows a load.
+    // A warp, which takes few: the least, the next, and so on.  A CTA: 8 bits at a time from the top, with
+    // counts of every digit's rows, and no further than to where a count is met.
+    auto border_kept = [&](const uint32_t *mask, int &left, uint32_t &at) {
+        auto real = [&](int j) {                             // which of rows j .. j + 3 there are
+            const uint32_t m = j + 3 < len ? 15u : (1u << (len - j)) - 1u;
+            return mask ? m & mask[j >> 5] >> (j & 31) : m;
+        };
+        if constexpr (NW == 1) {
+            bool begun = false;
+            for (;; begun = true) {
+                uint32_t next = ~0u;
+                int n = 0;
+                for (int j = 4 * tid; j < len; j += 4 * T) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(kept + j);
+                    const uint32_t y[4] = {x.x, x.y, x.z, x.w}, m = real(j);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (j + k < len && ((y[k] ^ at) & settled) == 0) atomicAdd(&hist[y[k] >> shift & 255], 1);
+                    for (int k = 0; k < 4; ++k)
+                        if (m >> k & 1u) {
+                            n += begun && y[k] == at;
+                            if (!begun || y[k] > at) next = min(next, y[k]);
+                        }
+                }
+                n = sum_all(n);
+                if (begun && n >= left) return n;
+                left -= n;
+                at = __reduce_min_sync(0xffffffffu, next);
             }
-            sync();
-            const int c = hist[tid];
-            int incl = c;
+        } else {
+            at = 0;
+            for (int shift = 24;; shift -= 8) {
+                hist[tid] = 0;
+                sync();
+                const uint32_t settled = shift == 24 ? 0u : ~0u << (shift + 8);
+                for (int j = 4 * tid; j < len; j += 4 * T) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(kept + j);
+                    const uint32_t y[4] = {x.x, x.y, x.z, x.w}, m = real(j);
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += x;
+                    for (int k = 0; k < 4; ++k)
+                        if ((m >> k & 1u) && ((y[k] ^ at) & settled) == 0) atomicAdd(&hist[y[k] >> shift & 255], 1);
+                }
+                sync();
+                const int c = hist[tid];
+                int incl = c;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int x = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += x;
+                }
+                if (lane == 31) xch[turn][warp].x = (uint32_t)incl;
+                sync();
+                for (int w = 0; w < warp; ++w) incl += (int)xch[turn][w].x;
+                turn ^= 1;
+                if (incl >= left && incl - c < left) {
+                    digit[0] = tid;
+                    digit[1] = incl - c;
+                }
+                sync();
+                at |= (uint32_t)digit[0] << shift;
+                left -= digit[1];
+                const int alike = hist[digit[0]];
+                sync();                                      // before the counts are cleared
+                if (alike == left) at |= (1u << shift) - 1u; // all that agree so far go
+                if (alike == left || shift == 0) return alike;
             }
-            if (lane == 31) xch[turn][warp].x = (uint32_t)incl;
-            sync();
-            for (int w = 0; w < warp; ++w) incl += (int)xch[turn][w].x;
-            turn ^= 1;
-            if (incl >= left && incl - c < left) {
-                digit[0] = tid;
-                digit[1] = incl - c;
-            }
-            sync();
-            at |= (uint32_t)digit[0] << shift;
-            left -= digit[1];
-            const int alike = hist[digit[0]];
-            sync();                                          // before the counts are cleared
-            if (alike == left) at |= (1u << shift) - 1u;     // all that agree so far go
-            if (alike == left || shift == 0) return alike;
         }
     };
-    int left = E;
-    uint32_t w_at = 0, p_at = 0, r_at = 0;                   // borders: rows at them go, too
-    // Whether not all rows of that weight go.
-    const bool tied = (NW > 1 && len <= p.keep ? border_kept(left, w_at) : border(key, any, left, w_at)) != left;
-    bool twins = false;                                      // nor all of that position among them
-    if (tied) {
-        auto tie = [&](int j) { return key(j) == w_at; };
-        twins = border(place, tie, left, p_at) != left;
-        if (twins) {
-            auto twin = [&](int j) { return key(j) == w_at && place(j) == p_at; };
-            border([](int j) { return ~(uint32_t)j; }, twin, left, r_at);
-        }
-    }
-    // One bit a row, so that weights and positions may move afterwards.
+    // What goes first: small weights, large positions, high rows.  One bit a row, so that weights and
+    // positions may move afterwards.
     const int nw = (len + 31) / 32;
-    for (int w = warp; w < nw; w += NW) {
-        const int j = w * 32 + lane;
-        bool go = false;
-        if (j < len) {
-            const uint32_t x = key(j);
-            go = x < w_at;
-            if (x == w_at) {
-                const uint32_t y = tied ? place(j) : 0;
-                go = y < p_at || (y == p_at && (!twins || ~(uint32_t)j <= r_at));
+    int left = E;
+    uint32_t w_at = 0, p_at = 0;                             // borders: rows at them go, too, if all do
+    if (len <= p.keep) {
+        const bool tied = border_kept(nullptr, left, w_at) != left;
+        for (int w = warp; w < nw; w += NW) {
+            const int j = w * 32 + lane;
+            const uint32_t x = j < len ? kept[j] : ~0u;
+            const unsigned m = __ballot_sync(0xffffffffu, j < len && (x < w_at || (!tied && x == w_at)));
+            const unsigned t = __ballot_sync(0xffffffffu, j < len && tied && x == w_at);
+            if (lane == 0) {
+                gone[w] = m;
+                ties[w] = t;
             }
         }
-        const unsigned m = __ballot_sync(0xffffffffu, go);
-        if (lane == 0) gone[w] = m;
+        sync();
+        if (tied) {
+            // Positions take the keys' place.
+            for (int j0 = 4 * tid; j0 < len; j0 += 16 * T) {
+                uint4 at[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int j = j0 + k * 4 * T;
+                    if (j + 3 < len && p.wide) at[k] = ld_dep_u4(reinterpret_cast<const uint4 *>(pos + j));
+                    else if (j < len)
+                        at[k] = make_uint4(ld_dep(pos + j), j + 1 < len ? ld_dep(pos + j + 1) : 0,
+                                           j + 2 < len ? ld_dep(pos + j + 2) : 0, j + 3 < len ? ld_dep(pos + j + 3) : 0);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (j0 + k * 4 * T < len)
+                        *reinterpret_cast<uint4 *>(kept + j0 + k * 4 * T) =
+                            make_uint4(place_of(at[k].x), place_of(at[k].y), place_of(at[k].z), place_of(at[k].w));
+            }
+            sync();
+            const int alike = border_kept(ties, left, p_at);
+            const bool twins = alike != left;
+            for (int w = warp; w < nw; w += NW) {
+                const int j = w * 32 + lane;
+                const bool tie = ties[w] >> lane & 1u;
+                const uint32_t x = tie ? kept[j] : 0;
+                const unsigned m = __ballot_sync(0xffffffffu, tie && (x < p_at || (!twins && x == p_at)));
+                const unsigned t = __ballot_sync(0xffffffffu, tie && twins && x == p_at);
+                __syncwarp();
+                if (lane == 0) {
+                    gone[w] |= m;
+                    ties[w] = t;
+                }
+            }
+            sync();
+            // Of rows alike in both the last `left` go.
+            int before = 0;                                  // in the words so far, alike in all threads
+            for (int w0 = 0; twins && w0 < nw; w0 += T) {
+                const int w = w0 + tid;
+                const unsigned t = w < nw ? ties[w] : 0;
+                int incl = __popc(t);
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int x = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += x;
+                }
+                int at = before + incl - __popc(t);
+                if (NW == 1) {
+                    before += __shfl_sync(0xffffffffu, incl, 31);
+                } else {
+                    if (lane == 31) xch[turn][warp].x = (uint32_t)incl;
+                    sync();
+                    for (int x = 0; x < NW; ++x) {
+                        if (x < warp) at += (int)xch[turn][x].x;
+                        before += (int)xch[turn][x].x;
+                    }
+                    turn ^= 1;
+                }
+                unsigned go = t;
+                for (; at < alike - left && go; ++at) go &= go - 1;      // the first ones stay
+                if (go) gone[w] |= go;
+            }
+            sync();
+        }
+    } else {
+        auto place = [&](int j) { return place_of(ld_dep(pos + j)); };
+        const bool tied = border(key, [](int) { return true; }, left, w_at) != left;
+        bool twins = false;
+        uint32_t r_at = 0;
+        if (tied) {
+            twins = border(place, [&](int j) { return key(j) == w_at; }, left, p_at) != left;
+            if (twins)
+                border([](int j) { return ~(uint32_t)j; }, [&](int j) { return key(j) == w_at && place(j) == p_at; }, left,
+                       r_at);
+        }
+        for (int w = warp; w < nw; w += NW) {
+            const int j = w * 32 + lane;
+            bool go = false;
+            if (j < len) {
+                const uint32_t x = key(j);
+                go = x < w_at;
+                if (x == w_at) {
+                    const uint32_t y = tied ? place(j) : 0;
+                    go = y < p_at || (y == p_at && (!twins || ~(uint32_t)j <= r_at));
+                }
+            }
+            const unsigned m = __ballot_sync(0xffffffffu, go);
+            if (lane == 0) gone[w] = m;
+        }
+        sync();
     }
-    sync();
     // Holes below the budget and the rows to fill them, listed LIST at a time.
     for (int done = 0, holes = 1; done < holes; done += LIST) {
         holes = 0;
@@ -796,7 +863,7 @@ constexpr int kEvMaxRows = 1 << 20;
 
 template <int NW>
 static magicdec_status launch_evict_t(EvictParams &p, cudaStream_t st) {
-    const int sets = kEvWarps / NW, smem = sets * (p.keep + (p.cap + 127) / 128 * 4) * 4;      // at most 192 KB
+    const int sets = kEvWarps / NW, smem = sets * (p.keep + ((p.cap + 127) / 128 + (p.keep + 127) / 128) * 4) * 4;
     if (!magicdec_host::allow_smem_once<heavy_evict_kernel<NW>>(200 * 1024)) return MAGICDEC_ERR_CUDA;
     return magicdec_host::launch_pdl(heavy_evict_kernel<NW>, dim3((unsigned)((p.items + sets - 1) / sets)),
                                      dim3(kEvThreads), (size_t)smem, st, p);
