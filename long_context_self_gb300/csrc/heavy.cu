@@ -418,8 +418,8 @@ magicdec_status launch_heavy_attn(int B, int H_q, int H_kv, int D, int cap, int 
 // keys are few (kEvWarpRows; keys in shared memory, reductions and lists inside the warp, no barrier of
 // a CTA), and 8 warps where they are many.  A warp from which few rows go ranks the few keys that lie
 // below a bound; a CTA finds the border digit by digit of 8 bits, with counts of the keys of every
-// digit, until a count is met.  Positions of ties take the keys' place and are searched likewise.  32 layers of 16 sequences, 8 heads, up to 1029
-// rows of which 5 go: 15.5 us; a CTA each 87.
+// digit, until a count is met.  Positions of ties take the keys' place and are searched likewise.
+// 32 layers of 16 sequences, 8 heads, up to 1029 rows of which 5 go: 15.5 us; with a CTA each 87.
 constexpr int kEvThreads = 256;
 constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvWarpRows = 2048;        // rows of a warp's own
@@ -546,7 +546,9 @@ __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictPara
             if (lane == __ffs(__ballot_sync(0xffffffffu, rest == bound)) - 1) rest = ~0u;
         }
         int found = 0;
-        for (int j0 = 0; j0 < len; j0 += 128) {
+        const bool alike = __popc(__ballot_sync(0xffffffffu, low == bound)) > kEvTake;   // rather many rows are
+        if (alike) found = 33;
+        for (int j0 = 0; !alike && j0 < len; j0 += 128) {
             const int j = j0 + 4 * lane;
             const uint4 x = j < len ? *reinterpret_cast<const uint4 *>(kept + j) : make_uint4(~0u, ~0u, ~0u, ~0u);
             if (!__any_sync(0xffffffffu, min(min(x.x, x.y), min(x.z, x.w)) <= bound)) continue;
@@ -565,9 +567,9 @@ __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictPara
             const bool in = lane < found;
             const int row = in ? src[lane] : -1;
             const uint32_t x = in ? kept[row] : ~0u;
-            const unsigned alike = __match_any_sync(0xffffffffu, x);
+            const unsigned same = __match_any_sync(0xffffffffu, x);
             uint32_t y = 0;                                  // positions only where weights are alike
-            if (__any_sync(0xffffffffu, in && (alike & (alike - 1)))) y = in ? place_of(ld_dep(pos + row)) : 0;
+            if (__any_sync(0xffffffffu, in && (same & (same - 1)))) y = in ? place_of(ld_dep(pos + row)) : 0;
             int rank = 0;
             for (int k = 0; k < found; ++k) {
                 const uint32_t x2 = __shfl_sync(0xffffffffu, x, k), y2 = __shfl_sync(0xffffffffu, y, k);
@@ -632,14 +634,13 @@ __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictPara
     // The same over what shared memory holds of the rows, or of those with a bit in `mask`, 4 rows a load.
     // A warp, which takes few: the least, the next, and so on.  A CTA: 8 bits at a time from the top, with
     // counts of every digit's rows, and no further than to where a count is met.
-    auto border_kept = [&](const uint32_t *mask, int &left, uint32_t &at) {
+    auto border_kept = [&](const uint32_t *mask, uint32_t least, int &left, uint32_t &at) {
         auto real = [&](int j) {                             // which of rows j .. j + 3 there are
             const uint32_t m = j + 3 < len ? 15u : (1u << (len - j)) - 1u;
             return mask ? m & mask[j >> 5] >> (j & 31) : m;
         };
         if constexpr (NW == 1) {
-            bool begun = false;
-            for (;; begun = true) {
+            for (at = __reduce_min_sync(0xffffffffu, least);;) {
                 uint32_t next = ~0u;
                 int n = 0;
                 for (int j = 4 * tid; j < len; j += 4 * T) {
@@ -648,12 +649,12 @@ __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictPara
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         if (m >> k & 1u) {
-                            n += begun && y[k] == at;
-                            if (!begun || y[k] > at) next = min(next, y[k]);
+                            n += y[k] == at;
+                            if (y[k] > at) next = min(next, y[k]);
                         }
                 }
                 n = sum_all(n);
-                if (begun && n >= left) return n;
+                if (n >= left) return n;
                 left -= n;
                 at = __reduce_min_sync(0xffffffffu, next);
             }
@@ -702,18 +703,39 @@ __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictPara
     int left = E;
     uint32_t w_at = 0, p_at = 0;                             // borders: rows at them go, too, if all do
     if (len <= p.keep) {
-        const bool tied = border_kept(nullptr, left, w_at) != left;
-        for (int w = warp; w < nw; w += NW) {
-            const int j = w * 32 + lane;
-            const uint32_t x = j < len ? kept[j] : ~0u;
-            const unsigned m = __ballot_sync(0xffffffffu, j < len && (x < w_at || (!tied && x == w_at)));
-            const unsigned t = __ballot_sync(0xffffffffu, j < len && tied && x == w_at);
-            if (lane == 0) {
-                gone[w] = m;
-                ties[w] = t;
+        const bool tied = border_kept(nullptr, low, left, w_at) != left;
+        // Bits of the rows below the border, and of those at it: 4 of a thread, 8 threads a word.
+        auto mark = [&](const uint32_t *mask, uint32_t at, bool all) {
+            for (int w0 = warp * 4; w0 < nw; w0 += NW * 4) {
+                const int j = w0 * 32 + 4 * lane, w = w0 + lane / 8;
+                uint32_t m = 0, t = 0;
+                if (j < len) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(kept + j);
+                    const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+                    const uint32_t in = (j + 3 < len ? 15u : (1u << (len - j)) - 1u) & (mask ? mask[w] >> (j & 31) : 15u);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        m |= (uint32_t)(y[k] < at) << k;
+                        t |= (uint32_t)(y[k] == at) << k;
+                    }
+                    m = (m | (all ? t : 0u)) & in;
+                    t = all ? 0u : t & in;
+                }
+                m <<= j & 31;
+                t <<= j & 31;
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1) {
+                    m |= __shfl_xor_sync(0xffffffffu, m, o);
+                    t |= __shfl_xor_sync(0xffffffffu, t, o);
+                }
+                if (lane % 8 == 0 && w < nw) {
+                    gone[w] = mask ? gone[w] | m : m;
+                    ties[w] = t;
+                }
             }
-        }
-        sync();
+            sync();
+        };
+        mark(nullptr, w_at, !tied);
         if (tied) {
             // Positions take the keys' place.
             for (int j0 = 4 * tid; j0 < len; j0 += 16 * T) {
@@ -733,21 +755,15 @@ __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictPara
                             make_uint4(place_of(at[k].x), place_of(at[k].y), place_of(at[k].z), place_of(at[k].w));
             }
             sync();
-            const int alike = border_kept(ties, left, p_at);
-            const bool twins = alike != left;
-            for (int w = warp; w < nw; w += NW) {
-                const int j = w * 32 + lane;
-                const bool tie = ties[w] >> lane & 1u;
-                const uint32_t x = tie ? kept[j] : 0;
-                const unsigned m = __ballot_sync(0xffffffffu, tie && (x < p_at || (!twins && x == p_at)));
-                const unsigned t = __ballot_sync(0xffffffffu, tie && twins && x == p_at);
-                __syncwarp();
-                if (lane == 0) {
-                    gone[w] |= m;
-                    ties[w] = t;
-                }
+            uint32_t least = ~0u;                            // of this thread's rows that are alike
+            for (int j = 4 * tid; NW == 1 && j < len; j += 4 * T) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(kept + j);
+                const uint32_t m = ties[j >> 5] >> (j & 31);
+                least = min(least, min(min(m & 1 ? x.x : ~0u, m & 2 ? x.y : ~0u), min(m & 4 ? x.z : ~0u, m & 8 ? x.w : ~0u)));
             }
-            sync();
+            const int alike = border_kept(ties, least, left, p_at);
+            const bool twins = alike != left;
+            mark(ties, p_at, !twins);
             // Of rows alike in both the last `left` go.
             int before = 0;                                  // in the words so far, alike in all threads
             for (int w0 = 0; twins && w0 < nw; w0 += T) {
