@@ -40,8 +40,10 @@ template <int D, int ROWS, int MT>
 struct PoShape {
     static constexpr int WARPS = 4 * MT, NT = WARPS * 32;
     static constexpr int HV = D / 64, OPER = HV * kPoHalf, STAGE = 2 * OPER;
-    static constexpr int PER_SM = 2;                    // CTAs
-    static constexpr int STAGES = D == 128 ? 3 : 6;
+    // CTAs an SM, and stages of a ring.  Three with 2 stages or two with 3 (128 sequences of 500 slots, 16
+    // rows: 69 and 79 us; 8 rows: 66 and 67, but 8 sequences 22 and 19; 32 rows have registers for two).
+    static constexpr int PER_SM = ROWS == 16 && MT == 1 ? 3 : 2;
+    static constexpr int STAGES = (PER_SM == 3 ? 2 : 3) * (D == 128 ? 1 : 2);
     static constexpr int QHALF = MT * ROWS * 128;
     static constexpr int BYTES = STAGES * STAGE + HV * QHALF;
     static constexpr int OROW = D + 8;                  // floats of a row of O: rows lie in other banks
