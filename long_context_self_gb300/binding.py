@@ -651,9 +651,8 @@ def _tokens(t, name, dev, B, n, d):
     return H, stride
 
 
-def _append_args(k, v, k_pages, v_pages, block_table, seq_len, inv_freq, q, n_new, parent, q_out, dev):
-    """Checks of what both appends take: (shape, n, (q, stride, k, stride, v, stride), (len, n_new, parent),
-    (inv_freq, rot_dim), table, q_out's address, kp, vp, q_out)."""
+def _append_args(k, v, k_pages, v_pages, block_table, seq_len, inv_freq, q, n_new, parent, interleaved, q_out, dev):
+    """Checks of what both appends take; q_out and the arguments of magicdec_paged_append but the stream."""
     if k.dim() != 4:
         raise ValueError("k must be [B, n, H_kv, d]")
     B, n, H_kv, d = k.shape
@@ -678,10 +677,11 @@ def _append_args(k, v, k_pages, v_pages, block_table, seq_len, inv_freq, q, n_ne
         rot = inv_freq.numel()
         inv = _at(inv_freq, "inv_freq", _F32, dev, (rot,))
         rot *= 2
-    return (_paged(B, H_q, H_kv, d, page_size, n_pages, max_pages), n,
-            (qp, qs, k.data_ptr(), ks, v.data_ptr(), vs),
-            (_at(seq_len, "seq_len", _I32, dev, (B,)), None if n_new is None else _at(n_new, "n_new", _I32, dev, (B,)),
-             None if parent is None else _at(parent, "parent", _I32, dev, (B, n))), (inv, rot), table, qo, kp, vp, q_out)
+    return q_out, (
+        _paged(B, H_q, H_kv, d, page_size, n_pages, max_pages), n, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs,
+        _at(seq_len, "seq_len", _I32, dev, (B,)), None if n_new is None else _at(n_new, "n_new", _I32, dev, (B,)),
+        None if parent is None else _at(parent, "parent", _I32, dev, (B, n)), inv, rot, 1 if interleaved else 0, table,
+        qo, kp, vp)
 
 
 def magicdec_paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -697,10 +697,9 @@ def magicdec_paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tenso
         with _on(dev, stream):
             return magicdec_paged_append(k, v, k_pages, v_pages, block_table, seq_len, inv_freq, q, n_new, parent,
                                          interleaved, q_out)
-    shape, n, rows, seq, rope, table, qo, kp, vp, q_out = _append_args(k, v, k_pages, v_pages, block_table, seq_len,
-                                                                       inv_freq, q, n_new, parent, q_out, dev)
-    _check("magicdec_paged_append", (_lib or lib()).magicdec_paged_append(
-        shape, n, *rows, *seq, *rope, 1 if interleaved else 0, table, qo, kp, vp, _raw_stream(dev.index)))
+    q_out, args = _append_args(k, v, k_pages, v_pages, block_table, seq_len, inv_freq, q, n_new, parent, interleaved,
+                               q_out, dev)
+    _check("magicdec_paged_append", (_lib or lib()).magicdec_paged_append(*args, _raw_stream(dev.index)))
     return q_out
 
 
@@ -720,9 +719,9 @@ def magicdec_norm_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor
         with _on(dev, stream):
             return magicdec_norm_append(k, v, k_pages, v_pages, block_table, seq_len, inv_freq, q, q_weight, k_weight,
                                         eps, n_new, parent, pos, axis, interleaved, q_out)
-    shape, n, rows, seq, rope, table, qo, kp, vp, q_out = _append_args(k, v, k_pages, v_pages, block_table, seq_len,
-                                                                       inv_freq, q, n_new, parent, q_out, dev)
-    d = (shape.d,)
+    q_out, args = _append_args(k, v, k_pages, v_pages, block_table, seq_len, inv_freq, q, n_new, parent, interleaved,
+                               q_out, dev)
+    B, n, _, d = k.shape
     axes, pp, ap = 0, None, None
     if pos is not None:
         at = getattr(pos, "shape", ())
@@ -730,13 +729,13 @@ def magicdec_norm_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor
             raise ValueError("pos must be [B, n] or [B, n, axes]")
         axes = at[2] if len(at) == 3 else 1
         _fits("axes", axes)
-        pp = _at(pos, "pos", _I32, dev, (shape.B, n, axes)[:len(at)])
+        pp = _at(pos, "pos", _I32, dev, (B, n, axes)[:len(at)])
     if axis is not None:
-        ap = _at(axis, "axis", _I32, dev, (rope[1] // 2,))
+        ap = _at(axis, "axis", _I32, dev, (args[12] // 2,))
     _check("magicdec_norm_append", (_lib or lib()).magicdec_norm_append(
-        shape, n, *rows, None if q_weight is None else _at(q_weight, "q_weight", _BF16, dev, d),
-        None if k_weight is None else _at(k_weight, "k_weight", _BF16, dev, d), eps, *seq, pp, axes, ap, *rope,
-        1 if interleaved else 0, table, qo, kp, vp, _raw_stream(dev.index)))
+        *args[:8], None if q_weight is None else _at(q_weight, "q_weight", _BF16, dev, (d,)),
+        None if k_weight is None else _at(k_weight, "k_weight", _BF16, dev, (d,)), eps, *args[8:11], pp, axes, ap,
+        *args[11:], _raw_stream(dev.index)))
     return q_out
 
 

@@ -30,9 +30,10 @@
 //
 // Behind shared prefixes (template parameter PRE) the list begins with the prefixes: an entry
 // "sequence" of which the rows of all sequences of a group are the nodes, B n G rows a KV
-// head, so that a prefix's K and V are read once for a row block of any of them; the sequences'
-// own slots follow.  Every entry's part goes to the workspace, and a joining kernel of its own
-// puts a row's parts together.
+// head, so that a prefix's K and V are read once for a row block of any of them.  Every entry's
+// part goes to the workspace.  Own slots of up to 32 query rows are the work of another kernel, which
+// joins a row's parts (prefix_own.cu); those of more follow in the list, and a joining kernel here
+// puts the parts together.
 //
 // Roles (640 threads): warps 0 and 3 issue the TMA boxes, warps 1 and 2 the MMAs, warps
 // 4-11 and 12-19 are the softmax of the two streams.  Every wait is bounded; after one that
