@@ -13,7 +13,7 @@ constexpr int kTrEntry = 2;
 
 // Where an entry of the list of work begins, its tiles and blocks; one more behind the last
 // holds the length of a CTA's run of tiles.
-struct PreEntry {
+struct __align__(16) PreEntry {
     long long start;
     int tiles, blocks;
 };
@@ -49,6 +49,12 @@ __device__ __forceinline__ long long pre_slot(int row0, int e, int h, int rb, in
     return (long long)(row0 / block_rows + e) * H_kv + h * blocks + rb;
 }
 
+// What another kernel has just written is read from L2: no line of L1 can then be older.
+__device__ __forceinline__ PreEntry entry_at(const PreEntry *e) {
+    const int4 x = __ldcg(reinterpret_cast<const int4 *>(e));
+    return PreEntry{(long long)(uint32_t)x.x | (long long)x.y << 32, x.z, x.w};
+}
+
 // x / d, in 32 bits where they suffice (a 64-bit division is a hundred instructions).
 __device__ __forceinline__ long long quotient(long long x, int d) {
     return x <= 0xffffffffll ? (long long)((uint32_t)x / (uint32_t)d) : x / d;
@@ -70,10 +76,10 @@ __device__ __forceinline__ RowParts pre_parts(const PreParts &p, int b, int i, i
         else hi = mid;
     }
     const Group q = group_at(p.first, p.B, lo, nullptr);
-    const PreEntry x = p.entry[lo];
+    const PreEntry x = entry_at(p.entry + lo), runs = entry_at(p.run);
     if (b < q.lo || b >= q.hi || x.tiles == 0) return r;
     const int node = (b - q.lo) * p.n + i, rb = node / (p.RT * p.NB), local = node - rb * p.RT * p.NB, rt = local / p.NB;
-    const int run = (int)p.run->start;
+    const int run = (int)runs.start;
     const long long t0 = x.start + (long long)(h * x.blocks + rb) * (x.tiles + kTrEntry) + kTrEntry;
     const long long c0 = quotient(t0, run), c1 = quotient(t0 + x.tiles - 1, run);
     r.count = (int)(c1 - c0) + 1;

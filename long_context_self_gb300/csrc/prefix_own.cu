@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>
     for (int x = 0; x < QV; ++x) {
         const int r = (x * NT + tid) / VR, c = (x * NT + tid) % VR, i = r / G;
         const uint16_t *src = p.q + (((long long)b * n + i) * p.H_q + h * G + (r - i * G)) * D + c * 8;
-        qv[x] = r < R ? ld_dep_u4(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
+        qv[x] = r < R ? __ldcg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
     }
     const int parent = p.parent && tid < n ? ld_dep(p.parent + (long long)b * n + tid) : tid - 1;
     const int cap = p.page_size * p.max_pages;
@@ -336,18 +336,21 @@ __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>
         for (int j = 0; j < NB; ++j)
             *reinterpret_cast<float2 *>(to + j * 8) = make_float2(o[j][2 * e] * f, o[j][2 * e + 1] * f);
     }
-    // The prefix's parts, 4 channels c4 of ITEMS rows a thread at most, whose loads go side by side, then
-    // the CTAs' O; the CTAs take the rows in turn.
-    constexpr int ITEMS = MT * ROWS * (D / 4) / NT, STEP = NT / (D / 4);
-    const int c4 = tid % (D / 4);
-    int row[ITEMS];
+    // The prefix's parts, then the CTAs' O: an item is 4 channels of a row, of which a thread has ITEMS at
+    // most, whose loads go side by side.  Neighbouring threads have up to 8 neighbouring rows of the same
+    // channels, which lie together in a part.
+    constexpr int ITEMS = MT * ROWS * (D / 4) / NT;
+    const int lg = R > 4 ? 3 : R > 2 ? 2 : R - 1;       // log2 of such rows
+    int row[ITEMS], c4[ITEMS];
     RowParts parts[ITEMS];
     float4 acc[ITEMS];
     float2 st[ITEMS];
     int most = 0;
 #pragma unroll
     for (int x = 0; x < ITEMS; ++x) {
-        row[x] = (x * (int)C + (int)rank) * STEP + tid / (D / 4);
+        const int i = (x * (int)C + (int)rank) * NT + tid;
+        row[x] = (i >> lg) / (D / 4) * (1 << lg) + (i & ((1 << lg) - 1));
+        c4[x] = (i >> lg) % (D / 4);
         parts[x] = row[x] < R ? parts_of[row[x]] : RowParts{0, 0, 1, 0};
         most = max(most, parts[x].count);
         acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -371,8 +374,8 @@ __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>
                 y[k][x] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (k0 + k < parts[x].count) {
                     const long long at = parts[x].tile + (long long)(k0 + k) * parts[x].step;
-                    e[k][x] = p.pre.stat[at * 128 + parts[x].row];
-                    y[k][x] = p.pre.part[(at * (D / 4) + c4) * 128 + parts[x].row];
+                    e[k][x] = __ldcg(p.pre.stat + at * 128 + parts[x].row);
+                    y[k][x] = __ldcg(p.pre.part + (at * (D / 4) + c4[x]) * 128 + parts[x].row);
                 }
             }
 #pragma unroll
@@ -391,13 +394,13 @@ __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>
                 float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int w = 0; w < L::WARPS / MT; ++w) {
-                    const float4 y = *reinterpret_cast<const float4 *>(osum + (w * R + r) * OROW + c4 * 4);
+                    const float4 y = *reinterpret_cast<const float4 *>(osum + (w * R + r) * OROW + c4[x] * 4);
                     sum = make_float4(sum.x + y.x, sum.y + y.y, sum.z + y.z, sum.w + y.w);
                 }
                 add(x, cstat[r], sum);
             } else {
                 for (uint32_t c = 0; c < C; ++c) {
-                    const uint32_t base = few_at(osum, c) + (uint32_t)(r * OROW + c4 * 4) * 4;
+                    const uint32_t base = few_at(osum, c) + (uint32_t)(r * OROW + c4[x] * 4) * 4;
                     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                     for (int w = 0; w < L::WARPS / MT; ++w) {
@@ -409,7 +412,7 @@ __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>
             }
         }
         const float inv = st[x].y > 0.f ? 1.f / st[x].y : 0.f;
-        *reinterpret_cast<uint2 *>(p.out + (((long long)b * n + t) * p.H_q + h * G + (r - t * G)) * D + c4 * 4) =
+        *reinterpret_cast<uint2 *>(p.out + (((long long)b * n + t) * p.H_q + h * G + (r - t * G)) * D + c4[x] * 4) =
             make_uint2(pack_bf16(acc[x].x * inv, acc[x].y * inv), pack_bf16(acc[x].z * inv, acc[x].w * inv));
     }
     if (C > 1) few_cluster_sync();                      // no CTA ends while another reads its O

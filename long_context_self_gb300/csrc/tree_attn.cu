@@ -1112,9 +1112,9 @@ __global__ void __launch_bounds__(kTjThreads) tree_attn_pre_join_kernel(const Tr
     RowParts piece[2] = {RowParts{0, 0, 1, 0}, RowParts{0, 0, 1, 0}};
     if (i < nodes) {
         piece[0] = pre_parts(p.pre, b, i, g, h);
-        const PreEntry x = p.pre.entry[p.pre.P + b];
+        const PreEntry x = entry_at(p.pre.entry + p.pre.P + b);
         if (x.tiles) {
-            const int rb = i / (RT * p.NB), local = i - rb * RT * p.NB, rt = local / p.NB, run = (int)p.pre.run->start;
+            const int rb = i / (RT * p.NB), local = i - rb * RT * p.NB, rt = local / p.NB, run = (int)entry_at(p.pre.run).start;
             const long long t0 = x.start + (long long)(h * x.blocks + rb) * (x.tiles + kTrEntry) + kTrEntry;
             const long long c0 = quotient(t0, run), c1 = quotient(t0 + x.tiles - 1, run);
             piece[1] = RowParts{(part_slot<RT>(p, p.pre.P + b, h, rb, x.blocks, 0) + c0) * p.own_rt + rt, (int)(c1 - c0) + 1,
@@ -1143,7 +1143,7 @@ __global__ void __launch_bounds__(kTjThreads) tree_attn_pre_join_kernel(const Tr
             for (int j = PL > 1 ? warp : 0; j < piece[k].count; j += PL) {
                 const long long s = piece[k].tile + (long long)j * piece[k].step;
                 const float4 *src = part + (s * (D / 4) + 2 * c) * rr + piece[k].row;
-                add(stat[s * rr + piece[k].row], src[0], src[rr]);
+                add(__ldcg(stat + s * rr + piece[k].row), __ldcg(src), __ldcg(src + rr));
             }
         }
         if (PL > 1) {
