@@ -255,7 +255,8 @@ __global__ void __launch_bounds__(kHvThreads, 2)
             for (uint32_t c = 0; c < C; ++c) join(s, few_ld2(few_at(&cstat[tid], c)));
         else
             s = cstat[tid];
-        all[tid] = make_float2(s.x == -INFINITY ? 0.f : s.x, s.y > 0.f ? 1.f / s.y : 0.f);
+        // A sum of zero: a row that sees nothing.  One of NaN stays so, in every weight that it has a part in.
+        all[tid] = make_float2(s.x == -INFINITY ? 0.f : s.x, s.y == 0.f ? 0.f : 1.f / s.y);
     }
     __syncthreads();
     // Every row's weight, summed over the query rows in their order.
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kHvThreads, 2)
 #pragma unroll
         for (int x = 0; x < KEYS; ++x) {
             const int j = j0 + x * kHvThreads;
-            old[x] = j < k1 && j < first_new ? p.weight[row0 + j] : 0.f;
+            old[x] = j < k1 && j < first_new ? __ldcg(p.weight + row0 + j) : 0.f;
         }
 #pragma unroll
         for (int x = 0; x < KEYS; ++x) {

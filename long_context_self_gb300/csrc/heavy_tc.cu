@@ -349,8 +349,11 @@ __global__ void __launch_bounds__(kHtThreads, 2)
                 const float mx = fmaxf(s.x, x.x), mu = mx == -INFINITY ? 0.f : mx;
                 s = make_float2(mx, s.y * fast_exp2(s.x - mu) + x.y * fast_exp2(x.x - mu));
             }
-            all[row] = row < p.R && s.y > 0.f ? make_float2(s.x, 1.f / s.y) : make_float2(0.f, 0.f);
-            moved[row] = tiles == 0 || held[row] == -INFINITY ? 0.f : fast_exp2(held[row] - all[row].x) * all[row].y;
+            // A sum of zero: a row that sees nothing.  One of NaN stays so, in the output (NaN * 0, where no score
+            // of this CTA's was a number) and in every weight that it has a part in.
+            const bool none = row >= p.R || s.y == 0.f;
+            all[row] = none ? make_float2(0.f, 0.f) : make_float2(s.x == -INFINITY ? 0.f : s.x, 1.f / s.y);
+            moved[row] = tiles == 0 ? 0.f : (held[row] == -INFINITY ? 0.f : fast_exp2(held[row] - all[row].x)) * all[row].y;
         }
         named_bar_sync(2, 128);
         // O, in the softmax's own scale, to the probabilities' place: [R][D].
@@ -372,7 +375,7 @@ __global__ void __launch_bounds__(kHtThreads, 2)
                 float y = f[i] == 0.f ? 0.f : __uint_as_float(o[i]) * f[i];
                 if (odd && real)
                     for (int j = max(own, k0); j < k1; ++j) {
-                        const uint32_t z = (uint32_t)p.v[(row0 + j) * D + chan] << 16;
+                        const uint32_t z = (uint32_t)__ldcg(p.v + (row0 + j) * D + chan) << 16;
                         if ((z & 0x7f800000u) == 0x7f800000u && c + i >= (j - own) * p.G) y += __uint_as_float(z);
                     }
                 if (real && c + i < p.R) osum[(c + i) * D + chan] = y;
@@ -383,7 +386,7 @@ __global__ void __launch_bounds__(kHtThreads, 2)
         const int first_new = p.next_pos ? own : INT_MAX;
         for (int t = 0; t < tiles; ++t) {
             const int key = k0 + t * kHtKeys + row;
-            const float old = key < k1 && key < first_new ? p.weight[row0 + key] : 0.f;
+            const float old = key < k1 && key < first_new ? __ldcg(p.weight + row0 + key) : 0.f;
             uint32_t x[NR];
             take(x);
             const int lo = from_row(key);

@@ -153,6 +153,37 @@ def test_a_token_behind_others_reaches_none_of_them(n, H_q):
     assert got[:, 1:].isnan().all()
 
 
+@pytest.mark.parametrize("n,H_q,d,cap", [(1, 8, 128, 200), (2, 8, 64, 12001), (3, 8, 128, 700), (8, 8, 64, 200), (8, 8, 128, 3000)])
+def test_scores_that_are_not_numbers(n, H_q, d, cap):
+    """A row that sees a NaN or a score of infinity is NaN, as are the weights of the rows that it sees;
+    all others are as without."""
+    B, H_kv = 4, 2
+    G, lens = H_q // H_kv, [cap, cap - 7, cap - 20, cap]
+    kc, vc, weight, pos = cache(B, H_kv, cap, d, lens, 81)
+    q = randn((B, n, H_q, d), 82)
+    w0, p0 = weight.clone(), pos.clone()
+    clean = mb.magicdec_heavy_attn(q, kc, vc, weight, i32(lens), pos=pos, next_pos=i32([5] * B))
+    kc[0, 0, 11, 3] = float("nan")                     # a row that all tokens see
+    kc[1, 1] = float("nan")                            # every row of a head
+    q[2, n - 1, 0, 5] = float("nan")                   # a query row
+    kc[3, 0, 40, 9] = float("inf")                     # scores of either infinity: NaN, and nothing for this row
+    bad = torch.zeros((B, n, H_kv, G), dtype=torch.bool, device=DEV)
+    bad[0, :, 0] = bad[1, :, 1] = bad[2, n - 1, 0, 0] = True
+    bad[3, :, 0] = q[3, :, :G, 9] > 0
+    got = mb.magicdec_heavy_attn(q, kc, vc, w0, i32(lens), pos=p0, next_pos=i32([5] * B))
+    hit = bad.view(B, n, H_q)
+    assert got[hit].isnan().all() and not got[~hit].isnan().any()
+    assert torch.equal(got[:3][~hit[:3]], clean[:3][~hit[:3]]) and torch.equal(got[3, :, G:], clean[3, :, G:])
+    any_row = bad.any(-1).any(1)                       # of a KV head
+    for b in range(B):
+        for h in range(H_kv):
+            if not any_row[b, h]:
+                assert torch.equal(w0[b, h, :lens[b]], weight[b, h, :lens[b]])
+            else:
+                first = int(bad[b, :, h].any(-1).nonzero().max())          # the last token that is NaN sees the most
+                assert w0[b, h, :lens[b] - n + 1 + first].isnan().all()
+
+
 def test_attention_of_growing_scores():
     """Keys whose scores grow, and fall, along the rows: the running maximum moves often."""
     B, n, H_q, H_kv, d, cap = 2, 2, 8, 2, 128, 2000

@@ -108,6 +108,31 @@ CASES = [
 ]
 
 
+@pytest.mark.parametrize("n,H_q,d", [(1, 8, 128), (4, 8, 64), (8, 8, 128), (20, 8, 128), (70, 8, 64)])
+def test_scores_that_are_not_numbers(n, H_q, d):
+    """A row that sees a NaN, in its prefix or among its own positions, is NaN; all others are as without."""
+    H_kv, page, first, plens, lens = 2, 16, [0, 3, 5], [900, 300], [40, 130, 20, 0, 300]
+    B, G = len(lens), H_q // H_kv
+    kp, vp, ptable, table = make(plens, first, lens, n, page, H_kv, d, 25)
+    q = randn((B, n, H_q, d), 26)
+    args = (ptable, i32(plens), table, i32(lens), i32(first))
+    clean = mb.magicdec_prefix_attn(q, kp, vp, *args)
+    hit = torch.zeros((B, n, H_kv, G), dtype=torch.bool, device=DEV)
+    kp[int(ptable[1, 5]), 3, 0, 7] = float("nan")      # a prefix's row: both sequences behind it
+    hit[3:, :, 0] = True
+    kp[table[0, :2].long(), :, 1] = float("nan")       # most of a sequence's own positions
+    hit[0, :, 1] = True
+    q[1, n - 1, 2, 1] = float("nan")                   # a query row
+    hit[1, n - 1, 2 // G, 2 % G] = True
+    got = mb.magicdec_prefix_attn(q, kp, vp, *args)
+    hit = hit.view(B, n, H_q)
+    assert got[hit].isnan().all()
+    assert torch.equal(got[~hit], clean[~hit])
+    kp[ptable[0].long(), :, 1] = float("nan")          # all of a prefix
+    got = mb.magicdec_prefix_attn(q, kp, vp, *args)
+    assert got[:3, :, G:].isnan().all() and torch.equal(got[:2, :n - 1, :G], clean[:2, :n - 1, :G])
+
+
 @pytest.mark.parametrize("H_q,H_kv,d,n,plens,first,lens,page,tree,counts", CASES)
 def test_attention(H_q, H_kv, d, n, plens, first, lens, page, tree, counts):
     B, P = len(lens), len(plens)
