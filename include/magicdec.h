@@ -617,8 +617,9 @@ MAGICDEC_API magicdec_status magicdec_tree_commit(magicdec_paged_shape shape, in
  *            is replaced, pos by next_pos[b] + i, the weight by this call's alone.  NULL: pos is not
  *            looked at (and may be NULL), and all weights are added to
  * Rows at or past len may hold anything, NaN included, and are left as they are; a token's own
- * row reaches it and later tokens only, whatever it holds.  Probabilities are summed in fp32, in
- * an order that is the same from run to run.
+ * row reaches it and later tokens only, whatever it holds; a query row that meets a score of NaN or
+ * plus infinity comes out as NaN, and so do the weights of the rows it sees.  Probabilities are summed
+ * in fp32, in an order that is the same from run to run.
  * Supported: (H_q/H_kv) * n_q <= 32 and H_kv <= 65535 (MAGICDEC_ERR_UNSUPPORTED beyond).
  * Errors: NULL pointers, bad shape, n_q <= 0, alignment (q, kc, vc, out).
  */
