@@ -417,7 +417,7 @@ magicdec_status launch_heavy_attn(int B, int H_q, int H_kv, int D, int cap, int 
 // Bound: 8 bytes a row (weight, position) from HBM; in practice the chain of loads, searches and
 // moves of a (layer, sequence, KV head), which only others can cover.  So one warp takes it where its
 // keys are few (kEvWarpRows; keys in shared memory, reductions and lists inside the warp, no barrier of
-// a CTA), and 8 warps where they are many.  A warp from which few rows go ranks the few keys that lie
+// a CTA) and few rows can go or there are many others, else 8 warps.  A warp from which few rows go ranks the few keys that lie
 // below a bound; a CTA finds the border digit by digit of 8 bits, with counts of the keys of every
 // digit, until a count is met.  Positions of ties take the keys' place and are searched likewise.
 // 32 layers of 16 sequences, 8 heads, up to 1029 rows of which 5 go: 15.5 us; with a CTA each 87.
@@ -632,15 +632,44 @@ __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictPara
         for (int j = tid; j < len; j += T) n += in(j) && part(j) == at;
         return sum_all(n);
     };
-    // The same over what shared memory holds of the rows, or of those with a bit in `mask`, 4 rows a load.
-    // A warp, which takes few: the least, the next, and so on.  A CTA: 8 bits at a time from the top, with
-    // counts of every digit's rows, and no further than to where a count is met.
+    // The same over what shared memory holds of the rows, or of those with a bit in `mask`, 4 rows a load,
+    // and no further than to where a count is met.  A warp that takes few: the least, the next, and so on;
+    // one that takes many: bit by bit from the top.  A CTA: 8 bits at a time, with counts of every digit's rows.
     auto border_kept = [&](const uint32_t *mask, uint32_t least, int &left, uint32_t &at) {
         auto real = [&](int j) {                             // which of rows j .. j + 3 there are
             const uint32_t m = j + 3 < len ? 15u : (1u << (len - j)) - 1u;
             return mask ? m & mask[j >> 5] >> (j & 31) : m;
         };
-        if constexpr (NW == 1) {
+        if (NW == 1 && left > kEvTake) {
+            at = 0;
+            for (int bit = 31;; --bit) {
+                int n = 0;                                   // rows that agree so far and have no such bit
+                for (int j = 4 * tid; j < len; j += 4 * T) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(kept + j);
+                    const uint32_t y[4] = {x.x, x.y, x.z, x.w}, m = real(j);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) n += (m >> k & 1u) && ((y[k] ^ at) >> bit) == 0;
+                }
+                n = sum_all(n);
+                if (n == left) {                             // all of them go
+                    at |= (1u << bit) - 1u;
+                    return n;
+                }
+                if (n < left) {
+                    left -= n;
+                    at |= 1u << bit;
+                }
+                if (bit == 0) break;
+            }
+            int n = 0;
+            for (int j = 4 * tid; j < len; j += 4 * T) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(kept + j);
+                const uint32_t y[4] = {x.x, x.y, x.z, x.w}, m = real(j);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) n += (m >> k & 1u) && y[k] == at;
+            }
+            return sum_all(n);
+        } else if constexpr (NW == 1) {
             for (at = __reduce_min_sync(0xffffffffu, least);;) {
                 uint32_t next = ~0u;
                 int n = 0;
@@ -909,8 +938,13 @@ magicdec_status launch_heavy_evict(int layers, int B, int H_kv, int D, int cap, 
     p.n_recent = n_recent;
     p.wide = cap % 4 == 0 && magicdec_host::aligned16(weight) && magicdec_host::aligned16(pos);
     p.keep = cap < kEvKeep ? (cap + 3) / 4 * 4 : cap <= kEvMaxRows / 2 ? kEvKeep : kEvKeep / 2;
-    // A warp an item where few rows can go, as it moves but one at a time.
-    return cap <= kEvWarpRows && cap - budget <= kEvTake ? launch_evict_t<1>(p, st) : launch_evict_t<kEvWarps>(p, st);
+    // A warp an item where few rows can go, as it moves but a few at a time, and where there are so many items
+    // that warps of other ones cover that.  Warps and CTAs, d = 128: 9728 items of 63 rows of which 17 go 40 and
+    // 113 us, of 1029 of which 5 go 38 and 111, of 1200 of which 800 go 496 and 470; 2432 of 1029 19 and 36, of 2048
+    // of which 1024 go 298 and 232; 1216 of 63 17 and 21, of 2048 191 and 128; 608 of 63 17 and 15.
+    const long long many = (cap <= 256 ? 8 : 16) * magicdec_host::sm_count();
+    return cap <= kEvWarpRows && (cap - budget <= kEvTake || p.items >= many) ? launch_evict_t<1>(p, st)
+                                                                              : launch_evict_t<kEvWarps>(p, st);
 }
 
 }  // namespace magicdec

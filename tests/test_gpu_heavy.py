@@ -218,6 +218,11 @@ EVICT = [
     # most of the rows go, more moves than are listed at a time
     (1, 2, 2, 128, 4000, [4000, 2100], 2000, 16, 100, "random"),
     (1, 1, 1, 64, 5000, [5000], 3, 1, 1, "few"),
+    # many caches, each of a few rows, of which a few or many go
+    (8, 39, 8, 64, 70, [(b * 29) % 72 for b in range(39)], 30, 2, 5, "random"),
+    (8, 39, 8, 64, 70, [(b * 29) % 72 for b in range(39)], 20, 0, 0, "few"),
+    (8, 39, 8, 64, 70, [(b * 29) % 72 for b in range(39)], 33, 0, 0, "twins"),
+    (2, 200, 8, 64, 280, [(b * 29) % 282 for b in range(200)], 130, 5, 20, "random"),
     # more rows than keys in shared memory
     (1, 1, 1, 64, 30001, [30001], 29000, 16, 1000, "random"),
     (1, 1, 1, 64, 30001, [29990], 1000, 16, 100, "few"),
