@@ -11,6 +11,9 @@ namespace magicdec {
 // to a few CTAs, and the call took 890 us instead of some 500.
 constexpr int kTrEntry = 2;
 
+// Tiles of a CTA's run at least: a tile more is soon done, a part more has to be written and joined.
+constexpr int kTrLeast = 2;
+
 // Where an entry of the list of work begins, its tiles and blocks; one more behind the last
 // holds the length of a CTA's run of tiles.
 struct __align__(16) PreEntry {
@@ -96,6 +99,7 @@ struct PreOwn {
     const int32_t *len, *n_nodes, *parent, *table;
     int *err;
     int H_q, page_size, n_pages, max_pages;
+    int parts;                   // of a row's prefix, about
     float scale_log2;            // log2(e) / sqrt(d)
 };
 magicdec_status launch_prefix_own(const PreOwn &p, int D, cudaStream_t st);

@@ -26,6 +26,7 @@ namespace magicdec {
 constexpr int kPoKeys = 64;              // keys of a stage
 constexpr int kPoHalf = kPoKeys * 128;   // bytes of 64 channels of them
 constexpr int kPoMaxCluster = 8;
+constexpr int kPoParts = 32;             // items' parts of a thread that are worth a CTA more
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
@@ -47,7 +48,14 @@ struct PoShape {
     static constexpr int QHALF = MT * ROWS * 128;
     static constexpr int BYTES = STAGES * STAGE + HV * QHALF;
     static constexpr int OROW = D + 8;                  // floats of a row of O: rows lie in other banks
+    static_assert(4 * (D / 4) <= NT, "4 rows are an item a thread, or less");
     static_assert(4 * MT * ROWS * OROW * 4 <= STAGES * STAGE, "the warps' O take the ring's place");
+};
+
+// A number that a generic lambda takes as a compile-time constant.
+template <int N>
+struct Items {
+    static constexpr int value = N;
 };
 
 template <int D, int ROWS, int MT>
@@ -63,6 +71,7 @@ __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>
     __shared__ uint32_t sees[32];                       // of a node's slots: itself and its ancestors
     __shared__ float2 wstat[L::WARPS][16];              // of a warp's rows: (max, sum)
     __shared__ float2 cstat[32];                        // of this CTA
+    __shared__ float2 both[32];                         // of this CTA and of the prefix's parts that it took
     __shared__ RowParts parts_of[32];                   // of the prefix
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int lq = lane & 3, lr = lane >> 2;
@@ -336,22 +345,22 @@ __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>
         for (int j = 0; j < NB; ++j)
             *reinterpret_cast<float2 *>(to + j * 8) = make_float2(o[j][2 * e] * f, o[j][2 * e + 1] * f);
     }
-    // The prefix's parts, then the CTAs' O: an item is 4 channels of a row, of which a thread has ITEMS at
-    // most, whose loads go side by side.  Neighbouring threads have up to 8 neighbouring rows of the same
-    // channels, which lie together in a part.
+    // The prefix's parts, of which the CTAs of the cluster take every C-th, then the CTA's own O, then the
+    // other CTAs' sums of both.  An item is 4 channels of a row, of which a thread has ITEMS, whose loads
+    // go side by side.  Neighbouring threads have up to 8 neighbouring rows of the same channels, which
+    // lie together in a part.
     constexpr int ITEMS = MT * ROWS * (D / 4) / NT;
     const int lg = R > 4 ? 3 : R > 2 ? 2 : R - 1;       // log2 of such rows
-    int row[ITEMS], c4[ITEMS];
+    auto row_of = [&](int i) { return (i >> lg) / (D / 4) * (1 << lg) + (i & ((1 << lg) - 1)); };
+    auto chan_of = [&](int i) { return (i >> lg) % (D / 4) * 4; };
     RowParts parts[ITEMS];
     float4 acc[ITEMS];
     float2 st[ITEMS];
     int most = 0;
 #pragma unroll
     for (int x = 0; x < ITEMS; ++x) {
-        const int i = (x * (int)C + (int)rank) * NT + tid;
-        row[x] = (i >> lg) / (D / 4) * (1 << lg) + (i & ((1 << lg) - 1));
-        c4[x] = (i >> lg) % (D / 4);
-        parts[x] = row[x] < R ? parts_of[row[x]] : RowParts{0, 0, 1, 0};
+        const int r = row_of(x * NT + tid);
+        parts[x] = r < R ? parts_of[r] : RowParts{0, 0, 1, 0};
         most = max(most, parts[x].count);
         acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
         st[x] = make_float2(-INFINITY, 0.f);
@@ -362,71 +371,86 @@ __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>
         st[x] = make_float2(mx, st[x].y * f + e.y * w);
         acc[x] = make_float4(acc[x].x * f + y.x * w, acc[x].y * f + y.y * w, acc[x].z * f + y.z * w, acc[x].w * f + y.w * w);
     };
-    constexpr int BATCH = 8 / ITEMS;                    // parts of a row whose loads go together
-    for (int k0 = 0; k0 < most; k0 += BATCH) {
-        float2 e[BATCH][ITEMS];
-        float4 y[BATCH][ITEMS];
+    auto write = [&](int x, int r, int c) {
+        const float inv = st[x].y > 0.f ? 1.f / st[x].y : 0.f;
+        const int t = r / G;
+        *reinterpret_cast<uint2 *>(p.out + (((long long)b * n + t) * p.H_q + h * G + (r - t * G)) * D + c) =
+            make_uint2(pack_bf16(acc[x].x * inv, acc[x].y * inv), pack_bf16(acc[x].z * inv, acc[x].w * inv));
+    };
+    // 8 loads of a thread under way: parts of ITEMS items, or, with half the rows, more parts of one.
+    auto join_parts = [&](auto of) {
+        constexpr int HAS = decltype(of)::value, BATCH = 8 / HAS;
+        for (int k0 = (int)rank; k0 < most; k0 += BATCH * (int)C) {
+            float2 e[BATCH][HAS];
+            float4 y[BATCH][HAS];
 #pragma unroll
-        for (int k = 0; k < BATCH; ++k)
+            for (int k = 0; k < BATCH; ++k)
 #pragma unroll
-            for (int x = 0; x < ITEMS; ++x) {
-                e[k][x] = make_float2(-INFINITY, 0.f);
-                y[k][x] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (k0 + k < parts[x].count) {
-                    const long long at = parts[x].tile + (long long)(k0 + k) * parts[x].step;
-                    e[k][x] = __ldcg(p.pre.stat + at * 128 + parts[x].row);
-                    y[k][x] = __ldcg(p.pre.part + (at * (D / 4) + c4[x]) * 128 + parts[x].row);
+                for (int x = 0; x < HAS; ++x) {
+                    e[k][x] = make_float2(-INFINITY, 0.f);
+                    y[k][x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    const int j = k0 + k * (int)C;
+                    if (j < parts[x].count) {
+                        const long long at = parts[x].tile + (long long)j * parts[x].step;
+                        e[k][x] = __ldcg(p.pre.stat + at * 128 + parts[x].row);
+                        y[k][x] = __ldcg(p.pre.part + (at * (D / 4) + chan_of(x * NT + tid) / 4) * 128 + parts[x].row);
+                    }
                 }
-            }
 #pragma unroll
-        for (int k = 0; k < BATCH; ++k)
+            for (int k = 0; k < BATCH; ++k)
 #pragma unroll
-            for (int x = 0; x < ITEMS; ++x) add(x, make_float2(e[k][x].x * sl, e[k][x].y), y[k][x]);
-    }
-    if (C > 1) few_cluster_sync();
-    else __syncthreads();
+                for (int x = 0; x < HAS; ++x) add(x, make_float2(e[k][x].x * sl, e[k][x].y), y[k][x]);
+        }
+    };
+    if (HR == 1 && R <= 4) join_parts(Items<1>());
+    else join_parts(Items<ITEMS>());
+    __syncthreads();
 #pragma unroll
     for (int x = 0; x < ITEMS; ++x) {
-        if (row[x] >= R) continue;
-        const int r = row[x], t = r / G;
-        if (t < nodes) {
-            if (C == 1) {
-                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int r = row_of(x * NT + tid), c = chan_of(x * NT + tid);
+        if (r >= R) continue;
+        float4 *o4 = reinterpret_cast<float4 *>(osum + r * OROW + c);
+        if (r / G < nodes) {
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int w = 0; w < L::WARPS / MT; ++w) {
-                    const float4 y = *reinterpret_cast<const float4 *>(osum + (w * R + r) * OROW + c4[x] * 4);
-                    sum = make_float4(sum.x + y.x, sum.y + y.y, sum.z + y.z, sum.w + y.w);
-                }
-                add(x, cstat[r], sum);
-            } else {
-                for (uint32_t c = 0; c < C; ++c) {
-                    const uint32_t base = few_at(osum, c) + (uint32_t)(r * OROW + c4[x] * 4) * 4;
-                    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int w = 0; w < L::WARPS / MT; ++w) {
-                        const float4 y = few_ld4(base + (uint32_t)(w * R * OROW) * 4);
-                        sum = make_float4(sum.x + y.x, sum.y + y.y, sum.z + y.z, sum.w + y.w);
-                    }
-                    add(x, few_ld2(few_at(&cstat[r], c)), sum);
-                }
+            for (int w = 0; w < L::WARPS / MT; ++w) {
+                const float4 y = *reinterpret_cast<const float4 *>(osum + (w * R + r) * OROW + c);
+                sum = make_float4(sum.x + y.x, sum.y + y.y, sum.z + y.z, sum.w + y.w);
             }
+            add(x, cstat[r], sum);
         }
-        const float inv = st[x].y > 0.f ? 1.f / st[x].y : 0.f;
-        *reinterpret_cast<uint2 *>(p.out + (((long long)b * n + t) * p.H_q + h * G + (r - t * G)) * D + c4[x] * 4) =
-            make_uint2(pack_bf16(acc[x].x * inv, acc[x].y * inv), pack_bf16(acc[x].z * inv, acc[x].w * inv));
+        if (C == 1) {
+            write(x, r, c);
+        } else {
+            *o4 = acc[x];                               // in the first warp's place, which only this thread has read
+            if (c == 0) both[r] = st[x];
+        }
     }
-    if (C > 1) few_cluster_sync();                      // no CTA ends while another reads its O
+    if (C == 1) return;
+    few_cluster_sync();
+    for (int i = (int)rank * NT + tid; i < ITEMS * NT; i += (int)C * NT) {
+        const int r = row_of(i), c = chan_of(i);
+        if (r >= R) continue;
+        acc[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+        st[0] = make_float2(-INFINITY, 0.f);
+        for (uint32_t k = 0; k < C; ++k) add(0, few_ld2(few_at(&both[r], k)), few_ld4(few_at(osum + r * OROW + c, k)));
+        write(0, r, c);
+    }
+    few_cluster_sync();                                 // no CTA ends while another reads its O
 }
 
 template <int D, int ROWS, int MT>
 static magicdec_status launch_own_t(const PreOwn &p, cudaStream_t st) {
     using L = PoShape<D, ROWS, MT>;
     if (!magicdec_host::allow_smem_once<prefix_own_kernel<D, ROWS, MT>>(L::BYTES)) return MAGICDEC_ERR_CUDA;
-    // As many CTAs a (sequence, KV head) as there are places for, with 64 slots each at least.
+    // As many CTAs a (sequence, KV head) as there are places for, with 64 slots each at least, or with parts of the
+    // prefix to share: 4 turns of 8 loads (17 parts of 4 rows, 8 sequences behind 4k: a CTA 19.3 us, four 20.1; 65 of
+    // 16 rows, 16 sequences of one KV head behind 16k: clusters of 2 and 8 34 and 26).
     const int slots = L::PER_SM * magicdec_host::sm_count();
     const long long cap = (long long)p.page_size * p.max_pages;
+    const int items = (p.pre.n * p.pre.G * (D / 4) + L::NT - 1) / L::NT;
     int C = 1;
-    while (C < kPoMaxCluster && 2ll * C * p.pre.B * p.pre.H_kv <= slots && cap > C * kPoKeys) C *= 2;
+    while (C < kPoMaxCluster && 2ll * C * p.pre.B * p.pre.H_kv <= slots && (cap > C * kPoKeys || (long long)p.parts * items > C * kPoParts)) C *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)C, (unsigned)p.pre.H_kv, (unsigned)p.pre.B);
     cfg.blockDim = dim3(L::NT);

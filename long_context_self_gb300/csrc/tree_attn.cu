@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             if (w < warp) before += x;
             all += x;
         }
-        const long long run = max(1ll, quotient(all + p.grid - 1, p.grid));
+        const long long run = max(PRE ? (long long)kTrLeast : 1ll, quotient(all + p.grid - 1, p.grid));
         const long long t0 = blockIdx.x * run;
         for (int b = ba; b < bz; ++b) {
             if (per > 1) sq = seq_at<RT, PRE>(p, b);
@@ -1340,7 +1340,7 @@ size_t prefix_attn_workspace_bytes(const magicdec_paged_shape &s, int P, int n) 
 template <int D, int RT>
 static magicdec_status launch_prefix_t(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv,
                                        const CUtensorMap &tmg, const TreeAttnParams &p, const uint16_t *q,
-                                       const uint16_t *k, cudaStream_t st) {
+                                       const uint16_t *k, int parts, cudaStream_t st) {
     auto kern = tree_attn_kernel<D, RT, true>;
     constexpr int smem = TrSmem<D, RT>::BYTES;
     if (!magicdec_host::allow_smem_once<tree_attn_kernel<D, RT, true>>(smem)) return MAGICDEC_ERR_CUDA;
@@ -1363,12 +1363,16 @@ static magicdec_status launch_prefix_t(const CUtensorMap &tmq, const CUtensorMap
         x.page_size = p.page_size;
         x.n_pages = p.n_pages;
         x.max_pages = p.max_pages;
+        x.parts = parts;
         x.scale_log2 = p.scale_log2;
         return launch_prefix_own(x, D, st);
     }
     const unsigned blocks = (unsigned)(((long long)p.B * p.n * p.G + 31) / 32);
-    // Parts shared out while the blocks of whole rows would not fill the GPU.
-    if ((long long)blocks * p.H_kv <= p.grid)
+    // Parts shared out while the blocks of whole rows are few, each of the 16 or 8 blocks of a row finding its
+    // parts anew (trees of 16 behind 4k, 8 KV heads, shared out and not: 1 sequence 18.2 and 31.0 us, 4 31.2 and
+    // 33.6; behind 1268, 4 28.6 and 25.9, 8 36.8 and 27.2).
+    const long long whole = (long long)blocks * p.H_kv;
+    if (4 * whole <= p.grid || (2 * whole <= p.grid && parts >= 8))
         return magicdec_host::launch_pdl(tree_attn_pre_join_kernel<RT, 8>, dim3(blocks, (unsigned)p.H_kv, D / 8),
                                          dim3(kTjThreads), 0, st, p, D);
     return magicdec_host::launch_pdl(tree_attn_pre_join_kernel<RT, 1>, dim3(blocks, (unsigned)p.H_kv), dim3(kTjThreads), 0,
@@ -1424,13 +1428,17 @@ magicdec_status launch_prefix_attn(const magicdec_paged_shape &s, int P, int pma
     p.rr = z.rr;
     p.own_rt = z.own_rt;
     p.own_blocks = z.own_blocks;
+    // A row's parts of its prefix, about: where prefixes and own slots are as long as they can be.
+    const long long blocks = (rows + z.RT * p.NB - 1) / (z.RT * p.NB), list = ((tiles(pmax) + kTrEntry) * (blocks > P ? blocks : P) +
+                             (tiles(s.max_pages) + kTrEntry) * z.own_blocks * z.own) * s.H_kv, run = (list + p.grid - 1) / p.grid;
+    const long long parts = tiles(pmax) / (run > kTrLeast ? run : kTrLeast) + 1;
     CUtensorMap tmq, tmk, tmv, tmg;
     if (!set_maps(p, s, q, kp, vp, &tmq, &tmk, &tmv, &tmg)) return MAGICDEC_ERR_CUDA;
     if (s.d == 128)
-        return z.RT == 1 ? launch_prefix_t<128, 1>(tmq, tmk, tmv, tmg, p, q, kp, st)
-                         : launch_prefix_t<128, 2>(tmq, tmk, tmv, tmg, p, q, kp, st);
-    return z.RT == 1 ? launch_prefix_t<64, 1>(tmq, tmk, tmv, tmg, p, q, kp, st)
-                     : launch_prefix_t<64, 2>(tmq, tmk, tmv, tmg, p, q, kp, st);
+        return z.RT == 1 ? launch_prefix_t<128, 1>(tmq, tmk, tmv, tmg, p, q, kp, (int)parts, st)
+                         : launch_prefix_t<128, 2>(tmq, tmk, tmv, tmg, p, q, kp, (int)parts, st);
+    return z.RT == 1 ? launch_prefix_t<64, 1>(tmq, tmk, tmv, tmg, p, q, kp, (int)parts, st)
+                     : launch_prefix_t<64, 2>(tmq, tmk, tmv, tmg, p, q, kp, (int)parts, st);
 }
 
 }  // namespace magicdec

@@ -83,6 +83,11 @@ CASES = [
     # long enough that a prefix is cut over many CTAs
     (8, 2, 128, 1, [20000], None, [100, 50, 7], 16, None, None),
     (8, 2, 128, 3, [9000], None, [100] * 50, 64, "random", None),
+    # few rows, each in many parts: clusters that share them, and own slots in the list
+    (16, 1, 128, 1, [16000], None, [10, 300, 0], 16, None, None),
+    (16, 1, 64, 2, [9000, 7000], [0, 1, 2], [10, 3], 64, "chain", None),
+    (5, 1, 128, 1, [12000], None, [33], 16, None, None),
+    (16, 1, 128, 5, [6000], None, [10, 65], 16, "random", None),
     # groups: empty ones, of one sequence, sequences in none, prefixes of no length
     (8, 2, 128, 2, [300, 500, 77], [0, 2, 2, 5], [10, 20, 0, 40, 50], 16, "random", None),
     (8, 2, 64, 3, [300, 0, 77, 1200], [1, 3, 4, 4, 6], [10, 20, 0, 40, 50, 300, 8, 9], 16, "forest", None),
