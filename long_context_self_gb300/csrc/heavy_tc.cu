@@ -10,8 +10,10 @@
 // of 16 rows, which bounded 9 rows and more (16 sequences of up to 12,001, R = 25: 166 us by them, 127
 // so, 3.2 TB/s).
 //
-// A row's weight needs the softmax's final maximum and sum: a second pass over K, out of L2, computes
-// the scores again.  CTAs, clusters and exchange as in heavy.cu, two CTAs an SM.
+// A row's weight needs the softmax's final maximum and sum.  TMEM keeps the scores of the last 6 or 14 tiles
+// (32 or 16 query rows) until then; those of earlier ones are computed again, by a second pass over their
+// K, out of L2.  CTAs, clusters and exchange as in heavy.cu, two CTAs an SM.  85 sequences of 1721 rows, 8
+// heads, R = 12: 140 us, with all scores computed again 153.
 // Roles: warp 0 issues the TMA boxes, warp 1 the products, warps 2 to 5 are the softmax.
 // Every wait is bounded; after one that gave up (error 1) the roles run on without waiting.
 #include <climits>
@@ -33,6 +35,9 @@ struct HtShape {
     static constexpr int SLOTS = 4 / HV;                         // of the ring: K and V of a tile or of two
     static constexpr int P = kHtKeys * 128, Q = HV * NR * 128;   // a key's probabilities: 128 bytes, 2 NR of them used
     static constexpr int BYTES = SLOTS * SLOT + P + Q;
+    // TMEM: scores of as many tiles as half of it holds beside O (two CTAs an SM).
+    static constexpr int COLS = 256, S = NR == 32 ? 6 : 14;
+    static_assert((S + 1) * NR <= COLS, "scores and O");
     static_assert(NR * D * 4 <= P, "O takes the probabilities' place");
 };
 
@@ -56,15 +61,36 @@ __device__ __forceinline__ void ht_load(uint32_t at, uint32_t (&x)[NR]) {
     else tmem_ld16(at, x);
 }
 
+// NR values of every lane, each put together over the lanes: lane r ends with value r's, by NR - 1
+// exchanges (and NR more where half a warp has a value) instead of 5 NR.
+template <int NR, class F>
+__device__ __forceinline__ float ht_rows(const uint32_t (&x)[NR], int lane, F put) {
+    float y[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        y[r] = __uint_as_float(x[r]);
+        if (NR == 16) y[r] = put(y[r], __shfl_xor_sync(0xffffffffu, y[r], 16));
+    }
+#pragma unroll
+    for (int w = NR / 2; w >= 1; w >>= 1)
+#pragma unroll
+        for (int i = 0; i < w; ++i) {
+            const bool up = lane & w;
+            const float mine = up ? y[i + w] : y[i], give = up ? y[i] : y[i + w];
+            y[i] = put(mine, __shfl_xor_sync(0xffffffffu, give, w));
+        }
+    return y[0];
+}
+
 template <int D, int NR>
 __global__ void __launch_bounds__(kHtThreads, 2)
     heavy_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const HeavyParams p) {
     using L = HtShape<D, NR>;
     constexpr int HV = L::HV, SLOT = L::SLOT, SLOTS = L::SLOTS, KS = D / 16, QHALF = NR * 128;
-    constexpr uint32_t COLS = 128, O_COL = 2 * NR;       // TMEM columns: two S, then O
+    constexpr uint32_t COLS = L::COLS, NS = L::S, O_COL = NS * NR;       // TMEM columns: S of NS tiles, then O
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *ring = smem, *pbuf = smem + SLOTS * SLOT, *qs = pbuf + L::P;
-    __shared__ uint64_t full[SLOTS], empty[SLOTS], s_full[2], s_free[2], p_full, o_done;
+    __shared__ uint64_t full[SLOTS], empty[SLOTS], s_full[NS], s_free[NS], p_full, o_done;
     __shared__ __align__(16) float held[NR];             // the value that a row's scores are taken from
     __shared__ __align__(16) float moved[NR];            // what its sums are scaled by when that moves
     __shared__ float wmax[4][NR];
@@ -82,7 +108,7 @@ __global__ void __launch_bounds__(kHtThreads, 2)
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        for (int s = 0; s < 2; ++s) {
+        for (uint32_t s = 0; s < NS; ++s) {
             mbar_init(&s_full[s], 1);
             mbar_init(&s_free[s], 4);
         }
@@ -118,6 +144,7 @@ __global__ void __launch_bounds__(kHtThreads, 2)
     const int per = ((len + (int)C - 1) / (int)C + kHtKeys - 1) / kHtKeys * kHtKeys;
     const int k0 = (int)min((long long)len, (long long)rank * per), k1 = (int)min((long long)len, (long long)k0 + per);
     const int tiles = (k1 - k0 + kHtKeys - 1) / kHtKeys;
+    const int again = max(0, tiles - (int)NS);           // tiles whose scores are computed twice
     const long long row0 = ((long long)b * p.H_kv + h) * p.cap;
     const int own = len - p.n;                           // the first of the tokens' own rows
     bool ok = smem_u32(smem) % 1024 == 0;
@@ -130,7 +157,7 @@ __global__ void __launch_bounds__(kHtThreads, 2)
     // A warp's role ends its first pass, all meet where the cluster exchanges, then the second.
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
-        // Slots in order: K and V of every tile, then K again.
+        // Slots in order: K and V of every tile, then K again of the first ones.
         const uint64_t once = policy_evict_first(), keep = policy_evict_normal();
         auto produce = [&](int from, int to) {
             for (int s = from; ok && s < to; ++s) {
@@ -146,14 +173,14 @@ __global__ void __launch_bounds__(kHtThreads, 2)
             }
         };
         // What the second pass has a place for does not wait for the exchange.
-        const int ahead = 2 * tiles + min(tiles, SLOTS);
+        const int ahead = 2 * tiles + min(again, SLOTS), last = 2 * tiles + again;
         if (lane == 0) produce(0, ahead);
         __syncwarp();
         if (C > 1) few_cluster_sync();
         if (lane == 0) {
-            produce(ahead, 3 * tiles);
+            produce(ahead, last);
             // No copy may be in flight when the CTA ends.
-            for (int s = max(0, 3 * tiles - SLOTS); s < 3 * tiles; ++s)
+            for (int s = max(0, last - SLOTS); s < last; ++s)
                 mbar_poll(&full[s % SLOTS], (uint32_t)s / SLOTS & 1, p.err);
         }
         __syncwarp();
@@ -169,9 +196,9 @@ __global__ void __launch_bounds__(kHtThreads, 2)
         };
         uint32_t made = 0;                               // S so far, in both passes
         auto scores = [&](int slot) {
-            const uint32_t st = (uint32_t)slot % SLOTS, buf = made & 1;
+            const uint32_t st = (uint32_t)slot % SLOTS, buf = made % NS;
             wait(&full[st], (uint32_t)slot / SLOTS & 1);
-            if (made >= 2) wait(&s_free[buf], (made / 2 - 1) & 1);
+            if (made >= NS) wait(&s_free[buf], (made / NS - 1) & 1);
             tc_fence_after();
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
@@ -201,9 +228,9 @@ __global__ void __launch_bounds__(kHtThreads, 2)
         __syncwarp();
         if (C > 1) few_cluster_sync();
         if (one) {
-            for (int t = 0; t < tiles; ++t) scores(2 * tiles + t);
+            for (int t = 0; t < again; ++t) scores(2 * tiles + t);
             // The products in flight end before the shared memory and TMEM that they use go.
-            for (uint32_t x = made > 1 ? made - 2 : 0; x < made; ++x) wait(&s_full[x & 1], x / 2 & 1);
+            if (made) wait(&s_full[(made - 1) % NS], (made - 1) / NS & 1);
         }
         __syncwarp();
     } else {
@@ -216,13 +243,16 @@ __global__ void __launch_bounds__(kHtThreads, 2)
         uint32_t used = 0;                               // S so far
         // The scores of this thread's key, and from which query row on they count: a token's own row
         // is seen by it and later ones.
-        auto take = [&](uint32_t (&x)[NR]) {
-            ok = few_wait(&s_full[used & 1], used / 2 & 1, p.err, ok, lane);
+        auto get = [&](uint32_t at, bool last, uint32_t (&x)[NR]) {
             tc_fence_after();
-            ht_load<NR>(ts + (used & 1) * NR, x);
+            ht_load<NR>(ts + at * NR, x);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s_free[used & 1]);
+            if (last && lane == 0) mbar_arrive(&s_free[at]);
+        };
+        auto take = [&](bool last, uint32_t (&x)[NR]) {
+            ok = few_wait(&s_full[used % NS], used / NS & 1, p.err, ok, lane);
+            get(used % NS, last, x);
             ++used;
         };
         auto from_row = [&](int key) { return key >= k1 ? NR : key < own ? 0 : min((key - own) * p.G, NR); };
@@ -230,7 +260,7 @@ __global__ void __launch_bounds__(kHtThreads, 2)
             const int key = k0 + t * kHtKeys + row;
             const bool edge = k0 + (t + 1) * kHtKeys > min(own + 1, k1);     // alike in all threads
             uint32_t x[NR];
-            take(x);
+            take(t < again, x);
             const int lo = edge ? from_row(key) : 0;
             bool move = false;
 #pragma unroll
@@ -248,11 +278,8 @@ __global__ void __launch_bounds__(kHtThreads, 2)
             if (ht_any(move)) {
                 // Maxima move, and what has been summed is scaled, only where a score is above by more than
                 // 2^kFewLazy: weights up to 2^24 instead of 1 cost a floating sum nothing.
-#pragma unroll
-                for (int r = 0; r < NR; ++r) {
-                    const float y = warp_max(__uint_as_float(x[r]));
-                    if (lane == 0) wmax[quad][r] = y;
-                }
+                const float y = ht_rows<NR>(x, lane, [](float a, float b) { return fmaxf(a, b); });
+                if (lane < NR) wmax[quad][lane] = y;
                 named_bar_sync(2, 128);
                 if (row < NR) {
                     const float was = held[row], y = fmaxf(fmaxf(wmax[0][row], wmax[1][row]), fmaxf(wmax[2][row], wmax[3][row]));
@@ -302,15 +329,17 @@ __global__ void __launch_bounds__(kHtThreads, 2)
                 // tokens' own rows, which earlier ones must not see, are taken out and added at the end.
                 const uint32_t slot = 2 * t + 1, st = slot % SLOTS;
                 ok = few_wait(&full[st], slot / SLOTS & 1, p.err, ok, lane);
-                if (key >= k1 || (p.n > 1 && key >= own)) {
-#pragma unroll 1
+                auto word = [&](int c) {
+                    return reinterpret_cast<uint4 *>(ring + st * SLOT + (c >> 3) * kHtHalf + swz128(row, c & 7));
+                };
+                if (key >= k1) {
+#pragma unroll
+                    for (int c = 0; c < HV * 8; ++c) *word(c) = make_uint4(0, 0, 0, 0);
+                } else if (p.n > 1 && key >= own) {
+#pragma unroll 4
                     for (int c = 0; c < HV * 8; ++c) {
-                        uint4 *at = reinterpret_cast<uint4 *>(ring + st * SLOT + (c >> 3) * kHtHalf + swz128(row, c & 7));
-                        if (key >= k1) {
-                            *at = make_uint4(0, 0, 0, 0);
-                            continue;
-                        }
-                        uint4 y = *at;
+                        uint4 *at = word(c);
+                        const uint4 y = *at;
                         const uint4 odd = make_uint4(few_odd_bits(y.x), few_odd_bits(y.y), few_odd_bits(y.z), few_odd_bits(y.w));
                         if (odd.x | odd.y | odd.z | odd.w) {
                             met = 1;
@@ -324,20 +353,12 @@ __global__ void __launch_bounds__(kHtThreads, 2)
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full);
         }
-        // The sums over the keys: lane r of a warp ends with row r's.
-        if (NR == 16) {
+        // The sums over the keys.
+        uint32_t sums[NR];
 #pragma unroll
-            for (int r = 0; r < NR; ++r) l[r] += __shfl_xor_sync(0xffffffffu, l[r], 16);
-        }
-#pragma unroll
-        for (int w = NR / 2; w >= 1; w >>= 1)
-#pragma unroll
-            for (int i = 0; i < w; ++i) {
-                const bool up = lane & w;
-                const float mine = up ? l[i + w] : l[i], give = up ? l[i] : l[i + w];
-                l[i] = mine + __shfl_xor_sync(0xffffffffu, give, w);
-            }
-        if (lane < NR) wsum[quad][lane] = l[0];
+        for (int r = 0; r < NR; ++r) sums[r] = __float_as_uint(l[r]);
+        const float sum_r = ht_rows<NR>(sums, lane, [](float a, float b) { return a + b; });
+        if (lane < NR) wsum[quad][lane] = sum_r;
         named_bar_sync(2, 128);
         if (row < NR) cstat[row] = make_float2(held[row], wsum[0][row] + wsum[1][row] + wsum[2][row] + wsum[3][row]);
         if (C > 1) few_cluster_sync();
@@ -372,23 +393,28 @@ __global__ void __launch_bounds__(kHtThreads, 2)
             for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4 *>(f + i) = *reinterpret_cast<const float4 *>(moved + c + i);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                float y = f[i] == 0.f ? 0.f : __uint_as_float(o[i]) * f[i];
-                if (odd && real)
-                    for (int j = max(own, k0); j < k1; ++j) {
-                        const uint32_t z = (uint32_t)__ldcg(p.v + (row0 + j) * D + chan) << 16;
-                        if ((z & 0x7f800000u) == 0x7f800000u && c + i >= (j - own) * p.G) y += __uint_as_float(z);
-                    }
+                const float y = f[i] == 0.f ? 0.f : __uint_as_float(o[i]) * f[i];
                 if (real && c + i < p.R) osum[(c + i) * D + chan] = y;
             }
             __syncwarp();                                // TMEM is read by whole warps
         }
-        // The second pass: every row's weight, summed over the query rows in their order.
+        if (odd && real)
+            for (int j = max(own, k0); j < k1; ++j) {
+                const uint32_t z = (uint32_t)__ldcg(p.v + (row0 + j) * D + chan) << 16;
+                if ((z & 0x7f800000u) == 0x7f800000u)
+                    for (int r = max(0, j - own) * p.G; r < p.R; ++r) osum[r * D + chan] += __uint_as_float(z);
+            }
+        // Every row's weight, summed over the query rows in their order: of the last tiles from the scores that
+        // are there still, then of the first ones, whose scores are computed again.
         const int first_new = p.next_pos ? own : INT_MAX;
-        for (int t = 0; t < tiles; ++t) {
+        for (int i = 0; i < tiles; ++i) {
+            const bool there = i < tiles - again;
+            const int t = there ? again + i : i - (tiles - again);
             const int key = k0 + t * kHtKeys + row;
             const float old = key < k1 && key < first_new ? __ldcg(p.weight + row0 + key) : 0.f;
             uint32_t x[NR];
-            take(x);
+            if (there) get((uint32_t)t % NS, true, x);
+            else take(true, x);
             const int lo = from_row(key);
             float w = 0.f;
 #pragma unroll
@@ -411,16 +437,29 @@ __global__ void __launch_bounds__(kHtThreads, 2)
         tc_fence_after();
         tmem_dealloc(tmem, COLS);
     }
+    // Several words of a thread side by side.
+    constexpr int WORDS = (NR * (D / 4) + kHtThreads - 1) / kHtThreads;
     const int vecs = p.R * (D / 4), share = (vecs + (int)C - 1) / (int)C;
-    for (int i = (int)rank * share + tid; i < min(vecs, (int)(rank + 1) * share); i += kHtThreads) {
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (uint32_t c = 0; c < C; ++c) {
-            const float4 x = few_ld4(few_at(pbuf, c) + (uint32_t)i * 16);
-            s = make_float4(s.x + x.x, s.y + x.y, s.z + x.z, s.w + x.w);
+    const int from = (int)rank * share + tid, end = min(vecs, (int)(rank + 1) * share);
+    float4 s[WORDS];
+#pragma unroll
+    for (int x = 0; x < WORDS; ++x) s[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (uint32_t c = 0; c < C; ++c) {
+        const uint32_t at = few_at(pbuf, c);
+#pragma unroll
+        for (int x = 0; x < WORDS; ++x) {
+            const int i = from + x * kHtThreads;
+            if (i >= end) continue;
+            const float4 y = few_ld4(at + (uint32_t)i * 16);
+            s[x] = make_float4(s[x].x + y.x, s[x].y + y.y, s[x].z + y.z, s[x].w + y.w);
         }
-        const int r = i / (D / 4), c4 = i - r * (D / 4), t = r / p.G;
-        *reinterpret_cast<uint2 *>(p.out + (((long long)b * p.n + t) * p.H_q + h * p.G + (r - t * p.G)) * D + c4 * 4) =
-            make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+    }
+#pragma unroll
+    for (int x = 0; x < WORDS; ++x) {
+        const int i = from + x * kHtThreads, r = i / (D / 4), c4 = i % (D / 4), t = r / p.G;
+        if (i < end)
+            *reinterpret_cast<uint2 *>(p.out + (((long long)b * p.n + t) * p.H_q + h * p.G + (r - t * p.G)) * D + c4 * 4) =
+                make_uint2(pack_bf16(s[x].x, s[x].y), pack_bf16(s[x].z, s[x].w));
     }
     if (C > 1) few_cluster_sync();                       // no CTA ends while another reads its O
 }
