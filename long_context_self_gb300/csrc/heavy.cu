@@ -546,27 +546,32 @@ __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictPara
             bound = __reduce_min_sync(0xffffffffu, rest);
             if (lane == __ffs(__ballot_sync(0xffffffffu, rest == bound)) - 1) rest = ~0u;
         }
-        int found = 0;
         const bool alike = __popc(__ballot_sync(0xffffffffu, low == bound)) > kEvTake;   // rather many rows are
-        if (alike) found = 33;
-        for (int j0 = 0; !alike && j0 < len; j0 += 128) {
-            const int j = j0 + 4 * lane;
-            const uint4 x = j < len ? *reinterpret_cast<const uint4 *>(kept + j) : make_uint4(~0u, ~0u, ~0u, ~0u);
-            if (!__any_sync(0xffffffffu, min(min(x.x, x.y), min(x.z, x.w)) <= bound)) continue;
-            const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+        // Lists the rows whose keys lie at or below a limit, the first 32; returns how many there are.
+        auto collect = [&](uint32_t limit) {
+            int found = 0;
+            for (int j0 = 0; j0 < len; j0 += 128) {
+                const int j = j0 + 4 * lane;
+                const uint4 x = j < len ? *reinterpret_cast<const uint4 *>(kept + j) : make_uint4(~0u, ~0u, ~0u, ~0u);
+                if (!__any_sync(0xffffffffu, min(min(x.x, x.y), min(x.z, x.w)) <= limit)) continue;
+                const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const bool in = j + k < len && y[k] <= bound;
-                const unsigned m = __ballot_sync(0xffffffffu, in);
-                const int to = found + __popc(m & ((1u << lane) - 1u));
-                if (in && to < 32) src[to] = j + k;
-                found += __popc(m);
+                for (int k = 0; k < 4; ++k) {
+                    const bool in = j + k < len && y[k] <= limit;
+                    const unsigned m = __ballot_sync(0xffffffffu, in);
+                    const int to = found + __popc(m & ((1u << lane) - 1u));
+                    if (in && to < 32) src[to] = j + k;
+                    found += __popc(m);
+                }
             }
-        }
-        __syncwarp();
-        if (found <= 32) {
+            __syncwarp();
+            return found;
+        };
+        int found = alike ? 33 : collect(bound), row = -1;
+        bool go = false, known = found <= 32;
+        if (known) {
             const bool in = lane < found;
-            const int row = in ? src[lane] : -1;
+            row = in ? src[lane] : -1;
             const uint32_t x = in ? kept[row] : ~0u;
             const unsigned same = __match_any_sync(0xffffffffu, x);
             uint32_t y = 0;                                  // positions only where weights are alike
@@ -577,7 +582,69 @@ __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictPara
                 const int row2 = __shfl_sync(0xffffffffu, row, k);
                 rank += x2 < x || (x2 == x && (y2 < y || (y2 == y && row2 > row)));
             }
-            const bool go = in && rank < E, hole = go && row < p.budget;
+            go = in && rank < E;
+        } else if (bound > 0 && bound < ev_key(INFINITY) && (found = collect(bound - 1)) < E) {
+            // Fewer than E lie below the bound, so that it is the E-th least key, which many rows have: those
+            // with the largest positions go, taken one after another, of equal ones the highest row.
+            // Positions take the keys' place, 0 that of other rows'; such a row is not protected, so
+            // that its position is not negative.
+            uint32_t best = 0;                               // of this thread's rows
+            int at = -1;
+            for (int j0 = 4 * lane; j0 < len; j0 += 16 * T) {
+                uint4 w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int j = j0 + k * 4 * T;
+                    if (j + 3 < len && p.wide) w[k] = ld_dep_u4(reinterpret_cast<const uint4 *>(pos + j));
+                    else if (j < len)
+                        w[k] = make_uint4(ld_dep(pos + j), j + 1 < len ? ld_dep(pos + j + 1) : 0,
+                                          j + 2 < len ? ld_dep(pos + j + 2) : 0, j + 3 < len ? ld_dep(pos + j + 3) : 0);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int j = j0 + k * 4 * T;
+                    if (j >= len) break;
+                    const uint4 x = *reinterpret_cast<const uint4 *>(kept + j);
+                    uint32_t y[4] = {x.x, x.y, x.z, x.w};
+                    const uint32_t v[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        y[e] = y[e] == bound ? v[e] | 0x80000000u : 0u;
+                        if (y[e] && y[e] >= best) {
+                            best = y[e];
+                            at = j + e;
+                        }
+                    }
+                    *reinterpret_cast<uint4 *>(kept + j) = make_uint4(y[0], y[1], y[2], y[3]);
+                }
+            }
+            for (; found < E; ++found) {
+                const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+                const int last = __reduce_max_sync(0xffffffffu, best == top ? at : -1);
+                if (lane == 0) src[found] = last;
+                if (at == last) {
+                    kept[last] = 0;
+                    best = 0;
+                    at = -1;
+                    for (int j = 4 * lane; j < len; j += 4 * T) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(kept + j);
+                        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (y[e] && y[e] >= best) {
+                                best = y[e];
+                                at = j + e;
+                            }
+                    }
+                }
+            }
+            __syncwarp();
+            known = true;
+            go = lane < E;
+            row = go ? src[lane] : -1;
+        }
+        if (known) {
+            const bool hole = go && row < p.budget;
             // Of the E rows from the budget on, those that do not go, ascending, into the holes, ascending.
             bool stay = lane < E;
             int before = 0;

@@ -218,6 +218,12 @@ EVICT = [
     # most of the rows go, more moves than are listed at a time
     (1, 2, 2, 128, 4000, [4000, 2100], 2000, 16, 100, "random"),
     (1, 1, 1, 64, 5000, [5000], 3, 1, 1, "few"),
+    # few rows to go, of many that are alike, in their positions too
+    (2, 3, 4, 64, 300, [300, 295, 285], 284, 2, 20, "few"),
+    (1, 2, 8, 64, 1041, [1041, 1035], 1030, 0, 0, "alike"),
+    (1, 2, 8, 64, 1041, [1041, 1035], 1025, 5, 7, "twins"),
+    (1, 2, 8, 64, 1030, [1030, 1029], 1029, 5, 7, "twins"),
+    (1, 3, 2, 128, 77, [77, 70, 64], 61, 0, 9, "twins"),
     # many caches, each of a few rows, of which a few or many go
     (8, 39, 8, 64, 70, [(b * 29) % 72 for b in range(39)], 30, 2, 5, "random"),
     (8, 39, 8, 64, 70, [(b * 29) % 72 for b in range(39)], 20, 0, 0, "few"),
