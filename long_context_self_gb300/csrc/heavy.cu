@@ -25,7 +25,7 @@ namespace magicdec {
 // keys of a stage each through ldmatrix and mma.sync (m16n8k16, the lower half of A empty): at 8 rows
 // the products are a few percent of the time.  128 sequences over 2053 rows, R = 4: 181 to 183 us,
 // 6.0 TB/s; with keys straight from global memory into the fragments, which left too few bytes
-// under way, 207; on tcgen05, with the scores computed again, 246.
+// under way, 207; on tcgen05 223.
 constexpr int kHvKeys = 64;          // keys of a stage
 constexpr int kHvHalf = kHvKeys * 128;   // bytes of 64 channels of them
 constexpr int kHvStages = 8;         // stages of a ring at most
@@ -371,7 +371,7 @@ magicdec_status launch_heavy_attn(int B, int H_q, int H_kv, int D, int cap, int 
     p.scale_log2 = kLog2e / sqrtf((float)D);
     // Clusters of 1 to 8 whose scores fit, by the time they should take.  128 sequences of 2053 rows, 8
     // heads, R = 4, clusters of 1, 2, 4 and 8: 184, 195, 216 and 331 us; 16 of up to 12,001 in
-    // clusters of 8, R = 5: 92 us, and on tcgen05, in clusters of 4, 109.
+    // clusters of 8, R = 5: 90 us, and on tcgen05, in clusters of 4, 103.
     int C = 0;
     double least = 0;
     for (int c = 1; p.R <= kHvRows && c <= 8; c *= 2) {

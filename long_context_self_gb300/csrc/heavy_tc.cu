@@ -7,8 +7,8 @@
 // inside one thread, and the running maxima need no shuffles (they are held at values that a score
 // may exceed by 2^24 before any is moved).  O^T += V^T P^T (d channels x NR) takes V as it lies
 // and P from shared memory, 64 bytes a key.  A quarter of the instructions of mma.sync tiles
-// of 16 rows, which bounded 9 rows and more (16 sequences of up to 12,001, R = 25: 166 us by them, 127
-// so, 3.2 TB/s).
+// of 16 rows, which bounded 9 rows and more (16 sequences of up to 12,001, R = 25: 166 us by them, 118
+// so, 3.5 TB/s).
 //
 // A row's weight needs the softmax's final maximum and sum.  TMEM keeps the scores of the last 6 or 14 tiles
 // (32 or 16 query rows) until then; those of earlier ones are computed again, by a second pass over their
@@ -489,7 +489,7 @@ static magicdec_status launch_ht_t(const CUtensorMap &tmk, const CUtensorMap &tm
 
 magicdec_status launch_heavy_tc(const HeavyParams &p, int D, const uint16_t *k, const uint16_t *v, cudaStream_t st) {
     // Clusters of 1 to 8, by the time they should take.  16 sequences of up to 12,001 rows, 8 heads,
-    // R = 25, clusters of 1, 2, 4 and 8: 257, 149, 127 and 132 us; 64 of 2053, R = 4: 87, 90, 115 and 184.
+    // R = 25, clusters of 1, 2, 4 and 8: 254, 144, 119 and 119 us; 128 of 1029: 138, 153, 220 and 350.
     int best = 1;
     double least = 0;
     for (int C = 1; C <= 8; C *= 2) {
