@@ -120,9 +120,11 @@ __global__ void __launch_bounds__(kHtThreads, 2)
         met = 0;
     }
     if (tid < NR) held[tid] = -INFINITY;
-    if (warp == 1) tmem_alloc(&tmem_slot, COLS);
     pdl_trigger();
     pdl_wait();
+    // TMEM is taken when the kernels before are done: one of them may be about to take its own on this
+    // SM, and would wait for this CTA, which waits for it.
+    if (warp == 1) tmem_alloc(&tmem_slot, COLS);
     // The query rows (row i * G + g: token i, head g of the group), K-major and swizzled.
     constexpr int QV = (NR * (D / 8) + kHtThreads - 1) / kHtThreads;     // 16-byte words a thread has
     uint4 qv[QV];

@@ -296,6 +296,35 @@ def test_steps_follow_the_64_bit_cache():
             assert (weight[b, :, :ln].double() - shadow[2][b, :, :ln]).abs().max() < 1e-4
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_right_behind_a_selection(d):
+    """Kernels of a selection and of the attention that hold tensor memory, many in a row, each let go before the
+    one in front has ended: they wait for one another in one order only."""
+    B, n, H_q, H_kv, cap, w = 2, 8, 8, 2, 300, 32
+    lens = i32([300, 77])
+    kc, vc, weight, pos = cache(B, H_kv, cap, d, [300, 77], 91)
+    q, q_win, k = randn((B, n, H_q, d), 92), randn((B, w, H_q, d), 93), randn((B, 2000, H_kv, d), 94)
+    long = i32([2000, 1500])
+    want = mb.magicdec_heavy_attn(q, kc, vc, weight.clone(), lens)
+    idx, _ = mb.magicdec_snapkv_select(q_win, k, long, w, 5, 128)
+    torch.cuda.synchronize()
+    w0, got = weight.clone(), [torch.empty_like(q) for _ in range(20)]
+    ws = torch.empty(mb.magicdec_snapkv_workspace_size(mb.kv_shape(B, H_q, H_kv, d, 2000), w), dtype=torch.uint8, device=DEV)
+    idx2, n_sel = torch.empty_like(idx), torch.empty((B,), dtype=I32, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for out in got:
+            mb.magicdec_snapkv_select(q_win, k, long, w, 5, 128, idx=idx2, n_sel=n_sel, ws=ws)
+            mb.magicdec_heavy_attn(q, kc, vc, w0, lens, out=out)
+    for _ in range(3):
+        for out in got:
+            out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(idx2, idx)
+        assert all(torch.equal(out, want) for out in got)
+
+
 def test_calls_on_a_stream_and_in_a_graph():
     """On a stream of their own, and captured and replayed beside another graph's calls."""
     B, H_q, H_kv, d, cap, budget = 4, 8, 2, 128, 300, 250
