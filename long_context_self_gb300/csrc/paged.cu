@@ -163,9 +163,9 @@ __device__ __forceinline__ void norm_head(Head16 &h, const Head16 &w, float eps,
 // lane's 16 squares and log2(LR) shuffles a row.  That is twice the instructions, and a row's chain is
 // longer, so what counts is how many CTAs fit: two passes under way instead of three, the next
 // loaded as soon as one is taken, the weights in shared memory, fp32 arithmetic by pairs, 80 registers
-// (MINB = 12 CTAs of 64 threads an SM).  128 trees of 32 with inputs from HBM: 27.8 us, with three
+// (MINB: 12 CTAs of 64 threads an SM).  128 trees of 32 with inputs from HBM: 27.8 us, with three
 // passes 31, one by one and in single fp32 34; 32,000 prompt tokens of 48 rows 140, 163 and 174 us.
-template <int NT, int LR, bool INTER, bool NORM, int MINB = NT == 64 ? 12 : 3>
+template <int NT, int LR, bool INTER, bool NORM, int MINB = NT == 32 ? 24 : NT == 64 ? 12 : 3>
 __global__ void __launch_bounds__(NT, NORM ? MINB : 0) paged_append_kernel(const AppendParams p) {
     constexpr int ROWS = NT / LR;               // rows of a pass
     constexpr int AHEAD = NORM ? 2 : 3;         // passes under way
@@ -296,8 +296,9 @@ __global__ void __launch_bounds__(NT, NORM ? MINB : 0) paged_append_kernel(const
 
 template <int NT, int LR>
 static magicdec_status launch_append_t(const AppendParams &p, int interleaved, bool norm, cudaStream_t st) {
-    auto kern = norm ? (interleaved ? paged_append_kernel<NT, LR, true, true> : paged_append_kernel<NT, LR, false, true>)
-                     : (interleaved ? paged_append_kernel<NT, LR, true, false> : paged_append_kernel<NT, LR, false, false>);
+    auto kern = interleaved ? paged_append_kernel<NT, LR, true, true> : paged_append_kernel<NT, LR, false, true>;
+    if constexpr (NT > 32)
+        if (!norm) kern = interleaved ? paged_append_kernel<NT, LR, true, false> : paged_append_kernel<NT, LR, false, false>;
     return magicdec_host::launch_pdl(kern, dim3((unsigned)p.n, (unsigned)p.B), dim3(NT), 0, st, p);
 }
 
@@ -313,7 +314,15 @@ static magicdec_status launch_append(AppendParams &p, const magicdec_paged_shape
     p.max_pages = s.max_pages;
     // Larger CTAs while there are fewer tokens than SMs: then a token's own rows take longest (one
     // token of 48 rows: 2.7 us with 256 threads, 3.5 us with 64).
-    if ((long long)s.B * p.n >= magicdec_host::sm_count())
+    const long long tokens = (long long)s.B * p.n;
+    // Normed, a warp a token where there are more tokens than CTAs of 64 threads have places, and a token's rows
+    // are few: with twice the tokens under way their first loads are covered better (15,000 tokens of 20 rows of
+    // 128 channels 53.5 and 45.5 us, of 64 41.5 and 29.1; 3000 of 36 rows 18.2 and 16.8; 4096 of 48 29.1 and 30.1,
+    // 600 of 20 7.4 and 8.8).
+    if (norm && tokens > 12ll * magicdec_host::sm_count() && ((p.q_out ? s.H_q : 0) + 2 * s.H_kv) * (s.d / 16) < 384)
+        return s.d == 128 ? launch_append_t<32, 8>(p, interleaved, norm, st)
+                          : launch_append_t<32, 4>(p, interleaved, norm, st);
+    if (tokens >= magicdec_host::sm_count())
         return s.d == 128 ? launch_append_t<64, 8>(p, interleaved, norm, st)
                           : launch_append_t<64, 4>(p, interleaved, norm, st);
     return s.d == 128 ? launch_append_t<256, 8>(p, interleaved, norm, st)

@@ -61,6 +61,11 @@ CASES = [
     (28, 4, 128, 128, False, 300, [5, 100], 16, None, None, 3, "qk"),
     (28, 4, 128, 96, False, 40, [5, 100], 16, None, None, 3, ""),
     (7, 7, 64, 32, True, 3, [1, 2, 3], 16, None, None, 5, "k"),
+    # many tokens of few rows
+    (15, 5, 128, 128, False, 700, [5, 0, 100, 7], 16, None, [700, 3, 0, 699], 3, "qk"),
+    (16, 1, 64, 64, True, 700, [5, 0, 100], 48, None, None, 0, "q"),
+    (8, 2, 128, 64, True, 200, [5, 100, 17, 0, 1, 2, 3, 4, 5, 6], 64, "random", None, 0, "qk"),
+    (3, 3, 64, 64, False, 1000, [5, 1], 1, None, None, 1, "k"),
 ]
 
 
