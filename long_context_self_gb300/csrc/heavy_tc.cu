@@ -32,7 +32,9 @@ constexpr int kHtThreads = 192;
 template <int D, int NR>
 struct HtShape {
     static constexpr int HV = D / 64, SLOT = HV * kHtHalf;
-    static constexpr int SLOTS = 4 / HV;                         // of the ring: K and V of a tile or of two
+    // Of the ring: K and V of a tile, or of two and a half (16 sequences of 12,001 rows, d = 64, R = 25: 110.5 us, with
+    // two 112.4), as two CTAs an SM leave room for.
+    static constexpr int SLOTS = HV == 1 ? 5 : 2;
     static constexpr int P = kHtKeys * 128, Q = HV * NR * 128;   // a key's probabilities: 128 bytes, 2 NR of them used
     static constexpr int BYTES = SLOTS * SLOT + P + Q;
     // TMEM: scores of as many tiles as half of it holds beside O (two CTAs an SM).
