@@ -122,11 +122,14 @@ __global__ void __launch_bounds__(kHtThreads, 2)
         met = 0;
     }
     if (tid < NR) held[tid] = -INFINITY;
-    pdl_trigger();
+    // TMEM is taken before the wait (behind it, 16 sequences of up to 12,001 rows took 120 us, so 114), and the kernels
+    // behind are let go afterwards.  Every kernel that takes any lets its followers go only then, or leaves them
+    // no room on the SM, so that none in front can be waiting for what this CTA holds while it waits for that one.
+    if (warp == 1) {
+        tmem_alloc(&tmem_slot, COLS);
+        pdl_trigger();
+    }
     pdl_wait();
-    // TMEM is taken when the kernels before are done: one of them may be about to take its own on this
-    // SM, and would wait for this CTA, which waits for it.
-    if (warp == 1) tmem_alloc(&tmem_slot, COLS);
     // The query rows (row i * G + g: token i, head g of the group), K-major and swizzled.
     constexpr int QV = (NR * (D / 8) + kHtThreads - 1) / kHtThreads;     // 16-byte words a thread has
     uint4 qv[QV];

@@ -85,7 +85,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
     const int chunk = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    pdl_trigger();
     pdl_wait();
     const int L = clamp_len_tc(checked(ld_dep(p.len + b), 0, p.L_cap, p.err), p.L_cap);
     if (L < p.w) return;
@@ -113,7 +112,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         prefetch_tensormap(&tmk);
         prefetch_tensormap(&tmq);
     }
-    if (warp == 1) tmem_alloc(tmem_slot, tmem_cols);
+    // The kernels behind are let go when this CTA has its tensor memory: one of them may take its own as
+    // soon as it runs, beside this CTA, and then wait for this one.
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, tmem_cols);
+        pdl_trigger();
+    }
     // Query rows M..QR-1 are padding: zero them (the TMA box writes rows < M).
     {
         const int pad = QR - p.M;
