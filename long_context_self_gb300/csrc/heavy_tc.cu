@@ -422,13 +422,16 @@ __global__ void __launch_bounds__(kHtThreads, 2)
             uint32_t x[NR];
             if (there) get((uint32_t)t % NS, true, x);
             else take(true, x);
+            // A bit for each query row that sees the key.  The columns behind the last row (queries of zero) are left out,
+            // not added as nothing: their scores are NaN where a key is infinite.
             const int lo = from_row(key);
+            const uint32_t sees = lo >= p.R ? 0u : ~0u >> (32 - p.R) & ~0u << lo;
             float w = 0.f;
 #pragma unroll
             for (int r = 0; r < NR; r += 2) {
                 const float4 a = *reinterpret_cast<const float4 *>(&all[r]);
-                if (r >= lo) w = fmaf(fast_exp2(fmaf(__uint_as_float(x[r]), sl, -a.x)), a.y, w);
-                if (r + 1 >= lo) w = fmaf(fast_exp2(fmaf(__uint_as_float(x[r + 1]), sl, -a.z)), a.w, w);
+                if (sees >> r & 1u) w = fmaf(fast_exp2(fmaf(__uint_as_float(x[r]), sl, -a.x)), a.y, w);
+                if (sees >> (r + 1) & 1u) w = fmaf(fast_exp2(fmaf(__uint_as_float(x[r + 1]), sl, -a.z)), a.w, w);
             }
             if (key < k1) {
                 p.weight[row0 + key] = old + w;

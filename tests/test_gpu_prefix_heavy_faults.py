@@ -1,0 +1,80 @@
+"""The normed append, the attention behind shared prefixes and the calls on a heavy-hitter draft cache where values that
+are not finite, sizes or an order of calls could go wrong: each against a plain form."""
+import pytest
+import torch
+
+from heavy_util import heavy_ref
+from long_context_self_gb300 import binding as mb
+from tree_util import gen
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+BF16, I32 = torch.bfloat16, torch.int32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from long_context_self_gb300 import build
+    build.build()
+    mb.lib()
+
+
+@pytest.fixture(autouse=True)
+def _no_device_error():
+    yield
+    assert mb.magicdec_device_error() == 0
+
+
+def i32(x):
+    return None if x is None else torch.tensor(x, dtype=I32, device=DEV)
+
+
+def randn(shape, seed):
+    return torch.randn(shape, generator=gen(seed)).to(BF16).to(DEV)
+
+
+def within(got, ref, tol, what=""):
+    assert torch.isfinite(got).all(), f"{what}: not finite"
+    over = ((got.double() - ref).abs() - tol).max().item()
+    assert over <= 0, f"{what}: off by {over:.3e} more than the bound"
+
+
+def cache(B, H_kv, cap, d, seed):
+    pos = torch.arange(cap, dtype=I32, device=DEV).expand(B, H_kv, cap).contiguous()
+    return (randn((B, H_kv, cap, d), seed), randn((B, H_kv, cap, d), seed + 1),
+            torch.rand((B, H_kv, cap), generator=gen(seed + 2)).to(DEV), pos)
+
+
+# Query rows of a KV head: fewer than the rows of a product and as many, by mma.sync and, with 9 rows and more or
+# stretches whose scores do not fit shared memory, on tcgen05; one CTA and clusters.  (H_q, H_kv, d, n, cap)
+ROWS = [(8, 2, 128, 1, 300), (8, 2, 64, 2, 12001), (12, 2, 128, 2, 300), (10, 2, 64, 5, 300), (32, 2, 64, 1, 300),
+        (8, 1, 128, 1, 60001), (16, 2, 64, 1, 30001), (32, 1, 128, 1, 700), (4, 2, 128, 9, 700)]
+
+
+@pytest.mark.parametrize("H_q,H_kv,d,n,cap", ROWS)
+def test_keys_whose_scores_are_minus_infinity(H_q, H_kv, d, n, cap):
+    """A key of an infinity whose scores are minus infinity for every query row has no part in anything: weights grow
+    by nothing there, and by what the 64-bit form says elsewhere."""
+    B, G = 2, H_q // H_kv
+    kc, vc, weight, pos = cache(B, H_kv, cap, d, 5)
+    lens = [cap, cap - 13]
+    q = randn((B, n, H_q, d), 9)
+    q[..., 3] = -q[..., 3].abs() - 0.25
+    hit = torch.zeros((B, H_kv, cap), dtype=torch.bool, device=DEV)
+    hit[:, :, [0, 7, 100]] = True
+    hit[:, 0, 150:170] = True
+    if n > 1:
+        for b, ln in enumerate(lens):
+            hit[b, :, ln - 1] = True                   # of the last token's own
+    kc[..., 3] = torch.where(hit, float("inf"), kc[..., 3].float()).to(BF16)
+    w0 = weight.clone()
+    got = mb.magicdec_heavy_attn(q, kc, vc, weight, i32(lens), pos=pos, next_pos=i32([cap, cap]))
+    (ref, tol), (w, wt), _ = heavy_ref(q, kc, vc, w0, pos, lens, [cap, cap])
+    within(got, ref, tol, "out")
+    for b, ln in enumerate(lens):
+        within(weight[b, :, :ln], w[b, :, :ln], wt[b, :, :ln], "weight")
+        old = hit[b] & (torch.arange(cap, device=DEV) < ln - n)
+        assert torch.equal(weight[b][old], w0[b][old])
+        if n > 1:
+            assert (weight[b, :, ln - 1] == 0).all()
