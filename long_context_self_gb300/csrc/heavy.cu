@@ -259,8 +259,9 @@ __global__ void __launch_bounds__(kHvThreads, 2)
         all[tid] = make_float2(s.x == -INFINITY ? 0.f : s.x, s.y == 0.f ? 0.f : 1.f / s.y);
     }
     __syncthreads();
-    // Every row's weight, summed over the query rows in their order.
-    const int first_new = p.next_pos ? len - p.n : INT_MAX;
+    // Every row's weight, summed over the query rows that see it, in their order: a token's own row has no part of an
+    // earlier token's, whose sum may be NaN.
+    const int own = len - p.n, first_new = p.next_pos ? own : INT_MAX;
     const int first_pos = p.next_pos ? ld_dep(p.next_pos + b) : 0;
     constexpr int KEYS = 8;                             // a thread's keys whose old weights are loaded together
     for (int j0 = k0 + tid; j0 < k1; j0 += KEYS * kHvThreads) {
@@ -275,7 +276,7 @@ __global__ void __launch_bounds__(kHvThreads, 2)
             const int j = j0 + x * kHvThreads;
             if (j >= k1) break;
             float sum = 0.f;
-            for (int r = 0; r < p.R; ++r)
+            for (int r = j < own ? 0 : (j - own) * p.G; r < p.R; ++r)
                 sum = fmaf(fast_exp2(scores[(long long)r * p.stride + j - k0] - all[r].x), all[r].y, sum);
             p.weight[row0 + j] = old[x] + sum;
             if (j >= first_new) p.pos[row0 + j] = first_pos + (j - first_new);

@@ -78,3 +78,30 @@ def test_keys_whose_scores_are_minus_infinity(H_q, H_kv, d, n, cap):
         assert torch.equal(weight[b][old], w0[b][old])
         if n > 1:
             assert (weight[b, :, ln - 1] == 0).all()
+
+
+@pytest.mark.parametrize("H_q,H_kv,d,n,cap", [r for r in ROWS if r[3] > 1] + [(4, 1, 128, 2, 24001), (2, 2, 64, 8, 300),
+                                                                            (8, 2, 128, 2, 300), (4, 2, 128, 2, 5000)])
+@pytest.mark.parametrize("value", ["nan", "inf"])
+def test_weights_that_a_token_does_not_see(H_q, H_kv, d, n, cap, value):
+    """A query row that is not finite makes the weights of the rows that it sees NaN, and leaves those of the later
+    tokens' own rows as they are without it."""
+    B, G = 2, H_q // H_kv
+    kc, vc, weight, pos = cache(B, H_kv, cap, d, 25)
+    lens = [cap, n]
+    q = randn((B, n, H_q, d), 29)
+    w0, w1 = weight.clone(), weight.clone()
+    call = lambda q, w: mb.magicdec_heavy_attn(q, kc, vc, w, i32(lens), pos=pos.clone(), next_pos=i32([cap, cap]))  # noqa: E731
+    clean = call(q, w0)
+    # the first query head of every KV head, of an early token
+    for token in sorted({0, n // 2 - 1 if n > 2 else 0}):
+        q1, w = q.clone(), w1.clone()
+        q1.view(B, n, H_kv, G, d)[:, token, :, 0] = float(value)
+        got = call(q1, w).view(B, n, H_kv, G, d)
+        bad = torch.zeros((B, n, H_kv, G), dtype=torch.bool, device=DEV)
+        bad[:, token, :, 0] = True
+        assert got[bad].isnan().all() and torch.equal(got[~bad], clean.view(B, n, H_kv, G, d)[~bad])
+        for b, ln in enumerate(lens):
+            sees = ln - n + 1 + token
+            assert w[b, :, :sees].isnan().all()
+            assert torch.equal(w[b, :, sees:], w0[b, :, sees:])
