@@ -130,14 +130,16 @@ __global__ void __launch_bounds__(kHtThreads, 2)
         pdl_trigger();
     }
     pdl_wait();
-    // The query rows (row i * G + g: token i, head g of the group), K-major and swizzled.
+    // The query rows (row i * G + g: token i, head g of the group), K-major and swizzled.  Those behind the last
+    // are the last again, which sees every key: their scores are its own, and with a factor of 0 add nothing to a
+    // weight that is a number (the score of a query of zeros and an infinite key is none).
     constexpr int QV = (NR * (D / 8) + kHtThreads - 1) / kHtThreads;     // 16-byte words a thread has
     uint4 qv[QV];
 #pragma unroll
     for (int x = 0; x < QV; ++x) {
-        const int r = (x * kHtThreads + tid) / (D / 8), c = (x * kHtThreads + tid) % (D / 8), i = r / p.G;
+        const int r = min((x * kHtThreads + tid) / (D / 8), p.R - 1), c = (x * kHtThreads + tid) % (D / 8), i = r / p.G;
         const uint16_t *src = p.q + (((long long)b * p.n + i) * p.H_q + h * p.G + (r - i * p.G)) * D + c * 8;
-        qv[x] = r < p.R ? ld_dep_u4(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
+        qv[x] = ld_dep_u4(reinterpret_cast<const uint4 *>(src));
     }
     const int len0 = checked(ld_dep(p.len + b), 0, p.cap, p.err);
 #pragma unroll
@@ -379,8 +381,7 @@ __global__ void __launch_bounds__(kHtThreads, 2)
             }
             // A sum of zero: a row that sees nothing.  One of NaN stays so, in the output (NaN * 0, where no score
             // of this CTA's was a number) and in every weight that it has a part in.
-            const bool none = row >= p.R || s.y == 0.f;
-            all[row] = none ? make_float2(0.f, 0.f) : make_float2(s.x == -INFINITY ? 0.f : s.x, 1.f / s.y);
+            all[row] = make_float2(s.x == -INFINITY ? 0.f : s.x, row >= p.R || s.y == 0.f ? 0.f : 1.f / s.y);
             moved[row] = tiles == 0 ? 0.f : (held[row] == -INFINITY ? 0.f : fast_exp2(held[row] - all[row].x)) * all[row].y;
         }
         named_bar_sync(2, 128);
@@ -422,16 +423,13 @@ __global__ void __launch_bounds__(kHtThreads, 2)
             uint32_t x[NR];
             if (there) get((uint32_t)t % NS, true, x);
             else take(true, x);
-            // A bit for each query row that sees the key.  The columns behind the last row (queries of zero) are left out,
-            // not added as nothing: their scores are NaN where a key is infinite.
             const int lo = from_row(key);
-            const uint32_t sees = lo >= p.R ? 0u : ~0u >> (32 - p.R) & ~0u << lo;
             float w = 0.f;
 #pragma unroll
             for (int r = 0; r < NR; r += 2) {
                 const float4 a = *reinterpret_cast<const float4 *>(&all[r]);
-                if (sees >> r & 1u) w = fmaf(fast_exp2(fmaf(__uint_as_float(x[r]), sl, -a.x)), a.y, w);
-                if (sees >> (r + 1) & 1u) w = fmaf(fast_exp2(fmaf(__uint_as_float(x[r + 1]), sl, -a.z)), a.w, w);
+                if (r >= lo) w = fmaf(fast_exp2(fmaf(__uint_as_float(x[r]), sl, -a.x)), a.y, w);
+                if (r + 1 >= lo) w = fmaf(fast_exp2(fmaf(__uint_as_float(x[r + 1]), sl, -a.z)), a.w, w);
             }
             if (key < k1) {
                 p.weight[row0 + key] = old + w;
