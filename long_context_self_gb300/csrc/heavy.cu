@@ -259,28 +259,35 @@ __global__ void __launch_bounds__(kHvThreads, 2)
         all[tid] = make_float2(s.x == -INFINITY ? 0.f : s.x, s.y == 0.f ? 0.f : 1.f / s.y);
     }
     __syncthreads();
-    // Every row's weight, summed over the query rows that see it, in their order: a token's own row has no part of an
-    // earlier token's, whose sum may be NaN.
-    const int own = len - p.n, first_new = p.next_pos ? own : INT_MAX;
+    // Every row's weight, summed over the query rows in their order; the tokens' own rows apart, over the query rows
+    // that see them: an earlier token's probability there is 0, but not if its sum is NaN.
+    const int own = max(k0, len - p.n), shared = min(k1, own);
     const int first_pos = p.next_pos ? ld_dep(p.next_pos + b) : 0;
+    auto grown = [&](int j, int from) {
+        float sum = 0.f;
+        for (int r = from; r < p.R; ++r)
+            sum = fmaf(fast_exp2(scores[(long long)r * p.stride + j - k0] - all[r].x), all[r].y, sum);
+        return sum;
+    };
     constexpr int KEYS = 8;                             // a thread's keys whose old weights are loaded together
-    for (int j0 = k0 + tid; j0 < k1; j0 += KEYS * kHvThreads) {
+    for (int j0 = k0 + tid; j0 < shared; j0 += KEYS * kHvThreads) {
         float old[KEYS];
 #pragma unroll
         for (int x = 0; x < KEYS; ++x) {
             const int j = j0 + x * kHvThreads;
-            old[x] = j < k1 && j < first_new ? __ldcg(p.weight + row0 + j) : 0.f;
+            old[x] = j < shared ? __ldcg(p.weight + row0 + j) : 0.f;
         }
 #pragma unroll
         for (int x = 0; x < KEYS; ++x) {
             const int j = j0 + x * kHvThreads;
-            if (j >= k1) break;
-            float sum = 0.f;
-            for (int r = j < own ? 0 : (j - own) * p.G; r < p.R; ++r)
-                sum = fmaf(fast_exp2(scores[(long long)r * p.stride + j - k0] - all[r].x), all[r].y, sum);
-            p.weight[row0 + j] = old[x] + sum;
-            if (j >= first_new) p.pos[row0 + j] = first_pos + (j - first_new);
+            if (j >= shared) break;
+            p.weight[row0 + j] = old[x] + grown(j, 0);
         }
+    }
+    for (int j = own + tid; j < k1; j += kHvThreads) {
+        const float old = p.next_pos ? 0.f : __ldcg(p.weight + row0 + j);
+        p.weight[row0 + j] = old + grown(j, (j - (len - p.n)) * p.G);
+        if (p.next_pos) p.pos[row0 + j] = first_pos + j - (len - p.n);
     }
     // O of the warps, in the softmax's own scale.
     float *osum = reinterpret_cast<float *>(ring);      // [kHvWarps][R][OROW]
