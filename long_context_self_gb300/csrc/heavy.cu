@@ -808,7 +808,8 @@ __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictPara
     int left = E;
     uint32_t w_at = 0, p_at = 0;                             // borders: rows at them go, too, if all do
     if (len <= p.keep) {
-        const bool tied = border_kept(nullptr, low, left, w_at) != left;
+        const int light = border_kept(nullptr, low, left, w_at);   // rows at the border, of which `left` go
+        const bool tied = light != left;
         // Bits of the rows below the border, and of those at it: 4 of a thread, 8 threads a word.
         auto mark = [&](const uint32_t *mask, uint32_t at, bool all) {
             for (int w0 = warp * 4; w0 < nw; w0 += NW * 4) {
@@ -900,11 +901,13 @@ __global__ void __launch_bounds__(kEvThreads) heavy_evict_kernel(const EvictPara
         }
     } else {
         auto place = [&](int j) { return place_of(ld_dep(pos + j)); };
-        const bool tied = border(key, [](int) { return true; }, left, w_at) != left;
+        const int light = border(key, [](int) { return true; }, left, w_at);
+        const bool tied = light != left;
         bool twins = false;
         uint32_t r_at = 0;
         if (tied) {
-            twins = border(place, [&](int j) { return key(j) == w_at; }, left, p_at) != left;
+            const int alike = border(place, [&](int j) { return key(j) == w_at; }, left, p_at);
+            twins = alike != left;
             if (twins)
                 border([](int j) { return ~(uint32_t)j; }, [&](int j) { return key(j) == w_at && place(j) == p_at; }, left,
                        r_at);
