@@ -122,32 +122,44 @@ __global__ void __launch_bounds__(kHtThreads, 2)
         met = 0;
     }
     if (tid < NR) held[tid] = -INFINITY;
-    // TMEM is taken before the wait (behind it, 16 sequences of up to 12,001 rows took 120 us, so 114), and the kernels
-    // behind are let go afterwards.  Every kernel that takes any lets its followers go only then, or leaves them
-    // no room on the SM, so that none in front can be waiting for what this CTA holds while it waits for that one.
-    if (warp == 1) {
-        tmem_alloc(&tmem_slot, COLS);
-        pdl_trigger();
-    }
+    __syncthreads();
     pdl_wait();
-    // The query rows (row i * G + g: token i, head g of the group), K-major and swizzled.  Those behind the last
-    // are the last again, which sees every key: their scores are its own, and with a factor of 0 add nothing to a
-    // weight that is a number (the score of a query of zeros and an infinite key is none).
-    constexpr int QV = (NR * (D / 8) + kHtThreads - 1) / kHtThreads;     // 16-byte words a thread has
-    uint4 qv[QV];
-#pragma unroll
-    for (int x = 0; x < QV; ++x) {
-        const int r = min((x * kHtThreads + tid) / (D / 8), p.R - 1), c = (x * kHtThreads + tid) % (D / 8), i = r / p.G;
-        const uint16_t *src = p.q + (((long long)b * p.n + i) * p.H_q + h * p.G + (r - i * p.G)) * D + c * 8;
-        qv[x] = ld_dep_u4(reinterpret_cast<const uint4 *>(src));
-    }
     const int len0 = checked(ld_dep(p.len + b), 0, p.cap, p.err);
+    uint32_t tmem = 0;
+    if (warp > 0) {
+        // The query rows (row i * G + g: token i, head g of the group), K-major and swizzled, while the producer asks
+        // for the first keys.  Those behind the last are the last again, which sees every key: their scores are its
+        // own, and with a factor of 0 add nothing to a weight that is a number (the score of a query of zeros and an
+        // infinite key is none).
+        constexpr int QT = kHtThreads - 32, QV = (NR * (D / 8) + QT - 1) / QT;   // 16-byte words a thread has
+        uint4 qv[QV];
 #pragma unroll
-    for (int x = 0; x < QV; ++x) {
-        const int r = (x * kHtThreads + tid) / (D / 8), c = (x * kHtThreads + tid) % (D / 8);
-        if (r < NR) *reinterpret_cast<uint4 *>(qs + (c >> 3) * QHALF + swz128(r, c & 7)) = qv[x];
+        for (int x = 0; x < QV; ++x) {
+            const int at = x * QT + tid - 32, r = min(at / (D / 8), p.R - 1), c = at % (D / 8), i = r / p.G;
+            const uint16_t *src = p.q + (((long long)b * p.n + i) * p.H_q + h * p.G + (r - i * p.G)) * D + c * 8;
+            qv[x] = ld_dep_u4(reinterpret_cast<const uint4 *>(src));
+        }
+        // TMEM is taken when the kernels in front are done, whoever's they are: one of them might be about to take
+        // its own on this SM, and wait for this CTA, which waits for it.  The kernels behind are let go afterwards, as
+        // one of them may take its own before it waits for this one.  An SM begins no second such CTA before the
+        // first has its columns, so that of the first ones half come 1 us behind the wait and find other SMs than
+        // side by side (taken in front of the wait, 16 sequences of up to 12,001 rows, R = 25, 113 us and now 118,
+        // all of 12,001 178 and 177, 85 of 1721 with R = 12 135 both).
+        if (warp == 1) {
+            tmem_alloc(&tmem_slot, COLS);
+            pdl_trigger();
+        }
+#pragma unroll
+        for (int x = 0; x < QV; ++x) {
+            const int at = x * QT + tid - 32, r = at / (D / 8), c = at % (D / 8);
+            if (r < NR) *reinterpret_cast<uint4 *>(qs + (c >> 3) * QHALF + swz128(r, c & 7)) = qv[x];
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        named_bar_sync(3, QT);
+        tc_fence_after();
+        tmem = tmem_slot;
     }
-    fence_proxy_async_smem();
     const int len = len0 < 0 ? 0 : (len0 > p.cap ? p.cap : len0);
     // This CTA's keys: [k0, k1), in tiles.
     const int per = ((len + (int)C - 1) / (int)C + kHtKeys - 1) / kHtKeys * kHtKeys;
@@ -158,10 +170,6 @@ __global__ void __launch_bounds__(kHtThreads, 2)
     const int own = len - p.n;                           // the first of the tokens' own rows
     bool ok = smem_u32(smem) % 1024 == 0;
     if (!ok && tid == 0) raise_error(p.err, kErrState);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = tmem_slot;
 
     // A warp's role ends its first pass, all meet where the cluster exchanges, then the second.
     if (warp == 0) {

@@ -419,11 +419,14 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         found[2] = found[11] = 0;
         *met = 0;
     }
-    if (warp == 1) tmem_alloc(tmem_slot, 512);
-    // The kernel behind PRE reads what was there before this one without waiting for its end.
-    if (!PRE) pdl_trigger();
+    // TMEM is taken when the kernels in front are done, which may be about to take their own, and the kernels behind are
+    // let go when it is there, as they may take theirs before they wait (in front of the wait: times as these).  The one
+    // behind PRE reads what was there before this kernel without waiting for its end.
     pdl_wait();
-    if (PRE) pdl_trigger();
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 512);
+        pdl_trigger();
+    }
 
     // The list of work: prefix sums over the sequences (a thread has one of them, or with more
     // than kTrThreads several in a row), this CTA's run of tiles, and the sequence that it
