@@ -98,18 +98,19 @@ __global__ void __launch_bounds__(PoShape<D, ROWS, MT>::NT, PoShape<D, ROWS, MT>
     const int per = ((total + (int)C - 1) / (int)C + 15) & ~15;
     const int k0 = min(total, (int)rank * per), k1 = min(total, k0 + per), tiles = (k1 - k0 + kPoKeys - 1) / kPoKeys;
     // Where a key lies; one outside the pool is zeros.  A page is asked for before a tile's products and
-    // its number used behind them.
+    // its number used behind them.  (Unsigned, as keys of tiles behind the last one may pass 2^31.)
     const int32_t *table = p.table + (long long)b * p.max_pages;
+    auto key_of = [&](int t, int at) { return (uint32_t)k0 + (uint32_t)t * kPoKeys + at; };
     auto ask = [&](int t, int at) {
-        const int key = k0 + t * kPoKeys + at;
-        return key < k1 ? ld_dep(table + key / p.page_size) : -1;
+        const uint32_t key = key_of(t, at);
+        return key < (uint32_t)k1 ? ld_dep(table + key / (uint32_t)p.page_size) : -1;
     };
     auto look_up = [&](int t, int at, int page) {
-        const int key = k0 + t * kPoKeys + at;
+        const uint32_t key = key_of(t, at);
         long long row = -1;
-        if (key < k1) {
+        if (key < (uint32_t)k1) {
             if (page < 0 || page >= p.n_pages) raise_error(p.err, kErrPage);
-            else row = (((long long)page * p.page_size + key % p.page_size) * p.pre.H_kv + h) * D;
+            else row = (((long long)page * p.page_size + key % (uint32_t)p.page_size) * p.pre.H_kv + h) * D;
         }
         rows_at[t & 7][at] = row;
     };

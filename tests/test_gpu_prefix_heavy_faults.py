@@ -105,3 +105,20 @@ def test_weights_that_a_token_does_not_see(H_q, H_kv, d, n, cap, value):
             sees = ln - n + 1 + token
             assert w[b, :, :sees].isnan().all()
             assert torch.equal(w[b, :, sees:], w0[b, :, sees:])
+
+
+def test_own_slots_up_to_the_largest_capacity():
+    """2^31 - 256 own slots, of two pages over and over: tiles are looked up some steps ahead, and positions behind the
+    last one pass 2^31."""
+    page, d = 47 * 256, 64
+    most = ((1 << 31) - 256) // page
+    assert page * most == (1 << 31) - 256
+    kp = randn((2, page, 1, d), 71)
+    # queries of zeros: every key has the same weight, and sums of powers of two are exact as long as the keys of a
+    # thread are fewer than 2^24 (a warp's 2^26, 4 of 16 a thread)
+    v = torch.tensor([(-1.0) ** c * 2.0 ** (c % 7 - 3) for c in range(d)], device=DEV).to(BF16)
+    vp = v.expand(2, page, 1, d).contiguous()
+    table = (torch.arange(most, device=DEV) % 2).to(I32).view(1, most)
+    q = torch.zeros((1, 1, 1, d), dtype=BF16, device=DEV)
+    got = mb.magicdec_prefix_attn(q, kp, vp, i32([[1]]), i32([3]), table, i32([page * most - 1]))
+    assert torch.equal(got.view(d), v)
