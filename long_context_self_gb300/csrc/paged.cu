@@ -139,12 +139,13 @@ __device__ __forceinline__ void norm_head(Head16 &h, const Head16 &w, float eps,
         s = squares<LR>(h, lanes);
         e *= 0x1p-140f;
     }
+    // The root first: x / rms(x) is of the order of one, while the root's inverse times the weight may leave fp32.
     const float inv = rsqrtf(fmaf(s, 1.f / (LR * 16), e));
     const uint64_t i2 = pair(inv, inv);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        h.lo[k] = mul2(h.lo[k], mul2(i2, w.lo[k]));
-        h.hi[k] = mul2(h.hi[k], mul2(i2, w.hi[k]));
+        h.lo[k] = mul2(mul2(h.lo[k], i2), w.lo[k]);
+        h.hi[k] = mul2(mul2(h.hi[k], i2), w.hi[k]);
     }
 }
 

@@ -3,9 +3,9 @@ are not finite, sizes or an order of calls could go wrong: each against a plain 
 import pytest
 import torch
 
-from heavy_util import heavy_ref
+from heavy_util import heavy_ref, norm_rope_ref
 from long_context_self_gb300 import binding as mb
-from tree_util import gen
+from tree_util import gen, make_cache, rows_of
 
 pytestmark = pytest.mark.gpu
 
@@ -122,3 +122,23 @@ def test_own_slots_up_to_the_largest_capacity():
     q = torch.zeros((1, 1, 1, d), dtype=BF16, device=DEV)
     got = mb.magicdec_prefix_attn(q, kp, vp, i32([[1]]), i32([3]), table, i32([page * most - 1]))
     assert torch.equal(got.view(d), v)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("size,weight,eps", [(2.0 ** -62, 2.0 ** 70, 2.0 ** -126), (2.0 ** 59, 2.0 ** -100, 1e-6),
+                                             (2.0 ** -40, 2.0 ** 90, 2.0 ** -126), (2.0 ** 80, 2.0 ** -60, 1e-6)])
+def test_norms_whose_weight_and_root_are_far_from_one(size, weight, eps, inter):
+    """x / rms(x) is of the order of one whatever x and its root are; only its product with the weight has to be a number."""
+    B, n, H_q, H_kv, d, page = 2, 3, 4, 2, 128, 16
+    q, k, v = (randn((B, n, H, d), 51 + H) for H in (H_q, H_kv, H_kv))
+    q, k = ((x.float() * size).to(BF16) for x in (q, k))
+    qw, kw = ((randn((d,), s).float() * weight).to(BF16) for s in (61, 62))
+    kp, vp, table = make_cache([5, 0], n, page, H_kv, d, 63, DEV)
+    inv = (10000.0 ** (-torch.arange(0, d, 2, dtype=torch.float64) / d)).float().to(DEV)
+    got = mb.magicdec_norm_append(k, v, kp, vp, table, i32([5, 0]), inv, q=q, q_weight=qw, k_weight=kw, eps=eps,
+                                  interleaved=inter)
+    for b, ln in enumerate([5, 0]):
+        at = torch.arange(ln, ln + n, device=DEV)[:, None].expand(n, d // 2)
+        rows = rows_of(table, b, ln + torch.arange(n), page).to(DEV)
+        within(got[b], *norm_rope_ref(q[b], qw, eps, at, inv, inter), "q")
+        within(kp.view(-1, H_kv, d)[rows], *norm_rope_ref(k[b], kw, eps, at, inv, inter), "k")
