@@ -474,14 +474,14 @@ MAGICDEC_API magicdec_status magicdec_paged_append(magicdec_paged_shape shape, i
  * in fp32, with one rounding to bf16 at the end.
  *   q_weight, k_weight (nullable, each) [d] bf16: NULL leaves the query (key) heads as
  *            they are
- *   eps      above zero and finite, if there is a weight
+ *   eps      finite and at least 2^-126, if there is a weight (squares below lose their last bits)
  *   pos      (nullable) [B, n, n_axes] int32: token i of sequence b has these positions
  *            instead of those counted from len; not with parent.  Slots go by len as before
  *   axis     (nullable if n_axes == 1) [rot_dim / 2] int32: pair f turns by the angle
  *            pos[b, i, axis[f]] * inv_freq[f]; an entry outside [0, n_axes) counts as 0 (and,
  *            in the range-checking build, sets error 4)
  * Everything else as there, the errors too; further ones: MAGICDEC_ERR_NULL for n_axes > 1
- * without axis, MAGICDEC_ERR_SHAPE for eps not above zero or not finite beside a weight, pos
+ * without axis, MAGICDEC_ERR_SHAPE for eps below 2^-126 or not finite beside a weight, pos
  * together with parent, n_axes <= 0 with pos, or axis without pos, MAGICDEC_ERR_ALIGN for
  * weights off a 16-byte boundary, MAGICDEC_ERR_UNSUPPORTED for n_axes > 64.
  */

@@ -456,7 +456,7 @@ magicdec_status magicdec_norm_append(magicdec_paged_shape shape, int n, const ui
     if (s != MAGICDEC_OK) return s;
     if (pos ? parent || n_axes <= 0 : axis != nullptr) return MAGICDEC_ERR_SHAPE;
     if (pos && n_axes > 1 && !axis) return MAGICDEC_ERR_NULL;
-    if ((q_weight || k_weight) && !(eps > 0.f && eps <= FLT_MAX)) return MAGICDEC_ERR_SHAPE;
+    if ((q_weight || k_weight) && !(eps >= FLT_MIN && eps <= FLT_MAX)) return MAGICDEC_ERR_SHAPE;
     if (pos && n_axes > 64) return MAGICDEC_ERR_UNSUPPORTED;
     if (!aligned16(q_weight) || !aligned16(k_weight)) return MAGICDEC_ERR_ALIGN;
     return magicdec::launch_norm_append(shape, n, q, q_stride, k, k_stride, v, v_stride, q_weight, k_weight, eps, len,

@@ -186,3 +186,13 @@ def test_binding_refuses_tensors_of_the_host(lib):
     for call in calls(q=x, k=x, kc=x).values():
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_append_refuses_an_eps_that_squares_in_fp32_cannot_tell_from_others(lib):
+    """Squares of some 2^-126 and less lose their last bits, so that beside a smaller eps the root would be off."""
+    def call(eps, weight=FAKE):                        # 65 axes are refused behind this check
+        return lib.magicdec_norm_append(paged(), 4, FAKE, 1024, FAKE, 256, FAKE, 256, weight, weight, eps, FAKE, NULL, NULL,
+                                        FAKE, 65, FAKE, FAKE, 128, 0, FAKE, FAKE, FAKE, FAKE, NULL)
+    for eps in (2.0 ** -127, 1e-40, 2.0 ** -149):
+        assert call(eps) == SHAPE
+    assert call(2.0 ** -126) == call(1e-6) == call(0.0, NULL) == UNSUPPORTED
