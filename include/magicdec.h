@@ -603,6 +603,20 @@ MAGICDEC_API magicdec_status magicdec_tree_commit(magicdec_paged_shape shape, in
  * int32.  A step appends a token's rows behind the others (magicdec_draft_cache_update),
  * attends with magicdec_heavy_attn, and, when the rows have outgrown the budget, drops those
  * of least weight with magicdec_heavy_evict.
+ *
+ * A speculative step, from L positions and r rows (table as magicdec_step_lengths gives it):
+ *   for each of the gamma drafted tokens magicdec_draft_cache_update(table[g], table[g],
+ *   table[g+1]) with ring = 0, origin = L and base = r, then magicdec_heavy_attn with
+ *   next_pos = table[g]; after verification magicdec_draft_cache_update(table[0],
+ *   table[gamma], L + n_acc + 1), which puts the verified rows in place of the drafted ones and
+ *   leaves out the rejected; then magicdec_heavy_evict with that length as seq_len.
+ * weight and pos are set by magicdec_heavy_attn alone, so what it has not attended with is the
+ * caller's to set: the rows that a cache begins with (magicdec_gather_kv), and row r + gamma,
+ * position L + gamma, which the refresh brings in where all gamma tokens were accepted (weight 0
+ * and that position, at any time between the step's last attention and its eviction; in other
+ * sequences the row is not in use, and both may be set there as well).
+ * Attention of tokens that are rejected afterwards stays in the weights of the rows that they saw.
+ * The update and the gather read dense K and V; rows of a paged cache are the caller's to bring in.
  */
 
 /*
