@@ -23,8 +23,8 @@ namespace magicdec {
 //
 // A producer warp keeps a ring of stages filled by TMA, 64 keys' K and V each; 4 consumer warps take 16
 // keys of a stage each through ldmatrix and mma.sync (m16n8k16, the lower half of A empty): at 8 rows
-// the products are a few percent of the time.  128 sequences over 2053 rows, R = 4: 181 to 183 us,
-// 6.0 TB/s; with keys straight from global memory into the fragments, which left too few bytes
+// the products are a few percent of the time.  128 sequences over 2053 rows, R = 4: 179 us,
+// 6.1 TB/s; with keys straight from global memory into the fragments, which left too few bytes
 // under way, 207; on tcgen05 223.
 constexpr int kHvKeys = 64;          // keys of a stage
 constexpr int kHvHalf = kHvKeys * 128;   // bytes of 64 channels of them

@@ -20,7 +20,7 @@ struct HeavyParams {
 };
 
 double heavy_time(long long pairs, int cap, int C, int keys, double each, double way);
-// By up to 32 query rows of a KV head, the scores computed twice.
+// By up to 32 query rows of a KV head, the scores of all but a stretch's last tiles computed twice.
 magicdec_status launch_heavy_tc(const HeavyParams &p, int D, const uint16_t *k, const uint16_t *v, cudaStream_t st);
 
 }  // namespace magicdec

@@ -13,7 +13,7 @@
 // A row's weight needs the softmax's final maximum and sum.  TMEM keeps the scores of the last 6 or 14 tiles
 // (32 or 16 query rows) until then; those of earlier ones are computed again, by a second pass over their
 // K, out of L2.  CTAs, clusters and exchange as in heavy.cu, two CTAs an SM.  85 sequences of 1721 rows, 8
-// heads, R = 12: 140 us, with all scores computed again 153.
+// heads, R = 12: 135 us, a tenth less than with all scores computed again.
 // Roles: warp 0 issues the TMA boxes, warp 1 the products, warps 2 to 5 are the softmax.
 // Every wait is bounded; after one that gave up (error 1) the roles run on without waiting.
 #include <climits>
@@ -32,8 +32,8 @@ constexpr int kHtThreads = 192;
 template <int D, int NR>
 struct HtShape {
     static constexpr int HV = D / 64, SLOT = HV * kHtHalf;
-    // Of the ring: K and V of a tile, or of two and a half (16 sequences of 12,001 rows, d = 64, R = 25: 110.5 us, with
-    // two 112.4), as two CTAs an SM leave room for.
+    // Of the ring: K and V of a tile, or of two and a half (16 sequences of 12,001 rows, d = 64, R = 25: 107 us, and 2
+    // more with two), as two CTAs an SM leave room for.
     static constexpr int SLOTS = HV == 1 ? 5 : 2;
     static constexpr int P = kHtKeys * 128, Q = HV * NR * 128;   // a key's probabilities: 128 bytes, 2 NR of them used
     static constexpr int BYTES = SLOTS * SLOT + P + Q;
@@ -505,7 +505,8 @@ static magicdec_status launch_ht_t(const CUtensorMap &tmk, const CUtensorMap &tm
 
 magicdec_status launch_heavy_tc(const HeavyParams &p, int D, const uint16_t *k, const uint16_t *v, cudaStream_t st) {
     // Clusters of 1 to 8, by the time they should take.  16 sequences of up to 12,001 rows, 8 heads,
-    // R = 25, clusters of 1, 2, 4 and 8: 254, 144, 119 and 119 us; 128 of 1029: 138, 153, 220 and 350.
+    // R = 25, clusters of 1, 2, 4 and 8: 254, 138, 119 and 116 us, of 12,001 each 266, 176, 178 and 187; 128 of
+    // 1029: 132, 144, 210 and 338.
     int best = 1;
     double least = 0;
     for (int C = 1; C <= 8; C *= 2) {

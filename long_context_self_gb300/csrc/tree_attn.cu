@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             // Behind shared prefixes a CTA begins with the end of its run, where that is the beginning of an
             // entry, and goes on with the run's own beginning, the end of one: then all CTAs of a prefix
             // sweep over it side by side, and find in L2 what others have read.  Trees of 8 for 128
-            // sequences behind 32k: 0.15 GB from HBM, 413 us a call; in the list's order 1.25 GB, 427 us.
+            // sequences behind 32k: 0.15 GB from HBM, some 420 us a call; in the list's order 1.25 GB, 14 us more.
             const long long last = min(t0 + run, all) - 1;
             if (PRE && last >= before && last < before + w) {
                 const int item = (int)((last - before) / list_tiles<PRE>(sq));
